@@ -51,6 +51,7 @@ typedef enum {
 /* Bits of the device status word (see mq_device_status). */
 #define MQ_DEV_BAD_EXPERT_ID  0x1u  /* a topk id outside [0, E); slot ignored   */
 #define MQ_DEV_WAIT_TIMEOUT   0x2u  /* a pipeline wait gave up; output invalid  */
+#define MQ_DEV_BAD_OFFSETS    0x4u  /* expert offsets that fall or leave [0, R] */
 
 const char* mq_status_string(int status);
 const char* mq_last_error_message(void);
@@ -389,6 +390,110 @@ int moe_quant_forward_noalloc(const void* x, int T, int H, int I, int E, int k,
                               void* out, void* stream);
 
 /*
+ * Microscaled (MX) formats
+ * ------------------------
+ * (No counterpart on the pages, whose 4-bit weights have f16 group scales;
+ * the format is the OCP Microscaling Formats specification's MXFP4 and
+ * MXFP8.)  A row is cut into blocks of 32 consecutive elements.  An element
+ * is E2M1 (bits = 4; magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6) or E4M3 (bits = 8;
+ * up to 448); a block shares the scale 2^(c - 127), c its E8M0 code, and
+ * c = 255 makes the block NaN.
+ *   q     uint8 [rows, cols * bits / 8]   4 bits: element 2j in the low nibble
+ *                                         of byte j, element 2j + 1 in the high
+ *   scale uint8 [rows, cols / 32]
+ * Quantisation of a block with a = max |v|: c - 127 = floor(log2 a) - emax,
+ * at least -127 (emax = 2 for E2M1, 8 for E4M3; a = 0 gives c = 0); element =
+ * v / 2^(c - 127) rounded to nearest even, clamped to +-6 or +-448.  The
+ * arithmetic is exact but for that rounding, so codes are reproducible bit for
+ * bit.  A block that holds an infinity or NaN gets c = 255 and elements 0.
+ *
+ * Data types of the plain side:
+ */
+#define MQ_DTYPE_BF16 0
+#define MQ_DTYPE_F16  1
+#define MQ_DTYPE_F32  2
+
+/*
+ * moe_quantize_mx -- rows of x (device, MQ_DTYPE_*, `row_stride` elements
+ * apart) to MX codes and scales (device, dense).
+ * Errors: MQ_ERR_INVALID_ARG for an unknown dtype or bits, rows < 0, cols not a
+ * positive multiple of 32, row_stride below cols or not a multiple of 8, null
+ * or misaligned pointers (x, q: 16 bytes; scale: 4); MQ_ERR_UNSUPPORTED for
+ * more than 2^40 elements.
+ */
+int moe_quantize_mx(const void* x, int dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                    int bits, uint8_t* q, uint8_t* scale, void* stream);
+
+/*
+ * moe_dequantize_mx -- the values that codes and scales stand for, out
+ * [rows, cols] (device, dense), rounded once to dtype (bf16 and float32 hold
+ * every 4-bit value exactly).  Errors as moe_quantize_mx.
+ */
+int moe_dequantize_mx(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols,
+                      int bits, void* out, int dtype, void* stream);
+
+/*
+ * moe_rmsnorm_mx -- residual addition, root-mean-square norm and MX rows in
+ * one pass (what stands between attention and the experts):
+ *   h = x + residual;  y = h / sqrt(mean(h^2) + eps) * weight
+ *   residual_out = h, y_out = y (each rounded once to dtype), (q, scale) = MX(y)
+ * h, the mean and y are float32; y and its codes are taken from the unrounded
+ * h.  x [T, H] with x_stride elements between rows; residual [T, H] with
+ * residual_stride, or NULL (h = x); weight [H] in dtype, or float32 with
+ * weight_f32 != 0.  residual_out and y_out are dense [T, H] in dtype, or NULL.
+ * residual_out may be residual or x itself where that is dense.
+ * Limits: dtype bf16 or f16, H a multiple of 32 up to 32768.
+ * Errors: MQ_ERR_INVALID_ARG for T < 0, H not a positive multiple of 32,
+ * strides below H or not multiples of 8, an unknown dtype or bits, eps
+ * negative or not finite, null or misaligned pointers; MQ_ERR_UNSUPPORTED for
+ * float32 rows or H above the limit.
+ */
+int moe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int dtype,
+                   int weight_f32, int T, int H, int64_t x_stride, int64_t residual_stride,
+                   float eps, void* residual_out, void* y_out, int bits, uint8_t* q,
+                   uint8_t* scale, void* stream);
+
+/*
+ * moe_mx_product -- rows grouped by expert times 4-bit MX weights:
+ *   out[r, n] = sum_k A[r, k] * W[e, n, k],  offsets[e] <= r < offsets[e + 1]
+ * a, a_scale: MX rows [R, K] with a_bits 8 or 4; w, w_scale: 4-bit MX
+ * [E, N, K]; expert_offsets int32 [E + 1] (device), rising from >= 0 to <= R, or
+ * NULL with E = 1 (a dense product).  Experts may be empty; rows outside
+ * [offsets[0], offsets[E]) are left as they are.  Offsets that fall or leave
+ * [0, R] set MQ_DEV_BAD_OFFSETS: no access leaves the arrays, and the output
+ * is unspecified.  out [R, N] dense in out_dtype.  Accumulation is float32
+ * with one final rounding; a result is the same on every run.
+ * The workspace holds float32 partial sums where K is split (few units of
+ * work); moe_mx_product_workspace may return 0 (workspace may then be NULL).
+ * Limits: K a multiple of 128, N >= 1, E <= 1024, R < 2^30.
+ * Errors: MQ_ERR_INVALID_ARG, MQ_ERR_UNSUPPORTED (limits), MQ_ERR_WORKSPACE.
+ */
+size_t moe_mx_product_workspace(int64_t R, int K, int N, int E);
+int moe_mx_product(const uint8_t* a, const uint8_t* a_scale, int a_bits, int64_t R, int K, int N,
+                   int E, const uint8_t* w, const uint8_t* w_scale,
+                   const int32_t* expert_offsets, void* out, int out_dtype, void* workspace,
+                   size_t ws_bytes, void* stream);
+
+/*
+ * moe_mx_forward -- moe_quant_forward with 4-bit MX experts and MX
+ * activations (from moe_rmsnorm_mx or moe_quantize_mx):
+ *   for every token t and slot j with e = topk_ids[t,j]:
+ *     h = W13[e] . A[t];  b = MX(silu(h[0:I]) * h[I:2I])  (a_bits again)
+ *     out[t] += topk_w[t,j] * (W2[e] . b)
+ * w13, s13: 4-bit MX [E, 2I, H] (gate rows first); w2, s2: [E, H, I]; a,
+ * a_scale: MX [T, H]; topk_w float32, topk_ids int32 [T, k]; out [T, H] bf16 or
+ * f16.  h, the activation and the sums are float32; b is the one further
+ * rounding.  An id outside [0, E) sets MQ_DEV_BAD_EXPERT_ID and its slot is
+ * left out.  Limits and errors as moe_quant_forward (H % 128 == 0, I % 128 ==
+ * 0, E <= 1024, k <= min(E, 32)); a_bits 8 or 4.
+ */
+size_t moe_mx_forward_workspace(int T, int H, int I, int E, int k, int a_bits);
+int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bits, int T, int H, int I,
+                   int E, int k, const uint8_t* w13, const uint8_t* s13, const uint8_t* w2,
+                   const uint8_t* s2, const float* topk_w, const int32_t* topk_ids, void* out,
+                   int out_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Instrumentation (no counterpart on the pages; used by the benchmark).
  *
  * mq_kernel_launch_count: kernels this library has launched in this process.
@@ -409,7 +514,8 @@ int moe_quant_forward_noalloc(const void* x, int T, int H, int I, int E, int k,
 #define MQ_PROF_GATHER  6
 #define MQ_PROF_ACTF16  7
 #define MQ_PROF_LAYER   8  /* both expert GEMMs in one launch (MQ_FWD_PATH_LAYER) */
-#define MQ_PROF_SLOTS   9
+#define MQ_PROF_NORM    9  /* moe_rmsnorm_mx */
+#define MQ_PROF_SLOTS   10
 
 long long mq_kernel_launch_count(void);
 int mq_profile_enable(int on);

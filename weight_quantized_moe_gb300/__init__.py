@@ -19,9 +19,17 @@ from .binding import (  # noqa: F401
     moe_quant_forward,
     moe_quant_forward_logits,
     moe_quant_forward_workspace,
+    moe_dequantize_mx,
+    moe_mx_forward,
+    moe_mx_forward_workspace,
+    moe_mx_product,
+    moe_mx_product_workspace,
     moe_quantize_int8_per_channel,
+    moe_quantize_mx,
     moe_quantize_uint4_group,
+    moe_rmsnorm_mx,
     moe_topk_route,
+    MQ_DEV_BAD_OFFSETS,
     MQ_DEV_BAD_EXPERT_ID,
     MQ_DEV_WAIT_TIMEOUT,
     MQ_FWD_W8_UINT8,

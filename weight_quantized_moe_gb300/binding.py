@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_PKG, "libmoeq.so")
 MQ_OK, MQ_ERR_INVALID_ARG, MQ_ERR_UNSUPPORTED, MQ_ERR_CUDA, MQ_ERR_WORKSPACE = range(5)
 MQ_DEV_BAD_EXPERT_ID = 0x1
 MQ_DEV_WAIT_TIMEOUT = 0x2
+MQ_DEV_BAD_OFFSETS = 0x4
 # moe_quant_forward_ex option flags (include/moeq.h)
 MQ_FWD_W8_UINT8 = 0x1
 MQ_FWD_SCALE_F16 = 0x2
@@ -35,6 +36,8 @@ _PATH_FLAGS = {"auto": 0, "tc": MQ_FWD_PATH_TENSOR_CORE, "decode": MQ_FWD_PATH_D
 # mq_route_opts.scoring_func
 MQ_SCORING_SOFTMAX = 0
 MQ_SCORING_SIGMOID = 1
+# MQ_DTYPE_*
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 class MqRouteOpts(ctypes.Structure):
@@ -46,6 +49,7 @@ class MqRouteOpts(ctypes.Structure):
 
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_f32 = ctypes.c_float
 _SIGNATURES = {
     "mq_status_string": (ctypes.c_char_p, [_i32]),
     "mq_last_error_message": (ctypes.c_char_p, []),
@@ -73,6 +77,16 @@ _SIGNATURES = {
                                            _vp]),
     "moe_quant_forward_noalloc": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
                                          _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_quantize_mx": (_i32, [_vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "moe_dequantize_mx": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _i32, _vp]),
+    "moe_rmsnorm_mx": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i64, _i64, _f32, _vp, _vp,
+                              _i32, _vp, _vp, _vp]),
+    "moe_mx_product_workspace": (_sz, [_i64, _i32, _i32, _i32]),
+    "moe_mx_product": (_i32, [_vp, _vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32,
+                              _vp, _sz, _vp]),
+    "moe_mx_forward_workspace": (_sz, [_i32] * 6),
+    "moe_mx_forward": (_i32, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                              _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
     "mq_kernel_launch_count": (ctypes.c_longlong, []),
     "mq_test_layer_wait_extra": (_i32, [_i32]),
     "mq_profile_enable": (_i32, [_i32]),
@@ -80,7 +94,7 @@ _SIGNATURES = {
 }
 
 PROF_SLOTS = ("quant", "route", "align", "gemm1", "gemm2", "combine", "gather", "act_f16",
-              "layer")
+              "layer", "norm")
 
 _lib = None
 
@@ -443,4 +457,216 @@ def moe_quant_forward_noalloc(x, w13, w2, s13, s2, topk_w, topk_ids, bits=8, gro
         _ptr(x), T, H, I, E, k, bits, group_size, int(bool(has_zp)),
         _ptr(w13), _ptr(w2), _ptr(s13), _ptr(s2), _ptr(z13 if has_zp else None),
         _ptr(z2 if has_zp else None), _ptr(topk_w), _ptr(topk_ids), _ptr(out), _stream(stream)))
+    return out
+
+
+# ------------------------------------------------- microscaled (MX) formats --
+_MX_BLOCK = 32
+
+
+def _mx_dtype(t, name, dtypes=tuple(_DTYPES)):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return _DTYPES[t.dtype]
+
+
+def _mx_rows(t, name):
+    """(rows, cols, elements between rows) of a tensor whose rows are dense
+    and evenly spaced."""
+    cols = t.shape[-1]
+    if t.dim() == 1:
+        t = t.unsqueeze(0)
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if t.dim() > 2:
+        try:
+            t = t.view(-1, cols)
+        except RuntimeError:
+            raise ValueError(f"{name}: the rows must be evenly spaced") from None
+    rows = t.shape[0]
+    return rows, cols, t.stride(0) if rows > 1 else cols
+
+
+def _mx_codes(q, scale, bits, name):
+    """Checks MX codes and scales; returns the number of elements in a row."""
+    if bits not in (4, 8):
+        raise ValueError(f"bits must be 4 or 8, got {bits}")
+    if bits == 8 and isinstance(q, torch.Tensor) and q.dtype == torch.float8_e4m3fn:
+        q = q.view(torch.uint8)
+    _need(q, torch.uint8, name)
+    _need(scale, torch.uint8, f"{name}_scale")
+    if q.dim() < 1:
+        raise ValueError(f"{name} must have at least one dim")
+    cols = q.shape[-1] * 8 // bits
+    if cols == 0 or cols % _MX_BLOCK:
+        raise ValueError(f"{name} must have rows of a positive multiple of {_MX_BLOCK} elements")
+    if tuple(scale.shape) != (*q.shape[:-1], cols // _MX_BLOCK):
+        raise ValueError(f"{name}_scale must be {[*q.shape[:-1], cols // _MX_BLOCK]}")
+    if scale.device != q.device:
+        raise ValueError(f"{name}_scale must be on {name}'s device")
+    return cols
+
+
+def _mx_out(t, shape, dtype, device, name):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t
+
+
+def _mx_code_shape(shape, bits):
+    if bits not in (4, 8):
+        raise ValueError(f"bits must be 4 or 8, got {bits}")
+    if len(shape) < 1 or shape[-1] == 0 or shape[-1] % _MX_BLOCK:
+        raise ValueError(f"rows must have a positive multiple of {_MX_BLOCK} elements")
+    return ((*shape[:-1], shape[-1] * bits // 8), (*shape[:-1], shape[-1] // _MX_BLOCK))
+
+
+def moe_quantize_mx(x, bits=4, q=None, scale=None, stream=None):
+    """bf16 / f16 / float32 [..., K] -> MX codes uint8 [..., K * bits / 8] (8
+    bits: E4M3 bytes; 4 bits: two E2M1 codes per byte, even element low) and
+    E8M0 scale codes uint8 [..., K / 32].  Rows may be strided."""
+    dt = _mx_dtype(x, "x")
+    qs, ss = _mx_code_shape(x.shape, bits)
+    rows, cols, stride = _mx_rows(x, "x")
+    q = _mx_out(q, qs, torch.uint8, x.device, "q")
+    scale = _mx_out(scale, ss, torch.uint8, x.device, "scale")
+    _check(lib().moe_quantize_mx(_ptr(x), dt, rows, cols, stride, bits, _ptr(q), _ptr(scale),
+                                 _stream(stream)))
+    return q, scale
+
+
+def moe_dequantize_mx(q, scale, bits=4, dtype=torch.bfloat16, out=None, stream=None):
+    """The values [..., K] that MX codes and scales stand for, in dtype."""
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    cols = _mx_codes(q, scale, bits, "q")
+    out = _mx_out(out, (*q.shape[:-1], cols), dtype, q.device, "out")
+    _check(lib().moe_dequantize_mx(_ptr(q), _ptr(scale), out.numel() // cols, cols, bits,
+                                   _ptr(out), _DTYPES[dtype], _stream(stream)))
+    return out
+
+
+def moe_rmsnorm_mx(x, weight, eps=1e-6, residual=None, bits=8, want_y=False, residual_out=None,
+                   y=None, q=None, scale=None, stream=None):
+    """Residual addition, RMS norm and MX rows (moe_rmsnorm_mx in
+    include/moeq.h): x, residual bf16 or f16 [T, H] (rows may be strided),
+    weight [H] of the same dtype or float32 -> (q, scale, x + residual or None,
+    the normed rows or None).  residual_out may be residual (in place)."""
+    half = (torch.bfloat16, torch.float16)
+    dt = _mx_dtype(x, "x", half)
+    if x.dim() != 2:
+        raise ValueError("x must have 2 dims")
+    T, H, xst = _mx_rows(x, "x")
+    _need(weight, weight.dtype if getattr(weight, "dtype", None) in (x.dtype, torch.float32)
+          else x.dtype, "weight", 1)
+    if weight.numel() != H:
+        raise ValueError(f"weight must hold H = {H} values")
+    rst = H
+    if residual is not None:
+        _mx_dtype(residual, "residual", (x.dtype,))
+        if residual.shape != x.shape:
+            raise ValueError(f"residual must be {list(x.shape)}")
+        rst = _mx_rows(residual, "residual")[2]
+    qs, ss = _mx_code_shape(x.shape, bits)
+    q = _mx_out(q, qs, torch.uint8, x.device, "q")
+    scale = _mx_out(scale, ss, torch.uint8, x.device, "scale")
+    if residual is not None or residual_out is not None:
+        residual_out = _mx_out(residual_out, x.shape, x.dtype, x.device, "residual_out")
+    if want_y or y is not None:
+        y = _mx_out(y, x.shape, x.dtype, x.device, "y")
+    _check(lib().moe_rmsnorm_mx(
+        _ptr(x), _ptr(residual), _ptr(weight), dt, int(weight.dtype == torch.float32), T, H, xst,
+        rst, float(eps), _ptr(residual_out), _ptr(y), bits, _ptr(q), _ptr(scale),
+        _stream(stream)))
+    return q, scale, residual_out, y
+
+
+def moe_mx_product_workspace(R, K, N, E=1) -> int:
+    return int(lib().moe_mx_product_workspace(R, K, N, E))
+
+
+def moe_mx_product(a, a_scale, w, w_scale, expert_offsets=None, a_bits=8, out=None,
+                   out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """MX rows [R, K] grouped by expert (expert_offsets int32 [E + 1]) times
+    4-bit MX weights [E, N, K]: [R, N].  Without expert_offsets w is [N, K] (or
+    [1, N, K]): a dense product."""
+    K = _mx_codes(a, a_scale, a_bits, "a")
+    if a.dim() != 2:
+        raise ValueError("a must have 2 dims")
+    if _mx_codes(w, w_scale, 4, "w") != K:
+        raise ValueError("a and w must have rows of the same length")
+    if w.dim() not in (2, 3):
+        raise ValueError("w must have 2 or 3 dims")
+    E = w.shape[0] if w.dim() == 3 else 1
+    N = w.shape[-2]
+    R = a.shape[0]
+    if expert_offsets is not None:
+        _need(expert_offsets, torch.int32, "expert_offsets", 1)
+        if expert_offsets.numel() != E + 1:
+            raise ValueError(f"expert_offsets must hold E + 1 = {E + 1} values")
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _DTYPES:
+        raise TypeError(f"out must be bfloat16, float16 or float32, got {out_dtype}")
+    out = _mx_out(out, (R, N), out_dtype, a.device, "out")
+    need = moe_mx_product_workspace(R, K, N, E)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+    _check(lib().moe_mx_product(
+        _ptr(a), _ptr(a_scale), a_bits, R, K, N, E, _ptr(w), _ptr(w_scale), _ptr(expert_offsets),
+        _ptr(out), _DTYPES[out_dtype], _ptr(workspace),
+        0 if workspace is None else workspace.numel(), _stream(stream)))
+    return out
+
+
+def moe_mx_forward_workspace(T, H, I, E, k, a_bits=8) -> int:
+    return int(lib().moe_mx_forward_workspace(T, H, I, E, k, a_bits))
+
+
+def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out=None,
+                   out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """The fused expert MLP with 4-bit MX experts on MX activations
+    (moe_mx_forward in include/moeq.h): a [T, H] with a_bits, w13 [E, 2I, H], w2
+    [E, H, I], topk_w / topk_ids [T, k] -> [T, H] bf16 or f16."""
+    H = _mx_codes(a, a_scale, a_bits, "a")
+    if a.dim() != 2:
+        raise ValueError("a must have 2 dims")
+    T = a.shape[0]
+    if _mx_codes(w13, s13, 4, "w13") != H:
+        raise ValueError(f"w13 must have rows of H = {H} elements")
+    I = _mx_codes(w2, s2, 4, "w2")
+    if w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("w13 and w2 must have 3 dims")
+    E = w13.shape[0]
+    if tuple(w13.shape[:2]) != (E, 2 * I) or tuple(w2.shape[:2]) != (E, H):
+        raise ValueError("w13 must be [E, 2I, H] and w2 [E, H, I]")
+    _need(topk_w, torch.float32, "topk_w", 2)
+    _need(topk_ids, torch.int32, "topk_ids", 2)
+    k = topk_ids.shape[1]
+    if topk_ids.shape[0] != T or topk_w.shape != topk_ids.shape:
+        raise ValueError(f"topk_w and topk_ids must be [{T}, k]")
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"out must be bfloat16 or float16, got {out_dtype}")
+    out = _mx_out(out, (T, H), out_dtype, a.device, "out")
+    if workspace is None:
+        need = moe_mx_forward_workspace(T, H, I, E, k, a_bits)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=a.device)
+    _need(workspace, torch.uint8, "workspace")
+    _check(lib().moe_mx_forward(
+        _ptr(a), _ptr(a_scale), a_bits, T, H, I, E, k, _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2),
+        _ptr(topk_w), _ptr(topk_ids), _ptr(out), _DTYPES[out_dtype], _ptr(workspace),
+        workspace.numel(), _stream(stream)))
     return out

@@ -1,6 +1,7 @@
 // C ABI of libmoeq.so: argument validation, workspace layout and launches.
 // Every exported function is declared, with its contract, in include/moeq.h.
 #include "common.cuh"
+#include "mx.cuh"
 
 #include <atomic>
 #include <cmath>
@@ -637,4 +638,265 @@ MQ_EXPORT int moe_quant_forward_logits_ex(const void* x, const float* router_log
   if (T > 0 && !router_logits) return fail(MQ_ERR_INVALID_ARG, "null router_logits");
   return forward_impl(x, T, H, I, E, k, bits, group_size, has_zp, w13, w2, s13, s2, z13, z2,
                       nullptr, nullptr, router_logits, ro, workspace, ws_bytes, out, flags, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Microscaled formats.
+// ---------------------------------------------------------------------------
+static bool dtype_ok(int dtype) {
+  return dtype == MQ_DTYPE_BF16 || dtype == MQ_DTYPE_F16 || dtype == MQ_DTYPE_F32;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks that the quantiser and its inverse share.
+static int mx_args(const void* x, int dtype, int64_t rows, int64_t cols, int bits,
+                   const uint8_t* q, const uint8_t* scale) {
+  if (!dtype_ok(dtype)) return fail(MQ_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (bits != 4 && bits != 8) return fail(MQ_ERR_INVALID_ARG, "bits must be 4 or 8");
+  if (rows < 0) return fail(MQ_ERR_INVALID_ARG, "rows must be >= 0");
+  if (cols <= 0 || cols % 32) return fail(MQ_ERR_INVALID_ARG, "cols must be a positive multiple of 32");
+  if (rows == 0) return MQ_OK;
+  if (cols > (int64_t(1) << 40) / rows) return fail(MQ_ERR_UNSUPPORTED, "too many elements");
+  if (!x || !q || !scale) return fail(MQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(q) || !aligned4(scale))
+    return fail(MQ_ERR_INVALID_ARG, "x / out and q must be 16-byte aligned, scale 4-byte");
+  return MQ_OK;
+}
+
+MQ_EXPORT int moe_quantize_mx(const void* x, int dtype, int64_t rows, int64_t cols,
+                              int64_t row_stride, int bits, uint8_t* q, uint8_t* scale,
+                              void* stream) {
+  const int rc = mx_args(x, dtype, rows, cols, bits, q, scale);
+  if (rc != MQ_OK) return rc;
+  if (row_stride < cols || row_stride % 8)
+    return fail(MQ_ERR_INVALID_ARG, "row_stride must be a multiple of 8, at least cols");
+  if (rows == 0) return MQ_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  LaunchScope ls(MQ_PROF_QUANT, st);
+  const cudaError_t err = launch_quant_mx(x, dtype, rows, cols, row_stride, bits, q, scale, st);
+  return err == cudaSuccess ? MQ_OK : cuda_fail(err, "quantize_mx launch");
+}
+
+MQ_EXPORT int moe_dequantize_mx(const uint8_t* q, const uint8_t* scale, int64_t rows,
+                                int64_t cols, int bits, void* out, int dtype, void* stream) {
+  const int rc = mx_args(out, dtype, rows, cols, bits, q, scale);
+  if (rc != MQ_OK || rows == 0) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  LaunchScope ls(MQ_PROF_QUANT, st);
+  const cudaError_t err = launch_dequant_mx(q, scale, rows * cols, bits, out, dtype, st);
+  return err == cudaSuccess ? MQ_OK : cuda_fail(err, "dequantize_mx launch");
+}
+
+MQ_EXPORT int moe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int dtype,
+                             int weight_f32, int T, int H, int64_t x_stride,
+                             int64_t residual_stride, float eps, void* residual_out, void* y_out,
+                             int bits, uint8_t* q, uint8_t* scale, void* stream) {
+  if (!dtype_ok(dtype)) return fail(MQ_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (dtype == MQ_DTYPE_F32) return fail(MQ_ERR_UNSUPPORTED, "rows must be bfloat16 or float16");
+  if (bits != 4 && bits != 8) return fail(MQ_ERR_INVALID_ARG, "bits must be 4 or 8");
+  if (T < 0) return fail(MQ_ERR_INVALID_ARG, "T must be >= 0");
+  if (H <= 0 || H % 32) return fail(MQ_ERR_INVALID_ARG, "H must be a positive multiple of 32");
+  if (H > 32768) return fail(MQ_ERR_UNSUPPORTED, "H must be at most 32768");
+  if (!(eps >= 0.0f) || !std::isfinite(eps))
+    return fail(MQ_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (x_stride < H || x_stride % 8 || (residual && (residual_stride < H || residual_stride % 8)))
+    return fail(MQ_ERR_INVALID_ARG, "row strides must be multiples of 8, at least H");
+  if (T == 0) return MQ_OK;
+  if (!x || !weight || !q || !scale) return fail(MQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || (residual && !aligned16(residual)) || !aligned16(weight) ||
+      (residual_out && !aligned16(residual_out)) || (y_out && !aligned16(y_out)) ||
+      !aligned16(q) || !aligned4(scale))
+    return fail(MQ_ERR_INVALID_ARG, "pointers must be 16-byte aligned, scale 4-byte");
+  if ((residual_out == x && x_stride != H) ||
+      (residual_out && residual_out == residual && residual_stride != H))
+    return fail(MQ_ERR_INVALID_ARG, "residual_out may be x or residual only where that is dense");
+  NormArgs a;
+  a.x = x; a.residual = residual; a.weight = weight;
+  a.dtype = dtype; a.weight_f32 = weight_f32 ? 1 : 0;
+  a.T = T; a.H = H;
+  a.x_stride = x_stride; a.residual_stride = residual_stride;
+  a.eps = eps;
+  a.residual_out = residual_out; a.y = y_out;
+  a.bits = bits; a.q = q; a.scale = scale;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  LaunchScope ls(MQ_PROF_NORM, st);
+  const cudaError_t err = launch_rmsnorm_mx(a, st);
+  return err == cudaSuccess ? MQ_OK : cuda_fail(err, "rmsnorm_mx launch");
+}
+
+static bool mx_product_sizes_ok(int64_t R, int K, int N, int E) {
+  return R >= 0 && K > 0 && N > 0 && E >= 1 && K % 128 == 0 && E <= 1024 &&
+         R < (int64_t(1) << 30);
+}
+
+MQ_EXPORT size_t moe_mx_product_workspace(int64_t R, int K, int N, int E) {
+  if (!mx_product_sizes_ok(R, K, N, E) || R == 0) return 0;
+  const MxPlan pl = mx_plan(R, E, K, N, false);
+  return pl.splits > 1 ? align256(sizeof(float) * (size_t)pl.splits * (size_t)R * (size_t)N) : 0;
+}
+
+MQ_EXPORT int moe_mx_product(const uint8_t* a, const uint8_t* a_scale, int a_bits, int64_t R,
+                             int K, int N, int E, const uint8_t* w, const uint8_t* w_scale,
+                             const int32_t* expert_offsets, void* out, int out_dtype,
+                             void* workspace, size_t ws_bytes, void* stream) {
+  if (R < 0 || K <= 0 || N <= 0 || E < 1) return fail(MQ_ERR_INVALID_ARG, "bad R, K, N or E");
+  if (a_bits != 4 && a_bits != 8) return fail(MQ_ERR_INVALID_ARG, "a_bits must be 4 or 8");
+  if (!dtype_ok(out_dtype)) return fail(MQ_ERR_INVALID_ARG, "unknown out_dtype %d", out_dtype);
+  if (!mx_product_sizes_ok(R, K, N, E))
+    return fail(MQ_ERR_UNSUPPORTED, "need K %% 128 == 0, E <= 1024 and R < 2^30");
+  if (!expert_offsets && E != 1)
+    return fail(MQ_ERR_INVALID_ARG, "expert_offsets may be NULL with E = 1 only");
+  if (R == 0) return MQ_OK;
+  if (!a || !a_scale || !w || !w_scale || !out) return fail(MQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(a) || !aligned16(a_scale) || !aligned16(w_scale) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(w) & 31u) || (expert_offsets && !aligned4(expert_offsets)))
+    return fail(MQ_ERR_INVALID_ARG,
+                "pointers must be 16-byte aligned, w 32-byte, expert_offsets 4-byte");
+  const MxPlan pl = mx_plan(R, E, K, N, false);
+  const size_t need = moe_mx_product_workspace(R, K, N, E);
+  if (need && (!workspace || ws_bytes < need))
+    return fail(MQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace ? ws_bytes : 0, need);
+  if (need && !aligned16(workspace))
+    return fail(MQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MxGemm g = {};
+  g.a_bits = a_bits;
+  g.epi = pl.splits > 1 ? MX_EPI_PART : MX_EPI_OUT;
+  g.a = a; g.a_scale = a_scale; g.w = w; g.w_scale = w_scale;
+  g.R = R; g.S = R; g.E = E; g.K = K; g.N = N; g.wrows = N;
+  g.seg_start = expert_offsets;
+  g.out = out; g.out_dtype = out_dtype;
+  g.part = static_cast<float*>(workspace); g.part_rows = R;
+  g.status = status_ptr();
+  cudaError_t err;
+  {
+    LaunchScope ls(MQ_PROF_GEMM1, st);
+    err = launch_mx_gemm(g, pl, st);
+  }
+  if (err != cudaSuccess) return cuda_fail(err, "mx_product launch");
+  if (pl.splits > 1) {
+    LaunchScope ls(MQ_PROF_COMBINE, st);
+    err = launch_mx_reduce(g.part, pl.splits, R, N, expert_offsets, E, out, out_dtype, st);
+    if (err != cudaSuccess) return cuda_fail(err, "mx_product: reduce launch");
+  }
+  return MQ_OK;
+}
+
+namespace {
+
+struct MxLayout {
+  size_t sorted, block_expert, offsets, num_padded, counts, xa, xs, act, act_s, y, total;
+  int64_t cap;
+  MxPlan up, down;
+};
+
+MxLayout mx_layout(int T, int H, int I, int E, int k, int bits) {
+  MxLayout L;
+  const int64_t S = (int64_t)T * k;
+  L.up = mx_plan(S, E, H, I, true);
+  L.down = mx_plan(S, E, I, H, false);
+  const int64_t cap = moe_align_capacity(T, k, E, kAlignBlock);
+  L.cap = cap;
+  size_t off = 0;
+  L.sorted = off;       off += align256(sizeof(int32_t) * (size_t)cap);
+  L.block_expert = off; off += align256(sizeof(int32_t) * (size_t)(cap / kAlignBlock));
+  L.offsets = off;      off += align256(sizeof(int32_t) * (size_t)(E + 1));
+  L.num_padded = off;   off += align256(sizeof(int32_t));
+  L.counts = off;       off += align256(sizeof(int32_t) * (size_t)E);
+  L.xa = off;           off += align256((size_t)cap * (size_t)H * bits / 8);
+  L.xs = off;           off += align256((size_t)cap * (size_t)H / 32);
+  L.act = off;          off += align256((size_t)cap * (size_t)I * bits / 8);
+  L.act_s = off;        off += align256((size_t)cap * (size_t)I / 32);
+  L.y = off;            off += align256(sizeof(float) * (size_t)L.down.splits * (size_t)S * (size_t)H);
+  L.total = off;
+  return L;
+}
+
+}  // namespace
+
+MQ_EXPORT size_t moe_mx_forward_workspace(int T, int H, int I, int E, int k, int a_bits) {
+  if (T < 0 || H <= 0 || I <= 0 || E < 1 || k < 1 || k > E || (a_bits != 4 && a_bits != 8)) return 0;
+  return mx_layout(T, H, I, E, k, a_bits).total;
+}
+
+MQ_EXPORT int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bits, int T, int H,
+                             int I, int E, int k, const uint8_t* w13, const uint8_t* s13,
+                             const uint8_t* w2, const uint8_t* s2, const float* topk_w,
+                             const int32_t* topk_ids, void* out, int out_dtype, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  if (T < 0 || H <= 0 || I <= 0 || E < 1) return fail(MQ_ERR_INVALID_ARG, "bad T, H, I or E");
+  if (k < 1 || k > E || k > 32) return fail(MQ_ERR_INVALID_ARG, "need 1 <= k <= min(E, 32)");
+  if (a_bits != 4 && a_bits != 8) return fail(MQ_ERR_INVALID_ARG, "a_bits must be 4 or 8");
+  if (out_dtype != MQ_DTYPE_BF16 && out_dtype != MQ_DTYPE_F16)
+    return fail(MQ_ERR_INVALID_ARG, "out_dtype must be MQ_DTYPE_BF16 or MQ_DTYPE_F16");
+  if (E > 1024) return fail(MQ_ERR_UNSUPPORTED, "E must be <= 1024");
+  if (H % 128 || I % 128) return fail(MQ_ERR_UNSUPPORTED, "H and I must be multiples of 128");
+  if ((int64_t)T * k > (int64_t(1) << 24)) return fail(MQ_ERR_UNSUPPORTED, "too many token-slots");
+  if (T == 0) return MQ_OK;
+  if (!a || !a_scale || !w13 || !s13 || !w2 || !s2 || !topk_w || !topk_ids || !out || !workspace)
+    return fail(MQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(a) || !aligned16(a_scale) || !aligned16(s13) || !aligned16(s2) ||
+      !aligned16(out) || !aligned16(workspace) || !aligned4(topk_w) || !aligned4(topk_ids) ||
+      (reinterpret_cast<uintptr_t>(w13) & 31u) || (reinterpret_cast<uintptr_t>(w2) & 31u))
+    return fail(MQ_ERR_INVALID_ARG, "pointers must be 16-byte aligned, w13 and w2 32-byte");
+  const MxLayout L = mx_layout(T, H, I, E, k, a_bits);
+  if (ws_bytes < L.total)
+    return fail(MQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws_bytes, L.total);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int32_t* sorted = reinterpret_cast<int32_t*>(ws + L.sorted);
+  int32_t* offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
+  int32_t* num_padded = reinterpret_cast<int32_t*>(ws + L.num_padded);
+  int32_t* counts = reinterpret_cast<int32_t*>(ws + L.counts);
+  unsigned* status = status_ptr();
+  const int S = T * k;
+  cudaError_t err;
+  {
+    LaunchScope ls(MQ_PROF_ALIGN, st);
+    err = launch_align(topk_ids, T, k, E, kAlignBlock, sorted,
+                       reinterpret_cast<int32_t*>(ws + L.block_expert), offsets, num_padded,
+                       status, st, 0, nullptr, nullptr, counts);
+  }
+  if (err != cudaSuccess) return cuda_fail(err, "mx_forward: align launch");
+  {
+    LaunchScope ls(MQ_PROF_GATHER, st);
+    err = launch_mx_gather(a, a_scale, H * a_bits / 8, H / 32, sorted, num_padded, k, S, L.cap,
+                           ws + L.xa, ws + L.xs, st);
+  }
+  if (err != cudaSuccess) return cuda_fail(err, "mx_forward: gather launch");
+  MxGemm g = {};
+  g.a_bits = a_bits;
+  g.R = L.cap; g.S = S; g.E = E;
+  g.seg_start = offsets; g.seg_count = counts;
+  g.status = status;
+  g.epi = MX_EPI_GATED;
+  g.a = ws + L.xa; g.a_scale = ws + L.xs; g.w = w13; g.w_scale = s13;
+  g.K = H; g.N = I; g.wrows = 2 * I;
+  g.act = ws + L.act; g.act_scale = ws + L.act_s;
+  {
+    LaunchScope ls(MQ_PROF_GEMM1, st);
+    err = launch_mx_gemm(g, L.up, st);
+  }
+  if (err != cudaSuccess) return cuda_fail(err, "mx_forward: gate/up launch");
+  g.epi = MX_EPI_PART;
+  g.a = ws + L.act; g.a_scale = ws + L.act_s; g.w = w2; g.w_scale = s2;
+  g.K = I; g.N = H; g.wrows = H;
+  g.part = reinterpret_cast<float*>(ws + L.y); g.part_rows = S;
+  g.dest = sorted; g.dest_w = topk_w;
+  {
+    LaunchScope ls(MQ_PROF_GEMM2, st);
+    err = launch_mx_gemm(g, L.down, st);
+  }
+  if (err != cudaSuccess) return cuda_fail(err, "mx_forward: down launch");
+  MoeArgs m = {};
+  m.T = T; m.H = H; m.I = I; m.E = E; m.k = k;
+  m.topk_ids = topk_ids;
+  m.flags = out_dtype == MQ_DTYPE_F16 ? MQ_FWD_ACT_F16 : 0;
+  m.out = out;
+  {
+    LaunchScope ls(MQ_PROF_COMBINE, st);
+    err = launch_combine_splits(m, g.part, L.down.splits, st);
+  }
+  return err == cudaSuccess ? MQ_OK : cuda_fail(err, "mx_forward: combine launch");
 }

@@ -1,0 +1,735 @@
+// Rows grouped by expert times 4-bit microscaled weights, on the block-scaled
+// tensor-core instructions.
+//
+//   out[r, n] = sum_k A[r, k] * W[e(r), n, k]
+//
+// A: E4M3 or E2M1 rows, W: E2M1 [E, N, K], each with one E8M0 scale per 32
+// consecutive k.  tcgen05.mma takes the codes and the scales as they are and
+// accumulates in float32, so nothing is converted on the way.
+//
+// One persistent CTA per SM.  D[128 weight rows x BN rows of A]: the weights
+// are the instruction's A operand (M = 128) and the token rows its B operand
+// (N = BN), so that a few rows cost a narrow tile and no padding.  A unit is
+// (expert, chunk of at most BN rows, weight tile, K split).  NACC = 2: a unit
+// holds two weight tiles (gate and up) that share its token rows.
+//
+// Roles: warp 0 streams codes by TMA; warp 1 issues the MMAs; warps 2-3 bring
+// the scales; warps 4-11 are the epilogue.
+//   * Codes.  A stage holds 128 bytes of each row, 128-byte swizzled: 128 k of
+//     E4M3 rows against 128 k of weights whose nibbles TMA spreads to 16-byte
+//     groups (the operand form of the mixed 8/4-bit instruction), or 256 k of
+//     both in 4 bits.  Four MMAs per stage and weight tile either way.
+//   * Scales.  The instruction reads them from tensor memory, 4 scale bytes
+//     (128 k, a "word") per row, row r in lane r % 32 and column r / 32.  The
+//     scale warps read the rows' scale bytes (16 bytes = 512 k per row), and
+//     write them to shared memory as that [32 lanes][4 columns] block for each
+//     word; the MMA thread copies a block to tensor memory with one
+//     tcgen05.cp, which the MMAs that follow it in the same thread see.
+//   * Epilogue.  A thread is one weight row (tensor-memory lane) and walks the
+//     columns, the rows of A.  32 lanes are 32 consecutive outputs: exactly
+//     one block when the activations are requantised.
+#include "mx.cuh"
+#include "sm100_ptx.cuh"
+
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+namespace {
+
+using namespace mq::ptx;
+
+constexpr int kTileM = 128;
+constexpr int kABytes = kTileM * 128;  // one weight tile of a stage
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kMaxStages = 12;
+constexpr int kSfRing = 4;             // scale slots, 512 k each
+constexpr int kMaxE = 1024;
+constexpr int kGroup = 8;              // weight tiles that a chunk walk shares
+constexpr unsigned long long kWaitNs = 1000000000ull;
+constexpr size_t kSmemMax = 227 * 1024;
+
+template <int BITS, int NACC, int BN>
+struct Cfg {
+  static constexpr int kWords = BITS == 8 ? 1 : 2;  // 128-k scale words per stage
+  static constexpr int kPerSb = 4 / kWords;         // stages per scale slot
+  static constexpr int kBBytes = BN * 128;
+  static constexpr int kStageBytes = NACC * kABytes + kBBytes;
+  // bytes TMA reports for a stage: those it reads, so half a weight tile where
+  // it spreads the nibbles
+  static constexpr int kTxBytes = NACC * (BITS == 8 ? kABytes / 2 : kABytes) + kBBytes;
+  static constexpr int kBBlocks = (BN + 127) / 128;
+  static constexpr int kSfWordBytes = (NACC + kBBlocks) * 512;
+  static constexpr int kSfSlotBytes = 4 * kSfWordBytes;
+  static constexpr int kSfCols = 4 * (NACC + kBBlocks) * 4;
+  static constexpr int kAccCols = NACC * BN;
+  static constexpr int kBufs = 2 * kAccCols + kSfCols <= 512 ? 2 : 1;
+  static constexpr int kSfBase = kBufs * kAccCols;
+  static_assert(kSfBase + kSfCols <= 512, "tensor memory");
+  static constexpr size_t kFixed = 1024 + kSfRing * (size_t)kSfSlotBytes + 1024 + (kMaxE + 1) * 4;
+  static constexpr int kFit = (int)((kSmemMax - kFixed) / kStageBytes);
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static_assert(kStages >= 2, "shared memory");
+  // one CTA per SM: each allocates all of tensor memory
+  static constexpr size_t kNeed = kFixed + (size_t)kStages * kStageBytes;
+  static constexpr size_t kSmem = kNeed < 120 * 1024 ? 120 * 1024 : kNeed;
+};
+
+struct Ctl {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t sf_full[kSfRing], sf_empty[kSfRing];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem;
+  volatile int abort_flag;
+};
+static_assert(sizeof(Ctl) <= 1024, "control block");
+
+struct Params {
+  const uint8_t* w_scale;
+  const uint8_t* a_scale;
+  const int32_t* seg_start;
+  const int32_t* seg_count;
+  int E, K, N, R;
+  int up_row;   // weight row of a unit's second tile, relative to its first
+  int wrows;
+  int mtiles, splits, words, sbs;
+  void* out;
+  int out_dtype;
+  float* part;
+  int64_t part_rows;
+  const int32_t* dest;
+  const float* dest_w;
+  uint8_t* act;
+  uint8_t* act_scale;
+  unsigned* status;
+};
+
+struct Unit {
+  int e, row0, n, m, split;  // expert, first row, rows, weight tile, K split
+  bool single;               // the expert has one chunk: its weights are read once
+};
+
+// Rows of expert e, kept inside [0, R) whatever the arrays hold; false where
+// that took a correction.
+__device__ __forceinline__ bool segment(const Params& p, int e, int& start, int& count) {
+  if (!p.seg_start) {
+    start = 0;
+    count = p.R;
+    return true;
+  }
+  const int s = p.seg_start[e];
+  const int64_t end = p.seg_count ? (int64_t)s + p.seg_count[e] : p.seg_start[e + 1];
+  start = min(max(s, 0), p.R);
+  count = (int)(min(max(end, (int64_t)start), (int64_t)p.R) - start);
+  return start == s && start + (int64_t)count == end;
+}
+
+// Unit u of the walk: expert by expert, groups of kGroup weight tiles, every
+// chunk over a group before the next one (the CTAs at work share the group's
+// weights and the chunks' rows in L2), K splits innermost.
+template <int BN>
+__device__ __forceinline__ Unit unit_at(const Params& p, const int* chunk_start, int64_t u) {
+  const int per = p.mtiles * p.splits;
+  const int g = (int)(u / per);  // global chunk-equivalent index: locates the expert
+  int lo = 0, hi = p.E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (chunk_start[mid] <= g) lo = mid;
+    else hi = mid;
+  }
+  Unit w;
+  w.e = lo;
+  const int nch = chunk_start[lo + 1] - chunk_start[lo];
+  const int64_t r = u - (int64_t)chunk_start[lo] * per;
+  const int64_t per_group = (int64_t)kGroup * nch * p.splits;
+  const int grp = (int)(r / per_group);
+  const int64_t rem = r - grp * per_group;
+  const int tiles = min(kGroup, p.mtiles - grp * kGroup) * p.splits;
+  const int c = (int)(rem / tiles);
+  const int t = (int)(rem - (int64_t)c * tiles);
+  w.m = grp * kGroup + t / p.splits;
+  w.split = t % p.splits;
+  int start, count;
+  segment(p, lo, start, count);
+  w.row0 = start + c * BN;
+  w.n = min(BN, count - c * BN);
+  w.single = nch == 1;
+  return w;
+}
+
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, Ctl* ctl,
+                                             unsigned* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = mq::global_timer_ns();
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 63u) == 0) {
+      if (ctl->abort_flag) return false;
+      if (mq::global_timer_ns() - t0 > kWaitNs) {
+        ctl->abort_flag = 1;
+        mq::flag(status, MQ_DEV_WAIT_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Ctl* ctl,
+                                          unsigned* status) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  ok = ok || wait_bounded(bar, parity, ctl, status);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// After an abort: lets what is in flight land; bounded, ignores the flag.
+__device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
+  const unsigned long long t0 = mq::global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (mq::global_timer_ns() - t0 > kWaitNs) return;
+}
+
+// Four scale words (512 k) of one row from word w0 on; words past the row's
+// end are 0 (their codes are 0 too).
+__device__ __forceinline__ uint4 load_words(const uint8_t* row, int w0, int words) {
+  const uint8_t* p = row + (int64_t)w0 * 4;
+  if ((words & 3) == 0) return __ldg(reinterpret_cast<const uint4*>(p));
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if ((words & 1) == 0) {
+    if (w0 < words) {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
+      v.x = a.x;
+      v.y = a.y;
+    }
+    if (w0 + 2 < words) {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(p) + 1);
+      v.z = a.x;
+      v.w = a.y;
+    }
+    return v;
+  }
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+  if (w0 < words) v.x = __ldg(q);
+  if (w0 + 1 < words) v.y = __ldg(q + 1);
+  if (w0 + 2 < words) v.z = __ldg(q + 2);
+  if (w0 + 3 < words) v.w = __ldg(q + 3);
+  return v;
+}
+
+__device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float v) {
+  if (dtype == MQ_DTYPE_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+  else if (dtype == MQ_DTYPE_F16) static_cast<__half*>(out)[i] = __float2half_rn(v);
+  else static_cast<float*>(out)[i] = v;
+}
+
+template <int BITS, int NACC, int BN, int EPI>
+__global__ void __launch_bounds__(kThreads, 1)
+    mx_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+            const Params p) {
+  using C = Cfg<BITS, NACC, BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* stages = smem;
+  uint8_t* sf = stages + (size_t)C::kStages * C::kStageBytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(sf + (size_t)kSfRing * C::kSfSlotBytes);
+  int* chunk_start = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(ctl) + 1024);
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+
+  if (tid == 0) {
+    tma_prefetch_desc(&map_w);
+    tma_prefetch_desc(&map_a);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    for (int i = 0; i < kSfRing; ++i) {
+      mbar_init(&ctl->sf_full[i], 1);
+      mbar_init(&ctl->sf_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->acc_full[i], 1);
+      mbar_init(&ctl->acc_empty[i], kEpiWarps);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem, 512);
+    tmem_relinquish();
+  }
+  mq::pdl_wait();
+  mq::pdl_trigger();
+  if (warp == 2) {  // chunks of each expert, scanned 32 experts at a time
+    int run = 0;
+    bool fine = true;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      int start, count = 0;
+      if (e < p.E) fine &= segment(p, e, start, count);
+      const int mine = (count + BN - 1) / BN;
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      if (e < p.E) chunk_start[e] = run + incl - mine;
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) chunk_start[p.E] = run;
+    if (!fine && blockIdx.x == 0) mq::flag(p.status, MQ_DEV_BAD_OFFSETS);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  const int64_t total = (int64_t)chunk_start[p.E] * p.mtiles * p.splits;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------- codes --
+      const uint64_t pol_once = l2_policy_evict_first();
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t u = blockIdx.x; u < total && ok; u += gridDim.x) {
+        const Unit w = unit_at<BN>(p, chunk_start, u);
+        const int sb0 = (int)((int64_t)p.sbs * w.split / p.splits);
+        const int sb1 = (int)((int64_t)p.sbs * (w.split + 1) / p.splits);
+        const int st0 = sb0 * C::kPerSb;
+        const int st1 = min(sb1 * C::kPerSb, (p.words + C::kWords - 1) / C::kWords);
+        for (int s = st0; s < st1; ++s, ++it) {
+          const uint32_t slot = it % C::kStages;
+          if (!wait_bounded(&ctl->empty[slot], ((it / C::kStages) & 1) ^ 1, ctl, p.status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = stages + (size_t)slot * C::kStageBytes;
+          mbar_arrive_expect_tx(&ctl->full[slot], C::kTxBytes);
+#pragma unroll
+          for (int a = 0; a < NACC; ++a) {
+            const int row = w.m * kTileM + a * p.up_row;
+            if (w.single)
+              tma_load_3d_hint(dst + a * kABytes, &map_w, &ctl->full[slot], s * 128, row, w.e, pol_once);
+            else
+              tma_load_3d(dst + a * kABytes, &map_w, &ctl->full[slot], s * 128, row, w.e);
+          }
+          tma_load_2d(dst + NACC * kABytes, &map_a, &ctl->full[slot], s * 128, w.row0);
+        }
+      }
+      if (ctl->abort_flag) {  // loads in flight land before the CTA goes
+        for (uint32_t j = it < (uint32_t)C::kStages ? 0 : it - C::kStages; j < it; ++j)
+          wait_drain(&ctl->full[j % C::kStages], (j / C::kStages) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // -------------------------------------------------------- MMAs --
+      uint32_t it = 0, sb_it = 0, t = 0;
+      bool ok = true;
+      for (int64_t u = blockIdx.x; u < total && ok; u += gridDim.x, ++t) {
+        const Unit w = unit_at<BN>(p, chunk_start, u);
+        const int sb0 = (int)((int64_t)p.sbs * w.split / p.splits);
+        const int sb1 = (int)((int64_t)p.sbs * (w.split + 1) / p.splits);
+        const int nst = (p.words + C::kWords - 1) / C::kWords;
+        const uint32_t buf = t % C::kBufs;
+        ok = wait_bounded(&ctl->acc_empty[buf], ((t / C::kBufs) & 1) ^ 1, ctl, p.status);
+        tc_fence_after();
+        const uint32_t acc = tmem + buf * C::kAccCols;
+        uint32_t accumulate = 0;
+        for (int sb = sb0; sb < sb1 && ok; ++sb, ++sb_it) {
+          const uint32_t ss = sb_it % kSfRing;
+          ok = wait_bounded(&ctl->sf_full[ss], (sb_it / kSfRing) & 1, ctl, p.status);
+          if (!ok) break;
+          const uint32_t sfa = smem_addr(sf + (size_t)ss * C::kSfSlotBytes);
+          // Scales to tensor memory: blocks of 4 columns, [word][tile].
+#pragma unroll
+          for (int b = 0; b < 4 * (NACC + C::kBBlocks); ++b)
+            tmem_cp_scales(tmem + C::kSfBase + b * 4, smem_desc_scales(sfa + b * 512));
+          const int last = min((sb + 1) * C::kPerSb, nst);
+          for (int s = sb * C::kPerSb; s < last; ++s, ++it) {
+            const uint32_t slot = it % C::kStages;
+            ok = wait_bounded(&ctl->full[slot], (it / C::kStages) & 1, ctl, p.status);
+            if (!ok) break;
+            const uint32_t base = smem_addr(stages + (size_t)slot * C::kStageBytes);
+            const int word0 = (s % C::kPerSb) * C::kWords;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int word = word0 + (BITS == 8 ? 0 : j / 2);
+              const uint32_t id = BITS == 8 ? j : (j & 1) * 2;
+              const uint32_t sfw = tmem + C::kSfBase + word * (NACC + C::kBBlocks) * 4;
+              const uint64_t bd = smem_desc_k_sw128(base + NACC * kABytes) + j * 2;
+#pragma unroll
+              for (int a = 0; a < NACC; ++a) {
+                const uint64_t ad = smem_desc_k_sw128(base + a * kABytes) + j * 2;
+                mma_mx<BITS>(acc + a * BN, ad, bd, idesc_mx<BITS>(kTileM, BN, id),
+                             sfw + a * 4, sfw + NACC * 4, accumulate);
+              }
+              accumulate = 1;
+            }
+            mma_commit(&ctl->empty[slot]);
+          }
+          if (ok) mma_commit(&ctl->sf_empty[ss]);
+        }
+        if (ok) mma_commit(&ctl->acc_full[buf]);
+      }
+      // nothing of this thread may be in flight when the memory goes
+      mma_commit(&ctl->drain);
+      wait_drain(&ctl->drain, 0);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ scales --
+    const int lw = warp - 2;
+    constexpr int kGroupsA = NACC * 4, kGroupsB = (BN + 31) / 32;
+    uint32_t sb_it = 0;
+    bool ok = true;
+    const int64_t row_bytes = (int64_t)p.words * 4;
+    for (int64_t u = blockIdx.x; u < total && ok; u += gridDim.x) {
+      const Unit w = unit_at<BN>(p, chunk_start, u);
+      const int sb0 = (int)((int64_t)p.sbs * w.split / p.splits);
+      const int sb1 = (int)((int64_t)p.sbs * (w.split + 1) / p.splits);
+      for (int sb = sb0; sb < sb1; ++sb, ++sb_it) {
+        if ((int)(sb_it & 1) != lw) continue;
+        uint4 va[kGroupsA], vb[kGroupsB];
+#pragma unroll
+        for (int g = 0; g < kGroupsA; ++g) {
+          const int r = w.m * kTileM + (g & 3) * 32 + lane;  // row of the gate (or only) half
+          const int wr = r + (g >> 2) * p.up_row;
+          va[g] = make_uint4(0, 0, 0, 0);
+          if (wr < p.wrows)
+            va[g] = load_words(p.w_scale + ((int64_t)w.e * p.wrows + wr) * row_bytes, sb * 4, p.words);
+        }
+#pragma unroll
+        for (int g = 0; g < kGroupsB; ++g) {
+          const int r = w.row0 + g * 32 + lane;
+          vb[g] = make_uint4(0, 0, 0, 0);
+          if (g * 32 + lane < w.n)
+            vb[g] = load_words(p.a_scale + (int64_t)r * row_bytes, sb * 4, p.words);
+        }
+        const uint32_t ss = sb_it % kSfRing;
+        if (!warp_wait(&ctl->sf_empty[ss], ((sb_it / kSfRing) & 1) ^ 1, ctl, p.status)) {
+          ok = false;
+          break;
+        }
+        uint8_t* slot = sf + (size_t)ss * C::kSfSlotBytes + lane * 16;
+#pragma unroll
+        for (int g = 0; g < kGroupsA + kGroupsB; ++g) {
+          const uint4 v = g < kGroupsA ? va[g < kGroupsA ? g : 0] : vb[g < kGroupsA ? 0 : g - kGroupsA];
+          const int block = g < kGroupsA ? g >> 2 : NACC + ((g - kGroupsA) >> 2);
+          const int col = g < kGroupsA ? g & 3 : (g - kGroupsA) & 3;
+          uint32_t* d = reinterpret_cast<uint32_t*>(slot + block * 512 + col * 4);
+          d[0 * (C::kSfWordBytes / 4)] = v.x;
+          d[1 * (C::kSfWordBytes / 4)] = v.y;
+          d[2 * (C::kSfWordBytes / 4)] = v.z;
+          d[3 * (C::kSfWordBytes / 4)] = v.w;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->sf_full[ss]);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue --
+    const int ew = warp - 4;
+    const int quad = warp & 3;  // the tensor-memory lanes this warp may read
+    const int half = ew >> 2;   // which 16-column steps it takes
+    uint32_t t = 0;
+    for (int64_t u = blockIdx.x; u < total; u += gridDim.x, ++t) {
+      const Unit w = unit_at<BN>(p, chunk_start, u);
+      const uint32_t buf = t % C::kBufs;
+      if (!warp_wait(&ctl->acc_full[buf], (t / C::kBufs) & 1, ctl, p.status)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + buf * C::kAccCols + ((uint32_t)(quad * 32) << 16);
+      const int n = w.m * kTileM + quad * 32 + lane;  // this lane's output
+      for (int c0 = half * 16; c0 < w.n; c0 += 32) {
+        uint32_t v0[16];
+        tmem_ld16_sync(acc + c0, v0);
+        if constexpr (EPI == MX_EPI_GATED) {
+          uint32_t v1[16];
+          tmem_ld16_sync(acc + BN + c0, v1);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (c0 + j >= w.n) break;  // warp-uniform
+            const float g = __uint_as_float(v0[j]), up = __uint_as_float(v1[j]);
+            const float a = __fdividef(g, 1.0f + __expf(-g)) * up;
+            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(a) & 0x7fffffffu);
+            const uint32_t code = mq::mx_scale_code<BITS>(m);
+            const float s = mq::mx_scaled(a, mq::mx_inv_scale(code));
+            const int64_t row = w.row0 + c0 + j;
+            if (BITS == 8) {
+              if (n < p.N) p.act[row * p.N + n] = (uint8_t)mq::e4m3x2(s, 0.0f);
+            } else {
+              const float hi = __shfl_down_sync(0xffffffffu, s, 1);
+              if ((lane & 1) == 0 && n < p.N) p.act[(row * p.N + n) >> 1] = (uint8_t)mq::e2m1x2(s, hi);
+            }
+            if (lane == 0 && n < p.N) p.act_scale[row * (p.N >> 5) + (n >> 5)] = (uint8_t)code;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (c0 + j >= w.n) break;
+            float v = __uint_as_float(v0[j]);
+            int64_t row = w.row0 + c0 + j;
+            if (EPI == MX_EPI_PART) {
+              if (p.dest) row = p.dest[row];
+              if (p.dest_w) v *= p.dest_w[row];
+              if (n < p.N) p.part[(w.split * p.part_rows + row) * p.N + n] = v;
+            } else if (n < p.N) {
+              store_out(p.out, p.out_dtype, row * p.N + n, v);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->acc_empty[buf]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float4 v);
+template <>
+__device__ __forceinline__ void store4(float* p, float4 v) {
+  *reinterpret_cast<float4*>(p) = v;
+}
+template <>
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+}
+template <>
+__device__ __forceinline__ void store4(__half* p, float4 v) {
+  __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+}
+
+// Sums the K splits in their order and rounds once; four outputs per thread.
+// With an odd N a group may cross rows and the splits are not 16-byte aligned:
+// one at a time then.
+template <typename T>
+__global__ void __launch_bounds__(256) mx_reduce(const float* __restrict__ part, int splits,
+                                                 int64_t rows, int N,
+                                                 const int32_t* __restrict__ offsets, int E,
+                                                 T* __restrict__ out) {
+  mq::pdl_wait();
+  mq::pdl_trigger();
+  const int64_t n = rows * N;
+  const int64_t lo = offsets ? min((int64_t)max(offsets[0], 0), rows) * N : 0;
+  const int64_t hi = offsets ? min((int64_t)max(offsets[E], 0), rows) * N : n;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if ((N & 3) == 0) {
+    if (i < lo || i >= hi) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < splits; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(part + k * n + i);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    store4(out + i, s);
+  } else {
+    for (int64_t j = max(i, lo); j < min(i + 4, hi); ++j) {
+      float s = 0.f;
+      for (int k = 0; k < splits; ++k) s += part[k * n + j];
+      out[j] = (T)s;
+    }
+  }
+}
+
+// One warp per row; 16-byte pieces of the codes, 4-byte words of the scales.
+__global__ void __launch_bounds__(256) mx_gather(const uint8_t* __restrict__ a,
+                                                 const uint8_t* __restrict__ a_scale,
+                                                 int row_bytes, int scale_bytes,
+                                                 const int32_t* __restrict__ sorted,
+                                                 const int32_t* __restrict__ num_padded, int k,
+                                                 int S, uint8_t* __restrict__ dst,
+                                                 uint8_t* __restrict__ dst_scale) {
+  mq::pdl_wait();
+  mq::pdl_trigger();
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= *num_padded) return;
+  const int s = sorted[row];
+  if (s >= S) return;  // padding
+  const int lane = threadIdx.x & 31;
+  const int64_t t = s / k;
+  const uint4* src = reinterpret_cast<const uint4*>(a + t * row_bytes);
+  uint4* d = reinterpret_cast<uint4*>(dst + row * row_bytes);
+#pragma unroll 4
+  for (int i = lane; i < row_bytes / 16; i += 32) d[i] = __ldg(src + i);
+  const uint32_t* ss = reinterpret_cast<const uint32_t*>(a_scale + t * scale_bytes);
+  uint32_t* ds = reinterpret_cast<uint32_t*>(dst_scale + row * scale_bytes);
+  for (int i = lane; i < scale_bytes / 4; i += 32) ds[i] = __ldg(ss + i);
+}
+
+// ------------------------------------------------------------ host side --
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+cudaError_t get_encoder() {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return g_encode ? cudaSuccess : cudaErrorNotSupported;
+}
+
+cudaError_t make_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base,
+                     const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t ones[3] = {1, 1, 1};
+  const CUresult r = g_encode(map, dt, rank, const_cast<void*>(base), dims, strides, box, ones,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int BITS, int NACC, int BN, int EPI>
+cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Params& p,
+                       int64_t units, cudaStream_t st) {
+  constexpr size_t smem = Cfg<BITS, NACC, BN>::kSmem;
+  static_assert(smem <= kSmemMax, "shared memory");
+  auto kern = mx_gemm<BITS, NACC, BN, EPI>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  const int sms = tc_num_sms();
+  const int grid = units < sms ? (int)units : sms;
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mw, ma, p);
+}
+
+template <int BITS, int EPI>
+cudaError_t launch_bn(int bn, const CUtensorMap& mw, const CUtensorMap& ma, const Params& p,
+                      int64_t units, cudaStream_t st) {
+  constexpr int NACC = EPI == MX_EPI_GATED ? 2 : 1;
+  switch (bn) {
+    case 16: return launch_one<BITS, NACC, 16, EPI>(mw, ma, p, units, st);
+    case 32: return launch_one<BITS, NACC, 32, EPI>(mw, ma, p, units, st);
+    case 64: return launch_one<BITS, NACC, 64, EPI>(mw, ma, p, units, st);
+    default: return launch_one<BITS, NACC, 96, EPI>(mw, ma, p, units, st);
+  }
+}
+
+template <int BITS>
+cudaError_t launch_epi(const MxGemm& g, int bn, const CUtensorMap& mw, const CUtensorMap& ma,
+                       const Params& p, int64_t units, cudaStream_t st) {
+  switch (g.epi) {
+    case MX_EPI_OUT: return launch_bn<BITS, MX_EPI_OUT>(bn, mw, ma, p, units, st);
+    case MX_EPI_PART: return launch_bn<BITS, MX_EPI_PART>(bn, mw, ma, p, units, st);
+    default: return launch_bn<BITS, MX_EPI_GATED>(bn, mw, ma, p, units, st);
+  }
+}
+
+}  // namespace
+
+MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated) {
+  MxPlan pl;
+  const int64_t live = S < E ? S : E;
+  const int64_t avg = live > 0 ? (S + live - 1) / live : 0;
+  pl.bn = avg <= 8 ? 16 : avg <= 20 ? 32 : avg <= 64 ? 64 : 96;
+  pl.splits = 1;
+  if (!gated) {
+    // K splits of at least 1024 k while the units leave SMs idle
+    const int64_t chunks = live > 0 ? std::max(live, (S + pl.bn - 1) / pl.bn) : 1;
+    const int64_t units = chunks * ((N + kTileM - 1) / kTileM);
+    const int most = std::max(1, K / 1024);
+    const int sms = tc_num_sms();
+    if (units < 3 * sms)
+      pl.splits = (int)std::min<int64_t>(std::min(most, 8), std::max<int64_t>(1, 4 * sms / std::max<int64_t>(1, units)));
+  }
+  return pl;
+}
+
+cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStream_t st) {
+  cudaError_t err = get_encoder();
+  if (err != cudaSuccess) return err;
+  const bool gated = g.epi == MX_EPI_GATED;
+  CUtensorMap mw, ma;
+  {
+    // 8-bit rows: the weights' nibbles are spread to the mixed instruction's
+    // operand form on the way; 4-bit rows: packed bytes, as both operands are
+    const bool spread = g.a_bits == 8;
+    const cuuint64_t kw = spread ? g.K : g.K / 2;
+    const cuuint64_t dims[3] = {kw, (cuuint64_t)g.wrows, (cuuint64_t)g.E};
+    const cuuint64_t strides[2] = {(cuuint64_t)g.K / 2, (cuuint64_t)g.K / 2 * g.wrows};
+    const cuuint32_t box[3] = {128, kTileM, 1};
+    err = make_map(&mw, spread ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                   3, g.w, dims, strides, box);
+    if (err != cudaSuccess) return err;
+    const cuuint64_t row = (cuuint64_t)g.K * g.a_bits / 8;
+    const cuuint64_t adims[2] = {row, (cuuint64_t)g.R};
+    const cuuint32_t abox[2] = {128, (cuuint32_t)pl.bn};
+    err = make_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, g.a, adims, &row, abox);
+    if (err != cudaSuccess) return err;
+  }
+  Params p = {};
+  p.w_scale = g.w_scale;
+  p.a_scale = g.a_scale;
+  p.seg_start = g.seg_start;
+  p.seg_count = g.seg_count;
+  p.E = g.E;
+  p.K = g.K;
+  p.N = g.N;
+  p.R = (int)g.R;
+  p.up_row = gated ? g.N : 0;
+  p.wrows = g.wrows;
+  p.mtiles = (g.N + kTileM - 1) / kTileM;
+  p.splits = pl.splits;
+  p.words = g.K / 128;
+  p.sbs = (p.words + 3) / 4;
+  p.out = g.out;
+  p.out_dtype = g.out_dtype;
+  p.part = g.part;
+  p.part_rows = g.part_rows;
+  p.dest = g.dest;
+  p.dest_w = g.dest_w;
+  p.act = g.act;
+  p.act_scale = g.act_scale;
+  p.status = g.status;
+  const int64_t live = g.S < g.E ? g.S : g.E;
+  const int64_t units = (live + g.S / pl.bn) * p.mtiles * p.splits;  // at most
+  if (units <= 0) return cudaSuccess;
+  return g.a_bits == 8 ? launch_epi<8>(g, pl.bn, mw, ma, p, units, st)
+                       : launch_epi<4>(g, pl.bn, mw, ma, p, units, st);
+}
+
+cudaError_t launch_mx_reduce(const float* part, int splits, int64_t rows, int N,
+                             const int32_t* offsets, int E, void* out, int out_dtype,
+                             cudaStream_t st) {
+  const dim3 grid((unsigned)((rows * N + 1023) / 1024)), block(256);
+  switch (out_dtype) {
+    case MQ_DTYPE_BF16:
+      return launch_pdl(mx_reduce<__nv_bfloat16>, grid, block, 0, st, part, splits, rows, N,
+                        offsets, E, static_cast<__nv_bfloat16*>(out));
+    case MQ_DTYPE_F16:
+      return launch_pdl(mx_reduce<__half>, grid, block, 0, st, part, splits, rows, N, offsets, E,
+                        static_cast<__half*>(out));
+    default:
+      return launch_pdl(mx_reduce<float>, grid, block, 0, st, part, splits, rows, N, offsets, E,
+                        static_cast<float*>(out));
+  }
+}
+
+cudaError_t launch_mx_gather(const uint8_t* a, const uint8_t* a_scale, int row_bytes,
+                             int scale_bytes, const int32_t* sorted, const int32_t* num_padded,
+                             int k, int S, int64_t cap, uint8_t* dst, uint8_t* dst_scale,
+                             cudaStream_t st) {
+  return launch_pdl(mx_gather, dim3((unsigned)((cap + 7) / 8)), dim3(256), 0, st, a, a_scale,
+                    row_bytes, scale_bytes, sorted, num_padded, k, S, dst, dst_scale);
+}

@@ -98,6 +98,31 @@ __device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                                 int c0, int c1, int c2, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2),
+      "l"(pol)
+      : "memory");
+}
+
+// Makes this thread's shared-memory stores visible to the asynchronous proxy
+// (tcgen05, TMA).
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // Bulk copy of `bytes` contiguous bytes (16-byte aligned, a multiple of 16)
 // from global to shared memory, completing on `bar` (transaction bytes).
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
@@ -266,7 +291,62 @@ __device__ __forceinline__ void tmem_ld_cols_sync(uint32_t taddr, uint32_t (&v)[
   else tmem_ld16_sync(taddr, v);
 }
 
+// ------------------------------------------- block-scaled (MX) operands --
+// Block scales of one 128-k word: 32 lanes x 16 bytes from shared memory to 4
+// tensor-memory columns, the same in all four lane quarters.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t s_desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc)
+               : "memory");
+}
+
+// D[tmem] (+)= (A * scales) * (B * scales)^T with one E8M0 scale per 32 k, A
+// E2M1 and B E4M3 (BITS = 8, K = 32 per instruction) or E2M1 (BITS = 4, K = 64).
+template <int BITS>
+__device__ __forceinline__ void mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                       uint32_t accumulate) {
+  if constexpr (BITS == 8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
+        "[%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X "
+        "[%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
+
 // ------------------------------------------------------- descriptors --
+// Shared-memory descriptor of a scale block: 32 rows of 16 bytes, not
+// swizzled, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);  // start address
+  d |= (uint64_t)(128u >> 4) << 32;        // stride byte offset: 8 rows x 16 B
+  d |= (uint64_t)1 << 46;                  // descriptor version (tcgen05)
+  return d;
+}
+
+// Instruction descriptor of mma_mx: A E2M1, B E4M3 or E2M1, both K-major,
+// E8M0 scales, scale byte `id` of each row's word for both operands.
+template <int BITS>
+__host__ __device__ constexpr uint32_t idesc_mx(int M, int N, uint32_t id) {
+  return (id << 4)                            // B scale byte
+         | ((BITS == 8 ? 5u : 1u) << 7)       // A format: E2M1
+         | ((BITS == 8 ? 0u : 1u) << 10)      // B format: E4M3 / E2M1
+         | ((uint32_t)(N >> 3) << 17)         // N / 8
+         | (1u << 23)                         // scale format: E8M0
+         | ((uint32_t)(M >> 7) << 27)         // M / 128
+         | (id << 29);                        // A scale byte
+}
+
 // Shared-memory matrix descriptor (tcgen05 format): K-major operand stored
 // with the 128-byte swizzle, rows of 128 bytes, 8-row core groups 1024 bytes
 // apart.  `addr` must lie in a 1024-byte aligned swizzle atom.
