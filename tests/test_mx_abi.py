@@ -97,9 +97,9 @@ def test_binding_refusals():
     with pytest.raises(TypeError):
         b.moe_quantize_mx(x.double())
     with pytest.raises(ValueError, match="contiguous"):
-        b._mx_rows(x.t(), "x")
+        b._mx_stride(x.t(), "x")
     with pytest.raises(ValueError, match="evenly"):
-        b._mx_rows(torch.zeros(4, 6, 64)[:, ::2].transpose(0, 1), "x")
+        b._mx_stride(torch.zeros(4, 6, 64)[:, ::2].transpose(0, 1), "x")
     with pytest.raises(ValueError, match="bits"):
         b._mx_code_shape((4, 64), 5)
     with pytest.raises(ValueError, match="multiple"):
@@ -109,5 +109,5 @@ def test_binding_refusals():
     with pytest.raises(TypeError):
         b.moe_rmsnorm_mx(x.float(), x)
     assert b._mx_code_shape((3, 4, 64), 4) == ((3, 4, 32), (3, 4, 2))
-    assert b._mx_rows(torch.zeros(4, 96)[:, :64], "x") == (4, 64, 96)
-    assert b._mx_rows(torch.zeros(64), "x") == (1, 64, 64)
+    assert b._mx_stride(torch.zeros(4, 96)[:, :64], "x") == 96
+    assert b._mx_stride(torch.zeros(64), "x") == 64

@@ -461,10 +461,27 @@ def moe_quant_forward_noalloc(x, w13, w2, s13, s2, topk_w, topk_ids, bits=8, gro
 
 
 # ------------------------------------------------- microscaled (MX) formats --
+# These calls stand beside kernels of a few microseconds, so their checks read
+# each attribute once and pass plain integers to ctypes.
 _MX_BLOCK = 32
+_HALVES = (torch.bfloat16, torch.float16)
+_U8 = torch.uint8
 
 
-def _mx_dtype(t, name, dtypes=tuple(_DTYPES)):
+def _mx_stream(stream, t):
+    """cudaStream_t of stream, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _mx_bits(bits):
+    if bits != 4 and bits != 8:
+        raise ValueError(f"bits must be 4 or 8, got {bits}")
+
+
+def _mx_plain(t, name, dtypes):
+    """Checks a tensor on the plain side; returns its MQ_DTYPE_*."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
@@ -474,12 +491,12 @@ def _mx_dtype(t, name, dtypes=tuple(_DTYPES)):
     return _DTYPES[t.dtype]
 
 
-def _mx_rows(t, name):
-    """(rows, cols, elements between rows) of a tensor whose rows are dense
-    and evenly spaced."""
+def _mx_stride(t, name):
+    """Elements between the rows of a tensor whose rows are dense and evenly
+    spaced."""
     cols = t.shape[-1]
-    if t.dim() == 1:
-        t = t.unsqueeze(0)
+    if t.is_contiguous():
+        return cols
     if cols > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
     if t.dim() > 2:
@@ -487,31 +504,37 @@ def _mx_rows(t, name):
             t = t.view(-1, cols)
         except RuntimeError:
             raise ValueError(f"{name}: the rows must be evenly spaced") from None
-    rows = t.shape[0]
-    return rows, cols, t.stride(0) if rows > 1 else cols
+    return t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else cols
 
 
-def _mx_codes(q, scale, bits, name):
-    """Checks MX codes and scales; returns the number of elements in a row."""
-    if bits not in (4, 8):
-        raise ValueError(f"bits must be 4 or 8, got {bits}")
-    if bits == 8 and isinstance(q, torch.Tensor) and q.dtype == torch.float8_e4m3fn:
-        q = q.view(torch.uint8)
-    _need(q, torch.uint8, name)
-    _need(scale, torch.uint8, f"{name}_scale")
-    if q.dim() < 1:
-        raise ValueError(f"{name} must have at least one dim")
-    cols = q.shape[-1] * 8 // bits
+def _mx_codes(q, scale, bits, name, dim=None):
+    """Checks MX codes and scales; returns (shape of the codes, elements in a
+    row)."""
+    _mx_bits(bits)
+    for t, n in ((q, name), (scale, name + "_scale")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a torch.Tensor")
+        if t.dtype != _U8 and not (t is q and bits == 8 and t.dtype == torch.float8_e4m3fn):
+            raise TypeError(f"{n} must be torch.uint8, got {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{n} must be on a CUDA device")
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    shape = q.shape
+    if len(shape) != dim if dim else len(shape) < 1:
+        raise ValueError(f"{name} must have {dim or 'at least one'} dims")
+    cols = shape[-1] * 2 if bits == 4 else shape[-1]
     if cols == 0 or cols % _MX_BLOCK:
         raise ValueError(f"{name} must have rows of a positive multiple of {_MX_BLOCK} elements")
-    if tuple(scale.shape) != (*q.shape[:-1], cols // _MX_BLOCK):
-        raise ValueError(f"{name}_scale must be {[*q.shape[:-1], cols // _MX_BLOCK]}")
+    if scale.shape[-1] * _MX_BLOCK != cols or scale.shape[:-1] != shape[:-1]:
+        raise ValueError(f"{name}_scale must be {[*shape[:-1], cols // _MX_BLOCK]}")
     if scale.device != q.device:
         raise ValueError(f"{name}_scale must be on {name}'s device")
-    return cols
+    return shape, cols
 
 
 def _mx_out(t, shape, dtype, device, name):
+    """The caller's output, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _need(t, dtype, name)
@@ -523,24 +546,26 @@ def _mx_out(t, shape, dtype, device, name):
 
 
 def _mx_code_shape(shape, bits):
-    if bits not in (4, 8):
-        raise ValueError(f"bits must be 4 or 8, got {bits}")
-    if len(shape) < 1 or shape[-1] == 0 or shape[-1] % _MX_BLOCK:
+    """Shapes of the codes and scales of rows."""
+    _mx_bits(bits)
+    cols = shape[-1] if len(shape) else 0
+    if cols == 0 or cols % _MX_BLOCK:
         raise ValueError(f"rows must have a positive multiple of {_MX_BLOCK} elements")
-    return ((*shape[:-1], shape[-1] * bits // 8), (*shape[:-1], shape[-1] // _MX_BLOCK))
+    lead = tuple(shape[:-1])
+    return lead + (cols // 2 if bits == 4 else cols,), lead + (cols // _MX_BLOCK,)
 
 
 def moe_quantize_mx(x, bits=4, q=None, scale=None, stream=None):
     """bf16 / f16 / float32 [..., K] -> MX codes uint8 [..., K * bits / 8] (8
     bits: E4M3 bytes; 4 bits: two E2M1 codes per byte, even element low) and
     E8M0 scale codes uint8 [..., K / 32].  Rows may be strided."""
-    dt = _mx_dtype(x, "x")
+    dt = _mx_plain(x, "x", _DTYPES)
     qs, ss = _mx_code_shape(x.shape, bits)
-    rows, cols, stride = _mx_rows(x, "x")
-    q = _mx_out(q, qs, torch.uint8, x.device, "q")
-    scale = _mx_out(scale, ss, torch.uint8, x.device, "scale")
-    _check(lib().moe_quantize_mx(_ptr(x), dt, rows, cols, stride, bits, _ptr(q), _ptr(scale),
-                                 _stream(stream)))
+    dev, cols = x.device, x.shape[-1]
+    q = _mx_out(q, qs, _U8, dev, "q")
+    scale = _mx_out(scale, ss, _U8, dev, "scale")
+    _check(lib().moe_quantize_mx(x.data_ptr(), dt, x.numel() // cols, cols, _mx_stride(x, "x"),
+                                 bits, q.data_ptr(), scale.data_ptr(), _mx_stream(stream, x)))
     return q, scale
 
 
@@ -548,10 +573,10 @@ def moe_dequantize_mx(q, scale, bits=4, dtype=torch.bfloat16, out=None, stream=N
     """The values [..., K] that MX codes and scales stand for, in dtype."""
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
-    cols = _mx_codes(q, scale, bits, "q")
-    out = _mx_out(out, (*q.shape[:-1], cols), dtype, q.device, "out")
-    _check(lib().moe_dequantize_mx(_ptr(q), _ptr(scale), out.numel() // cols, cols, bits,
-                                   _ptr(out), _DTYPES[dtype], _stream(stream)))
+    shape, cols = _mx_codes(q, scale, bits, "q")
+    out = _mx_out(out, (*shape[:-1], cols), dtype, q.device, "out")
+    _check(lib().moe_dequantize_mx(q.data_ptr(), scale.data_ptr(), out.numel() // cols, cols,
+                                   bits, out.data_ptr(), _DTYPES[dtype], _mx_stream(stream, q)))
     return out
 
 
@@ -561,37 +586,40 @@ def moe_rmsnorm_mx(x, weight, eps=1e-6, residual=None, bits=8, want_y=False, res
     include/moeq.h): x, residual bf16 or f16 [T, H] (rows may be strided),
     weight [H] of the same dtype or float32 -> (q, scale, x + residual or None,
     the normed rows or None).  residual_out may be residual (in place)."""
-    half = (torch.bfloat16, torch.float16)
-    dt = _mx_dtype(x, "x", half)
-    if x.dim() != 2:
+    dt = _mx_plain(x, "x", _HALVES)
+    xt, dev, shape = x.dtype, x.device, x.shape
+    if len(shape) != 2:
         raise ValueError("x must have 2 dims")
-    T, H, xst = _mx_rows(x, "x")
-    _need(weight, weight.dtype if getattr(weight, "dtype", None) in (x.dtype, torch.float32)
-          else x.dtype, "weight", 1)
-    if weight.numel() != H:
+    T, H = shape
+    _need(weight, torch.float32 if getattr(weight, "dtype", None) == torch.float32 else xt,
+          "weight", 1)
+    if weight.shape[0] != H:
         raise ValueError(f"weight must hold H = {H} values")
-    rst = H
+    rst, rp = H, None
     if residual is not None:
-        _mx_dtype(residual, "residual", (x.dtype,))
-        if residual.shape != x.shape:
-            raise ValueError(f"residual must be {list(x.shape)}")
-        rst = _mx_rows(residual, "residual")[2]
-    qs, ss = _mx_code_shape(x.shape, bits)
-    q = _mx_out(q, qs, torch.uint8, x.device, "q")
-    scale = _mx_out(scale, ss, torch.uint8, x.device, "scale")
+        _mx_plain(residual, "residual", (xt,))
+        if residual.shape != shape:
+            raise ValueError(f"residual must be {list(shape)}")
+        rst, rp = _mx_stride(residual, "residual"), residual.data_ptr()
+    qs, ss = _mx_code_shape(shape, bits)
+    q = _mx_out(q, qs, _U8, dev, "q")
+    scale = _mx_out(scale, ss, _U8, dev, "scale")
+    rop = yp = None
     if residual is not None or residual_out is not None:
-        residual_out = _mx_out(residual_out, x.shape, x.dtype, x.device, "residual_out")
+        residual_out = _mx_out(residual_out, shape, xt, dev, "residual_out")
+        rop = residual_out.data_ptr()
     if want_y or y is not None:
-        y = _mx_out(y, x.shape, x.dtype, x.device, "y")
+        y = _mx_out(y, shape, xt, dev, "y")
+        yp = y.data_ptr()
     _check(lib().moe_rmsnorm_mx(
-        _ptr(x), _ptr(residual), _ptr(weight), dt, int(weight.dtype == torch.float32), T, H, xst,
-        rst, float(eps), _ptr(residual_out), _ptr(y), bits, _ptr(q), _ptr(scale),
-        _stream(stream)))
+        x.data_ptr(), rp, weight.data_ptr(), dt, 1 if weight.dtype == torch.float32 else 0, T, H,
+        _mx_stride(x, "x"), rst, eps, rop, yp, bits, q.data_ptr(), scale.data_ptr(),
+        _mx_stream(stream, x)))
     return q, scale, residual_out, y
 
 
 def moe_mx_product_workspace(R, K, N, E=1) -> int:
-    return int(lib().moe_mx_product_workspace(R, K, N, E))
+    return lib().moe_mx_product_workspace(R, K, N, E)
 
 
 def moe_mx_product(a, a_scale, w, w_scale, expert_offsets=None, a_bits=8, out=None,
@@ -599,39 +627,42 @@ def moe_mx_product(a, a_scale, w, w_scale, expert_offsets=None, a_bits=8, out=No
     """MX rows [R, K] grouped by expert (expert_offsets int32 [E + 1]) times
     4-bit MX weights [E, N, K]: [R, N].  Without expert_offsets w is [N, K] (or
     [1, N, K]): a dense product."""
-    K = _mx_codes(a, a_scale, a_bits, "a")
-    if a.dim() != 2:
-        raise ValueError("a must have 2 dims")
-    if _mx_codes(w, w_scale, 4, "w") != K:
+    (R, _), K = _mx_codes(a, a_scale, a_bits, "a", 2)
+    ws, wk = _mx_codes(w, w_scale, 4, "w")
+    if wk != K:
         raise ValueError("a and w must have rows of the same length")
-    if w.dim() not in (2, 3):
+    if len(ws) not in (2, 3):
         raise ValueError("w must have 2 or 3 dims")
-    E = w.shape[0] if w.dim() == 3 else 1
-    N = w.shape[-2]
-    R = a.shape[0]
+    E, N, dev = ws[0] if len(ws) == 3 else 1, ws[-2], a.device
+    op = None
     if expert_offsets is not None:
         _need(expert_offsets, torch.int32, "expert_offsets", 1)
-        if expert_offsets.numel() != E + 1:
+        if expert_offsets.shape[0] != E + 1:
             raise ValueError(f"expert_offsets must hold E + 1 = {E + 1} values")
+        op = expert_offsets.data_ptr()
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in _DTYPES:
         raise TypeError(f"out must be bfloat16, float16 or float32, got {out_dtype}")
-    out = _mx_out(out, (R, N), out_dtype, a.device, "out")
-    need = moe_mx_product_workspace(R, K, N, E)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
-    if workspace is not None:
-        _need(workspace, torch.uint8, "workspace")
-    _check(lib().moe_mx_product(
-        _ptr(a), _ptr(a_scale), a_bits, R, K, N, E, _ptr(w), _ptr(w_scale), _ptr(expert_offsets),
-        _ptr(out), _DTYPES[out_dtype], _ptr(workspace),
-        0 if workspace is None else workspace.numel(), _stream(stream)))
+    out = _mx_out(out, (R, N), out_dtype, dev, "out")
+    L = lib()
+    wp, nbytes = None, 0
+    if workspace is None:
+        nbytes = L.moe_mx_product_workspace(R, K, N, E)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=_U8, device=dev)
+            wp = workspace.data_ptr()
+    else:
+        _need(workspace, _U8, "workspace")
+        wp, nbytes = workspace.data_ptr(), workspace.numel()
+    _check(L.moe_mx_product(a.data_ptr(), a_scale.data_ptr(), a_bits, R, K, N, E, w.data_ptr(),
+                            w_scale.data_ptr(), op, out.data_ptr(), _DTYPES[out_dtype], wp,
+                            nbytes, _mx_stream(stream, a)))
     return out
 
 
 def moe_mx_forward_workspace(T, H, I, E, k, a_bits=8) -> int:
-    return int(lib().moe_mx_forward_workspace(T, H, I, E, k, a_bits))
+    return lib().moe_mx_forward_workspace(T, H, I, E, k, a_bits)
 
 
 def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out=None,
@@ -639,34 +670,30 @@ def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out
     """The fused expert MLP with 4-bit MX experts on MX activations
     (moe_mx_forward in include/moeq.h): a [T, H] with a_bits, w13 [E, 2I, H], w2
     [E, H, I], topk_w / topk_ids [T, k] -> [T, H] bf16 or f16."""
-    H = _mx_codes(a, a_scale, a_bits, "a")
-    if a.dim() != 2:
-        raise ValueError("a must have 2 dims")
-    T = a.shape[0]
-    if _mx_codes(w13, s13, 4, "w13") != H:
-        raise ValueError(f"w13 must have rows of H = {H} elements")
-    I = _mx_codes(w2, s2, 4, "w2")
-    if w13.dim() != 3 or w2.dim() != 3:
-        raise ValueError("w13 and w2 must have 3 dims")
-    E = w13.shape[0]
-    if tuple(w13.shape[:2]) != (E, 2 * I) or tuple(w2.shape[:2]) != (E, H):
+    (T, _), H = _mx_codes(a, a_scale, a_bits, "a", 2)
+    (E, n13, _), k13 = _mx_codes(w13, s13, 4, "w13", 3)
+    (e2, n2, _), I = _mx_codes(w2, s2, 4, "w2", 3)
+    if k13 != H or n2 != H or n13 != 2 * I or e2 != E:
         raise ValueError("w13 must be [E, 2I, H] and w2 [E, H, I]")
     _need(topk_w, torch.float32, "topk_w", 2)
     _need(topk_ids, torch.int32, "topk_ids", 2)
     k = topk_ids.shape[1]
     if topk_ids.shape[0] != T or topk_w.shape != topk_ids.shape:
         raise ValueError(f"topk_w and topk_ids must be [{T}, k]")
+    dev = a.device
     if out is not None:
         out_dtype = out.dtype
-    if out_dtype not in (torch.bfloat16, torch.float16):
+    if out_dtype not in _HALVES:
         raise TypeError(f"out must be bfloat16 or float16, got {out_dtype}")
-    out = _mx_out(out, (T, H), out_dtype, a.device, "out")
+    out = _mx_out(out, (T, H), out_dtype, dev, "out")
+    L = lib()
     if workspace is None:
-        need = moe_mx_forward_workspace(T, H, I, E, k, a_bits)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=a.device)
-    _need(workspace, torch.uint8, "workspace")
-    _check(lib().moe_mx_forward(
-        _ptr(a), _ptr(a_scale), a_bits, T, H, I, E, k, _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2),
-        _ptr(topk_w), _ptr(topk_ids), _ptr(out), _DTYPES[out_dtype], _ptr(workspace),
-        workspace.numel(), _stream(stream)))
+        nbytes = L.moe_mx_forward_workspace(T, H, I, E, k, a_bits)
+        workspace = torch.empty(max(nbytes, 16), dtype=_U8, device=dev)
+    else:
+        _need(workspace, _U8, "workspace")
+    _check(L.moe_mx_forward(
+        a.data_ptr(), a_scale.data_ptr(), a_bits, T, H, I, E, k, w13.data_ptr(), s13.data_ptr(),
+        w2.data_ptr(), s2.data_ptr(), topk_w.data_ptr(), topk_ids.data_ptr(), out.data_ptr(),
+        _DTYPES[out_dtype], workspace.data_ptr(), workspace.numel(), _mx_stream(stream, a)))
     return out

@@ -3,6 +3,7 @@
 #include "common.cuh"
 #include "mx.cuh"
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <mutex>
@@ -732,8 +733,9 @@ static bool mx_product_sizes_ok(int64_t R, int K, int N, int E) {
 
 MQ_EXPORT size_t moe_mx_product_workspace(int64_t R, int K, int N, int E) {
   if (!mx_product_sizes_ok(R, K, N, E) || R == 0) return 0;
-  const MxPlan pl = mx_plan(R, E, K, N, false);
-  return pl.splits > 1 ? align256(sizeof(float) * (size_t)pl.splits * (size_t)R * (size_t)N) : 0;
+  const int splits = std::max(mx_plan(R, E, K, N, false, 8).splits,
+                              mx_plan(R, E, K, N, false, 4).splits);
+  return splits > 1 ? align256(sizeof(float) * (size_t)splits * (size_t)R * (size_t)N) : 0;
 }
 
 MQ_EXPORT int moe_mx_product(const uint8_t* a, const uint8_t* a_scale, int a_bits, int64_t R,
@@ -753,7 +755,7 @@ MQ_EXPORT int moe_mx_product(const uint8_t* a, const uint8_t* a_scale, int a_bit
       (reinterpret_cast<uintptr_t>(w) & 31u) || (expert_offsets && !aligned4(expert_offsets)))
     return fail(MQ_ERR_INVALID_ARG,
                 "pointers must be 16-byte aligned, w 32-byte, expert_offsets 4-byte");
-  const MxPlan pl = mx_plan(R, E, K, N, false);
+  const MxPlan pl = mx_plan(R, E, K, N, false, a_bits);
   const size_t need = moe_mx_product_workspace(R, K, N, E);
   if (need && (!workspace || ws_bytes < need))
     return fail(MQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace ? ws_bytes : 0, need);
@@ -794,8 +796,8 @@ struct MxLayout {
 MxLayout mx_layout(int T, int H, int I, int E, int k, int bits) {
   MxLayout L;
   const int64_t S = (int64_t)T * k;
-  L.up = mx_plan(S, E, H, I, true);
-  L.down = mx_plan(S, E, I, H, false);
+  L.up = mx_plan(S, E, H, I, true, bits);
+  L.down = mx_plan(S, E, I, H, false, bits);
   const int64_t cap = moe_align_capacity(T, k, E, kAlignBlock);
   L.cap = cap;
   size_t off = 0;

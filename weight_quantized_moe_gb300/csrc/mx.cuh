@@ -216,9 +216,10 @@ struct MxGemm {
 };
 struct MxPlan {
   int bn;      // rows per tile
+  int tiles;   // weight tiles per unit (2 when gated)
   int splits;  // K splits (MX_EPI_PART)
 };
-MQ_HIDDEN MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated);
+MQ_HIDDEN MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated, int a_bits);
 MQ_HIDDEN cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStream_t st);
 // out[r, :] = sum over splits of part[split, r, :], for the rows
 // [offsets[0], offsets[E]) (null: all rows).

@@ -93,6 +93,7 @@ struct Params {
   const int32_t* seg_start;
   const int32_t* seg_count;
   int E, K, N, R;
+  int mrows;    // outputs of a unit: 128 per tile, or 128 when gated
   int up_row;   // weight row of a unit's second tile, relative to its first
   int wrows;
   int mtiles, splits, words, sbs;
@@ -108,7 +109,7 @@ struct Params {
 };
 
 struct Unit {
-  int e, row0, n, m, split;  // expert, first row, rows, weight tile, K split
+  int e, row0, n, m, split;  // expert, first row, rows, first output, K split
   bool single;               // the expert has one chunk: its weights are read once
 };
 
@@ -150,7 +151,7 @@ __device__ __forceinline__ Unit unit_at(const Params& p, const int* chunk_start,
   const int tiles = min(kGroup, p.mtiles - grp * kGroup) * p.splits;
   const int c = (int)(rem / tiles);
   const int t = (int)(rem - (int64_t)c * tiles);
-  w.m = grp * kGroup + t / p.splits;
+  w.m = (grp * kGroup + t / p.splits) * p.mrows;
   w.split = t % p.splits;
   int start, count;
   segment(p, lo, start, count);
@@ -175,6 +176,12 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, Ctl
       }
     }
   }
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Ctl* ctl,
@@ -292,28 +299,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t total = (int64_t)chunk_start[p.E] * p.mtiles * p.splits;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------- codes --
-      const uint64_t pol_once = l2_policy_evict_first();
-      uint32_t it = 0;
-      bool ok = true;
-      for (int64_t u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        const Unit w = unit_at<BN>(p, chunk_start, u);
-        const int sb0 = (int)((int64_t)p.sbs * w.split / p.splits);
-        const int sb1 = (int)((int64_t)p.sbs * (w.split + 1) / p.splits);
-        const int st0 = sb0 * C::kPerSb;
-        const int st1 = min(sb1 * C::kPerSb, (p.words + C::kWords - 1) / C::kWords);
-        for (int s = st0; s < st1; ++s, ++it) {
-          const uint32_t slot = it % C::kStages;
-          if (!wait_bounded(&ctl->empty[slot], ((it / C::kStages) & 1) ^ 1, ctl, p.status)) {
-            ok = false;
-            break;
-          }
-          uint8_t* dst = stages + (size_t)slot * C::kStageBytes;
+    // ---------------------------------------------------------- codes --
+    const bool el = elect_one();
+    const uint64_t pol_once = l2_policy_evict_first();
+    uint32_t it = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; u < total && ok; u += gridDim.x) {
+      const Unit w = unit_at<BN>(p, chunk_start, u);
+      const int sb0 = (int)((int64_t)p.sbs * w.split / p.splits);
+      const int sb1 = (int)((int64_t)p.sbs * (w.split + 1) / p.splits);
+      const int st0 = sb0 * C::kPerSb;
+      const int st1 = min(sb1 * C::kPerSb, (p.words + C::kWords - 1) / C::kWords);
+      for (int s = st0; s < st1; ++s, ++it) {
+        const uint32_t slot = it % C::kStages;
+        if (!warp_wait(&ctl->empty[slot], ((it / C::kStages) & 1) ^ 1, ctl, p.status)) {
+          ok = false;
+          break;
+        }
+        uint8_t* dst = stages + (size_t)slot * C::kStageBytes;
+        if (el) {
           mbar_arrive_expect_tx(&ctl->full[slot], C::kTxBytes);
 #pragma unroll
           for (int a = 0; a < NACC; ++a) {
-            const int row = w.m * kTileM + a * p.up_row;
+            const int row = w.m + a * p.up_row;
             if (w.single)
               tma_load_3d_hint(dst + a * kABytes, &map_w, &ctl->full[slot], s * 128, row, w.e, pol_once);
             else
@@ -322,41 +330,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d(dst + NACC * kABytes, &map_a, &ctl->full[slot], s * 128, w.row0);
         }
       }
-      if (ctl->abort_flag) {  // loads in flight land before the CTA goes
-        for (uint32_t j = it < (uint32_t)C::kStages ? 0 : it - C::kStages; j < it; ++j)
-          wait_drain(&ctl->full[j % C::kStages], (j / C::kStages) & 1);
-      }
     }
-    __syncwarp();
+    if (ctl->abort_flag) {  // loads in flight land before the CTA goes
+      for (uint32_t j = it < (uint32_t)C::kStages ? 0 : it - C::kStages; j < it; ++j)
+        wait_drain(&ctl->full[j % C::kStages], (j / C::kStages) & 1);
+    }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // -------------------------------------------------------- MMAs --
-      uint32_t it = 0, sb_it = 0, t = 0;
-      bool ok = true;
-      for (int64_t u = blockIdx.x; u < total && ok; u += gridDim.x, ++t) {
-        const Unit w = unit_at<BN>(p, chunk_start, u);
-        const int sb0 = (int)((int64_t)p.sbs * w.split / p.splits);
-        const int sb1 = (int)((int64_t)p.sbs * (w.split + 1) / p.splits);
-        const int nst = (p.words + C::kWords - 1) / C::kWords;
-        const uint32_t buf = t % C::kBufs;
-        ok = wait_bounded(&ctl->acc_empty[buf], ((t / C::kBufs) & 1) ^ 1, ctl, p.status);
-        tc_fence_after();
-        const uint32_t acc = tmem + buf * C::kAccCols;
-        uint32_t accumulate = 0;
-        for (int sb = sb0; sb < sb1 && ok; ++sb, ++sb_it) {
-          const uint32_t ss = sb_it % kSfRing;
-          ok = wait_bounded(&ctl->sf_full[ss], (sb_it / kSfRing) & 1, ctl, p.status);
-          if (!ok) break;
+    // ----------------------------------------------------------- MMAs --
+    // The warp walks the loop together and one elected lane issues, so that
+    // the descriptors stay in uniform registers (a lone lane takes 3 to 5
+    // times as long per instruction: 8192 x 4096 x 28672 1892 -> 1236 us).
+    const bool el = elect_one();
+    const int nst = (p.words + C::kWords - 1) / C::kWords;
+    uint32_t it = 0, sb_it = 0, t = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; u < total && ok; u += gridDim.x, ++t) {
+      const Unit w = unit_at<BN>(p, chunk_start, u);
+      const int sb0 = (int)((int64_t)p.sbs * w.split / p.splits);
+      const int sb1 = (int)((int64_t)p.sbs * (w.split + 1) / p.splits);
+      const uint32_t buf = t % C::kBufs;
+      ok = warp_wait(&ctl->acc_empty[buf], ((t / C::kBufs) & 1) ^ 1, ctl, p.status);
+      tc_fence_after();
+      const uint32_t acc = tmem + buf * C::kAccCols;
+      uint32_t accumulate = 0;
+      for (int sb = sb0; sb < sb1 && ok; ++sb, ++sb_it) {
+        const uint32_t ss = sb_it % kSfRing;
+        ok = warp_wait(&ctl->sf_full[ss], (sb_it / kSfRing) & 1, ctl, p.status);
+        if (!ok) break;
+        if (el) {
+          // scales to tensor memory: blocks of 4 columns, [word][tile]
           const uint32_t sfa = smem_addr(sf + (size_t)ss * C::kSfSlotBytes);
-          // Scales to tensor memory: blocks of 4 columns, [word][tile].
 #pragma unroll
           for (int b = 0; b < 4 * (NACC + C::kBBlocks); ++b)
             tmem_cp_scales(tmem + C::kSfBase + b * 4, smem_desc_scales(sfa + b * 512));
-          const int last = min((sb + 1) * C::kPerSb, nst);
-          for (int s = sb * C::kPerSb; s < last; ++s, ++it) {
-            const uint32_t slot = it % C::kStages;
-            ok = wait_bounded(&ctl->full[slot], (it / C::kStages) & 1, ctl, p.status);
-            if (!ok) break;
+        }
+        const int last = min((sb + 1) * C::kPerSb, nst);
+        for (int s = sb * C::kPerSb; s < last; ++s, ++it) {
+          const uint32_t slot = it % C::kStages;
+          ok = warp_wait(&ctl->full[slot], (it / C::kStages) & 1, ctl, p.status);
+          if (!ok) break;
+          if (el) {
             const uint32_t base = smem_addr(stages + (size_t)slot * C::kStageBytes);
             const int word0 = (s % C::kPerSb) * C::kWords;
 #pragma unroll
@@ -368,22 +381,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int a = 0; a < NACC; ++a) {
                 const uint64_t ad = smem_desc_k_sw128(base + a * kABytes) + j * 2;
-                mma_mx<BITS>(acc + a * BN, ad, bd, idesc_mx<BITS>(kTileM, BN, id),
-                             sfw + a * 4, sfw + NACC * 4, accumulate);
+                mma_mx<BITS>(acc + a * BN, ad, bd, idesc_mx<BITS>(kTileM, BN, id), sfw + a * 4,
+                             sfw + NACC * 4, accumulate | j);
               }
-              accumulate = 1;
             }
             mma_commit(&ctl->empty[slot]);
           }
-          if (ok) mma_commit(&ctl->sf_empty[ss]);
+          accumulate = 1;
         }
-        if (ok) mma_commit(&ctl->acc_full[buf]);
+        if (ok && el) mma_commit(&ctl->sf_empty[ss]);
       }
-      // nothing of this thread may be in flight when the memory goes
-      mma_commit(&ctl->drain);
-      wait_drain(&ctl->drain, 0);
+      if (ok && el) mma_commit(&ctl->acc_full[buf]);
     }
-    __syncwarp();
+    // nothing this warp issued may be in flight when the memory goes
+    if (el) mma_commit(&ctl->drain);
+    wait_drain(&ctl->drain, 0);
   } else if (warp < 4) {
     // ------------------------------------------------------------ scales --
     const int lw = warp - 2;
@@ -400,8 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4 va[kGroupsA], vb[kGroupsB];
 #pragma unroll
         for (int g = 0; g < kGroupsA; ++g) {
-          const int r = w.m * kTileM + (g & 3) * 32 + lane;  // row of the gate (or only) half
-          const int wr = r + (g >> 2) * p.up_row;
+          const int wr = w.m + (g >> 2) * p.up_row + (g & 3) * 32 + lane;
           va[g] = make_uint4(0, 0, 0, 0);
           if (wr < p.wrows)
             va[g] = load_words(p.w_scale + ((int64_t)w.e * p.wrows + wr) * row_bytes, sb * 4, p.words);
@@ -437,52 +448,88 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------------------------------------------------- epilogue --
-    const int ew = warp - 4;
-    const int quad = warp & 3;  // the tensor-memory lanes this warp may read
-    const int half = ew >> 2;   // which 16-column steps it takes
+    const int quad = warp & 3;       // the tensor-memory lanes this warp may read
+    const int half = (warp - 4) >> 2;  // which 16-column steps it takes
     uint32_t t = 0;
     for (int64_t u = blockIdx.x; u < total; u += gridDim.x, ++t) {
       const Unit w = unit_at<BN>(p, chunk_start, u);
       const uint32_t buf = t % C::kBufs;
+      // Destination rows and factors of the chunk, one column per lane and
+      // 32-column group: loaded before the accumulators are there.
+      constexpr int kCols = (BN + 31) / 32;
+      int dest[EPI == MX_EPI_PART ? kCols : 1];
+      float factor[EPI == MX_EPI_PART ? kCols : 1];
+      if constexpr (EPI == MX_EPI_PART) {
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+          const int c = i * 32 + lane;
+          dest[i] = 0;
+          factor[i] = 1.0f;
+          if (c < w.n) {
+            dest[i] = p.dest ? p.dest[w.row0 + c] : w.row0 + c;
+            if (p.dest_w) factor[i] = p.dest_w[dest[i]];
+          }
+        }
+      }
       if (!warp_wait(&ctl->acc_full[buf], (t / C::kBufs) & 1, ctl, p.status)) break;
       tc_fence_after();
       const uint32_t acc = tmem + buf * C::kAccCols + ((uint32_t)(quad * 32) << 16);
-      const int n = w.m * kTileM + quad * 32 + lane;  // this lane's output
-      for (int c0 = half * 16; c0 < w.n; c0 += 32) {
-        uint32_t v0[16];
-        tmem_ld16_sync(acc + c0, v0);
-        if constexpr (EPI == MX_EPI_GATED) {
-          uint32_t v1[16];
+      if constexpr (EPI == MX_EPI_GATED) {
+        const int n = w.m + quad * 32 + lane;  // this lane's output
+        const bool live = n < p.N;             // (uniform: N is a multiple of 32)
+        for (int c0 = half * 16; c0 < w.n; c0 += 32) {
+          uint32_t v0[16], v1[16];
+          tmem_ld16_sync(acc + c0, v0);
           tmem_ld16_sync(acc + BN + c0, v1);
+          uint32_t codes = 0;  // lane j keeps column j's scale code
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            if (c0 + j >= w.n) break;  // warp-uniform
             const float g = __uint_as_float(v0[j]), up = __uint_as_float(v1[j]);
             const float a = __fdividef(g, 1.0f + __expf(-g)) * up;
             const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(a) & 0x7fffffffu);
             const uint32_t code = mq::mx_scale_code<BITS>(m);
             const float s = mq::mx_scaled(a, mq::mx_inv_scale(code));
+            if (lane == j) codes = code;
             const int64_t row = w.row0 + c0 + j;
+            const bool mine = live && c0 + j < w.n;
             if (BITS == 8) {
-              if (n < p.N) p.act[row * p.N + n] = (uint8_t)mq::e4m3x2(s, 0.0f);
+              if (mine) p.act[row * p.N + n] = (uint8_t)mq::e4m3x2(s, 0.0f);
             } else {
               const float hi = __shfl_down_sync(0xffffffffu, s, 1);
-              if ((lane & 1) == 0 && n < p.N) p.act[(row * p.N + n) >> 1] = (uint8_t)mq::e2m1x2(s, hi);
+              if (mine && (lane & 1) == 0)
+                p.act[(row * p.N + n) >> 1] = (uint8_t)mq::e2m1x2(s, hi);
             }
-            if (lane == 0 && n < p.N) p.act_scale[row * (p.N >> 5) + (n >> 5)] = (uint8_t)code;
           }
-        } else {
+          if (live && lane < 16 && c0 + lane < w.n)
+            p.act_scale[(int64_t)(w.row0 + c0 + lane) * (p.N >> 5) + ((n - lane) >> 5)] =
+                (uint8_t)codes;
+        }
+      } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (c0 + j >= w.n) break;
-            float v = __uint_as_float(v0[j]);
-            int64_t row = w.row0 + c0 + j;
-            if (EPI == MX_EPI_PART) {
-              if (p.dest) row = p.dest[row];
-              if (p.dest_w) v *= p.dest_w[row];
-              if (n < p.N) p.part[(w.split * p.part_rows + row) * p.N + n] = v;
-            } else if (n < p.N) {
-              store_out(p.out, p.out_dtype, row * p.N + n, v);
+        for (int tile = 0; tile < NACC; ++tile) {
+          const int n = w.m + tile * kTileM + quad * 32 + lane;  // this lane's output
+          if (n - lane >= p.N) break;
+          const bool live = n < p.N;
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) {
+            const int c0 = i * 32 + half * 16;
+            if (c0 >= w.n) break;
+            uint32_t v[16];
+            tmem_ld16_sync(acc + tile * BN + c0, v);
+            if constexpr (EPI == MX_EPI_PART) {
+              float* part = p.part + (int64_t)w.split * p.part_rows * p.N + n;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int row = __shfl_sync(0xffffffffu, dest[i], half * 16 + j);
+                const float f = __shfl_sync(0xffffffffu, factor[i], half * 16 + j);
+                if (live && c0 + j < w.n) part[(int64_t)row * p.N] = __uint_as_float(v[j]) * f;
+              }
+            } else {
+              const int64_t at = (int64_t)(w.row0 + c0) * p.N + n;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (live && c0 + j < w.n)
+                  store_out(p.out, p.out_dtype, at + (int64_t)j * p.N, __uint_as_float(v[j]));
             }
           }
         }
@@ -614,44 +661,65 @@ cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Param
   return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mw, ma, p);
 }
 
-template <int BITS, int EPI>
+template <int BITS, int NACC, int EPI>
 cudaError_t launch_bn(int bn, const CUtensorMap& mw, const CUtensorMap& ma, const Params& p,
-                      int64_t units, cudaStream_t st) {
-  constexpr int NACC = EPI == MX_EPI_GATED ? 2 : 1;
+                       int64_t units, cudaStream_t st) {
   switch (bn) {
     case 16: return launch_one<BITS, NACC, 16, EPI>(mw, ma, p, units, st);
     case 32: return launch_one<BITS, NACC, 32, EPI>(mw, ma, p, units, st);
     case 64: return launch_one<BITS, NACC, 64, EPI>(mw, ma, p, units, st);
-    default: return launch_one<BITS, NACC, 96, EPI>(mw, ma, p, units, st);
+    case 96: return launch_one<BITS, NACC, 96, EPI>(mw, ma, p, units, st);
+    default: return launch_one<BITS, NACC, 192, EPI>(mw, ma, p, units, st);
   }
 }
 
 template <int BITS>
-cudaError_t launch_epi(const MxGemm& g, int bn, const CUtensorMap& mw, const CUtensorMap& ma,
-                       const Params& p, int64_t units, cudaStream_t st) {
-  switch (g.epi) {
-    case MX_EPI_OUT: return launch_bn<BITS, MX_EPI_OUT>(bn, mw, ma, p, units, st);
-    case MX_EPI_PART: return launch_bn<BITS, MX_EPI_PART>(bn, mw, ma, p, units, st);
-    default: return launch_bn<BITS, MX_EPI_GATED>(bn, mw, ma, p, units, st);
-  }
+cudaError_t launch_epi(const MxGemm& g, const MxPlan& pl, const CUtensorMap& mw,
+                       const CUtensorMap& ma, const Params& p,
+                       int64_t units, cudaStream_t st) {
+  if (g.epi == MX_EPI_GATED) return launch_bn<BITS, 2, MX_EPI_GATED>(pl.bn, mw, ma, p, units, st);
+  if (g.epi == MX_EPI_OUT)
+    return pl.tiles == 2 ? launch_bn<BITS, 2, MX_EPI_OUT>(pl.bn, mw, ma, p, units, st)
+                         : launch_bn<BITS, 1, MX_EPI_OUT>(pl.bn, mw, ma, p, units, st);
+  return pl.tiles == 2 ? launch_bn<BITS, 2, MX_EPI_PART>(pl.bn, mw, ma, p, units, st)
+                       : launch_bn<BITS, 1, MX_EPI_PART>(pl.bn, mw, ma, p, units, st);
 }
 
 }  // namespace
 
-MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated) {
+// Rows per tile: above the average load of a live expert by half, so that
+// most experts are one chunk (their weights are then read once) without many
+// columns to spare.  Weight tiles per unit and K splits: the choice with the
+// least estimated time, in bytes that one SM brings in (a wave of units
+// brings in its weights and rows, and 24 KB more for a unit's start and end;
+// partial sums are written and read again, and cost a launch).
+MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated, int a_bits) {
   MxPlan pl;
-  const int64_t live = S < E ? S : E;
-  const int64_t avg = live > 0 ? (S + live - 1) / live : 0;
-  pl.bn = avg <= 8 ? 16 : avg <= 20 ? 32 : avg <= 64 ? 64 : 96;
+  const int64_t live = std::max<int64_t>(1, std::min<int64_t>(S, E));
+  const int64_t avg = (S + live - 1) / live;
+  pl.bn = avg <= 8 ? 16 : avg <= 20 ? 32 : avg <= 40 ? 64 : (avg <= 128 || gated || a_bits == 4) ? 96 : 192;
   pl.splits = 1;
-  if (!gated) {
-    // K splits of at least 1024 k while the units leave SMs idle
-    const int64_t chunks = live > 0 ? std::max(live, (S + pl.bn - 1) / pl.bn) : 1;
-    const int64_t units = chunks * ((N + kTileM - 1) / kTileM);
-    const int most = std::max(1, K / 1024);
-    const int sms = tc_num_sms();
-    if (units < 3 * sms)
-      pl.splits = (int)std::min<int64_t>(std::min(most, 8), std::max<int64_t>(1, 4 * sms / std::max<int64_t>(1, units)));
+  pl.tiles = 2;
+  if (gated) return pl;
+  const int sms = tc_num_sms();
+  const int sbs = (K + 511) / 512;
+  const int64_t chunks = std::max(live, (S + pl.bn - 1) / pl.bn);
+  const double row = a_bits / 8.0 + 1.0 / 32, wrow = 0.5 + 1.0 / 32;
+  double best = 0;
+  for (int tiles = 2; tiles >= 1; --tiles) {
+    const int64_t mt = (N + tiles * kTileM - 1) / (tiles * kTileM);
+    for (int sp = 1; sp <= 16 && sp <= sbs; ++sp) {
+      if (sp > 1 && S > 1024) break;  // partial sums would cost more than idle SMs
+      const double waves = std::ceil((double)(chunks * mt * sp) / sms);
+      const double unit = 512.0 * std::ceil((double)sbs / sp) * (tiles * kTileM * wrow + pl.bn * row);
+      double cost = waves * (unit + 24e3);
+      if (sp > 1) cost += 80e3 + 4.0 * sp * S * N / sms;
+      if (best == 0 || cost < best) {
+        best = cost;
+        pl.tiles = tiles;
+        pl.splits = sp;
+      }
+    }
   }
   return pl;
 }
@@ -687,9 +755,10 @@ cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStream_t st) {
   p.K = g.K;
   p.N = g.N;
   p.R = (int)g.R;
-  p.up_row = gated ? g.N : 0;
+  p.mrows = gated ? kTileM : pl.tiles * kTileM;
+  p.up_row = gated ? g.N : kTileM;
   p.wrows = g.wrows;
-  p.mtiles = (g.N + kTileM - 1) / kTileM;
+  p.mtiles = (g.N + p.mrows - 1) / p.mrows;
   p.splits = pl.splits;
   p.words = g.K / 128;
   p.sbs = (p.words + 3) / 4;
@@ -705,8 +774,8 @@ cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStream_t st) {
   const int64_t live = g.S < g.E ? g.S : g.E;
   const int64_t units = (live + g.S / pl.bn) * p.mtiles * p.splits;  // at most
   if (units <= 0) return cudaSuccess;
-  return g.a_bits == 8 ? launch_epi<8>(g, pl.bn, mw, ma, p, units, st)
-                       : launch_epi<4>(g, pl.bn, mw, ma, p, units, st);
+  return g.a_bits == 8 ? launch_epi<8>(g, pl, mw, ma, p, units, st)
+                       : launch_epi<4>(g, pl, mw, ma, p, units, st);
 }
 
 cudaError_t launch_mx_reduce(const float* part, int splits, int64_t rows, int N,
