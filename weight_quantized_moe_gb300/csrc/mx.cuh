@@ -216,7 +216,6 @@ struct MxGemm {
 };
 struct MxPlan {
   int bn;      // rows per tile
-  int tiles;   // weight tiles per unit (2 when gated)
   int splits;  // K splits (MX_EPI_PART)
 };
 MQ_HIDDEN MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated, int a_bits);

@@ -10,11 +10,11 @@
 // One persistent CTA per SM.  D[128 weight rows x BN rows of A]: the weights
 // are the instruction's A operand (M = 128) and the token rows its B operand
 // (N = BN), so that a few rows cost a narrow tile and no padding.  A unit is
-// (expert, chunk of at most BN rows, weight tile, K split).  NACC = 2: a unit
-// holds two weight tiles (gate and up) that share its token rows.
+// (expert, chunk of at most BN rows, two weight tiles, K split); the two tiles
+// share the unit's rows, and are gate and up where the epilogue joins them.
 //
-// Roles: warp 0 streams codes by TMA; warp 1 issues the MMAs; warps 2-3 bring
-// the scales; warps 4-11 are the epilogue.
+// Roles: warp 0 streams codes by TMA; warps 1-2 issue the MMAs; warps 3 and 12
+// bring the scales; warps 4-11 are the epilogue.
 //   * Codes.  A stage holds 128 bytes of each row, 128-byte swizzled: 128 k of
 //     E4M3 rows against 128 k of weights whose nibbles TMA spreads to 16-byte
 //     groups (the operand form of the mixed 8/4-bit instruction), or 256 k of
@@ -23,7 +23,7 @@
 //     (128 k, a "word") per row, row r in lane r % 32 and column r / 32.  The
 //     scale warps read the rows' scale bytes (16 bytes = 512 k per row), and
 //     write them to shared memory as that [32 lanes][4 columns] block for each
-//     word; the MMA thread copies a block to tensor memory with one
+//     word; the MMA warps copy a block to tensor memory with one
 //     tcgen05.cp, which the MMAs that follow it in the same thread see.
 //   * Epilogue.  A thread is one weight row (tensor-memory lane) and walks the
 //     columns, the rows of A.  32 lanes are 32 consecutive outputs: exactly
@@ -42,7 +42,8 @@ using namespace mq::ptx;
 
 constexpr int kTileM = 128;
 constexpr int kABytes = kTileM * 128;  // one weight tile of a stage
-constexpr int kThreads = 384;
+constexpr int kTiles = 2;              // weight tiles of a unit, one MMA warp each
+constexpr int kThreads = 416;
 constexpr int kEpiWarps = 8;
 constexpr int kMaxStages = 12;
 constexpr int kSfRing = 4;             // scale slots, 512 k each
@@ -51,23 +52,24 @@ constexpr int kGroup = 8;              // weight tiles that a chunk walk shares
 constexpr unsigned long long kWaitNs = 1000000000ull;
 constexpr size_t kSmemMax = 227 * 1024;
 
-template <int BITS, int NACC, int BN>
+template <int BITS, int BN>
 struct Cfg {
   static constexpr int kWords = BITS == 8 ? 1 : 2;  // 128-k scale words per stage
   static constexpr int kPerSb = 4 / kWords;         // stages per scale slot
   static constexpr int kBBytes = BN * 128;
-  static constexpr int kStageBytes = NACC * kABytes + kBBytes;
+  static constexpr int kStageBytes = kTiles * kABytes + kBBytes;
   // bytes TMA reports for a stage: those it reads, so half a weight tile where
   // it spreads the nibbles
-  static constexpr int kTxBytes = NACC * (BITS == 8 ? kABytes / 2 : kABytes) + kBBytes;
+  static constexpr int kTxBytes = kTiles * (BITS == 8 ? kABytes / 2 : kABytes) + kBBytes;
   static constexpr int kBBlocks = (BN + 127) / 128;
-  static constexpr int kSfWordBytes = (NACC + kBBlocks) * 512;
+  static constexpr int kSfWordBytes = (kTiles + kBBlocks) * 512;
   static constexpr int kSfSlotBytes = 4 * kSfWordBytes;
-  static constexpr int kSfCols = 4 * (NACC + kBBlocks) * 4;
-  static constexpr int kAccCols = NACC * BN;
-  static constexpr int kBufs = 2 * kAccCols + kSfCols <= 512 ? 2 : 1;
+  // tensor-memory columns of one MMA warp's scales: its tile's and the rows'
+  static constexpr int kSfCols = 4 * (1 + kBBlocks) * 4;
+  static constexpr int kAccCols = kTiles * BN;
+  static constexpr int kBufs = 2 * kAccCols + kTiles * kSfCols <= 512 ? 2 : 1;
   static constexpr int kSfBase = kBufs * kAccCols;
-  static_assert(kSfBase + kSfCols <= 512, "tensor memory");
+  static_assert(kSfBase + kTiles * kSfCols <= 512, "tensor memory");
   static constexpr size_t kFixed = 1024 + kSfRing * (size_t)kSfSlotBytes + 1024 + (kMaxE + 1) * 4;
   static constexpr int kFit = (int)((kSmemMax - kFixed) / kStageBytes);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
@@ -232,11 +234,11 @@ __device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float
   else static_cast<float*>(out)[i] = v;
 }
 
-template <int BITS, int NACC, int BN, int EPI>
+template <int BITS, int BN, int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
             const Params p) {
-  using C = Cfg<BITS, NACC, BN>;
+  using C = Cfg<BITS, BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* stages = smem;
@@ -252,21 +254,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&map_a);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&ctl->full[i], 1);
-      mbar_init(&ctl->empty[i], 1);
+      mbar_init(&ctl->empty[i], kTiles);
     }
     for (int i = 0; i < kSfRing; ++i) {
       mbar_init(&ctl->sf_full[i], 1);
-      mbar_init(&ctl->sf_empty[i], 1);
+      mbar_init(&ctl->sf_empty[i], kTiles);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->acc_full[i], 1);
+      mbar_init(&ctl->acc_full[i], kTiles);
       mbar_init(&ctl->acc_empty[i], kEpiWarps);
     }
-    mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->drain, kTiles);
     ctl->abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == 1) {  // (and warp 2 the table, below)
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
@@ -320,14 +322,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (el) {
           mbar_arrive_expect_tx(&ctl->full[slot], C::kTxBytes);
 #pragma unroll
-          for (int a = 0; a < NACC; ++a) {
+          for (int a = 0; a < kTiles; ++a) {
             const int row = w.m + a * p.up_row;
             if (w.single)
               tma_load_3d_hint(dst + a * kABytes, &map_w, &ctl->full[slot], s * 128, row, w.e, pol_once);
             else
               tma_load_3d(dst + a * kABytes, &map_w, &ctl->full[slot], s * 128, row, w.e);
           }
-          tma_load_2d(dst + NACC * kABytes, &map_a, &ctl->full[slot], s * 128, w.row0);
+          tma_load_2d(dst + kTiles * kABytes, &map_a, &ctl->full[slot], s * 128, w.row0);
         }
       }
     }
@@ -335,13 +337,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t j = it < (uint32_t)C::kStages ? 0 : it - C::kStages; j < it; ++j)
         wait_drain(&ctl->full[j % C::kStages], (j / C::kStages) & 1);
     }
-  } else if (warp == 1) {
+  } else if (warp <= kTiles) {
     // ----------------------------------------------------------- MMAs --
-    // The warp walks the loop together and one elected lane issues, so that
-    // the descriptors stay in uniform registers (a lone lane takes 3 to 5
-    // times as long per instruction: 8192 x 4096 x 28672 1892 -> 1236 us).
+    // One warp per weight tile: an instruction takes about 90 cycles to issue
+    // whatever its width, two warps issue at once.  The warp walks the loop
+    // together and one elected lane issues, so that the descriptors stay in
+    // uniform registers (a lone lane takes three times as long).
+    const int tile = warp - 1;
     const bool el = elect_one();
     const int nst = (p.words + C::kWords - 1) / C::kWords;
+    const uint32_t sfc = tmem + C::kSfBase + tile * C::kSfCols;  // [word][tile, rows] x 4 columns
     uint32_t it = 0, sb_it = 0, t = 0;
     bool ok = true;
     for (int64_t u = blockIdx.x; u < total && ok; u += gridDim.x, ++t) {
@@ -351,18 +356,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t buf = t % C::kBufs;
       ok = warp_wait(&ctl->acc_empty[buf], ((t / C::kBufs) & 1) ^ 1, ctl, p.status);
       tc_fence_after();
-      const uint32_t acc = tmem + buf * C::kAccCols;
+      const uint32_t acc = tmem + buf * C::kAccCols + tile * BN;
       uint32_t accumulate = 0;
       for (int sb = sb0; sb < sb1 && ok; ++sb, ++sb_it) {
         const uint32_t ss = sb_it % kSfRing;
         ok = warp_wait(&ctl->sf_full[ss], (sb_it / kSfRing) & 1, ctl, p.status);
         if (!ok) break;
         if (el) {
-          // scales to tensor memory: blocks of 4 columns, [word][tile]
-          const uint32_t sfa = smem_addr(sf + (size_t)ss * C::kSfSlotBytes);
+          const uint32_t slot = smem_addr(sf + (size_t)ss * C::kSfSlotBytes);
 #pragma unroll
-          for (int b = 0; b < 4 * (NACC + C::kBBlocks); ++b)
-            tmem_cp_scales(tmem + C::kSfBase + b * 4, smem_desc_scales(sfa + b * 512));
+          for (int wd = 0; wd < 4; ++wd) {
+            const uint32_t blk = slot + wd * C::kSfWordBytes;
+            const uint32_t col = sfc + wd * (1 + C::kBBlocks) * 4;
+            tmem_cp_scales(col, smem_desc_scales(blk + tile * 512));
+#pragma unroll
+            for (int b = 0; b < C::kBBlocks; ++b)
+              tmem_cp_scales(col + 4 + b * 4, smem_desc_scales(blk + (kTiles + b) * 512));
+          }
         }
         const int last = min((sb + 1) * C::kPerSb, nst);
         for (int s = sb * C::kPerSb; s < last; ++s, ++it) {
@@ -371,19 +381,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (el) {
             const uint32_t base = smem_addr(stages + (size_t)slot * C::kStageBytes);
+            const uint64_t ad = smem_desc_k_sw128(base + tile * kABytes);
+            const uint64_t bd = smem_desc_k_sw128(base + kTiles * kABytes);
             const int word0 = (s % C::kPerSb) * C::kWords;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int word = word0 + (BITS == 8 ? 0 : j / 2);
               const uint32_t id = BITS == 8 ? j : (j & 1) * 2;
-              const uint32_t sfw = tmem + C::kSfBase + word * (NACC + C::kBBlocks) * 4;
-              const uint64_t bd = smem_desc_k_sw128(base + NACC * kABytes) + j * 2;
-#pragma unroll
-              for (int a = 0; a < NACC; ++a) {
-                const uint64_t ad = smem_desc_k_sw128(base + a * kABytes) + j * 2;
-                mma_mx<BITS>(acc + a * BN, ad, bd, idesc_mx<BITS>(kTileM, BN, id), sfw + a * 4,
-                             sfw + NACC * 4, accumulate | j);
-              }
+              const uint32_t sfw = sfc + word * (1 + C::kBBlocks) * 4;
+              mma_mx<BITS>(acc, ad + j * 2, bd + j * 2, idesc_mx<BITS>(kTileM, BN, id), sfw,
+                           sfw + 4, accumulate | j);
             }
             mma_commit(&ctl->empty[slot]);
           }
@@ -393,13 +400,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok && el) mma_commit(&ctl->acc_full[buf]);
     }
-    // nothing this warp issued may be in flight when the memory goes
+    // nothing these warps issued may be in flight when the memory goes
     if (el) mma_commit(&ctl->drain);
     wait_drain(&ctl->drain, 0);
-  } else if (warp < 4) {
+  } else if (warp == 3 || warp == 12) {
     // ------------------------------------------------------------ scales --
-    const int lw = warp - 2;
-    constexpr int kGroupsA = NACC * 4, kGroupsB = (BN + 31) / 32;
+    const int lw = warp == 12;
+    constexpr int kGroupsA = kTiles * 4, kGroupsB = (BN + 31) / 32;
     uint32_t sb_it = 0;
     bool ok = true;
     const int64_t row_bytes = (int64_t)p.words * 4;
@@ -433,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int g = 0; g < kGroupsA + kGroupsB; ++g) {
           const uint4 v = g < kGroupsA ? va[g < kGroupsA ? g : 0] : vb[g < kGroupsA ? 0 : g - kGroupsA];
-          const int block = g < kGroupsA ? g >> 2 : NACC + ((g - kGroupsA) >> 2);
+          const int block = g < kGroupsA ? g >> 2 : kTiles + ((g - kGroupsA) >> 2);
           const int col = g < kGroupsA ? g & 3 : (g - kGroupsA) & 3;
           uint32_t* d = reinterpret_cast<uint32_t*>(slot + block * 512 + col * 4);
           d[0 * (C::kSfWordBytes / 4)] = v.x;
@@ -506,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
 #pragma unroll
-        for (int tile = 0; tile < NACC; ++tile) {
+        for (int tile = 0; tile < kTiles; ++tile) {
           const int n = w.m + tile * kTileM + quad * 32 + lane;  // this lane's output
           if (n - lane >= p.N) break;
           const bool live = n < p.N;
@@ -648,12 +655,12 @@ cudaError_t make_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, const v
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int BITS, int NACC, int BN, int EPI>
+template <int BITS, int BN, int EPI>
 cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Params& p,
                        int64_t units, cudaStream_t st) {
-  constexpr size_t smem = Cfg<BITS, NACC, BN>::kSmem;
+  constexpr size_t smem = Cfg<BITS, BN>::kSmem;
   static_assert(smem <= kSmemMax, "shared memory");
-  auto kern = mx_gemm<BITS, NACC, BN, EPI>;
+  auto kern = mx_gemm<BITS, BN, EPI>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   const int sms = tc_num_sms();
@@ -661,64 +668,58 @@ cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Param
   return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mw, ma, p);
 }
 
-template <int BITS, int NACC, int EPI>
+template <int BITS, int EPI>
 cudaError_t launch_bn(int bn, const CUtensorMap& mw, const CUtensorMap& ma, const Params& p,
-                       int64_t units, cudaStream_t st) {
+                      int64_t units, cudaStream_t st) {
   switch (bn) {
-    case 16: return launch_one<BITS, NACC, 16, EPI>(mw, ma, p, units, st);
-    case 32: return launch_one<BITS, NACC, 32, EPI>(mw, ma, p, units, st);
-    case 64: return launch_one<BITS, NACC, 64, EPI>(mw, ma, p, units, st);
-    case 96: return launch_one<BITS, NACC, 96, EPI>(mw, ma, p, units, st);
-    default: return launch_one<BITS, NACC, 192, EPI>(mw, ma, p, units, st);
+    case 16: return launch_one<BITS, 16, EPI>(mw, ma, p, units, st);
+    case 32: return launch_one<BITS, 32, EPI>(mw, ma, p, units, st);
+    case 64: return launch_one<BITS, 64, EPI>(mw, ma, p, units, st);
+    case 96: return launch_one<BITS, 96, EPI>(mw, ma, p, units, st);
+    default: return launch_one<BITS, 192, EPI>(mw, ma, p, units, st);
   }
 }
 
 template <int BITS>
 cudaError_t launch_epi(const MxGemm& g, const MxPlan& pl, const CUtensorMap& mw,
-                       const CUtensorMap& ma, const Params& p,
-                       int64_t units, cudaStream_t st) {
-  if (g.epi == MX_EPI_GATED) return launch_bn<BITS, 2, MX_EPI_GATED>(pl.bn, mw, ma, p, units, st);
-  if (g.epi == MX_EPI_OUT)
-    return pl.tiles == 2 ? launch_bn<BITS, 2, MX_EPI_OUT>(pl.bn, mw, ma, p, units, st)
-                         : launch_bn<BITS, 1, MX_EPI_OUT>(pl.bn, mw, ma, p, units, st);
-  return pl.tiles == 2 ? launch_bn<BITS, 2, MX_EPI_PART>(pl.bn, mw, ma, p, units, st)
-                       : launch_bn<BITS, 1, MX_EPI_PART>(pl.bn, mw, ma, p, units, st);
+                       const CUtensorMap& ma, const Params& p, int64_t units, cudaStream_t st) {
+  switch (g.epi) {
+    case MX_EPI_OUT: return launch_bn<BITS, MX_EPI_OUT>(pl.bn, mw, ma, p, units, st);
+    case MX_EPI_PART: return launch_bn<BITS, MX_EPI_PART>(pl.bn, mw, ma, p, units, st);
+    default: return launch_bn<BITS, MX_EPI_GATED>(pl.bn, mw, ma, p, units, st);
+  }
 }
 
 }  // namespace
 
 // Rows per tile: above the average load of a live expert by half, so that
 // most experts are one chunk (their weights are then read once) without many
-// columns to spare.  Weight tiles per unit and K splits: the choice with the
-// least estimated time, in bytes that one SM brings in (a wave of units
-// brings in its weights and rows, and 24 KB more for a unit's start and end;
-// partial sums are written and read again, and cost a launch).
+// columns to spare.  K splits: the count with the least estimated time, in
+// bytes that one SM brings in (a wave of units brings in its weights and rows,
+// and 24 KB more for a unit's start and end; partial sums are written and read
+// again, and cost a launch).
 MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated, int a_bits) {
   MxPlan pl;
   const int64_t live = std::max<int64_t>(1, std::min<int64_t>(S, E));
   const int64_t avg = (S + live - 1) / live;
   pl.bn = avg <= 8 ? 16 : avg <= 20 ? 32 : avg <= 40 ? 64 : (avg <= 128 || gated || a_bits == 4) ? 96 : 192;
   pl.splits = 1;
-  pl.tiles = 2;
   if (gated) return pl;
   const int sms = tc_num_sms();
   const int sbs = (K + 511) / 512;
   const int64_t chunks = std::max(live, (S + pl.bn - 1) / pl.bn);
+  const int64_t tiles = (N + kTiles * kTileM - 1) / (kTiles * kTileM);
   const double row = a_bits / 8.0 + 1.0 / 32, wrow = 0.5 + 1.0 / 32;
   double best = 0;
-  for (int tiles = 2; tiles >= 1; --tiles) {
-    const int64_t mt = (N + tiles * kTileM - 1) / (tiles * kTileM);
-    for (int sp = 1; sp <= 16 && sp <= sbs; ++sp) {
-      if (sp > 1 && S > 1024) break;  // partial sums would cost more than idle SMs
-      const double waves = std::ceil((double)(chunks * mt * sp) / sms);
-      const double unit = 512.0 * std::ceil((double)sbs / sp) * (tiles * kTileM * wrow + pl.bn * row);
-      double cost = waves * (unit + 24e3);
-      if (sp > 1) cost += 80e3 + 4.0 * sp * S * N / sms;
-      if (best == 0 || cost < best) {
-        best = cost;
-        pl.tiles = tiles;
-        pl.splits = sp;
-      }
+  for (int sp = 1; sp <= 16 && sp <= sbs; ++sp) {
+    if (sp > 1 && S > 1024) break;  // partial sums would cost more than idle SMs
+    const double waves = std::ceil((double)(chunks * tiles * sp) / sms);
+    const double unit = 512.0 * std::ceil((double)sbs / sp) * (kTiles * kTileM * wrow + pl.bn * row);
+    double cost = waves * (unit + 24e3);
+    if (sp > 1) cost += 80e3 + 4.0 * sp * S * N / sms;
+    if (best == 0 || cost < best) {
+      best = cost;
+      pl.splits = sp;
     }
   }
   return pl;
@@ -755,7 +756,7 @@ cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStream_t st) {
   p.K = g.K;
   p.N = g.N;
   p.R = (int)g.R;
-  p.mrows = gated ? kTileM : pl.tiles * kTileM;
+  p.mrows = gated ? kTileM : kTiles * kTileM;
   p.up_row = gated ? g.N : kTileM;
   p.wrows = g.wrows;
   p.mtiles = (g.N + p.mrows - 1) / p.mrows;
