@@ -48,6 +48,10 @@ __device__ __forceinline__ float mx_scaled(float v, float inv) {
   return inv == 0.0f ? 0.0f : v * inv;
 }
 
+// Larger of each 16-bit half, unsigned: magnitudes of two 16-bit floats (their
+// bits without the sign order as they do, NaN above infinity).
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
 // Two elements, rounded to nearest even and clamped to the largest finite
 // one; the first goes to the low nibble / byte.
 __device__ __forceinline__ uint32_t e2m1x2(float a, float b) {
@@ -61,30 +65,27 @@ __device__ __forceinline__ uint32_t max_bits(uint32_t m, float v) {
   return max(m, __float_as_uint(v) & 0x7fffffffu);
 }
 
-// Eight consecutive elements of a block, held by one of the four adjacent
-// lanes that share it: the block's scale code, and the lane's codes in
-// q[0] (4 bits) or q[0..1] (8 bits).
-template <int BITS>
-__device__ __forceinline__ uint32_t mx_pack8(const float (&v)[8], uint32_t (&q)[2]) {
+// Largest of the four adjacent lanes that share a block.
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+
+// Bits of the largest of eight magnitudes.
+__device__ __forceinline__ uint32_t max8_bits(const float (&v)[8]) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max_bits(m, v[i]);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const uint32_t code = mx_scale_code<BITS>(m);
-  const float inv = mx_inv_scale(code);
-  float t[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = mx_scaled(v[i], inv);
-  if (BITS == 4) {
-    q[0] = e2m1x2(t[0], t[1]) | e2m1x2(t[2], t[3]) << 8 | e2m1x2(t[4], t[5]) << 16 |
-           e2m1x2(t[6], t[7]) << 24;
-    q[1] = 0;
-  } else {
-    q[0] = e4m3x2(t[0], t[1]) | e4m3x2(t[2], t[3]) << 16;
-    q[1] = e4m3x2(t[4], t[5]) | e4m3x2(t[6], t[7]) << 16;
-  }
-  return code;
+  return m;
+}
+
+// Bits of the largest magnitude of a block of 16-bit floats, eight per lane.
+__device__ __forceinline__ uint32_t block_max16(uint4 r) {
+  uint32_t m = max_halves(max_halves(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu),
+                          max_halves(r.z & 0x7fff7fffu, r.w & 0x7fff7fffu));
+  m = max_halves(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max_halves(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  return max(m >> 16, m & 0xffffu);
 }
 
 // Eight consecutive values of type T as float32 (16-byte aligned; 32 bytes of
@@ -103,6 +104,8 @@ struct Row8<__nv_bfloat16> {
     v[0] = bf16_lo(r.x); v[1] = bf16_hi(r.x); v[2] = bf16_lo(r.y); v[3] = bf16_hi(r.y);
     v[4] = bf16_lo(r.z); v[5] = bf16_hi(r.z); v[6] = bf16_lo(r.w); v[7] = bf16_hi(r.w);
   }
+  // float32 bits of the block's largest magnitude (four adjacent lanes)
+  __device__ __forceinline__ uint32_t block_amax() const { return block_max16(r) << 16; }
 };
 
 template <>
@@ -120,6 +123,9 @@ struct Row8<__half> {
       v[2 * i + 1] = f.y;
     }
   }
+  __device__ __forceinline__ uint32_t block_amax() const {
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)block_max16(r))));
+  }
 };
 
 template <>
@@ -133,7 +139,31 @@ struct Row8<float> {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
+  __device__ __forceinline__ uint32_t block_amax() const {
+    float v[8];
+    get(v);
+    return block_max(max8_bits(v));
+  }
 };
+
+// Eight consecutive elements of a block with scale code `code`: their codes in
+// q[0] (4 bits) or q[0..1] (8 bits).
+template <int BITS>
+__device__ __forceinline__ void mx_pack8(const float (&v)[8], uint32_t code, uint32_t (&q)[2]) {
+  const float inv = mx_inv_scale(code);
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = v[i] * inv;
+  if (BITS == 4) {
+    q[0] = e2m1x2(t[0], t[1]) | e2m1x2(t[2], t[3]) << 8 | e2m1x2(t[4], t[5]) << 16 |
+           e2m1x2(t[6], t[7]) << 24;
+    q[1] = 0;
+  } else {
+    q[0] = e4m3x2(t[0], t[1]) | e4m3x2(t[2], t[3]) << 16;
+    q[1] = e4m3x2(t[4], t[5]) | e4m3x2(t[6], t[7]) << 16;
+  }
+  if (code == 255u) q[0] = q[1] = 0;  // (infinity times 0 above)
+}
 
 // Eight float32 values rounded once (to nearest even) and stored.
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
