@@ -465,7 +465,7 @@ int moe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int 
  * with one final rounding; a result is the same on every run.
  * The workspace holds float32 partial sums where K is split (few units of
  * work); moe_mx_product_workspace may return 0 (workspace may then be NULL).
- * Limits: K a multiple of 128, N >= 1, E <= 1024, R < 2^30.
+ * Limits: K a multiple of 128, N >= 1, E <= 1024, R < 2^30, R * N < 2^39.
  * Errors: MQ_ERR_INVALID_ARG, MQ_ERR_UNSUPPORTED (limits), MQ_ERR_WORKSPACE.
  */
 size_t moe_mx_product_workspace(int64_t R, int K, int N, int E);

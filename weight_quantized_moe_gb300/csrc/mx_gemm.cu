@@ -34,6 +34,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 namespace {
@@ -48,6 +49,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kMaxStages = 12;
 constexpr int kSfRing = 4;             // scale slots, 512 k each
 constexpr int kMaxE = 1024;
+constexpr int kUnitList = 128;         // units of a CTA that are decoded at its start
 constexpr int kGroup = 8;              // weight tiles that a chunk walk shares
 constexpr unsigned long long kWaitNs = 1000000000ull;
 constexpr size_t kSmemMax = 227 * 1024;
@@ -58,9 +60,9 @@ struct Cfg {
   static constexpr int kPerSb = 4 / kWords;         // stages per scale slot
   static constexpr int kBBytes = BN * 128;
   static constexpr int kStageBytes = kTiles * kABytes + kBBytes;
-  // bytes TMA reports for a stage: those it reads, so half a weight tile where
-  // it spreads the nibbles
-  static constexpr int kTxBytes = kTiles * (BITS == 8 ? kABytes / 2 : kABytes) + kBBytes;
+  // bytes TMA reports for a stage's weights: those it reads, so half a tile
+  // where it spreads the nibbles
+  static constexpr int kTxWeights = kTiles * (BITS == 8 ? kABytes / 2 : kABytes);
   static constexpr int kBBlocks = (BN + 127) / 128;
   static constexpr int kSfWordBytes = (kTiles + kBBlocks) * 512;
   static constexpr int kSfSlotBytes = 4 * kSfWordBytes;
@@ -70,7 +72,7 @@ struct Cfg {
   static constexpr int kBufs = 2 * kAccCols + kTiles * kSfCols <= 512 ? 2 : 1;
   static constexpr int kSfBase = kBufs * kAccCols;
   static_assert(kSfBase + kTiles * kSfCols <= 512, "tensor memory");
-  static constexpr size_t kFixed = 1024 + kSfRing * (size_t)kSfSlotBytes + 1024 + (kMaxE + 1) * 4;
+  static constexpr size_t kFixed = 1024 + kSfRing * (size_t)kSfSlotBytes + 1024 + kUnitList * 16 + (kMaxE + 1) * 4;
   static constexpr int kFit = (int)((kSmemMax - kFixed) / kStageBytes);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static_assert(kStages >= 2, "shared memory");
@@ -134,9 +136,9 @@ __device__ __forceinline__ bool segment(const Params& p, int e, int& start, int&
 // chunk over a group before the next one (the CTAs at work share the group's
 // weights and the chunks' rows in L2), K splits innermost.
 template <int BN>
-__device__ __forceinline__ Unit unit_at(const Params& p, const int* chunk_start, int64_t u) {
-  const int per = p.mtiles * p.splits;
-  const int g = (int)(u / per);  // global chunk-equivalent index: locates the expert
+__device__ __forceinline__ Unit decode_unit(const Params& p, const int* chunk_start, uint32_t u) {
+  const uint32_t per = p.mtiles * p.splits;
+  const int g = (int)(u / per);  // a chunk's position in the walk locates its expert
   int lo = 0, hi = p.E;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -145,21 +147,38 @@ __device__ __forceinline__ Unit unit_at(const Params& p, const int* chunk_start,
   }
   Unit w;
   w.e = lo;
-  const int nch = chunk_start[lo + 1] - chunk_start[lo];
-  const int64_t r = u - (int64_t)chunk_start[lo] * per;
-  const int64_t per_group = (int64_t)kGroup * nch * p.splits;
-  const int grp = (int)(r / per_group);
-  const int64_t rem = r - grp * per_group;
-  const int tiles = min(kGroup, p.mtiles - grp * kGroup) * p.splits;
-  const int c = (int)(rem / tiles);
-  const int t = (int)(rem - (int64_t)c * tiles);
-  w.m = (grp * kGroup + t / p.splits) * p.mrows;
-  w.split = t % p.splits;
+  const uint32_t nch = chunk_start[lo + 1] - chunk_start[lo];
+  const uint32_t r = u - chunk_start[lo] * per;
+  const uint32_t per_group = kGroup * nch * p.splits;
+  const uint32_t grp = r / per_group;
+  const uint32_t rem = r - grp * per_group;
+  const uint32_t tiles = min(kGroup, p.mtiles - (int)grp * kGroup) * p.splits;
+  const uint32_t c = rem / tiles;
+  const uint32_t t = rem - c * tiles;
+  w.m = (int)(grp * kGroup + t / p.splits) * p.mrows;
+  w.split = (int)(t % p.splits);
   int start, count;
   segment(p, lo, start, count);
-  w.row0 = start + c * BN;
-  w.n = min(BN, count - c * BN);
+  w.row0 = start + (int)c * BN;
+  w.n = min(BN, count - (int)c * BN);
   w.single = nch == 1;
+  return w;
+}
+
+// The i-th unit of this CTA: from the list in shared memory (decoded once, by
+// all threads at a time), past its end on the spot.
+template <int BN>
+__device__ __forceinline__ Unit unit_at(const Params& p, const int* chunk_start, const int4* list,
+                                        uint32_t i) {
+  if (i >= kUnitList) return decode_unit<BN>(p, chunk_start, blockIdx.x + i * gridDim.x);
+  const int4 v = list[i];
+  Unit w;
+  w.e = v.x & 0xffff;
+  w.single = (v.x >> 16) & 1;
+  w.split = v.x >> 17;
+  w.row0 = v.y;
+  w.n = v.z;
+  w.m = v.w;
   return w;
 }
 
@@ -237,14 +256,15 @@ __device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float
 template <int BITS, int BN, int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
-            const Params p) {
+            const __grid_constant__ CUtensorMap map_a32, const Params p) {
   using C = Cfg<BITS, BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* stages = smem;
   uint8_t* sf = stages + (size_t)C::kStages * C::kStageBytes;
   Ctl* ctl = reinterpret_cast<Ctl*>(sf + (size_t)kSfRing * C::kSfSlotBytes);
-  int* chunk_start = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(ctl) + 1024);
+  int4* list = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(ctl) + 1024);
+  int* chunk_start = reinterpret_cast<int*>(list + kUnitList);
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
@@ -252,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     tma_prefetch_desc(&map_w);
     tma_prefetch_desc(&map_a);
+    tma_prefetch_desc(&map_a32);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], kTiles);
@@ -268,20 +289,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl->abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {  // (and warp 2 the table, below)
+  if (warp == 1) {
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
   mq::pdl_wait();
   mq::pdl_trigger();
-  if (warp == 2) {  // chunks of each expert, scanned 32 experts at a time
+  // Chunks of each expert, scanned; then this CTA's units.
+  bool fine = true;
+  for (int e = tid; e < p.E; e += kThreads) {
+    int start, count;
+    fine &= segment(p, e, start, count);
+    chunk_start[e] = (count + BN - 1) / BN;
+  }
+  if (!fine && blockIdx.x == 0) mq::flag(p.status, MQ_DEV_BAD_OFFSETS);
+  __syncthreads();
+  if (warp == 0) {
     int run = 0;
-    bool fine = true;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      int start, count = 0;
-      if (e < p.E) fine &= segment(p, e, start, count);
-      const int mine = (count + BN - 1) / BN;
+      const int mine = e < p.E ? chunk_start[e] : 0;
       int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -292,13 +319,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       run += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) chunk_start[p.E] = run;
-    if (!fine && blockIdx.x == 0) mq::flag(p.status, MQ_DEV_BAD_OFFSETS);
+  }
+  __syncthreads();
+  const uint32_t total = (uint32_t)chunk_start[p.E] * p.mtiles * p.splits;
+  const uint32_t units = blockIdx.x < total ? (total - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+  if (tid < kUnitList && tid < units) {
+    const Unit w = decode_unit<BN>(p, chunk_start, blockIdx.x + tid * gridDim.x);
+    list[tid] = make_int4(w.e | (w.single ? 1 << 16 : 0) | w.split << 17, w.row0, w.n, w.m);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-  const int64_t total = (int64_t)chunk_start[p.E] * p.mtiles * p.splits;
 
   if (warp == 0) {
     // ---------------------------------------------------------- codes --
@@ -306,10 +338,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t pol_once = l2_policy_evict_first();
     uint32_t it = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < total && ok; u += gridDim.x) {
-      const Unit w = unit_at<BN>(p, chunk_start, u);
+    for (uint32_t u = 0; u < units && ok; ++u) {
+      const Unit w = unit_at<BN>(p, chunk_start, list, u);
       const int sb0 = (int)((int64_t)p.sbs * w.split / p.splits);
       const int sb1 = (int)((int64_t)p.sbs * (w.split + 1) / p.splits);
+      const int rows = min(BN, (w.n + 31) & ~31);  // a partly filled chunk: boxes of 32 rows
       const int st0 = sb0 * C::kPerSb;
       const int st1 = min(sb1 * C::kPerSb, (p.words + C::kWords - 1) / C::kWords);
       for (int s = st0; s < st1; ++s, ++it) {
@@ -320,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint8_t* dst = stages + (size_t)slot * C::kStageBytes;
         if (el) {
-          mbar_arrive_expect_tx(&ctl->full[slot], C::kTxBytes);
+          mbar_arrive_expect_tx(&ctl->full[slot], C::kTxWeights + rows * 128);
 #pragma unroll
           for (int a = 0; a < kTiles; ++a) {
             const int row = w.m + a * p.up_row;
@@ -329,7 +362,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             else
               tma_load_3d(dst + a * kABytes, &map_w, &ctl->full[slot], s * 128, row, w.e);
           }
-          tma_load_2d(dst + kTiles * kABytes, &map_a, &ctl->full[slot], s * 128, w.row0);
+          if (rows == BN) {
+            tma_load_2d(dst + kTiles * kABytes, &map_a, &ctl->full[slot], s * 128, w.row0);
+          } else {
+            for (int r = 0; r < rows; r += 32)
+              tma_load_2d(dst + kTiles * kABytes + r * 128, &map_a32, &ctl->full[slot], s * 128,
+                          w.row0 + r);
+          }
         }
       }
     }
@@ -347,16 +386,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool el = elect_one();
     const int nst = (p.words + C::kWords - 1) / C::kWords;
     const uint32_t sfc = tmem + C::kSfBase + tile * C::kSfCols;  // [word][tile, rows] x 4 columns
-    uint32_t it = 0, sb_it = 0, t = 0;
+    uint32_t it = 0, sb_it = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < total && ok; u += gridDim.x, ++t) {
-      const Unit w = unit_at<BN>(p, chunk_start, u);
+    for (uint32_t t = 0; t < units && ok; ++t) {
+      const Unit w = unit_at<BN>(p, chunk_start, list, t);
       const int sb0 = (int)((int64_t)p.sbs * w.split / p.splits);
       const int sb1 = (int)((int64_t)p.sbs * (w.split + 1) / p.splits);
       const uint32_t buf = t % C::kBufs;
       ok = warp_wait(&ctl->acc_empty[buf], ((t / C::kBufs) & 1) ^ 1, ctl, p.status);
       tc_fence_after();
       const uint32_t acc = tmem + buf * C::kAccCols + tile * BN;
+      // as many columns as the chunk has rows, in steps of 16
+      const uint32_t idesc = idesc_mx<BITS>(kTileM, (w.n + 15) & ~15, 0);
       uint32_t accumulate = 0;
       for (int sb = sb0; sb < sb1 && ok; ++sb, ++sb_it) {
         const uint32_t ss = sb_it % kSfRing;
@@ -389,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int word = word0 + (BITS == 8 ? 0 : j / 2);
               const uint32_t id = BITS == 8 ? j : (j & 1) * 2;
               const uint32_t sfw = sfc + word * (1 + C::kBBlocks) * 4;
-              mma_mx<BITS>(acc, ad + j * 2, bd + j * 2, idesc_mx<BITS>(kTileM, BN, id), sfw,
-                           sfw + 4, accumulate | j);
+              mma_mx<BITS>(acc, ad + j * 2, bd + j * 2, idesc | id << 4 | id << 29, sfw, sfw + 4,
+                           accumulate | j);
             }
             mma_commit(&ctl->empty[slot]);
           }
@@ -410,8 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t sb_it = 0;
     bool ok = true;
     const int64_t row_bytes = (int64_t)p.words * 4;
-    for (int64_t u = blockIdx.x; u < total && ok; u += gridDim.x) {
-      const Unit w = unit_at<BN>(p, chunk_start, u);
+    for (uint32_t u = 0; u < units && ok; ++u) {
+      const Unit w = unit_at<BN>(p, chunk_start, list, u);
       const int sb0 = (int)((int64_t)p.sbs * w.split / p.splits);
       const int sb1 = (int)((int64_t)p.sbs * (w.split + 1) / p.splits);
       for (int sb = sb0; sb < sb1; ++sb, ++sb_it) {
@@ -457,9 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------- epilogue --
     const int quad = warp & 3;       // the tensor-memory lanes this warp may read
     const int half = (warp - 4) >> 2;  // which 16-column steps it takes
-    uint32_t t = 0;
-    for (int64_t u = blockIdx.x; u < total; u += gridDim.x, ++t) {
-      const Unit w = unit_at<BN>(p, chunk_start, u);
+    for (uint32_t t = 0; t < units; ++t) {
+      const Unit w = unit_at<BN>(p, chunk_start, list, t);
       const uint32_t buf = t % C::kBufs;
       // Destination rows and factors of the chunk, one column per lane and
       // 32-column group: loaded before the accumulators are there.
@@ -656,37 +696,45 @@ cudaError_t make_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, const v
 }
 
 template <int BITS, int BN, int EPI>
-cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const Params& p,
+cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const CUtensorMap& mr, const Params& p,
                        int64_t units, cudaStream_t st) {
   constexpr size_t smem = Cfg<BITS, BN>::kSmem;
   static_assert(smem <= kSmemMax, "shared memory");
   auto kern = mx_gemm<BITS, BN, EPI>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   const int sms = tc_num_sms();
   const int grid = units < sms ? (int)units : sms;
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mw, ma, p);
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mw, ma, mr, p);
 }
 
 template <int BITS, int EPI>
-cudaError_t launch_bn(int bn, const CUtensorMap& mw, const CUtensorMap& ma, const Params& p,
+cudaError_t launch_bn(int bn, const CUtensorMap& mw, const CUtensorMap& ma, const CUtensorMap& mr, const Params& p,
                       int64_t units, cudaStream_t st) {
   switch (bn) {
-    case 16: return launch_one<BITS, 16, EPI>(mw, ma, p, units, st);
-    case 32: return launch_one<BITS, 32, EPI>(mw, ma, p, units, st);
-    case 64: return launch_one<BITS, 64, EPI>(mw, ma, p, units, st);
-    case 96: return launch_one<BITS, 96, EPI>(mw, ma, p, units, st);
-    default: return launch_one<BITS, 192, EPI>(mw, ma, p, units, st);
+    case 16: return launch_one<BITS, 16, EPI>(mw, ma, mr, p, units, st);
+    case 32: return launch_one<BITS, 32, EPI>(mw, ma, mr, p, units, st);
+    case 64: return launch_one<BITS, 64, EPI>(mw, ma, mr, p, units, st);
+    case 96: return launch_one<BITS, 96, EPI>(mw, ma, mr, p, units, st);
+    default: return launch_one<BITS, 192, EPI>(mw, ma, mr, p, units, st);
   }
 }
 
 template <int BITS>
 cudaError_t launch_epi(const MxGemm& g, const MxPlan& pl, const CUtensorMap& mw,
-                       const CUtensorMap& ma, const Params& p, int64_t units, cudaStream_t st) {
+                       const CUtensorMap& ma, const CUtensorMap& mr, const Params& p, int64_t units, cudaStream_t st) {
   switch (g.epi) {
-    case MX_EPI_OUT: return launch_bn<BITS, MX_EPI_OUT>(pl.bn, mw, ma, p, units, st);
-    case MX_EPI_PART: return launch_bn<BITS, MX_EPI_PART>(pl.bn, mw, ma, p, units, st);
-    default: return launch_bn<BITS, MX_EPI_GATED>(pl.bn, mw, ma, p, units, st);
+    case MX_EPI_OUT: return launch_bn<BITS, MX_EPI_OUT>(pl.bn, mw, ma, mr, p, units, st);
+    case MX_EPI_PART: return launch_bn<BITS, MX_EPI_PART>(pl.bn, mw, ma, mr, p, units, st);
+    default: return launch_bn<BITS, MX_EPI_GATED>(pl.bn, mw, ma, mr, p, units, st);
   }
 }
 
@@ -702,7 +750,7 @@ MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated, int a_bits) {
   MxPlan pl;
   const int64_t live = std::max<int64_t>(1, std::min<int64_t>(S, E));
   const int64_t avg = (S + live - 1) / live;
-  pl.bn = avg <= 8 ? 16 : avg <= 20 ? 32 : avg <= 40 ? 64 : (avg <= 128 || gated || a_bits == 4) ? 96 : 192;
+  pl.bn = avg <= 8 ? 16 : avg <= 20 ? 32 : avg <= 40 ? 64 : (avg <= 128 || (gated && a_bits == 4)) ? 96 : 192;
   pl.splits = 1;
   if (gated) return pl;
   const int sms = tc_num_sms();
@@ -729,7 +777,7 @@ cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStream_t st) {
   cudaError_t err = get_encoder();
   if (err != cudaSuccess) return err;
   const bool gated = g.epi == MX_EPI_GATED;
-  CUtensorMap mw, ma;
+  CUtensorMap mw, ma, mr;
   {
     // 8-bit rows: the weights' nibbles are spread to the mixed instruction's
     // operand form on the way; 4-bit rows: packed bytes, as both operands are
@@ -745,6 +793,9 @@ cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStream_t st) {
     const cuuint64_t adims[2] = {row, (cuuint64_t)g.R};
     const cuuint32_t abox[2] = {128, (cuuint32_t)pl.bn};
     err = make_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, g.a, adims, &row, abox);
+    if (err != cudaSuccess) return err;
+    const cuuint32_t rbox[2] = {128, 32};
+    err = make_map(&mr, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, g.a, adims, &row, rbox);
     if (err != cudaSuccess) return err;
   }
   Params p = {};
@@ -775,8 +826,8 @@ cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStream_t st) {
   const int64_t live = g.S < g.E ? g.S : g.E;
   const int64_t units = (live + g.S / pl.bn) * p.mtiles * p.splits;  // at most
   if (units <= 0) return cudaSuccess;
-  return g.a_bits == 8 ? launch_epi<8>(g, pl, mw, ma, p, units, st)
-                       : launch_epi<4>(g, pl, mw, ma, p, units, st);
+  return g.a_bits == 8 ? launch_epi<8>(g, pl, mw, ma, mr, p, units, st)
+                       : launch_epi<4>(g, pl, mw, ma, mr, p, units, st);
 }
 
 cudaError_t launch_mx_reduce(const float* part, int splits, int64_t rows, int N,
