@@ -72,7 +72,8 @@ struct Cfg {
   static constexpr int kBufs = 2 * kAccCols + kTiles * kSfCols <= 512 ? 2 : 1;
   static constexpr int kSfBase = kBufs * kAccCols;
   static_assert(kSfBase + kTiles * kSfCols <= 512, "tensor memory");
-  static constexpr size_t kFixed = 1024 + kSfRing * (size_t)kSfSlotBytes + 1024 + kUnitList * 16 + (kMaxE + 1) * 4;
+  static constexpr int kDestBytes = 2 * BN * 16;    // epilogue: where each column goes
+  static constexpr size_t kFixed = 1024 + kDestBytes + kSfRing * (size_t)kSfSlotBytes + 1024 + kUnitList * 16 + (kMaxE + 1) * 4;
   static constexpr int kFit = (int)((kSmemMax - kFixed) / kStageBytes);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static_assert(kStages >= 2, "shared memory");
@@ -247,6 +248,11 @@ __device__ __forceinline__ uint4 load_words(const uint8_t* row, int w0, int word
   return v;
 }
 
+// Joins the epilogue warps.
+__device__ __forceinline__ void epilogue_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+}
+
 __device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float v) {
   if (dtype == MQ_DTYPE_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
   else if (dtype == MQ_DTYPE_F16) static_cast<__half*>(out)[i] = __float2half_rn(v);
@@ -264,7 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sf = stages + (size_t)C::kStages * C::kStageBytes;
   Ctl* ctl = reinterpret_cast<Ctl*>(sf + (size_t)kSfRing * C::kSfSlotBytes);
   int4* list = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(ctl) + 1024);
-  int* chunk_start = reinterpret_cast<int*>(list + kUnitList);
+  int4* dest_table = list + kUnitList;  // [2][BN]
+  int* chunk_start = reinterpret_cast<int*>(dest_table + 2 * BN);
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
@@ -498,27 +505,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------- epilogue --
     const int quad = warp & 3;       // the tensor-memory lanes this warp may read
     const int half = (warp - 4) >> 2;  // which 16-column steps it takes
+    // MX_EPI_PART: thread c of the epilogue looks up where column c of a unit
+    // goes, one unit ahead, and passes it on through shared memory.
+    const int col = tid - 128;
+    int dest = 0;
+    float factor = 1.0f;
+    auto look_up = [&](uint32_t t) {
+      if (t >= units || col >= BN) return;
+      const Unit w = unit_at<BN>(p, chunk_start, list, t);
+      if (col >= w.n) return;
+      dest = p.dest ? p.dest[w.row0 + col] : w.row0 + col;
+      factor = p.dest_w ? p.dest_w[dest] : 1.0f;
+    };
+    if constexpr (EPI == MX_EPI_PART) look_up(0);
+    bool ok = true;  // (a warp that gave up still meets the others at the barrier)
     for (uint32_t t = 0; t < units; ++t) {
       const Unit w = unit_at<BN>(p, chunk_start, list, t);
       const uint32_t buf = t % C::kBufs;
-      // Destination rows and factors of the chunk, one column per lane and
-      // 32-column group: loaded before the accumulators are there.
-      constexpr int kCols = (BN + 31) / 32;
-      int dest[EPI == MX_EPI_PART ? kCols : 1];
-      float factor[EPI == MX_EPI_PART ? kCols : 1];
+      const int4* table = dest_table + (t & 1) * BN;
       if constexpr (EPI == MX_EPI_PART) {
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) {
-          const int c = i * 32 + lane;
-          dest[i] = 0;
-          factor[i] = 1.0f;
-          if (c < w.n) {
-            dest[i] = p.dest ? p.dest[w.row0 + c] : w.row0 + c;
-            if (p.dest_w) factor[i] = p.dest_w[dest[i]];
-          }
+        if (col < BN) {
+          const int64_t at = (int64_t)dest * p.N;
+          dest_table[(t & 1) * BN + col] =
+              make_int4((int)(uint32_t)at, (int)(at >> 32), __float_as_int(factor), 0);
         }
+        epilogue_barrier();
+        look_up(t + 1);
       }
-      if (!warp_wait(&ctl->acc_full[buf], (t / C::kBufs) & 1, ctl, p.status)) break;
+      ok = ok && warp_wait(&ctl->acc_full[buf], (t / C::kBufs) & 1, ctl, p.status);
+      if (!ok) continue;
       tc_fence_after();
       const uint32_t acc = tmem + buf * C::kAccCols + ((uint32_t)(quad * 32) << 16);
       if constexpr (EPI == MX_EPI_GATED) {
@@ -557,19 +572,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int n = w.m + tile * kTileM + quad * 32 + lane;  // this lane's output
           if (n - lane >= p.N) break;
           const bool live = n < p.N;
-#pragma unroll
-          for (int i = 0; i < kCols; ++i) {
-            const int c0 = i * 32 + half * 16;
-            if (c0 >= w.n) break;
+          for (int c0 = half * 16; c0 < w.n; c0 += 32) {
             uint32_t v[16];
             tmem_ld16_sync(acc + tile * BN + c0, v);
             if constexpr (EPI == MX_EPI_PART) {
               float* part = p.part + (int64_t)w.split * p.part_rows * p.N + n;
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const int row = __shfl_sync(0xffffffffu, dest[i], half * 16 + j);
-                const float f = __shfl_sync(0xffffffffu, factor[i], half * 16 + j);
-                if (live && c0 + j < w.n) part[(int64_t)row * p.N] = __uint_as_float(v[j]) * f;
+                const int4 d = table[c0 + j];
+                const int64_t at = (int64_t)(uint32_t)d.x | (int64_t)d.y << 32;
+                if (live && c0 + j < w.n)
+                  part[at] = __uint_as_float(v[j]) * __int_as_float(d.z);
               }
             } else {
               const int64_t at = (int64_t)(w.row0 + c0) * p.N + n;
