@@ -246,6 +246,7 @@ struct MxGemm {
 };
 struct MxPlan {
   int bn;      // rows per tile
+  bool pair;   // CTA pairs (cta_group::2), else single CTAs
   int splits;  // K splits (MX_EPI_PART)
 };
 MQ_HIDDEN MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated, int a_bits);

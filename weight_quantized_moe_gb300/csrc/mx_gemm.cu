@@ -43,22 +43,25 @@ using namespace mq::ptx;
 
 constexpr int kTileM = 128;
 constexpr int kABytes = kTileM * 128;  // one weight tile of a stage
-constexpr int kTiles = 2;              // weight tiles of a unit, one MMA warp each
-constexpr int kThreads = 416;
+constexpr int kThreads = 480;
+constexpr int kSfWarps = 4;            // warps 3 and 12-14
 constexpr int kEpiWarps = 8;
 constexpr int kMaxStages = 12;
 constexpr int kSfRing = 4;             // scale slots, 512 k each
 constexpr int kMaxE = 1024;
+constexpr int kPairRows = 224;         // rows per tile of a CTA pair
 constexpr int kUnitList = 128;         // units of a CTA that are decoded at its start
 constexpr int kGroup = 8;              // weight tiles that a chunk walk shares
 constexpr unsigned long long kWaitNs = 1000000000ull;
 constexpr size_t kSmemMax = 227 * 1024;
 
-template <int BITS, int BN>
+template <int BITS, int BN, int CG>
 struct Cfg {
+  static constexpr int kTiles = CG == 2 ? 1 : 2;    // weight tiles of a unit, one MMA warp each
   static constexpr int kWords = BITS == 8 ? 1 : 2;  // 128-k scale words per stage
   static constexpr int kPerSb = 4 / kWords;         // stages per scale slot
-  static constexpr int kBBytes = BN * 128;
+  static constexpr int kBRows = BN / CG;            // rows of A (operand B) in each CTA
+  static constexpr int kBBytes = kBRows * 128;
   static constexpr int kStageBytes = kTiles * kABytes + kBBytes;
   // bytes TMA reports for a stage's weights: those it reads, so half a tile
   // where it spreads the nibbles
@@ -73,7 +76,8 @@ struct Cfg {
   static constexpr int kSfBase = kBufs * kAccCols;
   static_assert(kSfBase + kTiles * kSfCols <= 512, "tensor memory");
   static constexpr int kDestBytes = 2 * BN * 16;    // epilogue: where each column goes
-  static constexpr size_t kFixed = 1024 + kDestBytes + kSfRing * (size_t)kSfSlotBytes + 1024 + kUnitList * 16 + (kMaxE + 1) * 4;
+  static constexpr int kSwapBytes = CG == 2 ? 2 * kEpiWarps * 1024 : 0;  // gate and up change warps
+  static constexpr size_t kFixed = 1024 + kDestBytes + kSwapBytes + kSfRing * (size_t)kSfSlotBytes + 1024 + kUnitList * 16 + (kMaxE + 1) * 4;
   static constexpr int kFit = (int)((kSmemMax - kFixed) / kStageBytes);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static_assert(kStages >= 2, "shared memory");
@@ -98,8 +102,10 @@ struct Params {
   const int32_t* seg_start;
   const int32_t* seg_count;
   int E, K, N, R;
-  int mrows;    // outputs of a unit: 128 per tile, or 128 when gated
-  int up_row;   // weight row of a unit's second tile, relative to its first
+  int mrows;      // outputs of a unit
+  int rank_rows;  // of them in each CTA of a pair
+  int box_rows;   // weight rows of one load
+  int up_row;     // weight row of a unit's second load, relative to its first
   int wrows;
   int mtiles, splits, words, sbs;
   void* out;
@@ -168,10 +174,14 @@ __device__ __forceinline__ Unit decode_unit(const Params& p, const int* chunk_st
 
 // The i-th unit of this CTA: from the list in shared memory (decoded once, by
 // all threads at a time), past its end on the spot.
-template <int BN>
+template <int BN, int CG>
 __device__ __forceinline__ Unit unit_at(const Params& p, const int* chunk_start, const int4* list,
                                         uint32_t i) {
-  if (i >= kUnitList) return decode_unit<BN>(p, chunk_start, blockIdx.x + i * gridDim.x);
+  if (i >= kUnitList) {
+    Unit w = decode_unit<BN>(p, chunk_start, blockIdx.x / CG + i * (gridDim.x / CG));
+    if (CG == 2) w.m += (int)cluster_rank() * p.rank_rows;
+    return w;
+  }
   const int4 v = list[i];
   Unit w;
   w.e = v.x & 0xffff;
@@ -183,12 +193,12 @@ __device__ __forceinline__ Unit unit_at(const Params& p, const int* chunk_start,
   return w;
 }
 
+template <int CG>
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, Ctl* ctl,
                                              unsigned* status) {
-  if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = mq::global_timer_ns();
   for (uint32_t n = 1;; ++n) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (CG == 2 ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
     if ((n & 63u) == 0) {
       if (ctl->abort_flag) return false;
       if (mq::global_timer_ns() - t0 > kWaitNs) {
@@ -206,13 +216,39 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// CG = 2: the arrivals may come from the other CTA of the pair.
+template <int CG = 1>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Ctl* ctl,
                                           unsigned* status) {
-  bool ok = mbar_try_wait(bar, parity);
+  bool ok = CG == 2 ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
   if (__all_sync(0xffffffffu, ok)) return true;
-  ok = ok || wait_bounded(bar, parity, ctl, status);
+  ok = ok || wait_bounded<CG>(bar, parity, ctl, status);
   return __all_sync(0xffffffffu, ok);
 }
+
+// Arrives on the barrier of the CTA that issues the MMAs.
+template <int CG>
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  if (CG == 2) mbar_arrive_cluster(map_rank(bar, 0));
+  else mbar_arrive(bar);
+}
+
+// Signals the MMAs issued so far: on both CTAs of a pair.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (CG == 2) mma_commit_pair(bar);
+  else mma_commit(bar);
+}
+
+// Columns of the instruction for a chunk of n rows: n in steps of 16 for each
+// CTA (32 for a pair), at most the tile's.
+template <int CG>
+__device__ __forceinline__ int columns(int n, int bn) {
+  return min(bn, (n + 16 * CG - 1) & -(16 * CG));
+}
+// Rows of the boxes that load a partly filled chunk.
+template <int CG>
+constexpr int kPartRows = CG == 2 ? 16 : 32;
 
 // After an abort: lets what is in flight land; bounded, ignores the flag.
 __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
@@ -253,17 +289,23 @@ __device__ __forceinline__ void epilogue_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
 }
 
+// Joins the gate warp and the up warp of one pair of lane quarters.
+__device__ __forceinline__ void swap_barrier(int pair) {
+  asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
+}
+
 __device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float v) {
   if (dtype == MQ_DTYPE_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
   else if (dtype == MQ_DTYPE_F16) static_cast<__half*>(out)[i] = __float2half_rn(v);
   else static_cast<float*>(out)[i] = v;
 }
 
-template <int BITS, int BN, int EPI>
+template <int BITS, int BN, int EPI, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
-            const __grid_constant__ CUtensorMap map_a32, const Params p) {
-  using C = Cfg<BITS, BN>;
+            const __grid_constant__ CUtensorMap map_part, const Params p) {
+  using C = Cfg<BITS, BN, CG>;
+  constexpr int kTiles = C::kTiles;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* stages = smem;
@@ -271,34 +313,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   Ctl* ctl = reinterpret_cast<Ctl*>(sf + (size_t)kSfRing * C::kSfSlotBytes);
   int4* list = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(ctl) + 1024);
   int4* dest_table = list + kUnitList;  // [2][BN]
-  int* chunk_start = reinterpret_cast<int*>(dest_table + 2 * BN);
+  float* swap = reinterpret_cast<float*>(dest_table + 2 * BN);  // [2][kEpiWarps][8][32]
+  int* chunk_start = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(swap) + C::kSwapBytes);
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;  // 0 issues the pair's MMAs
+  const uint32_t worker = blockIdx.x / CG, workers = gridDim.x / CG;
 
   if (tid == 0) {
     tma_prefetch_desc(&map_w);
     tma_prefetch_desc(&map_a);
-    tma_prefetch_desc(&map_a32);
+    tma_prefetch_desc(&map_part);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], kTiles);
     }
     for (int i = 0; i < kSfRing; ++i) {
-      mbar_init(&ctl->sf_full[i], 1);
+      mbar_init(&ctl->sf_full[i], CG);
       mbar_init(&ctl->sf_empty[i], kTiles);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->acc_full[i], kTiles);
-      mbar_init(&ctl->acc_empty[i], kEpiWarps);
+      mbar_init(&ctl->acc_empty[i], CG * kEpiWarps);
     }
     mbar_init(&ctl->drain, kTiles);
     ctl->abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&ctl->tmem, 512);
-    tmem_relinquish();
+    if (CG == 2) {
+      tmem_alloc_pair(&ctl->tmem, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&ctl->tmem, 512);
+      tmem_relinquish();
+    }
   }
   mq::pdl_wait();
   mq::pdl_trigger();
@@ -329,13 +379,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const uint32_t total = (uint32_t)chunk_start[p.E] * p.mtiles * p.splits;
-  const uint32_t units = blockIdx.x < total ? (total - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+  const uint32_t units = worker < total ? (total - worker + workers - 1) / workers : 0;
   if (tid < kUnitList && tid < units) {
-    const Unit w = decode_unit<BN>(p, chunk_start, blockIdx.x + tid * gridDim.x);
-    list[tid] = make_int4(w.e | (w.single ? 1 << 16 : 0) | w.split << 17, w.row0, w.n, w.m);
+    const Unit w = decode_unit<BN>(p, chunk_start, worker + tid * workers);
+    list[tid] = make_int4(w.e | (w.single ? 1 << 16 : 0) | w.split << 17, w.row0, w.n,
+                          w.m + (int)rank * p.rank_rows);
   }
   tc_fence_before();
-  __syncthreads();
+  if (CG == 2) cluster_sync();  // (the barriers are set up in both)
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
 
@@ -346,10 +398,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     bool ok = true;
     for (uint32_t u = 0; u < units && ok; ++u) {
-      const Unit w = unit_at<BN>(p, chunk_start, list, u);
+      const Unit w = unit_at<BN, CG>(p, chunk_start, list, u);
       const int sb0 = (int)((int64_t)p.sbs * w.split / p.splits);
       const int sb1 = (int)((int64_t)p.sbs * (w.split + 1) / p.splits);
-      const int rows = min(BN, (w.n + 31) & ~31);  // a partly filled chunk: boxes of 32 rows
+      // a partly filled chunk: as many boxes of kPartRows rows as its columns
+      // (CG = 2: each CTA brings its half of them)
+      const int n_cols = columns<CG>(w.n, BN);
+      const int rows = n_cols == BN ? C::kBRows : (n_cols / CG + kPartRows<CG> - 1) / kPartRows<CG> * kPartRows<CG>;
+      const int row0 = w.row0 + (int)rank * (n_cols / CG);
       const int st0 = sb0 * C::kPerSb;
       const int st1 = min(sb1 * C::kPerSb, (p.words + C::kWords - 1) / C::kWords);
       for (int s = st0; s < st1; ++s, ++it) {
@@ -359,31 +415,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         uint8_t* dst = stages + (size_t)slot * C::kStageBytes;
+        uint8_t* dst_a = dst + kTiles * kABytes;
         if (el) {
-          mbar_arrive_expect_tx(&ctl->full[slot], C::kTxWeights + rows * 128);
-#pragma unroll
-          for (int a = 0; a < kTiles; ++a) {
-            const int row = w.m + a * p.up_row;
-            if (w.single)
-              tma_load_3d_hint(dst + a * kABytes, &map_w, &ctl->full[slot], s * 128, row, w.e, pol_once);
-            else
-              tma_load_3d(dst + a * kABytes, &map_w, &ctl->full[slot], s * 128, row, w.e);
-          }
-          if (rows == BN) {
-            tma_load_2d(dst + kTiles * kABytes, &map_a, &ctl->full[slot], s * 128, w.row0);
+          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[slot], CG * (C::kTxWeights + rows * 128));
+          if constexpr (CG == 2) {
+            const uint32_t bar = map_rank(&ctl->full[slot], 0);
+            tma_load_3d_pair(dst, &map_w, bar, s * 128, w.m, w.e);
+            if (EPI == MX_EPI_GATED)  // 64 gate rows and their 64 up rows
+              tma_load_3d_pair(dst + kABytes / 2, &map_w, bar, s * 128, w.m + p.up_row, w.e);
+            if (n_cols == BN) {
+              tma_load_2d_pair(dst_a, &map_a, bar, s * 128, row0);
+            } else {
+              for (int r = 0; r < rows; r += kPartRows<CG>)
+                tma_load_2d_pair(dst_a + r * 128, &map_part, bar, s * 128, row0 + r);
+            }
           } else {
-            for (int r = 0; r < rows; r += 32)
-              tma_load_2d(dst + kTiles * kABytes + r * 128, &map_a32, &ctl->full[slot], s * 128,
-                          w.row0 + r);
+#pragma unroll
+            for (int a = 0; a < kTiles; ++a) {
+              const int row = w.m + a * p.up_row;
+              if (w.single)
+                tma_load_3d_hint(dst + a * kABytes, &map_w, &ctl->full[slot], s * 128, row, w.e, pol_once);
+              else
+                tma_load_3d(dst + a * kABytes, &map_w, &ctl->full[slot], s * 128, row, w.e);
+            }
+            if (n_cols == BN) {
+              tma_load_2d(dst_a, &map_a, &ctl->full[slot], s * 128, row0);
+            } else {
+              for (int r = 0; r < rows; r += kPartRows<CG>)
+                tma_load_2d(dst_a + r * 128, &map_part, &ctl->full[slot], s * 128, row0 + r);
+            }
           }
         }
       }
     }
-    if (ctl->abort_flag) {  // loads in flight land before the CTA goes
+    if (ctl->abort_flag && rank == 0) {  // loads in flight land before the CTA goes
       for (uint32_t j = it < (uint32_t)C::kStages ? 0 : it - C::kStages; j < it; ++j)
         wait_drain(&ctl->full[j % C::kStages], (j / C::kStages) & 1);
     }
-  } else if (warp <= kTiles) {
+  } else if (warp <= kTiles && rank == 0) {
     // ----------------------------------------------------------- MMAs --
     // One warp per weight tile: an instruction takes about 90 cycles to issue
     // whatever its width, two warps issue at once.  The warp walks the loop
@@ -396,19 +465,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, sb_it = 0;
     bool ok = true;
     for (uint32_t t = 0; t < units && ok; ++t) {
-      const Unit w = unit_at<BN>(p, chunk_start, list, t);
+      const Unit w = unit_at<BN, CG>(p, chunk_start, list, t);
       const int sb0 = (int)((int64_t)p.sbs * w.split / p.splits);
       const int sb1 = (int)((int64_t)p.sbs * (w.split + 1) / p.splits);
       const uint32_t buf = t % C::kBufs;
-      ok = warp_wait(&ctl->acc_empty[buf], ((t / C::kBufs) & 1) ^ 1, ctl, p.status);
+      ok = warp_wait<CG>(&ctl->acc_empty[buf], ((t / C::kBufs) & 1) ^ 1, ctl, p.status);
       tc_fence_after();
       const uint32_t acc = tmem + buf * C::kAccCols + tile * BN;
-      // as many columns as the chunk has rows, in steps of 16
-      const uint32_t idesc = idesc_mx<BITS>(kTileM, (w.n + 15) & ~15, 0);
+      const uint32_t idesc = idesc_mx<BITS>(CG * kTileM, columns<CG>(w.n, BN), 0);
       uint32_t accumulate = 0;
       for (int sb = sb0; sb < sb1 && ok; ++sb, ++sb_it) {
         const uint32_t ss = sb_it % kSfRing;
-        ok = warp_wait(&ctl->sf_full[ss], (sb_it / kSfRing) & 1, ctl, p.status);
+        ok = warp_wait<CG>(&ctl->sf_full[ss], (sb_it / kSfRing) & 1, ctl, p.status);
         if (!ok) break;
         if (el) {
           const uint32_t slot = smem_addr(sf + (size_t)ss * C::kSfSlotBytes);
@@ -416,10 +484,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int wd = 0; wd < 4; ++wd) {
             const uint32_t blk = slot + wd * C::kSfWordBytes;
             const uint32_t col = sfc + wd * (1 + C::kBBlocks) * 4;
-            tmem_cp_scales(col, smem_desc_scales(blk + tile * 512));
+            tmem_cp_scales<CG>(col, smem_desc_scales(blk + tile * 512));
 #pragma unroll
             for (int b = 0; b < C::kBBlocks; ++b)
-              tmem_cp_scales(col + 4 + b * 4, smem_desc_scales(blk + (kTiles + b) * 512));
+              tmem_cp_scales<CG>(col + 4 + b * 4, smem_desc_scales(blk + (kTiles + b) * 512));
           }
         }
         const int last = min((sb + 1) * C::kPerSb, nst);
@@ -437,37 +505,41 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int word = word0 + (BITS == 8 ? 0 : j / 2);
               const uint32_t id = BITS == 8 ? j : (j & 1) * 2;
               const uint32_t sfw = sfc + word * (1 + C::kBBlocks) * 4;
-              mma_mx<BITS>(acc, ad + j * 2, bd + j * 2, idesc | id << 4 | id << 29, sfw, sfw + 4,
+              mma_mx<BITS, CG>(acc, ad + j * 2, bd + j * 2, idesc | id << 4 | id << 29, sfw, sfw + 4,
                            accumulate | j);
             }
-            mma_commit(&ctl->empty[slot]);
+            commit<CG>(&ctl->empty[slot]);
           }
           accumulate = 1;
         }
-        if (ok && el) mma_commit(&ctl->sf_empty[ss]);
+        if (ok && el) commit<CG>(&ctl->sf_empty[ss]);
       }
-      if (ok && el) mma_commit(&ctl->acc_full[buf]);
+      if (ok && el) commit<CG>(&ctl->acc_full[buf]);
     }
     // nothing these warps issued may be in flight when the memory goes
-    if (el) mma_commit(&ctl->drain);
+    if (el) {
+      if (CG == 2) mma_commit_pair_here(&ctl->drain);
+      else mma_commit(&ctl->drain);
+    }
     wait_drain(&ctl->drain, 0);
-  } else if (warp == 3 || warp == 12) {
+  } else if (warp == 3 || warp >= 12) {
     // ------------------------------------------------------------ scales --
-    const int lw = warp == 12;
+    const int lw = warp == 3 ? 0 : warp - 11;  // the slot of the ring it fills
     constexpr int kGroupsA = kTiles * 4, kGroupsB = (BN + 31) / 32;
     uint32_t sb_it = 0;
     bool ok = true;
     const int64_t row_bytes = (int64_t)p.words * 4;
     for (uint32_t u = 0; u < units && ok; ++u) {
-      const Unit w = unit_at<BN>(p, chunk_start, list, u);
+      const Unit w = unit_at<BN, CG>(p, chunk_start, list, u);
       const int sb0 = (int)((int64_t)p.sbs * w.split / p.splits);
       const int sb1 = (int)((int64_t)p.sbs * (w.split + 1) / p.splits);
       for (int sb = sb0; sb < sb1; ++sb, ++sb_it) {
-        if ((int)(sb_it & 1) != lw) continue;
+        if ((int)(sb_it % kSfWarps) != lw) continue;
         uint4 va[kGroupsA], vb[kGroupsB];
 #pragma unroll
         for (int g = 0; g < kGroupsA; ++g) {
-          const int wr = w.m + (g >> 2) * p.up_row + (g & 3) * 32 + lane;
+          const int r = g * 32 + lane, second = r >= p.box_rows;
+          const int wr = w.m + (second ? p.up_row - p.box_rows : 0) + r;
           va[g] = make_uint4(0, 0, 0, 0);
           if (wr < p.wrows)
             va[g] = load_words(p.w_scale + ((int64_t)w.e * p.wrows + wr) * row_bytes, sb * 4, p.words);
@@ -498,10 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->sf_full[ss]);
+        if (lane == 0) arrive<CG>(&ctl->sf_full[ss]);
       }
     }
-  } else {
+  } else if (warp >= 4 && warp < 12) {
     // ---------------------------------------------------------- epilogue --
     const int quad = warp & 3;       // the tensor-memory lanes this warp may read
     const int half = (warp - 4) >> 2;  // which 16-column steps it takes
@@ -509,18 +581,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // goes, one unit ahead, and passes it on through shared memory.
     const int col = tid - 128;
     int dest = 0;
+    uint32_t swaps = 0;
     float factor = 1.0f;
     auto look_up = [&](uint32_t t) {
       if (t >= units || col >= BN) return;
-      const Unit w = unit_at<BN>(p, chunk_start, list, t);
+      const Unit w = unit_at<BN, CG>(p, chunk_start, list, t);
       if (col >= w.n) return;
       dest = p.dest ? p.dest[w.row0 + col] : w.row0 + col;
       factor = p.dest_w ? p.dest_w[dest] : 1.0f;
     };
     if constexpr (EPI == MX_EPI_PART) look_up(0);
-    bool ok = true;  // (a warp that gave up still meets the others at the barrier)
+    bool ok = true;  // (a warp that gave up still meets the others at their barriers)
     for (uint32_t t = 0; t < units; ++t) {
-      const Unit w = unit_at<BN>(p, chunk_start, list, t);
+      const Unit w = unit_at<BN, CG>(p, chunk_start, list, t);
       const uint32_t buf = t % C::kBufs;
       const int4* table = dest_table + (t & 1) * BN;
       if constexpr (EPI == MX_EPI_PART) {
@@ -533,27 +606,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         look_up(t + 1);
       }
       ok = ok && warp_wait(&ctl->acc_full[buf], (t / C::kBufs) & 1, ctl, p.status);
-      if (!ok) continue;
+      if (!ok) {
+        if constexpr (CG == 2 && EPI == MX_EPI_GATED)
+          for (int c0 = half * 16; c0 < w.n; c0 += 32) swap_barrier(half * 2 + (quad & 1));
+        continue;
+      }
       tc_fence_after();
       const uint32_t acc = tmem + buf * C::kAccCols + ((uint32_t)(quad * 32) << 16);
       if constexpr (EPI == MX_EPI_GATED) {
-        const int n = w.m + quad * 32 + lane;  // this lane's output
-        const bool live = n < p.N;             // (uniform: N is a multiple of 32)
+        // A lane's output: its weight row's, or with a pair's 64 + 64 rows the
+        // gate row's (quarters 0-1 hold gate rows, 2-3 their up rows).
+        const int n = w.m + (CG == 2 ? quad & 1 : quad) * 32 + lane;
+        const bool live = n < p.N;  // (uniform: N is a multiple of 32)
+        constexpr int kStep = CG == 2 ? 8 : 16;  // columns this warp finishes of 16
+        const int mine0 = CG == 2 && quad >= 2 ? 8 : 0;
         for (int c0 = half * 16; c0 < w.n; c0 += 32) {
           uint32_t v0[16], v1[16];
           tmem_ld16_sync(acc + c0, v0);
-          tmem_ld16_sync(acc + BN + c0, v1);
+          if constexpr (CG == 1) {
+            tmem_ld16_sync(acc + BN + c0, v1);
+          } else {
+            // The gate warp finishes columns 0-7 of the step and the up warp
+            // 8-15: each passes the other half on.
+            float* out = swap + ((swaps & 1) * kEpiWarps + (warp - 4)) * 256 + lane;
+            const float* in = swap + ((swaps & 1) * kEpiWarps + ((warp - 4) ^ 2)) * 256 + lane;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              out[j * 32] = __uint_as_float(quad < 2 ? v0[8 + j] : v0[j]);
+            swap_barrier(half * 2 + (quad & 1));
+            ++swaps;  // (the buffer is written again only after the next barrier)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t got = __float_as_uint(in[j * 32]);
+              v1[j] = quad < 2 ? got : v0[8 + j];  // up
+              v0[j] = quad < 2 ? v0[j] : got;      // gate
+            }
+          }
           uint32_t codes = 0;  // lane j keeps column j's scale code
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
+          for (int j = 0; j < kStep; ++j) {
             const float g = __uint_as_float(v0[j]), up = __uint_as_float(v1[j]);
             const float a = __fdividef(g, 1.0f + __expf(-g)) * up;
             const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(a) & 0x7fffffffu);
             const uint32_t code = mq::mx_scale_code<BITS>(m);
             const float s = mq::mx_scaled(a, mq::mx_inv_scale(code));
             if (lane == j) codes = code;
-            const int64_t row = w.row0 + c0 + j;
-            const bool mine = live && c0 + j < w.n;
+            const int c = c0 + mine0 + j;
+            const int64_t row = w.row0 + c;
+            const bool mine = live && c < w.n;
             if (BITS == 8) {
               if (mine) p.act[row * p.N + n] = (uint8_t)mq::e4m3x2(s, 0.0f);
             } else {
@@ -562,14 +662,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p.act[(row * p.N + n) >> 1] = (uint8_t)mq::e2m1x2(s, hi);
             }
           }
-          if (live && lane < 16 && c0 + lane < w.n)
-            p.act_scale[(int64_t)(w.row0 + c0 + lane) * (p.N >> 5) + ((n - lane) >> 5)] =
-                (uint8_t)codes;
+          const int c = c0 + mine0 + lane;
+          if (live && lane < kStep && c < w.n)
+            p.act_scale[(int64_t)(w.row0 + c) * (p.N >> 5) + ((n - lane) >> 5)] = (uint8_t)codes;
         }
       } else {
 #pragma unroll
         for (int tile = 0; tile < kTiles; ++tile) {
-          const int n = w.m + tile * kTileM + quad * 32 + lane;  // this lane's output
+          const int n = w.m + tile * p.up_row + quad * 32 + lane;  // this lane's output
           if (n - lane >= p.N) break;
           const bool live = n < p.N;
           for (int c0 = half * 16; c0 < w.n; c0 += 32) {
@@ -596,13 +696,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->acc_empty[buf]);
+      if (lane == 0) arrive<CG>(&ctl->acc_empty[buf]);
     }
   }
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  if (CG == 2) cluster_sync();  // (the other CTA's shared memory is in use until here)
+  else __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) {
+    if (CG == 2) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
+  }
 }
 
 template <typename T>
@@ -708,12 +813,12 @@ cudaError_t make_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, const v
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int BITS, int BN, int EPI>
+template <int BITS, int BN, int EPI, int CG>
 cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const CUtensorMap& mr, const Params& p,
                        int64_t units, cudaStream_t st) {
-  constexpr size_t smem = Cfg<BITS, BN>::kSmem;
+  constexpr size_t smem = Cfg<BITS, BN, CG>::kSmem;
   static_assert(smem <= kSmemMax, "shared memory");
-  auto kern = mx_gemm<BITS, BN, EPI>;
+  auto kern = mx_gemm<BITS, BN, EPI, CG>;
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -725,19 +830,19 @@ cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const CUten
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   const int sms = tc_num_sms();
-  const int grid = units < sms ? (int)units : sms;
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mw, ma, mr, p);
+  const int workers = (int)std::min<int64_t>(units, sms / CG);
+  return launch_pdl_cluster(kern, dim3(workers * CG), dim3(kThreads), CG, smem, st, mw, ma, mr, p);
 }
 
 template <int BITS, int EPI>
-cudaError_t launch_bn(int bn, const CUtensorMap& mw, const CUtensorMap& ma, const CUtensorMap& mr, const Params& p,
-                      int64_t units, cudaStream_t st) {
-  switch (bn) {
-    case 16: return launch_one<BITS, 16, EPI>(mw, ma, mr, p, units, st);
-    case 32: return launch_one<BITS, 32, EPI>(mw, ma, mr, p, units, st);
-    case 64: return launch_one<BITS, 64, EPI>(mw, ma, mr, p, units, st);
-    case 96: return launch_one<BITS, 96, EPI>(mw, ma, mr, p, units, st);
-    default: return launch_one<BITS, 192, EPI>(mw, ma, mr, p, units, st);
+cudaError_t launch_bn(const MxPlan& pl, const CUtensorMap& mw, const CUtensorMap& ma,
+                      const CUtensorMap& mr, const Params& p, int64_t units, cudaStream_t st) {
+  if (pl.pair) return launch_one<BITS, kPairRows, EPI, 2>(mw, ma, mr, p, units, st);
+  switch (pl.bn) {
+    case 16: return launch_one<BITS, 16, EPI, 1>(mw, ma, mr, p, units, st);
+    case 32: return launch_one<BITS, 32, EPI, 1>(mw, ma, mr, p, units, st);
+    case 64: return launch_one<BITS, 64, EPI, 1>(mw, ma, mr, p, units, st);
+    default: return launch_one<BITS, 96, EPI, 1>(mw, ma, mr, p, units, st);
   }
 }
 
@@ -745,9 +850,9 @@ template <int BITS>
 cudaError_t launch_epi(const MxGemm& g, const MxPlan& pl, const CUtensorMap& mw,
                        const CUtensorMap& ma, const CUtensorMap& mr, const Params& p, int64_t units, cudaStream_t st) {
   switch (g.epi) {
-    case MX_EPI_OUT: return launch_bn<BITS, MX_EPI_OUT>(pl.bn, mw, ma, mr, p, units, st);
-    case MX_EPI_PART: return launch_bn<BITS, MX_EPI_PART>(pl.bn, mw, ma, mr, p, units, st);
-    default: return launch_bn<BITS, MX_EPI_GATED>(pl.bn, mw, ma, mr, p, units, st);
+    case MX_EPI_OUT: return launch_bn<BITS, MX_EPI_OUT>(pl, mw, ma, mr, p, units, st);
+    case MX_EPI_PART: return launch_bn<BITS, MX_EPI_PART>(pl, mw, ma, mr, p, units, st);
+    default: return launch_bn<BITS, MX_EPI_GATED>(pl, mw, ma, mr, p, units, st);
   }
 }
 
@@ -763,19 +868,21 @@ MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated, int a_bits) {
   MxPlan pl;
   const int64_t live = std::max<int64_t>(1, std::min<int64_t>(S, E));
   const int64_t avg = (S + live - 1) / live;
-  pl.bn = avg <= 8 ? 16 : avg <= 20 ? 32 : avg <= 40 ? 64 : (avg <= 128 || (gated && a_bits == 4)) ? 96 : 192;
+  pl.pair = avg > 64;
+  pl.bn = pl.pair ? kPairRows : avg <= 8 ? 16 : avg <= 20 ? 32 : avg <= 40 ? 64 : 96;
   pl.splits = 1;
   if (gated) return pl;
   const int sms = tc_num_sms();
   const int sbs = (K + 511) / 512;
   const int64_t chunks = std::max(live, (S + pl.bn - 1) / pl.bn);
-  const int64_t tiles = (N + kTiles * kTileM - 1) / (kTiles * kTileM);
+  constexpr int per = 2 * kTileM;  // outputs of a unit: two tiles of one CTA, or one of each of a pair
+  const int64_t tiles = (N + per - 1) / per;
   const double row = a_bits / 8.0 + 1.0 / 32, wrow = 0.5 + 1.0 / 32;
   double best = 0;
   for (int sp = 1; sp <= 16 && sp <= sbs; ++sp) {
     if (sp > 1 && S > 1024) break;  // partial sums would cost more than idle SMs
-    const double waves = std::ceil((double)(chunks * tiles * sp) / sms);
-    const double unit = 512.0 * std::ceil((double)sbs / sp) * (kTiles * kTileM * wrow + pl.bn * row);
+    const double waves = std::ceil((double)(chunks * tiles * sp) / (pl.pair ? sms / 2 : sms));
+    const double unit = 512.0 * std::ceil((double)sbs / sp) * (per * wrow + pl.bn * row) / (pl.pair ? 2 : 1);
     double cost = waves * (unit + 24e3);
     if (sp > 1) cost += 80e3 + 4.0 * sp * S * N / sms;
     if (best == 0 || cost < best) {
@@ -798,16 +905,16 @@ cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStream_t st) {
     const cuuint64_t kw = spread ? g.K : g.K / 2;
     const cuuint64_t dims[3] = {kw, (cuuint64_t)g.wrows, (cuuint64_t)g.E};
     const cuuint64_t strides[2] = {(cuuint64_t)g.K / 2, (cuuint64_t)g.K / 2 * g.wrows};
-    const cuuint32_t box[3] = {128, kTileM, 1};
+    const cuuint32_t box[3] = {128, (cuuint32_t)(gated && pl.pair ? kTileM / 2 : kTileM), 1};
     err = make_map(&mw, spread ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8,
                    3, g.w, dims, strides, box);
     if (err != cudaSuccess) return err;
     const cuuint64_t row = (cuuint64_t)g.K * g.a_bits / 8;
     const cuuint64_t adims[2] = {row, (cuuint64_t)g.R};
-    const cuuint32_t abox[2] = {128, (cuuint32_t)pl.bn};
+    const cuuint32_t abox[2] = {128, (cuuint32_t)(pl.bn / (pl.pair ? 2 : 1))};
     err = make_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, g.a, adims, &row, abox);
     if (err != cudaSuccess) return err;
-    const cuuint32_t rbox[2] = {128, 32};
+    const cuuint32_t rbox[2] = {128, pl.pair ? 16u : 32u};
     err = make_map(&mr, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, g.a, adims, &row, rbox);
     if (err != cudaSuccess) return err;
   }
@@ -820,7 +927,11 @@ cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStream_t st) {
   p.K = g.K;
   p.N = g.N;
   p.R = (int)g.R;
-  p.mrows = gated ? kTileM : kTiles * kTileM;
+  // A unit is two weight tiles: gate and up of 128 outputs, or 256 outputs.
+  // One CTA holds both; of a pair each CTA holds 128 rows of them.
+  p.mrows = gated ? kTileM : 2 * kTileM;
+  p.rank_rows = p.mrows / 2;
+  p.box_rows = pl.pair ? p.rank_rows : kTileM;
   p.up_row = gated ? g.N : kTileM;
   p.wrows = g.wrows;
   p.mtiles = (g.N + p.mrows - 1) / p.mrows;
