@@ -556,17 +556,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        // block [word][32 lanes][4 groups]: a lane's words of four row groups
+        // side by side, one 16-byte store each
         uint8_t* slot = sf + (size_t)ss * C::kSfSlotBytes + lane * 16;
 #pragma unroll
-        for (int g = 0; g < kGroupsA + kGroupsB; ++g) {
-          const uint4 v = g < kGroupsA ? va[g < kGroupsA ? g : 0] : vb[g < kGroupsA ? 0 : g - kGroupsA];
-          const int block = g < kGroupsA ? g >> 2 : kTiles + ((g - kGroupsA) >> 2);
-          const int col = g < kGroupsA ? g & 3 : (g - kGroupsA) & 3;
-          uint32_t* d = reinterpret_cast<uint32_t*>(slot + block * 512 + col * 4);
-          d[0 * (C::kSfWordBytes / 4)] = v.x;
-          d[1 * (C::kSfWordBytes / 4)] = v.y;
-          d[2 * (C::kSfWordBytes / 4)] = v.z;
-          d[3 * (C::kSfWordBytes / 4)] = v.w;
+        for (int b = 0; b < kTiles + C::kBBlocks; ++b) {
+          uint4 g[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (b < kTiles) g[c] = va[b < kTiles ? b * 4 + c : 0];
+            else if ((b - kTiles) * 4 + c < kGroupsB) g[c] = vb[b < kTiles ? 0 : (b - kTiles) * 4 + c];
+            else g[c] = make_uint4(0, 0, 0, 0);
+          }
+          uint4* d = reinterpret_cast<uint4*>(slot + b * 512);
+          d[0 * (C::kSfWordBytes / 16)] = make_uint4(g[0].x, g[1].x, g[2].x, g[3].x);
+          d[1 * (C::kSfWordBytes / 16)] = make_uint4(g[0].y, g[1].y, g[2].y, g[3].y);
+          d[2 * (C::kSfWordBytes / 16)] = make_uint4(g[0].z, g[1].z, g[2].z, g[3].z);
+          d[3 * (C::kSfWordBytes / 16)] = make_uint4(g[0].w, g[1].w, g[2].w, g[3].w);
         }
         fence_proxy_async_smem();
         __syncwarp();
