@@ -648,24 +648,37 @@ __global__ void __launch_bounds__(kThreads, 1)
               v0[j] = quad < 2 ? v0[j] : got;      // gate
             }
           }
+          // One stage at a time over all columns, so that their latencies
+          // overlap.
+          float act[kStep];
+          uint32_t code[kStep];
+#pragma unroll
+          for (int j = 0; j < kStep; ++j) {
+            const float g = __uint_as_float(v0[j]);
+            act[j] = __fdividef(g, 1.0f + __expf(-g)) * __uint_as_float(v1[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < kStep; ++j)
+            code[j] = __reduce_max_sync(0xffffffffu, __float_as_uint(act[j]) & 0x7fffffffu);
           uint32_t codes = 0;  // lane j keeps column j's scale code
 #pragma unroll
           for (int j = 0; j < kStep; ++j) {
-            const float g = __uint_as_float(v0[j]), up = __uint_as_float(v1[j]);
-            const float a = __fdividef(g, 1.0f + __expf(-g)) * up;
-            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(a) & 0x7fffffffu);
-            const uint32_t code = mq::mx_scale_code<BITS>(m);
-            const float s = mq::mx_scaled(a, mq::mx_inv_scale(code));
-            if (lane == j) codes = code;
-            const int c = c0 + mine0 + j;
-            const int64_t row = w.row0 + c;
-            const bool mine = live && c < w.n;
-            if (BITS == 8) {
-              if (mine) p.act[row * p.N + n] = (uint8_t)mq::e4m3x2(s, 0.0f);
-            } else {
-              const float hi = __shfl_down_sync(0xffffffffu, s, 1);
-              if (mine && (lane & 1) == 0)
-                p.act[(row * p.N + n) >> 1] = (uint8_t)mq::e2m1x2(s, hi);
+            code[j] = mq::mx_scale_code<BITS>(code[j]);
+            act[j] = mq::mx_scaled(act[j], mq::mx_inv_scale(code[j]));
+            if (lane == j) codes = code[j];
+          }
+          // Two outputs of one column per lane: even lanes take the even
+          // columns of their pair of outputs, odd lanes the odd ones.
+          const int odd = lane & 1;
+          uint8_t* dst = p.act + (((int64_t)(w.row0 + c0 + mine0 + odd) * p.N + (n & ~1)) * BITS >> 3);
+          const int64_t two_rows = (int64_t)p.N * BITS >> 2;
+#pragma unroll
+          for (int j = 0; j < kStep; j += 2, dst += two_rows) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? act[j] : act[j + 1], 1);
+            const float lo = odd ? got : act[j], hi = odd ? act[j + 1] : got;
+            if (live && c0 + mine0 + j + odd < w.n) {
+              if (BITS == 8) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)mq::e4m3x2(lo, hi);
+              else *dst = (uint8_t)mq::e2m1x2(lo, hi);
             }
           }
           const int c = c0 + mine0 + lane;
