@@ -10,6 +10,7 @@ the library is missing, every call raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -465,7 +466,8 @@ def moe_quant_forward_noalloc(x, w13, w2, s13, s2, topk_w, topk_ids, bits=8, gro
 # each attribute once and pass plain integers to ctypes.
 _MX_BLOCK = 32
 _HALVES = (torch.bfloat16, torch.float16)
-_U8 = torch.uint8
+_U8, _E4M3, _I32, _F32 = torch.uint8, torch.float8_e4m3fn, torch.int32, torch.float32
+_Tensor, _empty = torch.Tensor, torch.empty
 
 
 def _mx_stream(stream, t):
@@ -482,13 +484,14 @@ def _mx_bits(bits):
 
 def _mx_plain(t, name, dtypes):
     """Checks a tensor on the plain side; returns its MQ_DTYPE_*."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    dt = t.dtype
+    if dt not in dtypes:
+        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {dt}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    return _DTYPES[t.dtype]
+    return _DTYPES[dt]
 
 
 def _mx_stride(t, name):
@@ -510,33 +513,36 @@ def _mx_stride(t, name):
 def _mx_codes(q, scale, bits, name, dim=None):
     """Checks MX codes and scales; returns (shape of the codes, elements in a
     row)."""
-    _mx_bits(bits)
-    for t, n in ((q, name), (scale, name + "_scale")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{n} must be a torch.Tensor")
-        if t.dtype != _U8 and not (t is q and bits == 8 and t.dtype == torch.float8_e4m3fn):
-            raise TypeError(f"{n} must be torch.uint8, got {t.dtype}")
-        if not t.is_cuda:
-            raise ValueError(f"{n} must be on a CUDA device")
-        if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
-    shape = q.shape
-    if len(shape) != dim if dim else len(shape) < 1:
+    if bits != 4 and bits != 8:
+        raise ValueError(f"bits must be 4 or 8, got {bits}")
+    if not isinstance(q, _Tensor) or not isinstance(scale, _Tensor):
+        raise TypeError(f"{name} and {name}_scale must be torch.Tensors")
+    if q.dtype is not _U8 and not (bits == 8 and q.dtype is _E4M3):
+        raise TypeError(f"{name} must be torch.uint8, got {q.dtype}")
+    if scale.dtype is not _U8:
+        raise TypeError(f"{name}_scale must be torch.uint8, got {scale.dtype}")
+    dev = q.get_device()
+    if dev < 0 or scale.get_device() != dev:
+        raise ValueError(f"{name} and {name}_scale must be on one CUDA device")
+    if not q.is_contiguous() or not scale.is_contiguous():
+        raise ValueError(f"{name} and {name}_scale must be contiguous")
+    shape, ss = q.shape, scale.shape
+    n = len(shape)
+    if n != dim if dim else n < 1:
         raise ValueError(f"{name} must have {dim or 'at least one'} dims")
     cols = shape[-1] * 2 if bits == 4 else shape[-1]
     if cols == 0 or cols % _MX_BLOCK:
         raise ValueError(f"{name} must have rows of a positive multiple of {_MX_BLOCK} elements")
-    if scale.shape[-1] * _MX_BLOCK != cols or scale.shape[:-1] != shape[:-1]:
+    if len(ss) != n or ss[-1] * _MX_BLOCK != cols or (
+            ss[:-1] != shape[:-1] if n > 2 else n == 2 and ss[0] != shape[0]):
         raise ValueError(f"{name}_scale must be {[*shape[:-1], cols // _MX_BLOCK]}")
-    if scale.device != q.device:
-        raise ValueError(f"{name}_scale must be on {name}'s device")
     return shape, cols
 
 
 def _mx_out(t, shape, dtype, device, name):
     """The caller's output, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype=dtype, device=device)
     _need(t, dtype, name)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}")
@@ -622,6 +628,10 @@ def moe_mx_product_workspace(R, K, N, E=1) -> int:
     return lib().moe_mx_product_workspace(R, K, N, E)
 
 
+# (the queries' answers depend on their arguments alone)
+_mx_product_bytes = functools.lru_cache(maxsize=1024)(moe_mx_product_workspace)
+
+
 def moe_mx_product(a, a_scale, w, w_scale, expert_offsets=None, a_bits=8, out=None,
                    out_dtype=torch.bfloat16, workspace=None, stream=None):
     """MX rows [R, K] grouped by expert (expert_offsets int32 [E + 1]) times
@@ -648,9 +658,9 @@ def moe_mx_product(a, a_scale, w, w_scale, expert_offsets=None, a_bits=8, out=No
     L = lib()
     wp, nbytes = None, 0
     if workspace is None:
-        nbytes = L.moe_mx_product_workspace(R, K, N, E)
+        nbytes = _mx_product_bytes(R, K, N, E)
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=_U8, device=dev)
+            workspace = _empty(nbytes, dtype=_U8, device=dev)
             wp = workspace.data_ptr()
     else:
         _need(workspace, _U8, "workspace")
@@ -665,6 +675,9 @@ def moe_mx_forward_workspace(T, H, I, E, k, a_bits=8) -> int:
     return lib().moe_mx_forward_workspace(T, H, I, E, k, a_bits)
 
 
+_mx_forward_bytes = functools.lru_cache(maxsize=1024)(moe_mx_forward_workspace)
+
+
 def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out=None,
                    out_dtype=torch.bfloat16, workspace=None, stream=None):
     """The fused expert MLP with 4-bit MX experts on MX activations
@@ -675,10 +688,10 @@ def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out
     (e2, n2, _), I = _mx_codes(w2, s2, 4, "w2", 3)
     if k13 != H or n2 != H or n13 != 2 * I or e2 != E:
         raise ValueError("w13 must be [E, 2I, H] and w2 [E, H, I]")
-    _need(topk_w, torch.float32, "topk_w", 2)
-    _need(topk_ids, torch.int32, "topk_ids", 2)
-    k = topk_ids.shape[1]
-    if topk_ids.shape[0] != T or topk_w.shape != topk_ids.shape:
+    _need(topk_w, _F32, "topk_w", 2)
+    _need(topk_ids, _I32, "topk_ids", 2)
+    t2, k = topk_ids.shape
+    if t2 != T or topk_w.shape != topk_ids.shape:
         raise ValueError(f"topk_w and topk_ids must be [{T}, k]")
     dev = a.device
     if out is not None:
@@ -688,12 +701,13 @@ def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out
     out = _mx_out(out, (T, H), out_dtype, dev, "out")
     L = lib()
     if workspace is None:
-        nbytes = L.moe_mx_forward_workspace(T, H, I, E, k, a_bits)
-        workspace = torch.empty(max(nbytes, 16), dtype=_U8, device=dev)
+        nbytes = max(_mx_forward_bytes(T, H, I, E, k, a_bits), 16)
+        workspace = _empty(nbytes, dtype=_U8, device=dev)
     else:
         _need(workspace, _U8, "workspace")
+        nbytes = workspace.numel()
     _check(L.moe_mx_forward(
         a.data_ptr(), a_scale.data_ptr(), a_bits, T, H, I, E, k, w13.data_ptr(), s13.data_ptr(),
         w2.data_ptr(), s2.data_ptr(), topk_w.data_ptr(), topk_ids.data_ptr(), out.data_ptr(),
-        _DTYPES[out_dtype], workspace.data_ptr(), workspace.numel(), _mx_stream(stream, a)))
+        _DTYPES[out_dtype], workspace.data_ptr(), nbytes, _mx_stream(stream, a)))
     return out

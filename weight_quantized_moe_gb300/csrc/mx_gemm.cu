@@ -35,6 +35,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 namespace {
@@ -879,33 +880,40 @@ cudaError_t launch_epi(const MxGemm& g, const MxPlan& pl, const CUtensorMap& mw,
 
 // Rows per tile: above the average load of a live expert by half, so that
 // most experts are one chunk (their weights are then read once) without many
-// columns to spare.  K splits: the count with the least estimated time, in
-// bytes that one SM brings in (a wave of units brings in its weights and rows,
-// and 24 KB more for a unit's start and end; partial sums are written and read
-// again, and cost a launch).
+// columns to spare; CTA pairs from 65 rows on.
+//
+// K splits: the count with the least estimated time, in us.  The weights come
+// in at the HBM's rate or, with few units, at what their SMs can take (70 GB/s
+// each measured, or the instructions' time: 64 cycles and half a cycle per
+// column); a unit costs 0.7 us more, partial sums their traffic and a launch.
+// Measured against every count from 1 to 16: 128 rows, E=8, K=14336, N=4096
+// 46.5 us unsplit, 50.9 with 7; 8 rows 35.3 and 32.8; one row, E=1, K=14336
+// 32.4 and 12.7.
 MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated, int a_bits) {
   MxPlan pl;
-  const int64_t live = std::max<int64_t>(1, std::min<int64_t>(S, E));
-  const int64_t avg = (S + live - 1) / live;
+  // experts with a row, if rows fall on experts at random
+  const double live = std::max(1.0, E * (1.0 - std::pow(1.0 - 1.0 / E, (double)S)));
+  const double avg = S / live;
   pl.pair = avg > 64;
   pl.bn = pl.pair ? kPairRows : avg <= 8 ? 16 : avg <= 20 ? 32 : avg <= 40 ? 64 : 96;
   pl.splits = 1;
-  if (gated) return pl;
-  const int sms = tc_num_sms();
+  if (gated || S > 1024) return pl;  // (more rows: partial sums would cost more than idle SMs)
+  const int sms = pl.pair ? tc_num_sms() / 2 : tc_num_sms();
   const int sbs = (K + 511) / 512;
-  const int64_t chunks = std::max(live, (S + pl.bn - 1) / pl.bn);
-  constexpr int per = 2 * kTileM;  // outputs of a unit: two tiles of one CTA, or one of each of a pair
-  const int64_t tiles = (N + per - 1) / per;
+  const double chunks = std::max(live, std::ceil((double)S / pl.bn));
+  const double tiles = (N + 2 * kTileM - 1) / (2 * kTileM);
   const double row = a_bits / 8.0 + 1.0 / 32, wrow = 0.5 + 1.0 / 32;
+  const double hbm = live * N * K * wrow / 6.6e6;
   double best = 0;
   for (int sp = 1; sp <= 16 && sp <= sbs; ++sp) {
-    if (sp > 1 && S > 1024) break;  // partial sums would cost more than idle SMs
-    const double waves = std::ceil((double)(chunks * tiles * sp) / (pl.pair ? sms / 2 : sms));
-    const double unit = 512.0 * std::ceil((double)sbs / sp) * (per * wrow + pl.bn * row) / (pl.pair ? 2 : 1);
-    double cost = waves * (unit + 24e3);
-    if (sp > 1) cost += 80e3 + 4.0 * sp * S * N / sms;
-    if (best == 0 || cost < best) {
-      best = cost;
+    const double sb = std::ceil((double)sbs / sp);
+    const double bytes = 512.0 * sb * (2 * kTileM * wrow + pl.bn * row) / (pl.pair ? 2 : 1);
+    const double cycles = sb * (a_bits == 8 ? 32 : 16) * (64 + pl.bn / 2) / (pl.pair ? 2 : 1);
+    const double waves = std::ceil(chunks * tiles * sp / sms);
+    double us = std::max(hbm, waves * (std::max(bytes / 70e3, cycles / 2000) + 0.7));
+    if (sp > 1) us += 3.0 + sp * (double)S * N * 8 / 5e6;
+    if (best == 0 || us < best) {
+      best = us;
       pl.splits = sp;
     }
   }
