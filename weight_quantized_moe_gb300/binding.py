@@ -566,12 +566,18 @@ def moe_quantize_mx(x, bits=4, q=None, scale=None, stream=None):
     bits: E4M3 bytes; 4 bits: two E2M1 codes per byte, even element low) and
     E8M0 scale codes uint8 [..., K / 32].  Rows may be strided."""
     dt = _mx_plain(x, "x", _DTYPES)
-    qs, ss = _mx_code_shape(x.shape, bits)
-    dev, cols = x.device, x.shape[-1]
-    q = _mx_out(q, qs, _U8, dev, "q")
-    scale = _mx_out(scale, ss, _U8, dev, "scale")
-    _check(lib().moe_quantize_mx(x.data_ptr(), dt, x.numel() // cols, cols, _mx_stride(x, "x"),
-                                 bits, q.data_ptr(), scale.data_ptr(), _mx_stream(stream, x)))
+    shape, dev = x.shape, x.device
+    qs, ss = _mx_code_shape(shape, bits)
+    cols = shape[-1]
+    q = _empty(qs, dtype=_U8, device=dev) if q is None else _mx_out(q, qs, _U8, dev, "q")
+    scale = (_empty(ss, dtype=_U8, device=dev) if scale is None
+             else _mx_out(scale, ss, _U8, dev, "scale"))
+    rc = (_lib or lib()).moe_quantize_mx(
+        x.data_ptr(), dt, x.numel() // cols, cols,
+        cols if x.is_contiguous() else _mx_stride(x, "x"), bits, q.data_ptr(), scale.data_ptr(),
+        _mx_stream(stream, x))
+    if rc:
+        _check(rc)
     return q, scale
 
 
@@ -597,30 +603,38 @@ def moe_rmsnorm_mx(x, weight, eps=1e-6, residual=None, bits=8, want_y=False, res
     if len(shape) != 2:
         raise ValueError("x must have 2 dims")
     T, H = shape
-    _need(weight, torch.float32 if getattr(weight, "dtype", None) == torch.float32 else xt,
-          "weight", 1)
+    wf = getattr(weight, "dtype", None) is _F32
+    _need(weight, _F32 if wf else xt, "weight", 1)
     if weight.shape[0] != H:
         raise ValueError(f"weight must hold H = {H} values")
-    rst, rp = H, None
+    xst = H if x.is_contiguous() else _mx_stride(x, "x")
+    rst, rp, rop, yp = H, None, None, None
     if residual is not None:
         _mx_plain(residual, "residual", (xt,))
         if residual.shape != shape:
             raise ValueError(f"residual must be {list(shape)}")
-        rst, rp = _mx_stride(residual, "residual"), residual.data_ptr()
-    qs, ss = _mx_code_shape(shape, bits)
-    q = _mx_out(q, qs, _U8, dev, "q")
-    scale = _mx_out(scale, ss, _U8, dev, "scale")
-    rop = yp = None
-    if residual is not None or residual_out is not None:
+        rst = H if residual.is_contiguous() else _mx_stride(residual, "residual")
+        rp = residual.data_ptr()
+        if residual_out is None:
+            residual_out = _empty(shape, dtype=xt, device=dev)
+    if residual_out is not None:
         residual_out = _mx_out(residual_out, shape, xt, dev, "residual_out")
         rop = residual_out.data_ptr()
-    if want_y or y is not None:
-        y = _mx_out(y, shape, xt, dev, "y")
+    if y is not None:
+        _mx_out(y, shape, xt, dev, "y")
         yp = y.data_ptr()
-    _check(lib().moe_rmsnorm_mx(
-        x.data_ptr(), rp, weight.data_ptr(), dt, 1 if weight.dtype == torch.float32 else 0, T, H,
-        _mx_stride(x, "x"), rst, eps, rop, yp, bits, q.data_ptr(), scale.data_ptr(),
-        _mx_stream(stream, x)))
+    elif want_y:
+        y = _empty(shape, dtype=xt, device=dev)
+        yp = y.data_ptr()
+    qs, ss = _mx_code_shape(shape, bits)
+    q = _empty(qs, dtype=_U8, device=dev) if q is None else _mx_out(q, qs, _U8, dev, "q")
+    scale = (_empty(ss, dtype=_U8, device=dev) if scale is None
+             else _mx_out(scale, ss, _U8, dev, "scale"))
+    rc = (_lib or lib()).moe_rmsnorm_mx(
+        x.data_ptr(), rp, weight.data_ptr(), dt, wf, T, H, xst, rst, eps, rop, yp, bits,
+        q.data_ptr(), scale.data_ptr(), _mx_stream(stream, x))
+    if rc:
+        _check(rc)
     return q, scale, residual_out, y
 
 
