@@ -79,8 +79,12 @@ struct Cfg {
   static constexpr int kDestBytes = 2 * BN * 16;    // epilogue: where each column goes
   static constexpr int kSwapBytes = CG == 2 ? 2 * kEpiWarps * 1024 : 0;  // gate and up change warps
   static constexpr size_t kFixed = 1024 + kDestBytes + kSwapBytes + kSfRing * (size_t)kSfSlotBytes + 1024 + kUnitList * 16 + (kMaxE + 1) * 4;
+  // 4-bit rows: a stage holds twice the weights, and where five or more fit
+  // one fewer measured faster (64 tokens, E=8: 137 -> 130 us; 8192 rows 386 ->
+  // 376)
   static constexpr int kFit = (int)((kSmemMax - kFixed) / kStageBytes);
-  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr int kWant = BITS == 4 && kFit > 4 ? kFit - 1 : kFit;
+  static constexpr int kStages = kWant < kMaxStages ? kWant : kMaxStages;
   static_assert(kStages >= 2, "shared memory");
   // one CTA per SM: each allocates all of tensor memory
   static constexpr size_t kNeed = kFixed + (size_t)kStages * kStageBytes;
