@@ -470,11 +470,21 @@ _U8, _E4M3, _I32, _F32 = torch.uint8, torch.float8_e4m3fn, torch.int32, torch.fl
 _Tensor, _empty = torch.Tensor, torch.empty
 
 
-def _mx_stream(stream, t):
-    """cudaStream_t of stream, or of the current stream of t's device."""
-    if stream is not None:
-        return stream.cuda_stream
+def _mx_stream(t):
+    """cudaStream_t of the current stream of t's device."""
     return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _on_stream(fn):
+    """With stream given, the call runs with that stream current: what it
+    allocates (outputs, workspace) then belongs to the stream that uses it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
 def _mx_bits(bits):
@@ -539,6 +549,14 @@ def _mx_codes(q, scale, bits, name, dim=None):
     return shape, cols
 
 
+def _mx_together(first, **others):
+    """Raises unless every tensor is on first's device."""
+    dev = first.get_device()
+    for name, t in others.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on {first.device}")
+
+
 def _mx_out(t, shape, dtype, device, name):
     """The caller's output, checked, or a new one."""
     if t is None:
@@ -561,7 +579,8 @@ def _mx_code_shape(shape, bits):
     return lead + (cols // 2 if bits == 4 else cols,), lead + (cols // _MX_BLOCK,)
 
 
-def moe_quantize_mx(x, bits=4, q=None, scale=None, stream=None):
+@_on_stream
+def moe_quantize_mx(x, bits=4, q=None, scale=None):
     """bf16 / f16 / float32 [..., K] -> MX codes uint8 [..., K * bits / 8] (8
     bits: E4M3 bytes; 4 bits: two E2M1 codes per byte, even element low) and
     E8M0 scale codes uint8 [..., K / 32].  Rows may be strided."""
@@ -575,25 +594,27 @@ def moe_quantize_mx(x, bits=4, q=None, scale=None, stream=None):
     rc = (_lib or lib()).moe_quantize_mx(
         x.data_ptr(), dt, x.numel() // cols, cols,
         cols if x.is_contiguous() else _mx_stride(x, "x"), bits, q.data_ptr(), scale.data_ptr(),
-        _mx_stream(stream, x))
+        _mx_stream(x))
     if rc:
         _check(rc)
     return q, scale
 
 
-def moe_dequantize_mx(q, scale, bits=4, dtype=torch.bfloat16, out=None, stream=None):
+@_on_stream
+def moe_dequantize_mx(q, scale, bits=4, dtype=torch.bfloat16, out=None):
     """The values [..., K] that MX codes and scales stand for, in dtype."""
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
     shape, cols = _mx_codes(q, scale, bits, "q")
     out = _mx_out(out, (*shape[:-1], cols), dtype, q.device, "out")
     _check(lib().moe_dequantize_mx(q.data_ptr(), scale.data_ptr(), out.numel() // cols, cols,
-                                   bits, out.data_ptr(), _DTYPES[dtype], _mx_stream(stream, q)))
+                                   bits, out.data_ptr(), _DTYPES[dtype], _mx_stream(q)))
     return out
 
 
+@_on_stream
 def moe_rmsnorm_mx(x, weight, eps=1e-6, residual=None, bits=8, want_y=False, residual_out=None,
-                   y=None, q=None, scale=None, stream=None):
+                   y=None, q=None, scale=None):
     """Residual addition, RMS norm and MX rows (moe_rmsnorm_mx in
     include/moeq.h): x, residual bf16 or f16 [T, H] (rows may be strided),
     weight [H] of the same dtype or float32 -> (q, scale, x + residual or None,
@@ -607,6 +628,7 @@ def moe_rmsnorm_mx(x, weight, eps=1e-6, residual=None, bits=8, want_y=False, res
     _need(weight, _F32 if wf else xt, "weight", 1)
     if weight.shape[0] != H:
         raise ValueError(f"weight must hold H = {H} values")
+    _mx_together(x, weight=weight, residual=residual)
     xst = H if x.is_contiguous() else _mx_stride(x, "x")
     rst, rp, rop, yp = H, None, None, None
     if residual is not None:
@@ -632,7 +654,7 @@ def moe_rmsnorm_mx(x, weight, eps=1e-6, residual=None, bits=8, want_y=False, res
              else _mx_out(scale, ss, _U8, dev, "scale"))
     rc = (_lib or lib()).moe_rmsnorm_mx(
         x.data_ptr(), rp, weight.data_ptr(), dt, wf, T, H, xst, rst, eps, rop, yp, bits,
-        q.data_ptr(), scale.data_ptr(), _mx_stream(stream, x))
+        q.data_ptr(), scale.data_ptr(), _mx_stream(x))
     if rc:
         _check(rc)
     return q, scale, residual_out, y
@@ -646,8 +668,9 @@ def moe_mx_product_workspace(R, K, N, E=1) -> int:
 _mx_product_bytes = functools.lru_cache(maxsize=1024)(moe_mx_product_workspace)
 
 
+@_on_stream
 def moe_mx_product(a, a_scale, w, w_scale, expert_offsets=None, a_bits=8, out=None,
-                   out_dtype=torch.bfloat16, workspace=None, stream=None):
+                   out_dtype=torch.bfloat16, workspace=None):
     """MX rows [R, K] grouped by expert (expert_offsets int32 [E + 1]) times
     4-bit MX weights [E, N, K]: [R, N].  Without expert_offsets w is [N, K] (or
     [1, N, K]): a dense product."""
@@ -657,6 +680,7 @@ def moe_mx_product(a, a_scale, w, w_scale, expert_offsets=None, a_bits=8, out=No
         raise ValueError("a and w must have rows of the same length")
     if len(ws) not in (2, 3):
         raise ValueError("w must have 2 or 3 dims")
+    _mx_together(a, w=w, expert_offsets=expert_offsets, workspace=workspace)
     E, N, dev = ws[0] if len(ws) == 3 else 1, ws[-2], a.device
     op = None
     if expert_offsets is not None:
@@ -681,7 +705,7 @@ def moe_mx_product(a, a_scale, w, w_scale, expert_offsets=None, a_bits=8, out=No
         wp, nbytes = workspace.data_ptr(), workspace.numel()
     _check(L.moe_mx_product(a.data_ptr(), a_scale.data_ptr(), a_bits, R, K, N, E, w.data_ptr(),
                             w_scale.data_ptr(), op, out.data_ptr(), _DTYPES[out_dtype], wp,
-                            nbytes, _mx_stream(stream, a)))
+                            nbytes, _mx_stream(a)))
     return out
 
 
@@ -692,8 +716,9 @@ def moe_mx_forward_workspace(T, H, I, E, k, a_bits=8) -> int:
 _mx_forward_bytes = functools.lru_cache(maxsize=1024)(moe_mx_forward_workspace)
 
 
+@_on_stream
 def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out=None,
-                   out_dtype=torch.bfloat16, workspace=None, stream=None):
+                   out_dtype=torch.bfloat16, workspace=None):
     """The fused expert MLP with 4-bit MX experts on MX activations
     (moe_mx_forward in include/moeq.h): a [T, H] with a_bits, w13 [E, 2I, H], w2
     [E, H, I], topk_w / topk_ids [T, k] -> [T, H] bf16 or f16."""
@@ -707,6 +732,7 @@ def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out
     t2, k = topk_ids.shape
     if t2 != T or topk_w.shape != topk_ids.shape:
         raise ValueError(f"topk_w and topk_ids must be [{T}, k]")
+    _mx_together(a, w13=w13, w2=w2, topk_w=topk_w, topk_ids=topk_ids, workspace=workspace)
     dev = a.device
     if out is not None:
         out_dtype = out.dtype
@@ -723,5 +749,5 @@ def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out
     _check(L.moe_mx_forward(
         a.data_ptr(), a_scale.data_ptr(), a_bits, T, H, I, E, k, w13.data_ptr(), s13.data_ptr(),
         w2.data_ptr(), s2.data_ptr(), topk_w.data_ptr(), topk_ids.data_ptr(), out.data_ptr(),
-        _DTYPES[out_dtype], workspace.data_ptr(), nbytes, _mx_stream(stream, a)))
+        _DTYPES[out_dtype], workspace.data_ptr(), nbytes, _mx_stream(a)))
     return out
