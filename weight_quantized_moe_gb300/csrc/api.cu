@@ -899,14 +899,9 @@ MQ_EXPORT int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bit
     err = launch_mx_gemm(g, L.down, st);
   }
   if (err != cudaSuccess) return cuda_fail(err, "mx_forward: down launch");
-  MoeArgs m = {};
-  m.T = T; m.H = H; m.I = I; m.E = E; m.k = k;
-  m.topk_ids = topk_ids;
-  m.flags = out_dtype == MQ_DTYPE_F16 ? MQ_FWD_ACT_F16 : 0;
-  m.out = out;
   {
     LaunchScope ls(MQ_PROF_COMBINE, st);
-    err = launch_combine_splits(m, g.part, L.down.splits, st);
+    err = launch_mx_combine(g.part, L.down.splits, topk_ids, T, k, E, H, out, out_dtype, st);
   }
   return err == cudaSuccess ? MQ_OK : cuda_fail(err, "mx_forward: combine launch");
 }

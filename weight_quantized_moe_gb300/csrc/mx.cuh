@@ -261,3 +261,7 @@ MQ_HIDDEN cudaError_t launch_mx_gather(const uint8_t* a, const uint8_t* a_scale,
                                        int scale_bytes, const int32_t* sorted,
                                        const int32_t* num_padded, int k, int S, int64_t cap,
                                        uint8_t* dst, uint8_t* dst_scale, cudaStream_t st);
+// The router-weighted sum of each token's slots (weights already applied).
+MQ_HIDDEN cudaError_t launch_mx_combine(const float* part, int splits, const int32_t* ids,
+                                        int tokens, int k, int E, int H, void* out,
+                                        int out_dtype, cudaStream_t st);

@@ -786,6 +786,53 @@ __global__ void __launch_bounds__(256) mx_reduce(const float* __restrict__ part,
   }
 }
 
+// out[t, :] = sum over the token's valid slots j and the K splits, in the order
+// (j, split), of part[split, t k + j, :], rounded once.  A thread sums U groups
+// of four outputs and has B slots' groups in flight.  Bound by HBM: with two
+// slots per token one group per thread leaves too little in flight (4096
+// tokens, k=2, H=4096, between events: 63 us with U = 1, 26 with 4).
+template <typename T, int U, int B>
+__global__ void __launch_bounds__(256) mx_combine(const float* __restrict__ part, int splits,
+                                                  const int32_t* __restrict__ ids, int tokens,
+                                                  int k, int E, int H, T* __restrict__ out) {
+  mq::pdl_wait();
+  mq::pdl_trigger();
+  constexpr int per = 256 * U;               // groups of a CTA
+  const int ctas = (H / 4 + per - 1) / per;  // of a row
+  const int64_t t = blockIdx.x / ctas;
+  const int c0 = (int)(blockIdx.x % ctas) * per + threadIdx.x;
+  const int64_t slots = (int64_t)tokens * k;
+  float4 acc[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q0 = 0; q0 < k * splits; q0 += B) {
+    float4 v[B][U];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int q = q0 + b, j = q / splits;
+      const int e = q < k * splits ? ids[t * k + j] : -1;
+      const float4* row = reinterpret_cast<const float4*>(
+          part + ((q - j * splits) * slots + t * k + j) * H);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        v[b][u] = e >= 0 && e < E && c0 + u * 256 < H / 4 ? __ldcs(row + c0 + u * 256)
+                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        acc[u].x += v[b][u].x;
+        acc[u].y += v[b][u].y;
+        acc[u].z += v[b][u].z;
+        acc[u].w += v[b][u].w;
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (c0 + u * 256 < H / 4) store4(out + t * H + (int64_t)(c0 + u * 256) * 4, acc[u]);
+}
+
 // One warp per row; 16-byte pieces of the codes, 4-byte words of the scales.
 __global__ void __launch_bounds__(256) mx_gather(const uint8_t* __restrict__ a,
                                                  const uint8_t* __restrict__ a_scale,
@@ -1011,4 +1058,22 @@ cudaError_t launch_mx_gather(const uint8_t* a, const uint8_t* a_scale, int row_b
                              cudaStream_t st) {
   return launch_pdl(mx_gather, dim3((unsigned)((cap + 7) / 8)), dim3(256), 0, st, a, a_scale,
                     row_bytes, scale_bytes, sorted, num_padded, k, S, dst, dst_scale);
+}
+
+template <typename T>
+static cudaError_t combine_t(const float* part, int splits, const int32_t* ids, int tokens, int k,
+                             int E, int H, T* out, cudaStream_t st) {
+  // U = 4 once its CTAs still cover the SMs several times
+  const bool wide = H >= 4096 && (int64_t)tokens * (H / 4096) >= 4 * tc_num_sms();
+  const int per = 256 * (wide ? 4 : 1);
+  const int64_t grid = (int64_t)tokens * ((H / 4 + per - 1) / per);
+  return launch_pdl(wide ? mx_combine<T, 4, 2> : mx_combine<T, 1, 8>, dim3((unsigned)grid), dim3(256), 0,
+                    st, part, splits, ids, tokens, k, E, H, out);
+}
+
+cudaError_t launch_mx_combine(const float* part, int splits, const int32_t* ids, int tokens, int k,
+                              int E, int H, void* out, int out_dtype, cudaStream_t st) {
+  return out_dtype == MQ_DTYPE_F16
+             ? combine_t(part, splits, ids, tokens, k, E, H, static_cast<__half*>(out), st)
+             : combine_t(part, splits, ids, tokens, k, E, H, static_cast<__nv_bfloat16*>(out), st);
 }
