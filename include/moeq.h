@@ -460,8 +460,8 @@ int moe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int 
  * [E, N, K]; expert_offsets int32 [E + 1] (device), rising from >= 0 to <= R, or
  * NULL with E = 1 (a dense product).  Experts may be empty; rows outside
  * [offsets[0], offsets[E]) are left as they are.  Offsets that fall or leave
- * [0, R] set MQ_DEV_BAD_OFFSETS: no access leaves the arrays, and the output
- * is unspecified.  out [R, N] dense in out_dtype.  Accumulation is float32
+ * [0, R] set MQ_DEV_BAD_OFFSETS: no access leaves the arrays, nothing is computed
+ * and the output is unspecified.  out [R, N] dense in out_dtype.  Accumulation is float32
  * with one final rounding; a result is the same on every run.
  * The workspace holds float32 partial sums where K is split (few units of
  * work); moe_mx_product_workspace may return 0 (workspace may then be NULL).

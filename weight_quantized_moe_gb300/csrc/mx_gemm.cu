@@ -7,14 +7,27 @@
 // consecutive k.  tcgen05.mma takes the codes and the scales as they are and
 // accumulates in float32, so nothing is converted on the way.
 //
-// One persistent CTA per SM.  D[128 weight rows x BN rows of A]: the weights
-// are the instruction's A operand (M = 128) and the token rows its B operand
-// (N = BN), so that a few rows cost a narrow tile and no padding.  A unit is
-// (expert, chunk of at most BN rows, two weight tiles, K split); the two tiles
-// share the unit's rows, and are gate and up where the epilogue joins them.
+// One persistent CTA per SM.  D[weight rows x rows of A]: the weights are the
+// instruction's A operand (128 rows) and the token rows its B operand (as many
+// columns as a chunk has rows, in steps of 16), so that a few rows cost a narrow
+// instruction and no padding.  A unit is (expert, chunk of at most BN rows, 256
+// weight rows, K split); when gated the 256 are 128 gate rows and their up rows.
 //
-// Roles: warp 0 streams codes by TMA; warps 1-2 issue the MMAs; warps 3 and 12
-// bring the scales; warps 4-11 are the epilogue.
+// Two shapes (CG):
+//   1  A CTA holds both 128-row tiles of a unit, BN <= 96.  For experts with few
+//      rows: the weight stream bounds these (128 rows, E=8, K=4096, N=28672:
+//      82 us, 91 % of the HBM's rate; 76 us, 99 %, with 4-bit rows).
+//   2  A pair of CTAs (cta_group::2) holds the unit, 128 weight rows and half of
+//      its 224 rows of A in each.  An instruction reads its operands from shared
+//      memory at 64 bytes per cycle (measured: 64 cycles for 128 weight rows and
+//      half a cycle per column), so a wide tile whose columns are split over two
+//      SMs comes nearest the arithmetic rate.  8192 x 4096 x 28672: 595 us (3.2
+//      PFLOP/s; at 1370 W the clock falls to 1.46 GHz, at 2.07 GHz it takes 525),
+//      373 us (5.2 PFLOP/s) with 4-bit rows.
+//
+// Roles: warp 0 streams codes by TMA; warps 1-2 issue the MMAs (of a pair: warp 1
+// of its first CTA); warps 3 and 12-14 bring the scales; warps 4-11 are the
+// epilogue.
 //   * Codes.  A stage holds 128 bytes of each row, 128-byte swizzled: 128 k of
 //     E4M3 rows against 128 k of weights whose nibbles TMA spreads to 16-byte
 //     groups (the operand form of the mixed 8/4-bit instruction), or 256 k of
@@ -23,11 +36,12 @@
 //     (128 k, a "word") per row, row r in lane r % 32 and column r / 32.  The
 //     scale warps read the rows' scale bytes (16 bytes = 512 k per row), and
 //     write them to shared memory as that [32 lanes][4 columns] block for each
-//     word; the MMA warps copy a block to tensor memory with one
-//     tcgen05.cp, which the MMAs that follow it in the same thread see.
+//     word; an MMA warp copies a block to tensor memory with one tcgen05.cp,
+//     which the MMAs that follow it in the same thread see.
 //   * Epilogue.  A thread is one weight row (tensor-memory lane) and walks the
 //     columns, the rows of A.  32 lanes are 32 consecutive outputs: exactly
-//     one block when the activations are requantised.
+//     one block when the activations are requantised.  Two accumulator buffers:
+//     the next unit's MMAs run meanwhile.
 #include "mx.cuh"
 #include "sm100_ptx.cuh"
 
@@ -56,7 +70,7 @@ constexpr int kGroup = 8;              // weight tiles that a chunk walk shares
 constexpr unsigned long long kWaitNs = 1000000000ull;
 constexpr size_t kSmemMax = 227 * 1024;
 
-template <int BITS, int BN, int CG>
+template <int BITS, int BN, int CG, int EPI>
 struct Cfg {
   static constexpr int kTiles = CG == 2 ? 1 : 2;    // weight tiles of a unit, one MMA warp each
   static constexpr int kWords = BITS == 8 ? 1 : 2;  // 128-k scale words per stage
@@ -73,17 +87,19 @@ struct Cfg {
   // tensor-memory columns of one MMA warp's scales: its tile's and the rows'
   static constexpr int kSfCols = 4 * (1 + kBBlocks) * 4;
   static constexpr int kAccCols = kTiles * BN;
-  static constexpr int kBufs = 2 * kAccCols + kTiles * kSfCols <= 512 ? 2 : 1;
+  static constexpr int kBufs = 2;
   static constexpr int kSfBase = kBufs * kAccCols;
   static_assert(kSfBase + kTiles * kSfCols <= 512, "tensor memory");
-  static constexpr int kDestBytes = 2 * BN * 16;    // epilogue: where each column goes
-  static constexpr int kSwapBytes = CG == 2 ? 2 * kEpiWarps * 1024 : 0;  // gate and up change warps
-  static constexpr size_t kFixed = 1024 + kDestBytes + kSwapBytes + kSfRing * (size_t)kSfSlotBytes + 1024 + kUnitList * 16 + (kMaxE + 1) * 4;
-  // 4-bit rows: a stage holds twice the weights, and where five or more fit
-  // one fewer measured faster (64 tokens, E=8: 137 -> 130 us; 8192 rows 386 ->
-  // 376)
+  // epilogue: where each column goes; gate and up values that change warps
+  static constexpr int kDestBytes = EPI == MX_EPI_PART ? 2 * BN * 16 : 0;
+  static constexpr int kSwapBytes = EPI == MX_EPI_GATED && CG == 2 ? 2 * kEpiWarps * 1024 : 0;
+  static constexpr size_t kFixed = 1024 + (size_t)kSfRing * kSfSlotBytes + 1024 + kUnitList * 16 +
+                                   kDestBytes + kSwapBytes + (kMaxE + 1) * 4;
+  // 4-bit rows: a stage holds twice the weights, and four stages measured
+  // faster than the five or six that fit (64 tokens, E=8: 137 -> 130 us; 8192
+  // rows 386 -> 373)
   static constexpr int kFit = (int)((kSmemMax - kFixed) / kStageBytes);
-  static constexpr int kWant = BITS == 4 && kFit > 4 ? kFit - 1 : kFit;
+  static constexpr int kWant = BITS == 4 && kFit > 4 ? 4 : kFit;
   static constexpr int kStages = kWant < kMaxStages ? kWant : kMaxStages;
   static_assert(kStages >= 2, "shared memory");
   // one CTA per SM: each allocates all of tensor memory
@@ -309,7 +325,7 @@ template <int BITS, int BN, int EPI, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
             const __grid_constant__ CUtensorMap map_part, const Params p) {
-  using C = Cfg<BITS, BN, CG>;
+  using C = Cfg<BITS, BN, CG, EPI>;
   constexpr int kTiles = C::kTiles;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -318,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Ctl* ctl = reinterpret_cast<Ctl*>(sf + (size_t)kSfRing * C::kSfSlotBytes);
   int4* list = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(ctl) + 1024);
   int4* dest_table = list + kUnitList;  // [2][BN]
-  float* swap = reinterpret_cast<float*>(dest_table + 2 * BN);  // [2][kEpiWarps][8][32]
+  float* swap = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(dest_table) + C::kDestBytes);  // [2][kEpiWarps][8][32]
   int* chunk_start = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(swap) + C::kSwapBytes);
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -364,8 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     fine &= segment(p, e, start, count);
     chunk_start[e] = (count + BN - 1) / BN;
   }
-  if (!fine && blockIdx.x == 0) mq::flag(p.status, MQ_DEV_BAD_OFFSETS);
-  __syncthreads();
+  // offsets that fall or leave [0, R]: nothing is computed
+  const bool bad = __syncthreads_or(!fine);
+  if (bad && tid == 0 && blockIdx.x == 0) mq::flag(p.status, MQ_DEV_BAD_OFFSETS);
   if (warp == 0) {
     int run = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
@@ -383,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) chunk_start[p.E] = run;
   }
   __syncthreads();
-  const uint32_t total = (uint32_t)chunk_start[p.E] * p.mtiles * p.splits;
+  const uint32_t total = bad ? 0 : (uint32_t)chunk_start[p.E] * p.mtiles * p.splits;
   const uint32_t units = worker < total ? (total - worker + workers - 1) / workers : 0;
   if (tid < kUnitList && tid < units) {
     const Unit w = decode_unit<BN>(p, chunk_start, worker + tid * workers);
@@ -887,7 +904,7 @@ cudaError_t make_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, const v
 template <int BITS, int BN, int EPI, int CG>
 cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const CUtensorMap& mr, const Params& p,
                        int64_t units, cudaStream_t st) {
-  constexpr size_t smem = Cfg<BITS, BN, CG>::kSmem;
+  constexpr size_t smem = Cfg<BITS, BN, CG, EPI>::kSmem;
   static_assert(smem <= kSmemMax, "shared memory");
   auto kern = mx_gemm<BITS, BN, EPI, CG>;
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
