@@ -63,6 +63,9 @@ constexpr int kSfWarps = 4;            // warps 3 and 12-14
 constexpr int kEpiWarps = 8;
 constexpr int kMaxStages = 12;
 constexpr int kSfRing = 4;             // scale slots, 512 k each
+// A slot is filled by one warp only: with more warps than slots one could be two
+// turns ahead of the barrier's phase, which its parity cannot tell from none.
+static_assert(kSfRing == kSfWarps, "one warp per scale slot");
 constexpr int kMaxE = 1024;
 constexpr int kPairRows = 224;         // rows per tile of a CTA pair
 constexpr int kUnitList = 128;         // units of a CTA that are decoded at its start
@@ -476,7 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp <= kTiles && rank == 0) {
     // ----------------------------------------------------------- MMAs --
-    // One warp per weight tile: an instruction takes about 90 cycles to issue
+    // Bound by operand reads (64 bytes per cycle) where rows are many, else by
+    // the weight stream.  One warp per weight tile: an instruction takes about 90 cycles to issue
     // whatever its width, two warps issue at once.  The warp walks the loop
     // together and one elected lane issues, so that the descriptors stay in
     // uniform registers (a lone lane takes three times as long).
@@ -546,6 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait_drain(&ctl->drain, 0);
   } else if (warp == 3 || warp >= 12) {
     // ------------------------------------------------------------ scales --
+    // A lane brings one row's 16 bytes of each 32-row group; the loads of a
+    // warp's next slot are in flight while it waits for the slot to come free
+    // (four warps: two left 8192 x 4096 x 28672 with 4-bit rows at 488 us
+    // instead of 419).  Whole 32-byte sectors per load, or a prefetch of the
+    // unit's scale rows into L2, changed nothing.
     const int lw = warp == 3 ? 0 : warp - 11;  // the slot of the ring it fills
     constexpr int kGroupsA = kTiles * 4, kGroupsB = (BN + 31) / 32;
     uint32_t sb_it = 0;

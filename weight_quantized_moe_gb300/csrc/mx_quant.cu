@@ -10,7 +10,9 @@ constexpr int kQuantThreads = 256;
 
 // One lane per 8 consecutive elements, so that the four lanes of a block are
 // adjacent; U such vectors per thread.  Bound by HBM: each element is read
-// and written once.
+// and written once (180224 x 2048 bf16 to 4 bits 139 us, 6.70 TB/s; to 8 bits
+// 156 us, 7.16 TB/s; a copy of such rows 6.72 TB/s).  The block maximum is taken
+// on packed 16-bit magnitudes (with eight float maxima per lane 156 us).
 template <typename T, int BITS, int U, bool DENSE>
 __global__ void __launch_bounds__(kQuantThreads) quant_mx_kernel(const T* __restrict__ x,
                                                                  int64_t nvec, uint32_t vec_per_row,
@@ -50,6 +52,8 @@ __global__ void __launch_bounds__(kQuantThreads) quant_mx_kernel(const T* __rest
   }
 }
 
+// The inverse: bound by HBM, mostly its writes (180224 x 2048 from 4 bits to
+// bf16 135 us, 6.91 TB/s).
 template <typename T, int BITS>
 __global__ void __launch_bounds__(256) dequant_mx_kernel(const uint8_t* __restrict__ q,
                                                          const uint8_t* __restrict__ scale,
@@ -95,7 +99,9 @@ __global__ void __launch_bounds__(256) dequant_mx_kernel(const uint8_t* __restri
 // One CTA per row; the row's float32 sums stay in registers (V vectors of 8
 // per thread) between the sum of squares and the output, so every input is
 // read once.  h = x + residual is rounded only where it is stored; the norm
-// and the codes are taken from the float32 values.
+// and the codes are taken from the float32 values.  Bound by HBM (8192 x 4096
+// with residual and 16-bit output 46.1 us, 6.57 TB/s).  V = 1 up to H = 4096:
+// the rows in flight come from several CTAs per SM.
 template <typename T, typename W, int BITS, int V>
 __global__ void __launch_bounds__(1024) rmsnorm_mx_kernel(const NormArgs a) {
   __shared__ float s_sum[32];
