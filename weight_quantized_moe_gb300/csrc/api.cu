@@ -862,23 +862,28 @@ MQ_EXPORT int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bit
   unsigned* status = status_ptr();
   const int S = T * k;
   cudaError_t err;
+  // Rows in expert order: one launch for up to 2048 slots, else the align
+  // kernel and a gather (see mx_arrange).
+  const bool small = S <= 2048;
   {
     LaunchScope ls(MQ_PROF_ALIGN, st);
-    err = launch_align(topk_ids, T, k, E, kAlignBlock, sorted,
-                       reinterpret_cast<int32_t*>(ws + L.block_expert), offsets, num_padded,
-                       status, st, 0, nullptr, nullptr, counts);
+    err = small ? launch_mx_arrange(topk_ids, S, k, E, a, a_scale, H * a_bits / 8, H / 32, sorted,
+                                    offsets, ws + L.xa, ws + L.xs, status, st)
+                : launch_align(topk_ids, T, k, E, kAlignBlock, sorted,
+                               reinterpret_cast<int32_t*>(ws + L.block_expert), offsets,
+                               num_padded, status, st, 0, nullptr, nullptr, counts);
   }
   if (err != cudaSuccess) return cuda_fail(err, "mx_forward: align launch");
-  {
+  if (!small) {
     LaunchScope ls(MQ_PROF_GATHER, st);
     err = launch_mx_gather(a, a_scale, H * a_bits / 8, H / 32, sorted, num_padded, k, S, L.cap,
                            ws + L.xa, ws + L.xs, st);
+    if (err != cudaSuccess) return cuda_fail(err, "mx_forward: gather launch");
   }
-  if (err != cudaSuccess) return cuda_fail(err, "mx_forward: gather launch");
   MxGemm g = {};
   g.a_bits = a_bits;
   g.R = L.cap; g.S = S; g.E = E;
-  g.seg_start = offsets; g.seg_count = counts;
+  g.seg_start = offsets; g.seg_count = small ? nullptr : counts;
   g.status = status;
   g.epi = MX_EPI_GATED;
   g.a = ws + L.xa; g.a_scale = ws + L.xs; g.w = w13; g.w_scale = s13;

@@ -256,6 +256,12 @@ MQ_HIDDEN cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStre
 MQ_HIDDEN cudaError_t launch_mx_reduce(const float* part, int splits, int64_t rows, int N,
                                        const int32_t* offsets, int E, void* out, int out_dtype,
                                        cudaStream_t st);
+// The token-slots in expert order (stable), each expert's first row [E + 1], and
+// their rows of a with the scales in that order: dst row p = row sorted[p] / k.
+MQ_HIDDEN cudaError_t launch_mx_arrange(const int32_t* ids, int S, int k, int E, const uint8_t* a,
+                                        const uint8_t* a_scale, int row_bytes, int scale_bytes,
+                                        int32_t* sorted, int32_t* offsets, uint8_t* dst,
+                                        uint8_t* dst_scale, unsigned* status, cudaStream_t st);
 // Rows of a (and their scales) in expert order: dst row p = src row sorted[p] / k.
 MQ_HIDDEN cudaError_t launch_mx_gather(const uint8_t* a, const uint8_t* a_scale, int row_bytes,
                                        int scale_bytes, const int32_t* sorted,
