@@ -153,6 +153,18 @@ def test_forward_non_finite_token_stays_alone(T):
     check_forward(np.delete(got, 3, 0), ref)
 
 
+@pytest.mark.parametrize("T", [10, 250])
+def test_forward_saturated_gates(T):
+    """Gate values far below and above the range of exp."""
+    c = forward_case(T, 2, 1, 256, 256, 8, seed=8)
+    c[1].add_(8)                       # rows 256 times as large: |gate| of some hundreds
+    ref = forward_ref(*c, 8)
+    got = mq.moe_mx_forward(*c, a_bits=8)
+    done()
+    assert np.isfinite(ref).all()
+    check_forward(np64(got), ref)
+
+
 def test_forward_of_zero_tokens_rows():
     """Rows of zeros: every block scale is the smallest, the output is 0."""
     c = forward_case(9, 4, 2, 256, 256, 4, seed=6)

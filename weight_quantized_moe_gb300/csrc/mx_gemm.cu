@@ -1060,7 +1060,10 @@ cudaError_t launch_epi(const MxGemm& g, const MxPlan& pl, const CUtensorMap& mw,
 // columns to spare; CTA pairs above 96 rows.  Forwards in us with each choice
 // (16, 32, 64, 96, pairs): E=8 k=2 H=4096 I=14336 T=64 186 142 144 145 180, T=256
 // 379 237 215 161 197, T=512 690 389 303 259 219; E=128 k=8 H=2048 I=768 T=64 73
-// 73 77 78 106, T=2048 404 257 206 202 202.
+// 73 77 78 106, T=2048 404 257 206 202 202.  Layers of more than 32 experts count
+// their load 1.7 times: it is seldom even there (that E=128 layer with Zipf
+// popularity, 32, 64, 96 rows: T=256 58 51 51, T=512 79 70 68; even load 83 86 87,
+// 108 97 98).
 //
 // K splits: the count with the least estimated time, in us.  The weights come
 // in at the HBM's rate or, with few units, at what their SMs can take (70 GB/s
@@ -1075,7 +1078,8 @@ MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated, int a_bits) {
   const double live = std::max(1.0, E * (1.0 - std::pow(1.0 - 1.0 / E, (double)S)));
   const double avg = S / live;
   pl.pair = avg > 96;
-  pl.bn = pl.pair ? kPairRows : S <= 16 ? 16 : avg <= 20 ? 32 : avg <= 40 ? 64 : 96;
+  const double load = E > 32 ? 1.7 * avg : avg;
+  pl.bn = pl.pair ? kPairRows : S <= 16 ? 16 : load <= 20 ? 32 : load <= 40 ? 64 : 96;
   pl.splits = 1;
   if (gated || S > 1024) return pl;  // (more rows: partial sums would cost more than idle SMs)
   const int sms = pl.pair ? tc_num_sms() / 2 : tc_num_sms();
