@@ -467,24 +467,14 @@ def moe_quant_forward_noalloc(x, w13, w2, s13, s2, topk_w, topk_ids, bits=8, gro
 _MX_BLOCK = 32
 _HALVES = (torch.bfloat16, torch.float16)
 _U8, _E4M3, _I32, _F32 = torch.uint8, torch.float8_e4m3fn, torch.int32, torch.float32
-_Tensor, _empty = torch.Tensor, torch.empty
+_Tensor, _empty, _empty_like = torch.Tensor, torch.empty, torch.empty_like
 
 
 def _mx_stream(t):
-    """cudaStream_t of the current stream of t's device."""
+    """cudaStream_t of the current stream of t's device.  A call with stream=
+    runs again with that stream current, so that what it allocates (outputs,
+    workspace) belongs to the stream that uses it."""
     return torch._C._cuda_getCurrentRawStream(t.device.index)
-
-
-def _on_stream(fn):
-    """With stream given, the call runs with that stream current: what it
-    allocates (outputs, workspace) then belongs to the stream that uses it."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
 
 
 def _mx_bits(bits):
@@ -579,11 +569,13 @@ def _mx_code_shape(shape, bits):
     return lead + (cols // 2 if bits == 4 else cols,), lead + (cols // _MX_BLOCK,)
 
 
-@_on_stream
-def moe_quantize_mx(x, bits=4, q=None, scale=None):
+def moe_quantize_mx(x, bits=4, q=None, scale=None, stream=None):
     """bf16 / f16 / float32 [..., K] -> MX codes uint8 [..., K * bits / 8] (8
     bits: E4M3 bytes; 4 bits: two E2M1 codes per byte, even element low) and
     E8M0 scale codes uint8 [..., K / 32].  Rows may be strided."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_quantize_mx(x, bits, q, scale)
     dt = _mx_plain(x, "x", _DTYPES)
     shape, dev = x.shape, x.device
     qs, ss = _mx_code_shape(shape, bits)
@@ -600,9 +592,11 @@ def moe_quantize_mx(x, bits=4, q=None, scale=None):
     return q, scale
 
 
-@_on_stream
-def moe_dequantize_mx(q, scale, bits=4, dtype=torch.bfloat16, out=None):
+def moe_dequantize_mx(q, scale, bits=4, dtype=torch.bfloat16, out=None, stream=None):
     """The values [..., K] that MX codes and scales stand for, in dtype."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_dequantize_mx(q, scale, bits, dtype, out)
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
     shape, cols = _mx_codes(q, scale, bits, "q")
@@ -612,13 +606,15 @@ def moe_dequantize_mx(q, scale, bits=4, dtype=torch.bfloat16, out=None):
     return out
 
 
-@_on_stream
 def moe_rmsnorm_mx(x, weight, eps=1e-6, residual=None, bits=8, want_y=False, residual_out=None,
-                   y=None, q=None, scale=None):
+                   y=None, q=None, scale=None, stream=None):
     """Residual addition, RMS norm and MX rows (moe_rmsnorm_mx in
     include/moeq.h): x, residual bf16 or f16 [T, H] (rows may be strided),
     weight [H] of the same dtype or float32 -> (q, scale, x + residual or None,
     the normed rows or None).  residual_out may be residual (in place)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_rmsnorm_mx(x, weight, eps, residual, bits, want_y, residual_out, y, q, scale)
     dt = _mx_plain(x, "x", _HALVES)
     xt, dev, shape = x.dtype, x.device, x.shape
     if len(shape) != 2:
@@ -638,7 +634,7 @@ def moe_rmsnorm_mx(x, weight, eps=1e-6, residual=None, bits=8, want_y=False, res
         rst = H if residual.is_contiguous() else _mx_stride(residual, "residual")
         rp = residual.data_ptr()
         if residual_out is None:
-            residual_out = _empty(shape, dtype=xt, device=dev)
+            residual_out = _empty_like(x) if xst == H else _empty(shape, dtype=xt, device=dev)
     if residual_out is not None:
         residual_out = _mx_out(residual_out, shape, xt, dev, "residual_out")
         rop = residual_out.data_ptr()
@@ -646,7 +642,7 @@ def moe_rmsnorm_mx(x, weight, eps=1e-6, residual=None, bits=8, want_y=False, res
         _mx_out(y, shape, xt, dev, "y")
         yp = y.data_ptr()
     elif want_y:
-        y = _empty(shape, dtype=xt, device=dev)
+        y = _empty_like(x) if xst == H else _empty(shape, dtype=xt, device=dev)
         yp = y.data_ptr()
     qs, ss = _mx_code_shape(shape, bits)
     q = _empty(qs, dtype=_U8, device=dev) if q is None else _mx_out(q, qs, _U8, dev, "q")
@@ -668,12 +664,15 @@ def moe_mx_product_workspace(R, K, N, E=1) -> int:
 _mx_product_bytes = functools.lru_cache(maxsize=1024)(moe_mx_product_workspace)
 
 
-@_on_stream
 def moe_mx_product(a, a_scale, w, w_scale, expert_offsets=None, a_bits=8, out=None,
-                   out_dtype=torch.bfloat16, workspace=None):
+                   out_dtype=torch.bfloat16, workspace=None, stream=None):
     """MX rows [R, K] grouped by expert (expert_offsets int32 [E + 1]) times
     4-bit MX weights [E, N, K]: [R, N].  Without expert_offsets w is [N, K] (or
     [1, N, K]): a dense product."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_mx_product(a, a_scale, w, w_scale, expert_offsets, a_bits, out, out_dtype,
+                                  workspace)
     (R, _), K = _mx_codes(a, a_scale, a_bits, "a", 2)
     ws, wk = _mx_codes(w, w_scale, 4, "w")
     if wk != K:
@@ -716,12 +715,15 @@ def moe_mx_forward_workspace(T, H, I, E, k, a_bits=8) -> int:
 _mx_forward_bytes = functools.lru_cache(maxsize=1024)(moe_mx_forward_workspace)
 
 
-@_on_stream
 def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out=None,
-                   out_dtype=torch.bfloat16, workspace=None):
+                   out_dtype=torch.bfloat16, workspace=None, stream=None):
     """The fused expert MLP with 4-bit MX experts on MX activations
     (moe_mx_forward in include/moeq.h): a [T, H] with a_bits, w13 [E, 2I, H], w2
     [E, H, I], topk_w / topk_ids [T, k] -> [T, H] bf16 or f16."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits, out,
+                                  out_dtype, workspace)
     (T, _), H = _mx_codes(a, a_scale, a_bits, "a", 2)
     (E, n13, _), k13 = _mx_codes(w13, s13, 4, "w13", 3)
     (e2, n2, _), I = _mx_codes(w2, s2, 4, "w2", 3)
