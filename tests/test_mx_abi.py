@@ -88,7 +88,7 @@ def test_mx_forward_refusals(lib):
     assert lib.moe_mx_forward_workspace(4, 128, 128, 8, 2, 6) == 0
 
 
-def test_binding_refusals():
+def test_binding_refusals(lib):
     """Wrong dtypes, devices, shapes and strides never reach the library."""
     from weight_quantized_moe_gb300 import binding as b
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
@@ -96,18 +96,13 @@ def test_binding_refusals():
         b.moe_quantize_mx(x)
     with pytest.raises(TypeError):
         b.moe_quantize_mx(x.double())
-    with pytest.raises(ValueError, match="contiguous"):
-        b._mx_stride(x.t(), "x")
-    with pytest.raises(ValueError, match="evenly"):
-        b._mx_stride(torch.zeros(4, 6, 64)[:, ::2].transpose(0, 1), "x")
-    with pytest.raises(ValueError, match="bits"):
-        b._mx_code_shape((4, 64), 5)
-    with pytest.raises(ValueError, match="multiple"):
-        b._mx_code_shape((4, 48), 4)
     with pytest.raises(TypeError):
         b.moe_dequantize_mx(x, x, dtype=torch.int8)
     with pytest.raises(TypeError):
         b.moe_rmsnorm_mx(x.float(), x)
-    assert b._mx_code_shape((3, 4, 64), 4) == ((3, 4, 32), (3, 4, 2))
-    assert b._mx_stride(torch.zeros(4, 96)[:, :64], "x") == 96
-    assert b._mx_stride(torch.zeros(64), "x") == 64
+    with pytest.raises(TypeError):
+        b.moe_mx_product(x, x, x, x, out_dtype=torch.float64)
+    with pytest.raises(TypeError):
+        b.moe_mx_forward(x, x, x, x, x, x, x, x, out_dtype=torch.float32)
+    with pytest.raises(TypeError):
+        b.moe_quantize_mx([1.0])

@@ -1,6 +1,7 @@
 """ctypes binding of libmoeq.so: same names as the C ABI in include/moeq.h.
 
-Argument marshalling only.  Each function checks dtypes/shapes/devices of
+Argument marshalling only (of the microscaled calls in a compiled part,
+pysrc/mx_binding.cpp).  Each function checks dtypes/shapes/devices of
 the torch tensors it is given, allocates missing outputs with torch (the
 caller side of the ABI owns memory), and passes raw device pointers plus the
 current CUDA stream.  All computation happens in the library's kernels; if
@@ -10,7 +11,8 @@ the library is missing, every call raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -462,148 +464,53 @@ def moe_quant_forward_noalloc(x, w13, w2, s13, s2, topk_w, topk_ids, bits=8, gro
 
 
 # ------------------------------------------------- microscaled (MX) formats --
-# These calls stand beside kernels of a few microseconds, so their checks read
-# each attribute once and pass plain integers to ctypes.
-_MX_BLOCK = 32
+# These calls stand beside kernels of a few microseconds: their checks, output
+# allocation and library call are compiled (pysrc/mx_binding.cpp).
+MX_BINDING_PATH = os.path.join(_PKG, "_mx_binding.so")
 _HALVES = (torch.bfloat16, torch.float16)
-_U8, _E4M3, _I32, _F32 = torch.uint8, torch.float8_e4m3fn, torch.int32, torch.float32
-_Tensor, _empty, _empty_like = torch.Tensor, torch.empty, torch.empty_like
+_mx = None
 
 
-def _mx_stream(t):
-    """cudaStream_t of the current stream of t's device.  A call with stream=
-    runs again with that stream current, so that what it allocates (outputs,
-    workspace) belongs to the stream that uses it."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
-
-
-def _mx_bits(bits):
-    if bits != 4 and bits != 8:
-        raise ValueError(f"bits must be 4 or 8, got {bits}")
-
-
-def _mx_plain(t, name, dtypes):
-    """Checks a tensor on the plain side; returns its MQ_DTYPE_*."""
-    if not isinstance(t, _Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    dt = t.dtype
-    if dt not in dtypes:
-        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {dt}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    return _DTYPES[dt]
-
-
-def _mx_stride(t, name):
-    """Elements between the rows of a tensor whose rows are dense and evenly
-    spaced."""
-    cols = t.shape[-1]
-    if t.is_contiguous():
-        return cols
-    if cols > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if t.dim() > 2:
-        try:
-            t = t.view(-1, cols)
-        except RuntimeError:
-            raise ValueError(f"{name}: the rows must be evenly spaced") from None
-    return t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else cols
-
-
-def _mx_codes(q, scale, bits, name, dim=None):
-    """Checks MX codes and scales; returns (shape of the codes, elements in a
-    row)."""
-    if bits != 4 and bits != 8:
-        raise ValueError(f"bits must be 4 or 8, got {bits}")
-    if not isinstance(q, _Tensor) or not isinstance(scale, _Tensor):
-        raise TypeError(f"{name} and {name}_scale must be torch.Tensors")
-    if q.dtype is not _U8 and not (bits == 8 and q.dtype is _E4M3):
-        raise TypeError(f"{name} must be torch.uint8, got {q.dtype}")
-    if scale.dtype is not _U8:
-        raise TypeError(f"{name}_scale must be torch.uint8, got {scale.dtype}")
-    dev = q.get_device()
-    if dev < 0 or scale.get_device() != dev:
-        raise ValueError(f"{name} and {name}_scale must be on one CUDA device")
-    if not q.is_contiguous() or not scale.is_contiguous():
-        raise ValueError(f"{name} and {name}_scale must be contiguous")
-    shape, ss = q.shape, scale.shape
-    n = len(shape)
-    if n != dim if dim else n < 1:
-        raise ValueError(f"{name} must have {dim or 'at least one'} dims")
-    cols = shape[-1] * 2 if bits == 4 else shape[-1]
-    if cols == 0 or cols % _MX_BLOCK:
-        raise ValueError(f"{name} must have rows of a positive multiple of {_MX_BLOCK} elements")
-    if len(ss) != n or ss[-1] * _MX_BLOCK != cols or (
-            ss[:-1] != shape[:-1] if n > 2 else n == 2 and ss[0] != shape[0]):
-        raise ValueError(f"{name}_scale must be {[*shape[:-1], cols // _MX_BLOCK]}")
-    return shape, cols
-
-
-def _mx_together(first, **others):
-    """Raises unless every tensor is on first's device."""
-    dev = first.get_device()
-    for name, t in others.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be on {first.device}")
-
-
-def _mx_out(t, shape, dtype, device, name):
-    """The caller's output, checked, or a new one."""
-    if t is None:
-        return _empty(shape, dtype=dtype, device=device)
-    _need(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    return t
-
-
-def _mx_code_shape(shape, bits):
-    """Shapes of the codes and scales of rows."""
-    _mx_bits(bits)
-    cols = shape[-1] if len(shape) else 0
-    if cols == 0 or cols % _MX_BLOCK:
-        raise ValueError(f"rows must have a positive multiple of {_MX_BLOCK} elements")
-    lead = tuple(shape[:-1])
-    return lead + (cols // 2 if bits == 4 else cols,), lead + (cols // _MX_BLOCK,)
+def _mx_binding():
+    """Load _mx_binding.so (raises if it has not been built)."""
+    global _mx
+    if _mx is None:
+        lib()
+        if not os.path.exists(MX_BINDING_PATH):
+            raise RuntimeError(
+                f"{MX_BINDING_PATH} is missing: build it with "
+                "`python -c 'import __graft_entry__ as g; g.build()'`")
+        loader = importlib.machinery.ExtensionFileLoader("_mx_binding", MX_BINDING_PATH)
+        m = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("_mx_binding", MX_BINDING_PATH, loader=loader))
+        loader.exec_module(m)
+        m.set_error_class(MoeqError)
+        _mx = m
+    return _mx
 
 
 def moe_quantize_mx(x, bits=4, q=None, scale=None, stream=None):
     """bf16 / f16 / float32 [..., K] -> MX codes uint8 [..., K * bits / 8] (8
     bits: E4M3 bytes; 4 bits: two E2M1 codes per byte, even element low) and
-    E8M0 scale codes uint8 [..., K / 32].  Rows may be strided."""
+    E8M0 scale codes uint8 [..., K / 32].  Rows may be strided.
+
+    With stream=, here and in the other moe_*_mx* calls, the call runs with
+    that stream current: what it allocates belongs to the stream that uses it."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_quantize_mx(x, bits, q, scale)
-    dt = _mx_plain(x, "x", _DTYPES)
-    shape, dev = x.shape, x.device
-    qs, ss = _mx_code_shape(shape, bits)
-    cols = shape[-1]
-    q = _empty(qs, dtype=_U8, device=dev) if q is None else _mx_out(q, qs, _U8, dev, "q")
-    scale = (_empty(ss, dtype=_U8, device=dev) if scale is None
-             else _mx_out(scale, ss, _U8, dev, "scale"))
-    rc = (_lib or lib()).moe_quantize_mx(
-        x.data_ptr(), dt, x.numel() // cols, cols,
-        cols if x.is_contiguous() else _mx_stride(x, "x"), bits, q.data_ptr(), scale.data_ptr(),
-        _mx_stream(x))
-    if rc:
-        _check(rc)
-    return q, scale
+    return (_mx or _mx_binding()).quantize(x, bits, q, scale)
 
 
 def moe_dequantize_mx(q, scale, bits=4, dtype=torch.bfloat16, out=None, stream=None):
-    """The values [..., K] that MX codes and scales stand for, in dtype."""
+    """The values [..., K] that MX codes and scales stand for, in dtype (bf16,
+    f16 or float32)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_dequantize_mx(q, scale, bits, dtype, out)
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
-    shape, cols = _mx_codes(q, scale, bits, "q")
-    out = _mx_out(out, (*shape[:-1], cols), dtype, q.device, "out")
-    _check(lib().moe_dequantize_mx(q.data_ptr(), scale.data_ptr(), out.numel() // cols, cols,
-                                   bits, out.data_ptr(), _DTYPES[dtype], _mx_stream(q)))
-    return out
+    return (_mx or _mx_binding()).dequantize(q, scale, bits, _DTYPES[dtype], out)
 
 
 def moe_rmsnorm_mx(x, weight, eps=1e-6, residual=None, bits=8, want_y=False, residual_out=None,
@@ -615,104 +522,34 @@ def moe_rmsnorm_mx(x, weight, eps=1e-6, residual=None, bits=8, want_y=False, res
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_rmsnorm_mx(x, weight, eps, residual, bits, want_y, residual_out, y, q, scale)
-    dt = _mx_plain(x, "x", _HALVES)
-    xt, dev, shape = x.dtype, x.device, x.shape
-    if len(shape) != 2:
-        raise ValueError("x must have 2 dims")
-    T, H = shape
-    wf = getattr(weight, "dtype", None) is _F32
-    _need(weight, _F32 if wf else xt, "weight", 1)
-    if weight.shape[0] != H:
-        raise ValueError(f"weight must hold H = {H} values")
-    _mx_together(x, weight=weight, residual=residual)
-    xst = H if x.is_contiguous() else _mx_stride(x, "x")
-    rst, rp, rop, yp = H, None, None, None
-    if residual is not None:
-        _mx_plain(residual, "residual", (xt,))
-        if residual.shape != shape:
-            raise ValueError(f"residual must be {list(shape)}")
-        rst = H if residual.is_contiguous() else _mx_stride(residual, "residual")
-        rp = residual.data_ptr()
-        if residual_out is None:
-            residual_out = _empty_like(x) if xst == H else _empty(shape, dtype=xt, device=dev)
-    if residual_out is not None:
-        residual_out = _mx_out(residual_out, shape, xt, dev, "residual_out")
-        rop = residual_out.data_ptr()
-    if y is not None:
-        _mx_out(y, shape, xt, dev, "y")
-        yp = y.data_ptr()
-    elif want_y:
-        y = _empty_like(x) if xst == H else _empty(shape, dtype=xt, device=dev)
-        yp = y.data_ptr()
-    qs, ss = _mx_code_shape(shape, bits)
-    q = _empty(qs, dtype=_U8, device=dev) if q is None else _mx_out(q, qs, _U8, dev, "q")
-    scale = (_empty(ss, dtype=_U8, device=dev) if scale is None
-             else _mx_out(scale, ss, _U8, dev, "scale"))
-    rc = (_lib or lib()).moe_rmsnorm_mx(
-        x.data_ptr(), rp, weight.data_ptr(), dt, wf, T, H, xst, rst, eps, rop, yp, bits,
-        q.data_ptr(), scale.data_ptr(), _mx_stream(x))
-    if rc:
-        _check(rc)
-    return q, scale, residual_out, y
+    return (_mx or _mx_binding()).rmsnorm(x, weight, eps, residual, bits, want_y, residual_out, y,
+                                          q, scale)
 
 
 def moe_mx_product_workspace(R, K, N, E=1) -> int:
-    return lib().moe_mx_product_workspace(R, K, N, E)
-
-
-# (the queries' answers depend on their arguments alone)
-_mx_product_bytes = functools.lru_cache(maxsize=1024)(moe_mx_product_workspace)
+    return int(lib().moe_mx_product_workspace(R, K, N, E))
 
 
 def moe_mx_product(a, a_scale, w, w_scale, expert_offsets=None, a_bits=8, out=None,
                    out_dtype=torch.bfloat16, workspace=None, stream=None):
     """MX rows [R, K] grouped by expert (expert_offsets int32 [E + 1]) times
-    4-bit MX weights [E, N, K]: [R, N].  Without expert_offsets w is [N, K] (or
-    [1, N, K]): a dense product."""
+    4-bit MX weights [E, N, K]: [R, N] in out's dtype or out_dtype (bf16, f16 or
+    float32).  Without expert_offsets w is [N, K] (or [1, N, K]): a dense
+    product."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_mx_product(a, a_scale, w, w_scale, expert_offsets, a_bits, out, out_dtype,
                                   workspace)
-    (R, _), K = _mx_codes(a, a_scale, a_bits, "a", 2)
-    ws, wk = _mx_codes(w, w_scale, 4, "w")
-    if wk != K:
-        raise ValueError("a and w must have rows of the same length")
-    if len(ws) not in (2, 3):
-        raise ValueError("w must have 2 or 3 dims")
-    _mx_together(a, w=w, expert_offsets=expert_offsets, workspace=workspace)
-    E, N, dev = ws[0] if len(ws) == 3 else 1, ws[-2], a.device
-    op = None
-    if expert_offsets is not None:
-        _need(expert_offsets, torch.int32, "expert_offsets", 1)
-        if expert_offsets.shape[0] != E + 1:
-            raise ValueError(f"expert_offsets must hold E + 1 = {E + 1} values")
-        op = expert_offsets.data_ptr()
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in _DTYPES:
         raise TypeError(f"out must be bfloat16, float16 or float32, got {out_dtype}")
-    out = _mx_out(out, (R, N), out_dtype, dev, "out")
-    L = lib()
-    wp, nbytes = None, 0
-    if workspace is None:
-        nbytes = _mx_product_bytes(R, K, N, E)
-        if nbytes:
-            workspace = _empty(nbytes, dtype=_U8, device=dev)
-            wp = workspace.data_ptr()
-    else:
-        _need(workspace, _U8, "workspace")
-        wp, nbytes = workspace.data_ptr(), workspace.numel()
-    _check(L.moe_mx_product(a.data_ptr(), a_scale.data_ptr(), a_bits, R, K, N, E, w.data_ptr(),
-                            w_scale.data_ptr(), op, out.data_ptr(), _DTYPES[out_dtype], wp,
-                            nbytes, _mx_stream(a)))
-    return out
+    return (_mx or _mx_binding()).product(a, a_scale, w, w_scale, expert_offsets, a_bits, out,
+                                          _DTYPES[out_dtype], workspace)
 
 
 def moe_mx_forward_workspace(T, H, I, E, k, a_bits=8) -> int:
-    return lib().moe_mx_forward_workspace(T, H, I, E, k, a_bits)
-
-
-_mx_forward_bytes = functools.lru_cache(maxsize=1024)(moe_mx_forward_workspace)
+    return int(lib().moe_mx_forward_workspace(T, H, I, E, k, a_bits))
 
 
 def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out=None,
@@ -724,32 +561,9 @@ def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out
         with torch.cuda.stream(stream):
             return moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits, out,
                                   out_dtype, workspace)
-    (T, _), H = _mx_codes(a, a_scale, a_bits, "a", 2)
-    (E, n13, _), k13 = _mx_codes(w13, s13, 4, "w13", 3)
-    (e2, n2, _), I = _mx_codes(w2, s2, 4, "w2", 3)
-    if k13 != H or n2 != H or n13 != 2 * I or e2 != E:
-        raise ValueError("w13 must be [E, 2I, H] and w2 [E, H, I]")
-    _need(topk_w, _F32, "topk_w", 2)
-    _need(topk_ids, _I32, "topk_ids", 2)
-    t2, k = topk_ids.shape
-    if t2 != T or topk_w.shape != topk_ids.shape:
-        raise ValueError(f"topk_w and topk_ids must be [{T}, k]")
-    _mx_together(a, w13=w13, w2=w2, topk_w=topk_w, topk_ids=topk_ids, workspace=workspace)
-    dev = a.device
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in _HALVES:
         raise TypeError(f"out must be bfloat16 or float16, got {out_dtype}")
-    out = _mx_out(out, (T, H), out_dtype, dev, "out")
-    L = lib()
-    if workspace is None:
-        nbytes = max(_mx_forward_bytes(T, H, I, E, k, a_bits), 16)
-        workspace = _empty(nbytes, dtype=_U8, device=dev)
-    else:
-        _need(workspace, _U8, "workspace")
-        nbytes = workspace.numel()
-    _check(L.moe_mx_forward(
-        a.data_ptr(), a_scale.data_ptr(), a_bits, T, H, I, E, k, w13.data_ptr(), s13.data_ptr(),
-        w2.data_ptr(), s2.data_ptr(), topk_w.data_ptr(), topk_ids.data_ptr(), out.data_ptr(),
-        _DTYPES[out_dtype], workspace.data_ptr(), nbytes, _mx_stream(a)))
-    return out
+    return (_mx or _mx_binding()).forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits,
+                                          out, _DTYPES[out_dtype], workspace)

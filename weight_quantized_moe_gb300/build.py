@@ -1,7 +1,9 @@
-"""Build libmoeq.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Build libmoeq.so (the C-ABI library) in-tree with nvcc for sm_103a, and
+_mx_binding.so (the compiled Python calls of the microscaled operators).
 
 Every ``csrc/*.cu`` is compiled to an object in parallel, then linked into
-``weight_quantized_moe_gb300/libmoeq.so``.  No fast-math: the quantisers
+``weight_quantized_moe_gb300/libmoeq.so``; ``pysrc/mx_binding.cpp`` is compiled
+beside them with the host compiler against torch's headers and linked to it.  No fast-math: the quantisers
 rely on IEEE division and denormals.
 """
 
@@ -13,12 +15,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoeq.so")
+PYSRC = os.path.join(PKG, "pysrc", "mx_binding.cpp")
+PYEXT = os.path.join(PKG, "_mx_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",
@@ -38,18 +43,64 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        os.path.join(ROOT, "include", "moeq.h"), os.path.abspath(__file__)]
+        os.path.join(ROOT, "include", "moeq.h"), os.path.abspath(__file__), PYSRC]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(PYEXT):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(PYEXT))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _cxx() -> str:
+    for cand in (os.environ.get("CXX"), shutil.which("g++"), shutil.which("c++")):
+        if cand:
+            return cand
+    raise RuntimeError("g++ not found: a C++ compiler is required to build _mx_binding.so")
+
+
+def _torch_dirs():
+    """(torch's include directories, torch's library directory)."""
+    import torch
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    inc = os.path.join(base, "include")
+    return ([inc, os.path.join(inc, "torch", "csrc", "api", "include")],
+            os.path.join(base, "lib"))
+
+
+def _run(cmd, what, verbose=False):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stderr}")
+    if verbose and r.stderr:
+        sys.stderr.write(r.stderr)
+
+
+def _compile_binding() -> str:
+    import torch
+    obj = os.path.join(BUILD, "mx_binding.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    system = [*_torch_dirs()[0], cuda, sysconfig.get_path("include")]
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    _run([_cxx(), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", os.path.join(ROOT, "include"),
+          *[a for d in system for a in ("-isystem", d)], "-c", PYSRC, "-o", obj],
+         "compiling mx_binding.cpp")
+    return obj
+
+
+def _link_binding(obj) -> None:
+    lib_dir = _torch_dirs()[1]
+    tmp = PYEXT + ".tmp"
+    _run([_cxx(), "-shared", "-o", tmp, obj, "-L", PKG, "-lmoeq", "-L", lib_dir, "-ltorch_python",
+          "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib_dir}"],
+         "linking _mx_binding.so")
+    os.replace(tmp, PYEXT)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libmoeq.so; returns its path."""
+    """Compile and link libmoeq.so and _mx_binding.so; returns the library's path."""
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()
@@ -59,21 +110,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stderr}")
-        if verbose and r.stderr:
-            sys.stderr.write(r.stderr)
+        _run(cmd, f"nvcc on {os.path.basename(src)}", verbose)
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding = binding.result()
     tmp = LIB + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
+    _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], "link")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 
