@@ -773,6 +773,7 @@ MQ_EXPORT int moe_mx_product(const uint8_t* a, const uint8_t* a_scale, int a_bit
   g.epi = pl.splits > 1 ? MX_EPI_PART : MX_EPI_OUT;
   g.a = a; g.a_scale = a_scale; g.w = w; g.w_scale = w_scale;
   g.R = R; g.S = R; g.E = E; g.K = K; g.N = N; g.wrows = N;
+  g.weight_bytes = (int64_t)std::min<int64_t>(E, R) * N * K / 2;
   g.seg_start = expert_offsets;
   g.out = out; g.out_dtype = out_dtype;
   g.part = static_cast<float*>(workspace); g.part_rows = R;
@@ -883,6 +884,7 @@ MQ_EXPORT int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bit
   MxGemm g = {};
   g.a_bits = a_bits;
   g.R = L.cap; g.S = S; g.E = E;
+  g.weight_bytes = (int64_t)std::min<int64_t>(E, S) * 3 * H * I / 2;
   g.seg_start = offsets; g.seg_count = small ? nullptr : counts;
   g.status = status;
   g.epi = MX_EPI_GATED;

@@ -232,6 +232,7 @@ struct MxGemm {
   int64_t R;                  // rows of a
   int64_t S;                  // live rows at most (the plan's estimate)
   int E, K, N, wrows;         // N outputs; wrows = N, or 2 N when gated
+  int64_t weight_bytes;       // codes of the weights that the call can reach (a forward: both products')
   const int32_t* seg_start;   // first row of each expert (null: one expert, all rows)
   const int32_t* seg_count;   // rows of each expert (null: seg_start[e + 1] - seg_start[e])
   void* out;                  // MX_EPI_OUT: [R, N]

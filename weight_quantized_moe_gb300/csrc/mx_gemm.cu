@@ -132,6 +132,7 @@ struct Params {
   int up_row;     // weight row of a unit's second load, relative to its first
   int wrows;
   int mtiles, splits, words, sbs;
+  bool evict_first;  // L2 policy of weights that are read once
   void* out;
   int out_dtype;
   float* part;
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int a = 0; a < kTiles; ++a) {
               const int row = w.m + a * p.up_row;
-              if (w.single)
+              if (w.single && p.evict_first)
                 tma_load_3d_hint(dst + a * kABytes, &map_w, &ctl->full[slot], s * 128, row, w.e, pol_once);
               else
                 tma_load_3d(dst + a * kABytes, &map_w, &ctl->full[slot], s * 128, row, w.e);
@@ -924,6 +925,15 @@ cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStream_t st) {
   p.mtiles = (g.N + p.mrows - 1) / p.mrows;
   p.splits = pl.splits;
   p.words = g.K / 128;
+  // Weights that are read once leave L2 first, so that more of it is left for
+  // the rest, and for weights of an earlier call that reads little.  Not so with
+  // 8-bit rows where a call may read several times L2: their loads take 64 bytes
+  // of the 256 that L2 fetches, and those have to last until the next stages take
+  // the others.  In us, evict-first and normal: E=8 k=2 H=4096 I=14336 forward at
+  // T=1 47 and 53, T=2 70 and 75, T=4 100 and 98, T=8 135 and 128, T=64 143 and 138;
+  // 128 rows, K=4096, N=28672 83.8 and 81.8, K=14336, N=4096 45.0 and 47.4; E=128
+  // T=64 69.7 and 74.5.
+  p.evict_first = g.a_bits == 4 || g.weight_bytes < int64_t(400) << 20;
   p.sbs = (p.words + 3) / 4;
   p.out = g.out;
   p.out_dtype = g.out_dtype;
