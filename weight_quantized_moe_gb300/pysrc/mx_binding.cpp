@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include "moeq.h"
@@ -147,9 +148,14 @@ at::Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const
   return t;
 }
 
-void* stream_of(const at::Tensor& t) {
-  return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
-}
+// Makes the tensors' device current for the rest of a call: the library plans,
+// launches and finds its status word on the current device.
+struct OnDevice {
+  c10::cuda::CUDAGuard guard;
+  void* stream;  // that device's current stream
+  explicit OnDevice(const at::Tensor& t)
+      : guard(t.device()), stream(c10::cuda::getCurrentCUDAStream(t.get_device()).stream()) {}
+};
 
 // Shapes of the codes and scales of rows.
 void code_shapes(const at::Tensor& x, int bits, c10::SmallVector<int64_t, 5>& q,
@@ -202,16 +208,16 @@ PyObject* quantize(PyObject* const* a) {
   if (dt < 0)
     raise(PyExc_TypeError, "x must be bfloat16, float16 or float32, got %s", c10::toString(x.scalar_type()));
   on_cuda(x, "x");
+  const OnDevice on(x);
   const int bits = bits_of(a[1]);
   c10::SmallVector<int64_t, 5> qs, ss;
   code_shapes(x, bits, qs, ss);
   const int64_t cols = x.size(-1), stride = row_stride(x, "x");
   const at::Tensor q = output(a[2], qs, at::kByte, x, "q");
   const at::Tensor s = output(a[3], ss, at::kByte, x, "scale");
-  void* st = stream_of(x);
   check(call([&] {
     return moe_quantize_mx(x.data_ptr(), dt, x.numel() / cols, cols, stride, bits, bytes(q),
-                           bytes(s), st);
+                           bytes(s), on.stream);
   }));
   return wrap_all({q, s});
 }
@@ -222,14 +228,14 @@ PyObject* dequantize(PyObject* const* a) {
   int64_t cols;
   const uint8_t* scale;
   const at::Tensor& q = codes(a[0], a[1], bits, -1, "q", "scale", cols, scale);
+  const OnDevice on(q);
   const long dt = as_long(a[3]);
   c10::SmallVector<int64_t, 5> shape(q.sizes().begin(), q.sizes().end());
   shape.back() = cols;
   const at::Tensor out = output(a[4], shape, scalar_type(dt), q, "out");
-  void* st = stream_of(q);
   check(call([&] {
     return moe_dequantize_mx(bytes(q), scale, out.numel() / cols, cols, bits, out.data_ptr(),
-                             (int)dt, st);
+                             (int)dt, on.stream);
   }));
   return wrap(out);
 }
@@ -241,6 +247,7 @@ PyObject* rmsnorm(PyObject* const* a) {
   if (xt != at::kBFloat16 && xt != at::kHalf)
     raise(PyExc_TypeError, "x must be bfloat16 or float16, got %s", c10::toString(xt));
   on_cuda(x, "x");
+  const OnDevice on(x);
   if (x.dim() != 2) raise(PyExc_ValueError, "x must have 2 dims");
   const int64_t T = x.size(0), H = x.size(1);
   const bool wf = THPVariable_Check(a[1]) && THPVariable_Unpack(a[1]).scalar_type() == at::kFloat;
@@ -271,11 +278,10 @@ PyObject* rmsnorm(PyObject* const* a) {
   const at::Tensor q = output(a[8], qs, at::kByte, x, "q");
   const at::Tensor s = output(a[9], ss, at::kByte, x, "scale");
   if (T > INT32_MAX || H > INT32_MAX) raise(PyExc_ValueError, "x is too large");
-  void* st = stream_of(x);
   check(call([&] {
     return moe_rmsnorm_mx(x.data_ptr(), rp, weight.data_ptr(), dtype_code(xt), wf, (int)T, (int)H,
                           xst, rst, (float)eps, ro.defined() ? ro.data_ptr() : nullptr,
-                          y.defined() ? y.data_ptr() : nullptr, bits, bytes(q), bytes(s), st);
+                          y.defined() ? y.data_ptr() : nullptr, bits, bytes(q), bytes(s), on.stream);
   }));
   return wrap_all({q, s, ro, y});
 }
@@ -298,6 +304,7 @@ PyObject* product(PyObject* const* v) {
   int64_t K, wk;
   const uint8_t *as, *ws;
   const at::Tensor& a = codes(v[0], v[1], bits, 2, "a", "a_scale", K, as);
+  const OnDevice on(a);
   const at::Tensor& w = codes(v[2], v[3], 4, -1, "w", "w_scale", wk, ws);
   same_device(w, a, "w");
   if (wk != K) raise(PyExc_ValueError, "a and w must have rows of the same length");
@@ -315,11 +322,10 @@ PyObject* product(PyObject* const* v) {
   const at::Tensor out = output(v[6], {R, N}, scalar_type(dt), a, "out");
   const at::Tensor wksp =
       workspace(v[8], v[8] == Py_None ? moe_mx_product_workspace(R, (int)K, (int)N, (int)E) : 0, a);
-  void* st = stream_of(a);
   check(call([&] {
     return moe_mx_product(bytes(a), as, bits, R, (int)K, (int)N, (int)E, bytes(w), ws, offsets,
                           out.data_ptr(), (int)dt, wksp.defined() ? wksp.data_ptr() : nullptr,
-                          wksp.defined() ? (size_t)wksp.numel() : 0, st);
+                          wksp.defined() ? (size_t)wksp.numel() : 0, on.stream);
   }));
   return wrap(out);
 }
@@ -330,6 +336,7 @@ PyObject* forward(PyObject* const* v) {
   int64_t H, k13, I;
   const uint8_t *as, *s13, *s2;
   const at::Tensor& a = codes(v[0], v[1], bits, 2, "a", "a_scale", H, as);
+  const OnDevice on(a);
   const at::Tensor& w13 = codes(v[2], v[3], 4, 3, "w13", "s13", k13, s13);
   const at::Tensor& w2 = codes(v[4], v[5], 4, 3, "w2", "s2", I, s2);
   const int64_t T = a.size(0), E = w13.size(0);
@@ -351,12 +358,11 @@ PyObject* forward(PyObject* const* v) {
           ? std::max<size_t>(16, moe_mx_forward_workspace((int)T, (int)H, (int)I, (int)E, (int)k, bits))
           : 0,
       a);
-  void* st = stream_of(a);
   check(call([&] {
     return moe_mx_forward(bytes(a), as, bits, (int)T, (int)H, (int)I, (int)E, (int)k, bytes(w13), s13,
                           bytes(w2), s2, static_cast<const float*>(tw.data_ptr()),
                           static_cast<const int32_t*>(ids.data_ptr()), out.data_ptr(), (int)dt,
-                          wksp.data_ptr(), (size_t)wksp.numel(), st);
+                          wksp.data_ptr(), (size_t)wksp.numel(), on.stream);
   }));
   return wrap(out);
 }
