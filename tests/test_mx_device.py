@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from mx_fake_device import compile_fake
+from weight_quantized_moe_gb300 import binding
 
 
 @pytest.fixture(scope="module")
@@ -60,3 +61,49 @@ def test_a_refused_call_leaves_the_device_as_it_was(fake, name):
     with pytest.raises((TypeError, ValueError)):
         getattr(calls, name)(*args)
     assert pretend.calls() == ([], 0)
+
+
+class Stream:
+    """Enough of a stream to be told apart by its device."""
+
+    def __init__(self, device):
+        self.device = torch.device("cuda", device)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_stream_of_another_device_is_refused(fake, monkeypatch, name):
+    """It would not be used: the call runs on its tensors' device."""
+    calls, pretend = fake
+    pretend.calls()
+    entered = []
+
+    class Current:
+        def __init__(self, stream):
+            entered.append(stream.device.index)
+
+        def __enter__(self):
+            pass
+
+        def __exit__(self, *exc):
+            pass
+
+    monkeypatch.setattr(torch.cuda, "stream", Current)
+    monkeypatch.setattr(binding, "_mx", calls)
+    keep = []
+
+    def on(t):
+        keep.append(t)
+        return pretend.on_device(t, 1)
+    args = arguments(on)[name]
+    call = {
+        "quantize": lambda st: binding.moe_quantize_mx(*args, stream=st),
+        "dequantize": lambda st: binding.moe_dequantize_mx(*args[:3], out=args[4], stream=st),
+        "rmsnorm": lambda st: binding.moe_rmsnorm_mx(*args, stream=st),
+        "product": lambda st: binding.moe_mx_product(*args[:7], workspace=args[8], stream=st),
+        "forward": lambda st: binding.moe_mx_forward(*args[:10], workspace=args[11], stream=st),
+    }[name]
+    with pytest.raises(ValueError, match="stream must be on cuda:1"):
+        call(Stream(0))
+    assert pretend.calls() == ([], 0) and not entered
+    call(Stream(1))
+    assert pretend.calls() == ([(1, 101)], 0) and entered == [1]

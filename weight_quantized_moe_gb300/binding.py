@@ -489,6 +489,14 @@ def _mx_binding():
     return _mx
 
 
+def _given(stream, t):
+    """The context that makes a given stream current; a stream of another
+    device than the tensors' is refused."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and stream.device != t.device:
+        raise ValueError(f"stream must be on {t.device}, the tensors' device, not {stream.device}")
+    return torch.cuda.stream(stream)
+
+
 def moe_quantize_mx(x, bits=4, q=None, scale=None, stream=None):
     """bf16 / f16 / float32 [..., K] -> MX codes uint8 [..., K * bits / 8] (8
     bits: E4M3 bytes; 4 bits: two E2M1 codes per byte, even element low) and
@@ -497,7 +505,7 @@ def moe_quantize_mx(x, bits=4, q=None, scale=None, stream=None):
     With stream=, here and in the other moe_*_mx* calls, the call runs with
     that stream current: what it allocates belongs to the stream that uses it."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _given(stream, x):
             return moe_quantize_mx(x, bits, q, scale)
     return (_mx or _mx_binding()).quantize(x, bits, q, scale)
 
@@ -506,7 +514,7 @@ def moe_dequantize_mx(q, scale, bits=4, dtype=torch.bfloat16, out=None, stream=N
     """The values [..., K] that MX codes and scales stand for, in dtype (bf16,
     f16 or float32)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _given(stream, q):
             return moe_dequantize_mx(q, scale, bits, dtype, out)
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
@@ -520,7 +528,7 @@ def moe_rmsnorm_mx(x, weight, eps=1e-6, residual=None, bits=8, want_y=False, res
     weight [H] of the same dtype or float32 -> (q, scale, x + residual or None,
     the normed rows or None).  residual_out may be residual (in place)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _given(stream, x):
             return moe_rmsnorm_mx(x, weight, eps, residual, bits, want_y, residual_out, y, q, scale)
     return (_mx or _mx_binding()).rmsnorm(x, weight, eps, residual, bits, want_y, residual_out, y,
                                           q, scale)
@@ -537,7 +545,7 @@ def moe_mx_product(a, a_scale, w, w_scale, expert_offsets=None, a_bits=8, out=No
     float32).  Without expert_offsets w is [N, K] (or [1, N, K]): a dense
     product."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _given(stream, a):
             return moe_mx_product(a, a_scale, w, w_scale, expert_offsets, a_bits, out, out_dtype,
                                   workspace)
     if out is not None:
@@ -558,7 +566,7 @@ def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out
     (moe_mx_forward in include/moeq.h): a [T, H] with a_bits, w13 [E, 2I, H], w2
     [E, H, I], topk_w / topk_ids [T, k] -> [T, H] bf16 or f16."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _given(stream, a):
             return moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits, out,
                                   out_dtype, workspace)
     if out is not None:
