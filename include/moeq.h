@@ -441,12 +441,15 @@ int moe_dequantize_mx(const uint8_t* q, const uint8_t* scale, int64_t rows, int6
  * h.  x [T, H] with x_stride elements between rows; residual [T, H] with
  * residual_stride, or NULL (h = x); weight [H] in dtype, or float32 with
  * weight_f32 != 0.  residual_out and y_out are dense [T, H] in dtype, or NULL.
- * residual_out may be residual or x itself where that is dense.
+ * residual_out and y_out may each be residual or x itself where that is dense
+ * (or T is 1); otherwise the outputs share no memory with the inputs or with one
+ * another.
  * Limits: dtype bf16 or f16, H a multiple of 32 up to 32768.
  * Errors: MQ_ERR_INVALID_ARG for T < 0, H not a positive multiple of 32,
  * strides below H or not multiples of 8, an unknown dtype or bits, eps
- * negative or not finite, null or misaligned pointers; MQ_ERR_UNSUPPORTED for
- * float32 rows or H above the limit.
+ * negative or not finite, null or misaligned pointers, residual_out or y_out over
+ * rows of x or residual in another place or over one another;
+ * MQ_ERR_UNSUPPORTED for float32 rows or H above the limit.
  */
 int moe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int dtype,
                    int weight_f32, int T, int H, int64_t x_stride, int64_t residual_stride,

@@ -106,3 +106,38 @@ def test_binding_refusals(lib):
         b.moe_mx_forward(x, x, x, x, x, x, x, x, out_dtype=torch.float32)
     with pytest.raises(TypeError):
         b.moe_quantize_mx([1.0])
+
+
+def test_rmsnorm_mx_outputs_may_not_share_memory_with_other_rows(lib):
+    """A row's output over another row's input is written while that row may not
+    have been read: refused, for both outputs and both inputs."""
+    base = 0x100000
+    T, H = 4, 64
+    row = 2 * H     # bytes
+
+    def refused(**k):
+        rc = n_checked(**k)
+        return rc == 1 and b"share" in lib.mq_last_error_message()
+
+    def n_checked(x=base, res=None, ro=None, y=None, xs=H, rs=H, T=T):
+        p = lambda v: None if v is None else vp(v)  # noqa: E731
+        # (the weight is misaligned: a call whose rows pass is refused for that)
+        return lib.moe_rmsnorm_mx(p(x), p(res), ODD, BF16, 0, T, H, xs, rs, 1e-6, p(ro), p(y), 8, P, P, None)
+    far = base + 0x80000
+    for out in ("y", "ro"):
+        assert refused(**{out: base, "xs": 2 * H})                     # dense rows over strided ones
+        assert refused(**{out: base + row})                            # the same rows, one on
+        assert refused(**{out: base - row})
+        assert refused(**{out: base + 16, "xs": 2 * H})                # across a gap
+        assert refused(x=far, res=base, **{out: base, "rs": H + 64})
+        assert refused(x=far, res=base, **{out: base + (T - 1) * row})
+        # in place, between the rows, before and behind them: not refused for this
+        assert not refused(**{out: base})
+        assert not refused(x=far, res=base, **{out: base})
+        assert not refused(**{out: base + T * row})
+        assert not refused(**{out: base - T * row})
+        assert not refused(**{out: base + row, "xs": (T + 1) * H})     # all of it in one gap
+        assert refused(**{out: base + row + 16, "xs": (T + 1) * H})
+        assert not refused(**{out: base, "xs": 2 * H, "T": 1})         # a single row has no stride
+    assert refused(y=base + row, ro=base, x=far)                       # the outputs on one another
+    assert not refused(y=base + T * row, ro=base, x=far)

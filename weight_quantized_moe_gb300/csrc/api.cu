@@ -689,6 +689,18 @@ MQ_EXPORT int moe_dequantize_mx(const uint8_t* q, const uint8_t* scale, int64_t 
   return err == cudaSuccess ? MQ_OK : cuda_fail(err, "dequantize_mx launch");
 }
 
+// Whether T dense 16-bit rows at `out` reach into T such rows `stride` elements
+// apart at `in`, other than as the very same rows: another CTA may read there
+// after the write.
+static bool rows_clash(const void* out, const void* in, int T, int H, int64_t stride) {
+  if (!out || !in || (out == in && (stride == H || T == 1))) return false;
+  const int64_t o = (int64_t)reinterpret_cast<uintptr_t>(out);
+  const int64_t i = (int64_t)reinterpret_cast<uintptr_t>(in);
+  const int64_t row = 2 * (int64_t)H, step = 2 * stride;
+  const int64_t r = o < i + row ? 0 : (o - i - row) / step + 1;  // first row that ends behind out
+  return r < T && i + r * step < o + T * row;
+}
+
 MQ_EXPORT int moe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int dtype,
                              int weight_f32, int T, int H, int64_t x_stride,
                              int64_t residual_stride, float eps, void* residual_out, void* y_out,
@@ -705,13 +717,16 @@ MQ_EXPORT int moe_rmsnorm_mx(const void* x, const void* residual, const void* we
     return fail(MQ_ERR_INVALID_ARG, "row strides must be multiples of 8, at least H");
   if (T == 0) return MQ_OK;
   if (!x || !weight || !q || !scale) return fail(MQ_ERR_INVALID_ARG, "null pointer");
+  for (const void* out : {residual_out, y_out})
+    if (rows_clash(out, x, T, H, x_stride) || rows_clash(out, residual, T, H, residual_stride))
+      return fail(MQ_ERR_INVALID_ARG,
+                  "residual_out and y_out may share memory with x or residual only as the same dense rows");
+  if (rows_clash(y_out, residual_out, T, H, H))
+    return fail(MQ_ERR_INVALID_ARG, "residual_out and y_out share memory");
   if (!aligned16(x) || (residual && !aligned16(residual)) || !aligned16(weight) ||
       (residual_out && !aligned16(residual_out)) || (y_out && !aligned16(y_out)) ||
       !aligned16(q) || !aligned4(scale))
     return fail(MQ_ERR_INVALID_ARG, "pointers must be 16-byte aligned, scale 4-byte");
-  if ((residual_out == x && x_stride != H) ||
-      (residual_out && residual_out == residual && residual_stride != H))
-    return fail(MQ_ERR_INVALID_ARG, "residual_out may be x or residual only where that is dense");
   NormArgs a;
   a.x = x; a.residual = residual; a.weight = weight;
   a.dtype = dtype; a.weight_f32 = weight_f32 ? 1 : 0;
