@@ -43,14 +43,26 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        os.path.join(ROOT, "include", "moeq.h"), os.path.abspath(__file__), PYSRC]
+        os.path.join(ROOT, "include", "moeq.h"), os.path.abspath(__file__)]
+
+
+def _newer(made, sources) -> bool:
+    if not os.path.exists(made):
+        return False
+    t = os.path.getmtime(made)
+    return all(os.path.getmtime(p) <= t for p in sources)
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def _binding_up_to_date() -> bool:
+    return _newer(PYEXT, [PYSRC, os.path.join(ROOT, "include", "moeq.h"), os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(PYEXT):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(PYEXT))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _library_up_to_date() and _binding_up_to_date()
 
 
 def _cxx() -> str:
@@ -100,12 +112,14 @@ def _link_binding(obj) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libmoeq.so and _mx_binding.so; returns the library's path."""
-    if not force and up_to_date():
+    """Compile and link libmoeq.so and _mx_binding.so, whichever is out of date;
+    returns the library's path.  The library needs nvcc only: it is linked before
+    anything that is missing for the binding (a C++ compiler, torch) raises."""
+    library = force or not _library_up_to_date()
+    bind = force or not _binding_up_to_date()
+    if not library and not bind:
         return LIB
-    nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
-    srcs = _sources()
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
@@ -114,13 +128,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(compile_one, srcs))
-        binding = binding.result()
-    tmp = LIB + ".tmp"
-    _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], "link")
-    os.replace(tmp, LIB)
-    _link_binding(binding)
+        binding = ex.submit(_compile_binding) if bind else None
+        if library:
+            nvcc = _nvcc()
+            objs = list(ex.map(compile_one, _sources()))
+            tmp = LIB + ".tmp"
+            _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], "link")
+            os.replace(tmp, LIB)
+        if bind:
+            _link_binding(binding.result())
     return LIB
 
 
