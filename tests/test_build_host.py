@@ -46,3 +46,18 @@ def test_build_makes_both_once(sandbox):
     first = len(sandbox)
     build.build()
     assert len(sandbox) == first
+
+
+def test_binding_is_made_again_for_another_torch(sandbox, monkeypatch):
+    """A binding belongs to the torch (and Python) that it was compiled against."""
+    import torch
+    build.build()
+    first = len(sandbox)
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    assert not build.up_to_date()
+    build.build()
+    assert build.up_to_date()
+    again = sandbox[first:]
+    assert again and all("binding" in what for what in again)   # the library stays
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: ".cpython-0.so")
+    assert not build.up_to_date()

@@ -57,8 +57,24 @@ def _library_up_to_date() -> bool:
     return _newer(LIB, _deps())
 
 
+def _binding_stamp() -> str:
+    """What a binding was compiled against: it fits no other torch or Python."""
+    import torch
+    return f"torch {torch.__version__} python {sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
+def _stamp_path() -> str:
+    return os.path.join(BUILD, "mx_binding.stamp")
+
+
 def _binding_up_to_date() -> bool:
-    return _newer(PYEXT, [PYSRC, os.path.join(ROOT, "include", "moeq.h"), os.path.abspath(__file__)])
+    if not _newer(PYEXT, [PYSRC, os.path.join(ROOT, "include", "moeq.h"), os.path.abspath(__file__)]):
+        return False
+    try:
+        with open(_stamp_path()) as f:
+            return f.read() == _binding_stamp()
+    except (OSError, ImportError):
+        return False
 
 
 def up_to_date() -> bool:
@@ -109,6 +125,8 @@ def _link_binding(obj) -> None:
           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib_dir}"],
          "linking _mx_binding.so")
     os.replace(tmp, PYEXT)
+    with open(_stamp_path(), "w") as f:
+        f.write(_binding_stamp())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
