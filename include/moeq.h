@@ -419,7 +419,7 @@ int moe_quant_forward_noalloc(const void* x, int T, int H, int I, int E, int k,
  * Errors: MQ_ERR_INVALID_ARG for an unknown dtype or bits, rows < 0, cols not a
  * positive multiple of 32, row_stride below cols or not a multiple of 8, null
  * or misaligned pointers (x, q: 16 bytes; scale: 4); MQ_ERR_UNSUPPORTED for
- * more than 2^40 elements.
+ * more than 2^40 elements, or strided rows of 2^35 or more.
  */
 int moe_quantize_mx(const void* x, int dtype, int64_t rows, int64_t cols, int64_t row_stride,
                     int bits, uint8_t* q, uint8_t* scale, void* stream);

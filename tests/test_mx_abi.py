@@ -141,3 +141,18 @@ def test_rmsnorm_mx_outputs_may_not_share_memory_with_other_rows(lib):
         assert not refused(**{out: base, "xs": 2 * H, "T": 1})         # a single row has no stride
     assert refused(y=base + row, ro=base, x=far)                       # the outputs on one another
     assert not refused(y=base + T * row, ro=base, x=far)
+
+
+def test_quantize_mx_strided_rows_past_the_kernels_row_count_are_refused(lib):
+    """Strided rows are found by dividing by the row's vectors of eight, counted in
+    32 bits; rows of 2^35 elements have more.  (Refused before anything is
+    launched; dense ones need no division.)"""
+    def q(cols, st, rows=2, x=P):
+        # (the scale is misaligned: a call whose sizes pass is refused for that)
+        rc = lib.moe_quantize_mx(x, BF16, rows, cols, st, 4, P, vp(0x1002), None)
+        return rc
+    assert q(1 << 35, (1 << 35) + 8) == 2
+    assert q(1 << 36, 1 << 37, rows=1) == 2
+    assert b"dense" in lib.mq_last_error_message()
+    assert q(1 << 35, 1 << 35) == 1
+    assert q((1 << 35) - 32, 1 << 35) == 1

@@ -668,6 +668,8 @@ static int mx_args(const void* x, int dtype, int64_t rows, int64_t cols, int bit
 MQ_EXPORT int moe_quantize_mx(const void* x, int dtype, int64_t rows, int64_t cols,
                               int64_t row_stride, int bits, uint8_t* q, uint8_t* scale,
                               void* stream) {
+  if (row_stride != cols && cols >= int64_t(1) << 35)  // (the kernel's vectors per row: 32 bits)
+    return fail(MQ_ERR_UNSUPPORTED, "rows of 2^35 elements or more must be dense");
   const int rc = mx_args(x, dtype, rows, cols, bits, q, scale);
   if (rc != MQ_OK) return rc;
   if (row_stride < cols || row_stride % 8)
