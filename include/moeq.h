@@ -468,7 +468,8 @@ int moe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int 
  * with one final rounding; a result is the same on every run.
  * The workspace holds float32 partial sums where K is split (few units of
  * work); moe_mx_product_workspace may return 0 (workspace may then be NULL).
- * Limits: K a multiple of 128, N >= 1, E <= 1024, R < 2^30, R * N < 2^39.
+ * Limits: K a multiple of 128, N >= 1, E <= 1024, R < 2^30, R * N < 2^39, K and N
+ * at most 2^31 - 512.
  * Errors: MQ_ERR_INVALID_ARG, MQ_ERR_UNSUPPORTED (limits), MQ_ERR_WORKSPACE.
  */
 size_t moe_mx_product_workspace(int64_t R, int K, int N, int E);
@@ -488,7 +489,7 @@ int moe_mx_product(const uint8_t* a, const uint8_t* a_scale, int a_bits, int64_t
  * f16.  h, the activation and the sums are float32; b is the one further
  * rounding.  An id outside [0, E) sets MQ_DEV_BAD_EXPERT_ID and its slot is
  * left out.  Limits and errors as moe_quant_forward (H % 128 == 0, I % 128 ==
- * 0, E <= 1024, k <= min(E, 32)); a_bits 8 or 4.
+ * 0, E <= 1024, k <= min(E, 32)), H < 2^28, I <= 2^30 - 256; a_bits 8 or 4.
  */
 size_t moe_mx_forward_workspace(int T, int H, int I, int E, int k, int a_bits);
 int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bits, int T, int H, int I,

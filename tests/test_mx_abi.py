@@ -156,3 +156,23 @@ def test_quantize_mx_strided_rows_past_the_kernels_row_count_are_refused(lib):
     assert b"dense" in lib.mq_last_error_message()
     assert q(1 << 35, 1 << 35) == 1
     assert q((1 << 35) - 32, 1 << 35) == 1
+
+
+def test_mx_sizes_whose_rounded_up_values_pass_32_bits_are_refused(lib):
+    """The product counts weight rows in tiles of 256 past its last one, k in
+    steps of 512; a forward has 2I weight rows and rows of H * a_bits bits."""
+    top = (1 << 31) - 1
+
+    # (a is misaligned: a call whose sizes pass is refused for that)
+    def p(K=128, N=64):
+        return lib.moe_mx_product(ODD, P, 8, 1, K, N, 1, P, P, None, P, BF16, None, 0, None)
+    assert p(N=top) == 2 and p(N=top - 510) == 2 and p(N=top - 511) == 1
+    assert p(K=(1 << 31) - 128) == 2 and p(K=(1 << 31) - 384) == 2 and p(K=(1 << 31) - 512) == 1
+    for K, N in ((128, top), ((1 << 31) - 128, 64)):
+        assert lib.moe_mx_product_workspace(1, K, N, 1) == 0
+
+    def f(H=128, I=128, bits=8, T=1):
+        return lib.moe_mx_forward(ODD, P, bits, T, H, I, 1, 1, P, P, P, P, P, P, P, BF16, P, 1 << 62, None)
+    assert f(I=1 << 30) == 2 and f(I=(1 << 30) + 128) == 2 and f(I=(1 << 31) - 128) == 2
+    assert f(H=1 << 28) == 2 and f(H=(1 << 31) - 128) == 2
+    assert f(I=(1 << 30) - 128) == 2 and f(I=(1 << 30) - 256) == 1 and f(H=(1 << 28) - 128) == 1

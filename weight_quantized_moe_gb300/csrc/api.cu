@@ -745,13 +745,16 @@ MQ_EXPORT int moe_rmsnorm_mx(const void* x, const void* residual, const void* we
 
 // The kernels count their units of work (at most 16 K splits of 16 rows by 256
 // outputs) in 32 bits.
-static bool mx_units_ok(int64_t rows, int N, int E) {
-  return (rows / 16 + E) * (((int64_t)N + 255) / 256) < (int64_t(1) << 27);
+static bool mx_units_ok(int64_t rows, int64_t N, int E) {
+  return (rows / 16 + E) * ((N + 255) / 256) < (int64_t(1) << 27);
 }
+
+// Weight rows and k are rounded up to 256 and 512 in 32 bits.
+static bool mx_rounds_up(int64_t n) { return n <= INT32_MAX - 511; }
 
 static bool mx_product_sizes_ok(int64_t R, int K, int N, int E) {
   return R >= 0 && K > 0 && N > 0 && E >= 1 && K % 128 == 0 && E <= 1024 &&
-         R < (int64_t(1) << 30) && mx_units_ok(R, N, E);
+         R < (int64_t(1) << 30) && mx_rounds_up(K) && mx_rounds_up(N) && mx_units_ok(R, N, E);
 }
 
 MQ_EXPORT size_t moe_mx_product_workspace(int64_t R, int K, int N, int E) {
@@ -769,7 +772,7 @@ MQ_EXPORT int moe_mx_product(const uint8_t* a, const uint8_t* a_scale, int a_bit
   if (a_bits != 4 && a_bits != 8) return fail(MQ_ERR_INVALID_ARG, "a_bits must be 4 or 8");
   if (!dtype_ok(out_dtype)) return fail(MQ_ERR_INVALID_ARG, "unknown out_dtype %d", out_dtype);
   if (!mx_product_sizes_ok(R, K, N, E))
-    return fail(MQ_ERR_UNSUPPORTED, "need K %% 128 == 0, E <= 1024, R < 2^30 and R * N < 2^39");
+    return fail(MQ_ERR_UNSUPPORTED, "need K %% 128 == 0, E <= 1024, R < 2^30, K and N <= 2^31 - 512 and R * N < 2^39");
   if (!expert_offsets && E != 1)
     return fail(MQ_ERR_INVALID_ARG, "expert_offsets may be NULL with E = 1 only");
   if (R == 0) return MQ_OK;
@@ -858,7 +861,10 @@ MQ_EXPORT int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bit
     return fail(MQ_ERR_INVALID_ARG, "out_dtype must be MQ_DTYPE_BF16 or MQ_DTYPE_F16");
   if (E > 1024) return fail(MQ_ERR_UNSUPPORTED, "E must be <= 1024");
   if (H % 128 || I % 128) return fail(MQ_ERR_UNSUPPORTED, "H and I must be multiples of 128");
-  if ((int64_t)T * k > (int64_t(1) << 24) || !mx_units_ok((int64_t)T * k, 2 * I, E) ||
+  // (2I weight rows; H * a_bits bits of a row, counted in 32 bits)
+  if (!mx_rounds_up(2 * (int64_t)I) || H >= 1 << 28)
+    return fail(MQ_ERR_UNSUPPORTED, "need I <= 2^30 - 256 and H < 2^28");
+  if ((int64_t)T * k > (int64_t(1) << 24) || !mx_units_ok((int64_t)T * k, 2 * (int64_t)I, E) ||
       !mx_units_ok((int64_t)T * k, H, E))
     return fail(MQ_ERR_UNSUPPORTED, "too many token-slots");
   if (T == 0) return MQ_OK;
