@@ -490,6 +490,7 @@ int moe_mx_product(const uint8_t* a, const uint8_t* a_scale, int a_bits, int64_t
  * rounding.  An id outside [0, E) sets MQ_DEV_BAD_EXPERT_ID and its slot is
  * left out.  Limits and errors as moe_quant_forward (H % 128 == 0, I % 128 ==
  * 0, E <= 1024, k <= min(E, 32)), H < 2^28, I <= 2^30 - 256; a_bits 8 or 4.
+ * The workspace query gives 0 for sizes that the forward refuses.
  */
 size_t moe_mx_forward_workspace(int T, int H, int I, int E, int k, int a_bits);
 int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bits, int T, int H, int I,

@@ -176,3 +176,18 @@ def test_mx_sizes_whose_rounded_up_values_pass_32_bits_are_refused(lib):
     assert f(I=1 << 30) == 2 and f(I=(1 << 30) + 128) == 2 and f(I=(1 << 31) - 128) == 2
     assert f(H=1 << 28) == 2 and f(H=(1 << 31) - 128) == 2
     assert f(I=(1 << 30) - 128) == 2 and f(I=(1 << 30) - 256) == 1 and f(H=(1 << 28) - 128) == 1
+
+
+def test_mx_forward_workspace_is_0_for_sizes_that_the_forward_refuses(lib):
+    """Else a caller allocates, or fails to, before it is told."""
+    w = lib.moe_mx_forward_workspace
+
+    def refused(T=4, H=128, I=128, E=8, k=2, bits=8):
+        assert lib.moe_mx_forward(P, P, bits, T, H, I, E, k, P, P, P, P, P, P, P, BF16, vp(0x1001), 1 << 62,
+                                  None) in (1, 2)
+        return w(T, H, I, E, k, bits) == 0
+    assert w(4, 128, 128, 8, 2, 8) > 0
+    assert refused(E=64, k=33) and refused(E=1025) and refused(H=192) and refused(I=100)
+    assert refused(T=1 << 24, k=2) and refused(T=(1 << 31) - 1, E=64, k=32)
+    assert refused(I=1 << 30) and refused(H=1 << 28) and refused(T=-1)
+    assert refused(T=1 << 20, H=1 << 24, I=1 << 24)      # too many units of work

@@ -842,23 +842,11 @@ MxLayout mx_layout(int T, int H, int I, int E, int k, int bits) {
   return L;
 }
 
-}  // namespace
-
-MQ_EXPORT size_t moe_mx_forward_workspace(int T, int H, int I, int E, int k, int a_bits) {
-  if (T < 0 || H <= 0 || I <= 0 || E < 1 || k < 1 || k > E || (a_bits != 4 && a_bits != 8)) return 0;
-  return mx_layout(T, H, I, E, k, a_bits).total;
-}
-
-MQ_EXPORT int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bits, int T, int H,
-                             int I, int E, int k, const uint8_t* w13, const uint8_t* s13,
-                             const uint8_t* w2, const uint8_t* s2, const float* topk_w,
-                             const int32_t* topk_ids, void* out, int out_dtype, void* workspace,
-                             size_t ws_bytes, void* stream) {
+// Refuses sizes that the forward does not take.
+int mx_forward_sizes(int T, int H, int I, int E, int k, int a_bits) {
   if (T < 0 || H <= 0 || I <= 0 || E < 1) return fail(MQ_ERR_INVALID_ARG, "bad T, H, I or E");
   if (k < 1 || k > E || k > 32) return fail(MQ_ERR_INVALID_ARG, "need 1 <= k <= min(E, 32)");
   if (a_bits != 4 && a_bits != 8) return fail(MQ_ERR_INVALID_ARG, "a_bits must be 4 or 8");
-  if (out_dtype != MQ_DTYPE_BF16 && out_dtype != MQ_DTYPE_F16)
-    return fail(MQ_ERR_INVALID_ARG, "out_dtype must be MQ_DTYPE_BF16 or MQ_DTYPE_F16");
   if (E > 1024) return fail(MQ_ERR_UNSUPPORTED, "E must be <= 1024");
   if (H % 128 || I % 128) return fail(MQ_ERR_UNSUPPORTED, "H and I must be multiples of 128");
   // (2I weight rows; H * a_bits bits of a row, counted in 32 bits)
@@ -867,6 +855,24 @@ MQ_EXPORT int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bit
   if ((int64_t)T * k > (int64_t(1) << 24) || !mx_units_ok((int64_t)T * k, 2 * (int64_t)I, E) ||
       !mx_units_ok((int64_t)T * k, H, E))
     return fail(MQ_ERR_UNSUPPORTED, "too many token-slots");
+  return MQ_OK;
+}
+
+}  // namespace
+
+MQ_EXPORT size_t moe_mx_forward_workspace(int T, int H, int I, int E, int k, int a_bits) {
+  return mx_forward_sizes(T, H, I, E, k, a_bits) == MQ_OK ? mx_layout(T, H, I, E, k, a_bits).total : 0;
+}
+
+MQ_EXPORT int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bits, int T, int H,
+                             int I, int E, int k, const uint8_t* w13, const uint8_t* s13,
+                             const uint8_t* w2, const uint8_t* s2, const float* topk_w,
+                             const int32_t* topk_ids, void* out, int out_dtype, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  const int rc = mx_forward_sizes(T, H, I, E, k, a_bits);
+  if (rc != MQ_OK) return rc;
+  if (out_dtype != MQ_DTYPE_BF16 && out_dtype != MQ_DTYPE_F16)
+    return fail(MQ_ERR_INVALID_ARG, "out_dtype must be MQ_DTYPE_BF16 or MQ_DTYPE_F16");
   if (T == 0) return MQ_OK;
   if (!a || !a_scale || !w13 || !s13 || !w2 || !s2 || !topk_w || !topk_ids || !out || !workspace)
     return fail(MQ_ERR_INVALID_ARG, "null pointer");
