@@ -107,3 +107,27 @@ def test_a_stream_of_another_device_is_refused(fake, monkeypatch, name):
     assert pretend.calls() == ([], 0) and not entered
     call(Stream(1))
     assert pretend.calls() == ([(1, 101)], 0) and entered == [1]
+
+
+@pytest.mark.parametrize("name", ("dequantize", "product", "forward"))
+def test_codes_and_scales_of_their_own_types_are_taken(fake, name):
+    """E4M3 codes as float8_e4m3fn and scales as float8_e8m0fnu: the bytes are the same."""
+    calls, pretend = fake
+    pretend.calls()
+    keep = []
+
+    def on(t):
+        if t.dtype == torch.uint8 and t.shape in ((4, 4), (2, 64, 4), (2, 256, 4), (2, 128, 4)):
+            t = t.view(torch.float8_e8m0fnu)
+        elif t.dtype == torch.uint8 and t.shape == (4, 128):
+            t = t.view(torch.float8_e4m3fn)
+        keep.append(t)
+        return pretend.on_device(t, 0)
+    args = arguments(on)[name]
+    assert args[1].dtype == torch.float8_e8m0fnu
+    getattr(calls, name)(*args)
+    assert pretend.calls() == ([(0, 100)], 0)
+    # not the other way round
+    swapped = (args[1].view(torch.uint8), args[0].view(torch.uint8).view(torch.float8_e8m0fnu), *args[2:])
+    with pytest.raises((TypeError, ValueError)):
+        getattr(calls, name)(*swapped)

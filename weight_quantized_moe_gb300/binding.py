@@ -500,7 +500,8 @@ def _given(stream, t):
 def moe_quantize_mx(x, bits=4, q=None, scale=None, stream=None):
     """bf16 / f16 / float32 [..., K] -> MX codes uint8 [..., K * bits / 8] (8
     bits: E4M3 bytes; 4 bits: two E2M1 codes per byte, even element low) and
-    E8M0 scale codes uint8 [..., K / 32].  Rows may be strided.
+    E8M0 scale codes uint8 [..., K / 32].  Rows may be strided.  The other calls take
+    8-bit codes as float8_e4m3fn and scales as float8_e8m0fnu too.
 
     With stream=, here and in the other moe_*_mx* calls, the call runs with
     that stream current: what it allocates belongs to the stream that uses it."""

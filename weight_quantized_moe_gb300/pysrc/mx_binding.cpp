@@ -110,7 +110,7 @@ int64_t row_stride(const at::Tensor& t, const char* name) {
   return stride;
 }
 
-// MX codes and scales; `cols` receives the elements of a row.
+// MX codes and scales, as bytes or E4M3 / E8M0 numbers; `cols` receives the elements of a row.
 const at::Tensor& codes(PyObject* q, PyObject* s, int bits, int dims, const char* name,
                         const char* scale_name, int64_t& cols, const uint8_t*& scale) {
   const at::Tensor& t = tensor(q, name);
@@ -118,7 +118,7 @@ const at::Tensor& codes(PyObject* q, PyObject* s, int bits, int dims, const char
   const bool e4m3 = bits == 8 && t.scalar_type() == at::kFloat8_e4m3fn;
   if (t.scalar_type() != at::kByte && !e4m3)
     raise(PyExc_TypeError, "%s must be torch.uint8, got %s", name, c10::toString(t.scalar_type()));
-  if (u.scalar_type() != at::kByte)
+  if (u.scalar_type() != at::kByte && u.scalar_type() != at::kFloat8_e8m0fnu)
     raise(PyExc_TypeError, "%s must be torch.uint8, got %s", scale_name,
           c10::toString(u.scalar_type()));
   on_cuda(t, name);
