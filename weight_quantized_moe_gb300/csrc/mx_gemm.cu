@@ -832,15 +832,22 @@ cudaError_t launch_epi(const MxGemm& g, const MxPlan& pl, const CUtensorMap& mw,
 
 }  // namespace
 
-// Rows per tile: above the average load of a live expert by half, so that
-// most experts are one chunk (their weights are then read once) without many
-// columns to spare; CTA pairs above 96 rows.  Forwards in us with each choice
-// (16, 32, 64, 96, pairs): E=8 k=2 H=4096 I=14336 T=64 186 142 144 145 180, T=256
-// 379 237 215 161 197, T=512 690 389 303 259 219; E=128 k=8 H=2048 I=768 T=64 73
-// 73 77 78 106, T=2048 404 257 206 202 202.  Layers of more than 32 experts count
-// their load 1.7 times: it is seldom even there (that E=128 layer with Zipf
-// popularity, 32, 64, 96 rows: T=256 58 51 51, T=512 79 70 68; even load 83 86 87,
-// 108 97 98).
+// Rows per tile: as many as the fullest expert is likely to have, so that most
+// experts are one chunk and their weights are read once; CTA pairs above 96 rows
+// on average.  Of E random loads of average m the fullest is near m + sqrt(2 m ln
+// E); half as much again covers routers that are less even.  A narrow tile leaves
+// room for more stages, a wide one reads no weights twice.  Forwards in us with 32
+// and 64 rows, 8-bit rows, the weights of three layers in turn; loads even / normal
+// bias / Zipf:
+//   E=8 k=2 H=4096 I=14336   m=16 137 146 / 132 143 / 121 129,  m=19 138 147 / 146
+//     144 / 170 146,  m=24 150 147 / 173 148 / 154 141
+//   E=40 k=4 H=2048 I=1408   m=13 51 54 / 48 49 / 38 38,  m=19 52 55 / 57 53 / 44 43
+//   E=128 k=8 H=2048 I=768   m=10 75 79 / 67 66 / 45 44,  m=12 77 81 / 68 67 / 48 46,
+//     m=16 80 83 / 74 73 / 56 50
+// (4-bit rows have four stages with either: they differ only where the narrow tile
+// reads weights twice.)  64 and 96 rows: m=24 to 40 within 1 % at an even load, up to
+// 7 % for 96 with a bias; a skewed product of 256 rows, E=8, 54.9 and 44.7.  One
+// expert, 24 rows, K=4096, N=28672: 15.6 with 32 rows, 18.2 with 64.
 //
 // K splits: the count with the least estimated time, in us.  The weights come
 // in at the HBM's rate or, with few units, at what their SMs can take (70 GB/s
@@ -855,8 +862,8 @@ MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated, int a_bits) {
   const double live = std::max(1.0, E * (1.0 - std::pow(1.0 - 1.0 / E, (double)S)));
   const double avg = S / live;
   pl.pair = avg > 96;
-  const double load = E > 32 ? 1.7 * avg : avg;
-  pl.bn = pl.pair ? kPairRows : S <= 16 ? 16 : load <= 20 ? 32 : load <= 40 ? 64 : 96;
+  const double fullest = avg + 1.5 * std::sqrt(2 * avg * std::log((double)E));
+  pl.bn = pl.pair ? kPairRows : S <= 16 ? 16 : fullest <= 32 || S <= 32 ? 32 : fullest <= 44 ? 64 : 96;
   pl.splits = 1;
   if (gated || S > 1024) return pl;  // (more rows: partial sums would cost more than idle SMs)
   const int sms = pl.pair ? tc_num_sms() / 2 : tc_num_sms();
@@ -925,14 +932,19 @@ cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStream_t st) {
   p.mtiles = (g.N + p.mrows - 1) / p.mrows;
   p.splits = pl.splits;
   p.words = g.K / 128;
-  // Weights that are read once leave L2 first, so that more of it is left for
-  // the rest, and for weights of an earlier call that reads little.  Not so with
-  // 8-bit rows where a call may read several times L2: their loads take 64 bytes
-  // of the 256 that L2 fetches, and those have to last until the next stages take
-  // the others.  In us, evict-first and normal: E=8 k=2 H=4096 I=14336 forward at
-  // T=1 47 and 53, T=2 70 and 75, T=4 100 and 98, T=8 135 and 128, T=64 143 and 138;
-  // 128 rows, K=4096, N=28672 83.8 and 81.8, K=14336, N=4096 45.0 and 47.4; E=128
-  // T=64 69.7 and 74.5.
+  // Weights that are read once leave L2 first, so that what the call reads again
+  // (rows of A, scales, partial sums) stays.  Not so with 8-bit rows where a call
+  // may read several times L2 (129 MB): a load takes 64 bytes of the 256 that L2
+  // fetches, and in a long stream the rest may be gone before the next stages take
+  // it.  Which of the two wins was measured with other weights streamed between any
+  // two calls (us, normal and evict-first, 8-bit rows): forwards E=8 k=2 H=4096
+  // I=14336 T=1 52.0 47.8, T=2 58.4 54.3, T=4 83.5 81.1, T=8 111 113, T=64 136 141,
+  // T=256 158 156; E=128 k=8 H=2048 I=768 (288 MiB) T=8 45.6 42.3, T=64 72.9 70.6;
+  // E=16 H=4096 I=6400 (600 MiB) T=64 130 132; products E=8 K=14336 N=4096 (224
+  // MiB) 128 rows 46.8 48.5, 512 rows 53.6 51.6; E=16 K=4096 N=28672 (896 MiB) 128
+  // rows 153 164.  The limit is where losses begin to outweigh gains, which either
+  // way are a few percent near it.  With 4-bit rows evict-first was faster or equal at
+  // all of these (E=8 T=64 131 127).
   p.evict_first = g.a_bits == 4 || g.weight_bytes < int64_t(400) << 20;
   p.sbs = (p.words + 3) / 4;
   p.out = g.out;
