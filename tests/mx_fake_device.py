@@ -20,12 +20,23 @@ HEADER = r"""
 #include <c10/core/Device.h>
 namespace fake { inline int current = 0; }
 namespace c10::cuda {
+inline c10::DeviceIndex current_device() { return (c10::DeviceIndex)fake::current; }
 struct CUDAGuard {
   int before;
   explicit CUDAGuard(c10::Device d) : before(fake::current) { fake::current = d.index(); }
   ~CUDAGuard() { fake::current = before; }
   CUDAGuard(const CUDAGuard&) = delete;
   CUDAGuard& operator=(const CUDAGuard&) = delete;
+};
+struct OptionalCUDAGuard {
+  int before = -1;
+  void set_device(c10::Device d) {
+    if (before < 0) before = fake::current;
+    fake::current = d.index();
+  }
+  ~OptionalCUDAGuard() {
+    if (before >= 0) fake::current = before;
+  }
 };
 struct CUDAStream {
   int device;
