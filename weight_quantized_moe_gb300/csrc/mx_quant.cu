@@ -10,9 +10,10 @@ constexpr int kQuantThreads = 256;
 
 // One lane per 8 consecutive elements, so that the four lanes of a block are
 // adjacent; U such vectors per thread.  Bound by HBM: each element is read
-// and written once (180224 x 2048 bf16 to 4 bits 139 us, 6.70 TB/s; to 8 bits
-// 156 us, 7.16 TB/s; a copy of such rows 6.72 TB/s).  The block maximum is taken
-// on packed 16-bit magnitudes (with eight float maxima per lane 156 us).
+// and written once (180224 x 2048 bf16 in a loop of 40 calls: to 4 bits 136 us, 6.87
+// TB/s; to 8 bits 155 us, 7.22 TB/s; a copy of such rows, with as many bytes
+// written as read, 6.73 TB/s).  The block maximum is taken on packed 16-bit
+// magnitudes (with eight float maxima per lane 156 us to 4 bits).
 template <typename T, int BITS, int U, bool DENSE>
 __global__ void __launch_bounds__(kQuantThreads) quant_mx_kernel(const T* __restrict__ x,
                                                                  int64_t nvec, uint32_t vec_per_row,
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_mx_kernel(const T* __rest
 }
 
 // The inverse: bound by HBM, mostly its writes (180224 x 2048 from 4 bits to
-// bf16 135 us, 6.91 TB/s).
+// bf16 134.6 us, 6.94 TB/s; from 8 bits 159 us, 7.03 TB/s).
 template <typename T, int BITS>
 __global__ void __launch_bounds__(256) dequant_mx_kernel(const uint8_t* __restrict__ q,
                                                          const uint8_t* __restrict__ scale,
@@ -190,10 +191,11 @@ template <typename T, int BITS>
 cudaError_t quant_t(const void* x, int64_t rows, int64_t cols, int64_t stride, uint8_t* q,
                     uint8_t* scale, cudaStream_t st) {
   const int64_t nvec = rows * (cols / 8);
-  // Large inputs: U vectors in flight per thread (16-bit: 8, 180224 x 2048 to
-  // 8 bits 162 us against 168 with 4).  Small ones: one, over more SMs.
-  constexpr int U = sizeof(T) == 2 ? 8 : 4;
-  const bool large = nvec >= (int64_t)tc_num_sms() * kQuantThreads * U;
+  // Large inputs: four vectors in flight per thread (180224 x 2048 bf16 to 4 / 8
+  // bits 136.1 / 154.9 us, with eight 138.3 / 155.5).  Small ones, up to where the
+  // SMs hold one per thread: one (600 x 4096 2.5 us, with four 3.0).
+  constexpr int U = 4;
+  const bool large = nvec >= (int64_t)tc_num_sms() * 2048;
   const int per = kQuantThreads * (large ? U : 1);
   const dim3 grid((unsigned)((nvec + per - 1) / per));
   const bool dense = stride == cols;
