@@ -265,3 +265,18 @@ def test_quantised_values_pass_through_the_inverse_in_bulk():
             got = mq.moe_dequantize_mx(q, s, bits=bits, dtype=dtype)
             done()
             assert torch.equal(got.cpu(), torch.from_numpy(want).float().to(dtype))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("R,E", [(16, 1), (17, 1), (32, 1), (33, 1), (44, 1), (45, 1), (46, 2), (47, 2),
+                                 (150, 8), (151, 8), (222, 8), (223, 8), (471, 40), (633, 40)])
+def test_product_at_the_borders_of_the_tile_choice(R, E, bits):
+    """Where the rows per tile change, with even loads and with most rows on one expert."""
+    K, N = 384, 260
+    even = [R // E + (e < R % E) for e in range(E)]
+    one = [0] * (E - 1) + [R] if E > 1 else even
+    for loads in (even, one):
+        qa, sa, qw, sw, offs, (ref, mag) = product_case(R, E, K, N, bits, loads, seed=R)
+        got = mq.moe_mx_product(qa, sa, qw, sw, expert_offsets=offs, a_bits=bits, out_dtype=torch.float32)
+        done()
+        check_long_product(got, ref, mag, K)
