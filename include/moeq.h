@@ -427,7 +427,7 @@ int moe_quantize_mx(const void* x, int dtype, int64_t rows, int64_t cols, int64_
 /*
  * moe_dequantize_mx -- the values that codes and scales stand for, out
  * [rows, cols] (device, dense), rounded once to dtype (bf16 and float32 hold
- * every 4-bit value exactly).  Errors as moe_quantize_mx.
+ * every 4-bit value of scale codes up to 252, the quantiser's largest, exactly).  Errors as moe_quantize_mx.
  */
 int moe_dequantize_mx(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols,
                       int bits, void* out, int dtype, void* stream);

@@ -100,9 +100,10 @@ __global__ void __launch_bounds__(256) dequant_mx_kernel(const uint8_t* __restri
 // One CTA per row; the row's float32 sums stay in registers (V vectors of 8
 // per thread) between the sum of squares and the output, so every input is
 // read once.  h = x + residual is rounded only where it is stored; the norm
-// and the codes are taken from the float32 values.  Bound by HBM (8192 x 4096
-// with residual and 16-bit output 46.1 us, 6.57 TB/s).  V = 1 up to H = 4096:
-// the rows in flight come from several CTAs per SM.
+// and the codes are taken from the float32 values.  Bound by HBM (bf16 with
+// residual and 16-bit output: 8192 x 4096 46.4 us, 6.5 TB/s; V = 2, 8192 x 5120 56.0
+// us, 4096 x 8192 45.5; V = 4, 4096 x 16384 89.1, 2048 x 32768 95.0, 6.4 TB/s).  V = 1
+// up to H = 4096: the rows in flight come from several CTAs per SM.
 template <typename T, typename W, int BITS, int V>
 __global__ void __launch_bounds__(1024) rmsnorm_mx_kernel(const NormArgs a) {
   __shared__ float s_sum[32];

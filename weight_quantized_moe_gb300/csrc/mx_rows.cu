@@ -110,8 +110,9 @@ constexpr int kArrangeSlots = 8;
 // owns eight consecutive slots; it counts every slot's expert itself (S ids from
 // L2), and those of the slots before its own, so that no CTA waits for another.
 // That counting bounds it: up to 2048 slots it takes less than the align kernel
-// and a gather (T=64 forwards: E=8 147 -> 144 us, E=128 k=8 38.3 -> 34.5), at 4096
-// as much (69.3 and 71.0), at 8192 more (22 us against 18 between events).
+// and a gather (T=64 forwards: E=8 147 -> 144 us, E=128 k=8 with Zipf popularity
+// 38.3 -> 34.5), at 4096 as much (69.3 and 71.0), at 8192 more (22 us against 18
+// between events).
 //   sorted [S]: slots in expert order; offsets [E + 1]; dst row p = row
 //   sorted[p] / k of a.  Slots with an id outside [0, E) are left out.
 __global__ void __launch_bounds__(256) mx_arrange(const int32_t* __restrict__ ids, int S, int k,

@@ -1,7 +1,7 @@
 // Python calls of the microscaled operators, compiled: argument checks, output
 // allocation and the library call without the interpreter between them.  Beside
 // kernels of a few microseconds the same steps in Python took most of a call
-// (norm with its four outputs 17 to 20 us, now about half).
+// (norm with its four outputs 17 to 20 us, now 7).
 //
 // binding.py declares the functions with their keywords and documentation and
 // passes the arguments on by position.  Checks raise TypeError or ValueError;
