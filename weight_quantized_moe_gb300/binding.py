@@ -544,7 +544,8 @@ def moe_mx_product(a, a_scale, w, w_scale, expert_offsets=None, a_bits=8, out=No
     """MX rows [R, K] grouped by expert (expert_offsets int32 [E + 1]) times
     4-bit MX weights [E, N, K]: [R, N] in out's dtype or out_dtype (bf16, f16 or
     float32).  Without expert_offsets w is [N, K] (or [1, N, K]): a dense
-    product."""
+    product.  Rows before the first offset and from the last on are not written:
+    they keep out's values, and hold anything where out is not given."""
     if stream is not None:
         with _given(stream, a):
             return moe_mx_product(a, a_scale, w, w_scale, expert_offsets, a_bits, out, out_dtype,
