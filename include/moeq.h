@@ -499,6 +499,53 @@ int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bits, int T, 
                    int out_dtype, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * 16-bit weights
+ * --------------
+ * (No counterpart on the pages: for layers, or experts, that are not quantised or
+ * are being trained, and for adapters beside those that are.)
+ *
+ * moe_grouped_product -- rows grouped by expert times 16-bit weights:
+ *   out[r, n] = sum_k a[r, k] * W[e, n, k],  offsets[e] <= r < offsets[e + 1]
+ * a [R, K] in dtype (bf16 or f16) with a_stride elements between rows; w in the same
+ * dtype, stored [E, N, K], or with w_transposed != 0 [E, K, N]; w_stride elements
+ * between its rows, w_expert_stride between experts.  expert_offsets int32 [E + 1]
+ * (device), rising from >= 0 to <= R, or NULL with E = 1 (a dense product).  Experts
+ * may be empty; rows outside [offsets[0], offsets[E]) are left as they are.  Offsets
+ * that fall or leave [0, R] set MQ_DEV_BAD_OFFSETS: no access leaves the arrays and
+ * the output is unspecified.  out [R, N] dense in out_dtype (MQ_DTYPE_*); it shares no
+ * memory with the inputs.  Accumulation is float32 with one final rounding; a result
+ * is the same on every run.
+ * The workspace holds float32 partial sums where K is split (few units of work); the
+ * query may return 0 (workspace may then be NULL).
+ * K and N are arbitrary; strides are multiples of 8, at least a row's length.
+ * Limits: E <= 1024, R < 2^30, K and N at most 2^31 - 512, strides below 2^39.
+ * Errors: MQ_ERR_INVALID_ARG, MQ_ERR_UNSUPPORTED (limits), MQ_ERR_WORKSPACE.
+ */
+size_t moe_grouped_product_workspace(int64_t R, int K, int N, int E);
+int moe_grouped_product(const void* a, int64_t a_stride, int dtype, int64_t R, int K, int N, int E,
+                        const void* w, int64_t w_stride, int64_t w_expert_stride, int w_transposed,
+                        const int32_t* expert_offsets, void* out, int out_dtype, void* workspace,
+                        size_t ws_bytes, void* stream);
+
+/*
+ * moe_grouped_product_grad -- the gradients of moe_grouped_product for dy = the
+ * gradient of out:
+ *   da[r, k] = sum_n dy[r, n] * W[e, n, k]         (0 for rows of no expert)
+ *   dw[e, n, k] = sum over e's rows r of dy[r, n] * a[r, k]   (0 for an empty expert)
+ * dy [R, N] and a [R, K] in dtype with dy_stride and a_stride elements between rows;
+ * da dense [R, K] in dtype, or NULL (w is then not read and may be NULL); dw dense
+ * [E, N, K], or [E, K, N] with w_transposed, in dw_dtype, or NULL (a may then be NULL).
+ * Rows of no expert are not read, whatever they hold.  Other arguments, limits,
+ * arithmetic and errors as moe_grouped_product.
+ */
+size_t moe_grouped_product_grad_workspace(int64_t R, int K, int N, int E);
+int moe_grouped_product_grad(const void* dy, int64_t dy_stride, const void* a, int64_t a_stride,
+                             int dtype, int64_t R, int K, int N, int E, const void* w,
+                             int64_t w_stride, int64_t w_expert_stride, int w_transposed,
+                             const int32_t* expert_offsets, void* da, void* dw, int dw_dtype,
+                             void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Instrumentation (no counterpart on the pages; used by the benchmark).
  *
  * mq_kernel_launch_count: kernels this library has launched in this process.

@@ -90,6 +90,12 @@ _SIGNATURES = {
     "moe_mx_forward_workspace": (_sz, [_i32] * 6),
     "moe_mx_forward": (_i32, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
                               _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
+    "moe_grouped_product_workspace": (_sz, [_i64, _i32, _i32, _i32]),
+    "moe_grouped_product": (_i32, [_vp, _i64, _i32, _i64, _i32, _i32, _i32, _vp, _i64, _i64, _i32,
+                                   _vp, _vp, _i32, _vp, _sz, _vp]),
+    "moe_grouped_product_grad_workspace": (_sz, [_i64, _i32, _i32, _i32]),
+    "moe_grouped_product_grad": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i32, _i32, _i32, _vp,
+                                        _i64, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
     "mq_kernel_launch_count": (ctypes.c_longlong, []),
     "mq_test_layer_wait_extra": (_i32, [_i32]),
     "mq_profile_enable": (_i32, [_i32]),
@@ -469,24 +475,38 @@ def moe_quant_forward_noalloc(x, w13, w2, s13, s2, topk_w, topk_ids, bits=8, gro
 MX_BINDING_PATH = os.path.join(_PKG, "_mx_binding.so")
 _HALVES = (torch.bfloat16, torch.float16)
 _mx = None
+_grouped = None
+
+
+def _compiled(name):
+    """Load one of _mx_binding.so's modules (raises if it has not been built)."""
+    lib()
+    if not os.path.exists(MX_BINDING_PATH):
+        raise RuntimeError(
+            f"{MX_BINDING_PATH} is missing: build it with "
+            "`python -c 'import __graft_entry__ as g; g.build()'`")
+    loader = importlib.machinery.ExtensionFileLoader(name, MX_BINDING_PATH)
+    m = importlib.util.module_from_spec(
+        importlib.util.spec_from_file_location(name, MX_BINDING_PATH, loader=loader))
+    loader.exec_module(m)
+    m.set_error_class(MoeqError)
+    return m
 
 
 def _mx_binding():
-    """Load _mx_binding.so (raises if it has not been built)."""
+    """The compiled calls of the microscaled operators."""
     global _mx
     if _mx is None:
-        lib()
-        if not os.path.exists(MX_BINDING_PATH):
-            raise RuntimeError(
-                f"{MX_BINDING_PATH} is missing: build it with "
-                "`python -c 'import __graft_entry__ as g; g.build()'`")
-        loader = importlib.machinery.ExtensionFileLoader("_mx_binding", MX_BINDING_PATH)
-        m = importlib.util.module_from_spec(
-            importlib.util.spec_from_file_location("_mx_binding", MX_BINDING_PATH, loader=loader))
-        loader.exec_module(m)
-        m.set_error_class(MoeqError)
-        _mx = m
+        _mx = _compiled("_mx_binding")
     return _mx
+
+
+def _grouped_binding():
+    """The compiled calls of the 16-bit operators."""
+    global _grouped
+    if _grouped is None:
+        _grouped = _compiled("_grouped_binding")
+    return _grouped
 
 
 def _given(stream, t):
@@ -577,3 +597,93 @@ def moe_mx_forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits=8, out
         raise TypeError(f"out must be bfloat16 or float16, got {out_dtype}")
     return (_mx or _mx_binding()).forward(a, a_scale, w13, s13, w2, s2, topk_w, topk_ids, a_bits,
                                           out, _DTYPES[out_dtype], workspace)
+
+
+# ------------------------------------------------------------- 16-bit weights --
+def moe_grouped_product_workspace(R, K, N, E=1) -> int:
+    return int(lib().moe_grouped_product_workspace(R, K, N, E))
+
+
+def moe_grouped_product_grad_workspace(R, K, N, E=1) -> int:
+    return int(lib().moe_grouped_product_grad_workspace(R, K, N, E))
+
+
+def moe_grouped_product(a, w, expert_offsets=None, out=None, out_dtype=None, workspace=None,
+                        stream=None):
+    """bf16 or f16 rows [R, K] grouped by expert (expert_offsets int32 [E + 1]) times
+    weights [E, N, K] of the same dtype: [R, N] in out's dtype or out_dtype (a's by
+    default; bf16, f16 or float32).  Without expert_offsets w is [N, K] (or [1, N, K]):
+    a dense product.  Rows may be strided (by multiples of 8 elements); w may be a
+    transposed view of weights stored [E, K, N].  Rows before the first offset and from
+    the last on are not written: they keep out's values, and hold anything where out is
+    not given.
+
+    Where a or w requires a gradient the call is recorded for autograd
+    (moe_grouped_product_grad is its backward pass); out cannot be given then.  The
+    gradient of a float32 result is rounded to a's dtype before the products."""
+    if torch.is_grad_enabled() and (getattr(a, "requires_grad", False)
+                                    or getattr(w, "requires_grad", False)):
+        if out is not None:
+            raise ValueError("out cannot be given where a or w requires a gradient")
+        if stream is not None:
+            with _given(stream, a):
+                return _GroupedProduct.apply(a, w, expert_offsets, out_dtype, workspace)
+        return _GroupedProduct.apply(a, w, expert_offsets, out_dtype, workspace)
+    if stream is not None:
+        with _given(stream, a):
+            return moe_grouped_product(a, w, expert_offsets, out, out_dtype, workspace)
+    if out is not None:
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = getattr(a, "dtype", None)
+    if out_dtype not in _DTYPES:
+        raise TypeError(f"out must be bfloat16, float16 or float32, got {out_dtype}")
+    return (_grouped or _grouped_binding()).product(a, w, expert_offsets, out, _DTYPES[out_dtype],
+                                                    workspace)
+
+
+def moe_grouped_product_grad(dy, a, w, expert_offsets=None, need_a=True, need_w=True, da=None,
+                             dw=None, dw_dtype=None, workspace=None, stream=None):
+    """The gradients of moe_grouped_product(a, w, expert_offsets) for dy [R, N], the
+    gradient of its result, in a's dtype: (da [R, K] in a's dtype or None, dw [E, N, K]
+    in dw's dtype or dw_dtype (w's by default) or None).  Rows of no expert give no
+    gradient and get 0, an expert without rows has 0.  dw is dense in the order that w
+    is stored in (a transposed view where w is one)."""
+    if stream is not None:
+        with _given(stream, a):
+            return moe_grouped_product_grad(dy, a, w, expert_offsets, need_a, need_w, da, dw,
+                                            dw_dtype, workspace)
+    if dw is not None:
+        dw_dtype = dw.dtype
+    elif dw_dtype is None:
+        dw_dtype = getattr(w, "dtype", None)
+    if dw_dtype not in _DTYPES:
+        raise TypeError(f"dw must be bfloat16, float16 or float32, got {dw_dtype}")
+    return (_grouped or _grouped_binding()).product_grad(dy, a, w, expert_offsets, need_a, need_w,
+                                                         da, dw, _DTYPES[dw_dtype], workspace)
+
+
+def _rows16(t, dtype):
+    """t as rows that the kernels take: of dtype, dense but for a row stride of a
+    multiple of 8 elements, on a 16-byte boundary."""
+    t = t.to(dtype)
+    if t.stride(1) == 1 and t.stride(0) >= t.shape[1] and t.stride(0) % 8 == 0 and t.data_ptr() % 16 == 0:
+        return t
+    wide = torch.empty(t.shape[0], -(-t.shape[1] // 8) * 8, dtype=dtype, device=t.device)
+    return wide[:, :t.shape[1]].copy_(t)
+
+
+class _GroupedProduct(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, a, w, expert_offsets, out_dtype, workspace):
+        ctx.save_for_backward(a, w, expert_offsets)
+        return moe_grouped_product(a, w, expert_offsets, None, out_dtype, workspace)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        a, w, expert_offsets = ctx.saved_tensors
+        da, dw = moe_grouped_product_grad(_rows16(dy, a.dtype), a, w, expert_offsets,
+                                          need_a=ctx.needs_input_grad[0],
+                                          need_w=ctx.needs_input_grad[1])
+        return da, dw, None, None, None

@@ -1,8 +1,9 @@
 """Build libmoeq.so (the C-ABI library) in-tree with nvcc for sm_103a, and
-_mx_binding.so (the compiled Python calls of the microscaled operators).
+_mx_binding.so (the compiled Python calls of the microscaled and the 16-bit
+operators).
 
 Every ``csrc/*.cu`` is compiled to an object in parallel, then linked into
-``weight_quantized_moe_gb300/libmoeq.so``; ``pysrc/mx_binding.cpp`` is compiled
+``weight_quantized_moe_gb300/libmoeq.so``; ``pysrc/*.cpp`` are compiled
 beside them with the host compiler against torch's headers and linked to it.  No fast-math: the quantisers
 rely on IEEE division and denormals.
 """
@@ -23,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoeq.so")
 PYSRC = os.path.join(PKG, "pysrc", "mx_binding.cpp")
+PYSRCS = [PYSRC, os.path.join(PKG, "pysrc", "grouped_binding.cpp")]
+PYHEADER = os.path.join(PKG, "pysrc", "binding_common.h")
 PYEXT = os.path.join(PKG, "_mx_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -68,7 +71,7 @@ def _stamp_path() -> str:
 
 
 def _binding_up_to_date() -> bool:
-    if not _newer(PYEXT, [PYSRC, os.path.join(ROOT, "include", "moeq.h"), os.path.abspath(__file__)]):
+    if not _newer(PYEXT, [*PYSRCS, PYHEADER, os.path.join(ROOT, "include", "moeq.h"), os.path.abspath(__file__)]):
         return False
     try:
         with open(_stamp_path()) as f:
@@ -105,23 +108,24 @@ def _run(cmd, what, verbose=False):
         sys.stderr.write(r.stderr)
 
 
-def _compile_binding() -> str:
+def _compile_binding(src) -> str:
     import torch
-    obj = os.path.join(BUILD, "mx_binding.o")
+    name = os.path.basename(src)
+    obj = os.path.join(BUILD, name[:-4] + ".o")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     system = [*_torch_dirs()[0], cuda, sysconfig.get_path("include")]
     abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
     _run([_cxx(), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
           f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", os.path.join(ROOT, "include"),
-          *[a for d in system for a in ("-isystem", d)], "-c", PYSRC, "-o", obj],
-         "compiling mx_binding.cpp")
+          *[a for d in system for a in ("-isystem", d)], "-c", src, "-o", obj],
+         f"compiling {name}")
     return obj
 
 
-def _link_binding(obj) -> None:
+def _link_binding(objs) -> None:
     lib_dir = _torch_dirs()[1]
     tmp = PYEXT + ".tmp"
-    _run([_cxx(), "-shared", "-o", tmp, obj, "-L", PKG, "-lmoeq", "-L", lib_dir, "-ltorch_python",
+    _run([_cxx(), "-shared", "-o", tmp, *objs, "-L", PKG, "-lmoeq", "-L", lib_dir, "-ltorch_python",
           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib_dir}"],
          "linking _mx_binding.so")
     os.replace(tmp, PYEXT)
@@ -146,7 +150,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_compile_binding) if bind else None
+        binding = [ex.submit(_compile_binding, src) for src in PYSRCS] if bind else []
         if library:
             nvcc = _nvcc()
             objs = list(ex.map(compile_one, _sources()))
@@ -154,7 +158,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], "link")
             os.replace(tmp, LIB)
         if bind:
-            _link_binding(binding.result())
+            _link_binding([b.result() for b in binding])
     return LIB
 
 

@@ -1,6 +1,7 @@
 // C ABI of libmoeq.so: argument validation, workspace layout and launches.
 // Every exported function is declared, with its contract, in include/moeq.h.
 #include "common.cuh"
+#include "grouped.cuh"
 #include "mx.cuh"
 
 #include <algorithm>
@@ -940,4 +941,179 @@ MQ_EXPORT int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bit
     err = launch_mx_combine(g.part, L.down.splits, topk_ids, T, k, E, H, out, out_dtype, st);
   }
   return err == cudaSuccess ? MQ_OK : cuda_fail(err, "mx_forward: combine launch");
+}
+
+// ---------------------------------------------------------------------------
+// 16-bit weights.
+// ---------------------------------------------------------------------------
+static bool half_ok(int dtype) { return dtype == MQ_DTYPE_BF16 || dtype == MQ_DTYPE_F16; }
+
+// Units of work are counted in 32 bits, with up to 16 splits of each.
+static bool gg_units_ok(int64_t rows, int64_t M, int E) {
+  return (rows / 16 + E) * ((M + 127) / 128) < (int64_t(1) << 27);
+}
+
+static bool gg_sizes_ok(int64_t R, int K, int N, int E) {
+  constexpr int kTop = INT32_MAX - 511;  // (sizes are rounded up to tiles in 32 bits)
+  return R >= 0 && K > 0 && N > 0 && E >= 1 && E <= 1024 && R < (int64_t(1) << 30) && K <= kTop &&
+         N <= kTop && gg_units_ok(R, N, E) && gg_units_ok(R, K, E) &&
+         (int64_t)E * ((N + 127) / 128) < (int64_t(1) << 27) / ((K + 127) / 128) &&
+         (int64_t)N * K < (int64_t(1) << 52) / E;
+}
+
+static size_t gg_part_bytes(GgForm form, int64_t R, int E, int M, int N, int K) {
+  const int splits = gg_plan(form, R, E, M, N, K).splits;
+  const size_t n = form == GG_ROWS ? (size_t)E * M * N : (size_t)R * M;
+  return splits > 1 ? align256(sizeof(float) * splits * n) : 0;
+}
+
+MQ_EXPORT size_t moe_grouped_product_workspace(int64_t R, int K, int N, int E) {
+  if (!gg_sizes_ok(R, K, N, E) || R == 0) return 0;
+  return gg_part_bytes(GG_W_K, R, E, N, 0, K);
+}
+
+MQ_EXPORT size_t moe_grouped_product_grad_workspace(int64_t R, int K, int N, int E) {
+  if (!gg_sizes_ok(R, K, N, E) || R == 0) return 0;
+  return std::max({gg_part_bytes(GG_W_K, R, E, K, 0, N), gg_part_bytes(GG_ROWS, R, E, N, K, 0),
+                   gg_part_bytes(GG_ROWS, R, E, K, N, 0)});
+}
+
+// One product: the kernel, and the sum of its splits.
+static int gg_run(GgGemm g, void* workspace, size_t ws_bytes, cudaStream_t st) {
+  const GgPlan pl = gg_plan(g.form, g.R, g.E, g.M, g.N, g.K);
+  const size_t need = gg_part_bytes(g.form, g.R, g.E, g.M, g.N, g.K);
+  if (need && (!workspace || ws_bytes < need))
+    return fail(MQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace ? ws_bytes : 0, need);
+  if (need && !aligned16(workspace))
+    return fail(MQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  g.part = static_cast<float*>(workspace);
+  g.status = status_ptr();
+  cudaError_t err;
+  {
+    LaunchScope ls(MQ_PROF_GEMM1, st);
+    err = launch_gg(g, pl, st);
+  }
+  if (err != cudaSuccess) return cuda_fail(err, "grouped product launch");
+  if (pl.splits > 1) {
+    LaunchScope ls(MQ_PROF_COMBINE, st);
+    err = g.form == GG_ROWS
+              ? launch_mx_reduce(g.part, pl.splits, (int64_t)g.E * g.M, g.N, nullptr, g.E, g.out, g.out_dtype, st)
+              : launch_mx_reduce(g.part, pl.splits, g.R, g.M, g.offsets, g.E, g.out, g.out_dtype, st);
+    if (err != cudaSuccess) return cuda_fail(err, "grouped product: reduce launch");
+  }
+  return MQ_OK;
+}
+
+// Checks that the product and its gradients share: sizes, and the weights' strides.
+static int gg_args(int dtype, int64_t R, int K, int N, int E, int64_t w_stride,
+                   int64_t w_expert_stride, int w_transposed, bool w_read,
+                   const int32_t* expert_offsets) {
+  if (!dtype_ok(dtype)) return fail(MQ_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (dtype == MQ_DTYPE_F32) return fail(MQ_ERR_UNSUPPORTED, "rows and weights must be bfloat16 or float16");
+  if (R < 0 || K <= 0 || N <= 0 || E < 1) return fail(MQ_ERR_INVALID_ARG, "bad R, K, N or E");
+  if (!gg_sizes_ok(R, K, N, E))
+    return fail(MQ_ERR_UNSUPPORTED, "need E <= 1024, R < 2^30, K and N <= 2^31 - 512 and fewer than 2^27 tiles");
+  if (!expert_offsets && E != 1)
+    return fail(MQ_ERR_INVALID_ARG, "expert_offsets may be NULL with E = 1 only");
+  const int row = w_transposed ? N : K, rows = w_transposed ? K : N;
+  if (!w_read) return MQ_OK;
+  if ((rows > 1 && w_stride < row) || w_stride < 0 || w_stride % 8 || (E > 1 && (w_expert_stride <= 0 || w_expert_stride % 8)))
+    return fail(MQ_ERR_INVALID_ARG, "the weights' strides must be multiples of 8, a row's at least its length");
+  return MQ_OK;
+}
+
+static bool gg_row_stride_ok(int64_t stride, int64_t cols, int64_t R) {
+  return stride % 8 == 0 && stride >= 0 && (R <= 1 || stride >= cols);
+}
+
+// The largest stride of a tensor map is below 2^40 bytes; a stride that is never
+// taken (one row, one expert) is replaced.
+static bool gg_map_strides(int64_t& row, int64_t rows, int64_t len, int64_t* expert, int E) {
+  const int64_t round = (len + 7) / 8 * 8;
+  if (rows <= 1) row = round;
+  if (expert && E == 1) *expert = round;
+  constexpr int64_t kTop = int64_t(1) << 39;
+  return row < kTop && (!expert || *expert < kTop);
+}
+
+MQ_EXPORT int moe_grouped_product(const void* a, int64_t a_stride, int dtype, int64_t R, int K,
+                                  int N, int E, const void* w, int64_t w_stride,
+                                  int64_t w_expert_stride, int w_transposed,
+                                  const int32_t* expert_offsets, void* out, int out_dtype,
+                                  void* workspace, size_t ws_bytes, void* stream) {
+  const int rc = gg_args(dtype, R, K, N, E, w_stride, w_expert_stride, w_transposed, true, expert_offsets);
+  if (rc != MQ_OK) return rc;
+  if (!dtype_ok(out_dtype)) return fail(MQ_ERR_INVALID_ARG, "unknown out_dtype %d", out_dtype);
+  if (!gg_row_stride_ok(a_stride, K, R))
+    return fail(MQ_ERR_INVALID_ARG, "a_stride must be a multiple of 8, at least K");
+  if (R == 0) return MQ_OK;
+  if (!a || !w || !out) return fail(MQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(a) || !aligned16(w) || !aligned16(out) || (expert_offsets && !aligned4(expert_offsets)))
+    return fail(MQ_ERR_INVALID_ARG, "pointers must be 16-byte aligned, expert_offsets 4-byte");
+  if (!gg_map_strides(a_stride, R, K, nullptr, 1) ||
+      !gg_map_strides(w_stride, w_transposed ? K : N, w_transposed ? N : K, &w_expert_stride, E))
+    return fail(MQ_ERR_UNSUPPORTED, "strides of 2^39 elements or more");
+  GgGemm g = {};
+  g.form = w_transposed ? GG_W_M : GG_W_K;
+  g.bf16 = dtype == MQ_DTYPE_BF16;
+  g.w = w; g.w_stride = w_stride; g.w_expert = w_expert_stride;
+  g.a = a; g.a_stride = a_stride;
+  g.R = R; g.E = E; g.M = N; g.K = K;
+  g.offsets = expert_offsets;
+  g.out = out; g.out_dtype = out_dtype;
+  return gg_run(g, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+MQ_EXPORT int moe_grouped_product_grad(const void* dy, int64_t dy_stride, const void* a,
+                                       int64_t a_stride, int dtype, int64_t R, int K, int N, int E,
+                                       const void* w, int64_t w_stride, int64_t w_expert_stride,
+                                       int w_transposed, const int32_t* expert_offsets, void* da,
+                                       void* dw, int dw_dtype, void* workspace, size_t ws_bytes,
+                                       void* stream) {
+  const int rc = gg_args(dtype, R, K, N, E, w_stride, w_expert_stride, w_transposed, da != nullptr, expert_offsets);
+  if (rc != MQ_OK) return rc;
+  if (!dtype_ok(dw_dtype)) return fail(MQ_ERR_INVALID_ARG, "unknown dw_dtype %d", dw_dtype);
+  if (!gg_row_stride_ok(a_stride, K, R) || !gg_row_stride_ok(dy_stride, N, R))
+    return fail(MQ_ERR_INVALID_ARG, "row strides must be multiples of 8, at least a row's length");
+  if (!aligned16(dy) || !aligned16(a) || !aligned16(w) || !aligned16(da) || !aligned16(dw) ||
+      (expert_offsets && !aligned4(expert_offsets)))
+    return fail(MQ_ERR_INVALID_ARG, "pointers must be 16-byte aligned, expert_offsets 4-byte");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (R == 0) {  // no rows: the weights' gradient is zero
+    if (!dw) return MQ_OK;
+    const size_t bytes = (size_t)E * N * K * (dw_dtype == MQ_DTYPE_F32 ? 4 : 2);
+    const cudaError_t err = cudaMemsetAsync(dw, 0, bytes, st);
+    return err == cudaSuccess ? MQ_OK : cuda_fail(err, "grouped product's gradient: memset");
+  }
+  if ((da || dw) && (!dy || (da && !w) || (dw && !a))) return fail(MQ_ERR_INVALID_ARG, "null pointer");
+  if (!gg_map_strides(a_stride, R, K, nullptr, 1) || !gg_map_strides(dy_stride, R, N, nullptr, 1) ||
+      !gg_map_strides(w_stride, w_transposed ? K : N, w_transposed ? N : K, &w_expert_stride, E))
+    return fail(MQ_ERR_UNSUPPORTED, "strides of 2^39 elements or more");
+  const size_t need = moe_grouped_product_grad_workspace(R, K, N, E);
+  if (need && (!workspace || ws_bytes < need))
+    return fail(MQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace ? ws_bytes : 0, need);
+  GgGemm g = {};
+  g.bf16 = dtype == MQ_DTYPE_BF16;
+  g.R = R; g.E = E;
+  g.offsets = expert_offsets;
+  if (da) {  // W's outputs are the contraction: the other of the two storages
+    g.form = w_transposed ? GG_W_K : GG_W_M;
+    g.w = w; g.w_stride = w_stride; g.w_expert = w_expert_stride;
+    g.a = dy; g.a_stride = dy_stride;
+    g.M = K; g.K = N;
+    g.out = da; g.out_dtype = dtype;
+    g.zero_outside = true;
+    const int r = gg_run(g, workspace, ws_bytes, st);
+    if (r != MQ_OK) return r;
+  }
+  if (dw) {  // laid out as the weights are
+    g.form = GG_ROWS;
+    g.w = w_transposed ? a : dy; g.w_stride = w_transposed ? a_stride : dy_stride; g.w_expert = 0;
+    g.a = w_transposed ? dy : a; g.a_stride = w_transposed ? dy_stride : a_stride;
+    g.M = w_transposed ? K : N; g.N = w_transposed ? N : K; g.K = 0;
+    g.out = dw; g.out_dtype = dw_dtype;
+    g.zero_outside = false;
+    return gg_run(g, workspace, ws_bytes, st);
+  }
+  return MQ_OK;
 }

@@ -1,0 +1,678 @@
+// Rows grouped by expert times 16-bit weights, and the gradients of that product,
+// on tcgen05 (kind::f16, float32 accumulation):
+//
+//   GG_W_K   out[r, m] = sum_k A[r, k] * W[e(r), m, k]       W stored [E][M][K]
+//   GG_W_M   the same with W stored [E][K][M]: the gradient of the rows, where W's
+//            outputs are the contraction, or weights stored the other way round
+//   GG_ROWS  out[e, m, n] = sum_{r in e} Y[r, m] * A[r, n]   the gradient of the weights
+//
+// One persistent CTA (or CTA pair) per SM (pair).  An accumulator tile has M in the
+// tensor-memory lanes (128 per CTA) and BN columns.  In the first two forms the
+// columns are rows of A, in steps of 16 (32 for a pair): an expert with a few rows
+// costs a narrow instruction and no padding.
+//
+// Operands come by TMA in stages of 64 k.  A stage's bytes are the same whichever
+// index is contiguous in memory: 128-byte swizzled lines of 64 elements, along k, or
+// along m (n) in blocks of 64 by 64, and the instruction's descriptors say which.  So
+// nothing is transposed on the way.
+//
+// GG_ROWS: an expert's rows end anywhere.  The rows behind them that the last stage
+// brings are another expert's, and may hold infinities or NaN: one warp of each CTA
+// overwrites both operands' lines with zeros up to the next step of 16 before the MMAs
+// see them, and the steps after that are not issued.
+//
+// Roles: warp 0 streams both operands; warp 1 issues the MMAs (of a pair: in its
+// first CTA); warp 2 clears the tail of GG_ROWS; warp 3 zeroes rows of no expert;
+// warps 4-11 are the epilogue.  Two accumulator buffers: the next unit's MMAs run
+// while the epilogue stores.
+#include "grouped.cuh"
+#include "pipe.cuh"
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+namespace {
+
+using namespace mq::pipe;
+
+constexpr int kTileM = 128;
+constexpr int kStageK = 64;                    // 128 bytes of k
+constexpr int kABytes = kTileM * 128;
+constexpr int kBlockBytes = kStageK * 128;     // 64 by 64 elements
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kMaxStages = 12;
+constexpr int kMaxE = 1024;
+constexpr int kUnitList = 128;  // units of a CTA that are decoded at its start
+constexpr int kGroup = 8;       // M tiles that a walk over the columns shares
+constexpr int kPartRows = 16;   // rows of the boxes that load a partly filled chunk
+constexpr size_t kSmemMax = 227 * 1024;
+
+template <int BN, int CG>
+struct Cfg {
+  static constexpr int kBRows = BN / CG;  // columns whose operand each CTA holds
+  static constexpr int kStageBytes = kABytes + kBRows * 128;
+  static constexpr int kBufs = 2;
+  static_assert(kBufs * BN <= 512, "tensor memory");
+  static constexpr size_t kFixed = 1024 + 1024 + kUnitList * 16 + (kMaxE + 1) * 4;
+  static constexpr int kFit = (int)((kSmemMax - kFixed) / kStageBytes);
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static_assert(kStages >= 3, "shared memory");
+  // one CTA per SM: each allocates all of tensor memory
+  static constexpr size_t kNeed = kFixed + (size_t)kStages * kStageBytes;
+  static constexpr size_t kSmem = kNeed < 120 * 1024 ? 120 * 1024 : kNeed;
+  static_assert(kSmem <= kSmemMax, "shared memory");
+};
+
+struct Ctl {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t tail[kMaxStages];  // the last stage of an expert's rows has landed
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem;
+  volatile int abort_flag;
+};
+static_assert(sizeof(Ctl) <= 1024, "control block");
+
+struct Params {
+  const int32_t* offsets;
+  int E, M, N, K, R;
+  int mtiles, ntiles, splits;
+  uint32_t idesc;  // without N
+  bool evict_first;
+  bool vector_rows;  // GG_ROWS: a result's rows start at 32-byte boundaries
+  bool zero_outside;
+  void* out;
+  int out_dtype;
+  float* part;
+  unsigned* status;
+};
+
+// row0, n: first row and rows of a chunk; GG_ROWS: the first of the rows that are
+// summed and their number, with col0 the first column.
+struct Unit {
+  int e, row0, n, m, split, col0;
+  bool single;  // the expert has one chunk: its weights are read once
+};
+
+// Rows of expert e, kept inside [0, R) whatever the offsets hold; false where that
+// took a correction.
+__device__ __forceinline__ bool segment(const Params& p, int e, int& start, int& count) {
+  if (!p.offsets) {
+    start = 0;
+    count = p.R;
+    return true;
+  }
+  const int s = p.offsets[e], end = p.offsets[e + 1];
+  start = min(max(s, 0), p.R);
+  count = min(max(end, start), p.R) - start;
+  return start == s && start + count == end;
+}
+
+// Unit u of the walk: expert by expert, groups of kGroup M tiles, every chunk of
+// rows (GG_ROWS: column tile) over a group before the next group (the CTAs at work
+// share the group's operands in L2), splits innermost.
+template <int FORM, int BN, int CG>
+__device__ __forceinline__ Unit decode_unit(const Params& p, const int* chunk_start, uint32_t u) {
+  Unit w;
+  const uint32_t per = p.mtiles * p.splits;
+  uint32_t nch, r;
+  if (FORM == GG_ROWS) {
+    nch = p.ntiles;
+    w.e = (int)(u / (per * nch));
+    r = u - (uint32_t)w.e * per * nch;
+  } else {
+    const int g = (int)(u / per);  // a chunk's position in the walk locates its expert
+    int lo = 0, hi = p.E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (chunk_start[mid] <= g) lo = mid;
+      else hi = mid;
+    }
+    w.e = lo;
+    nch = chunk_start[lo + 1] - chunk_start[lo];
+    r = u - chunk_start[lo] * per;
+  }
+  const uint32_t per_group = kGroup * nch * p.splits;
+  const uint32_t grp = r / per_group;
+  const uint32_t rem = r - grp * per_group;
+  const uint32_t tiles = min(kGroup, p.mtiles - (int)grp * kGroup) * p.splits;
+  const uint32_t c = rem / tiles;
+  const uint32_t t = rem - c * tiles;
+  w.m = (int)(grp * kGroup + t / p.splits) * (kTileM * CG);
+  w.split = (int)(t % p.splits);
+  int start, count;
+  segment(p, w.e, start, count);
+  if (FORM == GG_ROWS) {
+    // the split's share of the expert's stages
+    const int nst = (count + kStageK - 1) / kStageK;
+    const int s0 = (int)((int64_t)nst * w.split / p.splits) * kStageK;
+    const int s1 = (int)((int64_t)nst * (w.split + 1) / p.splits) * kStageK;
+    w.row0 = start + s0;
+    w.n = min(s1, count) - min(s0, count);
+    w.col0 = (int)c * BN;
+  } else {
+    w.row0 = start + (int)c * BN;
+    w.n = min(BN, count - (int)c * BN);
+    w.col0 = 0;
+  }
+  w.single = nch == 1;
+  return w;
+}
+
+// The i-th unit of this worker: from the list in shared memory (decoded once, by
+// all threads at a time), past its end on the spot.
+template <int FORM, int BN, int CG>
+__device__ __forceinline__ Unit unit_at(const Params& p, const int* chunk_start, const int4* list,
+                                        uint32_t i) {
+  if (FORM == GG_ROWS || i >= kUnitList)
+    return decode_unit<FORM, BN, CG>(p, chunk_start, blockIdx.x / CG + i * (gridDim.x / CG));
+  const int4 v = list[i];
+  Unit w;
+  w.e = v.x & 0xffff;
+  w.single = (v.x >> 16) & 1;
+  w.split = v.x >> 17;
+  w.row0 = v.y;
+  w.n = v.z;
+  w.m = v.w;
+  w.col0 = 0;
+  return w;
+}
+
+// Stages of a unit: [first, last).
+template <int FORM>
+__device__ __forceinline__ void stages_of(const Params& p, const Unit& w, int& s0, int& s1) {
+  if (FORM == GG_ROWS) {
+    s0 = 0;
+    s1 = (w.n + kStageK - 1) / kStageK;
+  } else {
+    const int nst = (p.K + kStageK - 1) / kStageK;
+    s0 = (int)((int64_t)nst * w.split / p.splits);
+    s1 = (int)((int64_t)nst * (w.split + 1) / p.splits);
+  }
+}
+
+// Columns of the instruction: in steps of 16 for each CTA (32 for a pair), at most BN.
+template <int FORM, int BN, int CG>
+__device__ __forceinline__ int columns(const Params& p, const Unit& w) {
+  const int n = FORM == GG_ROWS ? min(BN, p.N - w.col0) : w.n;
+  return min(BN, (n + 16 * CG - 1) & -(16 * CG));
+}
+
+// One lane's 16 columns of a GG_ROWS result, consecutive in memory from element i on.
+__device__ __forceinline__ void store_row16(void* out, int dtype, int64_t i, const uint32_t (&v)[16],
+                                            int live, bool vector) {
+  if (vector && live >= 16) {
+    if (dtype == MQ_DTYPE_F32) {
+      uint32_t* d = static_cast<uint32_t*>(out) + i;
+#pragma unroll
+      for (int j = 0; j < 16; j += 8)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d + j),
+                     "r"(v[j]), "r"(v[j + 1]), "r"(v[j + 2]), "r"(v[j + 3]), "r"(v[j + 4]),
+                     "r"(v[j + 5]), "r"(v[j + 6]), "r"(v[j + 7])
+                     : "memory");
+      return;
+    }
+    uint32_t h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a = __uint_as_float(v[2 * j]), b = __uint_as_float(v[2 * j + 1]);
+      if (dtype == MQ_DTYPE_BF16) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+        h[j] = *reinterpret_cast<const uint32_t*>(&t);
+      } else {
+        const __half2 t = __floats2half2_rn(a, b);
+        h[j] = *reinterpret_cast<const uint32_t*>(&t);
+      }
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                     static_cast<uint16_t*>(out) + i),
+                 "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]),
+                 "r"(h[7])
+                 : "memory");
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (j < live) store_out(out, dtype, i + j, __uint_as_float(v[j]));
+}
+
+template <int FORM, int BN, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+    gg_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+            const __grid_constant__ CUtensorMap map_part, const Params p) {
+  using C = Cfg<BN, CG>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* stages = smem;
+  Ctl* ctl = reinterpret_cast<Ctl*>(stages + (size_t)C::kStages * C::kStageBytes);
+  int4* list = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(ctl) + 1024);
+  int* chunk_start = reinterpret_cast<int*>(list + kUnitList);
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;  // 0 issues the pair's MMAs
+  const uint32_t worker = blockIdx.x / CG, workers = gridDim.x / CG;
+
+  if (tid == 0) {
+    tma_prefetch_desc(&map_w);
+    tma_prefetch_desc(&map_a);
+    tma_prefetch_desc(&map_part);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&ctl->full[i], CG);
+      mbar_init(&ctl->empty[i], 1);
+      mbar_init(&ctl->tail[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->acc_full[i], 1);
+      mbar_init(&ctl->acc_empty[i], CG * kEpiWarps);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    if (CG == 2) {
+      tmem_alloc_pair(&ctl->tmem, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&ctl->tmem, 512);
+      tmem_relinquish();
+    }
+  }
+  mq::pdl_wait();
+  mq::pdl_trigger();
+  // Chunks of each expert, scanned; then this worker's units.
+  bool fine = true;
+  for (int e = tid; e < p.E; e += kThreads) {
+    int start, count;
+    fine &= segment(p, e, start, count);
+    chunk_start[e] = (count + BN - 1) / BN;
+  }
+  // offsets that fall or leave [0, R]: nothing is computed
+  const bool bad = __syncthreads_or(!fine);
+  if (bad && tid == 0 && blockIdx.x == 0) mq::flag(p.status, MQ_DEV_BAD_OFFSETS);
+  if (FORM != GG_ROWS && warp == 0) {
+    int run = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int mine = e < p.E ? chunk_start[e] : 0;
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      if (e < p.E) chunk_start[e] = run + incl - mine;
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) chunk_start[p.E] = run;
+  }
+  __syncthreads();
+  const uint32_t chunks = FORM == GG_ROWS ? (uint32_t)p.E * p.ntiles : (uint32_t)chunk_start[p.E];
+  const uint32_t total = bad ? 0 : chunks * p.mtiles * p.splits;
+  const uint32_t units = worker < total ? (total - worker + workers - 1) / workers : 0;
+  if (FORM != GG_ROWS && tid < kUnitList && tid < units) {
+    const Unit w = decode_unit<FORM, BN, CG>(p, chunk_start, worker + tid * workers);
+    list[tid] = make_int4(w.e | (w.single ? 1 << 16 : 0) | w.split << 17, w.row0, w.n, w.m);
+  }
+  tc_fence_before();
+  if (CG == 2) cluster_sync();  // (the barriers are set up in both)
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+
+  if (warp == 0) {
+    // ------------------------------------------------------- operands --
+    const bool el = elect_one();
+    const uint64_t pol_once = l2_policy_evict_first();
+    uint32_t it = 0;
+    uint32_t tail_last = 0, tail_parity = 0;  // by slot: its last load was a tail; tails so far, mod 2
+    bool ok = true;
+    for (uint32_t u = 0; u < units && ok; ++u) {
+      const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u);
+      int s0, s1;
+      stages_of<FORM>(p, w, s0, s1);
+      const int cols = columns<FORM, BN, CG>(p, w);
+      const int m = w.m + (int)rank * kTileM;
+      // this CTA's columns: their first, and how many TMA brings
+      const int first = (int)rank * (cols / CG);
+      const int brought = FORM == GG_ROWS ? (cols / CG + 63) & -64
+                          : cols == BN    ? C::kBRows
+                                          : cols / CG;
+      const uint32_t bytes = kABytes + brought * 128;
+      const bool once = FORM != GG_ROWS && w.single && p.evict_first;
+      for (int s = s0; s < s1; ++s, ++it) {
+        const uint32_t slot = it % C::kStages;
+        if (!warp_wait(&ctl->empty[slot], ((it / C::kStages) & 1) ^ 1, ctl, p.status)) {
+          ok = false;
+          break;
+        }
+        uint8_t* dst = stages + (size_t)slot * C::kStageBytes;
+        uint8_t* dst_b = dst + kABytes;
+        // the last stage of an expert's rows goes by way of warp 2
+        const bool tail = FORM == GG_ROWS && s == s1 - 1 && (w.n & 15);
+        tail_last = (tail_last & ~(1u << slot)) | (uint32_t)tail << slot;
+        tail_parity ^= (uint32_t)tail << slot;
+        if (el) {
+          uint64_t* local = tail ? &ctl->tail[slot] : &ctl->full[slot];
+          const uint32_t bar = CG == 2 && !tail ? map_rank(local, 0) : smem_addr(local);
+          if (CG == 2) mbar_arrive_expect_tx_cluster(bar, bytes);
+          else mbar_arrive_expect_tx(local, bytes);
+          if constexpr (FORM == GG_ROWS) {
+            const int row = w.row0 + s * kStageK;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              if (CG == 2) tma_load_2d_pair(dst + b * kBlockBytes, &map_w, bar, m + b * 64, row);
+              else tma_load_2d(dst + b * kBlockBytes, &map_w, local, m + b * 64, row);
+            }
+            for (int b = 0; b < brought; b += 64) {
+              if (CG == 2) tma_load_2d_pair(dst_b + b * 128, &map_a, bar, w.col0 + first + b, row);
+              else tma_load_2d(dst_b + b * 128, &map_a, local, w.col0 + first + b, row);
+            }
+          } else {
+            const int k = s * kStageK;
+            if constexpr (FORM == GG_W_K) {
+              if (CG == 2) tma_load_3d_pair(dst, &map_w, bar, k, m, w.e);
+              else if (once) tma_load_3d_hint(dst, &map_w, local, k, m, w.e, pol_once);
+              else tma_load_3d(dst, &map_w, local, k, m, w.e);
+            } else {
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                uint8_t* d = dst + b * kBlockBytes;
+                if (CG == 2) tma_load_3d_pair(d, &map_w, bar, m + b * 64, k, w.e);
+                else if (once) tma_load_3d_hint(d, &map_w, local, m + b * 64, k, w.e, pol_once);
+                else tma_load_3d(d, &map_w, local, m + b * 64, k, w.e);
+              }
+            }
+            const int row = w.row0 + first;
+            if (cols == BN) {
+              if (CG == 2) tma_load_2d_pair(dst_b, &map_a, bar, k, row);
+              else tma_load_2d(dst_b, &map_a, local, k, row);
+            } else {
+              for (int r = 0; r < brought; r += kPartRows) {
+                if (CG == 2) tma_load_2d_pair(dst_b + r * 128, &map_part, bar, k, row + r);
+                else tma_load_2d(dst_b + r * 128, &map_part, local, k, row + r);
+              }
+            }
+          }
+        }
+      }
+    }
+    if (ctl->abort_flag) {  // loads in flight land before the CTA goes
+      for (uint32_t j = it < (uint32_t)C::kStages ? 0 : it - C::kStages; j < it; ++j) {
+        const uint32_t slot = j % C::kStages;
+        if (tail_last >> slot & 1) wait_drain(&ctl->tail[slot], (tail_parity >> slot & 1) ^ 1);
+        else if (rank == 0) wait_drain(&ctl->full[slot], (j / C::kStages) & 1);
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ----------------------------------------------------------- MMAs --
+    // The warp walks the loop together and one elected lane issues, so that the
+    // descriptors stay in uniform registers.
+    const bool el = elect_one();
+    uint32_t it = 0, done = 0;
+    bool ok = true;
+    for (uint32_t u = 0; u < units && ok; ++u) {
+      const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u);
+      int s0, s1;
+      stages_of<FORM>(p, w, s0, s1);
+      if (s0 == s1) continue;  // no rows: the epilogue stores zeros
+      const uint32_t buf = done & 1;
+      ok = warp_wait<CG>(&ctl->acc_empty[buf], ((done >> 1) & 1) ^ 1, ctl, p.status);
+      ++done;
+      tc_fence_after();
+      const uint32_t acc = tmem + buf * BN;
+      const uint32_t idesc = p.idesc | (uint32_t)(columns<FORM, BN, CG>(p, w) >> 3) << 17;
+      uint32_t accumulate = 0;
+      for (int s = s0; s < s1 && ok; ++s, ++it) {
+        const uint32_t slot = it % C::kStages;
+        ok = warp_wait<CG>(&ctl->full[slot], (it / C::kStages) & 1, ctl, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        if (el) {
+          const uint32_t base = smem_addr(stages + (size_t)slot * C::kStageBytes);
+          const uint64_t ad = FORM == GG_W_K ? smem_desc_k_sw128(base)
+                                             : smem_desc_mn_sw128(base, kBlockBytes);
+          const uint64_t bd = FORM == GG_ROWS ? smem_desc_mn_sw128(base + kABytes, kBlockBytes)
+                                              : smem_desc_k_sw128(base + kABytes);
+          const int steps = FORM == GG_ROWS ? min(4, (w.n - s * kStageK + 15) >> 4) : 4;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (FORM != GG_ROWS || j < steps)
+              mma_ss<CG>(acc, ad + j * (FORM == GG_W_K ? 2 : 128), bd + j * (FORM == GG_ROWS ? 128 : 2),
+                         idesc, accumulate | j);
+          commit<CG>(&ctl->empty[slot]);
+        }
+        accumulate = 1;
+      }
+      if (ok && el) commit<CG>(&ctl->acc_full[buf]);
+    }
+    // nothing this warp issued may be in flight when the memory goes
+    if (el) {
+      if (CG == 2) mma_commit_pair_here(&ctl->drain);
+      else mma_commit(&ctl->drain);
+    }
+    wait_drain(&ctl->drain, 0);
+  } else if (warp == 2 && FORM == GG_ROWS) {
+    // ----------------------------------------------------------- tails --
+    uint32_t it = 0, parity = 0;  // by slot: tails so far, mod 2
+    bool ok = true;
+    for (uint32_t u = 0; u < units && ok; ++u) {
+      const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u);
+      int s0, s1;
+      stages_of<FORM>(p, w, s0, s1);
+      it += s1 - s0;
+      if (!(w.n & 15)) continue;
+      const uint32_t slot = (it - 1) % C::kStages;
+      ok = warp_wait(&ctl->tail[slot], parity >> slot & 1, ctl, p.status);
+      parity ^= 1u << slot;
+      if (!ok) break;
+      const int live = w.n - (s1 - 1) * kStageK;  // rows of the stage that are the expert's
+      uint8_t* dst = stages + (size_t)slot * C::kStageBytes;
+      // line r of each 64 by 64 block; eight lanes cover its 128 bytes
+      for (int r = live; r < ((live + 15) & -16); ++r)
+        for (int b = lane >> 3; b < 2 + C::kBRows / 64; b += 4)
+          *reinterpret_cast<uint4*>(dst + b * kBlockBytes + r * 128 + (lane & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive<CG>(&ctl->full[slot]);
+    }
+  } else if (warp == 3 && FORM != GG_ROWS) {
+    // ------------------------------------------------ rows of no expert --
+    if (p.zero_outside && p.offsets && !bad) {
+      const int64_t lo = p.offsets[0], hi = p.offsets[p.E];
+      const int64_t outside = lo + p.R - hi;
+      for (int64_t i = blockIdx.x; i < outside; i += gridDim.x) {
+        const int64_t r = i < lo ? i : hi + i - lo;
+        for (int m = lane; m < p.M; m += 32) store_out(p.out, p.out_dtype, r * p.M + m, 0.0f);
+      }
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------- epilogue --
+    const int quad = warp & 3;         // the tensor-memory lanes this warp may read
+    const int half = (warp - 4) >> 2;  // which 16-column steps it takes
+    uint32_t done = 0;
+    bool ok = true;
+    for (uint32_t u = 0; u < units && ok; ++u) {
+      const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u);
+      const int m = w.m + (int)rank * kTileM + quad * 32 + lane;  // this lane's output
+      const int dtype = p.splits > 1 ? MQ_DTYPE_F32 : p.out_dtype;
+      const bool empty = FORM == GG_ROWS && w.n == 0;
+      const uint32_t buf = done & 1;
+      if (!empty) {
+        ok = warp_wait(&ctl->acc_full[buf], (done >> 1) & 1, ctl, p.status);
+        ++done;
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const uint32_t acc = tmem + buf * BN + ((uint32_t)(quad * 32) << 16);
+      if constexpr (FORM == GG_ROWS) {
+        void* out = p.out;
+        if (p.splits > 1) out = p.part + (int64_t)w.split * p.E * p.M * p.N;
+        const int64_t at = ((int64_t)w.e * p.M + m) * p.N + w.col0;
+        const int n = min(BN, p.N - w.col0);
+        if (m - lane < p.M) {
+          for (int c0 = half * 16; c0 < n; c0 += 32) {
+            uint32_t v[16];
+            if (empty) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = 0;
+            } else {
+              tmem_ld16_sync(acc + c0, v);
+            }
+            if (m < p.M) store_row16(out, dtype, at + c0, v, n - c0, p.vector_rows);
+          }
+        }
+      } else {
+        void* out = p.out;
+        if (p.splits > 1) out = p.part + (int64_t)w.split * p.R * p.M;
+        if (m - lane < p.M) {
+          const bool live = m < p.M;
+          for (int c0 = half * 16; c0 < w.n; c0 += 32) {
+            uint32_t v[16];
+            tmem_ld16_sync(acc + c0, v);
+            const int64_t at = (int64_t)(w.row0 + c0) * p.M + m;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (live && c0 + j < w.n)
+                store_out(out, dtype, at + (int64_t)j * p.M, __uint_as_float(v[j]));
+          }
+        }
+      }
+      if (!empty) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive<CG>(&ctl->acc_empty[buf]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (CG == 2) cluster_sync();  // (the other CTA's shared memory is in use until here)
+  else __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    if (CG == 2) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------ host side --
+template <int FORM, int BN, int CG>
+cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const CUtensorMap& mr,
+                       const Params& p, int64_t units, cudaStream_t st) {
+  constexpr size_t smem = Cfg<BN, CG>::kSmem;
+  auto kern = gg_gemm<FORM, BN, CG>;
+  static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int sms = tc_num_sms();
+  const int workers = (int)std::max<int64_t>(1, std::min<int64_t>(units, sms / CG));
+  return launch_pdl_cluster(kern, dim3(workers * CG), dim3(kThreads), CG, smem, st, mw, ma, mr, p);
+}
+
+template <int FORM>
+cudaError_t launch_form(const GgPlan& pl, const CUtensorMap& mw, const CUtensorMap& ma,
+                        const CUtensorMap& mr, const Params& p, int64_t units, cudaStream_t st) {
+  if (pl.pair) return launch_one<FORM, 256, 2>(mw, ma, mr, p, units, st);
+  if constexpr (FORM != GG_ROWS) {
+    switch (pl.bn) {
+      case 16: return launch_one<FORM, 16, 1>(mw, ma, mr, p, units, st);
+      case 32: return launch_one<FORM, 32, 1>(mw, ma, mr, p, units, st);
+      case 64: return launch_one<FORM, 64, 1>(mw, ma, mr, p, units, st);
+    }
+  }
+  return launch_one<FORM, 128, 1>(mw, ma, mr, p, units, st);
+}
+
+}  // namespace
+
+GgPlan gg_plan(GgForm form, int64_t R, int E, int M, int N, int K) {
+  GgPlan pl;
+  pl.splits = 1;
+  const int sms = tc_num_sms();
+  if (form == GG_ROWS) {
+    pl.pair = M > 128 && N > 128;
+    pl.bn = pl.pair ? 256 : 128;
+    const double units = (double)E * ((M + pl.bn - 1) / pl.bn) * ((N + pl.bn - 1) / pl.bn);
+    const double workers = pl.pair ? sms / 2 : sms;
+    const double stages = std::ceil(R / 64.0 / E);
+    while (pl.splits < 16 && units * pl.splits * 2 <= workers && stages >= pl.splits * 8) pl.splits *= 2;
+    return pl;
+  }
+  const double live = std::max(1.0, E * (1.0 - std::pow(1.0 - 1.0 / E, (double)R)));
+  const double avg = R / live;
+  pl.pair = avg > 128;
+  const double fullest = avg + 1.5 * std::sqrt(2 * avg * std::log((double)E));
+  pl.bn = pl.pair ? 256 : R <= 16 ? 16 : fullest <= 32 || R <= 32 ? 32 : fullest <= 64 || R <= 64 ? 64 : 128;
+  if (R > 1024) return pl;
+  const double workers = pl.pair ? sms / 2 : sms;
+  const double units = std::max(live, std::ceil((double)R / pl.bn)) * ((M + (pl.pair ? 255 : 127)) / (pl.pair ? 256 : 128));
+  const int stages = (K + kStageK - 1) / kStageK;
+  while (pl.splits < 16 && units * pl.splits * 2 <= workers && stages >= pl.splits * 8) pl.splits *= 2;
+  return pl;
+}
+
+cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
+  const CUtensorMapDataType dt = g.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const int cg = pl.pair ? 2 : 1;
+  CUtensorMap mw, ma, mr;
+  cudaError_t err;
+  const cuuint64_t ws = 2 * (cuuint64_t)g.w_stride, as = 2 * (cuuint64_t)g.a_stride;
+  const cuuint32_t block[3] = {64, 64, 1};
+  if (g.form == GG_ROWS) {
+    const cuuint64_t wd[2] = {(cuuint64_t)g.M, (cuuint64_t)g.R};
+    const cuuint64_t ad[2] = {(cuuint64_t)g.N, (cuuint64_t)g.R};
+    err = make_map(&mw, dt, 2, g.w, wd, &ws, block);
+    if (err == cudaSuccess) err = make_map(&ma, dt, 2, g.a, ad, &as, block);
+    mr = ma;
+  } else {
+    const bool by_k = g.form == GG_W_K;
+    const cuuint64_t wd[3] = {(cuuint64_t)(by_k ? g.K : g.M), (cuuint64_t)(by_k ? g.M : g.K), (cuuint64_t)g.E};
+    const cuuint64_t wst[2] = {ws, 2 * (cuuint64_t)g.w_expert};
+    const cuuint32_t rows[3] = {64, kTileM, 1};
+    err = make_map(&mw, dt, 3, g.w, wd, wst, by_k ? rows : block);
+    const cuuint64_t ad[2] = {(cuuint64_t)g.K, (cuuint64_t)g.R};
+    const cuuint32_t abox[2] = {64, (cuuint32_t)(pl.bn / cg)}, pbox[2] = {64, kPartRows};
+    if (err == cudaSuccess) err = make_map(&ma, dt, 2, g.a, ad, &as, abox);
+    if (err == cudaSuccess) err = make_map(&mr, dt, 2, g.a, ad, &as, pbox);
+  }
+  if (err != cudaSuccess) return err;
+  Params p = {};
+  p.offsets = g.offsets;
+  p.E = g.E;
+  p.M = g.M;
+  p.N = g.N;
+  p.K = g.K;
+  p.R = (int)g.R;
+  p.mtiles = (g.M + kTileM * cg - 1) / (kTileM * cg);
+  p.ntiles = g.form == GG_ROWS ? (g.N + pl.bn - 1) / pl.bn : 1;
+  p.splits = pl.splits;
+  p.idesc = idesc_16(g.bf16, kTileM * cg, 0, g.form != GG_W_K, g.form == GG_ROWS);
+  p.evict_first = true;
+  p.zero_outside = g.zero_outside;
+  p.out = g.out;
+  p.out_dtype = g.out_dtype;
+  p.part = g.part;
+  p.status = g.status;
+  const int64_t elem = pl.splits > 1 || g.out_dtype == MQ_DTYPE_F32 ? 4 : 2;
+  p.vector_rows = (int64_t)g.N * elem % 32 == 0 &&
+                  (reinterpret_cast<uintptr_t>(pl.splits > 1 ? (void*)g.part : g.out) & 31u) == 0;
+  const int64_t live = std::min<int64_t>(g.R, g.E);
+  const int64_t units = (g.form == GG_ROWS ? (int64_t)g.E * p.ntiles : live + g.R / pl.bn) * p.mtiles * p.splits;
+  switch (g.form) {
+    case GG_W_K: return launch_form<GG_W_K>(pl, mw, ma, mr, p, units, st);
+    case GG_W_M: return launch_form<GG_W_M>(pl, mw, ma, mr, p, units, st);
+    default: return launch_form<GG_ROWS>(pl, mw, ma, mr, p, units, st);
+  }
+}

@@ -43,18 +43,15 @@
 //     one block when the activations are requantised.  Two accumulator buffers:
 //     the next unit's MMAs run meanwhile.
 #include "mx.cuh"
-#include "sm100_ptx.cuh"
-
-#include <cudaTypedefs.h>
+#include "pipe.cuh"
 
 #include <algorithm>
 #include <atomic>
 #include <cmath>
-#include <mutex>
 
 namespace {
 
-using namespace mq::ptx;
+using namespace mq::pipe;
 
 constexpr int kTileM = 128;
 constexpr int kABytes = kTileM * 128;  // one weight tile of a stage
@@ -70,7 +67,6 @@ constexpr int kMaxE = 1024;
 constexpr int kPairRows = 224;         // rows per tile of a CTA pair
 constexpr int kUnitList = 128;         // units of a CTA that are decoded at its start
 constexpr int kGroup = 8;              // weight tiles that a chunk walk shares
-constexpr unsigned long long kWaitNs = 1000000000ull;
 constexpr size_t kSmemMax = 227 * 1024;
 
 template <int BITS, int BN, int CG, int EPI>
@@ -218,53 +214,6 @@ __device__ __forceinline__ Unit unit_at(const Params& p, const int* chunk_start,
   return w;
 }
 
-template <int CG>
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, Ctl* ctl,
-                                             unsigned* status) {
-  const unsigned long long t0 = mq::global_timer_ns();
-  for (uint32_t n = 1;; ++n) {
-    if (CG == 2 ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-    if ((n & 63u) == 0) {
-      if (ctl->abort_flag) return false;
-      if (mq::global_timer_ns() - t0 > kWaitNs) {
-        ctl->abort_flag = 1;
-        mq::flag(status, MQ_DEV_WAIT_TIMEOUT);
-        return false;
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
-// CG = 2: the arrivals may come from the other CTA of the pair.
-template <int CG = 1>
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Ctl* ctl,
-                                          unsigned* status) {
-  bool ok = CG == 2 ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  ok = ok || wait_bounded<CG>(bar, parity, ctl, status);
-  return __all_sync(0xffffffffu, ok);
-}
-
-// Arrives on the barrier of the CTA that issues the MMAs.
-template <int CG>
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-  if (CG == 2) mbar_arrive_cluster(map_rank(bar, 0));
-  else mbar_arrive(bar);
-}
-
-// Signals the MMAs issued so far: on both CTAs of a pair.
-template <int CG>
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  if (CG == 2) mma_commit_pair(bar);
-  else mma_commit(bar);
-}
-
 // Columns of the instruction for a chunk of n rows: n in steps of 16 for each
 // CTA (32 for a pair), at most the tile's.
 template <int CG>
@@ -274,13 +223,6 @@ __device__ __forceinline__ int columns(int n, int bn) {
 // Rows of the boxes that load a partly filled chunk.
 template <int CG>
 constexpr int kPartRows = CG == 2 ? 16 : 32;
-
-// After an abort: lets what is in flight land; bounded, ignores the flag.
-__device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
-  const unsigned long long t0 = mq::global_timer_ns();
-  while (!mbar_try_wait(bar, parity))
-    if (mq::global_timer_ns() - t0 > kWaitNs) return;
-}
 
 // Four scale words (512 k) of one row from word w0 on; words past the row's
 // end are 0 (their codes are 0 too).
@@ -317,12 +259,6 @@ __device__ __forceinline__ void epilogue_barrier() {
 // Joins the gate warp and the up warp of one pair of lane quarters.
 __device__ __forceinline__ void swap_barrier(int pair) {
   asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
-}
-
-__device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float v) {
-  if (dtype == MQ_DTYPE_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
-  else if (dtype == MQ_DTYPE_F16) static_cast<__half*>(out)[i] = __float2half_rn(v);
-  else static_cast<float*>(out)[i] = v;
 }
 
 template <int BITS, int BN, int EPI, int CG>
@@ -762,31 +698,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------ host side --
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-cudaError_t get_encoder() {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  return g_encode ? cudaSuccess : cudaErrorNotSupported;
-}
-
-cudaError_t make_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base,
-                     const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
-  const cuuint32_t ones[3] = {1, 1, 1};
-  const CUresult r = g_encode(map, dt, rank, const_cast<void*>(base), dims, strides, box, ones,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <int BITS, int BN, int EPI, int CG>
 cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const CUtensorMap& mr, const Params& p,
                        int64_t units, cudaStream_t st) {
@@ -889,8 +800,7 @@ MxPlan mx_plan(int64_t S, int E, int K, int N, bool gated, int a_bits) {
 }
 
 cudaError_t launch_mx_gemm(const MxGemm& g, const MxPlan& pl, cudaStream_t st) {
-  cudaError_t err = get_encoder();
-  if (err != cudaSuccess) return err;
+  cudaError_t err;
   const bool gated = g.epi == MX_EPI_GATED;
   CUtensorMap mw, ma, mr;
   {

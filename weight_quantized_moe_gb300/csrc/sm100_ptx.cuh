@@ -145,6 +145,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
                : "memory");
 }
 
+// Arrives on a barrier of either CTA and adds to the bytes that it waits for.
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
+                   bar),
+               "r"(bytes)
+               : "memory");
+}
+
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -382,6 +390,27 @@ __device__ __forceinline__ void tmem_ld_cols_sync(uint32_t taddr, uint32_t (&v)[
   else tmem_ld16_sync(taddr, v);
 }
 
+// D[tmem] (+)= A * B^T, both from shared memory, kind::f16 (K = 16).  CG = 2: 128
+// rows of A and D and half of B's in each CTA of the pair.
+template <int CG>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // ------------------------------------------- block-scaled (MX) operands --
 // Block scales of one 128-k word: 32 lanes x 16 bytes from shared memory to 4
 // tensor-memory columns, the same in all four lane quarters (CG = 2: in each
@@ -453,6 +482,32 @@ __device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t addr) {
   d |= (uint64_t)1 << 46;                         // descriptor version (tcgen05)
   d |= (uint64_t)2 << 61;                         // swizzle: 128 B
   return d;
+}
+
+// Shared-memory matrix descriptor of an operand whose M (or N) index is the
+// contiguous one, stored with the 128-byte swizzle: blocks of 64 elements (128
+// bytes) by 64 k, `block_bytes` apart, 8-k groups 1024 bytes apart.  A step of 16
+// k is 2048 bytes on.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr, uint32_t block_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);         // start address
+  d |= (uint64_t)(block_bytes >> 4) << 16;        // leading byte offset: next 64 elements
+  d |= (uint64_t)(1024u >> 4) << 32;              // stride byte offset: next 8 k
+  d |= (uint64_t)1 << 46;                         // descriptor version (tcgen05)
+  d |= (uint64_t)2 << 61;                         // swizzle: 128 B
+  return d;
+}
+
+// Instruction descriptor, kind::f16 with float32 accumulation: A and B both bf16
+// or both f16; a_mn / b_mn: the operand's M / N index is contiguous, not its k.
+__host__ __device__ constexpr uint32_t idesc_16(bool bf16, int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4)                      // D format: f32
+         | ((bf16 ? 1u : 0u) << 7)      // A format
+         | ((bf16 ? 1u : 0u) << 10)     // B format
+         | ((a_mn ? 1u : 0u) << 15)     // A transposed
+         | ((b_mn ? 1u : 0u) << 16)     // B transposed
+         | ((uint32_t)(N >> 3) << 17)   // N / 8
+         | ((uint32_t)(M >> 4) << 24);  // M / 16
 }
 
 // Instruction descriptor, kind::f16: bf16 x bf16 -> f32, A and B K-major.
