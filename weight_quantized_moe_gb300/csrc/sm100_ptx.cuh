@@ -146,8 +146,10 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
 }
 
 // Arrives on a barrier of either CTA and adds to the bytes that it waits for.
+// Relaxed: it orders nothing but the barrier itself (a release at cluster scope
+// held a producer for more than 1000 cycles at every stage).
 __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
                    bar),
                "r"(bytes)
                : "memory");
