@@ -52,6 +52,7 @@ typedef enum {
 #define MQ_DEV_BAD_EXPERT_ID  0x1u  /* a topk id outside [0, E); slot ignored   */
 #define MQ_DEV_WAIT_TIMEOUT   0x2u  /* a pipeline wait gave up; output invalid  */
 #define MQ_DEV_BAD_OFFSETS    0x4u  /* expert offsets that fall or leave [0, R] */
+#define MQ_DEV_BAD_ADAPTER_ID 0x8u  /* an adapter id outside [-1, L); taken as -1 */
 
 const char* mq_status_string(int status);
 const char* mq_last_error_message(void);
@@ -544,6 +545,37 @@ int moe_grouped_product_grad(const void* dy, int64_t dy_stride, const void* a, i
                              int64_t w_stride, int64_t w_expert_stride, int w_transposed,
                              const int32_t* expert_offsets, void* da, void* dw, int dw_dtype,
                              void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * moe_lora_product -- low-rank adapters of many requests in one call, beside a
+ * projection that is already computed (by any of this library's products, say):
+ *   out[t] = base[t] + scaling[l] * B[l, e] (A[l, e] x[t]),   l = adapter_ids[t]
+ * x [R, K] in dtype (bf16 or f16), x_stride elements between rows; lora_a
+ * [L, E, r, K] and lora_b [L, E, N, r] dense in the same dtype; adapter_ids int32 [R]
+ * (device), -1 for a row without an adapter (out = base); scaling float32 [L] (device)
+ * or NULL (1).  An id outside [-1, L) sets MQ_DEV_BAD_ADAPTER_ID and is taken as -1.
+ * expert_offsets int32 [E + 1] (device) groups the rows by expert as
+ * moe_grouped_product's does (rows outside are left as they are; offsets that fall or
+ * leave [0, R] set MQ_DEV_BAD_OFFSETS and nothing is written), or is NULL with E = 1.
+ * base [R, N] and out [R, N] in out_dtype with strides of their own; base may be NULL
+ * (0), and out may be base itself, with its stride; otherwise out shares no memory
+ * with the inputs.
+ * A x and the sums are float32; with many rows A x enters the second product as the
+ * sum of two 16-bit values (16 bits of precision relative to the row's largest for
+ * bf16, 22 for f16); one final rounding.  A row's result depends on no other row, and
+ * is the same on every run.
+ * Limits: K and r multiples of 8, r <= 128, E <= 1024, R, K, N and L * E < 2^30.
+ * x_stride is a multiple of 8; base and out whose strides and N are multiples of 8, on
+ * 16-byte boundaries, are faster than others.
+ * Errors: MQ_ERR_INVALID_ARG, MQ_ERR_UNSUPPORTED (limits), MQ_ERR_WORKSPACE.
+ */
+size_t moe_lora_product_workspace(int64_t R, int K, int N, int r, int L, int E);
+int moe_lora_product(const void* x, int64_t x_stride, int dtype, int64_t R, int K, int N, int r,
+                     int L, int E, const void* lora_a, const void* lora_b,
+                     const int32_t* adapter_ids, const int32_t* expert_offsets,
+                     const float* scaling, const void* base, int64_t base_stride, void* out,
+                     int64_t out_stride, int out_dtype, void* workspace, size_t ws_bytes,
+                     void* stream);
 
 /*
  * Instrumentation (no counterpart on the pages; used by the benchmark).

@@ -34,6 +34,13 @@ int moe_grouped_product_grad(const void*, int64_t, const void*, int64_t, int, in
                              int64_t, int64_t, int, const int32_t*, void*, void*, int, void*, size_t, void* st) {
   return note(st);
 }
+size_t moe_lora_product_workspace(int64_t, int, int, int, int, int) { return 0; }
+int moe_lora_product(const void*, int64_t, int, int64_t, int, int, int, int, int, const void*, const void*,
+                     const int32_t*, const int32_t*, const float*, const void*, int64_t bs, void*, int64_t os, int,
+                     void*, size_t, void* st) {
+  g_weights[0] = bs, g_weights[1] = os;
+  return note(st);
+}
 }
 """
 

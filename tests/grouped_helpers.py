@@ -57,3 +57,36 @@ def weights_grad64(dy, a, offsets, E):
         out[e] = dy[rows].T @ a[rows]
         mag[e] = dy[rows].abs().T @ a[rows].abs()
     return out, mag
+
+
+# What is lost of A x where it enters the second product as the sum of two 16-bit values:
+# two roundings by half a step, relative to the row's largest (whose power of two is at
+# most its magnitude), and half the smallest subnormal.
+SPLIT = {torch.bfloat16: 2.0 ** -16, torch.float16: 2.0 ** -22 + 2.0 ** -25}
+
+
+def lora64(x, a, b, ids, experts, scaling, base, dtype):
+    """(out, what it may be off by before its last rounding) of moe_lora_product for
+    rows with adapter ids and experts (host lists), a [L, E, r, K], b [L, E, N, r]."""
+    R, N, K, r = x.shape[0], b.shape[2], x.shape[1], a.shape[2]
+    out = torch.zeros(R, N, dtype=torch.float64) if base is None else base.double()
+    off = torch.zeros(R, N, dtype=torch.float64)
+    for l, e in {(l, e) for l, e in zip(ids, experts) if l >= 0 and e >= 0}:
+        rows = [t for t in range(R) if ids[t] == l and experts[t] == e]
+        s = 1.0 if scaling is None else float(scaling[l])
+        al, bl, xs = a[l, e].double(), b[l, e].double(), x[rows].double()
+        h = xs @ al.T * s
+        h_off = (K + 1) * STEP * (xs.abs() @ al.abs().T) * abs(s) + SPLIT[dtype] * h.abs().amax(1, keepdim=True)
+        out[rows] += h @ bl.T
+        off[rows] += h_off @ bl.abs().T + (2 * r + 1) * STEP * ((h.abs() + h_off) @ bl.abs().T)
+    return out, off + 2.0 ** -24 * out.abs()
+
+
+def check_lora(got, ref, off, what=""):
+    err = (got.double().cpu() - ref).abs()
+    tol = off + HALF_STEP[got.dtype] * (ref.abs() + off) + FLOOR[got.dtype]
+    bad = ~(err <= tol)
+    assert not bad.any(), (
+        f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {bad.nonzero()[0].tolist()}: "
+        f"{got.double().cpu()[tuple(bad.nonzero()[0])]} for {ref[tuple(bad.nonzero()[0])]} "
+        f"(allowed {tol[tuple(bad.nonzero()[0])]})")

@@ -71,6 +71,67 @@ def test_gradient_refusals(lib):
     assert g(R=4096, N=64, E=1, dst=64, nb=need - 1, wk=P) == 4
 
 
+def test_lora_refusals(lib):
+    far, farther = vp(0x10000000), vp(0x20000000)
+
+    def q(x=P, st=64, dt=BF16, R=4, K=64, N=72, r=16, L=3, E=2, a=P, b=P, ids=P, off=P, sc=None, base=far, bs=72,
+          out=farther, os=72, odt=BF16, wk=None, nb=0):
+        return lib.moe_lora_product(x, st, dt, R, K, N, r, L, E, a, b, ids, off, sc, base, bs, out, os, odt, wk, nb, None)
+    # (the scaling is misaligned: a call that passes the checks before it is refused for that)
+    last = dict(sc=vp(0x1002))
+    assert q(**last) == 1 and b"aligned" in lib.mq_last_error_message()
+    assert q(dt=F32) == 2 and q(dt=3) == 1 and q(odt=7) == 1
+    assert q(R=-1) == 1 and q(K=0) == 1 and q(N=0) == 1 and q(r=0) == 1 and q(L=0) == 1 and q(E=0) == 1
+    assert q(K=68, st=72) == 1 and q(r=12) == 1
+    assert q(r=136) == 2 and q(E=1025) == 2 and q(R=1 << 30) == 2 and q(K=1 << 30, st=1 << 30) == 2
+    assert q(N=1 << 30) == 2 and q(L=1 << 29, E=2) == 2 and q(L=1 << 20, E=512, K=1 << 20, st=1 << 20) == 2
+    assert q(off=None) == 1
+    assert q(st=56) == 1 and q(st=68) == 1 and q(os=71) == 1 and q(bs=64) == 1
+    for k in ("x", "a", "b", "ids", "out"):
+        assert q(**{k: None}) == 1, k
+    assert q(x=ODD) == 1 and q(a=ODD) == 1 and q(b=ODD) == 1 and q(ids=vp(0x1002)) == 1 and q(off=vp(0x1001)) == 1
+    assert q(out=vp(0x20000001)) == 1 and q(base=vp(0x10000001)) == 1 and q(out=vp(0x20000002), odt=F32) == 1
+    assert q(st=1 << 39) == 2 and q(os=1 << 39) == 2 and q(bs=1 << 39) == 2
+    assert q(R=0, x=None, out=None) == 0
+    need = lib.moe_lora_product_workspace(2000, 64, 72, 16, 3, 2)
+    assert need > 0
+    for wk, nb in ((None, 0), (P, need - 1), (None, need)):
+        assert q(R=2000, wk=wk, nb=nb) == 4
+    assert q(R=2000, wk=ODD, nb=need) == 1
+    w = lib.moe_lora_product_workspace
+    assert w(-1, 64, 72, 16, 3, 2) == 0 and w(0, 64, 72, 16, 3, 2) == 0 and w(2000, 60, 72, 16, 3, 2) == 0
+    assert w(2000, 64, 72, 256, 3, 2) == 0
+
+
+def test_lora_out_may_be_base_but_share_no_other_memory(lib):
+    base = 0x1000000
+    R, N = 4, 72
+    row = 2 * N
+
+    def refused(x=0x9000000, base_=base, bs=N, out=base, os=N, R=R, K=64, st=64):
+        # (the workspace is missing: a call whose rows pass is refused for that)
+        p = lambda v: None if v is None else vp(v)  # noqa: E731
+        rc = lib.moe_lora_product(p(x), st, BF16, R, K, N, 16, 3, 1, P, P, P, None, None, p(base_), bs, p(out), os, BF16,
+                                  None, 0, None)
+        if rc == 1 and b"share" in lib.mq_last_error_message():
+            return True
+        assert rc == 4, lib.mq_last_error_message()
+        return False
+    R = 2000     # (tiles: a workspace is needed)
+    k = dict(R=R)
+    assert not refused(**k)                                         # in place
+    assert not refused(out=base + R * row, **k) and not refused(out=base - R * row, **k)
+    assert refused(out=base + row, **k) and refused(out=base - row, **k) and refused(out=base + 2, **k)
+    assert refused(out=base + R * row - 2, **k) and refused(bs=80, **k) and refused(os=80, **k)
+    # slices of one wider buffer: the rows alternate
+    assert not refused(out=base + row, bs=2 * N, os=2 * N, **k)
+    assert not refused(out=base - row, bs=2 * N, os=2 * N, **k)
+    assert refused(out=base + row - 2, bs=2 * N, os=2 * N, **k)
+    assert refused(out=base + row + 2, bs=2 * N, os=2 * N, **k)     # its end reaches base's next row
+    assert refused(x=base, **k) and refused(x=base + 16, base_=None, **k)
+    assert not refused(base_=None, **k)
+
+
 def test_binding_refusals(lib):
     """Wrong dtypes, devices, shapes and strides never reach the library."""
     from weight_quantized_moe_gb300 import binding as b
@@ -87,6 +148,15 @@ def test_binding_refusals(lib):
         b.moe_grouped_product_grad(x, x, w, dw_dtype=torch.float64)
     with pytest.raises(ValueError, match="CUDA"):
         b.moe_grouped_product_grad(x, x, w)
+    ids = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        b.moe_lora_product(x, w, w, ids)
+    with pytest.raises(TypeError):
+        b.moe_lora_product(x, w, w, ids, out_dtype=torch.int8)
+    with pytest.raises(TypeError):
+        b.moe_lora_product([1.0], w, w, ids, out_dtype=torch.float32)
+    with pytest.raises(ValueError, match="gradient"):
+        b.moe_lora_product(x, w.requires_grad_(), w, ids)
 
 
 @pytest.fixture(scope="module")
@@ -138,7 +208,34 @@ def test_compiled_calls_check_shapes_and_strides(fake, on):
     refused("dy must be", on(z(4, 16)), *grad[1:], call=calls.product_grad)
     refused("w's shape", *grad[:7], on(z(2, 64, 8)), 0, None, call=calls.product_grad)
     refused("order", *grad[:7], on(z(2, 64, 8).transpose(1, 2)), 0, None, call=calls.product_grad)
+    x, la, lb, ids = on(z(4, 64)), on(z(3, 2, 16, 64)), on(z(3, 2, 8, 16)), on(z(4, dtype=torch.int32))
+    lora = (x, la, lb, ids, None, off, None, on(z(4, 8)), 0, None)
+
+    def unfit(match, kind=ValueError, **change):
+        names = ("x", "la", "lb", "ids", "base", "off", "scaling", "out", "dt", "ws")
+        with pytest.raises(kind, match=match):
+            calls.lora(*[change.get(n, v) for n, v in zip(names, lora)])
+    unfit("lora_a must be", la=on(z(3, 2, 16, 72)))
+    unfit("lora_a must be", lb=on(z(3, 2, 8, 24)))
+    unfit("lora_a must be", lb=on(z(2, 2, 8, 16)))
+    unfit("lora_a must be", lb=on(z(3, 1, 8, 16)))
+    unfit("3 or 4 dims", la=on(z(16, 64)))
+    unfit("contiguous", la=on(z(3, 2, 64, 16).transpose(2, 3)))
+    unfit("BFloat16", kind=TypeError, la=on(z(3, 2, 16, 64, dtype=torch.float16)))
+    unfit("Int", kind=TypeError, ids=on(z(4, dtype=torch.int64)))
+    unfit("R = 4", ids=on(z(5, dtype=torch.int32)))
+    unfit("missing", off=None)
+    unfit("L = 3", scaling=on(z(2, dtype=torch.float32)))
+    unfit("Float", kind=TypeError, scaling=on(z(3)))
+    unfit("base must be \\[4, 8", base=on(z(4, 9)))
+    unfit("base must be BFloat16", kind=TypeError, base=on(z(4, 8, dtype=torch.float32)))
+    unfit("contiguous", base=on(z(8, 4).T))
+    unfit("out must be \\[4, 8", out=on(z(3, 8)))
+    unfit("cuda:0", ids=on(z(4, dtype=torch.int32), 1))
+    unfit("cuda:0", base=on(z(4, 8), 1))
     assert pretend.calls() == ([], 0)
+    calls.lora(*lora[:4], on(z(4, 40)[:, 3:11]), off, None, on(z(4, 48)[:, 8:16]), 0, None)
+    assert pretend.weights()[:2] == (40, 48)
 
 
 @pytest.mark.parametrize("device", [0, 1, 3])
@@ -148,7 +245,8 @@ def test_compiled_calls_launch_on_their_tensors_device(fake, on, device):
     off, ws = t(3, dtype=torch.int32), t(16, dtype=torch.uint8)
     calls.product(t(4, 64), t(2, 8, 64), off, t(4, 8), 0, ws)
     calls.product_grad(t(4, 8), t(4, 64), t(2, 8, 64), off, True, True, t(4, 64), t(2, 8, 64), 0, ws)
-    assert pretend.calls() == ([(device, 100 + device)] * 2, 0)
+    calls.lora(t(4, 64), t(3, 2, 16, 64), t(3, 2, 8, 16), t(4, dtype=torch.int32), None, off, None, t(4, 8), 0, ws)
+    assert pretend.calls() == ([(device, 100 + device)] * 3, 0)
 
 
 def test_weights_storage(fake, on):

@@ -24,6 +24,7 @@ MQ_OK, MQ_ERR_INVALID_ARG, MQ_ERR_UNSUPPORTED, MQ_ERR_CUDA, MQ_ERR_WORKSPACE = r
 MQ_DEV_BAD_EXPERT_ID = 0x1
 MQ_DEV_WAIT_TIMEOUT = 0x2
 MQ_DEV_BAD_OFFSETS = 0x4
+MQ_DEV_BAD_ADAPTER_ID = 0x8
 # moe_quant_forward_ex option flags (include/moeq.h)
 MQ_FWD_W8_UINT8 = 0x1
 MQ_FWD_SCALE_F16 = 0x2
@@ -96,6 +97,9 @@ _SIGNATURES = {
     "moe_grouped_product_grad_workspace": (_sz, [_i64, _i32, _i32, _i32]),
     "moe_grouped_product_grad": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i32, _i32, _i32, _vp,
                                         _i64, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
+    "moe_lora_product_workspace": (_sz, [_i64] + [_i32] * 5),
+    "moe_lora_product": (_i32, [_vp, _i64, _i32, _i64, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
+                                _vp, _vp, _vp, _i64, _vp, _i64, _i32, _vp, _sz, _vp]),
     "mq_kernel_launch_count": (ctypes.c_longlong, []),
     "mq_test_layer_wait_extra": (_i32, [_i32]),
     "mq_profile_enable": (_i32, [_i32]),
@@ -661,6 +665,43 @@ def moe_grouped_product_grad(dy, a, w, expert_offsets=None, need_a=True, need_w=
         raise TypeError(f"dw must be bfloat16, float16 or float32, got {dw_dtype}")
     return (_grouped or _grouped_binding()).product_grad(dy, a, w, expert_offsets, need_a, need_w,
                                                          da, dw, _DTYPES[dw_dtype], workspace)
+
+
+def moe_lora_product_workspace(R, K, N, r, L, E=1) -> int:
+    return int(lib().moe_lora_product_workspace(R, K, N, r, L, E))
+
+
+def moe_lora_product(x, lora_a, lora_b, adapter_ids, base=None, expert_offsets=None, scaling=None,
+                     out=None, out_dtype=None, workspace=None, stream=None):
+    """Low-rank adapters of many requests in one call (moe_lora_product in
+    include/moeq.h): base[t] + scaling[l] * lora_b[l, e] @ (lora_a[l, e] @ x[t]) for row
+    t with adapter l = adapter_ids[t] (int32 [R]; -1: none, the row is base's) and
+    expert e (expert_offsets int32 [E + 1]; without, adapters are [L, r, K] and
+    [L, N, r]).  x [R, K], lora_a [L, E, r, K] and lora_b [L, E, N, r] are bf16 or f16
+    alike; scaling float32 [L], 1 by default.  base is another product's result [R, N]
+    (0 where it is not given) in the dtype of the result: out's or out_dtype, by
+    default base's, else x's.  out may be base: the adapters are added in place.  Rows of
+    x, base and out may be strided (x by multiples of 8 elements).
+
+    The call has no gradient.  Adapters are trained as two moe_grouped_product calls over
+    rows that are sorted by adapter."""
+    if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False)
+                                       for t in (x, lora_a, lora_b, base, scaling, out)):
+        raise ValueError("moe_lora_product has no gradient: call it under torch.no_grad(), or train "
+                         "adapters through moe_grouped_product")
+    if stream is not None:
+        with _given(stream, x):
+            return moe_lora_product(x, lora_a, lora_b, adapter_ids, base, expert_offsets, scaling,
+                                    out, out_dtype, workspace)
+    if out is not None:
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = getattr(x if base is None else base, "dtype", None)
+    if out_dtype not in _DTYPES:
+        raise TypeError(f"out must be bfloat16, float16 or float32, got {out_dtype}")
+    return (_grouped or _grouped_binding()).lora(x, lora_a, lora_b, adapter_ids, base,
+                                                 expert_offsets, scaling, out, _DTYPES[out_dtype],
+                                                 workspace)
 
 
 def _rows16(t, dtype):

@@ -2,6 +2,7 @@
 // Every exported function is declared, with its contract, in include/moeq.h.
 #include "common.cuh"
 #include "grouped.cuh"
+#include "lora.cuh"
 #include "mx.cuh"
 
 #include <algorithm>
@@ -1114,6 +1115,88 @@ MQ_EXPORT int moe_grouped_product_grad(const void* dy, int64_t dy_stride, const 
     g.out = dw; g.out_dtype = dw_dtype;
     g.zero_outside = false;
     return gg_run(g, workspace, ws_bytes, st);
+  }
+  return MQ_OK;
+}
+
+static bool lora_sizes_ok(int64_t R, int K, int N, int r, int L, int E) {
+  constexpr int kTop = 1 << 30;
+  return R >= 0 && R < kTop && K > 0 && N > 0 && K % 8 == 0 && K < kTop && N < kTop && r >= 8 && r <= 128 &&
+         r % 8 == 0 && L >= 1 && E >= 1 && E <= 1024 && (int64_t)L * E < kTop &&
+         (R + 127) / 128 * (((int64_t)N + 127) / 128) < (int64_t(1) << 27) &&
+         (int64_t)L * E < (int64_t(1) << 48) / ((int64_t)K + N);
+}
+
+MQ_EXPORT size_t moe_lora_product_workspace(int64_t R, int K, int N, int r, int L, int E) {
+  if (!lora_sizes_ok(R, K, N, r, L, E) || R == 0) return 0;
+  const LoraPlan pl = lora_plan(R, K, N, r, L, E);
+  return pl.rows ? 0 : align256(sizeof(float) * (size_t)pl.splits * (size_t)R * (size_t)r);
+}
+
+// Whether R rows of `len` bytes, `stride` bytes apart, share a byte with R others.
+// (With equal strides exactly; with others, whether the ranges do.)
+static bool rows_overlap(const void* p, int64_t stride, int64_t len, const void* q, int64_t q_stride,
+                         int64_t q_len, int64_t R) {
+  const int64_t a = (int64_t)reinterpret_cast<uintptr_t>(p), b = (int64_t)reinterpret_cast<uintptr_t>(q);
+  if (a + (R - 1) * stride + len <= b || b + (R - 1) * q_stride + q_len <= a) return false;
+  if (stride != q_stride || R <= 1) return true;
+  const int64_t d = b >= a ? (b - a) % stride : stride - 1 - (a - b - 1) % stride;  // of q's rows in p's
+  return d < len || d + q_len > stride;
+}
+
+MQ_EXPORT int moe_lora_product(const void* x, int64_t x_stride, int dtype, int64_t R, int K, int N, int r,
+                               int L, int E, const void* lora_a, const void* lora_b,
+                               const int32_t* adapter_ids, const int32_t* expert_offsets,
+                               const float* scaling, const void* base, int64_t base_stride, void* out,
+                               int64_t out_stride, int out_dtype, void* workspace, size_t ws_bytes,
+                               void* stream) {
+  if (!dtype_ok(dtype) || !dtype_ok(out_dtype)) return fail(MQ_ERR_INVALID_ARG, "unknown dtype");
+  if (!half_ok(dtype)) return fail(MQ_ERR_UNSUPPORTED, "rows and adapters must be bfloat16 or float16");
+  if (R < 0 || K <= 0 || N <= 0 || r <= 0 || L < 1 || E < 1)
+    return fail(MQ_ERR_INVALID_ARG, "bad R, K, N, r, L or E");
+  if (K % 8 || r % 8) return fail(MQ_ERR_INVALID_ARG, "K and r must be multiples of 8");
+  if (!lora_sizes_ok(R, K, N, r, L, E))
+    return fail(MQ_ERR_UNSUPPORTED, "need r <= 128, E <= 1024, and R, K, N and L * E < 2^30, fewer than 2^27 tiles");
+  if (!expert_offsets && E != 1)
+    return fail(MQ_ERR_INVALID_ARG, "expert_offsets may be NULL with E = 1 only");
+  if (!gg_row_stride_ok(x_stride, K, R))
+    return fail(MQ_ERR_INVALID_ARG, "x_stride must be a multiple of 8, at least K");
+  if (R > 1 && (out_stride < N || (base && base_stride < N)))
+    return fail(MQ_ERR_INVALID_ARG, "row strides must be at least a row's length");
+  if (R == 0) return MQ_OK;
+  if (!x || !lora_a || !lora_b || !adapter_ids || !out) return fail(MQ_ERR_INVALID_ARG, "null pointer");
+  const int64_t size = out_dtype == MQ_DTYPE_F32 ? 4 : 2;
+  if (!aligned16(x) || !aligned16(lora_a) || !aligned16(lora_b) || !aligned4(adapter_ids) ||
+      (expert_offsets && !aligned4(expert_offsets)) || (scaling && !aligned4(scaling)) ||
+      reinterpret_cast<uintptr_t>(out) % size || reinterpret_cast<uintptr_t>(base) % size)
+    return fail(MQ_ERR_INVALID_ARG, "x and the adapters must be 16-byte aligned, other pointers to their elements");
+  if (!gg_map_strides(x_stride, R, K, nullptr, 1) || !gg_map_strides(out_stride, R, N, nullptr, 1) ||
+      !gg_map_strides(base_stride, base ? R : 1, N, nullptr, 1))
+    return fail(MQ_ERR_UNSUPPORTED, "strides of 2^39 elements or more");
+  if (rows_overlap(out, out_stride * size, N * size, x, x_stride * 2, (int64_t)K * 2, R) ||
+      (base && !(base == out && (base_stride == out_stride || R == 1)) &&
+       rows_overlap(out, out_stride * size, N * size, base, base_stride * size, N * size, R)))
+    return fail(MQ_ERR_INVALID_ARG, "out must not share memory with x, or with base other than as the same rows");
+  const LoraPlan pl = lora_plan(R, K, N, r, L, E);
+  const size_t need = moe_lora_product_workspace(R, K, N, r, L, E);
+  if (need && (!workspace || ws_bytes < need))
+    return fail(MQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace ? ws_bytes : 0, need);
+  if (need && !aligned16(workspace)) return fail(MQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  LoraArgs g = {};
+  g.bf16 = dtype == MQ_DTYPE_BF16;
+  g.x = x; g.x_stride = x_stride;
+  g.R = R; g.K = K; g.N = N; g.r = r; g.L = L; g.E = E;
+  g.a = lora_a; g.b = lora_b;
+  g.ids = adapter_ids; g.offsets = expert_offsets; g.scaling = scaling;
+  g.base = base; g.base_stride = base_stride;
+  g.out = out; g.out_stride = out_stride; g.out_dtype = out_dtype;
+  g.part = static_cast<float*>(workspace);
+  g.status = status_ptr();
+  for (int which = 0; which < (pl.rows ? 1 : 2); ++which) {
+    LaunchScope ls(which ? MQ_PROF_GEMM2 : MQ_PROF_GEMM1, st);
+    const cudaError_t err = launch_lora(g, pl, which, st);
+    if (err != cudaSuccess) return cuda_fail(err, "lora_product launch");
   }
   return MQ_OK;
 }

@@ -141,8 +141,78 @@ PyObject* product_grad(PyObject* const* v) {
   return wrap_all({da, dw});
 }
 
+// Adapters [L, E, rows, cols], or [L, rows, cols] for one expert.
+const at::Tensor& adapters(PyObject* o, const char* name, const Rows& x, int64_t& L, int64_t& E) {
+  const at::Tensor& t = dense(o, x.t.scalar_type(), -1, x.t, name);
+  if (t.dim() != 3 && t.dim() != 4) raise(PyExc_ValueError, "%s must have 3 or 4 dims", name);
+  L = t.size(0);
+  E = t.dim() == 4 ? t.size(1) : 1;
+  return t;
+}
+
+// Rows [R, N] of a given type that may be strided: their stride.
+int64_t strided(const at::Tensor& t, at::ScalarType type, int64_t R, int64_t N, const at::Tensor& first,
+                const char* name) {
+  if (t.scalar_type() != type)
+    raise(PyExc_TypeError, "%s must be %s, got %s", name, c10::toString(type), c10::toString(t.scalar_type()));
+  on_cuda(t, name);
+  same_device(t, first, name);
+  if (t.dim() != 2 || t.size(0) != R || t.size(1) != N)
+    raise(PyExc_ValueError, "%s must be [%ld, %ld]", name, (long)R, (long)N);
+  if (N > 1 && t.stride(1) != 1)
+    raise(PyExc_ValueError, "%s: the elements of a row must be contiguous", name);
+  return R <= 1 ? N : t.stride(0);
+}
+
+// (x, lora_a, lora_b, adapter_ids, base, expert_offsets, scaling, out, out dtype code, workspace)
+PyObject* lora(PyObject* const* v) {
+  const Rows x = rows(v[0], "x");
+  const OnDevice on(x.t);
+  int64_t L, E, Lb, Eb;
+  const at::Tensor& a = adapters(v[1], "lora_a", x, L, E);
+  const at::Tensor& b = adapters(v[2], "lora_b", x, Lb, Eb);
+  const int64_t r = a.size(-2), K = x.C, N = b.size(-2), R = x.R;
+  if (a.size(-1) != K || b.size(-1) != r || Lb != L || Eb != E || b.dim() != a.dim())
+    raise(PyExc_ValueError, "lora_a must be [L, E, r, K] and lora_b [L, E, N, r] (or both without E)");
+  const at::Tensor& ids = dense(v[3], at::kInt, 1, x.t, "adapter_ids");
+  if (ids.size(0) != R) raise(PyExc_ValueError, "adapter_ids must hold R = %ld values", (long)R);
+  const long dt = as_long(v[8]);
+  const at::ScalarType type = scalar_type(dt);
+  at::Tensor base, out;
+  int64_t base_stride = N, out_stride = N;
+  if (v[4] != Py_None) {
+    base = tensor(v[4], "base");
+    base_stride = strided(base, type, R, N, x.t, "base");
+  }
+  const int32_t* offsets = expert_offsets(v[5], E, x.t);
+  const float* scaling = nullptr;
+  if (v[6] != Py_None) {
+    const at::Tensor& s = dense(v[6], at::kFloat, 1, x.t, "scaling");
+    if (s.size(0) != L) raise(PyExc_ValueError, "scaling must hold L = %ld values", (long)L);
+    scaling = static_cast<const float*>(s.data_ptr());
+  }
+  int_sizes({K, N, r, L, E});
+  if (v[7] != Py_None) {
+    out = tensor(v[7], "out");
+    out_stride = strided(out, type, R, N, x.t, "out");
+  } else {
+    out = at::empty({R, N}, x.t.options().dtype(type));
+  }
+  const at::Tensor wksp = workspace(
+      v[9],
+      v[9] == Py_None ? moe_lora_product_workspace(R, (int)K, (int)N, (int)r, (int)L, (int)E) : 0, x.t);
+  check(call([&] {
+    return moe_lora_product(x.t.data_ptr(), x.stride, x.dtype, R, (int)K, (int)N, (int)r, (int)L, (int)E,
+                            a.data_ptr(), b.data_ptr(), static_cast<const int32_t*>(ids.data_ptr()), offsets,
+                            scaling, ptr(base), base_stride, out.data_ptr(), out_stride, (int)dt, ptr(wksp),
+                            wksp.defined() ? (size_t)wksp.numel() : 0, on.stream);
+  }));
+  return wrap(out);
+}
+
 PyMethodDef g_methods[] = {method<product, 6>("product"),
                            method<product_grad, 10>("product_grad"),
+                           method<lora, 10>("lora"),
                            method<set_error_class, 1>("set_error_class"),
                            {nullptr, nullptr, 0, nullptr}};
 
