@@ -82,7 +82,7 @@ __device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8], 
 // BF16: type of rows and adapters.  LPO: lanes that share an output, r / 8 rounded up
 // to a power of two.
 template <bool BF16, int LPO>
-__global__ void __launch_bounds__(kRowThreads) lora_rows(const LoraArgs p) {
+__global__ void __launch_bounds__(kRowThreads, 4) lora_rows(const LoraArgs p) {
   __shared__ float parts[kCluster][kMaxRank];
   __shared__ float h[kMaxRank];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -212,26 +212,33 @@ __global__ void __launch_bounds__(kRowThreads) lora_rows(const LoraArgs p) {
 struct Table {
   int key[kTile];        // group of a row as an index into the adapters (l E + e); -1 none, -2 not written
   int group_key[kTile];  // key of each of the tile's groups, in order of their first rows
-  uint8_t slot[kTile];   // a row's group; kNone, kOut
-  uint8_t blocks[kTile]; // the 16-row blocks that hold rows of a group
+  unsigned blocks[kTile];               // the 16-row blocks that hold rows of a group
+  alignas(16) uint8_t slot[kTile];      // a row's group; kNone, kOut
   unsigned first[kTile / 32];
   int groups, rows;
   int inside;            // rows that are written
 };
 constexpr int kNone = 255, kOut = 254;
 
-// Fills in the table of tile `tile`, with all threads of the CTA (at least kTile);
-// `offsets` is a copy of the experts' in shared memory (null: one expert).
+// Joins THREADS threads that start at warp 0 (barrier 2); all of them take part below.
+template <int THREADS>
+__device__ __forceinline__ void join() {
+  asm volatile("bar.sync 2, %0;" ::"n"(THREADS) : "memory");
+}
+
+// Fills in the table of tile `tile`, with the first THREADS threads of the CTA (at least
+// kTile); `offsets` is a copy of the experts' in shared memory (null: one expert).
+template <int THREADS>
 __device__ __forceinline__ void build_table(Table& tb, const LoraArgs& p, const int* offsets, bool bad,
-                                            int tile) {
-  const int t = threadIdx.x;
+                                            int t, int tile) {
   const int64_t row0 = (int64_t)tile * kTile;
   const int rows = (int)min((int64_t)kTile, p.R - row0);
-  __syncthreads();  // (the last table is no longer read)
+  join<THREADS>();  // (the last table is no longer read)
   int key = -2;
   if (t < kTile) {
     if (t < rows && !bad) {
       const int64_t row = row0 + t;
+      const int l = p.ids[row];
       int e = 0;
       bool in = true;
       if (offsets) {
@@ -245,7 +252,6 @@ __device__ __forceinline__ void build_table(Table& tb, const LoraArgs& p, const 
         in = e < p.E && row >= offsets[0];
       }
       if (in) {
-        const int l = p.ids[row];
         if (l < -1 || l >= p.L) mq::flag(p.status, MQ_DEV_BAD_ADAPTER_ID);
         key = l >= 0 && l < p.L ? l * p.E + e : -1;
       }
@@ -257,12 +263,20 @@ __device__ __forceinline__ void build_table(Table& tb, const LoraArgs& p, const 
     tb.rows = rows;
     tb.inside = 0;
   }
-  __syncthreads();
+  join<THREADS>();
   int at = t;  // the first row of this row's group
   if (t < kTile) {
-    if (key >= 0)
-      for (int i = kTile - 1; i >= 0; --i)
-        if (i < t && tb.key[i] == key) at = i;
+    if (key >= 0) {
+      const int4* keys = reinterpret_cast<const int4*>(tb.key);
+#pragma unroll 8
+      for (int i = kTile / 4 - 1; i >= 0; --i) {
+        const int4 k = keys[i];
+        if (k.w == key) at = min(at, 4 * i + 3);
+        if (k.z == key) at = min(at, 4 * i + 2);
+        if (k.y == key) at = min(at, 4 * i + 1);
+        if (k.x == key) at = min(at, 4 * i);
+      }
+    }
     const unsigned firsts = __ballot_sync(0xffffffffu, key >= 0 && at == t);
     const unsigned in = __ballot_sync(0xffffffffu, key != -2);
     if ((t & 31) == 0) {
@@ -270,27 +284,24 @@ __device__ __forceinline__ void build_table(Table& tb, const LoraArgs& p, const 
       atomicAdd(&tb.inside, __popc(in));
     }
   }
-  __syncthreads();
+  join<THREADS>();
   if (t < kTile) {
-    int g = 0;
-    for (int w = 0; w < (at >> 5); ++w) g += __popc(tb.first[w]);
-    g += __popc(tb.first[at >> 5] & ((1u << (at & 31)) - 1u));
-    tb.slot[t] = (uint8_t)(key >= 0 ? g : key == -1 ? kNone : kOut);
-    if (key >= 0 && at == t) tb.group_key[g] = key;
-    if (t == kTile - 1) {
-      int n = 0;
-      for (int w = 0; w < kTile / 32; ++w) n += __popc(tb.first[w]);
-      tb.groups = n;
+    int g = 0, n = 0;
+#pragma unroll
+    for (int w = 0; w < kTile / 32; ++w) {
+      const unsigned f = tb.first[w];
+      n += __popc(f);
+      g += w < (at >> 5) ? __popc(f) : w == (at >> 5) ? __popc(f & ((1u << (at & 31)) - 1u)) : 0;
     }
+    const int slot = key >= 0 ? g : key == -1 ? kNone : kOut;
+    tb.slot[t] = (uint8_t)slot;
+    if (key >= 0 && at == t) tb.group_key[g] = key;
+    if (t == 0) tb.groups = n;
+    const unsigned peers = __match_any_sync(0xffffffffu, slot);
+    if (key >= 0 && (peers & ((1u << (t & 31)) - 1u)) == 0)
+      atomicOr(&tb.blocks[g], ((peers & 0xffffu ? 1u : 0u) | (peers >> 16 ? 2u : 0u)) << (t >> 5) * 2);
   }
-  __syncthreads();
-  if (t < kTile) {  // group t's blocks
-    unsigned m = 0;
-    if (t < tb.groups)
-      for (int i = 0; i < kTile; ++i) m |= (tb.slot[i] == t ? 1u : 0u) << (i >> 4);
-    tb.blocks[t] = (uint8_t)m;
-  }
-  __syncthreads();
+  join<THREADS>();
 }
 
 // The offsets' copy in shared memory; true where they fall or leave [0, R].
@@ -308,6 +319,11 @@ __device__ __forceinline__ bool copy_offsets(const LoraArgs& p, int* to) {
 }
 
 __device__ __forceinline__ int ceil16(int n) { return (n + 15) & -16; }
+
+__device__ __forceinline__ int byte_of(const uint4& v, int i) {
+  const uint32_t w = i < 4 ? v.x : i < 8 ? v.y : i < 12 ? v.z : v.w;
+  return (int)(w >> (i & 3) * 8 & 0xff);
+}
 
 // ---- first launch: h = A x ----
 constexpr int kDownThreads = 256;
@@ -357,7 +373,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   const int split = blockIdx.x % splits;
   const int mpart = blockIdx.x / splits % mparts;
   const int tile = blockIdx.x / (splits * mparts);
-  build_table(sh->table, p, p.offsets ? sh->offsets : nullptr, bad, tile);
+  build_table<kDownThreads>(sh->table, p, p.offsets ? sh->offsets : nullptr, bad, tid, tile);
   const Table& tb = sh->table;
   tc_fence_before();
   __syncthreads();
@@ -447,15 +463,16 @@ __global__ void __launch_bounds__(kDownThreads, 1)
       for (int b = b0; b < min(b0 + kBatch, mine); ++b) {
         const int g = (mpart + b * mparts) * per + gl;
         const bool live = g < tb.groups && j < p.r;
-        const unsigned any = __reduce_or_sync(0xffffffffu, live ? (unsigned)tb.blocks[g] : 0u);
+        const unsigned any = __reduce_or_sync(0xffffffffu, live ? tb.blocks[g] : 0u);
         float* dst = p.part + ((int64_t)split * p.R + row0) * p.r + j;
         for (int c = 0; c < kTile / 16; ++c) {
           if (!(any >> c & 1)) continue;
           uint32_t v[16];
           tmem_ld16_sync(tmem + (b - b0) * kTile + c * 16 + ((uint32_t)(quad * 32) << 16), v);
+          const uint4 of = *reinterpret_cast<const uint4*>(tb.slot + c * 16);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (live && tb.slot[c * 16 + i] == g) dst[(int64_t)(c * 16 + i) * p.r] = __uint_as_float(v[i]);
+            if (live && byte_of(of, i) == g) dst[(c * 16 + i) * p.r] = __uint_as_float(v[i]);
         }
       }
       tc_fence_before();
@@ -470,15 +487,20 @@ __global__ void __launch_bounds__(kDownThreads, 1)
 }
 
 // ---- second launch: out = base + B (s h) ----
-constexpr int kUpThreads = 384;
-constexpr int kUpSlots = 4;        // of 16 KB: 128 outputs by 64 ranks of a group
+// Warps 0 (B), 1 (MMAs) and 4-11 (epilogue) meet at each tile, warps 12 and up do not:
+// warp 12 streams base.
+constexpr int kUpThreads = 416;
+constexpr int kUpJoined = 384;
+constexpr int kIoWarp = 12;
+constexpr int kUpBytes = 65536;    // of 128 outputs by up to 64 ranks of a group a slot
+constexpr int kMaxUpSlots = 16;
 constexpr int kUpEpi = 8;          // epilogue warps
 constexpr int kIoBytes = kTile * kTile * 2;
 constexpr int kMaxIo = 3;
 constexpr int kAccs = 4;           // accumulators in flight, one group each
 
 struct UpCtl {
-  uint64_t full[kUpSlots], empty[kUpSlots];
+  uint64_t full[kMaxUpSlots], empty[kMaxUpSlots];
   uint64_t acc_full[kAccs], acc_empty[kAccs];
   uint64_t io_full[kMaxIo], io_empty[kMaxIo];
   uint64_t drain;
@@ -488,7 +510,7 @@ struct UpCtl {
 struct UpShared {
   UpCtl ctl;
   Table table;
-  float row_scale[kTile];  // 2^m of each row
+  alignas(16) float row_scale[kTile];  // 2^m of each row
   int offsets[kMaxE + 1];
 };
 
@@ -499,6 +521,8 @@ struct UpShape {
   int ntiles;  // of 128 outputs
   int units;   // (tile, part, 128 outputs)
   int nio;     // buffers of base and out; 0: read and written element by element
+  int line;    // bytes of a slot's lines: min(64, rp) ranks
+  int slots;   // kUpBytes / (128 * line)
 };
 
 __device__ __forceinline__ void epilogue_barrier() {
@@ -521,59 +545,84 @@ __device__ __forceinline__ float finite(float v) { return isfinite(v) ? fabsf(v)
 __device__ __forceinline__ void build_rows(uint8_t* hs, UpShared* sh, const LoraArgs& p, const UpShape& u,
                                            int64_t row0) {
   const Table& tb = sh->table;
-  const int sub = threadIdx.x & 7;
-  for (int t = threadIdx.x >> 3; t < kTile; t += kUpThreads / 8) {
-    const int key = tb.key[t];
-    const bool live = key >= 0;
-    const float s = live && p.scaling ? p.scaling[key / p.E] : 1.0f;
-    float4 v[4];
-    float most = 0;
+  constexpr int kPass = kUpJoined / 8;                   // rows at a time
+  constexpr int kTurns = (kTile + kPass - 1) / kPass;
+  const int sub = threadIdx.x & 7, first = threadIdx.x >> 3;
+  for (int c0 = 0; c0 < u.rp; c0 += 64) {  // (128 ranks: in two halves, the largest of both first)
+    float4 v[kTurns][2];
+    float s[kTurns], most[kTurns];
+    int key[kTurns];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int j = c * 32 + sub * 4;
-      v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (live && j < p.r) {
-        const float* src = p.part + (row0 + t) * p.r + j;
-#pragma unroll 4
-        for (int k = 0; k < u.splits; ++k) {
-          const float4 q = *reinterpret_cast<const float4*>(src + (int64_t)k * p.R * p.r);
-          v[c].x += q.x;
-          v[c].y += q.y;
-          v[c].z += q.z;
-          v[c].w += q.w;
-        }
-        v[c].x *= s;
-        v[c].y *= s;
-        v[c].z *= s;
-        v[c].w *= s;
-        most = fmaxf(fmaxf(most, fmaxf(finite(v[c].x), finite(v[c].y))), fmaxf(finite(v[c].z), finite(v[c].w)));
-      }
+    for (int q = 0; q < kTurns; ++q) {
+      const int t = first + q * kPass;
+      key[q] = t < kTile ? tb.key[t] : -1;
+      s[q] = key[q] >= 0 && p.scaling ? p.scaling[key[q] / p.E] : 1.0f;
+      most[q] = 0;
     }
+    auto fetch = [&](int base) {
 #pragma unroll
-    for (int o = 4; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    // 2^m with m the exponent of the largest, kept to where 2^m and 2^-m are normal
-    const int e = min(max((int)(__float_as_uint(most) >> 23), 1), 253);
-    const float up = __uint_as_float((uint32_t)e << 23), down = __uint_as_float((uint32_t)(254 - e) << 23);
-    if (sub == 0) sh->row_scale[t] = up;
+      for (int q = 0; q < kTurns; ++q)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int j = c * 32 + sub * 4;
-      if (j >= u.rp) continue;
-      const float f[4] = {v[c].x * down, v[c].y * down, v[c].z * down, v[c].w * down};
-      uint16_t hi[4], lo[4];
+        for (int c = 0; c < 2; ++c) v[q][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int k = 0; k < u.splits; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        hi[i] = to_half_bits(f[i], p.bf16);
-        const float rest = f[i] - from_half_bits(hi[i], p.bf16);
-        lo[i] = to_half_bits(isfinite(rest) ? rest : 0.0f, p.bf16);  // (infinity minus itself)
-      }
+        for (int q = 0; q < kTurns; ++q)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint16_t* q = half ? lo : hi;
-        const int k = j + half * u.rp;
-        const int chunk = ((k & 63) >> 3) ^ (t & 7);
-        uint2* dst = reinterpret_cast<uint2*>(hs + (k >> 6) * kSlot + t * 128 + chunk * 16 + (k & 7) * 2);
-        *dst = make_uint2(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16);
+          for (int c = 0; c < 2; ++c) {
+            const int j = base + c * 32 + sub * 4;
+            if (key[q] < 0 || j >= p.r) continue;
+            const float4 w = *reinterpret_cast<const float4*>(
+                p.part + ((int64_t)k * p.R + row0 + first + q * kPass) * p.r + j);
+            v[q][c].x += w.x;
+            v[q][c].y += w.y;
+            v[q][c].z += w.z;
+            v[q][c].w += w.w;
+          }
+#pragma unroll
+      for (int q = 0; q < kTurns; ++q)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float4& w = v[q][c];
+          w.x *= s[q];
+          w.y *= s[q];
+          w.z *= s[q];
+          w.w *= s[q];
+          most[q] = fmaxf(fmaxf(most[q], fmaxf(finite(w.x), finite(w.y))), fmaxf(finite(w.z), finite(w.w)));
+        }
+    };
+    if (u.rp == 128) fetch(64 - c0);
+    fetch(c0);
+#pragma unroll
+    for (int q = 0; q < kTurns; ++q) {
+      const int t = first + q * kPass;
+#pragma unroll
+      for (int o = 4; o; o >>= 1) most[q] = fmaxf(most[q], __shfl_xor_sync(0xffffffffu, most[q], o));
+      if (t >= kTile) continue;
+      // 2^m with m the exponent of the largest, kept to where 2^m and 2^-m are normal
+      const int e = min(max((int)(__float_as_uint(most[q]) >> 23), 1), 253);
+      const float up = __uint_as_float((uint32_t)e << 23), down = __uint_as_float((uint32_t)(254 - e) << 23);
+      if (sub == 0) sh->row_scale[t] = up;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int j = c0 + c * 32 + sub * 4;
+        if (j >= u.rp) continue;
+        const float f[4] = {v[q][c].x * down, v[q][c].y * down, v[q][c].z * down, v[q][c].w * down};
+        uint16_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          hi[i] = to_half_bits(f[i], p.bf16);
+          const float rest = f[i] - from_half_bits(hi[i], p.bf16);
+          lo[i] = to_half_bits(isfinite(rest) ? rest : 0.0f, p.bf16);  // (infinity minus itself)
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint16_t* h = half ? lo : hi;
+          const int k = j + half * u.rp;
+          const int chunk = ((k & 63) >> 3) ^ (t & 7);
+          uint2* dst = reinterpret_cast<uint2*>(hs + (k >> 6) * kSlot + t * 128 + chunk * 16 + (k & 7) * 2);
+          *dst = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+        }
       }
     }
   }
@@ -585,7 +634,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* hs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* slots = hs + ((2 * u.rp + 63) / 64) * kSlot;
-  uint8_t* io = slots + kUpSlots * kSlot;
+  uint8_t* io = slots + kUpBytes;
   UpShared* sh = reinterpret_cast<UpShared*>(io + u.nio * kIoBytes);
   UpCtl* ctl = &sh->ctl;
   const Table& tb = sh->table;
@@ -594,7 +643,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     tma_prefetch_desc(&map_b);
     tma_prefetch_desc(&map_base);
     tma_prefetch_desc(&map_out);
-    for (int i = 0; i < kUpSlots; ++i) {
+    for (int i = 0; i < u.slots; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], 1);
     }
@@ -632,46 +681,69 @@ __global__ void __launch_bounds__(kUpThreads, 1)
   // each role's place in its rings
   uint32_t w_it = 0, acc_it = 0, io_it = 0;
   bool ok = true;
-  for (int ua = u0, ub; ua < u1; ua = ub) {
+  if (warp == kIoWarp) {
+    // ------------------------------------------------------------- base --
+    // Runs ahead of the other warps, over the ends of tiles; so it finds out by itself
+    // which tiles have nothing to do.
+    const bool el = elect_one();
+    for (int un = u0, tile = -1; u.nio && un < u1 && ok; ++un) {
+      if (un / per_tile != tile) {
+        tile = un / per_tile;
+        bool some = false;
+        for (int t = lane; t < kTile; t += 32) {
+          const int64_t row = (int64_t)tile * kTile + t;
+          if (bad || row >= p.R || (p.offsets && (row < sh->offsets[0] || row >= sh->offsets[p.E]))) continue;
+          const int l = p.ids[row];
+          some |= p.base != p.out || (l >= 0 && l < p.L);
+        }
+        if (!__any_sync(0xffffffffu, some)) {
+          un = min(u1, (tile + 1) * per_tile) - 1;
+          continue;
+        }
+      }
+      const uint32_t s = io_it % u.nio;
+      ok = warp_wait(&ctl->io_empty[s], ((io_it / u.nio) & 1) ^ 1, ctl, p.status);
+      if (!ok) break;
+      if (el) {
+        if (add) {
+          mbar_arrive_expect_tx(&ctl->io_full[s], kIoBytes);
+          tma_load_2d(io + s * kIoBytes, &map_base, &ctl->io_full[s], un % per_part * kTile, tile * kTile);
+        } else {
+          mbar_arrive(&ctl->io_full[s]);
+        }
+      }
+      ++io_it;
+    }
+    if (ctl->abort_flag)  // loads in flight land before the CTA goes
+      for (uint32_t j = io_it < (uint32_t)u.nio ? 0 : io_it - u.nio; j < io_it; ++j)
+        wait_drain(&ctl->io_full[j % u.nio], (j / u.nio) & 1);
+  }
+  for (int ua = u0, ub; ua < u1 && warp != kIoWarp; ua = ub) {
     const int tile = ua / per_tile;
     ub = min(u1, (tile + 1) * per_tile);
     const int64_t row0 = (int64_t)tile * kTile;
-    build_table(sh->table, p, p.offsets ? sh->offsets : nullptr, bad, tile);
-    build_rows(hs, sh, p, u, row0);
-    fence_proxy_async_smem();
-    __syncthreads();
+    build_table<kUpJoined>(sh->table, p, p.offsets ? sh->offsets : nullptr, bad, tid, tile);
     const bool nothing = tb.inside == 0 || (tb.groups == 0 && p.base == p.out);
     if (nothing) continue;
+    build_rows(hs, sh, p, u, row0);
+    fence_proxy_async_smem();
+    join<kUpJoined>();
     const bool whole = tb.inside == tb.rows && u.gparts == 1;
 
     if (warp == 0) {
-      // -------------------------------------------- base and groups' B --
+      // ------------------------------------------------------ groups' B --
       const bool el = elect_one();
       for (int un = ua; un < ub && ok; ++un) {
         const int n0 = un % per_part * kTile, part = un % per_tile / per_part;
         const int g0 = tb.groups * part / u.gparts, g1 = tb.groups * (part + 1) / u.gparts;
-        if (u.nio) {
-          const uint32_t s = io_it % u.nio;
-          ok = warp_wait(&ctl->io_empty[s], ((io_it / u.nio) & 1) ^ 1, ctl, p.status);
-          if (!ok) break;
-          if (el) {
-            if (add) {
-              mbar_arrive_expect_tx(&ctl->io_full[s], kIoBytes);
-              tma_load_2d(io + s * kIoBytes, &map_base, &ctl->io_full[s], n0, (int)row0);
-            } else {
-              mbar_arrive(&ctl->io_full[s]);
-            }
-          }
-          ++io_it;
-        }
         for (int g = g0; g < g1 && ok; ++g)
           for (int k = 0; k < kblocks; ++k) {
-            const uint32_t s = w_it % kUpSlots;
-            ok = warp_wait(&ctl->empty[s], ((w_it / kUpSlots) & 1) ^ 1, ctl, p.status);
+            const uint32_t s = w_it % u.slots;
+            ok = warp_wait(&ctl->empty[s], ((w_it / u.slots) & 1) ^ 1, ctl, p.status);
             if (!ok) break;
             if (el) {
-              mbar_arrive_expect_tx(&ctl->full[s], kSlot);
-              tma_load_3d(slots + s * kSlot, &map_b, &ctl->full[s], k * 64, n0, tb.group_key[g]);
+              mbar_arrive_expect_tx(&ctl->full[s], kTile * u.line);
+              tma_load_3d(slots + s * kTile * u.line, &map_b, &ctl->full[s], k * 64, n0, tb.group_key[g]);
             }
             ++w_it;
           }
@@ -679,27 +751,30 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     } else if (warp == 1) {
       // ----------------------------------------------------------- MMAs --
       const bool el = elect_one();
-      const uint32_t idesc = idesc_16(p.bf16, kTile, ceil16(tb.rows), false, false);
+      // Of the columns only those from a group's first block of rows to its last.
+      const uint32_t idesc = idesc_16(p.bf16, kTile, 0, false, false);
       const uint32_t hb = smem_addr(hs);
       for (int un = ua; un < ub && ok; ++un) {
         const int part = un % per_tile / per_part;
         const int g0 = tb.groups * part / u.gparts, g1 = tb.groups * (part + 1) / u.gparts;
         for (int g = g0; g < g1 && ok; ++g, ++acc_it) {
           const uint32_t a = acc_it % kAccs;
+          const int c0 = __ffs(tb.blocks[g]) - 1, c1 = 32 - __clz(tb.blocks[g]);
           ok = warp_wait(&ctl->acc_empty[a], ((acc_it / kAccs) & 1) ^ 1, ctl, p.status);
+          tc_fence_after();
           for (int k = 0; k < kblocks && ok; ++k, ++w_it) {
-            const uint32_t s = w_it % kUpSlots;
-            ok = warp_wait(&ctl->full[s], (w_it / kUpSlots) & 1, ctl, p.status);
+            const uint32_t s = w_it % u.slots;
+            ok = warp_wait(&ctl->full[s], (w_it / u.slots) & 1, ctl, p.status);
             if (!ok) break;
-            tc_fence_after();
             if (el) {
-              const uint64_t ad = smem_desc_k_sw128(smem_addr(slots + s * kSlot));
+              const uint64_t ad = smem_desc_k(smem_addr(slots + s * kTile * u.line), u.line);
               for (int j = k * 4; j < min(ksteps, k * 4 + 4); ++j)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                   const int c = j + half * (u.rp / 16);  // the step's place among the columns' k
-                  const uint64_t bd = smem_desc_k_sw128(hb + (c >> 2) * kSlot);
-                  mma_ss<1>(tmem + a * kTile, ad + (j & 3) * 2, bd + (c & 3) * 2, idesc, j | half);
+                  const uint64_t bd = smem_desc_k_sw128(hb + (c >> 2) * kSlot + c0 * 2048);
+                  mma_ss<1>(tmem + a * kTile + c0 * 16, ad + (j & 3) * 2, bd + (c & 3) * 2,
+                            idesc | (uint32_t)(c1 - c0) * 2 << 17, j | half);
                 }
               mma_commit(&ctl->empty[s]);
             }
@@ -732,19 +807,37 @@ __global__ void __launch_bounds__(kUpThreads, 1)
             if (!(blocks >> c & 1)) continue;
             uint32_t v[16];
             tmem_ld16_sync(tmem + a * kTile + c * 16 + ((uint32_t)(quad * 32) << 16), v);
+            const uint4 of = *reinterpret_cast<const uint4*>(tb.slot + c * 16);
+            const float4* up = reinterpret_cast<const float4*>(sh->row_scale + c * 16);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int t = c * 16 + i;
-              if (tb.slot[t] != g) continue;
-              const float d = __uint_as_float(v[i]) * sh->row_scale[t];
-              if (u.nio) {
-                const float o = add ? from_half_bits(buf[t * kTile], bf) : 0.0f;
-                buf[t * kTile] = to_half_bits(o + d, bf);
-              } else if (n < p.N) {
-                const float o = add ? load_as(p.base, p.out_dtype, (row0 + t) * p.base_stride + n) : 0.0f;
-                store_out(p.out, p.out_dtype, (row0 + t) * p.out_stride + n, o + d);
+            for (int i = 0; i < 4; ++i) {
+              const float4 f = up[i];
+              v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) * f.x);
+              v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) * f.y);
+              v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) * f.z);
+              v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) * f.w);
+            }
+            if (u.nio) {
+              uint16_t* col = buf + c * 16 * kTile;
+              uint16_t old[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) old[i] = add ? col[i * kTile] : (uint16_t)0;
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                old[i] = to_half_bits(from_half_bits(old[i], bf) + __uint_as_float(v[i]), bf);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (byte_of(of, i) == g) col[i * kTile] = old[i];
+            } else if (n < p.N) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                if (byte_of(of, i) != g) continue;
+                const int64_t row = row0 + c * 16 + i;
+                const float o = add ? load_as(p.base, p.out_dtype, row * p.base_stride + n) : 0.0f;
+                store_out(p.out, p.out_dtype, row * p.out_stride + n, o + __uint_as_float(v[i]));
               }
             }
+            __syncwarp();
           }
           tc_fence_before();
           __syncwarp();
@@ -793,13 +886,9 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     }
     __syncwarp();
   }
-  if (warp == 0 && ctl->abort_flag) {  // loads in flight land before the CTA goes
-    for (uint32_t j = w_it < kUpSlots ? 0 : w_it - kUpSlots; j < w_it; ++j)
-      wait_drain(&ctl->full[j % kUpSlots], (j / kUpSlots) & 1);
-    if (u.nio)
-      for (uint32_t j = io_it < (uint32_t)u.nio ? 0 : io_it - u.nio; j < io_it; ++j)
-        wait_drain(&ctl->io_full[j % u.nio], (j / u.nio) & 1);
-  }
+  if (warp == 0 && ctl->abort_flag)  // loads in flight land before the CTA goes
+    for (uint32_t j = w_it < (uint32_t)u.slots ? 0 : w_it - u.slots; j < w_it; ++j)
+      wait_drain(&ctl->full[j % u.slots], (j / u.slots) & 1);
   if (warp == 1) {
     if (elect_one()) mma_commit(&ctl->drain);
     __syncwarp();
@@ -872,11 +961,16 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
   const bool tma = g.out_dtype != MQ_DTYPE_F32 && base_ok && g.out_stride % 8 == 0 && g.N % 8 == 0 &&
                    (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
   u.nio = !tma ? 0 : u.rp == 128 ? 2 : kMaxIo;
+  u.line = std::min(u.rp, 64) * 2;
+  u.slots = std::min(kMaxUpSlots, kUpBytes / (kTile * u.line));
   CUtensorMap mb, mbase, mout;
   const cuuint64_t bd[3] = {(cuuint64_t)g.r, (cuuint64_t)g.N, (cuuint64_t)g.L * g.E};
   const cuuint64_t bs[2] = {2 * (cuuint64_t)g.r, 2 * (cuuint64_t)g.r * g.N};
-  const cuuint32_t bb[3] = {64, kTile, 1};
-  cudaError_t err = make_map(&mb, dt, 3, g.b, bd, bs, bb);
+  const cuuint32_t bb[3] = {(cuuint32_t)u.line / 2, kTile, 1};
+  cudaError_t err = make_map(&mb, dt, 3, g.b, bd, bs, bb,
+                             u.line == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                             : u.line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                            : CU_TENSOR_MAP_SWIZZLE_32B);
   if (err != cudaSuccess) return err;
   mbase = mout = mb;
   if (tma) {
@@ -889,10 +983,10 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
     if (err == cudaSuccess && g.base) err = make_map(&mbase, ot, 2, g.base, d, &s0, box, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (err != cudaSuccess) return err;
   }
-  constexpr size_t most = 1024 + 4 * kSlot + kUpSlots * kSlot + 2 * kIoBytes + sizeof(UpShared);
-  constexpr size_t most3 = 1024 + 2 * kSlot + kUpSlots * kSlot + 3 * kIoBytes + sizeof(UpShared);
+  constexpr size_t most = 1024 + 4 * kSlot + kUpBytes + 2 * kIoBytes + sizeof(UpShared);
+  constexpr size_t most3 = 1024 + 2 * kSlot + kUpBytes + 3 * kIoBytes + sizeof(UpShared);
   static_assert(most <= kSmemMax && most3 <= kSmemMax, "shared memory");
-  const size_t need = 1024 + (2 * u.rp + 63) / 64 * kSlot + kUpSlots * kSlot + (size_t)u.nio * kIoBytes + sizeof(UpShared);
+  const size_t need = 1024 + (2 * u.rp + 63) / 64 * kSlot + kUpBytes + (size_t)u.nio * kIoBytes + sizeof(UpShared);
   const size_t smem = std::max<size_t>(need, 120 * 1024);  // one CTA per SM: each allocates all of tensor memory
   static std::atomic<uint64_t> ready{0};
   err = allow_smem(lora_up, kSmemMax, ready);
@@ -916,8 +1010,8 @@ LoraPlan lora_plan(int64_t R, int K, int N, int r, int L, int E) {
   const int tile_groups = (int)std::min<double>(kTile, groups);
   const int accs = (tile_groups + per - 1) / per;
   const int stages = (K + 63) / 64;
-  while (pl.mparts * 2 <= accs && tiles * pl.mparts * 2 <= sms) pl.mparts *= 2;
-  while (pl.splits < 16 && pl.splits * 4 <= stages && tiles * pl.mparts * pl.splits * 2 <= sms) pl.splits *= 2;
+  pl.splits = (int)std::max<int64_t>(1, std::min<int64_t>({16, stages / 4, sms / tiles}));
+  pl.mparts = (int)std::max<int64_t>(1, std::min<int64_t>(accs, sms / (tiles * pl.splits)));
   const int ntiles = (N + kTile - 1) / kTile;
   while (pl.gparts * 2 <= tile_groups && tiles * ntiles * pl.gparts * 2 <= sms) pl.gparts *= 2;
   return pl;

@@ -511,6 +511,17 @@ __device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t addr) {
   return d;
 }
 
+// The same for lines of 128, 64 or 32 bytes, each with the swizzle of its length.
+__device__ __forceinline__ uint64_t smem_desc_k(uint32_t addr, uint32_t line) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);           // start address
+  d |= (uint64_t)(16u >> 4) << 16;                  // leading byte offset (unused here)
+  d |= (uint64_t)(8u * line >> 4) << 32;            // stride byte offset: 8 rows
+  d |= (uint64_t)1 << 46;                           // descriptor version (tcgen05)
+  d |= (uint64_t)(line == 128 ? 2 : line == 64 ? 4 : 6) << 61;  // swizzle: 128, 64 or 32 B
+  return d;
+}
+
 // Shared-memory matrix descriptor of an operand whose M (or N) index is the
 // contiguous one, stored with the 128-byte swizzle: blocks of 64 elements (128
 // bytes) by 64 k, `block_bytes` apart, 8-k groups 1024 bytes apart.  A step of 16
