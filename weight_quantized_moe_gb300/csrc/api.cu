@@ -1130,7 +1130,7 @@ static bool lora_sizes_ok(int64_t R, int K, int N, int r, int L, int E) {
 MQ_EXPORT size_t moe_lora_product_workspace(int64_t R, int K, int N, int r, int L, int E) {
   if (!lora_sizes_ok(R, K, N, r, L, E) || R == 0) return 0;
   const LoraPlan pl = lora_plan(R, K, N, r, L, E);
-  return pl.rows ? 0 : align256(sizeof(float) * (size_t)pl.splits * (size_t)R * (size_t)r);
+  return pl.rows ? 0 : align256(lora_workspace(R, r));
 }
 
 // Whether R rows of `len` bytes, `stride` bytes apart, share a byte with R others.
@@ -1191,7 +1191,7 @@ MQ_EXPORT int moe_lora_product(const void* x, int64_t x_stride, int dtype, int64
   g.ids = adapter_ids; g.offsets = expert_offsets; g.scaling = scaling;
   g.base = base; g.base_stride = base_stride;
   g.out = out; g.out_stride = out_stride; g.out_dtype = out_dtype;
-  g.part = static_cast<float*>(workspace);
+  g.workspace = static_cast<uint8_t*>(workspace);
   g.status = status_ptr();
   for (int which = 0; which < (pl.rows ? 1 : 2); ++which) {
     LaunchScope ls(which ? MQ_PROF_GEMM2 : MQ_PROF_GEMM1, st);

@@ -17,11 +17,15 @@
 //          holds (infinities, NaN) stays in the columns that are not kept.
 //
 // Tiles, first launch (lora_down): h = A x in float32.  Groups are packed into the 128
-// lanes of an accumulator (eight of rank 16, two of rank 64), x is the other operand.
-// Second launch (lora_up): s h is the columns' operand.  It is split into two 16-bit
-// parts, h = 2^m (hi + lo), m the exponent of the row's largest |h|: 16 bits of
-// precision for bf16 and 22 for f16, whose range it cannot leave either, for twice a
-// small product.  base comes by TMA and goes back, with the sums added, the same way.
+// lanes of an accumulator (eight of rank 16, two of rank 64), x is the other operand; a
+// cluster's CTAs take a share of K each and sum their h through distributed shared
+// memory.  s h is written as the second product's operand, in two 16-bit parts: h = 2^m
+// (hi + lo), m the exponent of the row's largest |h|: 16 bits of precision for bf16 and
+// 22 for f16, whose range it cannot leave either, for twice a small product.
+// Second launch (lora_up): a group's product has the columns of its own rows only, so
+// that groups whose rows lie apart share an accumulator and a tile of several requests
+// takes one turn of the epilogue.  base comes by TMA and goes back, with the sums added,
+// the same way.
 #include "lora.cuh"
 #include "pipe.cuh"
 
@@ -208,32 +212,39 @@ __global__ void __launch_bounds__(kRowThreads, 4) lora_rows(const LoraArgs p) {
 }
 
 // ------------------------------------------------------------------ tiles --
-// Groups of a tile's rows.
+constexpr int kNone = 255, kOut = 254;  // rows without an adapter; rows that are not written
+
+// Groups of a tile's rows, as the first launch works them out.
 struct Table {
-  int key[kTile];        // group of a row as an index into the adapters (l E + e); -1 none, -2 not written
-  int group_key[kTile];  // key of each of the tile's groups, in order of their first rows
-  unsigned blocks[kTile];               // the 16-row blocks that hold rows of a group
-  alignas(16) uint8_t slot[kTile];      // a row's group; kNone, kOut
+  int key[kTile];                  // group of a row as an index into the adapters (l E + e); -1 none, -2 not written
+  int group_key[kTile];            // key of each of the tile's groups, in order of their first rows
+  unsigned blocks[kTile];          // the 16-row blocks that hold rows of a group
+  alignas(16) uint8_t slot[kTile]; // a row's group; kNone, kOut
   unsigned first[kTile / 32];
   int groups, rows;
-  int inside;            // rows that are written
+  int inside;                      // rows that are written
 };
-constexpr int kNone = 255, kOut = 254;
 
-// Joins THREADS threads that start at warp 0 (barrier 2); all of them take part below.
-template <int THREADS>
-__device__ __forceinline__ void join() {
-  asm volatile("bar.sync 2, %0;" ::"n"(THREADS) : "memory");
-}
+// What the second launch needs of it, in global memory.  A group's accumulator has
+// columns for the blocks from its first row to its last.  Groups whose ranges do not
+// meet share one: each has a color, and colors 2 i and 2 i + 1 are round i.
+struct TileTable {
+  alignas(16) uint8_t color[kTile];  // color of a row's group; kNone, kOut
+  float row_scale[kTile];            // 2^m of each row
+  int group_key[kTile];              // by round
+  int group_range[kTile];            // first block | behind its last << 8 | color << 16
+  int round_start[kTile / 2 + 4];    // first group of a round
+  int groups, rounds, rows, inside;
+};
+static_assert(sizeof(TileTable) % 16 == 0, "copied in steps of 16 bytes");
 
-// Fills in the table of tile `tile`, with the first THREADS threads of the CTA (at least
-// kTile); `offsets` is a copy of the experts' in shared memory (null: one expert).
-template <int THREADS>
+// Fills in the table of tile `tile`, with all threads of the CTA (at least kTile);
+// `offsets` is a copy of the experts' in shared memory (null: one expert).
 __device__ __forceinline__ void build_table(Table& tb, const LoraArgs& p, const int* offsets, bool bad,
-                                            int t, int tile) {
+                                            int tile) {
+  const int t = threadIdx.x;
   const int64_t row0 = (int64_t)tile * kTile;
   const int rows = (int)min((int64_t)kTile, p.R - row0);
-  join<THREADS>();  // (the last table is no longer read)
   int key = -2;
   if (t < kTile) {
     if (t < rows && !bad) {
@@ -263,7 +274,7 @@ __device__ __forceinline__ void build_table(Table& tb, const LoraArgs& p, const 
     tb.rows = rows;
     tb.inside = 0;
   }
-  join<THREADS>();
+  __syncthreads();
   int at = t;  // the first row of this row's group
   if (t < kTile) {
     if (key >= 0) {
@@ -284,7 +295,7 @@ __device__ __forceinline__ void build_table(Table& tb, const LoraArgs& p, const 
       atomicAdd(&tb.inside, __popc(in));
     }
   }
-  join<THREADS>();
+  __syncthreads();
   if (t < kTile) {
     int g = 0, n = 0;
 #pragma unroll
@@ -301,7 +312,59 @@ __device__ __forceinline__ void build_table(Table& tb, const LoraArgs& p, const 
     if (key >= 0 && (peers & ((1u << (t & 31)) - 1u)) == 0)
       atomicOr(&tb.blocks[g], ((peers & 0xffffu ? 1u : 0u) | (peers >> 16 ? 2u : 0u)) << (t >> 5) * 2);
   }
-  join<THREADS>();
+  __syncthreads();
+}
+
+// The second launch's table of a tile, by one warp: colors in the order of the groups,
+// each the least that no group of a meeting range has.  `color`: kTile bytes.
+__device__ __forceinline__ void write_table(TileTable* to, const Table& tb, uint8_t* color, int lane) {
+  unsigned used[4] = {};  // blocks taken, of colors lane, lane + 32, ...
+  int colors = 0;
+  for (int g = 0; g < tb.groups; ++g) {
+    const int b0 = __ffs(tb.blocks[g]) - 1, b1 = 32 - __clz(tb.blocks[g]);
+    const unsigned range = (1u << b1) - (1u << b0);
+    bool placed = false;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (placed) continue;
+      const unsigned free = __ballot_sync(0xffffffffu, (used[q] & range) == 0);
+      if (!free) continue;
+      const int l = __ffs(free) - 1;
+      if (lane == l) used[q] |= range;
+      if (lane == 0) color[g] = (uint8_t)(q * 32 + l);
+      colors = max(colors, q * 32 + l + 1);
+      placed = true;
+    }
+  }
+  __syncwarp();
+  const int rounds = (colors + 1) / 2;
+  int n = 0;
+  for (int rd = 0; rd < rounds; ++rd) {
+    if (lane == 0) to->round_start[rd] = n;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int g = q * 32 + lane;
+      const bool here = g < tb.groups && color[g] >> 1 == rd;
+      const unsigned all = __ballot_sync(0xffffffffu, here);
+      if (here) {
+        const int at = n + __popc(all & ((1u << lane) - 1u));
+        to->group_key[at] = tb.group_key[g];
+        to->group_range[at] = (__ffs(tb.blocks[g]) - 1) | (32 - __clz(tb.blocks[g])) << 8 | color[g] << 16;
+      }
+      n += __popc(all);
+    }
+  }
+  for (int t = lane; t < kTile; t += 32) {
+    const int s = tb.slot[t];
+    to->color[t] = s < kOut ? color[s] : (uint8_t)s;
+  }
+  if (lane == 0) {
+    to->round_start[rounds] = n;
+    to->groups = tb.groups;
+    to->rounds = rounds;
+    to->rows = tb.rows;
+    to->inside = tb.inside;
+  }
 }
 
 // The offsets' copy in shared memory; true where they fall or leave [0, R].
@@ -325,13 +388,24 @@ __device__ __forceinline__ int byte_of(const uint4& v, int i) {
   return (int)(w >> (i & 3) * 8 & 0xff);
 }
 
-// ---- first launch: h = A x ----
+__device__ __forceinline__ uint16_t to_half_bits(float v, bool bf16) {
+  return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+__device__ __forceinline__ float from_half_bits(uint16_t v, bool bf16) {
+  return bf16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+}
+
+// The magnitude of v, 0 where it is infinite or NaN.
+__device__ __forceinline__ float finite(float v) { return isfinite(v) ? fabsf(v) : 0.0f; }
+
+// ---- first launch: h = A x, its sum over the K splits, and s h in 16-bit parts ----
+// A cluster holds the K splits of a tile (or of a part of its accumulators).
 constexpr int kDownThreads = 256;
-constexpr int kDownSlots = 12;  // of 16 KB: a stage of x, or of an accumulator's groups
-constexpr int kBatch = 4;       // accumulators at a time
+constexpr int kXSlots = 4, kASlots = 4;  // of 16 KB: a stage of x, of an accumulator's groups
+constexpr int kBatch = 4;                // accumulators at a time
 
 struct DownCtl {
-  uint64_t full[kDownSlots], empty[kDownSlots];
+  uint64_t x_full[kXSlots], x_empty[kXSlots], a_full[kASlots], a_empty[kASlots];
   uint64_t acc_full, acc_empty, drain;
   uint32_t tmem;
   volatile int abort_flag;
@@ -340,22 +414,41 @@ struct DownShared {
   DownCtl ctl;
   Table table;
   int offsets[kMaxE + 1];
+  uint8_t color[kTile];
+};
+// floats between the rows of h in shared memory
+__host__ __device__ constexpr int h_pitch(int rp) { return rp + 4; }
+// 16-bit elements between the rows of the second product's operand
+__host__ __device__ constexpr int h_row(int rp) { return rp < 32 ? 64 : 2 * rp; }
+
+struct DownShape {
+  int rp;      // r rounded up to 16, 32, 64 or 128
+  int splits;  // K splits: CTAs of a cluster
+  int mparts;  // clusters among which a tile's accumulators are divided
+  TileTable* tables;
+  uint16_t* h;  // [tiles * kTile][h_row(rp)]
 };
 
 __global__ void __launch_bounds__(kDownThreads, 1)
     lora_down(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
-              const LoraArgs p, int rp, int splits, int mparts) {
+              const LoraArgs p, const DownShape d) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* slots = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  DownShared* sh = reinterpret_cast<DownShared*>(slots + kDownSlots * kSlot);
+  uint8_t* xs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* as = xs + kXSlots * kSlot;
+  float* hs = reinterpret_cast<float*>(as + kASlots * kSlot);
+  DownShared* sh = reinterpret_cast<DownShared*>(hs + kTile * h_pitch(d.rp));
   DownCtl* ctl = &sh->ctl;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     tma_prefetch_desc(&map_x);
     tma_prefetch_desc(&map_a);
-    for (int i = 0; i < kDownSlots; ++i) {
-      mbar_init(&ctl->full[i], 1);
-      mbar_init(&ctl->empty[i], 1);
+    for (int i = 0; i < kXSlots; ++i) {
+      mbar_init(&ctl->x_full[i], 1);
+      mbar_init(&ctl->x_empty[i], 1);
+    }
+    for (int i = 0; i < kASlots; ++i) {
+      mbar_init(&ctl->a_full[i], 1);
+      mbar_init(&ctl->a_empty[i], 1);
     }
     mbar_init(&ctl->acc_full, 1);
     mbar_init(&ctl->acc_empty, 4);
@@ -367,104 +460,119 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
+  const int split = blockIdx.x % d.splits;  // the rank in the cluster
+  const int mpart = blockIdx.x / d.splits % d.mparts;
+  const int tile = blockIdx.x / (d.splits * d.mparts);
+  const int64_t row0 = (int64_t)tile * kTile;
+  const int nst = (p.K + 63) / 64;
+  const int s0 = (int)((int64_t)nst * split / d.splits), s1 = (int)((int64_t)nst * (split + 1) / d.splits);
   mq::pdl_wait();
   mq::pdl_trigger();
   const bool bad = copy_offsets(p, sh->offsets);
-  const int split = blockIdx.x % splits;
-  const int mpart = blockIdx.x / splits % mparts;
-  const int tile = blockIdx.x / (splits * mparts);
-  build_table<kDownThreads>(sh->table, p, p.offsets ? sh->offsets : nullptr, bad, tid, tile);
+  // the first stages of x are on their way while the groups are worked out
+  const int early = min(kXSlots, s1 - s0);
+  if (warp == 0 && elect_one())
+    for (int i = 0; i < early; ++i) {
+      mbar_arrive_expect_tx(&ctl->x_full[i], kSlot);
+      tma_load_2d(xs + i * kSlot, &map_x, &ctl->x_full[i], (s0 + i) * 64, (int)row0);
+    }
+  __syncwarp();
+  build_table(sh->table, p, p.offsets ? sh->offsets : nullptr, bad, tile);
   const Table& tb = sh->table;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-  const int64_t row0 = (int64_t)tile * kTile;
-  const int per = kTile / rp;                          // groups of an accumulator
-  const int accs = (tb.groups + per - 1) / per;        // accumulators of the tile
-  const int mine = accs > mpart ? (accs - mpart + mparts - 1) / mparts : 0;
-  const int nst = (p.K + 63) / 64;
-  const int s0 = (int)((int64_t)nst * split / splits), s1 = (int)((int64_t)nst * (split + 1) / splits);
+  const int per = kTile / d.rp;                      // groups of an accumulator
+  const int accs = (tb.groups + per - 1) / per;      // accumulators of the tile
+  const int mine = accs > mpart ? (accs - mpart + d.mparts - 1) / d.mparts : 0;
 
   if (warp == 0) {
     const bool el = elect_one();
     uint32_t it = 0;
     bool ok = true;
-    auto take = [&]() -> uint8_t* {  // the next slot, once it is free
-      const uint32_t s = it % kDownSlots;
-      ok = warp_wait(&ctl->empty[s], ((it / kDownSlots) & 1) ^ 1, ctl, p.status);
-      return slots + s * kSlot;
-    };
     for (int b0 = 0; b0 < mine && ok; b0 += kBatch)
-      for (int s = s0; s < s1 && ok; ++s) {
-        uint8_t* dst = take();
+      for (int s = s0; s < s1; ++s, ++it) {
+        if (it < (uint32_t)early) continue;
+        const uint32_t slot = it % kXSlots;
+        ok = warp_wait(&ctl->x_empty[slot], ((it / kXSlots) & 1) ^ 1, ctl, p.status);
         if (!ok) break;
-        uint64_t* bar = &ctl->full[it % kDownSlots];
         if (el) {
-          mbar_arrive_expect_tx(bar, kSlot);
-          tma_load_2d(dst, &map_x, bar, s * 64, (int)row0);
-        }
-        ++it;
-        for (int b = b0; b < min(b0 + kBatch, mine); ++b) {
-          dst = take();
-          if (!ok) break;
-          bar = &ctl->full[it % kDownSlots];
-          const int g0 = (mpart + b * mparts) * per, n = min(per, tb.groups - g0);
-          if (el) {
-            mbar_arrive_expect_tx(bar, n * rp * 128);
-            for (int i = 0; i < n; ++i) tma_load_3d(dst + i * rp * 128, &map_a, bar, s * 64, 0, tb.group_key[g0 + i]);
-          }
-          ++it;
+          mbar_arrive_expect_tx(&ctl->x_full[slot], kSlot);
+          tma_load_2d(xs + slot * kSlot, &map_x, &ctl->x_full[slot], s * 64, (int)row0);
         }
       }
+    it = max(it, (uint32_t)early);
+    if (ctl->abort_flag || !mine)  // loads that nothing waits for land before the CTA goes
+      for (uint32_t j = it < kXSlots ? 0 : it - kXSlots; j < it; ++j)
+        wait_drain(&ctl->x_full[j % kXSlots], (j / kXSlots) & 1);
+  } else if (warp == 2) {
+    const bool el = elect_one();
+    uint32_t it = 0;
+    bool ok = true;
+    for (int b0 = 0; b0 < mine && ok; b0 += kBatch)
+      for (int s = s0; s < s1 && ok; ++s)
+        for (int b = b0; b < min(b0 + kBatch, mine); ++b, ++it) {
+          const uint32_t slot = it % kASlots;
+          ok = warp_wait(&ctl->a_empty[slot], ((it / kASlots) & 1) ^ 1, ctl, p.status);
+          if (!ok) break;
+          const int g0 = (mpart + b * d.mparts) * per, n = min(per, tb.groups - g0);
+          if (el) {
+            mbar_arrive_expect_tx(&ctl->a_full[slot], n * d.rp * 128);
+            for (int i = 0; i < n; ++i)
+              tma_load_3d(as + slot * kSlot + i * d.rp * 128, &map_a, &ctl->a_full[slot], s * 64, 0,
+                          tb.group_key[g0 + i]);
+          }
+        }
     if (ctl->abort_flag)
-      for (uint32_t j = it < kDownSlots ? 0 : it - kDownSlots; j < it; ++j)
-        wait_drain(&ctl->full[j % kDownSlots], (j / kDownSlots) & 1);
+      for (uint32_t j = it < kASlots ? 0 : it - kASlots; j < it; ++j)
+        wait_drain(&ctl->a_full[j % kASlots], (j / kASlots) & 1);
   } else if (warp == 1) {
     const bool el = elect_one();
     const uint32_t idesc = idesc_16(p.bf16, kTile, ceil16(tb.rows), false, false);
-    uint32_t it = 0;
+    uint32_t x_it = 0, a_it = 0;
     bool ok = true;
     for (int b0 = 0, turn = 0; b0 < mine && ok; b0 += kBatch, ++turn) {
       ok = warp_wait(&ctl->acc_empty, (turn & 1) ^ 1, ctl, p.status);
       tc_fence_after();
-      for (int s = s0; s < s1 && ok; ++s) {
-        const uint32_t xs = it++ % kDownSlots;
-        ok = warp_wait(&ctl->full[xs], ((it - 1) / kDownSlots) & 1, ctl, p.status);
-        const uint64_t bd = smem_desc_k_sw128(smem_addr(slots + xs * kSlot));
-        for (int b = b0; b < min(b0 + kBatch, mine) && ok; ++b) {
-          const uint32_t as = it++ % kDownSlots;
-          ok = warp_wait(&ctl->full[as], ((it - 1) / kDownSlots) & 1, ctl, p.status);
+      for (int s = s0; s < s1 && ok; ++s, ++x_it) {
+        const uint32_t xslot = x_it % kXSlots;
+        ok = warp_wait(&ctl->x_full[xslot], (x_it / kXSlots) & 1, ctl, p.status);
+        const uint64_t bd = smem_desc_k_sw128(smem_addr(xs + xslot * kSlot));
+        for (int b = b0; b < min(b0 + kBatch, mine) && ok; ++b, ++a_it) {
+          const uint32_t aslot = a_it % kASlots;
+          ok = warp_wait(&ctl->a_full[aslot], (a_it / kASlots) & 1, ctl, p.status);
           if (!ok) break;
           tc_fence_after();
           if (el) {
-            const uint64_t ad = smem_desc_k_sw128(smem_addr(slots + as * kSlot));
+            const uint64_t ad = smem_desc_k_sw128(smem_addr(as + aslot * kSlot));
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               mma_ss<1>(tmem + (b - b0) * kTile, ad + j * 2, bd + j * 2, idesc, (s > s0) | j);
-            mma_commit(&ctl->empty[as]);
+            mma_commit(&ctl->a_empty[aslot]);
           }
         }
-        if (ok && el) mma_commit(&ctl->empty[xs]);
+        if (ok && el) mma_commit(&ctl->x_empty[xslot]);
       }
       if (ok && el) mma_commit(&ctl->acc_full);
     }
     if (el) mma_commit(&ctl->drain);
     wait_drain(&ctl->drain, 0);
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    if (split == 0 && mpart == 0) write_table(d.tables + tile, tb, sh->color, lane);
+  } else {
     // A lane is one rank of one of the accumulator's groups.
     const int quad = warp & 3;
-    const int gl = (quad * 32 + lane) / rp, j = (quad * 32 + lane) % rp;
+    const int gl = (quad * 32 + lane) / d.rp, j = (quad * 32 + lane) % d.rp;
     bool ok = true;
     for (int b0 = 0, turn = 0; b0 < mine && ok; b0 += kBatch, ++turn) {
       ok = warp_wait(&ctl->acc_full, turn & 1, ctl, p.status);
       if (!ok) break;
       tc_fence_after();
       for (int b = b0; b < min(b0 + kBatch, mine); ++b) {
-        const int g = (mpart + b * mparts) * per + gl;
-        const bool live = g < tb.groups && j < p.r;
+        const int g = (mpart + b * d.mparts) * per + gl;
+        const bool live = g < tb.groups;
         const unsigned any = __reduce_or_sync(0xffffffffu, live ? tb.blocks[g] : 0u);
-        float* dst = p.part + ((int64_t)split * p.R + row0) * p.r + j;
         for (int c = 0; c < kTile / 16; ++c) {
           if (!(any >> c & 1)) continue;
           uint32_t v[16];
@@ -472,7 +580,8 @@ __global__ void __launch_bounds__(kDownThreads, 1)
           const uint4 of = *reinterpret_cast<const uint4*>(tb.slot + c * 16);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (live && byte_of(of, i) == g) dst[(c * 16 + i) * p.r] = __uint_as_float(v[i]);
+            if (live && byte_of(of, i) == g) hs[(c * 16 + i) * h_pitch(d.rp) + j] = __uint_as_float(v[i]);
+          __syncwarp();
         }
       }
       tc_fence_before();
@@ -481,195 +590,197 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  // The sum over the splits, in their order, of this CTA's share of the rows; eight
+  // lanes per row, four ranks a lane and turn.
+  const int share = kTile / d.splits, sub = tid & 7;
+  for (int i = tid >> 3; i < share; i += kDownThreads / 8) {
+    const int t = split * share + i, g = tb.slot[t];
+    const bool live = g < kOut && g / per % d.mparts == mpart;
+    const float s = live && p.scaling ? p.scaling[tb.key[t] / p.E] : 1.0f;
+    float4 v[4];
+    float most = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int j = q * 32 + sub * 4;
+      if (live && j < p.r) {  // (behind r: 0, whatever x holds)
+        const float* row = hs + t * h_pitch(d.rp) + j;
+#pragma unroll 4
+        for (int c = 0; c < d.splits; ++c) {
+          const float4 w = load_cluster(map_rank(row, c));
+          v[q].x += w.x;
+          v[q].y += w.y;
+          v[q].z += w.z;
+          v[q].w += w.w;
+        }
+        v[q].x *= s;
+        v[q].y *= s;
+        v[q].z *= s;
+        v[q].w *= s;
+        most = fmaxf(fmaxf(most, fmaxf(finite(v[q].x), finite(v[q].y))), fmaxf(finite(v[q].z), finite(v[q].w)));
+      }
+    }
+#pragma unroll
+    for (int o = 4; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (!live) continue;
+    // 2^m with m the exponent of the largest, kept to where 2^m and 2^-m are normal
+    const int e = min(max((int)(__float_as_uint(most) >> 23), 1), 253);
+    const float up = __uint_as_float((uint32_t)e << 23), down = __uint_as_float((uint32_t)(254 - e) << 23);
+    if (sub == 0) d.tables[tile].row_scale[t] = up;
+    uint16_t* dst = d.h + (row0 + t) * h_row(d.rp);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int j = q * 32 + sub * 4;
+      if (j >= d.rp) continue;
+      const float f[4] = {v[q].x * down, v[q].y * down, v[q].z * down, v[q].w * down};
+      uint16_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        hi[k] = to_half_bits(f[k], p.bf16);
+        const float rest = f[k] - from_half_bits(hi[k], p.bf16);
+        lo[k] = to_half_bits(isfinite(rest) ? rest : 0.0f, p.bf16);  // (infinity minus itself)
+      }
+      *reinterpret_cast<uint2*>(dst + j) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
+      *reinterpret_cast<uint2*>(dst + d.rp + j) =
+          make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // (the others read this CTA's h until here)
 }
 
 // ---- second launch: out = base + B (s h) ----
-// Warps 0 (B), 1 (MMAs) and 4-11 (epilogue) meet at each tile, warps 12 and up do not:
-// warp 12 streams base.
-constexpr int kUpThreads = 416;
-constexpr int kUpJoined = 384;
-constexpr int kIoWarp = 12;
-constexpr int kUpBytes = 65536;    // of 128 outputs by up to 64 ranks of a group a slot
+constexpr int kUpEpi = 16;         // epilogue warps
+constexpr int kUpThreads = 128 + 32 * kUpEpi;
 constexpr int kMaxUpSlots = 16;
-constexpr int kUpEpi = 8;          // epilogue warps
 constexpr int kIoBytes = kTile * kTile * 2;
-constexpr int kMaxIo = 3;
-constexpr int kAccs = 4;           // accumulators in flight, one group each
+constexpr int kMaxIo = 4;
 
 struct UpCtl {
   uint64_t full[kMaxUpSlots], empty[kMaxUpSlots];
-  uint64_t acc_full[kAccs], acc_empty[kAccs];
-  uint64_t io_full[kMaxIo], io_empty[kMaxIo];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t io_full[kMaxIo], io_done[kMaxIo], io_empty[kMaxIo];
+  uint64_t tile_full, tile_empty;
   uint64_t drain;
   uint32_t tmem;
   volatile int abort_flag;
 };
 struct UpShared {
+  TileTable table;
   UpCtl ctl;
-  Table table;
-  alignas(16) float row_scale[kTile];  // 2^m of each row
-  int offsets[kMaxE + 1];
 };
 
 struct UpShape {
   int rp;      // r rounded up to 16, 32, 64 or 128
-  int splits;  // partial sums of h
-  int gparts;  // parts of a tile's groups
+  int gparts;  // parts of a tile's rounds
   int ntiles;  // of 128 outputs
   int units;   // (tile, part, 128 outputs)
   int nio;     // buffers of base and out; 0: read and written element by element
   int line;    // bytes of a slot's lines: min(64, rp) ranks
-  int slots;   // kUpBytes / (128 * line)
+  int slots;   // of 128 outputs by up to 64 ranks of a group
+  const TileTable* tables;
 };
 
-__device__ __forceinline__ void epilogue_barrier() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kUpEpi * 32) : "memory");
+// base and out in shared memory: 128 rows of 64 outputs (128 bytes, swizzled) twice.
+// Element (row t, 16-byte chunk c of 8 outputs, 0 <= c < 16) of the tile:
+__device__ __forceinline__ uint32_t io_offset(int t, int c) {
+  return (uint32_t)((c >> 3) * (kIoBytes / 2) + t * 128 + (((c & 7) ^ (t & 7)) << 4));
 }
 
-__device__ __forceinline__ uint16_t to_half_bits(float v, bool bf16) {
-  return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
-}
-__device__ __forceinline__ float from_half_bits(uint16_t v, bool bf16) {
-  return bf16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
-}
-
-// The magnitude of v, 0 where it is infinite or NaN.
-__device__ __forceinline__ float finite(float v) { return isfinite(v) ? fabsf(v) : 0.0f; }
-
-// The columns' operand: each row's s h in two 16-bit parts, side by side along k
-// (ranks [0, rp) the high parts, [rp, 2 rp) the low ones), 128-byte swizzled lines in
-// blocks of 64 k.  Eight lanes per row, four ranks a lane and turn.
-__device__ __forceinline__ void build_rows(uint8_t* hs, UpShared* sh, const LoraArgs& p, const UpShape& u,
-                                           int64_t row0) {
-  const Table& tb = sh->table;
-  constexpr int kPass = kUpJoined / 8;                   // rows at a time
-  constexpr int kTurns = (kTile + kPass - 1) / kPass;
-  const int sub = threadIdx.x & 7, first = threadIdx.x >> 3;
-  for (int c0 = 0; c0 < u.rp; c0 += 64) {  // (128 ranks: in two halves, the largest of both first)
-    float4 v[kTurns][2];
-    float s[kTurns], most[kTurns];
-    int key[kTurns];
+// The 32 outputs of a quarter's lanes for eight rows from t0 on: the fragments v (of 16
+// columns, half c) scaled by the rows' 2^m and added to what is in shared memory, one
+// rounding, for the rows of the round.  The two rows that this thread has of each
+// fragment: whether they are of the round, and their scales.  Whole 16-byte chunks move
+// either way: two-byte accesses, 32 a warp, bound this loop.
+template <bool BF16>
+__device__ __forceinline__ void add_rows8(uint32_t io, int quad, int t0, const uint32_t (&v)[2][8], int c,
+                                          bool in0, bool in1, float2 scale, bool add, int lane) {
+  const uint32_t addr = io + io_offset(t0 + (lane & 7), quad * 4 + (lane >> 3));
+  uint32_t m[4];
+  ldmatrix_x4_trans(addr, m);
+  const uint32_t keep = (in0 ? 0u : 0xffffu) | (in1 ? 0u : 0xffff0000u);
 #pragma unroll
-    for (int q = 0; q < kTurns; ++q) {
-      const int t = first + q * kPass;
-      key[q] = t < kTile ? tb.key[t] : -1;
-      s[q] = key[q] >= 0 && p.scaling ? p.scaling[key[q] / p.E] : 1.0f;
-      most[q] = 0;
+  for (int k = 0; k < 4; ++k) {
+    const int r = 4 * c + 2 * (k & 1);
+    float lo = 0, hi = 0;
+    if (add) {
+      lo = from_half_bits((uint16_t)(m[k] & 0xffffu), BF16);
+      hi = from_half_bits((uint16_t)(m[k] >> 16), BF16);
     }
-    auto fetch = [&](int base) {
-#pragma unroll
-      for (int q = 0; q < kTurns; ++q)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) v[q][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-      for (int k = 0; k < u.splits; ++k)
-#pragma unroll
-        for (int q = 0; q < kTurns; ++q)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int j = base + c * 32 + sub * 4;
-            if (key[q] < 0 || j >= p.r) continue;
-            const float4 w = *reinterpret_cast<const float4*>(
-                p.part + ((int64_t)k * p.R + row0 + first + q * kPass) * p.r + j);
-            v[q][c].x += w.x;
-            v[q][c].y += w.y;
-            v[q][c].z += w.z;
-            v[q][c].w += w.w;
-          }
-#pragma unroll
-      for (int q = 0; q < kTurns; ++q)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float4& w = v[q][c];
-          w.x *= s[q];
-          w.y *= s[q];
-          w.z *= s[q];
-          w.w *= s[q];
-          most[q] = fmaxf(fmaxf(most[q], fmaxf(finite(w.x), finite(w.y))), fmaxf(finite(w.z), finite(w.w)));
-        }
-    };
-    if (u.rp == 128) fetch(64 - c0);
-    fetch(c0);
-#pragma unroll
-    for (int q = 0; q < kTurns; ++q) {
-      const int t = first + q * kPass;
-#pragma unroll
-      for (int o = 4; o; o >>= 1) most[q] = fmaxf(most[q], __shfl_xor_sync(0xffffffffu, most[q], o));
-      if (t >= kTile) continue;
-      // 2^m with m the exponent of the largest, kept to where 2^m and 2^-m are normal
-      const int e = min(max((int)(__float_as_uint(most[q]) >> 23), 1), 253);
-      const float up = __uint_as_float((uint32_t)e << 23), down = __uint_as_float((uint32_t)(254 - e) << 23);
-      if (sub == 0) sh->row_scale[t] = up;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int j = c0 + c * 32 + sub * 4;
-        if (j >= u.rp) continue;
-        const float f[4] = {v[q][c].x * down, v[q][c].y * down, v[q][c].z * down, v[q][c].w * down};
-        uint16_t hi[4], lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          hi[i] = to_half_bits(f[i], p.bf16);
-          const float rest = f[i] - from_half_bits(hi[i], p.bf16);
-          lo[i] = to_half_bits(isfinite(rest) ? rest : 0.0f, p.bf16);  // (infinity minus itself)
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint16_t* h = half ? lo : hi;
-          const int k = j + half * u.rp;
-          const int chunk = ((k & 63) >> 3) ^ (t & 7);
-          uint2* dst = reinterpret_cast<uint2*>(hs + (k >> 6) * kSlot + t * 128 + chunk * 16 + (k & 7) * 2);
-          *dst = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
-        }
-      }
+    lo = fmaf(__uint_as_float(v[k >> 1][r]), scale.x, lo);
+    hi = fmaf(__uint_as_float(v[k >> 1][r + 1]), scale.y, hi);
+    uint32_t q;
+    if constexpr (BF16) {
+      const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+      q = *reinterpret_cast<const uint32_t*>(&t);
+    } else {
+      const __half2 t = __floats2half2_rn(lo, hi);
+      q = *reinterpret_cast<const uint32_t*>(&t);
     }
+    m[k] = (m[k] & keep) | (q & ~keep);
   }
+  stmatrix_x4_trans(addr, m);
 }
 
+// 0xff in the bytes of v that, halved, are `rd`.
+__device__ __forceinline__ uint4 rows_of_round(const uint4& v, int rd) {
+  const uint32_t want = (uint32_t)rd * 0x01010101u, low = 0x7f7f7f7fu;
+  return make_uint4(__vcmpeq4(v.x >> 1 & low, want), __vcmpeq4(v.y >> 1 & low, want),
+                    __vcmpeq4(v.z >> 1 & low, want), __vcmpeq4(v.w >> 1 & low, want));
+}
+
+template <bool BF16>  // out is bf16
 __global__ void __launch_bounds__(kUpThreads, 1)
-    lora_up(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_base,
-            const __grid_constant__ CUtensorMap map_out, const LoraArgs p, const UpShape u) {
+    lora_up(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_h,
+            const __grid_constant__ CUtensorMap map_base, const __grid_constant__ CUtensorMap map_out,
+            const LoraArgs p, const UpShape u) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* hs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* slots = hs + ((2 * u.rp + 63) / 64) * kSlot;
-  uint8_t* io = slots + kUpBytes;
+  const int hblocks = (2 * u.rp + 63) / 64;
+  uint8_t* slots = hs + hblocks * kSlot;
+  uint8_t* io = slots + u.slots * kTile * u.line;
   UpShared* sh = reinterpret_cast<UpShared*>(io + u.nio * kIoBytes);
   UpCtl* ctl = &sh->ctl;
-  const Table& tb = sh->table;
+  const TileTable& tb = sh->table;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     tma_prefetch_desc(&map_b);
+    tma_prefetch_desc(&map_h);
     tma_prefetch_desc(&map_base);
     tma_prefetch_desc(&map_out);
     for (int i = 0; i < u.slots; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], 1);
     }
-    for (int i = 0; i < kAccs; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->acc_full[i], 1);
       mbar_init(&ctl->acc_empty[i], kUpEpi);
     }
     for (int i = 0; i < kMaxIo; ++i) {
       mbar_init(&ctl->io_full[i], 1);
+      mbar_init(&ctl->io_done[i], kUpEpi);
       mbar_init(&ctl->io_empty[i], 1);
     }
+    mbar_init(&ctl->tile_full, 1);
+    mbar_init(&ctl->tile_empty, 2 + kUpEpi);
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == 2) {
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
-  mq::pdl_wait();
-  mq::pdl_trigger();
-  const bool bad = copy_offsets(p, sh->offsets);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
+  mq::pdl_wait();
+  mq::pdl_trigger();
   const int kblocks = (u.rp + 63) / 64;  // slots of a group's 128 outputs
   const int ksteps = (p.r + 15) / 16;
   const bool add = p.base != nullptr;
@@ -677,227 +788,305 @@ __global__ void __launch_bounds__(kUpThreads, 1)
   // This CTA's units, one tile of rows after another.
   const int u0 = (int)((int64_t)u.units * blockIdx.x / gridDim.x);
   const int u1 = (int)((int64_t)u.units * (blockIdx.x + 1) / gridDim.x);
-  const int per_part = u.ntiles, per_tile = u.ntiles * u.gparts;
-  // each role's place in its rings
-  uint32_t w_it = 0, acc_it = 0, io_it = 0;
-  bool ok = true;
-  if (warp == kIoWarp) {
-    // ------------------------------------------------------------- base --
-    // Runs ahead of the other warps, over the ends of tiles; so it finds out by itself
-    // which tiles have nothing to do.
-    const bool el = elect_one();
-    for (int un = u0, tile = -1; u.nio && un < u1 && ok; ++un) {
-      if (un / per_tile != tile) {
-        tile = un / per_tile;
-        bool some = false;
-        for (int t = lane; t < kTile; t += 32) {
-          const int64_t row = (int64_t)tile * kTile + t;
-          if (bad || row >= p.R || (p.offsets && (row < sh->offsets[0] || row >= sh->offsets[p.E]))) continue;
-          const int l = p.ids[row];
-          some |= p.base != p.out || (l >= 0 && l < p.L);
-        }
-        if (!__any_sync(0xffffffffu, some)) {
-          un = min(u1, (tile + 1) * per_tile) - 1;
-          continue;
+  const int per_tile = u.ntiles * u.gparts;
+  // Tiles with nothing to write are passed over (by every role).
+  auto idle = [&](const TileTable& t) { return t.inside == 0 || (t.groups == 0 && p.base == p.out); };
+  // The walk over this CTA's units that every role makes: on_tile(tile) as it comes to a
+  // tile, on_unit(n0, part) for each unit of it, end_tile() behind them.  Each returns
+  // whether to go on.
+  auto walk = [&](auto on_tile, auto on_unit, auto end_tile) {
+    for (int un = u0; un < u1;) {
+      const int tile = un / per_tile;
+      const int end = min(u1, (tile + 1) * per_tile);
+      if (idle(u.tables[tile])) {
+        un = end;
+        continue;
+      }
+      if (!on_tile(tile)) return;
+      int part = (un - tile * per_tile) / u.ntiles;
+      int nt = un - tile * per_tile - part * u.ntiles;
+      for (; un < end; ++un) {
+        if (!on_unit(nt * kTile, part)) return;
+        if (++nt == u.ntiles) {
+          nt = 0;
+          ++part;
         }
       }
-      const uint32_t s = io_it % u.nio;
-      ok = warp_wait(&ctl->io_empty[s], ((io_it / u.nio) & 1) ^ 1, ctl, p.status);
-      if (!ok) break;
-      if (el) {
-        if (add) {
-          mbar_arrive_expect_tx(&ctl->io_full[s], kIoBytes);
-          tma_load_2d(io + s * kIoBytes, &map_base, &ctl->io_full[s], un % per_part * kTile, tile * kTile);
-        } else {
-          mbar_arrive(&ctl->io_full[s]);
-        }
-      }
-      ++io_it;
+      if (!end_tile()) return;
     }
-    if (ctl->abort_flag)  // loads in flight land before the CTA goes
-      for (uint32_t j = io_it < (uint32_t)u.nio ? 0 : io_it - u.nio; j < io_it; ++j)
-        wait_drain(&ctl->io_full[j % u.nio], (j / u.nio) & 1);
-  }
-  for (int ua = u0, ub; ua < u1 && warp != kIoWarp; ua = ub) {
-    const int tile = ua / per_tile;
-    ub = min(u1, (tile + 1) * per_tile);
-    const int64_t row0 = (int64_t)tile * kTile;
-    build_table<kUpJoined>(sh->table, p, p.offsets ? sh->offsets : nullptr, bad, tid, tile);
-    const bool nothing = tb.inside == 0 || (tb.groups == 0 && p.base == p.out);
-    if (nothing) continue;
-    build_rows(hs, sh, p, u, row0);
-    fence_proxy_async_smem();
-    join<kUpJoined>();
-    const bool whole = tb.inside == tb.rows && u.gparts == 1;
+  };
+  auto first_round = [&](int part) { return u.gparts == 1 ? (part ? tb.rounds : 0) : tb.rounds * part / u.gparts; };
 
-    if (warp == 0) {
-      // ------------------------------------------------------ groups' B --
-      const bool el = elect_one();
-      for (int un = ua; un < ub && ok; ++un) {
-        const int n0 = un % per_part * kTile, part = un % per_tile / per_part;
-        const int g0 = tb.groups * part / u.gparts, g1 = tb.groups * (part + 1) / u.gparts;
-        for (int g = g0; g < g1 && ok; ++g)
-          for (int k = 0; k < kblocks; ++k) {
-            const uint32_t s = w_it % u.slots;
-            ok = warp_wait(&ctl->empty[s], ((w_it / u.slots) & 1) ^ 1, ctl, p.status);
-            if (!ok) break;
-            if (el) {
-              mbar_arrive_expect_tx(&ctl->full[s], kTile * u.line);
-              tma_load_3d(slots + s * kTile * u.line, &map_b, &ctl->full[s], k * 64, n0, tb.group_key[g]);
-            }
-            ++w_it;
+  if (warp == 0) {
+    // ------------------------------------------------------------- base --
+    const bool el = elect_one();
+    Ring io_r;
+    int row0 = 0;
+    uint32_t it = 0;
+    if (u.nio)
+      walk([&](int tile) { row0 = tile * kTile; return true; },
+           [&](int n0, int) {
+             const uint32_t s = io_r.slot;
+             if (!warp_wait(&ctl->io_empty[s], io_r.turn ^ 1, ctl, p.status)) return false;
+             if (el) {
+               if (add) {
+                 mbar_arrive_expect_tx(&ctl->io_full[s], kIoBytes);
+                 // (the second half may lie behind the last output: nothing is read there)
+                 tma_load_2d(io + s * kIoBytes, &map_base, &ctl->io_full[s], n0, row0);
+                 tma_load_2d(io + s * kIoBytes + kIoBytes / 2, &map_base, &ctl->io_full[s], n0 + 64, row0);
+               } else {
+                 mbar_arrive(&ctl->io_full[s]);
+               }
+             }
+             io_r.next(u.nio);
+             ++it;
+             return true;
+           },
+           [] { return true; });
+    if (ctl->abort_flag)  // loads in flight land before the CTA goes
+      for (uint32_t j = it < (uint32_t)u.nio ? 0 : it - u.nio; j < it; ++j)
+        wait_drain(&ctl->io_full[j % u.nio], (j / u.nio) & 1);
+  } else if (warp == 1) {
+    // ---------------------------------- a tile's table and rows; groups' B --
+    const bool el = elect_one();
+    Ring w;
+    uint32_t it = 0, tiles = 0;
+    walk(
+        [&](int tile) {
+          if (!warp_wait(&ctl->tile_empty, (tiles & 1) ^ 1, ctl, p.status)) return false;
+          if (el) {
+            mbar_arrive_expect_tx(&ctl->tile_full, sizeof(TileTable) + hblocks * kSlot);
+            bulk_load(&sh->table, u.tables + tile, sizeof(TileTable), &ctl->tile_full);
+            for (int b = 0; b < hblocks; ++b)
+              tma_load_2d(hs + b * kSlot, &map_h, &ctl->tile_full, b * 64, tile * kTile);
           }
-      }
-    } else if (warp == 1) {
-      // ----------------------------------------------------------- MMAs --
-      const bool el = elect_one();
-      // Of the columns only those from a group's first block of rows to its last.
-      const uint32_t idesc = idesc_16(p.bf16, kTile, 0, false, false);
-      const uint32_t hb = smem_addr(hs);
-      for (int un = ua; un < ub && ok; ++un) {
-        const int part = un % per_tile / per_part;
-        const int g0 = tb.groups * part / u.gparts, g1 = tb.groups * (part + 1) / u.gparts;
-        for (int g = g0; g < g1 && ok; ++g, ++acc_it) {
-          const uint32_t a = acc_it % kAccs;
-          const int c0 = __ffs(tb.blocks[g]) - 1, c1 = 32 - __clz(tb.blocks[g]);
-          ok = warp_wait(&ctl->acc_empty[a], ((acc_it / kAccs) & 1) ^ 1, ctl, p.status);
-          tc_fence_after();
-          for (int k = 0; k < kblocks && ok; ++k, ++w_it) {
-            const uint32_t s = w_it % u.slots;
-            ok = warp_wait(&ctl->full[s], (w_it / u.slots) & 1, ctl, p.status);
-            if (!ok) break;
-            if (el) {
-              const uint64_t ad = smem_desc_k(smem_addr(slots + s * kTile * u.line), u.line);
-              for (int j = k * 4; j < min(ksteps, k * 4 + 4); ++j)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                  const int c = j + half * (u.rp / 16);  // the step's place among the columns' k
-                  const uint64_t bd = smem_desc_k_sw128(hb + (c >> 2) * kSlot + c0 * 2048);
-                  mma_ss<1>(tmem + a * kTile + c0 * 16, ad + (j & 3) * 2, bd + (c & 3) * 2,
-                            idesc | (uint32_t)(c1 - c0) * 2 << 17, j | half);
-                }
-              mma_commit(&ctl->empty[s]);
-            }
-          }
-          if (ok && el) mma_commit(&ctl->acc_full[a]);
-        }
-      }
-    } else if (warp >= 4) {
-      // ------------------------------------------------------- epilogue --
-      // A lane is an output, the columns are the rows.
-      const int quad = warp & 3, half = (warp - 4) >> 2;
-      const bool bf = p.out_dtype == MQ_DTYPE_BF16;
-      for (int un = ua; un < ub; ++un) {
-        const int n0 = un % per_part * kTile, part = un % per_tile / per_part;
-        const int g0 = tb.groups * part / u.gparts, g1 = tb.groups * (part + 1) / u.gparts;
-        const int n = n0 + quad * 32 + lane;
-        uint16_t* buf = nullptr;
-        const uint32_t s = u.nio ? io_it % u.nio : 0;
-        if (u.nio) {
-          ok = ok && warp_wait(&ctl->io_full[s], (io_it / u.nio) & 1, ctl, p.status);
-          buf = reinterpret_cast<uint16_t*>(io + s * kIoBytes) + quad * 32 + lane;
-        }
-        for (int g = g0; g < g1 && ok; ++g, ++acc_it) {
-          const uint32_t a = acc_it % kAccs;
-          ok = warp_wait(&ctl->acc_full[a], (acc_it / kAccs) & 1, ctl, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          const unsigned blocks = tb.blocks[g];
-          for (int c = half; c < kTile / 16; c += 2) {
-            if (!(blocks >> c & 1)) continue;
-            uint32_t v[16];
-            tmem_ld16_sync(tmem + a * kTile + c * 16 + ((uint32_t)(quad * 32) << 16), v);
-            const uint4 of = *reinterpret_cast<const uint4*>(tb.slot + c * 16);
-            const float4* up = reinterpret_cast<const float4*>(sh->row_scale + c * 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 f = up[i];
-              v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) * f.x);
-              v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) * f.y);
-              v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) * f.z);
-              v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) * f.w);
-            }
-            if (u.nio) {
-              uint16_t* col = buf + c * 16 * kTile;
-              uint16_t old[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) old[i] = add ? col[i * kTile] : (uint16_t)0;
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                old[i] = to_half_bits(from_half_bits(old[i], bf) + __uint_as_float(v[i]), bf);
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (byte_of(of, i) == g) col[i * kTile] = old[i];
-            } else if (n < p.N) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                if (byte_of(of, i) != g) continue;
-                const int64_t row = row0 + c * 16 + i;
-                const float o = add ? load_as(p.base, p.out_dtype, row * p.base_stride + n) : 0.0f;
-                store_out(p.out, p.out_dtype, row * p.out_stride + n, o + __uint_as_float(v[i]));
+          return warp_wait(&ctl->tile_full, tiles++ & 1, ctl, p.status);
+        },
+        [&](int n0, int part) {
+          const int g1 = tb.round_start[first_round(part + 1)];
+          for (int g = tb.round_start[first_round(part)]; g < g1; ++g) {
+            const int key = tb.group_key[g];
+            for (int k = 0; k < kblocks; ++k) {
+              if (!warp_wait(&ctl->empty[w.slot], w.turn ^ 1, ctl, p.status)) return false;
+              if (el) {
+                mbar_arrive_expect_tx(&ctl->full[w.slot], kTile * u.line);
+                tma_load_3d(slots + w.slot * kTile * u.line, &map_b, &ctl->full[w.slot], k * 64, n0, key);
               }
+              w.next(u.slots);
+              ++it;
             }
-            __syncwarp();
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->acc_empty[a]);
-        }
-        // rows without an adapter: base as it is, or 0
-        const bool copies = part == 0 && p.base != p.out;
-        if (u.nio) {
-          if (!add && part == 0)
-            for (int t = half; t < tb.rows; t += 2)
-              if (tb.slot[t] == kNone) buf[t * kTile] = 0;
-          fence_proxy_async_smem();
-          epilogue_barrier();
-          if (whole) {
-            if (warp == 4 && lane == 0) {
-              if (ok) tma_store_2d(&map_out, io + s * kIoBytes, n0, (int)row0);
+          return true;
+        },
+        [] { return true; });
+    if (ctl->abort_flag) {
+      for (uint32_t j = it < (uint32_t)u.slots ? 0 : it - u.slots; j < it; ++j)
+        wait_drain(&ctl->full[j % u.slots], (j / u.slots) & 1);
+      if (tiles) wait_drain(&ctl->tile_full, (tiles - 1) & 1);
+    }
+  } else if (warp == 2) {
+    // ----------------------------------------------------------- MMAs --
+    // Of the columns only those of a group's range.
+    const bool el = elect_one();
+    const uint32_t idesc = idesc_16(p.bf16, kTile, 0, false, false);
+    const uint32_t hb = smem_addr(hs), sb = smem_addr(slots);
+    const uint64_t desc = smem_desc_k(0, u.line);
+    Ring w, ar;
+    uint32_t tiles = 0;
+    walk([&](int) { return warp_wait(&ctl->tile_full, tiles++ & 1, ctl, p.status); },
+         [&](int, int part) {
+           const int r1 = first_round(part + 1);
+           for (int rd = first_round(part); rd < r1; ++rd) {
+             if (!warp_wait(&ctl->acc_empty[ar.slot], ar.turn ^ 1, ctl, p.status)) return false;
+             tc_fence_after();
+             const int g1 = tb.round_start[rd + 1];
+             for (int g = tb.round_start[rd]; g < g1; ++g) {
+               const int range = tb.group_range[g];
+               const int c0 = range & 0xff, c1 = range >> 8 & 0xff;
+               const uint32_t acc = tmem + (ar.slot * 2 + (range >> 16 & 1)) * kTile + c0 * 16;
+               const uint32_t id = idesc | (uint32_t)(c1 - c0) * 2 << 17;
+               for (int k = 0; k < kblocks; ++k) {
+                 if (!warp_wait(&ctl->full[w.slot], w.turn, ctl, p.status)) return false;
+                 if (el) {
+                   const uint64_t ad = desc + ((sb + w.slot * kTile * u.line) >> 4);
+#pragma unroll
+                   for (int j = 0; j < 4; ++j) {
+                     if (k * 4 + j >= ksteps) break;
+#pragma unroll
+                     for (int half = 0; half < 2; ++half) {
+                       const int c = k * 4 + j + half * (u.rp / 16);  // the step's place among the columns' k
+                       const uint64_t bd = smem_desc_k_sw128(hb + (c >> 2) * kSlot + c0 * 2048);
+                       mma_ss<1>(acc, ad + j * 2, bd + (c & 3) * 2, id, k | j | half);
+                     }
+                   }
+                   mma_commit(&ctl->empty[w.slot]);
+                 }
+                 w.next(u.slots);
+               }
+             }
+             if (el) mma_commit(&ctl->acc_full[ar.slot]);
+             ar.next(2);
+           }
+           return true;
+         },
+         [&] {
+           if (el) mma_commit(&ctl->tile_empty);
+           return true;
+         });
+    if (el) mma_commit(&ctl->drain);
+    wait_drain(&ctl->drain, 0);
+  } else if (warp == 3) {
+    // -------------------------------------------------------------- out --
+    // Finished buffers to memory: whole tiles by TMA, of others the rows that the unit
+    // writes.  Apart from the epilogue, so that a buffer is free for the next load as
+    // soon as it has been read.
+    Ring io_r;
+    uint32_t tiles = 0;
+    int tile = 0;
+    walk(
+        [&](int t) {
+          tile = t;
+          return warp_wait(&ctl->tile_full, tiles++ & 1, ctl, p.status);
+        },
+        [&](int n0, int part) {
+          if (!u.nio) return true;  // (the epilogue stores by itself)
+          const uint32_t s = io_r.slot;
+          if (!warp_wait(&ctl->io_done[s], io_r.turn, ctl, p.status)) return false;
+          if (tb.inside == tb.rows && u.gparts == 1) {
+            if (lane == 0) {
+              tma_store_2d(&map_out, io + s * kIoBytes, n0, tile * kTile);
+              if (n0 + 64 < p.N) tma_store_2d(&map_out, io + s * kIoBytes + kIoBytes / 2, n0 + 64, tile * kTile);
               bulk_commit();
-              // the store before this one has read its buffer
-              bulk_wait_read<1>();
-              if (un > ua) mbar_arrive(&ctl->io_empty[(io_it - 1) % u.nio]);
+              bulk_wait_read<0>();
             }
           } else {
+            const int r0 = first_round(part), r1 = first_round(part + 1);
             const int live = min(kTile, p.N - n0);  // (a multiple of 8)
-            for (int t = warp - 4; t < tb.rows && ok; t += kUpEpi) {
-              const int sl = tb.slot[t];
-              const bool write = sl == kNone ? copies : sl != kOut && sl >= g0 && sl < g1;
+            for (int t = 0; t < tb.rows; ++t) {
+              const int color = tb.color[t];
+              const bool write = color == kNone ? part == 0 && p.base != p.out
+                                                : color != kOut && color >> 1 >= r0 && color >> 1 < r1;
               if (!write || lane * 4 >= live) continue;
-              const uint2 q = *reinterpret_cast<const uint2*>(io + s * kIoBytes + t * kTile * 2 + lane * 8);
-              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (row0 + t) * p.out_stride + n0 + lane * 4) = q;
+              const uint2 q = *reinterpret_cast<const uint2*>(io + s * kIoBytes + io_offset(t, lane >> 1) + (lane & 1) * 8);
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((int64_t)tile * kTile + t) * p.out_stride +
+                                        n0 + lane * 4) = q;
             }
-            epilogue_barrier();
-            if (warp == 4 && lane == 0) mbar_arrive(&ctl->io_empty[s]);
           }
-          ++io_it;
-        } else if (copies) {
-          for (int t = half; t < tb.rows; t += 2)
-            if (tb.slot[t] == kNone && n < p.N)
-              copy_element(p.out, (row0 + t) * p.out_stride + n, p.base, (row0 + t) * p.base_stride + n,
-                           p.out_dtype);
-        }
-      }
-      if (u.nio && whole && warp == 4 && lane == 0) {
-        bulk_wait_read<0>();
-        mbar_arrive(&ctl->io_empty[(io_it - 1) % u.nio]);
-      }
-    }
-    __syncwarp();
-  }
-  if (warp == 0 && ctl->abort_flag)  // loads in flight land before the CTA goes
-    for (uint32_t j = w_it < (uint32_t)u.slots ? 0 : w_it - u.slots; j < w_it; ++j)
-      wait_drain(&ctl->full[j % u.slots], (j / u.slots) & 1);
-  if (warp == 1) {
-    if (elect_one()) mma_commit(&ctl->drain);
-    __syncwarp();
-    wait_drain(&ctl->drain, 0);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->io_empty[s]);
+          io_r.next(u.nio);
+          return true;
+        },
+        [&] {
+          if (lane == 0) mbar_arrive(&ctl->tile_empty);
+          return true;
+        });
+  } else {
+    // ------------------------------------------------------- epilogue --
+    // A lane is an output, the columns are the rows.
+    constexpr int kParts = kUpEpi / 4;
+    const int quad = warp & 3, sub = (warp - 4) >> 2;  // lanes, and which blocks of 16 rows
+    Ring ar, io_r;
+    uint32_t tiles = 0;
+    int64_t row0 = 0;
+    walk(
+        [&](int tile) {
+          row0 = (int64_t)tile * kTile;
+          return warp_wait(&ctl->tile_full, tiles++ & 1, ctl, p.status);
+        },
+        [&](int n0, int part) {
+          const int n = n0 + quad * 32 + lane;
+          const uint32_t buf = smem_addr(io) + io_r.slot * kIoBytes;
+          if (u.nio && !warp_wait(&ctl->io_full[io_r.slot], io_r.turn, ctl, p.status)) return false;
+          const int r1 = first_round(part + 1);
+          for (int rd = first_round(part); rd < r1; ++rd) {
+            if (!warp_wait(&ctl->acc_full[ar.slot], ar.turn, ctl, p.status)) return false;
+            tc_fence_after();
+            const uint32_t acc = tmem + ar.slot * 2 * kTile + ((uint32_t)(quad * 32) << 16);
+            for (int c = sub; c < kTile / 16; c += kParts) {
+              const uint4 color = *reinterpret_cast<const uint4*>(tb.color + c * 16);
+              const uint4 in = rows_of_round(color, rd);
+              if (!(in.x | in.y | in.z | in.w)) continue;
+              const uint4 odd = make_uint4(in.x & color.x, in.y & color.y, in.z & color.z, in.w & color.w);
+              const bool two = (odd.x | odd.y | odd.z | odd.w) & 0x01010101u;  // some of the second color
+              if (u.nio) {
+                uint32_t v[2][8], w[2][8];
+                tmem_ld_frag16_sync(acc + c * 16, v);
+                if (two) tmem_ld_frag16_sync(acc + kTile + c * 16, w);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // rows 8 h + 2 (lane % 4) and the next
+                  const uint32_t half_in = lane & 2 ? (h ? in.w : in.y) : (h ? in.z : in.x);
+                  const uint32_t half_odd = lane & 2 ? (h ? odd.w : odd.y) : (h ? odd.z : odd.x);
+                  const int shift = (lane & 1) * 16;
+                  if (two) {
+                    const bool o0 = half_odd >> shift & 1, o1 = half_odd >> shift & 0x100;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      const int r = 4 * h + 2 * (k & 1);
+                      v[k >> 1][r] = o0 ? w[k >> 1][r] : v[k >> 1][r];
+                      v[k >> 1][r + 1] = o1 ? w[k >> 1][r + 1] : v[k >> 1][r + 1];
+                    }
+                  }
+                  const int t0 = c * 16 + h * 8;
+                  add_rows8<BF16>(buf, quad, t0, v, h, half_in >> shift & 1, half_in >> shift & 0x100,
+                                  *reinterpret_cast<const float2*>(tb.row_scale + t0 + 2 * (lane & 3)), add, lane);
+                }
+              } else {
+                uint32_t v[16];
+                tmem_ld16_sync(acc + c * 16, v);
+                if (two) {
+                  uint32_t w[16];
+                  tmem_ld16_sync(acc + kTile + c * 16, w);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) v[i] = byte_of(odd, i) & 1 ? w[i] : v[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const int t = c * 16 + i;
+                  if (!byte_of(in, i) || n >= p.N) continue;
+                  const float o = add ? load_as(p.base, p.out_dtype, (row0 + t) * p.base_stride + n) : 0.0f;
+                  store_out(p.out, p.out_dtype, (row0 + t) * p.out_stride + n,
+                            fmaf(__uint_as_float(v[i]), tb.row_scale[t], o));
+                }
+              }
+              __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->acc_empty[ar.slot]);
+            ar.next(2);
+          }
+          // rows without an adapter: base as it is, or 0
+          if (u.nio) {
+            // (each warp where it has added itself: a block of rows is read and written whole)
+            if (!add && part == 0)
+              for (int c = sub; c < kTile / 16; c += kParts)
+                for (int t = c * 16; t < c * 16 + 16; ++t)
+                  if (tb.color[t] == kNone && lane < 4)
+                    *reinterpret_cast<uint4*>(io + io_r.slot * kIoBytes + io_offset(t, quad * 4 + lane)) =
+                        make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->io_done[io_r.slot]);
+            io_r.next(u.nio);
+          } else if (part == 0 && p.base != p.out) {
+            for (int t = sub; t < tb.rows; t += kParts)
+              if (tb.color[t] == kNone && n < p.N)
+                copy_element(p.out, (row0 + t) * p.out_stride + n, p.base, (row0 + t) * p.base_stride + n,
+                             p.out_dtype);
+          }
+          __syncwarp();
+          return true;
+        },
+        [&] {
+          if (lane == 0) mbar_arrive(&ctl->tile_empty);
+          return true;
+        });
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 2) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------ host side --
@@ -925,9 +1114,28 @@ cudaError_t launch_rows(const LoraArgs& g, cudaStream_t st) {
   return launch_pdl_cluster(lora_rows<BF16, 16>, grid, block, kCluster, 0, st, g);
 }
 
+// The workspace: tables, then the second product's operand.
+struct LoraLayout {
+  int64_t tiles;
+  size_t h, total;
+};
+LoraLayout lora_layout(int64_t R, int r) {
+  LoraLayout y;
+  y.tiles = (R + kTile - 1) / kTile;
+  y.h = ((size_t)y.tiles * sizeof(TileTable) + 255) & ~(size_t)255;
+  y.total = y.h + (size_t)y.tiles * kTile * h_row(padded_rank(r)) * 2;
+  return y;
+}
+
 cudaError_t launch_down(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
   const CUtensorMapDataType dt = g.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const int rp = padded_rank(g.r);
+  const LoraLayout y = lora_layout(g.R, g.r);
+  DownShape d;
+  d.rp = padded_rank(g.r);
+  d.splits = pl.splits;
+  d.mparts = pl.mparts;
+  d.tables = reinterpret_cast<TileTable*>(g.workspace);
+  d.h = reinterpret_cast<uint16_t*>(g.workspace + y.h);
   CUtensorMap mx, ma;
   const cuuint64_t xd[2] = {(cuuint64_t)g.K, (cuuint64_t)g.R}, xs = 2 * (cuuint64_t)g.x_stride;
   const cuuint32_t xb[2] = {64, kTile};
@@ -935,35 +1143,39 @@ cudaError_t launch_down(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) 
   if (err != cudaSuccess) return err;
   const cuuint64_t ad[3] = {(cuuint64_t)g.K, (cuuint64_t)g.r, (cuuint64_t)g.L * g.E};
   const cuuint64_t as[2] = {2 * (cuuint64_t)g.K, 2 * (cuuint64_t)g.K * g.r};
-  const cuuint32_t ab[3] = {64, (cuuint32_t)rp, 1};
+  const cuuint32_t ab[3] = {64, (cuuint32_t)d.rp, 1};
   err = make_map(&ma, dt, 3, g.a, ad, as, ab);
   if (err != cudaSuccess) return err;
-  constexpr size_t smem = 1024 + kDownSlots * kSlot + sizeof(DownShared);
-  static_assert(smem <= kSmemMax, "shared memory");
+  constexpr size_t fixed = 1024 + (kXSlots + kASlots) * kSlot + sizeof(DownShared);
+  static_assert(fixed + sizeof(float) * kTile * h_pitch(kMaxRank) <= kSmemMax, "shared memory");
+  static_assert(fixed >= 120 * 1024, "one CTA per SM: each allocates all of tensor memory");
+  const size_t smem = fixed + sizeof(float) * kTile * h_pitch(d.rp);
   static std::atomic<uint64_t> ready{0};
-  err = allow_smem(lora_down, smem, ready);
+  err = allow_smem(lora_down, kSmemMax, ready);
   if (err != cudaSuccess) return err;
-  const int64_t tiles = (g.R + kTile - 1) / kTile;
-  return launch_pdl(lora_down, dim3((unsigned)(tiles * pl.splits * pl.mparts)), dim3(kDownThreads), smem, st, mx,
-                    ma, g, rp, pl.splits, pl.mparts);
+  return launch_pdl_cluster(lora_down, dim3((unsigned)(y.tiles * pl.splits * pl.mparts)), dim3(kDownThreads),
+                            pl.splits, smem, st, mx, ma, g, d);
 }
 
 cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
   const CUtensorMapDataType dt = g.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const LoraLayout y = lora_layout(g.R, g.r);
   UpShape u;
   u.rp = padded_rank(g.r);
-  u.splits = pl.splits;
   u.gparts = pl.gparts;
   u.ntiles = (g.N + kTile - 1) / kTile;
-  u.units = (int)((g.R + kTile - 1) / kTile) * u.ntiles * u.gparts;
+  u.units = (int)y.tiles * u.ntiles * u.gparts;
+  u.tables = reinterpret_cast<const TileTable*>(g.workspace);
   // base and out by TMA: 16 bits, rows on 16-byte boundaries
   const bool base_ok = !g.base || (g.base_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(g.base) & 15u) == 0);
   const bool tma = g.out_dtype != MQ_DTYPE_F32 && base_ok && g.out_stride % 8 == 0 && g.N % 8 == 0 &&
                    (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
-  u.nio = !tma ? 0 : u.rp == 128 ? 2 : kMaxIo;
+  // In flight at a time: as many buffers of base, and as many groups, as fit beside the
+  // rows (K = N = 4096, 4099 rows, rank 64: with three buffers instead of four ...).
+  u.nio = !tma ? 0 : u.rp == 128 ? 3 : 4;
   u.line = std::min(u.rp, 64) * 2;
-  u.slots = std::min(kMaxUpSlots, kUpBytes / (kTile * u.line));
-  CUtensorMap mb, mbase, mout;
+  u.slots = u.rp >= 64 ? 3 : 65536 / (kTile * u.line);
+  CUtensorMap mb, mh, mbase, mout;
   const cuuint64_t bd[3] = {(cuuint64_t)g.r, (cuuint64_t)g.N, (cuuint64_t)g.L * g.E};
   const cuuint64_t bs[2] = {2 * (cuuint64_t)g.r, 2 * (cuuint64_t)g.r * g.N};
   const cuuint32_t bb[3] = {(cuuint32_t)u.line / 2, kTile, 1};
@@ -972,30 +1184,47 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
                              : u.line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                             : CU_TENSOR_MAP_SWIZZLE_32B);
   if (err != cudaSuccess) return err;
+  const cuuint64_t hd[2] = {(cuuint64_t)h_row(u.rp), (cuuint64_t)y.tiles * kTile}, hst = 2 * hd[0];
+  const cuuint32_t hb[2] = {64, kTile};
+  err = make_map(&mh, dt, 2, g.workspace + y.h, hd, &hst, hb);
+  if (err != cudaSuccess) return err;
   mbase = mout = mb;
   if (tma) {
     const CUtensorMapDataType ot =
         g.out_dtype == MQ_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const cuuint64_t d[2] = {(cuuint64_t)g.N, (cuuint64_t)g.R};
-    const cuuint64_t s0 = 2 * (cuuint64_t)g.base_stride, s1 = 2 * (cuuint64_t)g.out_stride;
-    const cuuint32_t box[2] = {kTile, kTile};
-    err = make_map(&mout, ot, 2, g.out, d, &s1, box, CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (err == cudaSuccess && g.base) err = make_map(&mbase, ot, 2, g.base, d, &s0, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+    const cuuint64_t t0 = 2 * (cuuint64_t)g.base_stride, t1 = 2 * (cuuint64_t)g.out_stride;
+    const cuuint32_t box[2] = {kTile / 2, kTile};
+    err = make_map(&mout, ot, 2, g.out, d, &t1, box);
+    if (err == cudaSuccess && g.base) err = make_map(&mbase, ot, 2, g.base, d, &t0, box);
     if (err != cudaSuccess) return err;
   }
-  constexpr size_t most = 1024 + 4 * kSlot + kUpBytes + 2 * kIoBytes + sizeof(UpShared);
-  constexpr size_t most3 = 1024 + 2 * kSlot + kUpBytes + 3 * kIoBytes + sizeof(UpShared);
-  static_assert(most <= kSmemMax && most3 <= kSmemMax, "shared memory");
-  const size_t need = 1024 + (2 * u.rp + 63) / 64 * kSlot + kUpBytes + (size_t)u.nio * kIoBytes + sizeof(UpShared);
+  const size_t need = 1024 + (2 * u.rp + 63) / 64 * kSlot + (size_t)u.slots * kTile * u.line + (size_t)u.nio * kIoBytes + sizeof(UpShared);
+  static_assert(1024 + 4 * kSlot + 3 * kSlot + 3 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
+                    1024 + 2 * kSlot + 3 * kSlot + 4 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
+                    1024 + kSlot + 65536 + 4 * kIoBytes + sizeof(UpShared) <= kSmemMax,
+                "shared memory");
   const size_t smem = std::max<size_t>(need, 120 * 1024);  // one CTA per SM: each allocates all of tensor memory
-  static std::atomic<uint64_t> ready{0};
-  err = allow_smem(lora_up, kSmemMax, ready);
+  static std::atomic<uint64_t> ready[2];
+  const bool bf = g.out_dtype == MQ_DTYPE_BF16;
+  const auto kern = bf ? lora_up<true> : lora_up<false>;
+  err = allow_smem(kern, kSmemMax, ready[bf]);
   if (err != cudaSuccess) return err;
-  const int grid = std::min(u.units, tc_num_sms());
-  return launch_pdl(lora_up, dim3(grid), dim3(kUpThreads), smem, st, mb, mbase, mout, g, u);
+  // A CTA fetches a tile's table and rows once for each tile that it works at, which
+  // takes about as long as a unit: whole shares of a tile each, where that costs less
+  // than an even share of all units.
+  const int sms = tc_num_sms(), tiles = (int)y.tiles, per_tile = u.ntiles * u.gparts;
+  int grid = std::min(u.units, sms);
+  if (tiles <= sms) {
+    const int shares = std::min(sms / tiles, per_tile);
+    if ((per_tile + shares - 1) / shares + 1 <= (u.units + grid - 1) / grid + 2) grid = tiles * shares;
+  }
+  return launch_pdl(kern, dim3(grid), dim3(kUpThreads), smem, st, mb, mh, mbase, mout, g, u);
 }
 
 }  // namespace
+
+size_t lora_workspace(int64_t R, int r) { return lora_layout(R, r).total; }
 
 LoraPlan lora_plan(int64_t R, int K, int N, int r, int L, int E) {
   LoraPlan pl = {};
@@ -1010,7 +1239,7 @@ LoraPlan lora_plan(int64_t R, int K, int N, int r, int L, int E) {
   const int tile_groups = (int)std::min<double>(kTile, groups);
   const int accs = (tile_groups + per - 1) / per;
   const int stages = (K + 63) / 64;
-  pl.splits = (int)std::max<int64_t>(1, std::min<int64_t>({16, stages / 4, sms / tiles}));
+  while (pl.splits < 8 && stages >= pl.splits * 8 && tiles * pl.splits * 2 <= sms) pl.splits *= 2;
   pl.mparts = (int)std::max<int64_t>(1, std::min<int64_t>(accs, sms / (tiles * pl.splits)));
   const int ntiles = (N + kTile - 1) / kTile;
   while (pl.gparts * 2 <= tile_groups && tiles * ntiles * pl.gparts * 2 <= sms) pl.gparts *= 2;

@@ -19,15 +19,16 @@ struct LoraArgs {
   void* out;                // [R][N]; may be base
   int64_t out_stride;
   int out_dtype;
-  float* part;              // [splits][R][r] partial sums of A x
+  uint8_t* workspace;       // of lora_workspace bytes, where the plan has tiles
   unsigned* status;
 };
 struct LoraPlan {
   bool rows;   // one cluster per row, one launch (else two launches over tiles of rows)
-  int splits;  // K splits of the first launch
-  int mparts;  // CTAs among which it divides a tile's adapters
+  int splits;  // K splits of the first launch: CTAs of a cluster
+  int mparts;  // clusters among which it divides a tile's adapters
   int gparts;  // parts of a tile's adapters in the second launch
 };
+MQ_HIDDEN size_t lora_workspace(int64_t R, int r);
 MQ_HIDDEN LoraPlan lora_plan(int64_t R, int K, int N, int r, int L, int E);
 // The plan's kernels one by one (which: 0 A x, or both in one; 1 the rest).
 MQ_HIDDEN cudaError_t launch_lora(const LoraArgs& g, const LoraPlan& pl, int which, cudaStream_t st);

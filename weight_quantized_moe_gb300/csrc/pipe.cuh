@@ -75,6 +75,18 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
     if (mq::global_timer_ns() - t0 > kWaitNs) return;
 }
 
+// A role's place in a ring of n slots: which slot, and how often round, mod 2.
+// (Counted on: a division by n costs more than a short stage.)
+struct Ring {
+  uint32_t slot = 0, turn = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++slot == n) {
+      slot = 0;
+      turn ^= 1;
+    }
+  }
+};
+
 __device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float v) {
   if (dtype == MQ_DTYPE_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
   else if (dtype == MQ_DTYPE_F16) static_cast<__half*>(out)[i] = __float2half_rn(v);

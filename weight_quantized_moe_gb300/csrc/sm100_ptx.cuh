@@ -148,6 +148,16 @@ __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
   return r;
 }
 
+// Loads from a CTA of the cluster (an address of map_rank).
+__device__ __forceinline__ float4 load_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
@@ -408,6 +418,35 @@ __device__ __forceinline__ void tmem_ld16_sync(uint32_t taddr, uint32_t (&v)[16]
         "=r"(v[14]), "=r"(v[15])
       : "r"(taddr)
       : "memory");
+}
+
+// 32 lanes x 16 columns as 8 x 8 fragments, lanes in halves of 16: v[h][4 c + 2 l + i]
+// is lane 16 h + 8 l + (thread / 4), column 8 c + 2 (thread % 4) + i.
+__device__ __forceinline__ void tmem_ld_frag16_sync(uint32_t taddr, uint32_t (&v)[2][8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0][0]), "=r"(v[0][1]), "=r"(v[0][2]), "=r"(v[0][3]), "=r"(v[0][4]), "=r"(v[0][5]),
+        "=r"(v[0][6]), "=r"(v[0][7]), "=r"(v[1][0]), "=r"(v[1][1]), "=r"(v[1][2]), "=r"(v[1][3]),
+        "=r"(v[1][4]), "=r"(v[1][5]), "=r"(v[1][6]), "=r"(v[1][7])
+      : "r"(taddr), "r"(taddr + (16u << 16))
+      : "memory");
+}
+
+// Four 8 x 8 blocks of 16-bit values, transposed: thread t gives the address of row t %
+// 8 (16 bytes) of block t / 8, and has of each block the elements [2 (t % 4) + i][t / 4]
+// in one register, i = 0 in its low half.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
 }
 
 template <int N>
