@@ -654,9 +654,11 @@ __global__ void __launch_bounds__(kDownThreads, 1)
 }
 
 // ---- second launch: out = base + B (s h) ----
-constexpr int kUpEpi = 16;         // epilogue warps
-constexpr int kUpThreads = 128 + 32 * kUpEpi;
-constexpr int kMaxUpSlots = 16;
+// Warps 0 (base), 1 (B), 2 and 12 (MMAs), 3 (out), 4-11 (epilogue).
+constexpr int kUpEpi = 8;
+constexpr int kUpMma = 2;
+constexpr int kUpThreads = 128 + 32 * kUpEpi + 32;
+constexpr int kMaxUpSlots = 24;
 constexpr int kIoBytes = kTile * kTile * 2;
 constexpr int kMaxIo = 4;
 
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
       mbar_init(&ctl->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->acc_full[i], 1);
+      mbar_init(&ctl->acc_full[i], kUpMma);
       mbar_init(&ctl->acc_empty[i], kUpEpi);
     }
     for (int i = 0; i < kMaxIo; ++i) {
@@ -766,8 +768,8 @@ __global__ void __launch_bounds__(kUpThreads, 1)
       mbar_init(&ctl->io_empty[i], 1);
     }
     mbar_init(&ctl->tile_full, 1);
-    mbar_init(&ctl->tile_empty, 2 + kUpEpi);
-    mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->tile_empty, kUpMma + 1 + kUpEpi);
+    mbar_init(&ctl->drain, kUpMma);
     ctl->abort_flag = 0;
     fence_mbar_init();
   }
@@ -884,9 +886,12 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         wait_drain(&ctl->full[j % u.slots], (j / u.slots) & 1);
       if (tiles) wait_drain(&ctl->tile_full, (tiles - 1) & 1);
     }
-  } else if (warp == 2) {
+  } else if (warp == 2 || warp == 12) {
     // ----------------------------------------------------------- MMAs --
-    // Of the columns only those of a group's range.
+    // Of the columns only those of a group's range.  Groups are small (their four to
+    // eight instructions take less than the way to them): two warps take them in turn.
+    const bool second = warp == 12;
+    bool odd = false;
     const bool el = elect_one();
     const uint32_t idesc = idesc_16(p.bf16, kTile, 0, false, false);
     const uint32_t hb = smem_addr(hs), sb = smem_addr(slots);
@@ -900,7 +905,11 @@ __global__ void __launch_bounds__(kUpThreads, 1)
              if (!warp_wait(&ctl->acc_empty[ar.slot], ar.turn ^ 1, ctl, p.status)) return false;
              tc_fence_after();
              const int g1 = tb.round_start[rd + 1];
-             for (int g = tb.round_start[rd]; g < g1; ++g) {
+             for (int g = tb.round_start[rd]; g < g1; ++g, odd = !odd) {
+               if (odd != second) {
+                 for (int k = 0; k < kblocks; ++k) w.next(u.slots);
+                 continue;
+               }
                const int range = tb.group_range[g];
                const int c0 = range & 0xff, c1 = range >> 8 & 0xff;
                const uint32_t acc = tmem + (ar.slot * 2 + (range >> 16 & 1)) * kTile + c0 * 16;
@@ -1172,9 +1181,9 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
                    (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
   // In flight at a time: as many buffers of base, and as many groups, as fit beside the
   // rows (K = N = 4096, 4099 rows, rank 64: with three buffers instead of four ...).
-  u.nio = !tma ? 0 : u.rp == 128 ? 3 : 4;
+  u.nio = !tma ? 0 : u.rp == 64 ? 4 : 3;
   u.line = std::min(u.rp, 64) * 2;
-  u.slots = u.rp >= 64 ? 3 : 65536 / (kTile * u.line);
+  u.slots = u.rp >= 64 ? 3 : 98304 / (kTile * u.line);
   CUtensorMap mb, mh, mbase, mout;
   const cuuint64_t bd[3] = {(cuuint64_t)g.r, (cuuint64_t)g.N, (cuuint64_t)g.L * g.E};
   const cuuint64_t bs[2] = {2 * (cuuint64_t)g.r, 2 * (cuuint64_t)g.r * g.N};
@@ -1202,7 +1211,7 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
   const size_t need = 1024 + (2 * u.rp + 63) / 64 * kSlot + (size_t)u.slots * kTile * u.line + (size_t)u.nio * kIoBytes + sizeof(UpShared);
   static_assert(1024 + 4 * kSlot + 3 * kSlot + 3 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
                     1024 + 2 * kSlot + 3 * kSlot + 4 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
-                    1024 + kSlot + 65536 + 4 * kIoBytes + sizeof(UpShared) <= kSmemMax,
+                    1024 + kSlot + 98304 + 3 * kIoBytes + sizeof(UpShared) <= kSmemMax,
                 "shared memory");
   const size_t smem = std::max<size_t>(need, 120 * 1024);  // one CTA per SM: each allocates all of tensor memory
   static std::atomic<uint64_t> ready[2];
