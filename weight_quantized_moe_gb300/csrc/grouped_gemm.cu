@@ -44,7 +44,7 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kMaxStages = 12;
 constexpr int kMaxE = 1024;
-constexpr int kUnitList = 128;  // units of a CTA that are decoded at its start
+constexpr int kUnitList = 256;  // units of a CTA that are decoded at its start
 constexpr int kGroup = 8;       // M tiles that a walk over the columns shares
 constexpr int kPartRows = 16;   // rows of the boxes that load a partly filled chunk
 constexpr size_t kSmemMax = 227 * 1024;
@@ -81,6 +81,7 @@ struct Params {
   int mtiles, ntiles, splits;
   uint32_t idesc;  // without N
   bool evict_first;
+  bool listed;       // tiles are numbered in 16 bits: units fit the list
   bool vector_rows;  // GG_ROWS: a result's rows start at 32-byte boundaries
   bool zero_outside;
   void* out;
@@ -162,11 +163,13 @@ __device__ __forceinline__ Unit decode_unit(const Params& p, const int* chunk_st
 }
 
 // The i-th unit of this worker: from the list in shared memory (decoded once, by
-// all threads at a time), past its end on the spot.
+// all threads at a time), past its end on the spot.  (Each role decoding each of its
+// units cost GG_ROWS, whose units are short, more than their work: 128 experts, 4096
+// rows, 1536 x 2048 ... us.)
 template <int FORM, int BN, int CG>
 __device__ __forceinline__ Unit unit_at(const Params& p, const int* chunk_start, const int4* list,
                                         uint32_t i) {
-  if (FORM == GG_ROWS || i >= kUnitList)
+  if (i >= kUnitList || !p.listed)
     return decode_unit<FORM, BN, CG>(p, chunk_start, blockIdx.x / CG + i * (gridDim.x / CG));
   const int4 v = list[i];
   Unit w;
@@ -175,8 +178,8 @@ __device__ __forceinline__ Unit unit_at(const Params& p, const int* chunk_start,
   w.split = v.x >> 17;
   w.row0 = v.y;
   w.n = v.z;
-  w.m = v.w;
-  w.col0 = 0;
+  w.m = (int)((uint32_t)v.w & 0xffffu) * (kTileM * CG);
+  w.col0 = (int)((uint32_t)v.w >> 16) * BN;
   return w;
 }
 
@@ -313,9 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t chunks = FORM == GG_ROWS ? (uint32_t)p.E * p.ntiles : (uint32_t)chunk_start[p.E];
   const uint32_t total = bad ? 0 : chunks * p.mtiles * p.splits;
   const uint32_t units = worker < total ? (total - worker + workers - 1) / workers : 0;
-  if (FORM != GG_ROWS && tid < kUnitList && tid < units) {
+  if (p.listed && tid < kUnitList && tid < units) {
     const Unit w = decode_unit<FORM, BN, CG>(p, chunk_start, worker + tid * workers);
-    list[tid] = make_int4(w.e | (w.single ? 1 << 16 : 0) | w.split << 17, w.row0, w.n, w.m);
+    list[tid] = make_int4(w.e | (w.single ? 1 << 16 : 0) | w.split << 17, w.row0, w.n,
+                          w.m / (kTileM * CG) | (w.col0 / BN) << 16);
   }
   tc_fence_before();
   if (CG == 2) cluster_sync();  // (the barriers are set up in both)
@@ -515,7 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t at = ((int64_t)w.e * p.M + m) * p.N + w.col0;
         const int n = min(BN, p.N - w.col0);
         if (m - lane < p.M) {
-          for (int c0 = half * 16; c0 < n; c0 += 32) {
+          // (half of the columns each, so that a line is written at one go)
+          const int c1 = min(n, (half + 1) * (BN / 2));
+          for (int c0 = half * (BN / 2); c0 < c1; c0 += 16) {
             uint32_t v[16];
             if (empty) {
 #pragma unroll
@@ -660,6 +666,7 @@ cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
   p.splits = pl.splits;
   p.idesc = idesc_16(g.bf16, kTileM * cg, 0, g.form != GG_W_K, g.form == GG_ROWS);
   p.evict_first = true;
+  p.listed = p.mtiles < 1 << 16 && p.ntiles < 1 << 16;
   p.zero_outside = g.zero_outside;
   p.out = g.out;
   p.out_dtype = g.out_dtype;
