@@ -49,13 +49,16 @@ constexpr int kGroup = 8;       // M tiles that a walk over the columns shares
 constexpr int kPartRows = 16;   // rows of the boxes that load a partly filled chunk
 constexpr size_t kSmemMax = 227 * 1024;
 
-template <int BN, int CG>
+constexpr int kChunkBytes = 32 * 128;  // an epilogue warp's 32 lanes by 128 bytes of columns
+
+template <int FORM, int BN, int CG>
 struct Cfg {
   static constexpr int kBRows = BN / CG;  // columns whose operand each CTA holds
   static constexpr int kStageBytes = kABytes + kBRows * 128;
   static constexpr int kBufs = 2;
   static_assert(kBufs * BN <= 512, "tensor memory");
-  static constexpr size_t kFixed = 1024 + 1024 + kUnitList * 16 + (kMaxE + 1) * 4;
+  static constexpr size_t kOutBytes = FORM == GG_ROWS ? kEpiWarps * kChunkBytes : 0;
+  static constexpr size_t kFixed = 1024 + kOutBytes + 1024 + kUnitList * 16 + (kMaxE + 1) * 4;
   static constexpr int kFit = (int)((kSmemMax - kFixed) / kStageBytes);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static_assert(kStages >= 3, "shared memory");
@@ -82,7 +85,7 @@ struct Params {
   uint32_t idesc;  // without N
   bool evict_first;
   bool listed;       // tiles are numbered in 16 bits: units fit the list
-  bool vector_rows;  // GG_ROWS: a result's rows start at 32-byte boundaries
+  bool tma_out;      // GG_ROWS: the result's rows start at 16-byte boundaries
   bool zero_outside;
   void* out;
   int out_dtype;
@@ -203,53 +206,44 @@ __device__ __forceinline__ int columns(const Params& p, const Unit& w) {
   return min(BN, (n + 16 * CG - 1) & -(16 * CG));
 }
 
-// One lane's 16 columns of a GG_ROWS result, consecutive in memory from element i on.
-__device__ __forceinline__ void store_row16(void* out, int dtype, int64_t i, const uint32_t (&v)[16],
-                                            int live, bool vector) {
-  if (vector && live >= 16) {
-    if (dtype == MQ_DTYPE_F32) {
-      uint32_t* d = static_cast<uint32_t*>(out) + i;
-#pragma unroll
-      for (int j = 0; j < 16; j += 8)
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d + j),
-                     "r"(v[j]), "r"(v[j + 1]), "r"(v[j + 2]), "r"(v[j + 3]), "r"(v[j + 4]),
-                     "r"(v[j + 5]), "r"(v[j + 6]), "r"(v[j + 7])
-                     : "memory");
-      return;
-    }
-    uint32_t h[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = __uint_as_float(v[2 * j]), b = __uint_as_float(v[2 * j + 1]);
-      if (dtype == MQ_DTYPE_BF16) {
-        const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
-        h[j] = *reinterpret_cast<const uint32_t*>(&t);
-      } else {
-        const __half2 t = __floats2half2_rn(a, b);
-        h[j] = *reinterpret_cast<const uint32_t*>(&t);
-      }
-    }
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                     static_cast<uint16_t*>(out) + i),
-                 "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]),
-                 "r"(h[7])
-                 : "memory");
-    return;
+// Two float32 values rounded to a 16-bit type.
+__device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi, bool bf16) {
+  const float a = __uint_as_float(lo), b = __uint_as_float(hi);
+  if (bf16) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&t);
   }
+  const __half2 t = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// 32 columns of one lane's row of the result, into its line of the warp's buffer: all of
+// it (float32), or half h of it (16 bits).
+template <bool F32>
+__device__ __forceinline__ void stage_row32(uint8_t* line, int lane, int h, const uint32_t (&v)[32], bool bf16) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (j < live) store_out(out, dtype, i + j, __uint_as_float(v[j]));
+  for (int j = 0; j < (F32 ? 8 : 4); ++j) {
+    uint4 q;
+    if constexpr (F32) {
+      q = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    } else {
+      q = make_uint4(pack2(v[8 * j], v[8 * j + 1], bf16), pack2(v[8 * j + 2], v[8 * j + 3], bf16),
+                     pack2(v[8 * j + 4], v[8 * j + 5], bf16), pack2(v[8 * j + 6], v[8 * j + 7], bf16));
+    }
+    *reinterpret_cast<uint4*>(line + (((h * 4 + j) ^ (lane & 7)) << 4)) = q;
+  }
 }
 
 template <int FORM, int BN, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     gg_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
             const __grid_constant__ CUtensorMap map_part, const Params p) {
-  using C = Cfg<BN, CG>;
+  using C = Cfg<FORM, BN, CG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* stages = smem;
-  Ctl* ctl = reinterpret_cast<Ctl*>(stages + (size_t)C::kStages * C::kStageBytes);
+  uint8_t* chunks_out = stages + (size_t)C::kStages * C::kStageBytes;  // GG_ROWS
+  Ctl* ctl = reinterpret_cast<Ctl*>(chunks_out + C::kOutBytes);
   int4* list = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(ctl) + 1024);
   int* chunk_start = reinterpret_cast<int*>(list + kUnitList);
   const int tid = threadIdx.x;
@@ -514,22 +508,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t acc = tmem + buf * BN + ((uint32_t)(quad * 32) << 16);
       if constexpr (FORM == GG_ROWS) {
-        void* out = p.out;
-        if (p.splits > 1) out = p.part + (int64_t)w.split * p.E * p.M * p.N;
-        const int64_t at = ((int64_t)w.e * p.M + m) * p.N + w.col0;
+        // A lane is a row of the result: lines of 128 bytes of it go to shared memory
+        // (swizzled) and from there by TMA, which leaves out what lies outside.
         const int n = min(BN, p.N - w.col0);
+        const int c1 = min(n, (half + 1) * (BN / 2));
+        const bool f32 = dtype == MQ_DTYPE_F32;
+        const int step = f32 ? 32 : 64;
+        uint8_t* chunk = chunks_out + (warp - 4) * kChunkBytes;
         if (m - lane < p.M) {
-          // (half of the columns each, so that a line is written at one go)
-          const int c1 = min(n, (half + 1) * (BN / 2));
-          for (int c0 = half * (BN / 2); c0 < c1; c0 += 16) {
-            uint32_t v[16];
-            if (empty) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = 0;
-            } else {
-              tmem_ld16_sync(acc + c0, v);
+          for (int c0 = half * (BN / 2); c0 < c1; c0 += step) {
+            uint32_t v[32];
+            if (p.tma_out) {
+              if (lane == 0) bulk_wait_read<0>();  // the buffer's last line
+              __syncwarp();
             }
-            if (m < p.M) store_row16(out, dtype, at + c0, v, n - c0, p.vector_rows);
+            for (int h = 0; h < step / 32; ++h) {
+              if (empty) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0;
+              } else {
+                tmem_ld32_sync(acc + c0 + h * 32, v);
+              }
+              if (p.tma_out) {
+                if (f32) stage_row32<true>(chunk + lane * 128, lane, 0, v, false);
+                else stage_row32<false>(chunk + lane * 128, lane, h, v, dtype == MQ_DTYPE_BF16);
+              } else if (m < p.M) {
+                void* out = p.splits > 1 ? p.part + (int64_t)w.split * p.E * p.M * p.N : p.out;
+                const int64_t at = ((int64_t)w.e * p.M + m) * p.N + w.col0 + c0 + h * 32;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (c0 + h * 32 + i < n) store_out(out, dtype, at + i, __uint_as_float(v[i]));
+              }
+            }
+            if (p.tma_out) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_3d(&map_part, chunk, w.col0 + c0, m - lane, w.split * p.E + w.e);
+                bulk_commit();
+              }
+            }
           }
         }
       } else {
@@ -555,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  if (FORM == GG_ROWS && warp >= 4 && lane == 0) bulk_wait_read<0>();
   tc_fence_before();
   __syncwarp();
   if (CG == 2) cluster_sync();  // (the other CTA's shared memory is in use until here)
@@ -570,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int FORM, int BN, int CG>
 cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const CUtensorMap& mr,
                        const Params& p, int64_t units, cudaStream_t st) {
-  constexpr size_t smem = Cfg<BN, CG>::kSmem;
+  constexpr size_t smem = Cfg<FORM, BN, CG>::kSmem;
   auto kern = gg_gemm<FORM, BN, CG>;
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
   int dev = 0;
@@ -632,6 +651,7 @@ GgPlan gg_plan(GgForm form, int64_t R, int E, int M, int N, int K) {
 cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
   const CUtensorMapDataType dt = g.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const int cg = pl.pair ? 2 : 1;
+  bool tma_out = false;
   CUtensorMap mw, ma, mr;
   cudaError_t err;
   const cuuint64_t ws = 2 * (cuuint64_t)g.w_stride, as = 2 * (cuuint64_t)g.a_stride;
@@ -642,6 +662,19 @@ cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
     err = make_map(&mw, dt, 2, g.w, wd, &ws, block);
     if (err == cudaSuccess) err = make_map(&ma, dt, 2, g.a, ad, &as, block);
     mr = ma;
+    const bool f32 = pl.splits > 1 || g.out_dtype == MQ_DTYPE_F32;
+    const void* out = pl.splits > 1 ? g.part : g.out;
+    const cuuint64_t row = (cuuint64_t)g.N * (f32 ? 4 : 2);
+    tma_out = row % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && row * g.M < cuuint64_t(1) << 40;
+    if (err == cudaSuccess && tma_out) {
+      const cuuint64_t od[3] = {(cuuint64_t)g.N, (cuuint64_t)g.M, (cuuint64_t)g.E * pl.splits};
+      const cuuint64_t os[2] = {row, row * g.M};
+      const cuuint32_t ob[3] = {f32 ? 32u : 64u, 32, 1};
+      const CUtensorMapDataType ot = f32                               ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : g.out_dtype == MQ_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+      err = make_map(&mr, ot, 3, out, od, os, ob);
+    }
   } else {
     const bool by_k = g.form == GG_W_K;
     const cuuint64_t wd[3] = {(cuuint64_t)(by_k ? g.K : g.M), (cuuint64_t)(by_k ? g.M : g.K), (cuuint64_t)g.E};
@@ -672,9 +705,7 @@ cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
   p.out_dtype = g.out_dtype;
   p.part = g.part;
   p.status = g.status;
-  const int64_t elem = pl.splits > 1 || g.out_dtype == MQ_DTYPE_F32 ? 4 : 2;
-  p.vector_rows = (int64_t)g.N * elem % 32 == 0 &&
-                  (reinterpret_cast<uintptr_t>(pl.splits > 1 ? (void*)g.part : g.out) & 31u) == 0;
+  p.tma_out = tma_out;
   const int64_t live = std::min<int64_t>(g.R, g.E);
   const int64_t units = (g.form == GG_ROWS ? (int64_t)g.E * p.ntiles : live + g.R / pl.bn) * p.mtiles * p.splits;
   switch (g.form) {
