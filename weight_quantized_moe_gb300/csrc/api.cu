@@ -1097,26 +1097,33 @@ MQ_EXPORT int moe_grouped_product_grad(const void* dy, int64_t dy_stride, const 
   g.bf16 = dtype == MQ_DTYPE_BF16;
   g.R = R; g.E = E;
   g.offsets = expert_offsets;
+  GgGemm of_rows = g, of_weights = g;
   if (da) {  // W's outputs are the contraction: the other of the two storages
-    g.form = w_transposed ? GG_W_K : GG_W_M;
-    g.w = w; g.w_stride = w_stride; g.w_expert = w_expert_stride;
-    g.a = dy; g.a_stride = dy_stride;
-    g.M = K; g.K = N;
-    g.out = da; g.out_dtype = dtype;
-    g.zero_outside = true;
-    const int r = gg_run(g, workspace, ws_bytes, st);
-    if (r != MQ_OK) return r;
+    of_rows.form = w_transposed ? GG_W_K : GG_W_M;
+    of_rows.w = w; of_rows.w_stride = w_stride; of_rows.w_expert = w_expert_stride;
+    of_rows.a = dy; of_rows.a_stride = dy_stride;
+    of_rows.M = K; of_rows.K = N;
+    of_rows.out = da; of_rows.out_dtype = dtype;
+    of_rows.zero_outside = true;
   }
   if (dw) {  // laid out as the weights are
-    g.form = GG_ROWS;
-    g.w = w_transposed ? a : dy; g.w_stride = w_transposed ? a_stride : dy_stride; g.w_expert = 0;
-    g.a = w_transposed ? dy : a; g.a_stride = w_transposed ? dy_stride : a_stride;
-    g.M = w_transposed ? K : N; g.N = w_transposed ? N : K; g.K = 0;
-    g.out = dw; g.out_dtype = dw_dtype;
-    g.zero_outside = false;
-    return gg_run(g, workspace, ws_bytes, st);
+    of_weights.form = GG_ROWS;
+    of_weights.w = w_transposed ? a : dy; of_weights.w_stride = w_transposed ? a_stride : dy_stride;
+    of_weights.a = w_transposed ? dy : a; of_weights.a_stride = w_transposed ? dy_stride : a_stride;
+    of_weights.M = w_transposed ? K : N; of_weights.N = w_transposed ? N : K;
+    of_weights.out = dw; of_weights.out_dtype = dw_dtype;
   }
-  return MQ_OK;
+  if (da && dw && gg_side_by_side(of_rows, of_weights)) {
+    of_rows.status = of_weights.status = status_ptr();
+    LaunchScope ls(MQ_PROF_GEMM1, st);
+    const cudaError_t err = launch_gg_both(of_rows, of_weights, st);
+    return err == cudaSuccess ? MQ_OK : cuda_fail(err, "grouped product's gradients launch");
+  }
+  if (da) {
+    const int r = gg_run(of_rows, workspace, ws_bytes, st);
+    if (r != MQ_OK) return r;
+  }
+  return dw ? gg_run(of_weights, workspace, ws_bytes, st) : MQ_OK;
 }
 
 static bool lora_sizes_ok(int64_t R, int K, int N, int r, int L, int E) {

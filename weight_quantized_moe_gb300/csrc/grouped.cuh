@@ -38,3 +38,6 @@ struct GgPlan {
 };
 MQ_HIDDEN GgPlan gg_plan(GgForm form, int64_t R, int E, int M, int N, int K);
 MQ_HIDDEN cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st);
+// Both gradients of a product in one launch, and whether that is the better way.
+MQ_HIDDEN bool gg_side_by_side(const GgGemm& rows, const GgGemm& weights);
+MQ_HIDDEN cudaError_t launch_gg_both(const GgGemm& rows, const GgGemm& weights, cudaStream_t st);

@@ -50,6 +50,7 @@ constexpr int kPartRows = 16;   // rows of the boxes that load a partly filled c
 constexpr size_t kSmemMax = 227 * 1024;
 
 constexpr int kChunkBytes = 32 * 128;  // an epilogue warp's 32 lanes by 128 bytes of columns
+constexpr int kChunks = 2;             // of each warp
 
 template <int FORM, int BN, int CG>
 struct Cfg {
@@ -57,7 +58,7 @@ struct Cfg {
   static constexpr int kStageBytes = kABytes + kBRows * 128;
   static constexpr int kBufs = 2;
   static_assert(kBufs * BN <= 512, "tensor memory");
-  static constexpr size_t kOutBytes = FORM == GG_ROWS ? kEpiWarps * kChunkBytes : 0;
+  static constexpr size_t kOutBytes = FORM == GG_ROWS ? kEpiWarps * kChunks * kChunkBytes : 0;
   static constexpr size_t kFixed = 1024 + kOutBytes + 1024 + kUnitList * 16 + (kMaxE + 1) * 4;
   static constexpr int kFit = (int)((kSmemMax - kFixed) / kStageBytes);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
@@ -171,9 +172,9 @@ __device__ __forceinline__ Unit decode_unit(const Params& p, const int* chunk_st
 // rows, 1536 x 2048 ... us.)
 template <int FORM, int BN, int CG>
 __device__ __forceinline__ Unit unit_at(const Params& p, const int* chunk_start, const int4* list,
-                                        uint32_t i) {
+                                        uint32_t i, uint32_t worker, uint32_t workers) {
   if (i >= kUnitList || !p.listed)
-    return decode_unit<FORM, BN, CG>(p, chunk_start, blockIdx.x / CG + i * (gridDim.x / CG));
+    return decode_unit<FORM, BN, CG>(p, chunk_start, worker + i * workers);
   const int4 v = list[i];
   Unit w;
   w.e = v.x & 0xffff;
@@ -234,10 +235,11 @@ __device__ __forceinline__ void stage_row32(uint8_t* line, int lane, int h, cons
   }
 }
 
+// One product, by the CTA `block` of `blocks` that work at it.
 template <int FORM, int BN, int CG>
-__global__ void __launch_bounds__(kThreads, 1)
-    gg_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
-            const __grid_constant__ CUtensorMap map_part, const Params p) {
+__device__ __forceinline__ void gg_body(const CUtensorMap& map_w, const CUtensorMap& map_a,
+                                        const CUtensorMap& map_part, const Params& p, uint32_t block,
+                                        uint32_t blocks) {
   using C = Cfg<FORM, BN, CG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = tid >> 5;
   const int lane = tid & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;  // 0 issues the pair's MMAs
-  const uint32_t worker = blockIdx.x / CG, workers = gridDim.x / CG;
+  const uint32_t worker = block / CG, workers = blocks / CG;
 
   if (tid == 0) {
     tma_prefetch_desc(&map_w);
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // offsets that fall or leave [0, R]: nothing is computed
   const bool bad = __syncthreads_or(!fine);
-  if (bad && tid == 0 && blockIdx.x == 0) mq::flag(p.status, MQ_DEV_BAD_OFFSETS);
+  if (bad && tid == 0 && block == 0) mq::flag(p.status, MQ_DEV_BAD_OFFSETS);
   if (FORM != GG_ROWS && warp == 0) {
     int run = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t tail_last = 0, tail_parity = 0;  // by slot: its last load was a tail; tails so far, mod 2
     bool ok = true;
     for (uint32_t u = 0; u < units && ok; ++u) {
-      const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u);
+      const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u, worker, workers);
       int s0, s1;
       stages_of<FORM>(p, w, s0, s1);
       const int cols = columns<FORM, BN, CG>(p, w);
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, done = 0;
     bool ok = true;
     for (uint32_t u = 0; u < units && ok; ++u) {
-      const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u);
+      const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u, worker, workers);
       int s0, s1;
       stages_of<FORM>(p, w, s0, s1);
       if (s0 == s1) continue;  // no rows: the epilogue stores zeros
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, parity = 0;  // by slot: tails so far, mod 2
     bool ok = true;
     for (uint32_t u = 0; u < units && ok; ++u) {
-      const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u);
+      const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u, worker, workers);
       int s0, s1;
       stages_of<FORM>(p, w, s0, s1);
       it += s1 - s0;
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.zero_outside && p.offsets && !bad) {
       const int64_t lo = p.offsets[0], hi = p.offsets[p.E];
       const int64_t outside = lo + p.R - hi;
-      for (int64_t i = blockIdx.x; i < outside; i += gridDim.x) {
+      for (int64_t i = block; i < outside; i += blocks) {
         const int64_t r = i < lo ? i : hi + i - lo;
         for (int m = lane; m < p.M; m += 32) store_out(p.out, p.out_dtype, r * p.M + m, 0.0f);
       }
@@ -493,9 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3;         // the tensor-memory lanes this warp may read
     const int half = (warp - 4) >> 2;  // which 16-column steps it takes
     uint32_t done = 0;
+    int turn = 0;  // of the warp's buffers
     bool ok = true;
     for (uint32_t u = 0; u < units && ok; ++u) {
-      const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u);
+      const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u, worker, workers);
       const int m = w.m + (int)rank * kTileM + quad * 32 + lane;  // this lane's output
       const int dtype = p.splits > 1 ? MQ_DTYPE_F32 : p.out_dtype;
       const bool empty = FORM == GG_ROWS && w.n == 0;
@@ -514,12 +517,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c1 = min(n, (half + 1) * (BN / 2));
         const bool f32 = dtype == MQ_DTYPE_F32;
         const int step = f32 ? 32 : 64;
-        uint8_t* chunk = chunks_out + (warp - 4) * kChunkBytes;
         if (m - lane < p.M) {
           for (int c0 = half * (BN / 2); c0 < c1; c0 += step) {
             uint32_t v[32];
+            uint8_t* chunk = chunks_out + ((warp - 4) * kChunks + turn) * kChunkBytes;
+            turn = (turn + 1) % kChunks;
             if (p.tma_out) {
-              if (lane == 0) bulk_wait_read<0>();  // the buffer's last line
+              if (lane == 0) bulk_wait_read<kChunks - 1>();  // the buffer's last lines
               __syncwarp();
             }
             for (int h = 0; h < step / 32; ++h) {
@@ -585,22 +589,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+template <int FORM, int BN, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+    gg_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+            const __grid_constant__ CUtensorMap map_part, const Params p) {
+  gg_body<FORM, BN, CG>(map_w, map_a, map_part, p, blockIdx.x, gridDim.x);
+}
+
+// Both gradients side by side: the first `rows_blocks` CTAs work at the rows', the others
+// at the weights'.  For gradients that memory bounds: one reads the weights and the other
+// writes as much, and HBM takes both at once at nearly twice the rate of writes alone (a
+// fill runs at 3.84 TB/s, a copy at 6.69).
+template <int FORM>
+__global__ void __launch_bounds__(kThreads, 1)
+    gg_both(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+            const __grid_constant__ CUtensorMap map_part, const __grid_constant__ CUtensorMap map_y,
+            const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_out,
+            const Params rows, const Params weights, uint32_t rows_blocks) {
+  if (blockIdx.x < rows_blocks)
+    gg_body<FORM, 256, 2>(map_w, map_a, map_part, rows, blockIdx.x, rows_blocks);
+  else
+    gg_body<GG_ROWS, 256, 2>(map_y, map_x, map_out, weights, blockIdx.x - rows_blocks,
+                             gridDim.x - rows_blocks);
+}
+
 // ------------------------------------------------------------ host side --
+template <typename K>
+cudaError_t allow_smem(K kern, size_t smem, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = uint64_t(1) << (dev & 63);  // devices whose attribute is set
+  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return err;
+}
+
 template <int FORM, int BN, int CG>
 cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const CUtensorMap& mr,
                        const Params& p, int64_t units, cudaStream_t st) {
   constexpr size_t smem = Cfg<FORM, BN, CG>::kSmem;
   auto kern = gg_gemm<FORM, BN, CG>;
-  static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t err = allow_smem(kern, smem, ready);
   if (err != cudaSuccess) return err;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err != cudaSuccess) return err;
-    ready.fetch_or(bit, std::memory_order_relaxed);
-  }
   const int sms = tc_num_sms();
   const int workers = (int)std::max<int64_t>(1, std::min<int64_t>(units, sms / CG));
   return launch_pdl_cluster(kern, dim3(workers * CG), dim3(kThreads), CG, smem, st, mw, ma, mr, p);
@@ -648,11 +681,20 @@ GgPlan gg_plan(GgForm form, int64_t R, int E, int M, int N, int K) {
   return pl;
 }
 
-cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
+namespace {
+
+// A product's tensor maps, parameters and (at most) units.
+struct Prepared {
+  CUtensorMap mw, ma, mr;
+  Params p;
+  int64_t units;
+};
+
+cudaError_t prepare(const GgGemm& g, const GgPlan& pl, Prepared& out) {
   const CUtensorMapDataType dt = g.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const int cg = pl.pair ? 2 : 1;
   bool tma_out = false;
-  CUtensorMap mw, ma, mr;
+  CUtensorMap &mw = out.mw, &ma = out.ma, &mr = out.mr;
   cudaError_t err;
   const cuuint64_t ws = 2 * (cuuint64_t)g.w_stride, as = 2 * (cuuint64_t)g.a_stride;
   const cuuint32_t block[3] = {64, 64, 1};
@@ -663,9 +705,9 @@ cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
     if (err == cudaSuccess) err = make_map(&ma, dt, 2, g.a, ad, &as, block);
     mr = ma;
     const bool f32 = pl.splits > 1 || g.out_dtype == MQ_DTYPE_F32;
-    const void* out = pl.splits > 1 ? g.part : g.out;
+    const void* result = pl.splits > 1 ? g.part : g.out;
     const cuuint64_t row = (cuuint64_t)g.N * (f32 ? 4 : 2);
-    tma_out = row % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && row * g.M < cuuint64_t(1) << 40;
+    tma_out = row % 16 == 0 && (reinterpret_cast<uintptr_t>(result) & 15u) == 0 && row * g.M < cuuint64_t(1) << 40;
     if (err == cudaSuccess && tma_out) {
       const cuuint64_t od[3] = {(cuuint64_t)g.N, (cuuint64_t)g.M, (cuuint64_t)g.E * pl.splits};
       const cuuint64_t os[2] = {row, row * g.M};
@@ -673,7 +715,7 @@ cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
       const CUtensorMapDataType ot = f32                               ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                      : g.out_dtype == MQ_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-      err = make_map(&mr, ot, 3, out, od, os, ob);
+      err = make_map(&mr, ot, 3, result, od, os, ob);
     }
   } else {
     const bool by_k = g.form == GG_W_K;
@@ -687,7 +729,8 @@ cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
     if (err == cudaSuccess) err = make_map(&mr, dt, 2, g.a, ad, &as, pbox);
   }
   if (err != cudaSuccess) return err;
-  Params p = {};
+  Params& p = out.p;
+  p = {};
   p.offsets = g.offsets;
   p.E = g.E;
   p.M = g.M;
@@ -707,10 +750,55 @@ cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
   p.status = g.status;
   p.tma_out = tma_out;
   const int64_t live = std::min<int64_t>(g.R, g.E);
-  const int64_t units = (g.form == GG_ROWS ? (int64_t)g.E * p.ntiles : live + g.R / pl.bn) * p.mtiles * p.splits;
+  out.units = (g.form == GG_ROWS ? (int64_t)g.E * p.ntiles : live + g.R / pl.bn) * p.mtiles * p.splits;
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
+  Prepared q;
+  const cudaError_t err = prepare(g, pl, q);
+  if (err != cudaSuccess) return err;
   switch (g.form) {
-    case GG_W_K: return launch_form<GG_W_K>(pl, mw, ma, mr, p, units, st);
-    case GG_W_M: return launch_form<GG_W_M>(pl, mw, ma, mr, p, units, st);
-    default: return launch_form<GG_ROWS>(pl, mw, ma, mr, p, units, st);
+    case GG_W_K: return launch_form<GG_W_K>(pl, q.mw, q.ma, q.mr, q.p, q.units, st);
+    case GG_W_M: return launch_form<GG_W_M>(pl, q.mw, q.ma, q.mr, q.p, q.units, st);
+    default: return launch_form<GG_ROWS>(pl, q.mw, q.ma, q.mr, q.p, q.units, st);
   }
+}
+
+// Side by side where memory bounds both and neither is split: the weights read and
+// written at 6.6 and 3.8 TB/s, against the products at 1.5 PFLOP/s.
+bool gg_side_by_side(const GgGemm& rows, const GgGemm& weights) {
+  const int64_t n = (int64_t)rows.M * rows.K;
+  const double live = (double)std::min<int64_t>(rows.R, rows.E);
+  const double read = live * n * 2 / 6.6e6;
+  const double write = (double)rows.E * n * (weights.out_dtype == MQ_DTYPE_F32 ? 4 : 2) / 3.8e6;
+  const double flops = 4.0 * rows.R * n / 1.5e9;
+  return rows.M > 128 && rows.K > 128 && read + write > 2 * flops &&
+         gg_plan(rows.form, rows.R, rows.E, rows.M, rows.N, rows.K).splits == 1 &&
+         gg_plan(GG_ROWS, weights.R, weights.E, weights.M, weights.N, weights.K).splits == 1;
+}
+
+cudaError_t launch_gg_both(const GgGemm& rows, const GgGemm& weights, cudaStream_t st) {
+  const GgPlan pair = {256, true, 1};
+  Prepared r, w;
+  cudaError_t err = prepare(rows, pair, r);
+  if (err == cudaSuccess) err = prepare(weights, pair, w);
+  if (err != cudaSuccess) return err;
+  // SMs by the time that either would take by itself
+  const double read = (double)std::min<int64_t>(rows.R, rows.E) * 2 / 6.6;
+  const double write = (double)rows.E * (weights.out_dtype == MQ_DTYPE_F32 ? 4 : 2) / 3.8;
+  const int pairs = tc_num_sms() / 2;
+  int first = (int)(pairs * std::min(0.6, std::max(0.25, read / (read + write))));
+  first = (int)std::max<int64_t>(1, std::min<int64_t>(first, r.units));
+  const int second = (int)std::max<int64_t>(1, std::min<int64_t>(pairs - first, w.units));
+  constexpr size_t smem = std::max({Cfg<GG_W_K, 256, 2>::kSmem, Cfg<GG_ROWS, 256, 2>::kSmem});
+  const bool by_k = rows.form == GG_W_K;
+  const auto kern = by_k ? gg_both<GG_W_K> : gg_both<GG_W_M>;
+  static std::atomic<uint64_t> ready[2];
+  err = allow_smem(kern, smem, ready[by_k]);
+  if (err != cudaSuccess) return err;
+  return launch_pdl_cluster(kern, dim3(2 * (first + second)), dim3(kThreads), 2, smem, st, r.mw, r.ma, r.mr, w.mw,
+                            w.ma, w.mr, r.p, w.p, (uint32_t)(2 * first));
 }
