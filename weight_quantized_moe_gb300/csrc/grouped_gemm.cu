@@ -49,8 +49,7 @@ constexpr int kGroup = 8;       // M tiles that a walk over the columns shares
 constexpr int kPartRows = 16;   // rows of the boxes that load a partly filled chunk
 constexpr size_t kSmemMax = 227 * 1024;
 
-constexpr int kChunkBytes = 32 * 128;  // an epilogue warp's 32 lanes by 128 bytes of columns
-constexpr int kChunks = 2;             // of each warp
+constexpr int kChunkBytes = 32 * 64;  // an epilogue warp's 32 lanes by 64 bytes of columns
 
 template <int FORM, int BN, int CG>
 struct Cfg {
@@ -58,7 +57,7 @@ struct Cfg {
   static constexpr int kStageBytes = kABytes + kBRows * 128;
   static constexpr int kBufs = 2;
   static_assert(kBufs * BN <= 512, "tensor memory");
-  static constexpr size_t kOutBytes = FORM == GG_ROWS ? kEpiWarps * kChunks * kChunkBytes : 0;
+  static constexpr size_t kOutBytes = FORM == GG_ROWS ? kEpiWarps * kChunkBytes : 0;
   static constexpr size_t kFixed = 1024 + kOutBytes + 1024 + kUnitList * 16 + (kMaxE + 1) * 4;
   static constexpr int kFit = (int)((kSmemMax - kFixed) / kStageBytes);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
@@ -218,21 +217,13 @@ __device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi, bool bf16) {
   return *reinterpret_cast<const uint32_t*>(&t);
 }
 
-// 32 columns of one lane's row of the result, into its line of the warp's buffer: all of
-// it (float32), or half h of it (16 bits).
-template <bool F32>
-__device__ __forceinline__ void stage_row32(uint8_t* line, int lane, int h, const uint32_t (&v)[32], bool bf16) {
+// 64 bytes of one lane's row of the result (16 float32 or 32 16-bit columns), into its
+// line of the warp's buffer.
+__device__ __forceinline__ void stage_line(uint8_t* chunk, int lane, const uint32_t (&w)[16]) {
 #pragma unroll
-  for (int j = 0; j < (F32 ? 8 : 4); ++j) {
-    uint4 q;
-    if constexpr (F32) {
-      q = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    } else {
-      q = make_uint4(pack2(v[8 * j], v[8 * j + 1], bf16), pack2(v[8 * j + 2], v[8 * j + 3], bf16),
-                     pack2(v[8 * j + 4], v[8 * j + 5], bf16), pack2(v[8 * j + 6], v[8 * j + 7], bf16));
-    }
-    *reinterpret_cast<uint4*>(line + (((h * 4 + j) ^ (lane & 7)) << 4)) = q;
-  }
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(chunk + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
 // One product, by the CTA `block` of `blocks` that work at it.
@@ -495,7 +486,6 @@ __device__ __forceinline__ void gg_body(const CUtensorMap& map_w, const CUtensor
     const int quad = warp & 3;         // the tensor-memory lanes this warp may read
     const int half = (warp - 4) >> 2;  // which 16-column steps it takes
     uint32_t done = 0;
-    int turn = 0;  // of the warp's buffers
     bool ok = true;
     for (uint32_t u = 0; u < units && ok; ++u) {
       const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u, worker, workers);
@@ -511,46 +501,51 @@ __device__ __forceinline__ void gg_body(const CUtensorMap& map_w, const CUtensor
       }
       const uint32_t acc = tmem + buf * BN + ((uint32_t)(quad * 32) << 16);
       if constexpr (FORM == GG_ROWS) {
-        // A lane is a row of the result: lines of 128 bytes of it go to shared memory
-        // (swizzled) and from there by TMA, which leaves out what lies outside.
+        // A lane is a row of the result: 64 bytes of it at a time go to shared memory
+        // (swizzled) and from there by TMA, which leaves out what lies outside.  (Longer
+        // lines would take a stage's place.)
         const int n = min(BN, p.N - w.col0);
         const int c1 = min(n, (half + 1) * (BN / 2));
         const bool f32 = dtype == MQ_DTYPE_F32;
-        const int step = f32 ? 32 : 64;
+        uint8_t* chunk = chunks_out + (warp - 4) * kChunkBytes;
         if (m - lane < p.M) {
-          for (int c0 = half * (BN / 2); c0 < c1; c0 += step) {
+          for (int c0 = half * (BN / 2); c0 < c1; c0 += 32) {
             uint32_t v[32];
-            uint8_t* chunk = chunks_out + ((warp - 4) * kChunks + turn) * kChunkBytes;
-            turn = (turn + 1) % kChunks;
-            if (p.tma_out) {
-              if (lane == 0) bulk_wait_read<kChunks - 1>();  // the buffer's last lines
-              __syncwarp();
-            }
-            for (int h = 0; h < step / 32; ++h) {
-              if (empty) {
+            if (empty) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0;
-              } else {
-                tmem_ld32_sync(acc + c0 + h * 32, v);
-              }
-              if (p.tma_out) {
-                if (f32) stage_row32<true>(chunk + lane * 128, lane, 0, v, false);
-                else stage_row32<false>(chunk + lane * 128, lane, h, v, dtype == MQ_DTYPE_BF16);
-              } else if (m < p.M) {
-                void* out = p.splits > 1 ? p.part + (int64_t)w.split * p.E * p.M * p.N : p.out;
-                const int64_t at = ((int64_t)w.e * p.M + m) * p.N + w.col0 + c0 + h * 32;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (c0 + h * 32 + i < n) store_out(out, dtype, at + i, __uint_as_float(v[i]));
-              }
+              for (int i = 0; i < 32; ++i) v[i] = 0;
+            } else {
+              tmem_ld32_sync(acc + c0, v);
             }
             if (p.tma_out) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                tma_store_3d(&map_part, chunk, w.col0 + c0, m - lane, w.split * p.E + w.e);
-                bulk_commit();
+              uint32_t line[16];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (f32) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) line[i] = v[16 * h + i];
+                } else {
+                  if (h) break;
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) line[i] = pack2(v[2 * i], v[2 * i + 1], dtype == MQ_DTYPE_BF16);
+                }
+                if (lane == 0) bulk_wait_read<0>();  // what was there has been read
+                __syncwarp();
+                stage_line(chunk, lane, line);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  tma_store_3d(&map_part, chunk, w.col0 + c0 + 16 * h, m - lane, w.split * p.E + w.e);
+                  bulk_commit();
+                }
+                if (f32 && c0 + 16 >= c1) break;
               }
+            } else if (m < p.M) {
+              void* out = p.splits > 1 ? p.part + (int64_t)w.split * p.E * p.M * p.N : p.out;
+              const int64_t at = ((int64_t)w.e * p.M + m) * p.N + w.col0 + c0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c0 + i < n) store_out(out, dtype, at + i, __uint_as_float(v[i]));
             }
           }
         }
@@ -573,7 +568,10 @@ __device__ __forceinline__ void gg_body(const CUtensorMap& map_w, const CUtensor
       if (!empty) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive<CG>(&ctl->acc_empty[buf]);
+        if (lane == 0) {
+          if (CG == 2) mbar_arrive_tmem_free(map_rank(&ctl->acc_empty[buf], 0));
+          else mbar_arrive(&ctl->acc_empty[buf]);
+        }
       }
     }
   }
@@ -711,11 +709,11 @@ cudaError_t prepare(const GgGemm& g, const GgPlan& pl, Prepared& out) {
     if (err == cudaSuccess && tma_out) {
       const cuuint64_t od[3] = {(cuuint64_t)g.N, (cuuint64_t)g.M, (cuuint64_t)g.E * pl.splits};
       const cuuint64_t os[2] = {row, row * g.M};
-      const cuuint32_t ob[3] = {f32 ? 32u : 64u, 32, 1};
+      const cuuint32_t ob[3] = {f32 ? 16u : 32u, 32, 1};
       const CUtensorMapDataType ot = f32                               ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                      : g.out_dtype == MQ_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-      err = make_map(&mr, ot, 3, result, od, os, ob);
+      err = make_map(&mr, ot, 3, result, od, os, ob, CU_TENSOR_MAP_SWIZZLE_64B);
     }
   } else {
     const bool by_k = g.form == GG_W_K;
@@ -786,11 +784,13 @@ cudaError_t launch_gg_both(const GgGemm& rows, const GgGemm& weights, cudaStream
   cudaError_t err = prepare(rows, pair, r);
   if (err == cudaSuccess) err = prepare(weights, pair, w);
   if (err != cudaSuccess) return err;
-  // SMs by the time that either would take by itself
-  const double read = (double)std::min<int64_t>(rows.R, rows.E) * 2 / 6.6;
-  const double write = (double)rows.E * (weights.out_dtype == MQ_DTYPE_F32 ? 4 : 2) / 3.8;
+  // SMs by what a pair of them reads and writes (102 and 85 GB/s measured), within the
+  // shares that were tried (4096 rows, 128 experts, 1536 x 2048: 309, 274 and 296 us with
+  // 35, 45 and 55 %; 517 rows, 16 experts, float32: 53.9, 52.3 and 56.5)
+  const double read = (double)std::min<int64_t>(rows.R, rows.E) * 2 / 102;
+  const double write = (double)rows.E * (weights.out_dtype == MQ_DTYPE_F32 ? 4 : 2) / 85;
   const int pairs = tc_num_sms() / 2;
-  int first = (int)(pairs * std::min(0.6, std::max(0.25, read / (read + write))));
+  int first = (int)(pairs * std::min(0.5, std::max(0.4, read / (read + write))));
   first = (int)std::max<int64_t>(1, std::min<int64_t>(first, r.units));
   const int second = (int)std::max<int64_t>(1, std::min<int64_t>(pairs - first, w.units));
   constexpr size_t smem = std::max({Cfg<GG_W_K, 256, 2>::kSmem, Cfg<GG_ROWS, 256, 2>::kSmem});

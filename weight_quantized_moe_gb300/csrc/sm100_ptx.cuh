@@ -173,6 +173,13 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint
                : "memory");
 }
 
+// Arrives on a barrier of either CTA, ordered behind this thread's tensor-memory reads
+// (tcgen05.wait, tc_fence_before) and no memory access of another kind: without the
+// release at cluster scope, which waits for all of them.
+__device__ __forceinline__ void mbar_arrive_tmem_free(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
