@@ -33,7 +33,13 @@ def storage(w, transposed):
 SHAPES = [
     ([1], 0, 0, 64, 128),                       # one row
     ([1], 0, 0, 4096, 256),                     # one row, K split
+    ([20], 0, 0, 4096, 256),
     ([3, 0, 1], 0, 0, 72, 40),                  # an empty expert, K and N that fill no tile
+    ([0, 2, 4, 0, 1], 1, 0, 264, 33 * 8),       # eight rows: the most that take no tensor cores
+    ([8], 0, 0, 8200, 24),
+    ([0, 1, 3], 2, 2, 2056, 40),
+    ([40] * 24, 1, 2, 136, 264),                # both gradients in one launch
+    ([0, 130, 7, 0, 33, 64], 0, 0, 520, 392),
     ([0, 5, 0, 16, 17], 2, 3, 200, 136),        # rows of no expert on both sides
     ([31, 32, 33], 0, 1, 64, 264),
     ([63, 64, 65, 0], 5, 0, 136, 128),
@@ -179,6 +185,21 @@ def test_no_rows(mq):
     da, dw = mq.moe_grouped_product_grad(torch.empty(0, 64, dtype=F16, device="cuda"), a, w, off)
     assert da.shape == (0, 72) and (dw == 0).all() and dw.shape == w.shape
     clean(mq)
+
+
+def test_gradients_alone_and_together(mq):
+    """Each gradient by itself has the bits that both together have, where they run side
+    by side (many experts, few rows) and where they do not."""
+    for counts, K, N in (([40] * 24, 136, 264), ([900, 300], 256, 392), ([5, 3], 64, 64)):
+        off = gh.offsets_of(counts).cuda()
+        a, dy = gh.randn(sum(counts), K, seed=1, dtype=BF16).cuda(), gh.randn(sum(counts), N, seed=2, dtype=BF16).cuda()
+        w = gh.randn(len(counts), N, K, seed=3, dtype=BF16).cuda()
+        da, dw = mq.moe_grouped_product_grad(dy, a, w, off)
+        da1, none = mq.moe_grouped_product_grad(dy, a, w, off, need_w=False)
+        assert none is None and torch.equal(da, da1)
+        none, dw1 = mq.moe_grouped_product_grad(dy, a, w, off, need_a=False)
+        assert none is None and torch.equal(dw, dw1)
+        clean(mq)
 
 
 @pytest.mark.parametrize("counts,K,N", [([1], 4096, 512), ([700, 300], 512, 512), ([3, 1, 0, 2], 2048, 136)])

@@ -970,12 +970,13 @@ static size_t gg_part_bytes(GgForm form, int64_t R, int E, int M, int N, int K) 
 
 MQ_EXPORT size_t moe_grouped_product_workspace(int64_t R, int K, int N, int E) {
   if (!gg_sizes_ok(R, K, N, E) || R == 0) return 0;
-  return gg_part_bytes(GG_W_K, R, E, N, 0, K);
+  return std::max(gg_part_bytes(GG_W_K, R, E, N, 0, K), gg_part_bytes(GG_W_M, R, E, N, 0, K));
 }
 
 MQ_EXPORT size_t moe_grouped_product_grad_workspace(int64_t R, int K, int N, int E) {
   if (!gg_sizes_ok(R, K, N, E) || R == 0) return 0;
-  return std::max({gg_part_bytes(GG_W_K, R, E, K, 0, N), gg_part_bytes(GG_ROWS, R, E, N, K, 0),
+  return std::max({gg_part_bytes(GG_W_K, R, E, K, 0, N), gg_part_bytes(GG_W_M, R, E, K, 0, N),
+                   gg_part_bytes(GG_ROWS, R, E, N, K, 0),
                    gg_part_bytes(GG_ROWS, R, E, K, N, 0)});
 }
 

@@ -31,13 +31,16 @@ struct GgGemm {
   float* part;            // float32 partial sums [split] of out's shape, where split
   unsigned* status;
 };
+constexpr int kFewRows = 16;  // rows at most of the product that takes one launch (GG_W_K)
 struct GgPlan {
+  bool few;    // at most kFewRows rows: one launch of gg_few
   int bn;      // columns per tile: rows of A, or GG_ROWS columns of the result
   bool pair;   // CTA pairs (cta_group::2), else single CTAs
   int splits;  // splits of the contraction
 };
 MQ_HIDDEN GgPlan gg_plan(GgForm form, int64_t R, int E, int M, int N, int K);
 MQ_HIDDEN cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st);
+MQ_HIDDEN cudaError_t launch_gg_few(const GgGemm& g, cudaStream_t st);
 // Both gradients of a product in one launch, and whether that is the better way.
 MQ_HIDDEN bool gg_side_by_side(const GgGemm& rows, const GgGemm& weights);
 MQ_HIDDEN cudaError_t launch_gg_both(const GgGemm& rows, const GgGemm& weights, cudaStream_t st);

@@ -654,8 +654,14 @@ cudaError_t launch_form(const GgPlan& pl, const CUtensorMap& mw, const CUtensorM
 }  // namespace
 
 GgPlan gg_plan(GgForm form, int64_t R, int E, int M, int N, int K) {
-  GgPlan pl;
+  GgPlan pl = {};
   pl.splits = 1;
+  // Few rows and weights: one launch (grouped_few.cu).  us there and here, K x N and rows:
+  // 4096 x 4096 1 7.7 10.4, 8 8.0 10.4, 16 9.8 11.3; 2048 x 1536 1 3.5 7.2, 16 4.3 8.9;
+  // 4096 x 14336 (117 MB) 1 21.9 21.8, 8 27.2 21.8, 16 33.9 22.0.
+  pl.few = form == GG_W_K && R <= kFewRows &&
+           2.0 * std::min<int64_t>(R, E) * M * K <= 64e6;
+  if (pl.few) return pl;
   const int sms = tc_num_sms();
   if (form == GG_ROWS) {
     pl.pair = M > 128 && N > 128;
@@ -755,6 +761,7 @@ cudaError_t prepare(const GgGemm& g, const GgPlan& pl, Prepared& out) {
 }  // namespace
 
 cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
+  if (pl.few) return launch_gg_few(g, st);
   Prepared q;
   const cudaError_t err = prepare(g, pl, q);
   if (err != cudaSuccess) return err;
@@ -779,7 +786,7 @@ bool gg_side_by_side(const GgGemm& rows, const GgGemm& weights) {
 }
 
 cudaError_t launch_gg_both(const GgGemm& rows, const GgGemm& weights, cudaStream_t st) {
-  const GgPlan pair = {256, true, 1};
+  const GgPlan pair = {false, 256, true, 1};
   Prepared r, w;
   cudaError_t err = prepare(rows, pair, r);
   if (err == cudaSuccess) err = prepare(weights, pair, w);
