@@ -310,3 +310,26 @@ def test_gradients_are_refused(mq):
     with torch.no_grad():
         c.call(mq)
     clean(mq)
+
+
+@pytest.mark.parametrize("r", [16, 32, 64, 128])
+def test_many_calls_in_a_queue(mq, r):
+    """Thousands of calls without a wait between them, on inputs in turn: tiles with two
+    and more groups, whose loads come in any order.  (Two warps consume them: each has to
+    have slots of its own.)"""
+    R, K, N = 1100, 512, 1024
+    cases = [Case(R, K, N, r, 6, runs(40), seed=s) for s in (1, 2, 3)]
+    dev = [tuple(t.cuda() for t in (c.x, c.a[:, 0].contiguous(), c.b[:, 0].contiguous(), c.ids, c.base, c.scaling))
+           for c in cases]
+
+    def call(i):
+        x, a, b, ids, base, s = dev[i % 3]
+        return mq.moe_lora_product(x, a, b, ids, base=base, scaling=s)
+    first = [call(i) for i in range(3)]
+    for c, got in zip(cases, first):
+        c.check(got)
+    for rounds in range(3):
+        last = [call(i) for i in range(999)][-3:]
+        clean(mq)
+        for got, want in zip(last, first):
+            assert torch.equal(got, want)

@@ -240,8 +240,9 @@ static_assert(sizeof(TileTable) % 16 == 0, "copied in steps of 16 bytes");
 
 // Fills in the table of tile `tile`, with all threads of the CTA (at least kTile);
 // `offsets` is a copy of the experts' in shared memory (null: one expert).
+// `id`: thread t's row's adapter (any value behind the last row).
 __device__ __forceinline__ void build_table(Table& tb, const LoraArgs& p, const int* offsets, bool bad,
-                                            int tile) {
+                                            int tile, int id) {
   const int t = threadIdx.x;
   const int64_t row0 = (int64_t)tile * kTile;
   const int rows = (int)min((int64_t)kTile, p.R - row0);
@@ -249,7 +250,7 @@ __device__ __forceinline__ void build_table(Table& tb, const LoraArgs& p, const 
   if (t < kTile) {
     if (t < rows && !bad) {
       const int64_t row = row0 + t;
-      const int l = p.ids[row];
+      const int l = id;
       int e = 0;
       bool in = true;
       if (offsets) {
@@ -468,6 +469,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   const int s0 = (int)((int64_t)nst * split / d.splits), s1 = (int)((int64_t)nst * (split + 1) / d.splits);
   mq::pdl_wait();
   mq::pdl_trigger();
+  const int id = tid < kTile && row0 + tid < p.R ? p.ids[row0 + tid] : -1;
   const bool bad = copy_offsets(p, sh->offsets);
   // the first stages of x are on their way while the groups are worked out
   const int early = min(kXSlots, s1 - s0);
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
       tma_load_2d(xs + i * kSlot, &map_x, &ctl->x_full[i], (s0 + i) * 64, (int)row0);
     }
   __syncwarp();
-  build_table(sh->table, p, p.offsets ? sh->offsets : nullptr, bad, tile);
+  build_table(sh->table, p, p.offsets ? sh->offsets : nullptr, bad, tile, id);
   const Table& tb = sh->table;
   tc_fence_before();
   __syncthreads();
@@ -486,6 +488,13 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   const int per = kTile / d.rp;                      // groups of an accumulator
   const int accs = (tb.groups + per - 1) / per;      // accumulators of the tile
   const int mine = accs > mpart ? (accs - mpart + d.mparts - 1) / d.mparts : 0;
+  // the scaling of this thread's (first) row of the last step, which is short
+  const int row_share = kTile / d.splits, sub = tid & 7;
+  auto scaling_of = [&](int i) {
+    const int key = tb.key[split * row_share + i];
+    return p.scaling && key >= 0 ? p.scaling[key / p.E] : 1.0f;
+  };
+  const float first_scaling = (tid >> 3) < row_share ? scaling_of(tid >> 3) : 1.0f;
 
   if (warp == 0) {
     const bool el = elect_one();
@@ -596,11 +605,10 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
   // The sum over the splits, in their order, of this CTA's share of the rows; eight
   // lanes per row, four ranks a lane and turn.
-  const int share = kTile / d.splits, sub = tid & 7;
-  for (int i = tid >> 3; i < share; i += kDownThreads / 8) {
-    const int t = split * share + i, g = tb.slot[t];
+  for (int i = tid >> 3; i < row_share; i += kDownThreads / 8) {
+    const int t = split * row_share + i, g = tb.slot[t];
     const bool live = g < kOut && g / per % d.mparts == mpart;
-    const float s = live && p.scaling ? p.scaling[tb.key[t] / p.E] : 1.0f;
+    const float s = i < kDownThreads / 8 ? first_scaling : scaling_of(i);
     float4 v[4];
     float most = 0;
 #pragma unroll
@@ -660,13 +668,13 @@ constexpr int kUpMma = 2;
 constexpr int kUpThreads = 128 + 32 * kUpEpi + 32;
 constexpr int kMaxUpSlots = 24;
 constexpr int kIoBytes = kTile * kTile * 2;
-constexpr int kMaxIo = 4;
+constexpr int kMaxIo = 3;
 
 struct UpCtl {
   uint64_t full[kMaxUpSlots], empty[kMaxUpSlots];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t io_full[kMaxIo], io_done[kMaxIo], io_empty[kMaxIo];
-  uint64_t tile_full, tile_empty;
+  uint64_t tile_full, go;
   uint64_t drain;
   uint32_t tmem;
   volatile int abort_flag;
@@ -680,7 +688,7 @@ struct UpShape {
   int rp;      // r rounded up to 16, 32, 64 or 128
   int gparts;  // parts of a tile's rounds
   int ntiles;  // of 128 outputs
-  int units;   // (tile, part, 128 outputs)
+  int shares;  // CTAs of a tile, among which its (part, 128 outputs) are divided
   int nio;     // buffers of base and out; 0: read and written element by element
   int line;    // bytes of a slot's lines: min(64, rp) ranks
   int slots;   // of 128 outputs by up to 64 ranks of a group
@@ -768,7 +776,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
       mbar_init(&ctl->io_empty[i], 1);
     }
     mbar_init(&ctl->tile_full, 1);
-    mbar_init(&ctl->tile_empty, kUpMma + 1 + kUpEpi);
+    mbar_init(&ctl->go, 1);
     mbar_init(&ctl->drain, kUpMma);
     ctl->abort_flag = 0;
     fence_mbar_init();
@@ -787,109 +795,111 @@ __global__ void __launch_bounds__(kUpThreads, 1)
   const int ksteps = (p.r + 15) / 16;
   const bool add = p.base != nullptr;
 
-  // This CTA's units, one tile of rows after another.
-  const int u0 = (int)((int64_t)u.units * blockIdx.x / gridDim.x);
-  const int u1 = (int)((int64_t)u.units * (blockIdx.x + 1) / gridDim.x);
+  // This CTA's units: a share of one tile's.
   const int per_tile = u.ntiles * u.gparts;
-  // Tiles with nothing to write are passed over (by every role).
-  auto idle = [&](const TileTable& t) { return t.inside == 0 || (t.groups == 0 && p.base == p.out); };
-  // The walk over this CTA's units that every role makes: on_tile(tile) as it comes to a
-  // tile, on_unit(n0, part) for each unit of it, end_tile() behind them.  Each returns
-  // whether to go on.
-  auto walk = [&](auto on_tile, auto on_unit, auto end_tile) {
-    for (int un = u0; un < u1;) {
-      const int tile = un / per_tile;
-      const int end = min(u1, (tile + 1) * per_tile);
-      if (idle(u.tables[tile])) {
-        un = end;
-        continue;
+  const int tile = blockIdx.x / u.shares, share = blockIdx.x % u.shares;
+  const int u0 = (int)((int64_t)per_tile * share / u.shares), u1 = (int)((int64_t)per_tile * (share + 1) / u.shares);
+  const int row0 = tile * kTile;
+  const TileTable* const table = u.tables + tile;
+  // nothing to write: no rows, or no groups and base in place
+  const bool idle = table->inside == 0 || (table->groups == 0 && p.base == p.out);
+  // Every role's walk over the units: on_unit(n0, part) returns whether to go on.
+  auto walk = [&](auto on_unit) {
+    if (idle) return;
+    int part = u0 / u.ntiles, nt = u0 - part * u.ntiles;
+    for (int un = u0; un < u1; ++un) {
+      if (!on_unit(nt * kTile, part)) return;
+      if (++nt == u.ntiles) {
+        nt = 0;
+        ++part;
       }
-      if (!on_tile(tile)) return;
-      int part = (un - tile * per_tile) / u.ntiles;
-      int nt = un - tile * per_tile - part * u.ntiles;
-      for (; un < end; ++un) {
-        if (!on_unit(nt * kTile, part)) return;
-        if (++nt == u.ntiles) {
-          nt = 0;
-          ++part;
-        }
-      }
-      if (!end_tile()) return;
     }
   };
-  auto first_round = [&](int part) { return u.gparts == 1 ? (part ? tb.rounds : 0) : tb.rounds * part / u.gparts; };
+  auto first_round = [&](const TileTable& t, int part) {
+    return u.gparts == 1 ? (part ? t.rounds : 0) : t.rounds * part / u.gparts;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------- base --
+    // Behind the first groups' loads, which would else wait for all CTAs' buffers.
     const bool el = elect_one();
     Ring io_r;
-    int row0 = 0;
     uint32_t it = 0;
-    if (u.nio)
-      walk([&](int tile) { row0 = tile * kTile; return true; },
-           [&](int n0, int) {
-             const uint32_t s = io_r.slot;
-             if (!warp_wait(&ctl->io_empty[s], io_r.turn ^ 1, ctl, p.status)) return false;
-             if (el) {
-               if (add) {
-                 mbar_arrive_expect_tx(&ctl->io_full[s], kIoBytes);
-                 // (the second half may lie behind the last output: nothing is read there)
-                 tma_load_2d(io + s * kIoBytes, &map_base, &ctl->io_full[s], n0, row0);
-                 tma_load_2d(io + s * kIoBytes + kIoBytes / 2, &map_base, &ctl->io_full[s], n0 + 64, row0);
-               } else {
-                 mbar_arrive(&ctl->io_full[s]);
-               }
-             }
-             io_r.next(u.nio);
-             ++it;
-             return true;
-           },
-           [] { return true; });
+    bool ok = u.nio && (idle || warp_wait(&ctl->go, 0, ctl, p.status));
+    if (ok)
+      walk([&](int n0, int) {
+        const uint32_t s = io_r.slot;
+        if (!warp_wait(&ctl->io_empty[s], io_r.turn ^ 1, ctl, p.status)) return false;
+        if (el) {
+          if (add) {
+            mbar_arrive_expect_tx(&ctl->io_full[s], kIoBytes);
+            // (the second half may lie behind the last output: nothing is read there)
+            tma_load_2d(io + s * kIoBytes, &map_base, &ctl->io_full[s], n0, row0);
+            tma_load_2d(io + s * kIoBytes + kIoBytes / 2, &map_base, &ctl->io_full[s], n0 + 64, row0);
+          } else {
+            mbar_arrive(&ctl->io_full[s]);
+          }
+        }
+        io_r.next(u.nio);
+        ++it;
+        return true;
+      });
     if (ctl->abort_flag)  // loads in flight land before the CTA goes
       for (uint32_t j = it < (uint32_t)u.nio ? 0 : it - u.nio; j < it; ++j)
         wait_drain(&ctl->io_full[j % u.nio], (j / u.nio) & 1);
   } else if (warp == 1) {
-    // ---------------------------------- a tile's table and rows; groups' B --
+    // --------------------------------- the tile's table and rows; groups' B --
+    // (The groups' keys from global memory: sooner than by way of the table's copy.)
     const bool el = elect_one();
+    if (el) {
+      mbar_arrive_expect_tx(&ctl->tile_full, sizeof(TileTable) + hblocks * kSlot);
+      for (int b = 0; b < hblocks; ++b) tma_load_2d(hs + b * kSlot, &map_h, &ctl->tile_full, b * 64, row0);
+      bulk_load(&sh->table, table, sizeof(TileTable), &ctl->tile_full);
+    }
+    int keys[kTile / 32];
+#pragma unroll
+    for (int q = 0; q < kTile / 32; ++q) keys[q] = q * 32 + lane < table->groups ? table->group_key[q * 32 + lane] : 0;
     Ring w;
-    uint32_t it = 0, tiles = 0;
-    walk(
-        [&](int tile) {
-          if (!warp_wait(&ctl->tile_empty, (tiles & 1) ^ 1, ctl, p.status)) return false;
+    uint32_t it = 0;
+    bool gone = false;
+    auto go = [&] {
+      if (el && !gone) mbar_arrive(&ctl->go);
+      gone = true;
+    };
+    walk([&](int n0, int part) {
+      const int g0 = u.gparts == 1 ? 0 : table->round_start[first_round(*table, part)];
+      const int g1 = u.gparts == 1 ? table->groups : table->round_start[first_round(*table, part + 1)];
+      for (int g = g0; g < g1; ++g) {
+        int key = 0;
+#pragma unroll
+        for (int q = 0; q < kTile / 32; ++q) {
+          const int v = __shfl_sync(0xffffffffu, keys[q], g & 31);
+          if (g >> 5 == q) key = v;
+        }
+        for (int k = 0; k < kblocks; ++k) {
+          if (it == (uint32_t)u.slots) go();
+          if (!warp_wait(&ctl->empty[w.slot], w.turn ^ 1, ctl, p.status)) return false;
           if (el) {
-            mbar_arrive_expect_tx(&ctl->tile_full, sizeof(TileTable) + hblocks * kSlot);
-            bulk_load(&sh->table, u.tables + tile, sizeof(TileTable), &ctl->tile_full);
-            for (int b = 0; b < hblocks; ++b)
-              tma_load_2d(hs + b * kSlot, &map_h, &ctl->tile_full, b * 64, tile * kTile);
+            mbar_arrive_expect_tx(&ctl->full[w.slot], kTile * u.line);
+            tma_load_3d(slots + w.slot * kTile * u.line, &map_b, &ctl->full[w.slot], k * 64, n0, key);
           }
-          return warp_wait(&ctl->tile_full, tiles++ & 1, ctl, p.status);
-        },
-        [&](int n0, int part) {
-          const int g1 = tb.round_start[first_round(part + 1)];
-          for (int g = tb.round_start[first_round(part)]; g < g1; ++g) {
-            const int key = tb.group_key[g];
-            for (int k = 0; k < kblocks; ++k) {
-              if (!warp_wait(&ctl->empty[w.slot], w.turn ^ 1, ctl, p.status)) return false;
-              if (el) {
-                mbar_arrive_expect_tx(&ctl->full[w.slot], kTile * u.line);
-                tma_load_3d(slots + w.slot * kTile * u.line, &map_b, &ctl->full[w.slot], k * 64, n0, key);
-              }
-              w.next(u.slots);
-              ++it;
-            }
-          }
-          return true;
-        },
-        [] { return true; });
-    if (ctl->abort_flag) {
+          w.next(u.slots);
+          ++it;
+        }
+      }
+      go();
+      return true;
+    });
+    // loads that nothing else may have waited for land before the CTA goes
+    wait_drain(&ctl->tile_full, 0);
+    if (ctl->abort_flag)
       for (uint32_t j = it < (uint32_t)u.slots ? 0 : it - u.slots; j < it; ++j)
         wait_drain(&ctl->full[j % u.slots], (j / u.slots) & 1);
-      if (tiles) wait_drain(&ctl->tile_full, (tiles - 1) & 1);
-    }
   } else if (warp == 2 || warp == 12) {
     // ----------------------------------------------------------- MMAs --
     // Of the columns only those of a group's range.  Groups are small (their four to
-    // eight instructions take less than the way to them): two warps take them in turn.
+    // eight instructions take less than the way to them): two warps take them in turn,
+    // each with slots of its own.
     const bool second = warp == 12;
     bool odd = false;
     const bool el = elect_one();
@@ -897,11 +907,10 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     const uint32_t hb = smem_addr(hs), sb = smem_addr(slots);
     const uint64_t desc = smem_desc_k(0, u.line);
     Ring w, ar;
-    uint32_t tiles = 0;
-    walk([&](int) { return warp_wait(&ctl->tile_full, tiles++ & 1, ctl, p.status); },
-         [&](int, int part) {
-           const int r1 = first_round(part + 1);
-           for (int rd = first_round(part); rd < r1; ++rd) {
+    if (warp_wait(&ctl->tile_full, 0, ctl, p.status))
+      walk([&](int, int part) {
+           const int r1 = first_round(tb, part + 1);
+           for (int rd = first_round(tb, part); rd < r1; ++rd) {
              if (!warp_wait(&ctl->acc_empty[ar.slot], ar.turn ^ 1, ctl, p.status)) return false;
              tc_fence_after();
              const int g1 = tb.round_start[rd + 1];
@@ -937,10 +946,6 @@ __global__ void __launch_bounds__(kUpThreads, 1)
              ar.next(2);
            }
            return true;
-         },
-         [&] {
-           if (el) mma_commit(&ctl->tile_empty);
-           return true;
          });
     if (el) mma_commit(&ctl->drain);
     wait_drain(&ctl->drain, 0);
@@ -950,26 +955,19 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     // writes.  Apart from the epilogue, so that a buffer is free for the next load as
     // soon as it has been read.
     Ring io_r;
-    uint32_t tiles = 0;
-    int tile = 0;
-    walk(
-        [&](int t) {
-          tile = t;
-          return warp_wait(&ctl->tile_full, tiles++ & 1, ctl, p.status);
-        },
-        [&](int n0, int part) {
-          if (!u.nio) return true;  // (the epilogue stores by itself)
+    if (u.nio && warp_wait(&ctl->tile_full, 0, ctl, p.status))
+      walk([&](int n0, int part) {
           const uint32_t s = io_r.slot;
           if (!warp_wait(&ctl->io_done[s], io_r.turn, ctl, p.status)) return false;
           if (tb.inside == tb.rows && u.gparts == 1) {
             if (lane == 0) {
-              tma_store_2d(&map_out, io + s * kIoBytes, n0, tile * kTile);
-              if (n0 + 64 < p.N) tma_store_2d(&map_out, io + s * kIoBytes + kIoBytes / 2, n0 + 64, tile * kTile);
+              tma_store_2d(&map_out, io + s * kIoBytes, n0, row0);
+              if (n0 + 64 < p.N) tma_store_2d(&map_out, io + s * kIoBytes + kIoBytes / 2, n0 + 64, row0);
               bulk_commit();
               bulk_wait_read<0>();
             }
           } else {
-            const int r0 = first_round(part), r1 = first_round(part + 1);
+            const int r0 = first_round(tb, part), r1 = first_round(tb, part + 1);
             const int live = min(kTile, p.N - n0);  // (a multiple of 8)
             for (int t = 0; t < tb.rows; ++t) {
               const int color = tb.color[t];
@@ -977,17 +975,13 @@ __global__ void __launch_bounds__(kUpThreads, 1)
                                                 : color != kOut && color >> 1 >= r0 && color >> 1 < r1;
               if (!write || lane * 4 >= live) continue;
               const uint2 q = *reinterpret_cast<const uint2*>(io + s * kIoBytes + io_offset(t, lane >> 1) + (lane & 1) * 8);
-              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((int64_t)tile * kTile + t) * p.out_stride +
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((int64_t)row0 + t) * p.out_stride +
                                         n0 + lane * 4) = q;
             }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->io_empty[s]);
           io_r.next(u.nio);
-          return true;
-        },
-        [&] {
-          if (lane == 0) mbar_arrive(&ctl->tile_empty);
           return true;
         });
   } else {
@@ -996,19 +990,13 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     constexpr int kParts = kUpEpi / 4;
     const int quad = warp & 3, sub = (warp - 4) >> 2;  // lanes, and which blocks of 16 rows
     Ring ar, io_r;
-    uint32_t tiles = 0;
-    int64_t row0 = 0;
-    walk(
-        [&](int tile) {
-          row0 = (int64_t)tile * kTile;
-          return warp_wait(&ctl->tile_full, tiles++ & 1, ctl, p.status);
-        },
-        [&](int n0, int part) {
+    if (warp_wait(&ctl->tile_full, 0, ctl, p.status))
+      walk([&](int n0, int part) {
           const int n = n0 + quad * 32 + lane;
           const uint32_t buf = smem_addr(io) + io_r.slot * kIoBytes;
           if (u.nio && !warp_wait(&ctl->io_full[io_r.slot], io_r.turn, ctl, p.status)) return false;
-          const int r1 = first_round(part + 1);
-          for (int rd = first_round(part); rd < r1; ++rd) {
+          const int r1 = first_round(tb, part + 1);
+          for (int rd = first_round(tb, part); rd < r1; ++rd) {
             if (!warp_wait(&ctl->acc_full[ar.slot], ar.turn, ctl, p.status)) return false;
             tc_fence_after();
             const uint32_t acc = tmem + ar.slot * 2 * kTile + ((uint32_t)(quad * 32) << 16);
@@ -1053,8 +1041,8 @@ __global__ void __launch_bounds__(kUpThreads, 1)
                 for (int i = 0; i < 16; ++i) {
                   const int t = c * 16 + i;
                   if (!byte_of(in, i) || n >= p.N) continue;
-                  const float o = add ? load_as(p.base, p.out_dtype, (row0 + t) * p.base_stride + n) : 0.0f;
-                  store_out(p.out, p.out_dtype, (row0 + t) * p.out_stride + n,
+                  const float o = add ? load_as(p.base, p.out_dtype, ((int64_t)row0 + t) * p.base_stride + n) : 0.0f;
+                  store_out(p.out, p.out_dtype, ((int64_t)row0 + t) * p.out_stride + n,
                             fmaf(__uint_as_float(v[i]), tb.row_scale[t], o));
                 }
               }
@@ -1081,18 +1069,15 @@ __global__ void __launch_bounds__(kUpThreads, 1)
           } else if (part == 0 && p.base != p.out) {
             for (int t = sub; t < tb.rows; t += kParts)
               if (tb.color[t] == kNone && n < p.N)
-                copy_element(p.out, (row0 + t) * p.out_stride + n, p.base, (row0 + t) * p.base_stride + n,
+                copy_element(p.out, ((int64_t)row0 + t) * p.out_stride + n, p.base, ((int64_t)row0 + t) * p.base_stride + n,
                              p.out_dtype);
           }
           __syncwarp();
           return true;
-        },
-        [&] {
-          if (lane == 0) mbar_arrive(&ctl->tile_empty);
-          return true;
         });
   }
   tc_fence_before();
+  __syncwarp();  // (the barrier and the deallocation are for whole warps)
   __syncthreads();
   tc_fence_after();
   if (warp == 2) tmem_dealloc(tmem, 512);
@@ -1173,17 +1158,19 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
   u.rp = padded_rank(g.r);
   u.gparts = pl.gparts;
   u.ntiles = (g.N + kTile - 1) / kTile;
-  u.units = (int)y.tiles * u.ntiles * u.gparts;
   u.tables = reinterpret_cast<const TileTable*>(g.workspace);
   // base and out by TMA: 16 bits, rows on 16-byte boundaries
   const bool base_ok = !g.base || (g.base_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(g.base) & 15u) == 0);
   const bool tma = g.out_dtype != MQ_DTYPE_F32 && base_ok && g.out_stride % 8 == 0 && g.N % 8 == 0 &&
                    (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
   // In flight at a time: as many buffers of base, and as many groups, as fit beside the
-  // rows (K = N = 4096, 4099 rows, rank 64: with three buffers instead of four ...).
-  u.nio = !tma ? 0 : u.rp == 64 ? 4 : 3;
+  // rows.  Two warps consume the groups' slots in turn, so a slot has to belong to one of
+  // them for good (a multiple of two groups' slots): a warp that came to a slot of which
+  // the other had the last turn could be a whole turn ahead of its barrier, whose parity
+  // cannot tell that from none.
+  u.nio = !tma ? 0 : u.rp == 128 ? 2 : 3;
   u.line = std::min(u.rp, 64) * 2;
-  u.slots = u.rp >= 64 ? 3 : 98304 / (kTile * u.line);
+  u.slots = u.rp >= 64 ? 4 : 98304 / (kTile * u.line);
   CUtensorMap mb, mh, mbase, mout;
   const cuuint64_t bd[3] = {(cuuint64_t)g.r, (cuuint64_t)g.N, (cuuint64_t)g.L * g.E};
   const cuuint64_t bs[2] = {2 * (cuuint64_t)g.r, 2 * (cuuint64_t)g.r * g.N};
@@ -1209,26 +1196,28 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
     if (err != cudaSuccess) return err;
   }
   const size_t need = 1024 + (2 * u.rp + 63) / 64 * kSlot + (size_t)u.slots * kTile * u.line + (size_t)u.nio * kIoBytes + sizeof(UpShared);
-  static_assert(1024 + 4 * kSlot + 3 * kSlot + 3 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
-                    1024 + 2 * kSlot + 3 * kSlot + 4 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
+  static_assert(1024 + 4 * kSlot + 4 * kSlot + 2 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
+                    1024 + 2 * kSlot + 4 * kSlot + 3 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
                     1024 + kSlot + 98304 + 3 * kIoBytes + sizeof(UpShared) <= kSmemMax,
                 "shared memory");
+  static_assert(98304 / (kTile * 32) <= kMaxUpSlots && 98304 / (kTile * 32) % 2 == 0 &&
+                    98304 / (kTile * 64) % 2 == 0 && 4 % (2 * 2) == 0,
+                "a slot belongs to one of the two MMA warps");
   const size_t smem = std::max<size_t>(need, 120 * 1024);  // one CTA per SM: each allocates all of tensor memory
   static std::atomic<uint64_t> ready[2];
   const bool bf = g.out_dtype == MQ_DTYPE_BF16;
   const auto kern = bf ? lora_up<true> : lora_up<false>;
   err = allow_smem(kern, kSmemMax, ready[bf]);
   if (err != cudaSuccess) return err;
-  // A CTA fetches a tile's table and rows once for each tile that it works at, which
-  // takes about as long as a unit: whole shares of a tile each, where that costs less
-  // than an even share of all units.
-  const int sms = tc_num_sms(), tiles = (int)y.tiles, per_tile = u.ntiles * u.gparts;
-  int grid = std::min(u.units, sms);
-  if (tiles <= sms) {
-    const int shares = std::min(sms / tiles, per_tile);
-    if ((per_tile + shares - 1) / shares + 1 <= (u.units + grid - 1) / grid + 2) grid = tiles * shares;
+  // Shares by estimated time: the way to a CTA's first unit takes about as long as three.
+  const int sms = tc_num_sms(), per_tile = u.ntiles * u.gparts;
+  int64_t best = 0;
+  for (int n = 1; n <= per_tile && n <= 256; ++n) {
+    const int64_t t = (y.tiles * n + sms - 1) / sms * ((per_tile + n - 1) / n + 3);
+    if (best == 0 || t < best) best = t, u.shares = n;
   }
-  return launch_pdl(kern, dim3(grid), dim3(kUpThreads), smem, st, mb, mh, mbase, mout, g, u);
+  const int64_t grid = y.tiles * u.shares;
+  return launch_pdl(kern, dim3((unsigned)grid), dim3(kUpThreads), smem, st, mb, mh, mbase, mout, g, u);
 }
 
 }  // namespace

@@ -68,11 +68,14 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
   else mma_commit(bar);
 }
 
-// After an abort: lets what is in flight land; bounded, ignores the flag.
+// At the end, or after an abort: lets what is in flight land; bounded, ignores the
+// flag.  For whole warps: lanes may see the barrier's phase end at different polls, and
+// what follows (barriers, tensor-memory deallocation) takes the warp together.
 __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
   const unsigned long long t0 = mq::global_timer_ns();
   while (!mbar_try_wait(bar, parity))
-    if (mq::global_timer_ns() - t0 > kWaitNs) return;
+    if (mq::global_timer_ns() - t0 > kWaitNs) break;
+  __syncwarp();
 }
 
 // A role's place in a ring of n slots: which slot, and how often round, mod 2.
