@@ -666,9 +666,10 @@ __global__ void __launch_bounds__(kDownThreads, 1)
 constexpr int kUpEpi = 8;
 constexpr int kUpMma = 2;
 constexpr int kUpThreads = 128 + 32 * kUpEpi + 32;
-constexpr int kMaxUpSlots = 24;
+constexpr int kMaxUpSlots = 16;
 constexpr int kIoBytes = kTile * kTile * 2;
-constexpr int kMaxIo = 3;
+constexpr int kMaxIo = 4;
+constexpr int kGroupBytes = 65536;  // of slots at ranks up to 32
 
 struct UpCtl {
   uint64_t full[kMaxUpSlots], empty[kMaxUpSlots];
@@ -914,7 +915,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
              if (!warp_wait(&ctl->acc_empty[ar.slot], ar.turn ^ 1, ctl, p.status)) return false;
              tc_fence_after();
              const int g1 = tb.round_start[rd + 1];
-             for (int g = tb.round_start[rd]; g < g1; ++g, odd = !odd) {
+             for (int g = tb.round_start[rd]; g < g1; ++g, odd = !odd && kblocks == 1) {
                if (odd != second) {
                  for (int k = 0; k < kblocks; ++k) w.next(u.slots);
                  continue;
@@ -1164,13 +1165,13 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
   const bool tma = g.out_dtype != MQ_DTYPE_F32 && base_ok && g.out_stride % 8 == 0 && g.N % 8 == 0 &&
                    (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
   // In flight at a time: as many buffers of base, and as many groups, as fit beside the
-  // rows.  Two warps consume the groups' slots in turn, so a slot has to belong to one of
-  // them for good (a multiple of two groups' slots): a warp that came to a slot of which
-  // the other had the last turn could be a whole turn ahead of its barrier, whose parity
-  // cannot tell that from none.
-  u.nio = !tma ? 0 : u.rp == 128 ? 2 : 3;
+  // rows.  Two warps consume the groups' slots in turn (one where a group has two slots),
+  // so a slot has to belong to one of them for good, and their number is even: a warp
+  // that came to a slot of which the other had the last turn could be a whole turn ahead
+  // of its barrier, whose parity cannot tell that from none.
+  u.nio = !tma ? 0 : u.rp == 128 ? 3 : 4;
   u.line = std::min(u.rp, 64) * 2;
-  u.slots = u.rp >= 64 ? 4 : 98304 / (kTile * u.line);
+  u.slots = u.rp >= 64 ? 2 : kGroupBytes / (kTile * u.line);
   CUtensorMap mb, mh, mbase, mout;
   const cuuint64_t bd[3] = {(cuuint64_t)g.r, (cuuint64_t)g.N, (cuuint64_t)g.L * g.E};
   const cuuint64_t bs[2] = {2 * (cuuint64_t)g.r, 2 * (cuuint64_t)g.r * g.N};
@@ -1196,12 +1197,12 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
     if (err != cudaSuccess) return err;
   }
   const size_t need = 1024 + (2 * u.rp + 63) / 64 * kSlot + (size_t)u.slots * kTile * u.line + (size_t)u.nio * kIoBytes + sizeof(UpShared);
-  static_assert(1024 + 4 * kSlot + 4 * kSlot + 2 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
-                    1024 + 2 * kSlot + 4 * kSlot + 3 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
-                    1024 + kSlot + 98304 + 3 * kIoBytes + sizeof(UpShared) <= kSmemMax,
+  static_assert(1024 + 4 * kSlot + 2 * kSlot + 3 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
+                    1024 + 2 * kSlot + 2 * kSlot + 4 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
+                    1024 + kSlot + kGroupBytes + 4 * kIoBytes + sizeof(UpShared) <= kSmemMax,
                 "shared memory");
-  static_assert(98304 / (kTile * 32) <= kMaxUpSlots && 98304 / (kTile * 32) % 2 == 0 &&
-                    98304 / (kTile * 64) % 2 == 0 && 4 % (2 * 2) == 0,
+  static_assert(kGroupBytes / (kTile * 32) <= kMaxUpSlots && kGroupBytes / (kTile * 32) % 2 == 0 &&
+                    kGroupBytes / (kTile * 64) % 2 == 0,
                 "a slot belongs to one of the two MMA warps");
   const size_t smem = std::max<size_t>(need, 120 * 1024);  // one CTA per SM: each allocates all of tensor memory
   static std::atomic<uint64_t> ready[2];
