@@ -1138,7 +1138,7 @@ static bool lora_sizes_ok(int64_t R, int K, int N, int r, int L, int E) {
 MQ_EXPORT size_t moe_lora_product_workspace(int64_t R, int K, int N, int r, int L, int E) {
   if (!lora_sizes_ok(R, K, N, r, L, E) || R == 0) return 0;
   const LoraPlan pl = lora_plan(R, K, N, r, L, E);
-  return pl.rows ? 0 : align256(lora_workspace(R, r));
+  return pl.rows ? 0 : align256(lora_workspace(pl, R, r));
 }
 
 // Whether R rows of `len` bytes, `stride` bytes apart, share a byte with R others.

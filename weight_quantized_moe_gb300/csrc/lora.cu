@@ -38,7 +38,7 @@ namespace {
 
 using namespace mq::pipe;
 
-constexpr int kTile = 128;     // rows of a tile
+constexpr int kTile = 128;     // rows of a tile at most; outputs of an accumulator
 constexpr int kSlot = 16384;   // 128 lines of 128 bytes
 constexpr int kMaxE = 1024;
 constexpr size_t kSmemMax = 227 * 1024;
@@ -238,14 +238,12 @@ struct TileTable {
 };
 static_assert(sizeof(TileTable) % 16 == 0, "copied in steps of 16 bytes");
 
-// Fills in the table of tile `tile`, with all threads of the CTA (at least kTile);
+// Fills in the table of the tile of `rows` rows from row0 on, with all threads of the CTA (at least kTile);
 // `offsets` is a copy of the experts' in shared memory (null: one expert).
 // `id`: thread t's row's adapter (any value behind the last row).
 __device__ __forceinline__ void build_table(Table& tb, const LoraArgs& p, const int* offsets, bool bad,
-                                            int tile, int id) {
+                                            int64_t row0, int rows, int id) {
   const int t = threadIdx.x;
-  const int64_t row0 = (int64_t)tile * kTile;
-  const int rows = (int)min((int64_t)kTile, p.R - row0);
   int key = -2;
   if (t < kTile) {
     if (t < rows && !bad) {
@@ -423,11 +421,12 @@ __host__ __device__ constexpr int h_pitch(int rp) { return rp + 4; }
 __host__ __device__ constexpr int h_row(int rp) { return rp < 32 ? 64 : 2 * rp; }
 
 struct DownShape {
+  int height;  // rows of a tile
   int rp;      // r rounded up to 16, 32, 64 or 128
   int splits;  // K splits: CTAs of a cluster
   int mparts;  // clusters among which a tile's accumulators are divided
   TileTable* tables;
-  uint16_t* h;  // [tiles * kTile][h_row(rp)]
+  uint16_t* h;  // [tiles * height][h_row(rp)]
 };
 
 __global__ void __launch_bounds__(kDownThreads, 1)
@@ -464,22 +463,23 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   const int split = blockIdx.x % d.splits;  // the rank in the cluster
   const int mpart = blockIdx.x / d.splits % d.mparts;
   const int tile = blockIdx.x / (d.splits * d.mparts);
-  const int64_t row0 = (int64_t)tile * kTile;
+  const int64_t row0 = (int64_t)tile * d.height;
+  const int rows = (int)min((int64_t)d.height, p.R - row0);
   const int nst = (p.K + 63) / 64;
   const int s0 = (int)((int64_t)nst * split / d.splits), s1 = (int)((int64_t)nst * (split + 1) / d.splits);
   mq::pdl_wait();
   mq::pdl_trigger();
-  const int id = tid < kTile && row0 + tid < p.R ? p.ids[row0 + tid] : -1;
+  const int id = tid < rows ? p.ids[row0 + tid] : -1;
   const bool bad = copy_offsets(p, sh->offsets);
   // the first stages of x are on their way while the groups are worked out
   const int early = min(kXSlots, s1 - s0);
   if (warp == 0 && elect_one())
     for (int i = 0; i < early; ++i) {
-      mbar_arrive_expect_tx(&ctl->x_full[i], kSlot);
+      mbar_arrive_expect_tx(&ctl->x_full[i], d.height * 128);
       tma_load_2d(xs + i * kSlot, &map_x, &ctl->x_full[i], (s0 + i) * 64, (int)row0);
     }
   __syncwarp();
-  build_table(sh->table, p, p.offsets ? sh->offsets : nullptr, bad, tile, id);
+  build_table(sh->table, p, p.offsets ? sh->offsets : nullptr, bad, row0, rows, id);
   const Table& tb = sh->table;
   tc_fence_before();
   __syncthreads();
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
         ok = warp_wait(&ctl->x_empty[slot], ((it / kXSlots) & 1) ^ 1, ctl, p.status);
         if (!ok) break;
         if (el) {
-          mbar_arrive_expect_tx(&ctl->x_full[slot], kSlot);
+          mbar_arrive_expect_tx(&ctl->x_full[slot], d.height * 128);
           tma_load_2d(xs + slot * kSlot, &map_x, &ctl->x_full[slot], s * 64, (int)row0);
         }
       }
@@ -686,6 +686,7 @@ struct UpShared {
 };
 
 struct UpShape {
+  int height;  // rows of a tile
   int rp;      // r rounded up to 16, 32, 64 or 128
   int gparts;  // parts of a tile's rounds
   int ntiles;  // of 128 outputs
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
   const int per_tile = u.ntiles * u.gparts;
   const int tile = blockIdx.x / u.shares, share = blockIdx.x % u.shares;
   const int u0 = (int)((int64_t)per_tile * share / u.shares), u1 = (int)((int64_t)per_tile * (share + 1) / u.shares);
-  const int row0 = tile * kTile;
+  const int row0 = tile * u.height;
   const TileTable* const table = u.tables + tile;
   // nothing to write: no rows, or no groups and base in place
   const bool idle = table->inside == 0 || (table->groups == 0 && p.base == p.out);
@@ -833,7 +834,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         if (!warp_wait(&ctl->io_empty[s], io_r.turn ^ 1, ctl, p.status)) return false;
         if (el) {
           if (add) {
-            mbar_arrive_expect_tx(&ctl->io_full[s], kIoBytes);
+            mbar_arrive_expect_tx(&ctl->io_full[s], u.height * 256);
             // (the second half may lie behind the last output: nothing is read there)
             tma_load_2d(io + s * kIoBytes, &map_base, &ctl->io_full[s], n0, row0);
             tma_load_2d(io + s * kIoBytes + kIoBytes / 2, &map_base, &ctl->io_full[s], n0 + 64, row0);
@@ -853,7 +854,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     // (The groups' keys from global memory: sooner than by way of the table's copy.)
     const bool el = elect_one();
     if (el) {
-      mbar_arrive_expect_tx(&ctl->tile_full, sizeof(TileTable) + hblocks * kSlot);
+      mbar_arrive_expect_tx(&ctl->tile_full, sizeof(TileTable) + hblocks * u.height * 128);
       for (int b = 0; b < hblocks; ++b) tma_load_2d(hs + b * kSlot, &map_h, &ctl->tile_full, b * 64, row0);
       bulk_load(&sh->table, table, sizeof(TileTable), &ctl->tile_full);
     }
@@ -1114,18 +1115,34 @@ struct LoraLayout {
   int64_t tiles;
   size_t h, total;
 };
-LoraLayout lora_layout(int64_t R, int r) {
+LoraLayout lora_layout(const LoraPlan& pl, int64_t R, int r) {
   LoraLayout y;
-  y.tiles = (R + kTile - 1) / kTile;
+  y.tiles = (R + pl.height - 1) / pl.height;
   y.h = ((size_t)y.tiles * sizeof(TileTable) + 255) & ~(size_t)255;
-  y.total = y.h + (size_t)y.tiles * kTile * h_row(padded_rank(r)) * 2;
+  y.total = y.h + (size_t)y.tiles * pl.height * h_row(padded_rank(r)) * 2;
   return y;
+}
+
+// CTAs of a tile in the second launch, and the launch's time in units of 128 rows by 128
+// outputs: the way to a CTA's first unit takes about as long as three.
+int up_shares(int64_t tiles, int height, int per_tile, double* time = nullptr) {
+  const int sms = tc_num_sms();
+  int shares = 1;
+  double best = 0;
+  for (int i = 1; i <= 4; ++i) {  // shares that fill i waves; one to four where a share each does
+    const int n = (int)std::min<int64_t>(per_tile, tiles <= sms ? i * sms / tiles : i);
+    const double t = (double)((tiles * n + sms - 1) / sms) * ((per_tile + n - 1) / n * (height / 128.0) + 3);
+    if (i == 1 || t < best) best = t, shares = n;
+  }
+  if (time) *time = best;
+  return shares;
 }
 
 cudaError_t launch_down(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
   const CUtensorMapDataType dt = g.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const LoraLayout y = lora_layout(g.R, g.r);
+  const LoraLayout y = lora_layout(pl, g.R, g.r);
   DownShape d;
+  d.height = pl.height;
   d.rp = padded_rank(g.r);
   d.splits = pl.splits;
   d.mparts = pl.mparts;
@@ -1133,7 +1150,7 @@ cudaError_t launch_down(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) 
   d.h = reinterpret_cast<uint16_t*>(g.workspace + y.h);
   CUtensorMap mx, ma;
   const cuuint64_t xd[2] = {(cuuint64_t)g.K, (cuuint64_t)g.R}, xs = 2 * (cuuint64_t)g.x_stride;
-  const cuuint32_t xb[2] = {64, kTile};
+  const cuuint32_t xb[2] = {64, (cuuint32_t)pl.height};
   cudaError_t err = make_map(&mx, dt, 2, g.x, xd, &xs, xb);
   if (err != cudaSuccess) return err;
   const cuuint64_t ad[3] = {(cuuint64_t)g.K, (cuuint64_t)g.r, (cuuint64_t)g.L * g.E};
@@ -1154,8 +1171,9 @@ cudaError_t launch_down(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) 
 
 cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
   const CUtensorMapDataType dt = g.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const LoraLayout y = lora_layout(g.R, g.r);
+  const LoraLayout y = lora_layout(pl, g.R, g.r);
   UpShape u;
+  u.height = pl.height;
   u.rp = padded_rank(g.r);
   u.gparts = pl.gparts;
   u.ntiles = (g.N + kTile - 1) / kTile;
@@ -1181,8 +1199,8 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
                              : u.line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                             : CU_TENSOR_MAP_SWIZZLE_32B);
   if (err != cudaSuccess) return err;
-  const cuuint64_t hd[2] = {(cuuint64_t)h_row(u.rp), (cuuint64_t)y.tiles * kTile}, hst = 2 * hd[0];
-  const cuuint32_t hb[2] = {64, kTile};
+  const cuuint64_t hd[2] = {(cuuint64_t)h_row(u.rp), (cuuint64_t)y.tiles * pl.height}, hst = 2 * hd[0];
+  const cuuint32_t hb[2] = {64, (cuuint32_t)pl.height};
   err = make_map(&mh, dt, 2, g.workspace + y.h, hd, &hst, hb);
   if (err != cudaSuccess) return err;
   mbase = mout = mb;
@@ -1191,7 +1209,7 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
         g.out_dtype == MQ_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const cuuint64_t d[2] = {(cuuint64_t)g.N, (cuuint64_t)g.R};
     const cuuint64_t t0 = 2 * (cuuint64_t)g.base_stride, t1 = 2 * (cuuint64_t)g.out_stride;
-    const cuuint32_t box[2] = {kTile / 2, kTile};
+    const cuuint32_t box[2] = {kTile / 2, (cuuint32_t)pl.height};
     err = make_map(&mout, ot, 2, g.out, d, &t1, box);
     if (err == cudaSuccess && g.base) err = make_map(&mbase, ot, 2, g.base, d, &t0, box);
     if (err != cudaSuccess) return err;
@@ -1210,20 +1228,14 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
   const auto kern = bf ? lora_up<true> : lora_up<false>;
   err = allow_smem(kern, kSmemMax, ready[bf]);
   if (err != cudaSuccess) return err;
-  // Shares by estimated time: the way to a CTA's first unit takes about as long as three.
-  const int sms = tc_num_sms(), per_tile = u.ntiles * u.gparts;
-  int64_t best = 0;
-  for (int n = 1; n <= per_tile && n <= 256; ++n) {
-    const int64_t t = (y.tiles * n + sms - 1) / sms * ((per_tile + n - 1) / n + 3);
-    if (best == 0 || t < best) best = t, u.shares = n;
-  }
+  u.shares = up_shares(y.tiles, pl.height, u.ntiles * u.gparts);
   const int64_t grid = y.tiles * u.shares;
   return launch_pdl(kern, dim3((unsigned)grid), dim3(kUpThreads), smem, st, mb, mh, mbase, mout, g, u);
 }
 
 }  // namespace
 
-size_t lora_workspace(int64_t R, int r) { return lora_layout(R, r).total; }
+size_t lora_workspace(const LoraPlan& pl, int64_t R, int r) { return lora_layout(pl, R, r).total; }
 
 LoraPlan lora_plan(int64_t R, int K, int N, int r, int L, int E) {
   LoraPlan pl = {};
@@ -1233,14 +1245,30 @@ LoraPlan lora_plan(int64_t R, int K, int N, int r, int L, int E) {
   pl.splits = pl.mparts = pl.gparts = 1;
   pl.rows = R <= 1024 && R * adapter <= 48e6 + groups * adapter;
   if (pl.rows) return pl;
-  const int64_t tiles = (R + kTile - 1) / kTile;
+  // Rows of a tile, and K splits (with the clusters of that many CTAs that this GPU holds at
+  // a time): by the estimated time of both launches, in units of 128 x 128 outputs of the
+  // second, 1.45 us.  A stage of the first takes a quarter of one, half of it for the
+  // groups; the way in and out of it six.
+  constexpr int kClusters[4] = {152, 76, 36, 15};
+  const int ntiles = (N + kTile - 1) / kTile, stages = (K + 63) / 64;
+  double best = 0;
+  for (int h = kTile; h >= 64; h -= 16) {
+    const int64_t n = (R + h - 1) / h;
+    double up, down = 0;
+    int splits = 1;
+    up_shares(n, h, ntiles, &up);
+    for (int i = 0; i < 4 && (i == 0 || stages >= 8 << i); ++i) {
+      const double t = (double)((n + kClusters[i] - 1) / kClusters[i]) * ((stages >> i) * (0.13 + 0.13 * h / 128) + 6);
+      if (i == 0 || t < down) down = t, splits = 1 << i;
+    }
+    if (h == kTile || up + down < 0.97 * best) best = up + down, pl.height = h, pl.splits = splits;
+  }
+  const int64_t tiles = (R + pl.height - 1) / pl.height;
   const int per = kTile / padded_rank(r);
-  const int tile_groups = (int)std::min<double>(kTile, groups);
+  const int tile_groups = (int)std::min<double>(pl.height, groups);
   const int accs = (tile_groups + per - 1) / per;
-  const int stages = (K + 63) / 64;
-  while (pl.splits < 8 && stages >= pl.splits * 8 && tiles * pl.splits * 2 <= sms) pl.splits *= 2;
-  pl.mparts = (int)std::max<int64_t>(1, std::min<int64_t>(accs, sms / (tiles * pl.splits)));
-  const int ntiles = (N + kTile - 1) / kTile;
+  const int clusters = pl.splits == 1 ? 152 : pl.splits == 2 ? 76 : pl.splits == 4 ? 36 : 15;
+  pl.mparts = (int)std::max<int64_t>(1, std::min<int64_t>(accs, clusters / tiles));
   while (pl.gparts * 2 <= tile_groups && tiles * ntiles * pl.gparts * 2 <= sms) pl.gparts *= 2;
   return pl;
 }

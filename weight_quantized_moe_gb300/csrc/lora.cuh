@@ -24,11 +24,12 @@ struct LoraArgs {
 };
 struct LoraPlan {
   bool rows;   // one cluster per row, one launch (else two launches over tiles of rows)
+  int height;  // rows of a tile, a multiple of 16
   int splits;  // K splits of the first launch: CTAs of a cluster
   int mparts;  // clusters among which it divides a tile's adapters
   int gparts;  // parts of a tile's adapters in the second launch
 };
-MQ_HIDDEN size_t lora_workspace(int64_t R, int r);
+MQ_HIDDEN size_t lora_workspace(const LoraPlan& pl, int64_t R, int r);
 MQ_HIDDEN LoraPlan lora_plan(int64_t R, int K, int N, int r, int L, int E);
 // The plan's kernels one by one (which: 0 A x, or both in one; 1 the rest).
 MQ_HIDDEN cudaError_t launch_lora(const LoraArgs& g, const LoraPlan& pl, int which, cudaStream_t st);
