@@ -131,7 +131,6 @@ __global__ void __launch_bounds__(kRowThreads, 4) lora_rows(const LoraArgs p) {
   const uint16_t* a = static_cast<const uint16_t*>(p.a) + g * p.r * p.K;
   const uint16_t* b = static_cast<const uint16_t*>(p.b) + g * p.r * p.N;
 
-  // The first outputs' rows of B and base are on their way while A x is summed.
   constexpr int kOuts = kRowThreads / LPO;  // outputs of a pass
   constexpr int kAhead = 4;
   const int chunk = tid % LPO;
@@ -145,30 +144,42 @@ __global__ void __launch_bounds__(kRowThreads, 4) lora_rows(const LoraArgs p) {
     old[i] = live && chunk == 0 && p.base ? load_as(p.base, p.out_dtype, t * p.base_stride + n) : 0.0f;
   };
   const int first = n0 + tid / LPO;
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) fetch(first + i * kOuts, i);
 
-  // A x over this CTA's vectors of eight; a warp takes four ranks at a time.
+  // A x over this CTA's vectors of eight; a warp takes two ranks at a time, with
+  // two vectors of each and of x in flight.
   const int vecs = p.K / 8;
   const int v0 = (int)((int64_t)vecs * rank / kCluster), v1 = (int)((int64_t)vecs * (rank + 1) / kCluster);
-  constexpr int kRanks = 4;
+  constexpr int kRanks = 2, kDeep = 2;
   bool met = false;
   for (int j0 = warp; j0 < p.r; j0 += 8 * kRanks) {
     float acc[kRanks] = {};
-#pragma unroll 2
-    for (int v = v0 + lane; v < v1; v += 32) {
-      const uint4 xv = __ldg(reinterpret_cast<const uint4*>(x) + v);
-      uint4 av[kRanks];
+    for (int v = v0 + lane; v < v1; v += 32 * kDeep) {
+      uint4 xv[kDeep], av[kDeep][kRanks];
 #pragma unroll
-      for (int i = 0; i < kRanks; ++i)
-        av[i] = j0 + 8 * i < p.r ? __ldg(reinterpret_cast<const uint4*>(a + (int64_t)(j0 + 8 * i) * p.K) + v) : zero;
-      float xf[8], af[8];
-      unpack8(xv, BF16, xf);
+      for (int d = 0; d < kDeep; ++d) {
+        const int w = v + 32 * d;
+        xv[d] = w < v1 ? __ldg(reinterpret_cast<const uint4*>(x) + w) : zero;
 #pragma unroll
-      for (int i = 0; i < kRanks; ++i) {
-        unpack8(av[i], BF16, af);
-        acc[i] = dot8(xf, af, acc[i]);
+        for (int i = 0; i < kRanks; ++i)
+          av[d][i] = w < v1 && j0 + 8 * i < p.r
+                         ? __ldg(reinterpret_cast<const uint4*>(a + (int64_t)(j0 + 8 * i) * p.K) + w)
+                         : zero;
       }
+      float xf[8], af[8];
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) {
+        unpack8(xv[d], BF16, xf);
+#pragma unroll
+        for (int i = 0; i < kRanks; ++i) {
+          unpack8(av[d][i], BF16, af);
+          acc[i] = dot8(xf, af, acc[i]);
+        }
+      }
+    }
+    if (!met) {
+      // the first outputs' rows of B and base are on their way while the sums meet
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) fetch(first + i * kOuts, i);
     }
     if (!met) cluster_wait();
     met = true;
