@@ -44,9 +44,10 @@ def test_product_refusals(lib):
     assert lib.moe_grouped_product_workspace(4, 64, 64, 2000) == 0
     need = lib.moe_grouped_product_workspace(1, 4096, 256, 1)
     assert need > 0
+    # (one row times weights stored [E, K, N] is summed in splits; stored [E, N, K] it needs no workspace)
     for wk, nb in ((None, 0), (P, need - 1), (None, need)):
-        assert p(R=1, K=4096, N=256, E=1, st=4096, ws=4096, off=None, wk=wk, nb=nb) == 4
-    assert p(R=1, K=4096, N=256, E=1, st=4096, ws=4096, off=None, wk=ODD, nb=need) == 1
+        assert p(R=1, K=4096, N=256, E=1, st=4096, ws=256, tr=1, off=None, wk=wk, nb=nb) == 4
+    assert p(R=1, K=4096, N=256, E=1, st=4096, ws=256, tr=1, off=None, wk=ODD, nb=need) == 1
 
 
 def test_gradient_refusals(lib):
