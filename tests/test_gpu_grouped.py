@@ -35,7 +35,7 @@ SHAPES = [
     ([1], 0, 0, 4096, 256),                     # one row, K split
     ([20], 0, 0, 4096, 256),
     ([3, 0, 1], 0, 0, 72, 40),                  # an empty expert, K and N that fill no tile
-    ([0, 2, 4, 0, 1], 1, 0, 264, 33 * 8),       # eight rows: the most that take no tensor cores
+    ([0, 2, 4, 0, 1], 1, 0, 264, 33 * 8),       # eight rows with one of no expert
     ([8], 0, 0, 8200, 24),
     ([0, 1, 3], 2, 2, 2056, 40),
     ([40] * 24, 1, 2, 136, 264),                # both gradients in one launch

@@ -25,6 +25,14 @@
 // first CTA); warp 2 clears the tail of GG_ROWS; warp 3 zeroes rows of no expert;
 // warps 4-11 are the epilogue.  Two accumulator buffers: the next unit's MMAs run
 // while the epilogue stores.
+//
+// What bounds it: with few rows per expert the weights (128 rows, 8 experts, 4096 x 28672:
+// 273 us, 6.9 TB/s); with many the tensor pipe, and with it power (8192 rows there: 1245 us,
+// 1.55 PFLOP/s in a loop at 1.45 GHz; there a CTA pair holds 256 by 256, which halves the
+// operand reads of two CTAs by themselves).  The gradient of the weights writes more than
+// it reads where experts have few rows, and writes alone go at little more than half the
+// rate of a copy, so both gradients then run side by side in one launch: 128 experts, 4096
+// rows, 1536 x 2048: 304 us one after the other, 274 together.
 #include "grouped.cuh"
 #include "pipe.cuh"
 
@@ -167,8 +175,8 @@ __device__ __forceinline__ Unit decode_unit(const Params& p, const int* chunk_st
 
 // The i-th unit of this worker: from the list in shared memory (decoded once, by
 // all threads at a time), past its end on the spot.  (Each role decoding each of its
-// units cost GG_ROWS, whose units are short, more than their work: 128 experts, 4096
-// rows, 1536 x 2048 ... us.)
+// units cost GG_ROWS, whose units are short, more than their work: both gradients of 128 experts,
+// 4096 rows, 1536 x 2048, 410 us that way and 372 with the list.)
 template <int FORM, int BN, int CG>
 __device__ __forceinline__ Unit unit_at(const Params& p, const int* chunk_start, const int4* list,
                                         uint32_t i, uint32_t worker, uint32_t workers) {
@@ -642,11 +650,7 @@ cudaError_t launch_form(const GgPlan& pl, const CUtensorMap& mw, const CUtensorM
                         const CUtensorMap& mr, const Params& p, int64_t units, cudaStream_t st) {
   if (pl.pair) return launch_one<FORM, 256, 2>(mw, ma, mr, p, units, st);
   if constexpr (FORM != GG_ROWS) {
-    switch (pl.bn) {
-      case 16: return launch_one<FORM, 16, 1>(mw, ma, mr, p, units, st);
-      case 32: return launch_one<FORM, 32, 1>(mw, ma, mr, p, units, st);
-      case 64: return launch_one<FORM, 64, 1>(mw, ma, mr, p, units, st);
-    }
+    if (pl.bn == 64) return launch_one<FORM, 64, 1>(mw, ma, mr, p, units, st);
   }
   return launch_one<FORM, 128, 1>(mw, ma, mr, p, units, st);
 }
@@ -673,10 +677,24 @@ GgPlan gg_plan(GgForm form, int64_t R, int E, int M, int N, int K) {
     return pl;
   }
   const double live = std::max(1.0, E * (1.0 - std::pow(1.0 - 1.0 / E, (double)R)));
-  const double avg = R / live;
-  pl.pair = avg > 128;
-  const double fullest = avg + 1.5 * std::sqrt(2 * avg * std::log((double)E));
-  pl.bn = pl.pair ? 256 : R <= 16 ? 16 : fullest <= 32 || R <= 32 ? 32 : fullest <= 64 || R <= 64 ? 64 : 128;
+  // Columns of a tile: so many that a popular expert, with twice the average and 1.5
+  // standard deviations of the fullest of E, is likely to fit.  Narrow tiles read a popular
+  // expert's weights, from L2, for each of its chunks; wide ones cost little where the loads
+  // are even, as the instructions are no wider than the rows.  us with 64, 128 and pairs'
+  // 256 columns: 128 experts, 2048 x 1536, 16 rows each 124, 128, 130, 32 rows 126, 130, 132
+  // (by Zipf's law 136, 129, 130), 64 rows 133, 138, 138 (156, 143, 136), 128 rows 178, 151,
+  // 148 (206, 172, 154); 8 experts, 4096 x 14336, 16 rows 140, 142, 144, 64 rows 160, 147,
+  // 149, 128 rows 191, 174, 154, 512 rows 632, 386, 294.  (16 and 32 columns save nothing
+  // but the tail of an epilogue: 8 experts, 4096 x 28672, 16 rows 278 with 32, 270 with 64;
+  // 1 row, 4096 x 28672, 40.9 with 16, 39.6 with 64.)
+  const double likely = 2 * R / live;
+  const double fullest = std::min<double>(R, likely + 1.5 * std::sqrt(2 * likely * std::log((double)E)));
+  pl.pair = fullest > 128;
+  pl.bn = pl.pair ? 256 : fullest > 64 ? 128 : 64;
+  // K splits while they leave a wave of units and eight stages each (us unsplit, with 2, 4 and
+  // 8): 4096 x 4096, 17 rows 15.5, 11.9, 10.7, 11.9, 256 rows 25.0, 19.4, 16.4, 19.2, 1024 rows
+  // 26.1, 32.8, 42.4, 65.7; 8 experts, 14336 x 1024, 128 rows 48.3, 40.3, 41.0, 43.5; 16
+  // experts, 2048 x 768, 128 rows 12.0, 14.6, 13.9, 14.9.
   if (R > 1024) return pl;
   const double workers = pl.pair ? sms / 2 : sms;
   const double units = std::max(live, std::ceil((double)R / pl.bn)) * ((M + (pl.pair ? 255 : 127)) / (pl.pair ? 256 : 128));
@@ -773,7 +791,11 @@ cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
 }
 
 // Side by side where memory bounds both and neither is split: the weights read and
-// written at 6.6 and 3.8 TB/s, against the products at 1.5 PFLOP/s.
+// written at 6.6 and 3.8 TB/s, against the products at 1.5 PFLOP/s.  us one after the other
+// and side by side: 128 experts, 2048 x 1536, 4096 rows 277 and 273, 16384 rows 325 and 297,
+// 65536 rows 640 and 661; 8 experts, 4096 x 14336, 128 rows 335 and 316, 1024 rows 368 and
+// 330, 2048 rows 440 and 462, 4096 rows 697 and 712; 16 experts, 1408 x 2048, 517 rows 57
+// and 43.  (In between it depends on the loads' last chunks.)
 bool gg_side_by_side(const GgGemm& rows, const GgGemm& weights) {
   const int64_t n = (int64_t)rows.M * rows.K;
   const double live = (double)std::min<int64_t>(rows.R, rows.E);

@@ -1254,7 +1254,18 @@ LoraPlan lora_plan(int64_t R, int K, int N, int r, int L, int E) {
   const double adapter = 2.0 * r * ((double)K + N);                     // bytes
   const double groups = std::min<double>((double)R, (double)L * E);    // at most
   pl.splits = pl.mparts = pl.gparts = 1;
-  pl.rows = R <= 1024 && R * adapter <= 48e6 + groups * adapter;
+  // Rows or tiles, by their estimated times in us.  Rows: 64 at a time, each its adapter.
+  // Tiles: the way through two launches, more with more groups in a tile; a mean over
+  // adapters in runs and at random.  Measured, rows and tiles (at random / in runs), 4096 x
+  // 4096: rank 16, 48 adapters, 64 rows 6.1 and 25 / 26, 256 rows 22.6 and 31 / 19, 512 rows
+  // 48.6 and 52 / 22; of 4 adapters, 128 rows 11.0 and 21 / 22, 256 rows 20.7 and 15.9 /
+  // 14.7; rank 32, 128 rows 20.5 and 29 / 24, 192 rows 30.6 and 28 / 18; rank 64, 1 row 9.7
+  // and 13.0, 64 rows 16.7 and 22.7, 96 rows 35 and 33; rank 128, 1 row 17.0 and 14.0.  1024 x
+  // 1024, rank 8: 256 rows 16.3 and 27.5 / 23.5, 512 rows 30.8 and 31.7 / 23.5.
+  const double waves = R / 64.0, many = std::max(1.0, waves);
+  const double rows_us = 3 * many + 7 * adapter * 1e-6 * (many + waves);
+  const double tiles_us = 13.5 + 0.15 * std::min(64.0, 4 * groups);
+  pl.rows = rows_us <= tiles_us;
   if (pl.rows) return pl;
   // Rows of a tile, and K splits (with the clusters of that many CTAs that this GPU holds at
   // a time): by the estimated time of both launches, in units of 128 x 128 outputs of the
