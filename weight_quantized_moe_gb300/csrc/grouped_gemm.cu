@@ -57,6 +57,8 @@ constexpr int kGroup = 8;       // M tiles that a walk over the columns shares
 constexpr int kPartRows = 16;   // rows of the boxes that load a partly filled chunk
 constexpr size_t kSmemMax = 227 * 1024;
 
+constexpr int kSegment = 4;     // stages whose sum tensor memory holds, of float32 results
+
 constexpr int kChunkBytes = 32 * 64;  // an epilogue warp's 32 lanes by 64 bytes of columns
 
 template <int FORM, int BN, int CG>
@@ -234,8 +236,9 @@ __device__ __forceinline__ void stage_line(uint8_t* chunk, int lane, const uint3
         make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
-// One product, by the CTA `block` of `blocks` that work at it.
-template <int FORM, int BN, int CG>
+// One product, by the CTA `block` of `blocks` that work at it.  SEG: sums of kSegment
+// stages leave tensor memory and are added up in the epilogue's registers.
+template <int FORM, int BN, int CG, bool SEG>
 __device__ __forceinline__ void gg_body(const CUtensorMap& map_w, const CUtensorMap& map_a,
                                         const CUtensorMap& map_part, const Params& p, uint32_t block,
                                         uint32_t blocks) {
@@ -418,35 +421,38 @@ __device__ __forceinline__ void gg_body(const CUtensorMap& map_w, const CUtensor
       int s0, s1;
       stages_of<FORM>(p, w, s0, s1);
       if (s0 == s1) continue;  // no rows: the epilogue stores zeros
-      const uint32_t buf = done & 1;
-      ok = warp_wait<CG>(&ctl->acc_empty[buf], ((done >> 1) & 1) ^ 1, ctl, p.status);
-      ++done;
-      tc_fence_after();
-      const uint32_t acc = tmem + buf * BN;
       const uint32_t idesc = p.idesc | (uint32_t)(columns<FORM, BN, CG>(p, w) >> 3) << 17;
-      uint32_t accumulate = 0;
-      for (int s = s0; s < s1 && ok; ++s, ++it) {
-        const uint32_t slot = it % C::kStages;
-        ok = warp_wait<CG>(&ctl->full[slot], (it / C::kStages) & 1, ctl, p.status);
-        if (!ok) break;
+      for (int s = s0; s < s1 && ok;) {
+        const int end = SEG ? min(s + kSegment, s1) : s1;
+        const uint32_t buf = done & 1;
+        ok = warp_wait<CG>(&ctl->acc_empty[buf], ((done >> 1) & 1) ^ 1, ctl, p.status);
+        ++done;
         tc_fence_after();
-        if (el) {
-          const uint32_t base = smem_addr(stages + (size_t)slot * C::kStageBytes);
-          const uint64_t ad = FORM == GG_W_K ? smem_desc_k_sw128(base)
-                                             : smem_desc_mn_sw128(base, kBlockBytes);
-          const uint64_t bd = FORM == GG_ROWS ? smem_desc_mn_sw128(base + kABytes, kBlockBytes)
-                                              : smem_desc_k_sw128(base + kABytes);
-          const int steps = FORM == GG_ROWS ? min(4, (w.n - s * kStageK + 15) >> 4) : 4;
+        const uint32_t acc = tmem + buf * BN;
+        uint32_t accumulate = 0;
+        for (; s < end && ok; ++s, ++it) {
+          const uint32_t slot = it % C::kStages;
+          ok = warp_wait<CG>(&ctl->full[slot], (it / C::kStages) & 1, ctl, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          if (el) {
+            const uint32_t base = smem_addr(stages + (size_t)slot * C::kStageBytes);
+            const uint64_t ad = FORM == GG_W_K ? smem_desc_k_sw128(base)
+                                               : smem_desc_mn_sw128(base, kBlockBytes);
+            const uint64_t bd = FORM == GG_ROWS ? smem_desc_mn_sw128(base + kABytes, kBlockBytes)
+                                                : smem_desc_k_sw128(base + kABytes);
+            const int steps = FORM == GG_ROWS ? min(4, (w.n - s * kStageK + 15) >> 4) : 4;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (FORM != GG_ROWS || j < steps)
-              mma_ss<CG>(acc, ad + j * (FORM == GG_W_K ? 2 : 128), bd + j * (FORM == GG_ROWS ? 128 : 2),
-                         idesc, accumulate | j);
-          commit<CG>(&ctl->empty[slot]);
+            for (int j = 0; j < 4; ++j)
+              if (FORM != GG_ROWS || j < steps)
+                mma_ss<CG>(acc, ad + j * (FORM == GG_W_K ? 2 : 128), bd + j * (FORM == GG_ROWS ? 128 : 2),
+                           idesc, accumulate | j);
+            commit<CG>(&ctl->empty[slot]);
+          }
+          accumulate = 1;
         }
-        accumulate = 1;
+        if (ok && el) commit<CG>(&ctl->acc_full[buf]);
       }
-      if (ok && el) commit<CG>(&ctl->acc_full[buf]);
     }
     // nothing this warp issued may be in flight when the memory goes
     if (el) {
@@ -500,86 +506,130 @@ __device__ __forceinline__ void gg_body(const CUtensorMap& map_w, const CUtensor
       const int m = w.m + (int)rank * kTileM + quad * 32 + lane;  // this lane's output
       const int dtype = p.splits > 1 ? MQ_DTYPE_F32 : p.out_dtype;
       const bool empty = FORM == GG_ROWS && w.n == 0;
-      const uint32_t buf = done & 1;
-      if (!empty) {
-        ok = warp_wait(&ctl->acc_full[buf], (done >> 1) & 1, ctl, p.status);
-        ++done;
-        if (!ok) break;
+      const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+      auto sums_ready = [&]() -> bool {
+        if (!warp_wait(&ctl->acc_full[done & 1], (done >> 1) & 1, ctl, p.status)) return false;
         tc_fence_after();
-      }
-      const uint32_t acc = tmem + buf * BN + ((uint32_t)(quad * 32) << 16);
-      if constexpr (FORM == GG_ROWS) {
-        // A lane is a row of the result: 64 bytes of it at a time go to shared memory
-        // (swizzled) and from there by TMA, which leaves out what lies outside.  (Longer
-        // lines would take a stage's place.)
-        const int n = min(BN, p.N - w.col0);
-        const int c1 = min(n, (half + 1) * (BN / 2));
-        const bool f32 = dtype == MQ_DTYPE_F32;
-        uint8_t* chunk = chunks_out + (warp - 4) * kChunkBytes;
-        if (m - lane < p.M) {
-          for (int c0 = half * (BN / 2); c0 < c1; c0 += 32) {
-            uint32_t v[32];
-            if (empty) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0;
-            } else {
-              tmem_ld32_sync(acc + c0, v);
-            }
-            if (p.tma_out) {
-              uint32_t line[16];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if (f32) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) line[i] = v[16 * h + i];
-                } else {
-                  if (h) break;
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) line[i] = pack2(v[2 * i], v[2 * i + 1], dtype == MQ_DTYPE_BF16);
-                }
-                if (lane == 0) bulk_wait_read<0>();  // what was there has been read
-                __syncwarp();
-                stage_line(chunk, lane, line);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                  tma_store_3d(&map_part, chunk, w.col0 + c0 + 16 * h, m - lane, w.split * p.E + w.e);
-                  bulk_commit();
-                }
-                if (f32 && c0 + 16 >= c1) break;
-              }
-            } else if (m < p.M) {
-              void* out = p.splits > 1 ? p.part + (int64_t)w.split * p.E * p.M * p.N : p.out;
-              const int64_t at = ((int64_t)w.e * p.M + m) * p.N + w.col0 + c0;
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (c0 + i < n) store_out(out, dtype, at + i, __uint_as_float(v[i]));
-            }
-          }
-        }
-      } else {
-        void* out = p.out;
-        if (p.splits > 1) out = p.part + (int64_t)w.split * p.R * p.M;
-        if (m - lane < p.M) {
-          const bool live = m < p.M;
-          for (int c0 = half * 16; c0 < w.n; c0 += 32) {
-            uint32_t v[16];
-            tmem_ld16_sync(acc + c0, v);
-            const int64_t at = (int64_t)(w.row0 + c0) * p.M + m;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (live && c0 + j < w.n)
-                store_out(out, dtype, at + (int64_t)j * p.M, __uint_as_float(v[j]));
-          }
-        }
-      }
-      if (!empty) {
+        return true;
+      };
+      auto sums_read = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (CG == 2) mbar_arrive_tmem_free(map_rank(&ctl->acc_empty[buf], 0));
-          else mbar_arrive(&ctl->acc_empty[buf]);
+          if (CG == 2) mbar_arrive_tmem_free(map_rank(&ctl->acc_empty[done & 1], 0));
+          else mbar_arrive(&ctl->acc_empty[done & 1]);
         }
+        ++done;
+      };
+      // Columns of a lane: a half of the tile in steps of 32 (GG_ROWS), or every other
+      // step of 16.
+      constexpr int kStep = FORM == GG_ROWS ? 32 : 16;
+      constexpr int kSteps = BN / 2 / kStep;
+      const int n = FORM == GG_ROWS ? min(BN, p.N - w.col0) : w.n;
+      const int c1 = FORM == GG_ROWS ? min(n, (half + 1) * (BN / 2)) : n;
+      auto column = [&](int i) { return FORM == GG_ROWS ? half * (BN / 2) + i * 32 : half * 16 + i * 32; };
+      auto read = [&](int c0, uint32_t (&v)[kStep]) {
+        const uint32_t at = tmem + (done & 1) * BN + lanes + c0;
+        if constexpr (FORM == GG_ROWS) tmem_ld32_sync(at, v);
+        else tmem_ld16_sync(at, v);
+      };
+      auto store = [&](int c0, const uint32_t (&v)[kStep]) {
+        if constexpr (FORM == GG_ROWS) {
+          // A lane is a row of the result: 64 bytes of it at a time go to shared memory
+          // (swizzled) and from there by TMA, which leaves out what lies outside.  (Longer
+          // lines would take a stage's place.)
+          const bool f32 = dtype == MQ_DTYPE_F32;
+          uint8_t* chunk = chunks_out + (warp - 4) * kChunkBytes;
+          if (p.tma_out) {
+            uint32_t line[16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (f32) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) line[i] = v[16 * h + i];
+              } else {
+                if (h) break;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) line[i] = pack2(v[2 * i], v[2 * i + 1], dtype == MQ_DTYPE_BF16);
+              }
+              if (lane == 0) bulk_wait_read<0>();  // what was there has been read
+              __syncwarp();
+              stage_line(chunk, lane, line);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_3d(&map_part, chunk, w.col0 + c0 + 16 * h, m - lane, w.split * p.E + w.e);
+                bulk_commit();
+              }
+              if (f32 && c0 + 16 >= c1) break;
+            }
+          } else if (m < p.M) {
+            void* out = p.splits > 1 ? p.part + (int64_t)w.split * p.E * p.M * p.N : p.out;
+            const int64_t at = ((int64_t)w.e * p.M + m) * p.N + w.col0 + c0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c0 + i < n) store_out(out, dtype, at + i, __uint_as_float(v[i]));
+          }
+        } else {
+          void* out = p.out;
+          if (p.splits > 1) out = p.part + (int64_t)w.split * p.R * p.M;
+          const int64_t at = (int64_t)(w.row0 + c0) * p.M + m;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (m < p.M && c0 + j < n) store_out(out, dtype, at + (int64_t)j * p.M, __uint_as_float(v[j]));
+        }
+      };
+      if constexpr (SEG) {
+        uint32_t sum[kSteps][kStep];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+          for (int j = 0; j < kStep; ++j) sum[i][j] = 0;
+        int s0, s1;
+        stages_of<FORM>(p, w, s0, s1);
+        for (int s = s0; s < s1; s += kSegment) {
+          ok = sums_ready();
+          if (!ok) break;
+          if (m - lane < p.M) {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+              if (column(i) >= c1) continue;
+#pragma unroll
+              for (int h = 0; h < kStep; h += 16) {
+                uint32_t v[16];
+                tmem_ld16_sync(tmem + (done & 1) * BN + lanes + column(i) + h, v);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  sum[i][h + j] = __float_as_uint(__uint_as_float(sum[i][h + j]) + __uint_as_float(v[j]));
+              }
+            }
+          }
+          sums_read();
+        }
+        if (!ok) break;
+        if (m - lane < p.M) {
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i)
+            if (column(i) < c1) store(column(i), sum[i]);
+        }
+      } else {
+        if (!empty) {
+          ok = sums_ready();
+          if (!ok) break;
+        }
+        if (m - lane < p.M) {
+          for (int i = 0; column(i) < c1; ++i) {
+            uint32_t v[kStep];
+            if (empty) {
+#pragma unroll
+              for (int j = 0; j < kStep; ++j) v[j] = 0;
+            } else {
+              read(column(i), v);
+            }
+            store(column(i), v);
+          }
+        }
+        if (!empty) sums_read();
       }
     }
   }
@@ -595,27 +645,27 @@ __device__ __forceinline__ void gg_body(const CUtensorMap& map_w, const CUtensor
   }
 }
 
-template <int FORM, int BN, int CG>
+template <int FORM, int BN, int CG, bool SEG>
 __global__ void __launch_bounds__(kThreads, 1)
     gg_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
             const __grid_constant__ CUtensorMap map_part, const Params p) {
-  gg_body<FORM, BN, CG>(map_w, map_a, map_part, p, blockIdx.x, gridDim.x);
+  gg_body<FORM, BN, CG, SEG>(map_w, map_a, map_part, p, blockIdx.x, gridDim.x);
 }
 
 // Both gradients side by side: the first `rows_blocks` CTAs work at the rows', the others
 // at the weights'.  For gradients that memory bounds: one reads the weights and the other
 // writes as much, and HBM takes both at once at nearly twice the rate of writes alone (a
 // fill runs at 3.84 TB/s, a copy at 6.69).
-template <int FORM>
+template <int FORM, bool SEG>
 __global__ void __launch_bounds__(kThreads, 1)
     gg_both(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
             const __grid_constant__ CUtensorMap map_part, const __grid_constant__ CUtensorMap map_y,
             const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_out,
             const Params rows, const Params weights, uint32_t rows_blocks) {
   if (blockIdx.x < rows_blocks)
-    gg_body<FORM, 256, 2>(map_w, map_a, map_part, rows, blockIdx.x, rows_blocks);
+    gg_body<FORM, 256, 2, false>(map_w, map_a, map_part, rows, blockIdx.x, rows_blocks);
   else
-    gg_body<GG_ROWS, 256, 2>(map_y, map_x, map_out, weights, blockIdx.x - rows_blocks,
+    gg_body<GG_ROWS, 256, 2, SEG>(map_y, map_x, map_out, weights, blockIdx.x - rows_blocks,
                              gridDim.x - rows_blocks);
 }
 
@@ -636,9 +686,10 @@ template <int FORM, int BN, int CG>
 cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const CUtensorMap& mr,
                        const Params& p, int64_t units, cudaStream_t st) {
   constexpr size_t smem = Cfg<FORM, BN, CG>::kSmem;
-  auto kern = gg_gemm<FORM, BN, CG>;
-  static std::atomic<uint64_t> ready{0};
-  const cudaError_t err = allow_smem(kern, smem, ready);
+  const bool seg = p.out_dtype == MQ_DTYPE_F32;
+  auto kern = seg ? gg_gemm<FORM, BN, CG, true> : gg_gemm<FORM, BN, CG, false>;
+  static std::atomic<uint64_t> ready[2];
+  const cudaError_t err = allow_smem(kern, smem, ready[seg]);
   if (err != cudaSuccess) return err;
   const int sms = tc_num_sms();
   const int workers = (int)std::max<int64_t>(1, std::min<int64_t>(units, sms / CG));
@@ -824,9 +875,11 @@ cudaError_t launch_gg_both(const GgGemm& rows, const GgGemm& weights, cudaStream
   const int second = (int)std::max<int64_t>(1, std::min<int64_t>(pairs - first, w.units));
   constexpr size_t smem = std::max({Cfg<GG_W_K, 256, 2>::kSmem, Cfg<GG_ROWS, 256, 2>::kSmem});
   const bool by_k = rows.form == GG_W_K;
-  const auto kern = by_k ? gg_both<GG_W_K> : gg_both<GG_W_M>;
-  static std::atomic<uint64_t> ready[2];
-  err = allow_smem(kern, smem, ready[by_k]);
+  const bool seg = w.p.out_dtype == MQ_DTYPE_F32;
+  const auto kern = seg ? (by_k ? gg_both<GG_W_K, true> : gg_both<GG_W_M, true>)
+                        : (by_k ? gg_both<GG_W_K, false> : gg_both<GG_W_M, false>);
+  static std::atomic<uint64_t> ready[4];
+  err = allow_smem(kern, smem, ready[seg * 2 + by_k]);
   if (err != cudaSuccess) return err;
   return launch_pdl_cluster(kern, dim3(2 * (first + second)), dim3(kThreads), 2, smem, st, r.mw, r.ma, r.mr, w.mw,
                             w.ma, w.mr, r.p, w.p, (uint32_t)(2 * first));
