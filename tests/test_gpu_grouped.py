@@ -202,6 +202,35 @@ def test_gradients_alone_and_together(mq):
         clean(mq)
 
 
+@pytest.mark.parametrize("R,K,N", [(1, 65536, 128), (40, 65536, 72), (1040, 65536, 128)])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_long_sums_with_float32_results(mq, R, K, N, transposed):
+    """The tensor core cuts off where it adds.  Sums of 256 products do so 256 times at most,
+    by a step of 2^-23 of their own size; their sum, of K / 256 of them, rounds to nearest.
+    In one go values of one sign, which are all cut off to the same side, would be out by
+    about K / 16 times half a step of half the sum: 1.2e-4 here, where 4.6e-5 are allowed."""
+    g = torch.Generator().manual_seed(R)
+    a = (torch.rand(R, K, generator=g) + 0.5).to(BF16).cuda()
+    w = (torch.rand(N, K, generator=g) + 0.5).to(BF16)
+    out = mq.moe_grouped_product(a, storage(w, transposed)[None], out_dtype=F32)
+    clean(mq)
+    ref = a.double() @ w.cuda().double().T
+    assert ((out.double() - ref).abs() <= (256 * gh.STEP + K // 256 * 2.0 ** -24 + 2.0 ** -24) * ref).all()
+
+
+def test_long_sums_of_weight_gradients(mq):
+    """The same over an expert's rows."""
+    R, K, N = 16384, 2048, 2048
+    g = torch.Generator().manual_seed(3)
+    a = (torch.rand(R, K, generator=g) + 0.5).to(F16).cuda()
+    dy = (torch.rand(R, N, generator=g) + 0.5).to(F16).cuda()
+    w = torch.zeros(1, N, K, dtype=F16, device="cuda")
+    _, dw = mq.moe_grouped_product_grad(dy, a, w, need_a=False, dw_dtype=F32)
+    clean(mq)
+    ref = dy.double().T @ a.double()
+    assert ((dw[0].double() - ref).abs() <= (256 * gh.STEP + R // 256 * 2.0 ** -24 + 2.0 ** -24) * ref).all()
+
+
 @pytest.mark.parametrize("counts,K,N", [([1], 4096, 512), ([700, 300], 512, 512), ([3, 1, 0, 2], 2048, 136)])
 def test_same_result_every_time(mq, counts, K, N):
     off = gh.offsets_of(counts).cuda()

@@ -51,7 +51,8 @@ __device__ __forceinline__ uint4 last_piece(const uint16_t* row, int q, int K) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// D steps of 32 k from piece q of two weight rows on, for NT times eight rows.
+// D steps of 32 k from piece q of two weight rows on, for NT times eight rows.  (The tensor
+// core's additions round towards zero: long sums are made of short ones.)
 template <bool BF16, int NT, int D>
 __device__ __forceinline__ void steps_of(float (&acc)[NT][4], const uint4* w0, const uint4* w1,
                                          const uint16_t* const (&a)[NT], const bool (&live)[NT], int q) {
@@ -61,14 +62,19 @@ __device__ __forceinline__ void steps_of(float (&acc)[NT][4], const uint4* w0, c
     v0[d] = __ldcs(w0 + q + d * 4);
     v1[d] = __ldcs(w1 + q + d * 4);
   }
+  float c[NT][4] = {};
 #pragma unroll
   for (int d = 0; d < D; ++d)
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const uint4 x = live[j] ? __ldg(reinterpret_cast<const uint4*>(a[j]) + q + d * 4) : make_uint4(0, 0, 0, 0);
-      mma16816<BF16>(acc[j], v0[d].x, v1[d].x, v0[d].y, v1[d].y, x.x, x.y);
-      mma16816<BF16>(acc[j], v0[d].z, v1[d].z, v0[d].w, v1[d].w, x.z, x.w);
+      mma16816<BF16>(c[j], v0[d].x, v1[d].x, v0[d].y, v1[d].y, x.x, x.y);
+      mma16816<BF16>(c[j], v0[d].z, v1[d].z, v0[d].w, v1[d].w, x.z, x.w);
     }
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] += c[j][i];
 }
 
 // Grid: (outputs, rows).  The CTAs of a row that is its expert's first take all of that
