@@ -537,7 +537,8 @@ int moe_grouped_product(const void* a, int64_t a_stride, int dtype, int64_t R, i
  * da dense [R, K] in dtype, or NULL (w is then not read and may be NULL); dw dense
  * [E, N, K], or [E, K, N] with w_transposed, in dw_dtype, or NULL (a may then be NULL).
  * Rows of no expert are not read, whatever they hold.  Other arguments, limits,
- * arithmetic and errors as moe_grouped_product.
+ * arithmetic and errors as moe_grouped_product.  da and dw share no memory with each
+ * other or the inputs.
  */
 size_t moe_grouped_product_grad_workspace(int64_t R, int K, int N, int E);
 int moe_grouped_product_grad(const void* dy, int64_t dy_stride, const void* a, int64_t a_stride,

@@ -355,6 +355,29 @@ def test_training_step_in_a_graph(mq):
     gh.check(da, *gh.product64(gy.cpu(), w.detach().cpu().transpose(1, 2), off.cpu()), 72, "da")
 
 
+def test_operands_and_results_side_by_side_in_one_allocation(mq):
+    """Results that begin where an input ends, and the other way round."""
+    R, K, N, E = 64, 64, 128, 2
+    buf = torch.zeros(R * N + R * K + E * N * K + R * N + R * K + E * N * K, dtype=BF16, device="cuda")
+    parts, at = [], 0
+    for shape in ((R, N), (R, K), (E, N, K), (R, N), (R, K), (E, N, K)):
+        n = torch.Size(shape).numel()
+        parts.append(buf[at:at + n].view(shape))
+        at += n
+    out, a, w, dy, da, dw = parts
+    for t, seed in ((a, 1), (w, 2), (dy, 3)):
+        t.copy_(gh.randn(*t.shape, seed=seed, dtype=BF16))
+    off = gh.offsets_of([24, 40])
+    mq.moe_grouped_product(a, w, off.cuda(), out=out)
+    mq.moe_grouped_product_grad(dy, a, w, off.cuda(), da=da, dw=dw)
+    clean(mq)
+    gh.check(out, *gh.product64(a.cpu(), w.cpu(), off), K, "out")
+    gh.check(da, *gh.product64(dy.cpu(), w.cpu().transpose(1, 2), off), N, "da")
+    gh.check(dw, *gh.weights_grad64(dy.cpu(), a.cpu(), off, E), 40, "dw")
+    with pytest.raises(mq.MoeqError, match="share"):
+        mq.moe_grouped_product(a, w, off.cuda(), out=buf[R * N - 64:2 * R * N - 64].view(R, N))
+
+
 def test_call_from_a_new_thread(mq):
     """A thread whose first CUDA work is the call."""
     import threading

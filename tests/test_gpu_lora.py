@@ -106,6 +106,20 @@ def test_both_forms_are_tested(mq):
         assert mq.moe_lora_product_workspace(R, K, N, r, L) > 0
 
 
+@pytest.mark.parametrize("R", [1, 3, 17, 129])
+@pytest.mark.parametrize("r", [96, 128])
+def test_few_rows_of_high_rank(mq, R, r):
+    """Tiles that are mostly empty."""
+    K, N = 4096, 4104
+    assert r == 96 or mq.moe_lora_product_workspace(R, K, N, r, 5) > 0
+    for ids in (mixed, runs(2), [0] * R):
+        for dtype, out_dtype in ((BF16, BF16), (F16, F32)):
+            c = Case(R, K, N, r, 5, ids, dtype=dtype, out_dtype=out_dtype, seed=R)
+            got = c.call(mq)
+            clean(mq)
+            c.check(got)
+
+
 @pytest.mark.parametrize("r,L", [(128, 40), (64, 100), (16, 300)])
 def test_many_large_adapters_on_few_tiles(mq, r, L):
     """Few rows whose adapters are large: a tile's groups are divided among CTAs."""

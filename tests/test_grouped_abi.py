@@ -72,6 +72,35 @@ def test_gradient_refusals(lib):
     assert g(R=4096, N=64, E=1, dst=64, nb=need - 1, wk=P) == 4
 
 
+def test_product_and_gradients_share_no_memory_with_their_inputs(lib):
+    """Results on top of an input, or ending or beginning inside one (no workspace is needed)."""
+    R, K, N, E = 64, 64, 128, 8
+    A, W, OFF, Y, DA, DW = (vp(0x1000000 * i) for i in range(1, 7))
+    sizes = {"a": 2 * R * K, "w": 2 * E * N * K, "off": 4 * (E + 1), "dy": 2 * R * N}
+
+    def product(out, transposed=0, a_stride=K):
+        rc = lib.moe_grouped_product(A, a_stride, BF16, R, K, N, E, W, N if transposed else K, N * K, transposed, OFF,
+                                     out, BF16, None, 0, None)
+        return rc == 1 and b"share" in lib.mq_last_error_message()
+    assert lib.moe_grouped_product_workspace(R, K, N, E) == 0
+
+    def grad(da, dw):
+        rc = lib.moe_grouped_product_grad(Y, N, A, K, BF16, R, K, N, E, W, K, N * K, 0, OFF, da, dw, F32, P,
+                                          1 << 40, None)
+        return rc == 1 and b"share" in lib.mq_last_error_message()
+    out, da, dw = 2 * R * N, 2 * R * K, 4 * E * N * K
+    for name, at in (("a", A), ("w", W), ("off", OFF)):
+        for t in (0, 1):
+            assert product(at, t) and product(vp(at.value + sizes[name] // 16 * 16 - 16), t), name
+            assert product(vp(at.value - out + 16), t), name
+    assert product(vp(A.value + 2 * (R - 1) * 1024 + 2 * K - 16), a_stride=1024)
+    for name, at in (("a", A), ("w", W), ("off", OFF), ("dy", Y)):
+        for place in (at.value, at.value + sizes[name] // 16 * 16 - 16):
+            assert grad(vp(place), DW) and grad(DA, vp(place)), name
+        assert grad(vp(at.value - da + 16), DW) and grad(DA, vp(at.value - dw + 16)), name
+    assert grad(DA, DA) and grad(DA, vp(DA.value + da - 16)) and grad(vp(DW.value + dw - 16), DW)
+
+
 def test_lora_refusals(lib):
     far, farther = vp(0x10000000), vp(0x20000000)
 
@@ -98,6 +127,13 @@ def test_lora_refusals(lib):
     assert need > 0
     for wk, nb in ((None, 0), (P, need - 1), (None, need)):
         assert q(R=2000, wk=wk, nb=nb) == 4
+    for k, size in (("a", 2 * 3 * 2 * 16 * 64), ("b", 2 * 3 * 2 * 16 * 72), ("ids", 4 * 4), ("off", 4 * 3), ("sc", 4 * 3)):
+        for place in (farther, vp(farther.value + 2 * 4 * 72 - 16), vp(farther.value - size // 16 * 16)):
+            if place.value < farther.value and size % 16:
+                place = vp(farther.value - size + 4)    # its last element is out's first
+            elif place.value < farther.value:
+                place = vp(place.value + 16) if k in ("a", "b") else vp(place.value + 4)
+            assert q(**{k: place}) == 1 and b"share" in lib.mq_last_error_message(), (k, place)
     assert q(R=2000, wk=ODD, nb=need) == 1
     w = lib.moe_lora_product_workspace
     assert w(-1, 64, 72, 16, 3, 2) == 0 and w(0, 64, 72, 16, 3, 2) == 0 and w(2000, 60, 72, 16, 3, 2) == 0

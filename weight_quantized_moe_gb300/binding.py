@@ -624,7 +624,9 @@ def moe_grouped_product(a, w, expert_offsets=None, out=None, out_dtype=None, wor
 
     Where a or w requires a gradient the call is recorded for autograd
     (moe_grouped_product_grad is its backward pass); out cannot be given then.  The
-    gradient of a float32 result is rounded to a's dtype before the products."""
+    gradient of a float32 result is rounded to a's dtype before the products.  As with any
+    operator under autograd, capture a backward pass into a graph only while no result that was
+    recorded outside the capture from the same a or w lives."""
     if torch.is_grad_enabled() and (getattr(a, "requires_grad", False)
                                     or getattr(w, "requires_grad", False)):
         if out is not None:

@@ -980,14 +980,20 @@ MQ_EXPORT size_t moe_grouped_product_grad_workspace(int64_t R, int K, int N, int
                    gg_part_bytes(GG_ROWS, R, E, K, N, 0)});
 }
 
-// One product: the kernel, and the sum of its splits.
-static int gg_run(GgGemm g, void* workspace, size_t ws_bytes, cudaStream_t st) {
-  const GgPlan pl = gg_plan(g.form, g.R, g.E, g.M, g.N, g.K);
+static int gg_workspace(const GgGemm& g, const void* workspace, size_t ws_bytes) {
   const size_t need = gg_part_bytes(g.form, g.R, g.E, g.M, g.N, g.K);
   if (need && (!workspace || ws_bytes < need))
     return fail(MQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace ? ws_bytes : 0, need);
   if (need && !aligned16(workspace))
     return fail(MQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  return MQ_OK;
+}
+
+// One product: the kernel, and the sum of its splits.
+static int gg_run(GgGemm g, void* workspace, size_t ws_bytes, cudaStream_t st) {
+  const GgPlan pl = gg_plan(g.form, g.R, g.E, g.M, g.N, g.K);
+  const int ws = gg_workspace(g, workspace, ws_bytes);
+  if (ws != MQ_OK) return ws;
   g.part = static_cast<float*>(workspace);
   g.status = status_ptr();
   cudaError_t err;
@@ -1038,6 +1044,25 @@ static bool gg_map_strides(int64_t& row, int64_t rows, int64_t len, int64_t* exp
   return row < kTop && (!expert || *expert < kTop);
 }
 
+// The bytes from the first to the last one of an array (none where it is missing).
+struct Span {
+  uintptr_t lo, hi;
+  Span(const void* p, int64_t elements, int64_t size)
+      : lo(reinterpret_cast<uintptr_t>(p)), hi(p ? lo + (uintptr_t)(elements * size) : lo) {}
+  bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
+};
+
+static Span row_span(const void* p, int64_t R, int64_t stride, int64_t cols) {
+  return Span(p, (R - 1) * stride + cols, 2);
+}
+
+static Span weight_span(const void* w, int K, int N, int E, int64_t stride, int64_t expert, int transposed) {
+  const int64_t rows = transposed ? K : N, len = transposed ? N : K;
+  return Span(w, (E - 1) * expert + (rows - 1) * stride + len, 2);
+}
+
+static int64_t dtype_size(int dtype) { return dtype == MQ_DTYPE_F32 ? 4 : 2; }
+
 MQ_EXPORT int moe_grouped_product(const void* a, int64_t a_stride, int dtype, int64_t R, int K,
                                   int N, int E, const void* w, int64_t w_stride,
                                   int64_t w_expert_stride, int w_transposed,
@@ -1063,6 +1088,13 @@ MQ_EXPORT int moe_grouped_product(const void* a, int64_t a_stride, int dtype, in
   g.R = R; g.E = E; g.M = N; g.K = K;
   g.offsets = expert_offsets;
   g.out = out; g.out_dtype = out_dtype;
+  const int ws = gg_workspace(g, workspace, ws_bytes);
+  if (ws != MQ_OK) return ws;
+  const Span written(out, R * N, dtype_size(out_dtype));
+  if (written.meets(row_span(a, R, a_stride, K)) ||
+      written.meets(weight_span(w, K, N, E, w_stride, w_expert_stride, w_transposed)) ||
+      written.meets(Span(expert_offsets, E + 1, 4)))
+    return fail(MQ_ERR_INVALID_ARG, "out must not share memory with a, w or expert_offsets");
   return gg_run(g, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
@@ -1094,6 +1126,14 @@ MQ_EXPORT int moe_grouped_product_grad(const void* dy, int64_t dy_stride, const 
   const size_t need = moe_grouped_product_grad_workspace(R, K, N, E);
   if (need && (!workspace || ws_bytes < need))
     return fail(MQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace ? ws_bytes : 0, need);
+  const Span da_span(da, R * K, 2), dw_span(dw, (int64_t)E * N * K, dtype_size(dw_dtype));
+  const Span read[4] = {row_span(dy, R, dy_stride, N), row_span(dw ? a : nullptr, R, a_stride, K),
+                        weight_span(da ? w : nullptr, K, N, E, w_stride, w_expert_stride, w_transposed),
+                        Span(expert_offsets, E + 1, 4)};
+  for (const Span& in : read)
+    if (da_span.meets(in) || dw_span.meets(in))
+      return fail(MQ_ERR_INVALID_ARG, "da and dw must not share memory with dy, a, w or expert_offsets");
+  if (da_span.meets(dw_span)) return fail(MQ_ERR_INVALID_ARG, "da and dw must not share memory");
   GgGemm g = {};
   g.bf16 = dtype == MQ_DTYPE_BF16;
   g.R = R; g.E = E;
@@ -1190,6 +1230,12 @@ MQ_EXPORT int moe_lora_product(const void* x, int64_t x_stride, int dtype, int64
   if (need && (!workspace || ws_bytes < need))
     return fail(MQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace ? ws_bytes : 0, need);
   if (need && !aligned16(workspace)) return fail(MQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  const Span written(out, (R - 1) * out_stride + N, size);
+  const int64_t groups = (int64_t)L * E;
+  if (written.meets(Span(lora_a, groups * r * K, 2)) || written.meets(Span(lora_b, groups * r * N, 2)) ||
+      written.meets(Span(adapter_ids, R, 4)) || written.meets(Span(expert_offsets, E + 1, 4)) ||
+      written.meets(Span(scaling, L, 4)))
+    return fail(MQ_ERR_INVALID_ARG, "out must not share memory with the adapters, their ids, scaling or expert_offsets");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   LoraArgs g = {};
   g.bf16 = dtype == MQ_DTYPE_BF16;
