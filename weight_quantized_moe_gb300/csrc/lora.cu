@@ -236,12 +236,16 @@ struct Table {
   int inside;                      // rows that are written
 };
 
-// What the second launch needs of it, in global memory.  A group's accumulator has
-// columns for the blocks from its first row to its last.  Groups whose ranges do not
-// meet share one: each has a color, and colors 2 i and 2 i + 1 are round i.
+// What the second launch needs of it, in global memory.  It has the tile's rows in the
+// order of their groups (then those without an adapter, then those that are not
+// written): a row's place.  A group's accumulator has columns for the 16-row blocks of
+// its places.  Groups whose blocks do not meet share one: each has a color, and colors 2 i
+// and 2 i + 1 are round i.  (In the order that the rows come in, a group's range would reach
+// from its first row to its last: 16 groups at random in a tile took 3.6 rounds, so 2.)
 struct TileTable {
-  alignas(16) uint8_t color[kTile];  // color of a row's group; kNone, kOut
-  float row_scale[kTile];            // 2^m of each row
+  alignas(16) uint8_t color[kTile];  // by place: color of the row's group; kNone, kOut
+  alignas(16) uint8_t row[kTile];    // by place: the row
+  float row_scale[kTile];            // by place: 2^m of the row
   int group_key[kTile];              // by round
   int group_range[kTile];            // first block | behind its last << 8 | color << 16
   int round_start[kTile / 2 + 4];    // first group of a round
@@ -325,14 +329,63 @@ __device__ __forceinline__ void build_table(Table& tb, const LoraArgs& p, const 
   __syncthreads();
 }
 
+// A tile's rows in the order of their groups.
+struct Places {
+  int begin[kTile + 2];    // first place of a group, of rows without an adapter (kTile), of others
+  int fill[kTile + 2];     // while they are worked out: rows of each so far
+  uint8_t of_row[kTile];
+  uint8_t color[kTile];    // of a group
+};
+
+__device__ __forceinline__ int place_class(int slot) {
+  return slot == kNone ? kTile : slot == kOut ? kTile + 1 : slot;
+}
+
+// By one warp.
+__device__ __forceinline__ void sort_rows(Places& pl, const Table& tb, int lane) {
+  constexpr int kClasses = kTile + 2;
+  for (int i = lane; i < kClasses; i += 32) pl.fill[i] = 0;
+  __syncwarp();
+  unsigned peers[kTile / 32];
+  int cls[kTile / 32], before[kTile / 32];
+#pragma unroll
+  for (int q = 0; q < kTile / 32; ++q) {
+    cls[q] = place_class(tb.slot[q * 32 + lane]);
+    peers[q] = __match_any_sync(0xffffffffu, cls[q]);
+    const int rank = __popc(peers[q] & ((1u << lane) - 1u));
+    const int so_far = pl.fill[cls[q]];
+    before[q] = so_far + rank;
+    __syncwarp();
+    if (rank == 0) pl.fill[cls[q]] = so_far + __popc(peers[q]);
+    __syncwarp();
+  }
+  int carry = 0;
+  for (int i0 = 0; i0 < kClasses; i0 += 32) {
+    const int n = i0 + lane < kClasses ? pl.fill[i0 + lane] : 0;
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (i0 + lane < kClasses) pl.begin[i0 + lane] = carry + sum - n;
+    carry += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < kTile / 32; ++q) pl.of_row[q * 32 + lane] = (uint8_t)(pl.begin[cls[q]] + before[q]);
+  __syncwarp();
+}
+
 // The second launch's table of a tile, by one warp: colors in the order of the groups,
-// each the least that no group of a meeting range has.  `color`: kTile bytes.
-__device__ __forceinline__ void write_table(TileTable* to, const Table& tb, uint8_t* color, int lane) {
+// each the least that no group of a meeting range has.
+__device__ __forceinline__ void write_table(TileTable* to, const Table& tb, Places& pl, int lane) {
+  auto first_block = [&](int g) { return pl.begin[g] >> 4; };
+  auto end_block = [&](int g) { return (pl.begin[g] + pl.fill[g] + 15) >> 4; };
   unsigned used[4] = {};  // blocks taken, of colors lane, lane + 32, ...
   int colors = 0;
   for (int g = 0; g < tb.groups; ++g) {
-    const int b0 = __ffs(tb.blocks[g]) - 1, b1 = 32 - __clz(tb.blocks[g]);
-    const unsigned range = (1u << b1) - (1u << b0);
+    const unsigned range = (1u << end_block(g)) - (1u << first_block(g));
     bool placed = false;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -341,7 +394,7 @@ __device__ __forceinline__ void write_table(TileTable* to, const Table& tb, uint
       if (!free) continue;
       const int l = __ffs(free) - 1;
       if (lane == l) used[q] |= range;
-      if (lane == 0) color[g] = (uint8_t)(q * 32 + l);
+      if (lane == 0) pl.color[g] = (uint8_t)(q * 32 + l);
       colors = max(colors, q * 32 + l + 1);
       placed = true;
     }
@@ -354,19 +407,20 @@ __device__ __forceinline__ void write_table(TileTable* to, const Table& tb, uint
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int g = q * 32 + lane;
-      const bool here = g < tb.groups && color[g] >> 1 == rd;
+      const bool here = g < tb.groups && pl.color[g] >> 1 == rd;
       const unsigned all = __ballot_sync(0xffffffffu, here);
       if (here) {
         const int at = n + __popc(all & ((1u << lane) - 1u));
         to->group_key[at] = tb.group_key[g];
-        to->group_range[at] = (__ffs(tb.blocks[g]) - 1) | (32 - __clz(tb.blocks[g])) << 8 | color[g] << 16;
+        to->group_range[at] = first_block(g) | end_block(g) << 8 | pl.color[g] << 16;
       }
       n += __popc(all);
     }
   }
   for (int t = lane; t < kTile; t += 32) {
-    const int s = tb.slot[t];
-    to->color[t] = s < kOut ? color[s] : (uint8_t)s;
+    const int s = tb.slot[t], place = pl.of_row[t];
+    to->row[place] = (uint8_t)t;
+    to->color[place] = s < kOut ? pl.color[s] : (uint8_t)s;
   }
   if (lane == 0) {
     to->round_start[rounds] = n;
@@ -424,7 +478,7 @@ struct DownShared {
   DownCtl ctl;
   Table table;
   int offsets[kMaxE + 1];
-  uint8_t color[kTile];
+  Places places;
 };
 // floats between the rows of h in shared memory
 __host__ __device__ constexpr int h_pitch(int rp) { return rp + 4; }
@@ -437,7 +491,7 @@ struct DownShape {
   int splits;  // K splits: CTAs of a cluster
   int mparts;  // clusters among which a tile's accumulators are divided
   TileTable* tables;
-  uint16_t* h;  // [tiles * height][h_row(rp)]
+  uint16_t* h;  // [tiles * height][h_row(rp)], a tile's rows by place
 };
 
 __global__ void __launch_bounds__(kDownThreads, 1)
@@ -579,7 +633,8 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     if (el) mma_commit(&ctl->drain);
     wait_drain(&ctl->drain, 0);
   } else if (warp == 3) {
-    if (split == 0 && mpart == 0) write_table(d.tables + tile, tb, sh->color, lane);
+    sort_rows(sh->places, tb, lane);
+    if (split == 0 && mpart == 0) write_table(d.tables + tile, tb, sh->places, lane);
   } else {
     // A lane is one rank of one of the accumulator's groups.
     const int quad = warp & 3;
@@ -649,8 +704,9 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     // 2^m with m the exponent of the largest, kept to where 2^m and 2^-m are normal
     const int e = min(max((int)(__float_as_uint(most) >> 23), 1), 253);
     const float up = __uint_as_float((uint32_t)e << 23), down = __uint_as_float((uint32_t)(254 - e) << 23);
-    if (sub == 0) d.tables[tile].row_scale[t] = up;
-    uint16_t* dst = d.h + (row0 + t) * h_row(d.rp);
+    const int place = sh->places.of_row[t];
+    if (sub == 0) d.tables[tile].row_scale[place] = up;
+    uint16_t* dst = d.h + (row0 + place) * h_row(d.rp);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int j = q * 32 + sub * 4;
@@ -714,39 +770,26 @@ __device__ __forceinline__ uint32_t io_offset(int t, int c) {
   return (uint32_t)((c >> 3) * (kIoBytes / 2) + t * 128 + (((c & 7) ^ (t & 7)) << 4));
 }
 
-// The 32 outputs of a quarter's lanes for eight rows from t0 on: the fragments v (of 16
-// columns, half c) scaled by the rows' 2^m and added to what is in shared memory, one
-// rounding, for the rows of the round.  The two rows that this thread has of each
-// fragment: whether they are of the round, and their scales.  Whole 16-byte chunks move
-// either way: two-byte accesses, 32 a warp, bound this loop.
+// Two outputs of a row pair, m from memory and the sums a and b of the rows' scales: one
+// rounding, where `in` has the rows' bits.
 template <bool BF16>
-__device__ __forceinline__ void add_rows8(uint32_t io, int quad, int t0, const uint32_t (&v)[2][8], int c,
-                                          bool in0, bool in1, float2 scale, bool add, int lane) {
-  const uint32_t addr = io + io_offset(t0 + (lane & 7), quad * 4 + (lane >> 3));
-  uint32_t m[4];
-  ldmatrix_x4_trans(addr, m);
-  const uint32_t keep = (in0 ? 0u : 0xffffu) | (in1 ? 0u : 0xffff0000u);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int r = 4 * c + 2 * (k & 1);
-    float lo = 0, hi = 0;
-    if (add) {
-      lo = from_half_bits((uint16_t)(m[k] & 0xffffu), BF16);
-      hi = from_half_bits((uint16_t)(m[k] >> 16), BF16);
-    }
-    lo = fmaf(__uint_as_float(v[k >> 1][r]), scale.x, lo);
-    hi = fmaf(__uint_as_float(v[k >> 1][r + 1]), scale.y, hi);
-    uint32_t q;
-    if constexpr (BF16) {
-      const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-      q = *reinterpret_cast<const uint32_t*>(&t);
-    } else {
-      const __half2 t = __floats2half2_rn(lo, hi);
-      q = *reinterpret_cast<const uint32_t*>(&t);
-    }
-    m[k] = (m[k] & keep) | (q & ~keep);
+__device__ __forceinline__ uint32_t add_pair(uint32_t m, uint32_t a, uint32_t b, float2 scale, bool add, uint32_t in) {
+  float lo = 0, hi = 0;
+  if (add) {
+    lo = from_half_bits((uint16_t)(m & 0xffffu), BF16);
+    hi = BF16 ? __uint_as_float(m & 0xffff0000u) : from_half_bits((uint16_t)(m >> 16), BF16);
   }
-  stmatrix_x4_trans(addr, m);
+  lo = fmaf(__uint_as_float(a), scale.x, lo);
+  hi = fmaf(__uint_as_float(b), scale.y, hi);
+  uint32_t q;
+  if constexpr (BF16) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+    q = *reinterpret_cast<const uint32_t*>(&t);
+  } else {
+    const __half2 t = __floats2half2_rn(lo, hi);
+    q = *reinterpret_cast<const uint32_t*>(&t);
+  }
+  return (m & ~in) | (q & in);
 }
 
 // 0xff in the bytes of v that, halved, are `rd`.
@@ -987,8 +1030,9 @@ __global__ void __launch_bounds__(kUpThreads, 1)
               const bool write = color == kNone ? part == 0 && p.base != p.out
                                                 : color != kOut && color >> 1 >= r0 && color >> 1 < r1;
               if (!write || lane * 4 >= live) continue;
-              const uint2 q = *reinterpret_cast<const uint2*>(io + s * kIoBytes + io_offset(t, lane >> 1) + (lane & 1) * 8);
-              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((int64_t)row0 + t) * p.out_stride +
+              const int row = tb.row[t];
+              const uint2 q = *reinterpret_cast<const uint2*>(io + s * kIoBytes + io_offset(row, lane >> 1) + (lane & 1) * 8);
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((int64_t)row0 + row) * p.out_stride +
                                         n0 + lane * 4) = q;
             }
           }
@@ -1003,7 +1047,21 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     constexpr int kParts = kUpEpi / 4;
     const int quad = warp & 3, sub = (warp - 4) >> 2;  // lanes, and which blocks of 16 rows
     Ring ar, io_r;
-    if (warp_wait(&ctl->tile_full, 0, ctl, p.status))
+    const bool ready = warp_wait(&ctl->tile_full, 0, ctl, p.status);
+    // By this warp's blocks of 16 places: the rows of places lane % 8 (a byte each) and
+    // eight on, and the colors of the four places of which this lane has sums.
+    constexpr int kBlocks = kTile / 16 / kParts;
+    static_assert(kBlocks == 4, "a byte each, two blocks at a time");
+    uint32_t rows0 = 0, rows1 = 0, own[kBlocks];
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      const int at = (sub + i * kParts) * 16;
+      rows0 |= (uint32_t)tb.row[at + (lane & 7)] << i * 8;
+      rows1 |= (uint32_t)tb.row[at + 8 + (lane & 7)] << i * 8;
+      const uint16_t* pair = reinterpret_cast<const uint16_t*>(tb.color + at);
+      own[i] = pair[lane & 3] | (uint32_t)pair[4 + (lane & 3)] << 16;
+    }
+    if (ready)
       walk([&](int n0, int part) {
           const int n = n0 + quad * 32 + lane;
           const uint32_t buf = smem_addr(io) + io_r.slot * kIoBytes;
@@ -1013,38 +1071,72 @@ __global__ void __launch_bounds__(kUpThreads, 1)
             if (!warp_wait(&ctl->acc_full[ar.slot], ar.turn, ctl, p.status)) return false;
             tc_fence_after();
             const uint32_t acc = tmem + ar.slot * 2 * kTile + ((uint32_t)(quad * 32) << 16);
-            for (int c = sub; c < kTile / 16; c += kParts) {
-              const uint4 color = *reinterpret_cast<const uint4*>(tb.color + c * 16);
-              const uint4 in = rows_of_round(color, rd);
-              if (!(in.x | in.y | in.z | in.w)) continue;
-              const uint4 odd = make_uint4(in.x & color.x, in.y & color.y, in.z & color.z, in.w & color.w);
-              const bool two = (odd.x | odd.y | odd.z | odd.w) & 0x01010101u;  // some of the second color
-              if (u.nio) {
-                uint32_t v[2][8], w[2][8];
-                tmem_ld_frag16_sync(acc + c * 16, v);
-                if (two) tmem_ld_frag16_sync(acc + kTile + c * 16, w);
+            if (u.nio) {
+              // Whole 16-byte chunks of a row move either way (two-byte accesses, 32 a warp,
+              // bound this loop), for two blocks at a time.
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {  // rows 8 h + 2 (lane % 4) and the next
-                  const uint32_t half_in = lane & 2 ? (h ? in.w : in.y) : (h ? in.z : in.x);
-                  const uint32_t half_odd = lane & 2 ? (h ? odd.w : odd.y) : (h ? odd.z : odd.x);
-                  const int shift = (lane & 1) * 16;
-                  if (two) {
-                    const bool o0 = half_odd >> shift & 1, o1 = half_odd >> shift & 0x100;
+              for (int i0 = 0; i0 < kBlocks; i0 += 2) {
+                uint32_t in[2], odd[2];
+                bool any[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                  in[b] = __vcmpeq4(own[i0 + b] >> 1 & 0x7f7f7f7fu, (uint32_t)rd * 0x01010101u);
+                  odd[b] = in[b] & own[i0 + b] & 0x01010101u;  // of the second color
+                  any[b] = __any_sync(0xffffffffu, in[b]);
+                }
+                if (!any[0] && !any[1]) continue;
+                uint32_t at[2][2], m[2][2][4];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    at[b][h] = buf + io_offset((h ? rows1 : rows0) >> (i0 + b) * 8 & 0xff, quad * 4 + (lane >> 3));
+                    ldmatrix_x4_trans(at[b][h], m[b][h]);
+                  }
+                const uint32_t c0 = acc + (sub + i0 * kParts) * 16, c1 = c0 + kParts * 16;
+                uint32_t v[2][2][8];
+                tmem_ld_frag16_sync(c0, c1, v);
+                if (__any_sync(0xffffffffu, odd[0] | odd[1])) {
+                  uint32_t w[2][2][8];
+                  tmem_ld_frag16_sync(c0 + kTile, c1 + kTile, w);
+#pragma unroll
+                  for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                      for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {  // rows 2 (lane % 4) + e % 2 of the eight
+                          uint32_t& x = v[b][k][4 * h + e];
+                          x = odd[b] >> (16 * h + 8 * (e & 1)) & 1 ? w[b][k][4 * h + e] : x;
+                        }
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                  if (!any[b]) continue;
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const float2 scale = *reinterpret_cast<const float2*>(
+                        tb.row_scale + (sub + (i0 + b) * kParts) * 16 + h * 8 + 2 * (lane & 3));
+                    const uint32_t mask = __byte_perm(in[b], 0, h ? 0x3322 : 0x1100);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                      const int r = 4 * h + 2 * (k & 1);
-                      v[k >> 1][r] = o0 ? w[k >> 1][r] : v[k >> 1][r];
-                      v[k >> 1][r + 1] = o1 ? w[k >> 1][r + 1] : v[k >> 1][r + 1];
+                      const int e = 4 * h + 2 * (k & 1);
+                      m[b][h][k] = add_pair<BF16>(m[b][h][k], v[b][k >> 1][e], v[b][k >> 1][e + 1], scale, add, mask);
                     }
+                    stmatrix_x4_trans(at[b][h], m[b][h]);
                   }
-                  const int t0 = c * 16 + h * 8;
-                  add_rows8<BF16>(buf, quad, t0, v, h, half_in >> shift & 1, half_in >> shift & 0x100,
-                                  *reinterpret_cast<const float2*>(tb.row_scale + t0 + 2 * (lane & 3)), add, lane);
                 }
-              } else {
+              }
+            } else {
+              for (int c = sub; c < kTile / 16; c += kParts) {
+                const uint4 color = *reinterpret_cast<const uint4*>(tb.color + c * 16);
+                const uint4 in = rows_of_round(color, rd);
+                if (!(in.x | in.y | in.z | in.w)) continue;
+                const uint4 odd = make_uint4(in.x & color.x, in.y & color.y, in.z & color.z, in.w & color.w);
                 uint32_t v[16];
                 tmem_ld16_sync(acc + c * 16, v);
-                if (two) {
+                if ((odd.x | odd.y | odd.z | odd.w) & 0x01010101u) {  // some of the second color
                   uint32_t w[16];
                   tmem_ld16_sync(acc + kTile + c * 16, w);
 #pragma unroll
@@ -1052,14 +1144,14 @@ __global__ void __launch_bounds__(kUpThreads, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                  const int t = c * 16 + i;
                   if (!byte_of(in, i) || n >= p.N) continue;
-                  const float o = add ? load_as(p.base, p.out_dtype, ((int64_t)row0 + t) * p.base_stride + n) : 0.0f;
-                  store_out(p.out, p.out_dtype, ((int64_t)row0 + t) * p.out_stride + n,
-                            fmaf(__uint_as_float(v[i]), tb.row_scale[t], o));
+                  const int64_t row = (int64_t)row0 + tb.row[c * 16 + i];
+                  const float o = add ? load_as(p.base, p.out_dtype, row * p.base_stride + n) : 0.0f;
+                  store_out(p.out, p.out_dtype, row * p.out_stride + n,
+                            fmaf(__uint_as_float(v[i]), tb.row_scale[c * 16 + i], o));
                 }
+                __syncwarp();
               }
-              __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
@@ -1073,7 +1165,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
               for (int c = sub; c < kTile / 16; c += kParts)
                 for (int t = c * 16; t < c * 16 + 16; ++t)
                   if (tb.color[t] == kNone && lane < 4)
-                    *reinterpret_cast<uint4*>(io + io_r.slot * kIoBytes + io_offset(t, quad * 4 + lane)) =
+                    *reinterpret_cast<uint4*>(io + io_r.slot * kIoBytes + io_offset(tb.row[t], quad * 4 + lane)) =
                         make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
@@ -1081,9 +1173,10 @@ __global__ void __launch_bounds__(kUpThreads, 1)
             io_r.next(u.nio);
           } else if (part == 0 && p.base != p.out) {
             for (int t = sub; t < tb.rows; t += kParts)
-              if (tb.color[t] == kNone && n < p.N)
-                copy_element(p.out, ((int64_t)row0 + t) * p.out_stride + n, p.base, ((int64_t)row0 + t) * p.base_stride + n,
-                             p.out_dtype);
+              if (tb.color[t] == kNone && n < p.N) {
+                const int64_t row = (int64_t)row0 + tb.row[t];
+                copy_element(p.out, row * p.out_stride + n, p.base, row * p.base_stride + n, p.out_dtype);
+              }
           }
           __syncwarp();
           return true;

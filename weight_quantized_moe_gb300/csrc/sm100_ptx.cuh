@@ -447,6 +447,25 @@ __device__ __forceinline__ void tmem_ld_frag16_sync(uint32_t taddr, uint32_t (&v
       : "memory");
 }
 
+// Two of them, with one wait.
+__device__ __forceinline__ void tmem_ld_frag16_sync(uint32_t t0, uint32_t t1, uint32_t (&v)[2][2][8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%33];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%34];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%35];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0][0][0]), "=r"(v[0][0][1]), "=r"(v[0][0][2]), "=r"(v[0][0][3]), "=r"(v[0][0][4]),
+        "=r"(v[0][0][5]), "=r"(v[0][0][6]), "=r"(v[0][0][7]), "=r"(v[0][1][0]), "=r"(v[0][1][1]),
+        "=r"(v[0][1][2]), "=r"(v[0][1][3]), "=r"(v[0][1][4]), "=r"(v[0][1][5]), "=r"(v[0][1][6]),
+        "=r"(v[0][1][7]), "=r"(v[1][0][0]), "=r"(v[1][0][1]), "=r"(v[1][0][2]), "=r"(v[1][0][3]),
+        "=r"(v[1][0][4]), "=r"(v[1][0][5]), "=r"(v[1][0][6]), "=r"(v[1][0][7]), "=r"(v[1][1][0]),
+        "=r"(v[1][1][1]), "=r"(v[1][1][2]), "=r"(v[1][1][3]), "=r"(v[1][1][4]), "=r"(v[1][1][5]),
+        "=r"(v[1][1][6]), "=r"(v[1][1][7])
+      : "r"(t0), "r"(t0 + (16u << 16)), "r"(t1), "r"(t1 + (16u << 16))
+      : "memory");
+}
+
 // Four 8 x 8 blocks of 16-bit values, transposed: thread t gives the address of row t %
 // 8 (16 bytes) of block t / 8, and has of each block the elements [2 (t % 4) + i][t / 4]
 // in one register, i = 0 in its low half.
