@@ -13,8 +13,9 @@
 //          launches on tcgen05.  Rows are the columns of the accumulators, so that a
 //          column has one group whatever its neighbours have: every group of a tile is
 //          multiplied with all its columns and each column keeps its own group's sums.
-//          Nothing is sorted, gathered or masked, and what another request's adapter
-//          holds (infinities, NaN) stays in the columns that are not kept.
+//          Nothing is masked, and what another request's adapter holds (infinities,
+//          NaN) stays in the columns that are not kept.  x, base and out are never
+//          gathered; only h, between the launches, has a tile's rows by group.
 //
 // Tiles, first launch (lora_down): h = A x in float32.  Groups are packed into the 128
 // lanes of an accumulator (eight of rank 16, two of rank 64), x is the other operand; a
@@ -23,9 +24,15 @@
 // (hi + lo), m the exponent of the row's largest |h|: 16 bits of precision for bf16 and
 // 22 for f16, whose range it cannot leave either, for twice a small product.
 // Second launch (lora_up): a group's product has the columns of its own rows only, so
-// that groups whose rows lie apart share an accumulator and a tile of several requests
-// takes one turn of the epilogue.  base comes by TMA and goes back, with the sums added,
-// the same way.
+// that groups in different blocks of 16 rows share an accumulator and a tile of several
+// requests takes one turn of the epilogue, or a few.  base comes by TMA and goes back, with
+// the sums added, the same way.
+//
+// Measured: rows, 4096 x 4096, rank 16: 1 row 5.2 us, 64 rows of 48 adapters 7.0 (a chain of
+// dependent reads: ids, A, the exchange; B is on its way meanwhile).  Tiles: 4099 rows of 16
+// adapters, rank 64, 37 us (67 MB of base and out beside two launches' ways in and out);
+// 4096 rows of 64 experts, 2048 x 2816, rank 32, 16 groups in a tile, 68 us (an instruction
+// takes its time with 16 columns as with 128: four for each group and 128 outputs).
 #include "lora.cuh"
 #include "pipe.cuh"
 
@@ -1350,11 +1357,11 @@ LoraPlan lora_plan(int64_t R, int K, int N, int r, int L, int E) {
   // Rows or tiles, by their estimated times in us.  Rows: 64 at a time, each its adapter.
   // Tiles: the way through two launches, more with more groups in a tile; a mean over
   // adapters in runs and at random.  Measured, rows and tiles (at random / in runs), 4096 x
-  // 4096: rank 16, 48 adapters, 64 rows 6.1 and 25 / 26, 256 rows 22.6 and 31 / 19, 512 rows
-  // 48.6 and 52 / 22; of 4 adapters, 128 rows 11.0 and 21 / 22, 256 rows 20.7 and 15.9 /
+  // 4096: rank 16, 48 adapters, 64 rows 6.1 and 25 / 26, 256 rows 22.6 and 28 / 18, 512 rows
+  // 48.6 and 46 / 19; of 4 adapters, 128 rows 11.0 and 21 / 22, 256 rows 20.7 and 15.9 /
   // 14.7; rank 32, 128 rows 20.5 and 29 / 24, 192 rows 30.6 and 28 / 18; rank 64, 1 row 9.7
-  // and 13.0, 64 rows 16.7 and 22.7, 96 rows 35 and 33; rank 128, 1 row 17.0 and 14.0.  1024 x
-  // 1024, rank 8: 256 rows 16.3 and 27.5 / 23.5, 512 rows 30.8 and 31.7 / 23.5.
+  // and 13.0, 64 rows 16.7 and 22.7, 96 rows 35 and 27 / 25; rank 128, 1 row 17.0 and 14.0.
+  // 1024 x 1024, rank 8: 256 rows 16.3 and 27.5 / 23.5, 512 rows 30.8 and 31.7 / 23.5.
   const double waves = R / 64.0, many = std::max(1.0, waves);
   const double rows_us = 3 * many + 7 * adapter * 1e-6 * (many + waves);
   const double tiles_us = 13.5 + 0.15 * std::min(64.0, 4 * groups);
