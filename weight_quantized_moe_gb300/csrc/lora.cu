@@ -76,6 +76,16 @@ __device__ __forceinline__ float load_as(const void* p, int dtype, int64_t i) {
   return static_cast<const float*>(p)[i];
 }
 
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_float(float v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else if constexpr (std::is_same_v<T, __half>) return __float2half_rn(v);
+  else return __float2bfloat16_rn(v);
+}
+
 // out[i] = base[j], bit for bit; 0 where there is no base.
 __device__ __forceinline__ void copy_element(void* out, int64_t i, const void* base, int64_t j, int dtype) {
   if (dtype == MQ_DTYPE_F32)
@@ -806,6 +816,76 @@ __device__ __forceinline__ uint4 rows_of_round(const uint4& v, int rd) {
                     __vcmpeq4(v.z >> 1 & low, want), __vcmpeq4(v.w >> 1 & low, want));
 }
 
+// A round's sums of a lane's output n added to base where rows move element by element, for
+// the 16-row blocks of epilogue part `sub`.
+template <typename T>
+__device__ __forceinline__ void plain_blocks(const LoraArgs& p, const TileTable& tb, uint32_t acc, int rd, int sub,
+                                             int row0, int n) {
+  constexpr int kParts = kUpEpi / 4;
+  const T* base = static_cast<const T*>(p.base) + (int64_t)row0 * p.base_stride + n;
+  T* out = static_cast<T*>(p.out) + (int64_t)row0 * p.out_stride + n;
+#pragma unroll 1
+  for (int c0 = sub; c0 < kTile / 16; c0 += 2 * kParts) {
+    uint4 in[2];
+    uint32_t any = 0, second = 0;
+    float old[2][16];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const uint4 color = *reinterpret_cast<const uint4*>(tb.color + (c0 + b * kParts) * 16);
+      in[b] = rows_of_round(color, rd);
+      any |= in[b].x | in[b].y | in[b].z | in[b].w;
+      second |= in[b].x & color.x | in[b].y & color.y | in[b].z & color.z | in[b].w & color.w;
+    }
+    if (!any) continue;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        old[b][i] = 0.0f;
+        if (p.base && byte_of(in[b], i) && n < p.N)
+          old[b][i] = as_float(base[tb.row[(c0 + b * kParts) * 16 + i] * p.base_stride]);
+      }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int c = c0 + b * kParts;
+      uint32_t v[16];
+      __syncwarp();
+      tmem_ld16_sync(acc + c * 16, v);
+      if (second & 0x01010101u) {  // some of the second color
+        const uint4 color = *reinterpret_cast<const uint4*>(tb.color + c * 16);
+        uint32_t w[16];
+        tmem_ld16_sync(acc + kTile + c * 16, w);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = byte_of(color, i) & 1 ? w[i] : v[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (byte_of(in[b], i) && n < p.N)
+          out[tb.row[c * 16 + i] * p.out_stride] =
+              from_float<T>(fmaf(__uint_as_float(v[i]), tb.row_scale[c * 16 + i], old[b][i]));
+    }
+    __syncwarp();
+  }
+}
+
+// Rows without an adapter there: base as it is, or 0.
+template <typename T>
+__device__ __forceinline__ void plain_copies(const LoraArgs& p, const TileTable& tb, int sub, int row0, int n) {
+  const T* base = static_cast<const T*>(p.base) + (int64_t)row0 * p.base_stride + n;
+  T* out = static_cast<T*>(p.out) + (int64_t)row0 * p.out_stride + n;
+#pragma unroll 1
+  for (int c = sub; c < kTile / 16; c += kUpEpi / 4) {
+    const uint4 color = *reinterpret_cast<const uint4*>(tb.color + c * 16);
+    T v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      v[i] = p.base && byte_of(color, i) == kNone && n < p.N ? base[tb.row[c * 16 + i] * p.base_stride] : T(0.0f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (byte_of(color, i) == kNone && n < p.N) out[tb.row[c * 16 + i] * p.out_stride] = v[i];
+  }
+}
+
 template <bool BF16>  // out is bf16
 __global__ void __launch_bounds__(kUpThreads, 1)
     lora_up(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_h,
@@ -1136,29 +1216,10 @@ __global__ void __launch_bounds__(kUpThreads, 1)
                 }
               }
             } else {
-              for (int c = sub; c < kTile / 16; c += kParts) {
-                const uint4 color = *reinterpret_cast<const uint4*>(tb.color + c * 16);
-                const uint4 in = rows_of_round(color, rd);
-                if (!(in.x | in.y | in.z | in.w)) continue;
-                const uint4 odd = make_uint4(in.x & color.x, in.y & color.y, in.z & color.z, in.w & color.w);
-                uint32_t v[16];
-                tmem_ld16_sync(acc + c * 16, v);
-                if ((odd.x | odd.y | odd.z | odd.w) & 0x01010101u) {  // some of the second color
-                  uint32_t w[16];
-                  tmem_ld16_sync(acc + kTile + c * 16, w);
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) v[i] = byte_of(odd, i) & 1 ? w[i] : v[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  if (!byte_of(in, i) || n >= p.N) continue;
-                  const int64_t row = (int64_t)row0 + tb.row[c * 16 + i];
-                  const float o = add ? load_as(p.base, p.out_dtype, row * p.base_stride + n) : 0.0f;
-                  store_out(p.out, p.out_dtype, row * p.out_stride + n,
-                            fmaf(__uint_as_float(v[i]), tb.row_scale[c * 16 + i], o));
-                }
-                __syncwarp();
-              }
+              // Element by element, two blocks' reads in flight together.
+              if (p.out_dtype == MQ_DTYPE_F32) plain_blocks<float>(p, tb, acc, rd, sub, row0, n);
+              else if (p.out_dtype == MQ_DTYPE_BF16) plain_blocks<__nv_bfloat16>(p, tb, acc, rd, sub, row0, n);
+              else plain_blocks<__half>(p, tb, acc, rd, sub, row0, n);
             }
             tc_fence_before();
             __syncwarp();
@@ -1179,11 +1240,9 @@ __global__ void __launch_bounds__(kUpThreads, 1)
             if (lane == 0) mbar_arrive(&ctl->io_done[io_r.slot]);
             io_r.next(u.nio);
           } else if (part == 0 && p.base != p.out) {
-            for (int t = sub; t < tb.rows; t += kParts)
-              if (tb.color[t] == kNone && n < p.N) {
-                const int64_t row = (int64_t)row0 + tb.row[t];
-                copy_element(p.out, row * p.out_stride + n, p.base, row * p.base_stride + n, p.out_dtype);
-              }
+            if (p.out_dtype == MQ_DTYPE_F32) plain_copies<float>(p, tb, sub, row0, n);
+            else if (p.out_dtype == MQ_DTYPE_BF16) plain_copies<__nv_bfloat16>(p, tb, sub, row0, n);
+            else plain_copies<__half>(p, tb, sub, row0, n);
           }
           __syncwarp();
           return true;
