@@ -822,13 +822,13 @@ template <typename T>
 __device__ __forceinline__ void plain_blocks(const LoraArgs& p, const TileTable& tb, uint32_t acc, int rd, int sub,
                                              int row0, int n) {
   constexpr int kParts = kUpEpi / 4;
-  const T* base = static_cast<const T*>(p.base) + (int64_t)row0 * p.base_stride + n;
+  const T* base = static_cast<const T*>(p.base) + (int64_t)row0 * p.base_stride + min(n, p.N - 1);
   T* out = static_cast<T*>(p.out) + (int64_t)row0 * p.out_stride + n;
 #pragma unroll 1
   for (int c0 = sub; c0 < kTile / 16; c0 += 2 * kParts) {
     uint4 in[2];
     uint32_t any = 0, second = 0;
-    float old[2][16];
+    T old[2][16];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const uint4 color = *reinterpret_cast<const uint4*>(tb.color + (c0 + b * kParts) * 16);
@@ -841,9 +841,9 @@ __device__ __forceinline__ void plain_blocks(const LoraArgs& p, const TileTable&
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        old[b][i] = 0.0f;
-        if (p.base && byte_of(in[b], i) && n < p.N)
-          old[b][i] = as_float(base[tb.row[(c0 + b * kParts) * 16 + i] * p.base_stride]);
+        // (the tile's first row for those of other rounds: no branch holds the reads up)
+        const int row = byte_of(in[b], i) ? tb.row[(c0 + b * kParts) * 16 + i] : 0;
+        old[b][i] = p.base ? base[row * p.base_stride] : T(0.0f);
       }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -862,7 +862,7 @@ __device__ __forceinline__ void plain_blocks(const LoraArgs& p, const TileTable&
       for (int i = 0; i < 16; ++i)
         if (byte_of(in[b], i) && n < p.N)
           out[tb.row[c * 16 + i] * p.out_stride] =
-              from_float<T>(fmaf(__uint_as_float(v[i]), tb.row_scale[c * 16 + i], old[b][i]));
+              from_float<T>(fmaf(__uint_as_float(v[i]), tb.row_scale[c * 16 + i], as_float(old[b][i])));
     }
     __syncwarp();
   }
@@ -871,15 +871,17 @@ __device__ __forceinline__ void plain_blocks(const LoraArgs& p, const TileTable&
 // Rows without an adapter there: base as it is, or 0.
 template <typename T>
 __device__ __forceinline__ void plain_copies(const LoraArgs& p, const TileTable& tb, int sub, int row0, int n) {
-  const T* base = static_cast<const T*>(p.base) + (int64_t)row0 * p.base_stride + n;
+  const T* base = static_cast<const T*>(p.base) + (int64_t)row0 * p.base_stride + min(n, p.N - 1);
   T* out = static_cast<T*>(p.out) + (int64_t)row0 * p.out_stride + n;
 #pragma unroll 1
   for (int c = sub; c < kTile / 16; c += kUpEpi / 4) {
     const uint4 color = *reinterpret_cast<const uint4*>(tb.color + c * 16);
     T v[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      v[i] = p.base && byte_of(color, i) == kNone && n < p.N ? base[tb.row[c * 16 + i] * p.base_stride] : T(0.0f);
+    for (int i = 0; i < 16; ++i) {
+      const int row = byte_of(color, i) == kNone ? tb.row[c * 16 + i] : 0;
+      v[i] = p.base ? base[row * p.base_stride] : T(0.0f);
+    }
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if (byte_of(color, i) == kNone && n < p.N) out[tb.row[c * 16 + i] * p.out_stride] = v[i];
