@@ -750,8 +750,8 @@ GgPlan gg_plan(GgForm form, int64_t R, int E, int M, int N, int K) {
   // K splits while they leave a wave of units and eight stages each (us unsplit, with 2, 4 and
   // 8): 4096 x 4096, 17 rows 15.5, 11.9, 10.7, 11.9, 256 rows 25.0, 19.4, 16.4, 19.2, 1024 rows
   // 26.1, 32.8, 42.4, 65.7; 8 experts, 14336 x 1024, 128 rows 48.3, 40.3, 41.0, 43.5; 16
-  // experts, 2048 x 768, 128 rows 12.0, 14.6, 13.9, 14.9.
-  if (R > 1024) return pl;
+  // experts, 2048 x 768, 128 rows 12.0, 14.6, 13.9, 14.9.  (As good with many rows: 8192 x
+  // 512, 1500 rows 41.3 unsplit, 19.5 with two.)
   const double workers = pl.pair ? sms / 2 : sms;
   const double units = std::max(live, std::ceil((double)R / pl.bn)) * ((M + (pl.pair ? 255 : 127)) / (pl.pair ? 256 : 128));
   const int stages = (K + kStageK - 1) / kStageK;
@@ -850,15 +850,16 @@ cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
 // written at 6.6 and 3.8 TB/s, against the products at 1.5 PFLOP/s.  us one after the other
 // and side by side: 128 experts, 2048 x 1536, 4096 rows 277 and 273, 16384 rows 325 and 297,
 // 65536 rows 640 and 661; 8 experts, 4096 x 14336, 128 rows 335 and 316, 1024 rows 368 and
-// 330, 2048 rows 440 and 462, 4096 rows 697 and 712; 16 experts, 1408 x 2048, 517 rows 57
-// and 43.  (In between it depends on the loads' last chunks.)
+// 330, 1500 rows 357 and 337, 2048 rows 440 and 462, 4096 rows 697 and 712; 16 experts, 1408
+// x 2048, 517 rows 57 and 43; 2 experts, 12792 x 2448, 353 rows 83 and 66.  (About where the
+// products take as long, it depends on the loads' last chunks.)
 bool gg_side_by_side(const GgGemm& rows, const GgGemm& weights) {
   const int64_t n = (int64_t)rows.M * rows.K;
   const double live = (double)std::min<int64_t>(rows.R, rows.E);
   const double read = live * n * 2 / 6.6e6;
   const double write = (double)rows.E * n * (weights.out_dtype == MQ_DTYPE_F32 ? 4 : 2) / 3.8e6;
   const double flops = 4.0 * rows.R * n / 1.5e9;
-  return rows.M > 128 && rows.K > 128 && read + write > 2 * flops &&
+  return rows.M > 128 && rows.K > 128 && read + write > 1.3 * flops &&
          gg_plan(rows.form, rows.R, rows.E, rows.M, rows.N, rows.K).splits == 1 &&
          gg_plan(GG_ROWS, weights.R, weights.E, weights.M, weights.N, weights.K).splits == 1;
 }
