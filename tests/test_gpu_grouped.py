@@ -47,6 +47,8 @@ SHAPES = [
     ([255, 256, 257, 300], 1, 2, 192, 520),     # CTA pairs
     ([700], 0, 0, 2048, 256),                   # pairs, one expert
     ([40] * 24, 0, 0, 64, 96),
+    ([1500], 3, 2, 1024, 264),                  # many rows, K split
+    ([900, 0, 700], 1, 4, 2056, 136),
     ([0, 0, 0], 4, 4, 64, 64),                  # no rows at all
 ]
 
