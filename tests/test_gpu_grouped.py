@@ -47,6 +47,9 @@ SHAPES = [
     ([255, 256, 257, 300], 1, 2, 192, 520),     # CTA pairs
     ([700], 0, 0, 2048, 256),                   # pairs, one expert
     ([40] * 24, 0, 0, 64, 96),
+    ([1, 0, 0, 2, 0, 0, 0, 1], 1, 1, 264, 48),  # more experts than rows
+    ([3], 0, 0, 72, 8200),                      # few rows, more outputs than CTAs at a time
+    ([2, 0, 5], 1, 2, 296, 8200),
     ([1500], 3, 2, 1024, 264),                  # many rows, K split
     ([900, 0, 700], 1, 4, 2056, 136),
     ([0, 0, 0], 4, 4, 64, 64),                  # no rows at all

@@ -716,11 +716,20 @@ cudaError_t launch_form(const GgPlan& pl, const CUtensorMap& mw, const CUtensorM
 GgPlan gg_plan(GgForm form, int64_t R, int E, int M, int N, int K) {
   GgPlan pl = {};
   pl.splits = 1;
-  // Few rows and weights: one launch (grouped_few.cu).  us there and here, K x N and rows:
-  // 4096 x 4096 1 7.7 10.4, 8 8.0 10.4, 16 9.8 11.3; 2048 x 1536 1 3.5 7.2, 16 4.3 8.9;
-  // 4096 x 14336 (117 MB) 1 21.9 21.8, 8 27.2 21.8, 16 33.9 22.0.
-  pl.few = form == GG_W_K && R <= kFewRows &&
-           2.0 * std::min<int64_t>(R, E) * M * K <= 64e6;
+  // Few rows and weights: one launch (grouped_few.cu), where its estimated time is less: reads
+  // in chunks of 2048 k (1.3 us each, one after the other) for as many turns as the CTAs take,
+  // or the weights at 5.5 TB/s.  us there and here, K x N and rows: 4096 x 4096 1 7.8 10.2, 16
+  // 8.6 10.5; 2048 x 1536 1 4.1 7.2, 16 4.6 7.6; 4096 x 256 1 5.4 7.7; of 8 experts, 2048 x 768
+  // 4 5.2 7.8, 16 8.2 9.5; of 128, 768 x 2048 4 4.5 6.5, 16 14.0 10.0; of 13, 11096 x 79 1 11.4
+  // 9.1; 4096 x 14336 (117 MB) 1 21.9 21.8, 8 27.2 21.8.
+  if (form == GG_W_K && R <= kFewRows) {
+    const double groups = (double)std::min<int64_t>(R, E);
+    const double bytes = 2.0 * groups * M * K;
+    const double turns = std::ceil(std::ceil(M / 16.0) / std::max(1.0, std::floor(2 * tc_num_sms() / groups)));
+    const double chunks = std::ceil(K / 2048.0);
+    const double few_us = std::max(2 + turns * (0.3 + 1.3 * chunks), 2 + bytes / 5.5e6);
+    pl.few = bytes <= 64e6 && few_us <= 6.2 + bytes / 9e6;
+  }
   if (pl.few) return pl;
   const int sms = tc_num_sms();
   if (form == GG_ROWS) {
