@@ -880,12 +880,16 @@ cudaError_t launch_gg_both(const GgGemm& rows, const GgGemm& weights, cudaStream
   if (err == cudaSuccess) err = prepare(weights, pair, w);
   if (err != cudaSuccess) return err;
   // SMs by what a pair of them reads and writes (102 and 85 GB/s measured), within the
-  // shares that were tried (4096 rows, 128 experts, 1536 x 2048: 309, 274 and 296 us with
-  // 35, 45 and 55 %; 517 rows, 16 experts, float32: 53.9, 52.3 and 56.5)
+  // shares that were tried, and more for the rows' side where an expert has many.  us with 30,
+  // 35, 40, 45 and 50 % of them for it: 128 experts, 1536 x 2048, 4096 rows 340, 309, 287, 274,
+  // 272; float32: 87 experts, 12528 x 344, 284 rows 449, 484, 531, 586, 637; 8 experts, 4096 x
+  // 14336, 512 rows 491, 465, 480, 484, 533; 16 experts, 1408 x 2048, 517 rows 58, 54, 55, 56,
+  // 62; 128 experts, 2048 x 1536, 16384 rows 455, 428, 409, 436, 480.
   const double read = (double)std::min<int64_t>(rows.R, rows.E) * 2 / 102;
   const double write = (double)rows.E * (weights.out_dtype == MQ_DTYPE_F32 ? 4 : 2) / 85;
   const int pairs = tc_num_sms() / 2;
-  int first = (int)(pairs * std::min(0.5, std::max(0.4, read / (read + write))));
+  const double least = 0.3 + 0.1 * std::min(1.0, (double)rows.R / (128.0 * rows.E));
+  int first = (int)(pairs * std::min(0.5, std::max(least, read / (read + write) + 0.05)));
   first = (int)std::max<int64_t>(1, std::min<int64_t>(first, r.units));
   const int second = (int)std::max<int64_t>(1, std::min<int64_t>(pairs - first, w.units));
   constexpr size_t smem = std::max({Cfg<GG_W_K, 256, 2>::kSmem, Cfg<GG_ROWS, 256, 2>::kSmem});
