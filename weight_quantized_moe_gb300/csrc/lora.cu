@@ -31,8 +31,8 @@
 // Measured: rows, 4096 x 4096, rank 16: 1 row 5.2 us, 64 rows of 48 adapters 7.0 (a chain of
 // dependent reads: ids, A, the exchange; B is on its way meanwhile).  Tiles: 4099 rows of 16
 // adapters, rank 64, 37 us (67 MB of base and out beside two launches' ways in and out);
-// 4096 rows of 64 experts, 2048 x 2816, rank 32, 16 groups in a tile, 68 us (an instruction
-// takes its time with 16 columns as with 128: four for each group and 128 outputs).
+// 4096 rows of 64 experts, 2048 x 2816, rank 32, 16 groups in a tile, 68 us (four
+// instructions for each group and 128 outputs, about 120 cycles each for their few columns).
 #include "lora.cuh"
 #include "pipe.cuh"
 
