@@ -39,6 +39,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 namespace {
 
@@ -57,12 +58,18 @@ constexpr int kGroup = 8;       // M tiles that a walk over the columns shares
 constexpr int kPartRows = 16;   // rows of the boxes that load a partly filled chunk
 constexpr size_t kSmemMax = 227 * 1024;
 
-// Float32 results: stages whose sum stays in tensor memory.  The tensor core's additions
-// round towards zero, so an error grows with their number: K 2056, 2.3e-6 of the values in
-// one go, 2.6e-7 in segments of four stages that the epilogue adds up in registers (to
-// nearest).  3001 rows of 64 experts, 2056 x 2817: 128 and 132 us.  (Results of 16 bits round
-// by a thousand times as much.)
+// Stages whose sum stays in tensor memory; longer sums are made of such segments, which the
+// epilogue adds up in registers, to nearest.  The tensor core's additions round towards
+// zero, four of them a stage, so that an error grows with their number: K 2056, 2.3e-6 of
+// the values in one go, 2.6e-7 in segments of four stages.  Four for float32 results: 3001
+// rows of 64 experts, 2056 x 2817, 128 us in one go and 132.  16 for results of 16 bits: what
+// is cut off stays below a 250th of f16's half step however long the sum is (in one go a
+// ninth at 28672).  us in one go and in segments of 16, 12, 8 and 4 stages: 8192 rows of 8
+// experts, 4096 x 28672, 1221, 1245, 1259, 1306, 1363, both gradients there 2607, 2636, 2658,
+// 2669, 2739 (storing 256 columns takes longer than the two short segments that the
+// accumulators hold meanwhile).
 constexpr int kSegment = 4;
+constexpr int kSegment16 = 16;
 
 constexpr int kChunkBytes = 32 * 64;  // an epilogue warp's 32 lanes by 64 bytes of columns
 
@@ -102,6 +109,7 @@ struct Params {
   bool listed;       // tiles are numbered in 16 bits: units fit the list
   bool tma_out;      // GG_ROWS: the result's rows start at 16-byte boundaries
   bool zero_outside;
+  int segment;       // stages whose sum stays in tensor memory
   void* out;
   int out_dtype;
   float* part;
@@ -241,7 +249,7 @@ __device__ __forceinline__ void stage_line(uint8_t* chunk, int lane, const uint3
         make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
-// One product, by the CTA `block` of `blocks` that work at it.  SEG: sums of kSegment
+// One product, by the CTA `block` of `blocks` that work at it.  SEG: sums of p.segment
 // stages leave tensor memory and are added up in the epilogue's registers.
 template <int FORM, int BN, int CG, bool SEG>
 __device__ __forceinline__ void gg_body(const CUtensorMap& map_w, const CUtensorMap& map_a,
@@ -290,15 +298,17 @@ __device__ __forceinline__ void gg_body(const CUtensorMap& map_w, const CUtensor
   mq::pdl_wait();
   mq::pdl_trigger();
   // Chunks of each expert, scanned; then this worker's units.
-  bool fine = true;
+  bool fine = true, longer = FORM != GG_ROWS;  // (the others have one length: the kernel is chosen by it)
   for (int e = tid; e < p.E; e += kThreads) {
     int start, count;
     fine &= segment(p, e, start, count);
     chunk_start[e] = (count + BN - 1) / BN;
+    longer |= count > p.segment * kStageK;
   }
   // offsets that fall or leave [0, R]: nothing is computed
   const bool bad = __syncthreads_or(!fine);
   if (bad && tid == 0 && block == 0) mq::flag(p.status, MQ_DEV_BAD_OFFSETS);
+  const bool long_sums = SEG && __syncthreads_or(longer);  // some unit's sum has several segments
   if (FORM != GG_ROWS && warp == 0) {
     int run = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
@@ -428,7 +438,7 @@ __device__ __forceinline__ void gg_body(const CUtensorMap& map_w, const CUtensor
       if (s0 == s1) continue;  // no rows: the epilogue stores zeros
       const uint32_t idesc = p.idesc | (uint32_t)(columns<FORM, BN, CG>(p, w) >> 3) << 17;
       for (int s = s0; s < s1 && ok;) {
-        const int end = SEG ? min(s + kSegment, s1) : s1;
+        const int end = SEG ? min(s + p.segment, s1) : s1;
         const uint32_t buf = done & 1;
         ok = warp_wait<CG>(&ctl->acc_empty[buf], ((done >> 1) & 1) ^ 1, ctl, p.status);
         ++done;
@@ -504,137 +514,159 @@ __device__ __forceinline__ void gg_body(const CUtensorMap& map_w, const CUtensor
     // ---------------------------------------------------------- epilogue --
     const int quad = warp & 3;         // the tensor-memory lanes this warp may read
     const int half = (warp - 4) >> 2;  // which 16-column steps it takes
-    uint32_t done = 0;
+    uint32_t u = 0, done = 0;
     bool ok = true;
-    for (uint32_t u = 0; u < units && ok; ++u) {
-      const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u, worker, workers);
-      const int m = w.m + (int)rank * kTileM + quad * 32 + lane;  // this lane's output
-      const int dtype = p.splits > 1 ? MQ_DTYPE_F32 : p.out_dtype;
-      const bool empty = FORM == GG_ROWS && w.n == 0;
-      const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-      auto sums_ready = [&]() -> bool {
-        if (!warp_wait(&ctl->acc_full[done & 1], (done >> 1) & 1, ctl, p.status)) return false;
-        tc_fence_after();
-        return true;
-      };
-      auto sums_read = [&]() {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (CG == 2) mbar_arrive_tmem_free(map_rank(&ctl->acc_empty[done & 1], 0));
-          else mbar_arrive(&ctl->acc_empty[done & 1]);
-        }
-        ++done;
-      };
-      // Columns of a lane: a half of the tile in steps of 32 (GG_ROWS), or every other
-      // step of 16.
-      constexpr int kStep = FORM == GG_ROWS ? 32 : 16;
-      constexpr int kSteps = BN / 2 / kStep;
-      const int n = FORM == GG_ROWS ? min(BN, p.N - w.col0) : w.n;
-      const int c1 = FORM == GG_ROWS ? min(n, (half + 1) * (BN / 2)) : n;
-      auto column = [&](int i) { return FORM == GG_ROWS ? half * (BN / 2) + i * 32 : half * 16 + i * 32; };
-      auto read = [&](int c0, uint32_t (&v)[kStep]) {
-        const uint32_t at = tmem + (done & 1) * BN + lanes + c0;
-        if constexpr (FORM == GG_ROWS) tmem_ld32_sync(at, v);
-        else tmem_ld16_sync(at, v);
-      };
-      auto store = [&](int c0, const uint32_t (&v)[kStep]) {
-        if constexpr (FORM == GG_ROWS) {
-          // A lane is a row of the result: 64 bytes of it at a time go to shared memory
-          // (swizzled) and from there by TMA, which leaves out what lies outside.  (Longer
-          // lines would take a stage's place.)
-          const bool f32 = dtype == MQ_DTYPE_F32;
-          uint8_t* chunk = chunks_out + (warp - 4) * kChunkBytes;
-          if (p.tma_out) {
-            uint32_t line[16];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (f32) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) line[i] = v[16 * h + i];
-              } else {
-                if (h) break;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) line[i] = pack2(v[2 * i], v[2 * i + 1], dtype == MQ_DTYPE_BF16);
-              }
-              if (lane == 0) bulk_wait_read<0>();  // what was there has been read
-              __syncwarp();
-              stage_line(chunk, lane, line);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                tma_store_3d(&map_part, chunk, w.col0 + c0 + 16 * h, m - lane, w.split * p.E + w.e);
-                bulk_commit();
-              }
-              if (f32 && c0 + 16 >= c1) break;
-            }
-          } else if (m < p.M) {
-            void* out = p.splits > 1 ? p.part + (int64_t)w.split * p.E * p.M * p.N : p.out;
-            const int64_t at = ((int64_t)w.e * p.M + m) * p.N + w.col0 + c0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c0 + i < n) store_out(out, dtype, at + i, __uint_as_float(v[i]));
-          }
-        } else {
-          void* out = p.out;
-          if (p.splits > 1) out = p.part + (int64_t)w.split * p.R * p.M;
-          const int64_t at = (int64_t)(w.row0 + c0) * p.M + m;
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (m < p.M && c0 + j < n) store_out(out, dtype, at + (int64_t)j * p.M, __uint_as_float(v[j]));
-        }
-      };
-      if constexpr (SEG) {
-        uint32_t sum[kSteps][kStep];
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-          for (int j = 0; j < kStep; ++j) sum[i][j] = 0;
+    // Units from u on: sums of one segment, or (kSegs) of several; where there are both
+    // (kMixed), as long as they are of that kind.
+    auto epilogue = [&](auto segs, auto mixed) {
+      constexpr bool kSegs = decltype(segs)::value, kMixed = decltype(mixed)::value;
+      for (; u < units && ok; ++u) {
+        const Unit w = unit_at<FORM, BN, CG>(p, chunk_start, list, u, worker, workers);
         int s0, s1;
         stages_of<FORM>(p, w, s0, s1);
-        for (int s = s0; s < s1; s += kSegment) {
-          ok = sums_ready();
+        if (kMixed && (s1 - s0 > p.segment) != kSegs) return;
+        const int m = w.m + (int)rank * kTileM + quad * 32 + lane;  // this lane's output
+        const int dtype = p.splits > 1 ? MQ_DTYPE_F32 : p.out_dtype;
+        const bool empty = FORM == GG_ROWS && w.n == 0;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        auto sums_ready = [&]() -> bool {
+          if (!warp_wait(&ctl->acc_full[done & 1], (done >> 1) & 1, ctl, p.status)) return false;
+          tc_fence_after();
+          return true;
+        };
+        auto sums_read = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (CG == 2) mbar_arrive_tmem_free(map_rank(&ctl->acc_empty[done & 1], 0));
+            else mbar_arrive(&ctl->acc_empty[done & 1]);
+          }
+          ++done;
+        };
+        // Columns of a lane: a half of the tile in steps of 32 (GG_ROWS), or every other
+        // step of 16.
+        constexpr int kStep = FORM == GG_ROWS ? 32 : 16;
+        constexpr int kSteps = BN / 2 / kStep;
+        const int n = FORM == GG_ROWS ? min(BN, p.N - w.col0) : w.n;
+        const int c1 = FORM == GG_ROWS ? min(n, (half + 1) * (BN / 2)) : n;
+        auto column = [&](int i) { return FORM == GG_ROWS ? half * (BN / 2) + i * 32 : half * 16 + i * 32; };
+        auto read = [&](int c0, uint32_t (&v)[kStep]) {
+          const uint32_t at = tmem + (done & 1) * BN + lanes + c0;
+          if constexpr (FORM == GG_ROWS) tmem_ld32_sync(at, v);
+          else tmem_ld16_sync(at, v);
+        };
+        auto store = [&](int c0, const uint32_t (&v)[kStep]) {
+          if constexpr (FORM == GG_ROWS) {
+            // A lane is a row of the result: 64 bytes of it at a time go to shared memory
+            // (swizzled) and from there by TMA, which leaves out what lies outside.  (Longer
+            // lines would take a stage's place.)
+            const bool f32 = dtype == MQ_DTYPE_F32;
+            uint8_t* chunk = chunks_out + (warp - 4) * kChunkBytes;
+            if (p.tma_out) {
+              uint32_t line[16];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (f32) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) line[i] = v[16 * h + i];
+                } else {
+                  if (h) break;
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) line[i] = pack2(v[2 * i], v[2 * i + 1], dtype == MQ_DTYPE_BF16);
+                }
+                if (lane == 0) bulk_wait_read<0>();  // what was there has been read
+                __syncwarp();
+                stage_line(chunk, lane, line);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  tma_store_3d(&map_part, chunk, w.col0 + c0 + 16 * h, m - lane, w.split * p.E + w.e);
+                  bulk_commit();
+                }
+                if (f32 && c0 + 16 >= c1) break;
+              }
+            } else if (m < p.M) {
+              void* out = p.splits > 1 ? p.part + (int64_t)w.split * p.E * p.M * p.N : p.out;
+              const int64_t at = ((int64_t)w.e * p.M + m) * p.N + w.col0 + c0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c0 + i < n) store_out(out, dtype, at + i, __uint_as_float(v[i]));
+            }
+          } else {
+            void* out = p.out;
+            if (p.splits > 1) out = p.part + (int64_t)w.split * p.R * p.M;
+            const int64_t at = (int64_t)(w.row0 + c0) * p.M + m;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (m < p.M && c0 + j < n) store_out(out, dtype, at + (int64_t)j * p.M, __uint_as_float(v[j]));
+          }
+        };
+        if constexpr (!kSegs) {
+          if (!empty) {
+            ok = sums_ready();
+            if (!ok) break;
+          }
+          if (m - lane < p.M) {
+            for (int i = 0; column(i) < c1; ++i) {
+              uint32_t v[kStep];
+              if (empty) {
+#pragma unroll
+                for (int j = 0; j < kStep; ++j) v[j] = 0;
+              } else {
+                read(column(i), v);
+              }
+              store(column(i), v);
+            }
+          }
+          if (!empty) sums_read();
+        } else {
+          uint32_t sum[kSteps][kStep];
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+            for (int j = 0; j < kStep; ++j) sum[i][j] = 0;
+          for (int s = s0; s < s1; s += p.segment) {
+            ok = sums_ready();
+            if (!ok) break;
+            if (m - lane < p.M) {
+#pragma unroll
+              for (int i = 0; i < kSteps; ++i) {
+                if (column(i) >= c1) continue;
+#pragma unroll
+                for (int h = 0; h < kStep; h += 16) {
+                  uint32_t v[16];
+                  tmem_ld16_sync(tmem + (done & 1) * BN + lanes + column(i) + h, v);
+#pragma unroll
+                  for (int j = 0; j < 16; ++j)
+                    sum[i][h + j] = __float_as_uint(__uint_as_float(sum[i][h + j]) + __uint_as_float(v[j]));
+                }
+              }
+            }
+            sums_read();
+          }
           if (!ok) break;
           if (m - lane < p.M) {
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-              if (column(i) >= c1) continue;
-#pragma unroll
-              for (int h = 0; h < kStep; h += 16) {
-                uint32_t v[16];
-                tmem_ld16_sync(tmem + (done & 1) * BN + lanes + column(i) + h, v);
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  sum[i][h + j] = __float_as_uint(__uint_as_float(sum[i][h + j]) + __uint_as_float(v[j]));
-              }
-            }
-          }
-          sums_read();
-        }
-        if (!ok) break;
-        if (m - lane < p.M) {
-#pragma unroll
-          for (int i = 0; i < kSteps; ++i)
-            if (column(i) < c1) store(column(i), sum[i]);
-        }
-      } else {
-        if (!empty) {
-          ok = sums_ready();
-          if (!ok) break;
-        }
-        if (m - lane < p.M) {
-          for (int i = 0; column(i) < c1; ++i) {
-            uint32_t v[kStep];
-            if (empty) {
-#pragma unroll
-              for (int j = 0; j < kStep; ++j) v[j] = 0;
-            } else {
-              read(column(i), v);
-            }
-            store(column(i), v);
+            for (int i = 0; i < kSteps; ++i)
+              if (column(i) < c1) store(column(i), sum[i]);
           }
         }
-        if (!empty) sums_read();
+      }
+    };
+    // (A choice for each unit costs where units are short: 128 experts, 4096 rows, 1536 x 2048,
+    // whose sums are of one segment: 298 us with it, 364 as if all had several, 278 without.)
+    constexpr std::true_type yes;
+    constexpr std::false_type no;
+    if constexpr (!SEG) {
+      epilogue(no, no);
+    } else if (!long_sums) {
+      epilogue(no, no);
+    } else if constexpr (FORM != GG_ROWS) {
+      epilogue(yes, no);
+    } else {
+      while (u < units && ok) {
+        epilogue(no, yes);
+        epilogue(yes, yes);
       }
     }
   }
@@ -668,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_out,
             const Params rows, const Params weights, uint32_t rows_blocks) {
   if (blockIdx.x < rows_blocks)
-    gg_body<FORM, 256, 2, false>(map_w, map_a, map_part, rows, blockIdx.x, rows_blocks);
+    gg_body<FORM, 256, 2, SEG>(map_w, map_a, map_part, rows, blockIdx.x, rows_blocks);
   else
     gg_body<GG_ROWS, 256, 2, SEG>(map_y, map_x, map_out, weights, blockIdx.x - rows_blocks,
                              gridDim.x - rows_blocks);
@@ -687,11 +719,18 @@ cudaError_t allow_smem(K kern, size_t smem, std::atomic<uint64_t>& ready) {
   return err;
 }
 
+// Whether a sum may be longer than a segment (GG_ROWS: where an expert has most rows).
+template <int FORM>
+bool segmented(const Params& p) {
+  const int64_t stages = ((int64_t)(FORM == GG_ROWS ? p.R : p.K) + kStageK - 1) / kStageK;
+  return (stages + p.splits - 1) / p.splits > p.segment;
+}
+
 template <int FORM, int BN, int CG>
 cudaError_t launch_one(const CUtensorMap& mw, const CUtensorMap& ma, const CUtensorMap& mr,
                        const Params& p, int64_t units, cudaStream_t st) {
   constexpr size_t smem = Cfg<FORM, BN, CG>::kSmem;
-  const bool seg = p.out_dtype == MQ_DTYPE_F32;
+  const bool seg = segmented<FORM>(p);
   auto kern = seg ? gg_gemm<FORM, BN, CG, true> : gg_gemm<FORM, BN, CG, false>;
   static std::atomic<uint64_t> ready[2];
   const cudaError_t err = allow_smem(kern, smem, ready[seg]);
@@ -831,6 +870,7 @@ cudaError_t prepare(const GgGemm& g, const GgPlan& pl, Prepared& out) {
   p.evict_first = true;
   p.listed = p.mtiles < 1 << 16 && p.ntiles < 1 << 16;
   p.zero_outside = g.zero_outside;
+  p.segment = g.out_dtype == MQ_DTYPE_F32 ? kSegment : kSegment16;
   p.out = g.out;
   p.out_dtype = g.out_dtype;
   p.part = g.part;
@@ -894,7 +934,7 @@ cudaError_t launch_gg_both(const GgGemm& rows, const GgGemm& weights, cudaStream
   const int second = (int)std::max<int64_t>(1, std::min<int64_t>(pairs - first, w.units));
   constexpr size_t smem = std::max({Cfg<GG_W_K, 256, 2>::kSmem, Cfg<GG_ROWS, 256, 2>::kSmem});
   const bool by_k = rows.form == GG_W_K;
-  const bool seg = w.p.out_dtype == MQ_DTYPE_F32;
+  const bool seg = segmented<GG_W_K>(r.p) || segmented<GG_ROWS>(w.p);
   const auto kern = seg ? (by_k ? gg_both<GG_W_K, true> : gg_both<GG_W_M, true>)
                         : (by_k ? gg_both<GG_W_K, false> : gg_both<GG_W_M, false>);
   static std::atomic<uint64_t> ready[4];
