@@ -484,10 +484,14 @@ __device__ __forceinline__ float finite(float v) { return isfinite(v) ? fabsf(v)
 constexpr int kDownThreads = 256;
 constexpr int kXSlots = 4, kASlots = 4;  // of 16 KB: a stage of x, of an accumulator's groups
 constexpr int kBatch = 4;                // accumulators at a time
+// Stages whose sum stays in tensor memory, whose additions round towards zero, for results
+// of 32 and of 16 bits; longer sums are made of such segments, added up in shared memory, to
+// nearest (as in grouped_gemm.cu).  Then two accumulators at a time, in two buffers.
+constexpr int kSegment = 4, kSegment16 = 16;
 
 struct DownCtl {
   uint64_t x_full[kXSlots], x_empty[kXSlots], a_full[kASlots], a_empty[kASlots];
-  uint64_t acc_full, acc_empty, drain;
+  uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   volatile int abort_flag;
 };
@@ -507,6 +511,7 @@ struct DownShape {
   int rp;      // r rounded up to 16, 32, 64 or 128
   int splits;  // K splits: CTAs of a cluster
   int mparts;  // clusters among which a tile's accumulators are divided
+  int segment; // stages whose sum stays in tensor memory
   TileTable* tables;
   uint16_t* h;  // [tiles * height][h_row(rp)], a tile's rows by place
 };
@@ -532,8 +537,10 @@ __global__ void __launch_bounds__(kDownThreads, 1)
       mbar_init(&ctl->a_full[i], 1);
       mbar_init(&ctl->a_empty[i], 1);
     }
-    mbar_init(&ctl->acc_full, 1);
-    mbar_init(&ctl->acc_empty, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->acc_full[i], 1);
+      mbar_init(&ctl->acc_empty[i], 4);
+    }
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
@@ -570,6 +577,8 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   const int per = kTile / d.rp;                      // groups of an accumulator
   const int accs = (tb.groups + per - 1) / per;      // accumulators of the tile
   const int mine = accs > mpart ? (accs - mpart + d.mparts - 1) / d.mparts : 0;
+  const int bufs = s1 - s0 > d.segment ? 2 : 1;      // of the accumulators
+  const int batch = kBatch / bufs;
   // the scaling of this thread's (first) row of the last step, which is short
   const int row_share = kTile / d.splits, sub = tid & 7;
   auto scaling_of = [&](int i) {
@@ -582,7 +591,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     const bool el = elect_one();
     uint32_t it = 0;
     bool ok = true;
-    for (int b0 = 0; b0 < mine && ok; b0 += kBatch)
+    for (int b0 = 0; b0 < mine && ok; b0 += batch)
       for (int s = s0; s < s1; ++s, ++it) {
         if (it < (uint32_t)early) continue;
         const uint32_t slot = it % kXSlots;
@@ -601,9 +610,9 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     const bool el = elect_one();
     uint32_t it = 0;
     bool ok = true;
-    for (int b0 = 0; b0 < mine && ok; b0 += kBatch)
+    for (int b0 = 0; b0 < mine && ok; b0 += batch)
       for (int s = s0; s < s1 && ok; ++s)
-        for (int b = b0; b < min(b0 + kBatch, mine); ++b, ++it) {
+        for (int b = b0; b < min(b0 + batch, mine); ++b, ++it) {
           const uint32_t slot = it % kASlots;
           ok = warp_wait(&ctl->a_empty[slot], ((it / kASlots) & 1) ^ 1, ctl, p.status);
           if (!ok) break;
@@ -622,30 +631,37 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     const bool el = elect_one();
     const uint32_t idesc = idesc_16(p.bf16, kTile, ceil16(tb.rows), false, false);
     uint32_t x_it = 0, a_it = 0;
+    Ring ar;
     bool ok = true;
-    for (int b0 = 0, turn = 0; b0 < mine && ok; b0 += kBatch, ++turn) {
-      ok = warp_wait(&ctl->acc_empty, (turn & 1) ^ 1, ctl, p.status);
-      tc_fence_after();
-      for (int s = s0; s < s1 && ok; ++s, ++x_it) {
-        const uint32_t xslot = x_it % kXSlots;
-        ok = warp_wait(&ctl->x_full[xslot], (x_it / kXSlots) & 1, ctl, p.status);
-        const uint64_t bd = smem_desc_k_sw128(smem_addr(xs + xslot * kSlot));
-        for (int b = b0; b < min(b0 + kBatch, mine) && ok; ++b, ++a_it) {
-          const uint32_t aslot = a_it % kASlots;
-          ok = warp_wait(&ctl->a_full[aslot], (a_it / kASlots) & 1, ctl, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          if (el) {
-            const uint64_t ad = smem_desc_k_sw128(smem_addr(as + aslot * kSlot));
+    for (int b0 = 0; b0 < mine && ok; b0 += batch) {
+      const int b1 = min(b0 + batch, mine);
+      for (int s = s0; s < s1 && ok;) {
+        const int first = s, end = min(s + d.segment, s1);
+        ok = warp_wait(&ctl->acc_empty[ar.slot], ar.turn ^ 1, ctl, p.status);
+        tc_fence_after();
+        const uint32_t acc = tmem + ar.slot * batch * kTile;
+        for (; s < end && ok; ++s, ++x_it) {
+          const uint32_t xslot = x_it % kXSlots;
+          ok = warp_wait(&ctl->x_full[xslot], (x_it / kXSlots) & 1, ctl, p.status);
+          const uint64_t bd = smem_desc_k_sw128(smem_addr(xs + xslot * kSlot));
+          for (int b = b0; b < b1 && ok; ++b, ++a_it) {
+            const uint32_t aslot = a_it % kASlots;
+            ok = warp_wait(&ctl->a_full[aslot], (a_it / kASlots) & 1, ctl, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            if (el) {
+              const uint64_t ad = smem_desc_k_sw128(smem_addr(as + aslot * kSlot));
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma_ss<1>(tmem + (b - b0) * kTile, ad + j * 2, bd + j * 2, idesc, (s > s0) | j);
-            mma_commit(&ctl->a_empty[aslot]);
+              for (int j = 0; j < 4; ++j)
+                mma_ss<1>(acc + (b - b0) * kTile, ad + j * 2, bd + j * 2, idesc, (s > first) | j);
+              mma_commit(&ctl->a_empty[aslot]);
+            }
           }
+          if (ok && el) mma_commit(&ctl->x_empty[xslot]);
         }
-        if (ok && el) mma_commit(&ctl->x_empty[xslot]);
+        if (ok && el) mma_commit(&ctl->acc_full[ar.slot]);
+        ar.next(bufs);
       }
-      if (ok && el) mma_commit(&ctl->acc_full);
     }
     if (el) mma_commit(&ctl->drain);
     wait_drain(&ctl->drain, 0);
@@ -656,29 +672,40 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     // A lane is one rank of one of the accumulator's groups.
     const int quad = warp & 3;
     const int gl = (quad * 32 + lane) / d.rp, j = (quad * 32 + lane) % d.rp;
-    bool ok = true;
-    for (int b0 = 0, turn = 0; b0 < mine && ok; b0 += kBatch, ++turn) {
-      ok = warp_wait(&ctl->acc_full, turn & 1, ctl, p.status);
-      if (!ok) break;
+    Ring ar;
+    // A segment's sums to shared memory, or onto those that are there.
+    auto take = [&](int b0, auto onto) {
+      if (!warp_wait(&ctl->acc_full[ar.slot], ar.turn, ctl, p.status)) return false;
       tc_fence_after();
-      for (int b = b0; b < min(b0 + kBatch, mine); ++b) {
+      for (int b = b0; b < min(b0 + batch, mine); ++b) {
         const int g = (mpart + b * d.mparts) * per + gl;
         const bool live = g < tb.groups;
         const unsigned any = __reduce_or_sync(0xffffffffu, live ? tb.blocks[g] : 0u);
         for (int c = 0; c < kTile / 16; ++c) {
           if (!(any >> c & 1)) continue;
           uint32_t v[16];
-          tmem_ld16_sync(tmem + (b - b0) * kTile + c * 16 + ((uint32_t)(quad * 32) << 16), v);
+          tmem_ld16_sync(tmem + (ar.slot * batch + b - b0) * kTile + c * 16 + ((uint32_t)(quad * 32) << 16), v);
           const uint4 of = *reinterpret_cast<const uint4*>(tb.slot + c * 16);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (live && byte_of(of, i) == g) hs[(c * 16 + i) * h_pitch(d.rp) + j] = __uint_as_float(v[i]);
+            if (live && byte_of(of, i) == g) {
+              float& h = hs[(c * 16 + i) * h_pitch(d.rp) + j];
+              if constexpr (decltype(onto)::value) h += __uint_as_float(v[i]);
+              else h = __uint_as_float(v[i]);
+            }
           __syncwarp();
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->acc_empty);
+      if (lane == 0) mbar_arrive(&ctl->acc_empty[ar.slot]);
+      ar.next(bufs);
+      return true;
+    };
+    bool ok = true;
+    for (int b0 = 0; b0 < mine && ok; b0 += batch) {
+      ok = take(b0, std::false_type());
+      for (int s = s0 + d.segment; s < s1 && ok; s += d.segment) ok = take(b0, std::true_type());
     }
   }
   tc_fence_before();
@@ -1318,6 +1345,7 @@ cudaError_t launch_down(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) 
   d.rp = padded_rank(g.r);
   d.splits = pl.splits;
   d.mparts = pl.mparts;
+  d.segment = g.out_dtype == MQ_DTYPE_F32 ? kSegment : kSegment16;
   d.tables = reinterpret_cast<TileTable*>(g.workspace);
   d.h = reinterpret_cast<uint16_t*>(g.workspace + y.h);
   CUtensorMap mx, ma;
