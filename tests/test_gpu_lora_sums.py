@@ -63,3 +63,33 @@ def test_several_segments_and_accumulators(mq, dtype, r, L):
                                   base=base.to(out).cuda())
         clean(mq)
         gh.check_lora(got, *gh.lora64(x, a, b, ids.tolist(), [0] * R, None, base.to(out), dtype))
+
+
+@pytest.mark.parametrize("R", [30, 1100])
+@pytest.mark.parametrize("dtype,out_dtype", [(BF16, BF16), (F16, F16), (BF16, F32), (F16, F32)])
+def test_infinite_entries_of_b(mq, R, dtype, out_dtype):
+    """What an infinite entry of B makes of a finite A x: an infinity of the product's sign, NaN
+    where A x is 0 or infinities of both signs meet, whatever A x looks like in 16 bits; the
+    row's other outputs stay as they are."""
+    K, N, r = 64, 72, 16
+    g = torch.Generator().manual_seed(R)
+    x = torch.randint(-3, 4, (R, K), generator=g).to(dtype)
+    x[::5] = gh.randn(len(x[::5]), K, seed=4, dtype=dtype)
+    a = torch.zeros(1, r, K, dtype=dtype)
+    a[0, torch.arange(r), torch.arange(r)] = 1
+    a[0, 3, 0] = 2.0 ** -13 if dtype == F16 else 2.0 ** -100     # beside a larger one: next to nothing
+    a[0, 3, 3] = 0
+    b = gh.randn(1, N, r, seed=3, dtype=dtype)
+    inf = float("inf")
+    b[0, 5, 2], b[0, 6, 2], b[0, 7, 3], b[0, 8, 4], b[0, 8, 9] = inf, -inf, inf, inf, inf
+    ids = torch.zeros(R, dtype=torch.int32)
+    got = mq.moe_lora_product(x.cuda(), a.cuda(), b.cuda(), ids.cuda(), out_dtype=out_dtype)
+    clean(mq)
+    h = x.double() @ a[0].double().T
+    want = (h[:, None, :] * b[0].double()).sum(2).float()
+    special = [5, 6, 7, 8]
+    assert not want[:, special].isfinite().any()
+    assert torch.equal(got[:, special].float().cpu().nan_to_num(nan=7.0), want[:, special].nan_to_num(nan=7.0))
+    rest = [n for n in range(N) if n not in special]
+    ref, off = gh.lora64(x, a[:, None], b[:, None, rest], [0] * R, [0] * R, None, None, dtype)
+    gh.check_lora(got[:, rest], ref, off)

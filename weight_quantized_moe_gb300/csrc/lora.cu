@@ -469,8 +469,16 @@ __device__ __forceinline__ int byte_of(const uint4& v, int i) {
   return (int)(w >> (i & 3) * 8 & 0xff);
 }
 
-__device__ __forceinline__ uint16_t to_half_bits(float v, bool bf16) {
-  return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+// Two values rounded to 16 bits, the first in the low half.
+template <bool BF16>
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&t);
+  } else {
+    const __half2 t = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&t);
+  }
 }
 __device__ __forceinline__ float from_half_bits(uint16_t v, bool bf16) {
   return bf16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
@@ -478,6 +486,39 @@ __device__ __forceinline__ float from_half_bits(uint16_t v, bool bf16) {
 
 // The magnitude of v, 0 where it is infinite or NaN.
 __device__ __forceinline__ float finite(float v) { return isfinite(v) ? fabsf(v) : 0.0f; }
+
+// v * down as the sum of two 16-bit values, both of its sign and neither zero (unless v is;
+// infinite or NaN where it is): what an infinite factor makes of them then has the sign, and
+// the kind, that it has with v.  The first is rounded towards zero, or, where that leaves
+// nothing for the second, a unit lower.  (Too small a value is raised, by at most 2^-23 of
+// the row's largest.)
+template <bool BF16>
+__device__ __forceinline__ void two_parts(float v, float down, float& hi, float& lo) {
+  const float f = copysignf(fmaxf(fabsf(v * down), BF16 ? 0x1p-100f : 0x1p-23f), v);
+  if constexpr (BF16) {
+    hi = __uint_as_float(__float_as_uint(f) & 0xffff0000u);
+    if (hi == f) hi = __uint_as_float(__float_as_uint(f) - 0x10000u);
+    lo = f - hi;
+  } else {
+    const uint16_t h = __half_as_ushort(__float2half_rz(f));
+    hi = from_half_bits(h, false);
+    if (hi == f) hi = from_half_bits(h - 1, false);
+    lo = copysignf(fmaxf(fabsf(f - hi), 0x1p-24f), v);
+  }
+  if (v == 0 || !isfinite(v)) hi = lo = v;
+}
+
+// Four values' parts, `apart` elements from one another.
+template <bool BF16>
+__device__ __forceinline__ void store_parts(uint16_t* dst, int apart, const float4& v, float down) {
+  float hi[4], lo[4];
+  two_parts<BF16>(v.x, down, hi[0], lo[0]);
+  two_parts<BF16>(v.y, down, hi[1], lo[1]);
+  two_parts<BF16>(v.z, down, hi[2], lo[2]);
+  two_parts<BF16>(v.w, down, hi[3], lo[3]);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(half_pair<BF16>(hi[0], hi[1]), half_pair<BF16>(hi[2], hi[3]));
+  *reinterpret_cast<uint2*>(dst + apart) = make_uint2(half_pair<BF16>(lo[0], lo[1]), half_pair<BF16>(lo[2], lo[3]));
+}
 
 // ---- first launch: h = A x, its sum over the K splits, and s h in 16-bit parts ----
 // A cluster holds the K splits of a tile (or of a part of its accumulators).
@@ -755,17 +796,8 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     for (int q = 0; q < 4; ++q) {
       const int j = q * 32 + sub * 4;
       if (j >= d.rp) continue;
-      const float f[4] = {v[q].x * down, v[q].y * down, v[q].z * down, v[q].w * down};
-      uint16_t hi[4], lo[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        hi[k] = to_half_bits(f[k], p.bf16);
-        const float rest = f[k] - from_half_bits(hi[k], p.bf16);
-        lo[k] = to_half_bits(isfinite(rest) ? rest : 0.0f, p.bf16);  // (infinity minus itself)
-      }
-      *reinterpret_cast<uint2*>(dst + j) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
-      *reinterpret_cast<uint2*>(dst + d.rp + j) =
-          make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
+      if (p.bf16) store_parts<true>(dst + j, d.rp, v[q], down);
+      else store_parts<false>(dst + j, d.rp, v[q], down);
     }
   }
   __syncwarp();
@@ -825,15 +857,7 @@ __device__ __forceinline__ uint32_t add_pair(uint32_t m, uint32_t a, uint32_t b,
   }
   lo = fmaf(__uint_as_float(a), scale.x, lo);
   hi = fmaf(__uint_as_float(b), scale.y, hi);
-  uint32_t q;
-  if constexpr (BF16) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-    q = *reinterpret_cast<const uint32_t*>(&t);
-  } else {
-    const __half2 t = __floats2half2_rn(lo, hi);
-    q = *reinterpret_cast<const uint32_t*>(&t);
-  }
-  return (m & ~in) | (q & in);
+  return (m & ~in) | (half_pair<BF16>(lo, hi) & in);
 }
 
 // 0xff in the bytes of v that, halved, are `rd`.
