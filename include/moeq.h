@@ -563,7 +563,7 @@ int moe_grouped_product_grad(const void* dy, int64_t dy_stride, const void* a, i
  * with the inputs.
  * A x and the sums are float32; with many rows A x enters the second product as the
  * sum of two 16-bit values (16 bits of precision relative to the row's largest for
- * bf16, 22 for f16); one final rounding.  A row's result depends on no other row, and
+ * bf16, 22 for f16), of three (24 bits) where out is float32; one final rounding.  A row's result depends on no other row, and
  * is the same on every run.
  * Limits: K and r multiples of 8, r <= 128, E <= 1024, R, K, N and L * E < 2^30.
  * x_stride is a multiple of 8; base and out whose strides and N are multiples of 8, on

@@ -93,3 +93,28 @@ def test_infinite_entries_of_b(mq, R, dtype, out_dtype):
     rest = [n for n in range(N) if n not in special]
     ref, off = gh.lora64(x, a[:, None], b[:, None, rest], [0] * R, [0] * R, None, None, dtype)
     gh.check_lora(got[:, rest], ref, off)
+
+
+@pytest.mark.parametrize("R", [30, 1100])
+@pytest.mark.parametrize("r", [8, 24, 64, 72])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_float32_results_have_24_bits(mq, R, r, dtype):
+    """A picks an element of x for each rank and B one rank for each output: the result is the
+    scaled element, whose float32 product with the scaling is off by half a step of 2^-23; then
+    24 bits of it, relative to the row's largest at most, and the last rounding."""
+    K, N, L = 128, 96, 3
+    g = torch.Generator().manual_seed(r)
+    x = gh.randn(R, K, seed=1, dtype=dtype)
+    x[::3] *= torch.exp2(torch.randint(-12, 1, (K,), generator=g).float()).to(dtype)   # elements of all sizes
+    pick, rank = torch.randint(K, (r,), generator=g), torch.randint(r, (N,), generator=g)
+    a, b = torch.zeros(L, r, K, dtype=dtype), torch.zeros(L, N, r, dtype=dtype)
+    a[:, torch.arange(r), pick] = 1
+    b[:, torch.arange(N), rank] = 1
+    scaling = torch.rand(L, generator=g) + 0.5
+    ids = torch.randint(L, (R,), generator=g, dtype=torch.int32)
+    got = mq.moe_lora_product(x.cuda(), a.cuda(), b.cuda(), ids.cuda(), scaling=scaling.cuda(), out_dtype=F32)
+    clean(mq)
+    h = x[:, pick].double() * scaling[ids.long()].double()[:, None]
+    ref = h[:, rank]
+    allowed = 2.0 ** -24 * h.abs().amax(1, keepdim=True) + 2 * 2.0 ** -24 * ref.abs()
+    assert ((got.double().cpu() - ref).abs() <= allowed).all()

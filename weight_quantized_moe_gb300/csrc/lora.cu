@@ -21,8 +21,9 @@
 // lanes of an accumulator (eight of rank 16, two of rank 64), x is the other operand; a
 // cluster's CTAs take a share of K each and sum their h through distributed shared
 // memory.  s h is written as the second product's operand, in two 16-bit parts: h = 2^m
-// (hi + lo), m the exponent of the row's largest |h|: 16 bits of precision for bf16 and
-// 22 for f16, whose range it cannot leave either, for twice a small product.
+// (hi + lo), m by the exponent of the row's largest |h|: 16 bits of precision for bf16 and
+// 22 for f16, whose range it cannot leave either, for twice a small product; in three (24
+// bits) where the result is float32.
 // Second launch (lora_up): a group's product has the columns of its own rows only, so
 // that groups in different blocks of 16 rows share an accumulator and a tile of several
 // requests takes one turn of the epilogue, or a few.  base comes by TMA and goes back, with
@@ -487,37 +488,50 @@ __device__ __forceinline__ float from_half_bits(uint16_t v, bool bf16) {
 // The magnitude of v, 0 where it is infinite or NaN.
 __device__ __forceinline__ float finite(float v) { return isfinite(v) ? fabsf(v) : 0.0f; }
 
-// v * down as the sum of two 16-bit values, both of its sign and neither zero (unless v is;
-// infinite or NaN where it is): what an infinite factor makes of them then has the sign, and
-// the kind, that it has with v.  The first is rounded towards zero, or, where that leaves
-// nothing for the second, a unit lower.  (Too small a value is raised, by at most 2^-23 of
-// the row's largest.)
+// f as the sum of two 16-bit values, both of its sign and neither zero: what an infinite
+// factor makes of them then has the sign, and the kind, that it has with f.  The first is
+// rounded towards zero, or, where that leaves nothing for the second, a unit lower.  (Of f16
+// f has two units of 2^-24 at least.)
 template <bool BF16>
-__device__ __forceinline__ void two_parts(float v, float down, float& hi, float& lo) {
-  const float f = copysignf(fmaxf(fabsf(v * down), BF16 ? 0x1p-100f : 0x1p-23f), v);
+__device__ __forceinline__ void two_parts(float f, float& hi, float& rest) {
   if constexpr (BF16) {
     hi = __uint_as_float(__float_as_uint(f) & 0xffff0000u);
     if (hi == f) hi = __uint_as_float(__float_as_uint(f) - 0x10000u);
-    lo = f - hi;
   } else {
     const uint16_t h = __half_as_ushort(__float2half_rz(f));
     hi = from_half_bits(h, false);
     if (hi == f) hi = from_half_bits(h - 1, false);
-    lo = copysignf(fmaxf(fabsf(f - hi), 0x1p-24f), v);
   }
-  if (v == 0 || !isfinite(v)) hi = lo = v;
+  rest = f - hi;
+}
+
+// v, or `least` of its sign.
+__device__ __forceinline__ float raised(float v, float least) { return copysignf(fmaxf(fabsf(v), least), v); }
+
+// v * down in PARTS parts (infinite or NaN, or zero, where v is).  Too small a value is
+// raised, by at most 2^-36 of the row's largest.
+template <bool BF16, int PARTS>
+__device__ __forceinline__ void split_value(float v, float down, float (&part)[PARTS]) {
+  constexpr float kUnit = BF16 ? 0.0f : 0x1p-24f;
+  two_parts<BF16>(raised(copysignf(v * down, v), BF16 ? 0x1p-90f : 2 * kUnit), part[0], part[1]);
+  if constexpr (PARTS == 3) two_parts<BF16>(raised(part[1], 2 * kUnit), part[1], part[2]);
+  if constexpr (!BF16) part[PARTS - 1] = copysignf(fmaxf(fabsf(part[PARTS - 1]), kUnit), v);
+  if (v == 0 || !isfinite(v))
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) part[i] = v;
 }
 
 // Four values' parts, `apart` elements from one another.
-template <bool BF16>
+template <bool BF16, int PARTS>
 __device__ __forceinline__ void store_parts(uint16_t* dst, int apart, const float4& v, float down) {
-  float hi[4], lo[4];
-  two_parts<BF16>(v.x, down, hi[0], lo[0]);
-  two_parts<BF16>(v.y, down, hi[1], lo[1]);
-  two_parts<BF16>(v.z, down, hi[2], lo[2]);
-  two_parts<BF16>(v.w, down, hi[3], lo[3]);
-  *reinterpret_cast<uint2*>(dst) = make_uint2(half_pair<BF16>(hi[0], hi[1]), half_pair<BF16>(hi[2], hi[3]));
-  *reinterpret_cast<uint2*>(dst + apart) = make_uint2(half_pair<BF16>(lo[0], lo[1]), half_pair<BF16>(lo[2], lo[3]));
+  float part[4][PARTS];
+  split_value<BF16>(v.x, down, part[0]);
+  split_value<BF16>(v.y, down, part[1]);
+  split_value<BF16>(v.z, down, part[2]);
+  split_value<BF16>(v.w, down, part[3]);
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i)
+    *reinterpret_cast<uint2*>(dst + i * apart) = make_uint2(half_pair<BF16>(part[0][i], part[1][i]), half_pair<BF16>(part[2][i], part[3][i]));
 }
 
 // ---- first launch: h = A x, its sum over the K splits, and s h in 16-bit parts ----
@@ -544,8 +558,12 @@ struct DownShared {
 };
 // floats between the rows of h in shared memory
 __host__ __device__ constexpr int h_pitch(int rp) { return rp + 4; }
+// s h is the sum of two 16-bit values, of three where the result is float32, which shows more
+// of it: 16 bits for bf16 and 22 for f16, or 24.
+constexpr int kMaxParts = 3;
+int parts_of(int out_dtype) { return out_dtype == MQ_DTYPE_F32 ? 3 : 2; }
 // 16-bit elements between the rows of the second product's operand
-__host__ __device__ constexpr int h_row(int rp) { return rp < 32 ? 64 : 2 * rp; }
+__host__ __device__ constexpr int h_row(int rp, int parts) { return (parts * rp + 63) / 64 * 64; }
 
 struct DownShape {
   int height;  // rows of a tile
@@ -554,9 +572,11 @@ struct DownShape {
   int mparts;  // clusters among which a tile's accumulators are divided
   int segment; // stages whose sum stays in tensor memory
   TileTable* tables;
-  uint16_t* h;  // [tiles * height][h_row(rp)], a tile's rows by place
+  uint16_t* h;  // [tiles * height][h_row(rp, parts)], a tile's rows by place
 };
 
+// BF16: x and the adapters are.
+template <bool BF16, int PARTS>
 __global__ void __launch_bounds__(kDownThreads, 1)
     lora_down(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
               const LoraArgs p, const DownShape d) {
@@ -727,13 +747,17 @@ __global__ void __launch_bounds__(kDownThreads, 1)
           uint32_t v[16];
           tmem_ld16_sync(tmem + (ar.slot * batch + b - b0) * kTile + c * 16 + ((uint32_t)(quad * 32) << 16), v);
           const uint4 of = *reinterpret_cast<const uint4*>(tb.slot + c * 16);
+          float* const at = hs + c * 16 * h_pitch(d.rp) + j;
+          if constexpr (decltype(onto)::value) {  // (all reads before the writes: one after the other took 2 us)
+            float old[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) old[i] = live ? at[i * h_pitch(d.rp)] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(old[i] + __uint_as_float(v[i]));
+          }
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (live && byte_of(of, i) == g) {
-              float& h = hs[(c * 16 + i) * h_pitch(d.rp) + j];
-              if constexpr (decltype(onto)::value) h += __uint_as_float(v[i]);
-              else h = __uint_as_float(v[i]);
-            }
+            if (live && byte_of(of, i) == g) at[i * h_pitch(d.rp)] = __uint_as_float(v[i]);
           __syncwarp();
         }
       }
@@ -786,18 +810,19 @@ __global__ void __launch_bounds__(kDownThreads, 1)
 #pragma unroll
     for (int o = 4; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
     if (!live) continue;
-    // 2^m with m the exponent of the largest, kept to where 2^m and 2^-m are normal
-    const int e = min(max((int)(__float_as_uint(most) >> 23), 1), 253);
+    // 2^m with m the exponent of the largest, for f16, which has less room below than above,
+    // less 14; kept to where 2^m and 2^-m are normal
+    constexpr int below = BF16 ? 0 : 14;
+    const int e = min(max((int)(__float_as_uint(most) >> 23), 1 + below), 253) - below;
     const float up = __uint_as_float((uint32_t)e << 23), down = __uint_as_float((uint32_t)(254 - e) << 23);
     const int place = sh->places.of_row[t];
     if (sub == 0) d.tables[tile].row_scale[place] = up;
-    uint16_t* dst = d.h + (row0 + place) * h_row(d.rp);
+    uint16_t* dst = d.h + (row0 + place) * h_row(d.rp, PARTS);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int j = q * 32 + sub * 4;
       if (j >= d.rp) continue;
-      if (p.bf16) store_parts<true>(dst + j, d.rp, v[q], down);
-      else store_parts<false>(dst + j, d.rp, v[q], down);
+      store_parts<BF16, PARTS>(dst + j, d.rp, v[q], down);
     }
   }
   __syncwarp();
@@ -939,14 +964,15 @@ __device__ __forceinline__ void plain_copies(const LoraArgs& p, const TileTable&
   }
 }
 
-template <bool BF16>  // out is bf16
+// BF16: out is bf16.  PARTS: 16-bit values of which s h is the sum.
+template <bool BF16, int PARTS>
 __global__ void __launch_bounds__(kUpThreads, 1)
     lora_up(const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_h,
             const __grid_constant__ CUtensorMap map_base, const __grid_constant__ CUtensorMap map_out,
             const LoraArgs p, const UpShape u) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* hs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  const int hblocks = (2 * u.rp + 63) / 64;
+  const int hblocks = h_row(u.rp, PARTS) / 64;
   uint8_t* slots = hs + hblocks * kSlot;
   uint8_t* io = slots + u.slots * kTile * u.line;
   UpShared* sh = reinterpret_cast<UpShared*>(io + u.nio * kIoBytes);
@@ -1127,10 +1153,10 @@ __global__ void __launch_bounds__(kUpThreads, 1)
                    for (int j = 0; j < 4; ++j) {
                      if (k * 4 + j >= ksteps) break;
 #pragma unroll
-                     for (int half = 0; half < 2; ++half) {
-                       const int c = k * 4 + j + half * (u.rp / 16);  // the step's place among the columns' k
+                     for (int part = 0; part < PARTS; ++part) {
+                       const int c = k * 4 + j + part * (u.rp / 16);  // the step's place among the columns' k
                        const uint64_t bd = smem_desc_k_sw128(hb + (c >> 2) * kSlot + c0 * 2048);
-                       mma_ss<1>(acc, ad + j * 2, bd + (c & 3) * 2, id, k | j | half);
+                       mma_ss<1>(acc, ad + j * 2, bd + (c & 3) * 2, id, k | j | part);
                      }
                    }
                    mma_commit(&ctl->empty[w.slot]);
@@ -1342,7 +1368,7 @@ LoraLayout lora_layout(const LoraPlan& pl, int64_t R, int r) {
   LoraLayout y;
   y.tiles = (R + pl.height - 1) / pl.height;
   y.h = ((size_t)y.tiles * sizeof(TileTable) + 255) & ~(size_t)255;
-  y.total = y.h + (size_t)y.tiles * pl.height * h_row(padded_rank(r)) * 2;
+  y.total = y.h + (size_t)y.tiles * pl.height * h_row(padded_rank(r), kMaxParts) * 2;
   return y;
 }
 
@@ -1386,10 +1412,13 @@ cudaError_t launch_down(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) 
   static_assert(fixed + sizeof(float) * kTile * h_pitch(kMaxRank) <= kSmemMax, "shared memory");
   static_assert(fixed >= 120 * 1024, "one CTA per SM: each allocates all of tensor memory");
   const size_t smem = fixed + sizeof(float) * kTile * h_pitch(d.rp);
-  static std::atomic<uint64_t> ready{0};
-  err = allow_smem(lora_down, kSmemMax, ready);
+  static std::atomic<uint64_t> ready[4];
+  const bool wide = parts_of(g.out_dtype) == 3;
+  const auto kern = wide ? (g.bf16 ? lora_down<true, 3> : lora_down<false, 3>)
+                         : (g.bf16 ? lora_down<true, 2> : lora_down<false, 2>);
+  err = allow_smem(kern, kSmemMax, ready[2 * wide + g.bf16]);
   if (err != cudaSuccess) return err;
-  return launch_pdl_cluster(lora_down, dim3((unsigned)(y.tiles * pl.splits * pl.mparts)), dim3(kDownThreads),
+  return launch_pdl_cluster(kern, dim3((unsigned)(y.tiles * pl.splits * pl.mparts)), dim3(kDownThreads),
                             pl.splits, smem, st, mx, ma, g, d);
 }
 
@@ -1399,6 +1428,7 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
   UpShape u;
   u.height = pl.height;
   u.rp = padded_rank(g.r);
+  const int parts = parts_of(g.out_dtype);
   u.gparts = pl.gparts;
   u.ntiles = (g.N + kTile - 1) / kTile;
   u.tables = reinterpret_cast<const TileTable*>(g.workspace);
@@ -1423,7 +1453,7 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
                              : u.line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                             : CU_TENSOR_MAP_SWIZZLE_32B);
   if (err != cudaSuccess) return err;
-  const cuuint64_t hd[2] = {(cuuint64_t)h_row(u.rp), (cuuint64_t)y.tiles * pl.height}, hst = 2 * hd[0];
+  const cuuint64_t hd[2] = {(cuuint64_t)h_row(u.rp, parts), (cuuint64_t)y.tiles * pl.height}, hst = 2 * hd[0];
   const cuuint32_t hb[2] = {64, (cuuint32_t)pl.height};
   err = make_map(&mh, dt, 2, g.workspace + y.h, hd, &hst, hb);
   if (err != cudaSuccess) return err;
@@ -1438,19 +1468,20 @@ cudaError_t launch_up(const LoraArgs& g, const LoraPlan& pl, cudaStream_t st) {
     if (err == cudaSuccess && g.base) err = make_map(&mbase, ot, 2, g.base, d, &t0, box);
     if (err != cudaSuccess) return err;
   }
-  const size_t need = 1024 + (2 * u.rp + 63) / 64 * kSlot + (size_t)u.slots * kTile * u.line + (size_t)u.nio * kIoBytes + sizeof(UpShared);
+  const size_t need = 1024 + h_row(u.rp, parts) / 64 * kSlot + (size_t)u.slots * kTile * u.line + (size_t)u.nio * kIoBytes + sizeof(UpShared);
   static_assert(1024 + 4 * kSlot + 2 * kSlot + 3 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
                     1024 + 2 * kSlot + 2 * kSlot + 4 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
-                    1024 + kSlot + kGroupBytes + 4 * kIoBytes + sizeof(UpShared) <= kSmemMax,
+                    1024 + kSlot + kGroupBytes + 4 * kIoBytes + sizeof(UpShared) <= kSmemMax &&
+                    1024 + 6 * kSlot + kGroupBytes + sizeof(UpShared) <= kSmemMax,
                 "shared memory");
   static_assert(kGroupBytes / (kTile * 32) <= kMaxUpSlots && kGroupBytes / (kTile * 32) % 2 == 0 &&
                     kGroupBytes / (kTile * 64) % 2 == 0,
                 "a slot belongs to one of the two MMA warps");
   const size_t smem = std::max<size_t>(need, 120 * 1024);  // one CTA per SM: each allocates all of tensor memory
-  static std::atomic<uint64_t> ready[2];
+  static std::atomic<uint64_t> ready[3];
   const bool bf = g.out_dtype == MQ_DTYPE_BF16;
-  const auto kern = bf ? lora_up<true> : lora_up<false>;
-  err = allow_smem(kern, kSmemMax, ready[bf]);
+  const auto kern = parts == 3 ? lora_up<false, 3> : bf ? lora_up<true, 2> : lora_up<false, 2>;
+  err = allow_smem(kern, kSmemMax, ready[parts == 3 ? 2 : bf]);
   if (err != cudaSuccess) return err;
   u.shares = up_shares(y.tiles, pl.height, u.ntiles * u.gparts);
   const int64_t grid = y.tiles * u.shares;
