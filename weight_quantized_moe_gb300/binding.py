@@ -145,6 +145,14 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _written(*tensors):
+    """After a call that wrote to tensors of the caller (None: not given): their versions count,
+    as with any in-place operation, so that a backward pass that saved one refuses to run."""
+    given = [t for t in tensors if t is not None]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def _stream(stream=None):
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -205,6 +213,7 @@ def moe_quantize_int8_per_channel(w, q=None, scale=None, stream=None):
     w2d = w.reshape(-1, w.shape[-1])
     _need(w2d, torch.bfloat16, "w", 2)
     rows, cols = w2d.shape
+    given = (q, scale)
     if q is None:
         q = torch.empty(w.shape, dtype=torch.int8, device=w.device)
     if scale is None:
@@ -215,6 +224,7 @@ def moe_quantize_int8_per_channel(w, q=None, scale=None, stream=None):
         raise ValueError("q / scale have the wrong size")
     _check(lib().moe_quantize_int8_per_channel(_ptr(w2d), rows, cols, _ptr(q), _ptr(scale),
                                                _stream(stream)))
+    _written(*given)
     return q, scale
 
 
@@ -263,6 +273,7 @@ def moe_topk_route(logits, k, renormalize, topk_w=None, topk_ids=None, stream=No
     T, E = logits.shape
     opts, plain = route_opts(E, renormalize, scoring_func, num_expert_group, topk_group,
                              e_score_correction_bias, routed_scaling_factor)
+    given = (topk_w, topk_ids)
     if topk_w is None:
         topk_w = torch.empty(T, k, dtype=torch.float32, device=logits.device)
     if topk_ids is None:
@@ -277,6 +288,7 @@ def moe_topk_route(logits, k, renormalize, topk_w=None, topk_ids=None, stream=No
     else:
         _check(lib().moe_topk_route_ex(_ptr(logits), T, E, k, ctypes.byref(opts), _ptr(topk_w),
                                        _ptr(topk_ids), _stream(stream)))
+    _written(*given)
     return topk_w, topk_ids
 
 
@@ -393,6 +405,7 @@ def moe_quant_forward(x, w13, w2, s13, s2, topk_w, topk_ids, bits=8, group_size=
     _need(workspace, torch.uint8, "workspace")
     if inplace:
         out = x
+    given = out
     if out is None:
         out = torch.empty(T, H, dtype=x.dtype, device=x.device)
     _need(out, x.dtype, "out", 2)
@@ -401,6 +414,7 @@ def moe_quant_forward(x, w13, w2, s13, s2, topk_w, topk_ids, bits=8, group_size=
         _ptr(w13), _ptr(w2), _ptr(s13), _ptr(s2), _ptr(z13 if has_zp else None),
         _ptr(z2 if has_zp else None), _ptr(topk_w), _ptr(topk_ids),
         _ptr(workspace), workspace.numel(), _ptr(out), flags, _stream(stream)))
+    _written(given)
     return out
 
 
@@ -432,6 +446,7 @@ def moe_quant_forward_logits(x, router_logits, w13, w2, s13, s2, top_k, renormal
     _need(workspace, torch.uint8, "workspace")
     if inplace:
         out = x
+    given = out
     if out is None:
         out = torch.empty(T, H, dtype=x.dtype, device=x.device)
     _need(out, x.dtype, "out", 2)
@@ -444,6 +459,7 @@ def moe_quant_forward_logits(x, router_logits, w13, w2, s13, s2, top_k, renormal
     else:
         _check(lib().moe_quant_forward_logits_ex(_ptr(x), _ptr(router_logits), T, H, I, E, top_k,
                                                  ctypes.byref(opts), *tail))
+    _written(given)
     return out
 
 
@@ -463,6 +479,7 @@ def moe_quant_forward_noalloc(x, w13, w2, s13, s2, topk_w, topk_ids, bits=8, gro
                         "float32 per-channel scales) or uint4")
     _need(topk_w, torch.float32, "topk_w")
     _need(topk_ids, torch.int32, "topk_ids")
+    given = out
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
     _need(out, torch.bfloat16, "out", 2)
@@ -470,6 +487,7 @@ def moe_quant_forward_noalloc(x, w13, w2, s13, s2, topk_w, topk_ids, bits=8, gro
         _ptr(x), T, H, I, E, k, bits, group_size, int(bool(has_zp)),
         _ptr(w13), _ptr(w2), _ptr(s13), _ptr(s2), _ptr(z13 if has_zp else None),
         _ptr(z2 if has_zp else None), _ptr(topk_w), _ptr(topk_ids), _ptr(out), _stream(stream)))
+    _written(given)
     return out
 
 

@@ -109,6 +109,14 @@ at::Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const
   return t;
 }
 
+// After a call that wrote to tensors of the caller (None: not given): their versions count, as
+// with any in-place operation, so that a backward pass that saved one refuses to run.
+void written(std::initializer_list<PyObject*> os) {
+  for (PyObject* o : os)
+    if (o != Py_None && !THPVariable_Unpack(o).is_inference())
+      THPVariable_Unpack(o).unsafeGetTensorImpl()->bump_version();
+}
+
 // Makes the tensors' device current for the rest of a call: the library plans,
 // launches and finds its status word on the current device.  (Where it is current
 // already, as almost always, one look-up instead of a guard's two.)

@@ -94,6 +94,7 @@ PyObject* product(PyObject* const* v) {
                                w.stride, w.expert, w.transposed, offsets, out.data_ptr(), (int)dt,
                                ptr(wksp), wksp.defined() ? (size_t)wksp.numel() : 0, on.stream);
   }));
+  written({v[3]});
   return wrap(out);
 }
 
@@ -138,6 +139,7 @@ PyObject* product_grad(PyObject* const* v) {
                                     offsets, ptr(da), ptr(dw), (int)dt, ptr(wksp),
                                     wksp.defined() ? (size_t)wksp.numel() : 0, on.stream);
   }));
+  written({v[6], v[7]});
   return wrap_all({da, dw});
 }
 
@@ -207,6 +209,7 @@ PyObject* lora(PyObject* const* v) {
                             scaling, ptr(base), base_stride, out.data_ptr(), out_stride, (int)dt, ptr(wksp),
                             wksp.defined() ? (size_t)wksp.numel() : 0, on.stream);
   }));
+  written({v[7]});
   return wrap(out);
 }
 

@@ -75,6 +75,7 @@ PyObject* quantize(PyObject* const* a) {
     return moe_quantize_mx(x.data_ptr(), dt, x.numel() / cols, cols, stride, bits, bytes(q),
                            bytes(s), on.stream);
   }));
+  written({a[2], a[3]});
   return wrap_all({q, s});
 }
 
@@ -93,6 +94,7 @@ PyObject* dequantize(PyObject* const* a) {
     return moe_dequantize_mx(bytes(q), scale, out.numel() / cols, cols, bits, out.data_ptr(),
                              (int)dt, on.stream);
   }));
+  written({a[4]});
   return wrap(out);
 }
 
@@ -139,6 +141,7 @@ PyObject* rmsnorm(PyObject* const* a) {
                           xst, rst, (float)eps, ro.defined() ? ro.data_ptr() : nullptr,
                           y.defined() ? y.data_ptr() : nullptr, bits, bytes(q), bytes(s), on.stream);
   }));
+  written({a[6], a[7], a[8], a[9]});
   return wrap_all({q, s, ro, y});
 }
 
@@ -171,6 +174,7 @@ PyObject* product(PyObject* const* v) {
                           out.data_ptr(), (int)dt, wksp.defined() ? wksp.data_ptr() : nullptr,
                           wksp.defined() ? (size_t)wksp.numel() : 0, on.stream);
   }));
+  written({v[6]});
   return wrap(out);
 }
 
@@ -208,6 +212,7 @@ PyObject* forward(PyObject* const* v) {
                           static_cast<const int32_t*>(ids.data_ptr()), out.data_ptr(), (int)dt,
                           wksp.data_ptr(), (size_t)wksp.numel(), on.stream);
   }));
+  written({v[9]});
   return wrap(out);
 }
 
