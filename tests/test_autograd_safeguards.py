@@ -103,6 +103,28 @@ def test_given_results_of_the_quantised_calls_change_version(monkeypatch):
     versions_rise(lambda: b.moe_quantize_int8_per_channel(torch.zeros(E, H, I, dtype=BF16), q=q, scale=s), [q, s])
 
 
+def test_tangents_are_refused(grouped):
+    """A result without a tangent would be a derivative of zero."""
+    import torch.autograd.forward_ad as fwd
+    calls, t = grouped[0], Maker(grouped[1])
+    a, w, off, out = t(4, 64), t(2, 8, 64), t(3, dtype=I32), t(4, 8)
+    da, dw = t(4, 64), t(2, 8, 64)
+    product = (a, w, off, out, 0, None)
+    grad = (t(4, 8), a, w, off, True, True, da, dw, 0, None)
+    lora = (a, t(3, 2, 16, 64), t(3, 2, 8, 16), t(4, dtype=I32), t(4, 8), off, t(3, dtype=F32), out, 0, None)
+    for call, args, floats in ((calls.product, product, (0, 1, 3)), (calls.product_grad, grad, (0, 1, 2, 6, 7)),
+                               (calls.lora, lora, (0, 1, 2, 4, 6, 7))):
+        call(*args)
+        for i in floats:
+            with fwd.dual_level():
+                dual = list(args)
+                dual[i] = fwd.make_dual(args[i], t(*args[i].shape, dtype=args[i].dtype))
+                assert not dual[i].requires_grad
+                with pytest.raises(ValueError, match="tangent"):
+                    call(*dual)
+        call(*args)
+
+
 @pytest.mark.gpu
 def test_a_saved_input_that_was_written_is_refused():
     """h is saved for a backward pass; adapters added to it in place change its version."""
@@ -132,3 +154,16 @@ def test_a_saved_input_that_was_written_is_refused():
     assert w2.grad is not None
     torch.cuda.synchronize()
     assert mq.mq_device_status() == 0
+
+
+@pytest.mark.gpu
+def test_tangents_are_refused_where_the_call_is_recorded():
+    import torch.autograd.forward_ad as fwd
+
+    import weight_quantized_moe_gb300 as mq
+    x, w = torch.zeros(8, 64, dtype=BF16, device="cuda"), torch.zeros(72, 64, dtype=BF16, device="cuda")
+    for grad in (False, True):
+        w = w.detach().requires_grad_(grad)
+        with fwd.dual_level(), pytest.raises((ValueError, RuntimeError, NotImplementedError)):
+            mq.moe_grouped_product(fwd.make_dual(x, torch.ones_like(x)), w)
+    mq.moe_grouped_product(x, w).sum().backward()

@@ -5,6 +5,13 @@
 
 namespace {
 
+// The calls have no forward-mode derivative: a tensor with a tangent is refused, as the result
+// would have none.
+void no_tangent(const at::Tensor& t, const char* name) {
+  if (t._fw_grad(0).defined())
+    raise(PyExc_ValueError, "%s has a tangent: there is no forward-mode derivative", name);
+}
+
 // 16-bit rows [R, C]: their type, and the elements between rows.
 struct Rows {
   const at::Tensor& t;
@@ -19,6 +26,7 @@ Rows rows(PyObject* o, const char* name, const at::Tensor* first = nullptr) {
     raise(PyExc_TypeError, "%s must be %s, got %s", name,
           first ? c10::toString(first->scalar_type()) : "bfloat16 or float16", c10::toString(type));
   on_cuda(t, name);
+  no_tangent(t, name);
   if (first) same_device(t, *first, name);
   if (t.dim() != 2) raise(PyExc_ValueError, "%s must have 2 dims", name);
   if (t.size(1) < 1) raise(PyExc_ValueError, "%s must have rows of at least one element", name);
@@ -42,6 +50,7 @@ Weights weights(PyObject* o, const char* name, const Rows& a) {
     raise(PyExc_TypeError, "%s must be %s, got %s", name, c10::toString(a.t.scalar_type()),
           c10::toString(t.scalar_type()));
   on_cuda(t, name);
+  no_tangent(t, name);
   same_device(t, a.t, name);
   if (t.dim() != 2 && t.dim() != 3) raise(PyExc_ValueError, "%s must have 2 or 3 dims", name);
   const int64_t E = t.dim() == 3 ? t.size(0) : 1, N = t.size(-2), K = t.size(-1);
@@ -86,6 +95,7 @@ PyObject* product(PyObject* const* v) {
   const long dt = as_long(v[4]);
   int_sizes({w.K, w.N, w.E});
   const at::Tensor out = output(v[3], {a.R, w.N}, scalar_type(dt), a.t, "out");
+  no_tangent(out, "out");
   const int K = (int)w.K, N = (int)w.N, E = (int)w.E;
   const at::Tensor wksp =
       workspace(v[5], v[5] == Py_None ? moe_grouped_product_workspace(a.R, K, N, E) : 0, a.t);
@@ -131,6 +141,8 @@ PyObject* product_grad(PyObject* const* v) {
       if (w.transposed) dw = dw.transpose(-1, -2);
     }
   }
+  if (da.defined()) no_tangent(da, "da");
+  if (dw.defined()) no_tangent(dw, "dw");
   const at::Tensor wksp =
       workspace(v[9], v[9] == Py_None ? moe_grouped_product_grad_workspace(a.R, K, N, E) : 0, a.t);
   check(call([&] {
@@ -146,6 +158,7 @@ PyObject* product_grad(PyObject* const* v) {
 // Adapters [L, E, rows, cols], or [L, rows, cols] for one expert.
 const at::Tensor& adapters(PyObject* o, const char* name, const Rows& x, int64_t& L, int64_t& E) {
   const at::Tensor& t = dense(o, x.t.scalar_type(), -1, x.t, name);
+  no_tangent(t, name);
   if (t.dim() != 3 && t.dim() != 4) raise(PyExc_ValueError, "%s must have 3 or 4 dims", name);
   L = t.size(0);
   E = t.dim() == 4 ? t.size(1) : 1;
@@ -184,18 +197,21 @@ PyObject* lora(PyObject* const* v) {
   int64_t base_stride = N, out_stride = N;
   if (v[4] != Py_None) {
     base = tensor(v[4], "base");
+    no_tangent(base, "base");
     base_stride = strided(base, type, R, N, x.t, "base");
   }
   const int32_t* offsets = expert_offsets(v[5], E, x.t);
   const float* scaling = nullptr;
   if (v[6] != Py_None) {
     const at::Tensor& s = dense(v[6], at::kFloat, 1, x.t, "scaling");
+    no_tangent(s, "scaling");
     if (s.size(0) != L) raise(PyExc_ValueError, "scaling must hold L = %ld values", (long)L);
     scaling = static_cast<const float*>(s.data_ptr());
   }
   int_sizes({K, N, r, L, E});
   if (v[7] != Py_None) {
     out = tensor(v[7], "out");
+    no_tangent(out, "out");
     out_stride = strided(out, type, R, N, x.t, "out");
   } else {
     out = at::empty({R, N}, x.t.options().dtype(type));
