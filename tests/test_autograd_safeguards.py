@@ -125,6 +125,28 @@ def test_tangents_are_refused(grouped):
         call(*args)
 
 
+def test_calls_without_a_gradient_refuse_tensors_that_require_one(grouped, monkeypatch):
+    from weight_quantized_moe_gb300 import binding as b
+    calls, t = grouped[0], Maker(grouped[1])
+    monkeypatch.setattr(b, "_grouped", calls)
+    dy, a, w, off = t(4, 8), t(4, 64), t(2, 8, 64), t(3, dtype=I32)
+    da, dw, out = t(4, 64), t(2, 8, 64), t(4, 8)
+    given = dict(dy=dy, a=a, w=w, expert_offsets=off, da=da, dw=dw)
+    b.moe_grouped_product_grad(**given)
+    for name in ("dy", "a", "w", "da", "dw"):
+        leaf = given[name].detach().requires_grad_()
+        with pytest.raises(ValueError, match="no_grad"):
+            b.moe_grouped_product_grad(**{**given, name: leaf})
+        with torch.no_grad():
+            b.moe_grouped_product_grad(**{**given, name: leaf})
+    b.moe_grouped_product(a, w, off, out=out)
+    leaf = out.detach().requires_grad_()
+    with pytest.raises(ValueError, match="out"):
+        b.moe_grouped_product(a, w, off, out=leaf)
+    with torch.no_grad():
+        b.moe_grouped_product(a, w, off, out=leaf)
+
+
 @pytest.mark.gpu
 def test_a_saved_input_that_was_written_is_refused():
     """h is saved for a backward pass; adapters added to it in place change its version."""

@@ -646,9 +646,10 @@ def moe_grouped_product(a, w, expert_offsets=None, out=None, out_dtype=None, wor
     operator under autograd, capture a backward pass into a graph only while no result that was
     recorded outside the capture from the same a or w lives."""
     if torch.is_grad_enabled() and (getattr(a, "requires_grad", False)
-                                    or getattr(w, "requires_grad", False)):
+                                    or getattr(w, "requires_grad", False)
+                                    or getattr(out, "requires_grad", False)):
         if out is not None:
-            raise ValueError("out cannot be given where a or w requires a gradient")
+            raise ValueError("out cannot be given where a, w or out itself requires a gradient")
         if stream is not None:
             with _given(stream, a):
                 return _GroupedProduct.apply(a, w, expert_offsets, out_dtype, workspace)
@@ -672,7 +673,12 @@ def moe_grouped_product_grad(dy, a, w, expert_offsets=None, need_a=True, need_w=
     gradient of its result, in a's dtype: (da [R, K] in a's dtype or None, dw [E, N, K]
     in dw's dtype or dw_dtype (w's by default) or None).  Rows of no expert give no
     gradient and get 0, an expert without rows has 0.  dw is dense in the order that w
-    is stored in (a transposed view where w is one)."""
+    is stored in (a transposed view where w is one).
+
+    The call has no gradient of its own: under autograd's recording no tensor of it may require
+    one (torch.no_grad())."""
+    if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (dy, a, w, da, dw)):
+        raise ValueError("moe_grouped_product_grad has no gradient of its own: call it under torch.no_grad()")
     if stream is not None:
         with _given(stream, a):
             return moe_grouped_product_grad(dy, a, w, expert_offsets, need_a, need_w, da, dw,
