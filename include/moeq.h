@@ -537,7 +537,9 @@ int moe_grouped_product(const void* a, int64_t a_stride, int dtype, int64_t R, i
  * da dense [R, K] in dtype, or NULL (w is then not read and may be NULL); dw dense
  * [E, N, K], or [E, K, N] with w_transposed, in dw_dtype, or NULL (a may then be NULL).
  * Rows of no expert are not read, whatever they hold.  Other arguments, limits,
- * arithmetic and errors as moe_grouped_product.  da and dw share no memory with each
+ * arithmetic and errors as moe_grouped_product.  A gradient is the same on every run of
+ * the same call; with up to 16 rows da may differ in its last bits between a call for da
+ * alone and one for both.  da and dw share no memory with each
  * other or the inputs.
  */
 size_t moe_grouped_product_grad_workspace(int64_t R, int K, int N, int E);

@@ -901,7 +901,10 @@ cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
 // 65536 rows 640 and 661; 8 experts, 4096 x 14336, 128 rows 335 and 316, 1024 rows 368 and
 // 330, 1500 rows 357 and 337, 2048 rows 440 and 462, 4096 rows 697 and 712; 16 experts, 1408
 // x 2048, 517 rows 57 and 43; 2 experts, 12792 x 2448, 353 rows 83 and 66.  (About where the
-// products take as long, it depends on the loads' last chunks.)
+// products take as long, it depends on the loads' last chunks.)  Also where the rows' by itself
+// would be gg_few's, which adds in another order: 4096 x 4096 stored [K, N], 1 row 24.9 and 19.4,
+// 16 rows 31.5 and 19.4; 8 experts, 2048 x 768, 8 rows 22.3 and 14.7; 64 experts there, 4 rows
+// 41.5 and 44.4.
 bool gg_side_by_side(const GgGemm& rows, const GgGemm& weights) {
   const int64_t n = (int64_t)rows.M * rows.K;
   const double live = (double)std::min<int64_t>(rows.R, rows.E);
