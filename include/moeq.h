@@ -517,7 +517,8 @@ int moe_mx_forward(const uint8_t* a, const uint8_t* a_scale, int a_bits, int T, 
  * memory with the inputs.  Accumulation is float32 with one final rounding; a result
  * is the same on every run.
  * The workspace holds float32 partial sums where K is split (few units of work); the
- * query may return 0 (workspace may then be NULL).
+ * query may return 0 (workspace may then be NULL); it shares no memory with the inputs and
+ * results of its call.
  * K and N are arbitrary; strides are multiples of 8, at least a row's length.
  * Limits: E <= 1024, R < 2^30, K and N at most 2^31 - 512, strides below 2^39.
  * Errors: MQ_ERR_INVALID_ARG, MQ_ERR_UNSUPPORTED (limits), MQ_ERR_WORKSPACE.
@@ -562,7 +563,7 @@ int moe_grouped_product_grad(const void* dy, int64_t dy_stride, const void* a, i
  * leave [0, R] set MQ_DEV_BAD_OFFSETS and nothing is written), or is NULL with E = 1.
  * base [R, N] and out [R, N] in out_dtype with strides of their own; base may be NULL
  * (0), and out may be base itself, with its stride; otherwise out shares no memory
- * with the inputs.
+ * with the inputs, nor does the workspace with them or out.
  * A x and the sums are float32; with many rows A x enters the second product as the
  * sum of two 16-bit values (16 bits of precision relative to the row's largest for
  * bf16, 22 for f16), of three (24 bits) where out is float32; one final rounding.  A row's result depends on no other row, and

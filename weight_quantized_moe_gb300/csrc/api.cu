@@ -1056,6 +1056,19 @@ static Span row_span(const void* p, int64_t R, int64_t stride, int64_t cols) {
   return Span(p, (R - 1) * stride + cols, 2);
 }
 
+// Whether one of R rows of `len` bytes, `stride` bytes apart, meets a span.
+static bool rows_meet(const void* p, int64_t R, int64_t stride, int64_t len, const Span& s) {
+  if (!p || s.lo == s.hi) return false;
+  const int64_t first = (int64_t)reinterpret_cast<uintptr_t>(p), lo = (int64_t)s.lo, hi = (int64_t)s.hi;
+  int64_t i = 0;  // the first row that ends behind the span's beginning
+  if (R > 1 && first + len <= lo) i = (lo - len - first) / stride + 1;
+  return i < R && first + i * stride + len > lo && first + i * stride < hi;
+}
+
+static int workspace_shared() {
+  return fail(MQ_ERR_INVALID_ARG, "the workspace must not share memory with an input or a result");
+}
+
 static Span weight_span(const void* w, int K, int N, int E, int64_t stride, int64_t expert, int transposed) {
   const int64_t rows = transposed ? K : N, len = transposed ? N : K;
   return Span(w, (E - 1) * expert + (rows - 1) * stride + len, 2);
@@ -1095,6 +1108,11 @@ MQ_EXPORT int moe_grouped_product(const void* a, int64_t a_stride, int dtype, in
       written.meets(weight_span(w, K, N, E, w_stride, w_expert_stride, w_transposed)) ||
       written.meets(Span(expert_offsets, E + 1, 4)))
     return fail(MQ_ERR_INVALID_ARG, "out must not share memory with a, w or expert_offsets");
+  const Span used(workspace, (int64_t)gg_part_bytes(g.form, R, E, N, 0, K), 1);
+  if (used.meets(written) || rows_meet(a, R, a_stride * 2, (int64_t)K * 2, used) ||
+      used.meets(weight_span(w, K, N, E, w_stride, w_expert_stride, w_transposed)) ||
+      used.meets(Span(expert_offsets, E + 1, 4)))
+    return workspace_shared();
   return gg_run(g, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
@@ -1134,6 +1152,11 @@ MQ_EXPORT int moe_grouped_product_grad(const void* dy, int64_t dy_stride, const 
     if (da_span.meets(in) || dw_span.meets(in))
       return fail(MQ_ERR_INVALID_ARG, "da and dw must not share memory with dy, a, w or expert_offsets");
   if (da_span.meets(dw_span)) return fail(MQ_ERR_INVALID_ARG, "da and dw must not share memory");
+  if (need && !aligned16(workspace)) return fail(MQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  const Span used(workspace, (int64_t)need, 1);
+  if (used.meets(da_span) || used.meets(dw_span) || rows_meet(dy, R, dy_stride * 2, (int64_t)N * 2, used) ||
+      (dw && rows_meet(a, R, a_stride * 2, (int64_t)K * 2, used)) || used.meets(read[2]) || used.meets(read[3]))
+    return workspace_shared();
   GgGemm g = {};
   g.bf16 = dtype == MQ_DTYPE_BF16;
   g.R = R; g.E = E;
@@ -1236,6 +1259,12 @@ MQ_EXPORT int moe_lora_product(const void* x, int64_t x_stride, int dtype, int64
       written.meets(Span(adapter_ids, R, 4)) || written.meets(Span(expert_offsets, E + 1, 4)) ||
       written.meets(Span(scaling, L, 4)))
     return fail(MQ_ERR_INVALID_ARG, "out must not share memory with the adapters, their ids, scaling or expert_offsets");
+  const Span used(workspace, (int64_t)need, 1);
+  if (rows_meet(out, R, out_stride * size, N * size, used) || rows_meet(base, R, base_stride * size, N * size, used) ||
+      rows_meet(x, R, x_stride * 2, (int64_t)K * 2, used) || used.meets(Span(lora_a, groups * r * K, 2)) ||
+      used.meets(Span(lora_b, groups * r * N, 2)) || used.meets(Span(adapter_ids, R, 4)) ||
+      used.meets(Span(expert_offsets, E + 1, 4)) || used.meets(Span(scaling, L, 4)))
+    return workspace_shared();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   LoraArgs g = {};
   g.bf16 = dtype == MQ_DTYPE_BF16;
