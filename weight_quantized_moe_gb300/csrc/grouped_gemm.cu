@@ -37,7 +37,6 @@
 #include "pipe.cuh"
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -105,7 +104,6 @@ struct Params {
   int E, M, N, K, R;
   int mtiles, ntiles, splits;
   uint32_t idesc;  // without N
-  bool evict_first;
   bool listed;       // tiles are numbered in 16 bits: units fit the list
   bool tma_out;      // GG_ROWS: the result's rows start at 16-byte boundaries
   bool zero_outside;
@@ -359,7 +357,7 @@ __device__ __forceinline__ void gg_body(const CUtensorMap& map_w, const CUtensor
                           : cols == BN    ? C::kBRows
                                           : cols / CG;
       const uint32_t bytes = kABytes + brought * 128;
-      const bool once = FORM != GG_ROWS && w.single && p.evict_first;
+      const bool once = FORM != GG_ROWS && w.single;
       for (int s = s0; s < s1; ++s, ++it) {
         const uint32_t slot = it % C::kStages;
         if (!warp_wait(&ctl->empty[slot], ((it / C::kStages) & 1) ^ 1, ctl, p.status)) {
@@ -707,18 +705,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------ host side --
-template <typename K>
-cudaError_t allow_smem(K kern, size_t smem, std::atomic<uint64_t>& ready) {
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  const uint64_t bit = uint64_t(1) << (dev & 63);  // devices whose attribute is set
-  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (err == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
-  return err;
-}
-
 // Whether a sum may be longer than a segment (GG_ROWS: where an expert has most rows).
 template <int FORM>
 bool segmented(const Params& p) {
@@ -867,7 +853,6 @@ cudaError_t prepare(const GgGemm& g, const GgPlan& pl, Prepared& out) {
   p.ntiles = g.form == GG_ROWS ? (g.N + pl.bn - 1) / pl.bn : 1;
   p.splits = pl.splits;
   p.idesc = idesc_16(g.bf16, kTileM * cg, 0, g.form != GG_W_K, g.form == GG_ROWS);
-  p.evict_first = true;
   p.listed = p.mtiles < 1 << 16 && p.ntiles < 1 << 16;
   p.zero_outside = g.zero_outside;
   p.segment = g.out_dtype == MQ_DTYPE_F32 ? kSegment : kSegment16;

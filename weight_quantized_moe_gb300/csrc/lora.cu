@@ -38,7 +38,6 @@
 #include "pipe.cuh"
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -1337,18 +1336,6 @@ __global__ void __launch_bounds__(kUpThreads, 1)
 // ------------------------------------------------------------ host side --
 int padded_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
-template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& ready) {
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (err == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
-  return err;
-}
-
 template <bool BF16>
 cudaError_t launch_rows(const LoraArgs& g, cudaStream_t st) {
   const dim3 grid((unsigned)g.R * kCluster), block(kRowThreads);
@@ -1511,11 +1498,13 @@ LoraPlan lora_plan(int64_t R, int K, int N, int r, int L, int E) {
   const double tiles_us = 13.5 + 0.15 * std::min(64.0, 4 * groups);
   pl.rows = rows_us <= tiles_us;
   if (pl.rows) return pl;
-  // Rows of a tile, and K splits (with the clusters of that many CTAs that this GPU holds at
-  // a time): by the estimated time of both launches, in units of 128 x 128 outputs of the
+  // Rows of a tile, and K splits (with the clusters of that many CTAs that the GPU holds at
+  // a time: measured with 152 SMs): by the estimated time of both launches, in units of 128 x 128 outputs of the
   // second, 1.45 us.  A stage of the first takes a quarter of one, half of it for the
   // groups; the way in and out of it six.
-  constexpr int kClusters[4] = {152, 76, 36, 15};
+  constexpr int kOf152[4] = {152, 76, 36, 15};
+  int held[4];
+  for (int i = 0; i < 4; ++i) held[i] = std::max(1, kOf152[i] * sms / 152);
   const int ntiles = (N + kTile - 1) / kTile, stages = (K + 63) / 64;
   double best = 0;
   for (int h = kTile; h >= 64; h -= 16) {
@@ -1524,7 +1513,7 @@ LoraPlan lora_plan(int64_t R, int K, int N, int r, int L, int E) {
     int splits = 1;
     up_shares(n, h, ntiles, &up);
     for (int i = 0; i < 4 && (i == 0 || stages >= 8 << i); ++i) {
-      const double t = (double)((n + kClusters[i] - 1) / kClusters[i]) * ((stages >> i) * (0.13 + 0.13 * h / 128) + 6);
+      const double t = (double)((n + held[i] - 1) / held[i]) * ((stages >> i) * (0.13 + 0.13 * h / 128) + 6);
       if (i == 0 || t < down) down = t, splits = 1 << i;
     }
     if (h == kTile || up + down < 0.97 * best) best = up + down, pl.height = h, pl.splits = splits;
@@ -1533,7 +1522,7 @@ LoraPlan lora_plan(int64_t R, int K, int N, int r, int L, int E) {
   const int per = kTile / padded_rank(r);
   const int tile_groups = (int)std::min<double>(pl.height, groups);
   const int accs = (tile_groups + per - 1) / per;
-  const int clusters = pl.splits == 1 ? 152 : pl.splits == 2 ? 76 : pl.splits == 4 ? 36 : 15;
+  const int clusters = held[pl.splits == 1 ? 0 : pl.splits == 2 ? 1 : pl.splits == 4 ? 2 : 3];
   pl.mparts = (int)std::max<int64_t>(1, std::min<int64_t>(accs, clusters / tiles));
   while (pl.gparts * 2 <= tile_groups && tiles * ntiles * pl.gparts * 2 <= sms) pl.gparts *= 2;
   return pl;

@@ -12,6 +12,7 @@
 
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 namespace mq {
@@ -132,6 +133,20 @@ inline cudaError_t make_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, 
   if (err == cudaSuccess) err = cudaSetDevice(dev);
   if (err != cudaSuccess) return err;
   return make() ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Lets a kernel have `bytes` of shared memory on the current device; `ready`: the devices
+// where it has them.
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (err == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return err;
 }
 
 }  // namespace pipe
