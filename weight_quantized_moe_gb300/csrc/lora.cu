@@ -1499,9 +1499,9 @@ LoraPlan lora_plan(int64_t R, int K, int N, int r, int L, int E) {
   pl.rows = rows_us <= tiles_us;
   if (pl.rows) return pl;
   // Rows of a tile, and K splits (with the clusters of that many CTAs that the GPU holds at
-  // a time: measured with 152 SMs): by the estimated time of both launches, in units of 128 x 128 outputs of the
-  // second, 1.45 us.  A stage of the first takes a quarter of one, half of it for the
-  // groups; the way in and out of it six.
+  // a time, measured with 152 SMs): by the estimated time of both launches, in units of 128 x
+  // 128 outputs of the second, 1.45 us.  A stage of the first takes a quarter of one, half of
+  // it for the groups; the way in and out of it six.
   constexpr int kOf152[4] = {152, 76, 36, 15};
   int held[4];
   for (int i = 0; i < 4; ++i) held[i] = std::max(1, kOf152[i] * sms / 152);
