@@ -118,3 +118,27 @@ def test_float32_results_have_24_bits(mq, R, r, dtype):
     ref = h[:, rank]
     allowed = 2.0 ** -24 * h.abs().amax(1, keepdim=True) + 2 * 2.0 ** -24 * ref.abs()
     assert ((got.double().cpu() - ref).abs() <= allowed).all()
+
+
+@pytest.mark.parametrize("N", [264, 65])
+def test_float32_in_place(mq, N):
+    """Adapters added in place to float32 results, dense and as slices of a wider buffer."""
+    R, K, r, L = 1300, 64, 16, 4
+    g = torch.Generator().manual_seed(N)
+    x, a = gh.randn(R, K, seed=1, dtype=BF16), gh.randn(L, 1, r, K, seed=2, dtype=BF16, scale=K ** -0.5)
+    b, base = gh.randn(L, 1, N, r, seed=3, dtype=BF16, scale=r ** -0.5), gh.randn(R, N, seed=4, dtype=F32)
+    ids = torch.randint(-1, L, (R,), generator=g, dtype=torch.int32)
+    args = (x.cuda(), a[:, 0].contiguous().cuda(), b[:, 0].contiguous().cuda(), ids.cuda())
+    ref, off = gh.lora64(x, a, b, ids.tolist(), [0] * R, None, base, BF16)
+    out = base.cuda()
+    assert mq.moe_lora_product(*args, base=out, out=out) is out
+    clean(mq)
+    gh.check_lora(out, ref, off)
+    wide = torch.full((R, N + 8), 7.0, device="cuda")
+    mid = wide[:, 3:3 + N]
+    mid.copy_(base)
+    mq.moe_lora_product(*args, base=mid, out=mid)
+    clean(mq)
+    gh.check_lora(mid, ref, off)
+    assert (wide[:, :3] == 7).all() and (wide[:, 3 + N:] == 7).all()
+    assert torch.equal(out[(ids == -1).cuda()].cpu(), base[ids == -1])

@@ -642,7 +642,9 @@ def moe_grouped_product(a, w, expert_offsets=None, out=None, out_dtype=None, wor
 
     Where a or w requires a gradient the call is recorded for autograd
     (moe_grouped_product_grad is its backward pass); out cannot be given then.  The
-    gradient of a float32 result is rounded to a's dtype before the products.  As with any
+    gradient of a float32 result is rounded to a's dtype before the products, and takes on its
+    range: below 6e-8 float16 has 0, above 65504 infinity (scale the loss, or use bfloat16).
+    w's gradient comes in w's dtype; moe_grouped_product_grad gives it in float32.  As with any
     operator under autograd, capture a backward pass into a graph only while no result that was
     recorded outside the capture from the same a or w lives."""
     if torch.is_grad_enabled() and (getattr(a, "requires_grad", False)
@@ -710,7 +712,7 @@ def moe_lora_product(x, lora_a, lora_b, adapter_ids, base=None, expert_offsets=N
     x, base and out may be strided (x by multiples of 8 elements).
 
     The call has no gradient.  Adapters are trained as two moe_grouped_product calls over
-    rows that are sorted by adapter."""
+    rows that are sorted by adapter (and expert): up to 1024 of them at a time."""
     if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False)
                                        for t in (x, lora_a, lora_b, base, scaling, out)):
         raise ValueError("moe_lora_product has no gradient: call it under torch.no_grad(), or train "
