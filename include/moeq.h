@@ -552,7 +552,8 @@ int moe_grouped_product_grad(const void* dy, int64_t dy_stride, const void* a, i
 
 /*
  * moe_lora_product -- low-rank adapters of many requests in one call, beside a
- * projection that is already computed (by any of this library's products, say):
+ * projection that is already computed (moe_mx_product's or moe_grouped_product's, say; the
+ * int8 and uint4 layers are fused, with no point between their products):
  *   out[t] = base[t] + scaling[l] * B[l, e] (A[l, e] x[t]),   l = adapter_ids[t]
  * x [R, K] in dtype (bf16 or f16), x_stride elements between rows; lora_a
  * [L, E, r, K] and lora_b [L, E, N, r] dense in the same dtype; adapter_ids int32 [R]

@@ -29,11 +29,12 @@
 // requests takes one turn of the epilogue, or a few.  base comes by TMA and goes back, with
 // the sums added, the same way.
 //
-// Measured: rows, 4096 x 4096, rank 16: 1 row 5.2 us, 64 rows of 48 adapters 7.0 (a chain of
-// dependent reads: ids, A, the exchange; B is on its way meanwhile).  Tiles: 4099 rows of 16
-// adapters, rank 64, 37 us (67 MB of base and out beside two launches' ways in and out);
-// 4096 rows of 64 experts, 2048 x 2816, rank 32, 16 groups in a tile, 68 us (four
-// instructions for each group and 128 outputs, about 120 cycles each for their few columns).
+// Measured: rows, 4096 x 4096, rank 16: 1 row 5.5 to 6.1 us, 64 rows of 48 adapters 7.1 (a
+// chain of dependent reads: ids, A, the exchange; B is on its way meanwhile).  Tiles: 4099
+// rows of 16 adapters, rank 64, 38 us (67 MB of base and out beside two launches' ways in and
+// out); 4096 rows of 64 experts, 2048 x 2816, rank 32, 16 groups in a tile, 70 us (short steps
+// for each group and 128 outputs: DRAM at 30 %, the tensor pipe at 12 and 4 %).  Float32
+// results, 2000 rows of 8 adapters, rank 16, 4096 x 4096: 52 us.
 #include "lora.cuh"
 #include "pipe.cuh"
 
