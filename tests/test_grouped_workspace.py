@@ -45,6 +45,16 @@ def test_product(lib):
             assert shared(lib, call(ws)), (hex(at), hex(ws))
 
 
+def test_workspaces_that_are_not_needed_are_not_looked_at(lib):
+    """(Nothing runs: without a GPU the launch fails.)"""
+    R, K, N, E = 64, 64, 128, 8
+    assert lib.moe_grouped_product_workspace(R, K, N, E) == 0
+    for ws in (A + 64, W + 64, OUT + 64):
+        rc = lib.moe_grouped_product(vp(A), K, BF16, R, K, N, E, vp(W), K, N * K, 0, vp(OFF), vp(OUT), BF16, vp(ws),
+                                     1 << 20, None)
+        assert not shared(lib, rc)
+
+
 def test_gradients(lib):
     R, K, N = 4096, 64, 64
     need = lib.moe_grouped_product_grad_workspace(R, K, N, 1)

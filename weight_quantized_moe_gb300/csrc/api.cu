@@ -1049,7 +1049,7 @@ struct Span {
   uintptr_t lo, hi;
   Span(const void* p, int64_t elements, int64_t size)
       : lo(reinterpret_cast<uintptr_t>(p)), hi(p ? lo + (uintptr_t)(elements * size) : lo) {}
-  bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
+  bool meets(const Span& o) const { return lo < hi && o.lo < o.hi && lo < o.hi && o.lo < hi; }
 };
 
 static Span row_span(const void* p, int64_t R, int64_t stride, int64_t cols) {
