@@ -31,8 +31,8 @@
 // 1.55 PFLOP/s in a loop at 1.45 GHz; there a CTA pair holds 256 by 256, which halves the
 // operand reads of two CTAs by themselves).  The gradient of the weights writes more than
 // it reads where experts have few rows, and writes alone go at little more than half the
-// rate of a copy, so both gradients then run side by side in one launch: 128 experts, 4096
-// rows, 1536 x 2048: 304 us one after the other, 278 together.
+// rate of a copy, so both gradients then run side by side in one launch: 16 experts, 517 rows,
+// 1408 x 2048, float32: 66 us one after the other, 55 together.
 #include "grouped.cuh"
 #include "pipe.cuh"
 
@@ -892,14 +892,13 @@ cudaError_t launch_gg(const GgGemm& g, const GgPlan& pl, cudaStream_t st) {
 
 // Side by side where memory bounds both and neither is split: the weights read and
 // written at 6.6 and 3.8 TB/s, against the products at 1.5 PFLOP/s.  us one after the other
-// and side by side: 128 experts, 2048 x 1536, 4096 rows 277 and 273, 16384 rows 325 and 297,
-// 65536 rows 640 and 661; 8 experts, 4096 x 14336, 128 rows 335 and 316, 1024 rows 368 and
-// 330, 1500 rows 357 and 337, 2048 rows 440 and 462, 4096 rows 697 and 712; 16 experts, 1408
-// x 2048, 517 rows 57 and 43; 2 experts, 12792 x 2448, 353 rows 83 and 66.  (About where the
-// products take as long, it depends on the loads' last chunks.)  Also where the rows' by itself
-// would be gg_few's, which adds in another order: 4096 x 4096 stored [K, N], 1 row 24.9 and 19.4,
-// 16 rows 31.5 and 19.4; 8 experts, 2048 x 768, 8 rows 22.3 and 14.7; 64 experts there, 4 rows
-// 41.5 and 44.4.
+// and side by side: 16 experts, 1408 x 2048, 517 rows, float32, 66 and 55; 2 experts, 12792 x
+// 2448, 353 rows 88 and 77; 128 experts, 2048 x 1536, 4096 rows (by Zipf's law) 281 and 286,
+// 16384 rows 356 and 348; 8 experts, 4096 x 14336, 128 rows 310 and 321, 1024 rows 338 and 340,
+// 1500 rows 382 and 386.  (Where the launches are long it makes little difference.)  Also where
+// the rows' by itself would be gg_few's, which adds in another order: 4096 x 4096 stored [K, N],
+// 1 row 24.9 and 19.4, 16 rows 31.5 and 19.4; 8 experts, 2048 x 768, 8 rows 22.3 and 14.7; 64
+// experts there, 4 rows 41.5 and 44.4.
 bool gg_side_by_side(const GgGemm& rows, const GgGemm& weights) {
   const int64_t n = (int64_t)rows.M * rows.K;
   const double live = (double)std::min<int64_t>(rows.R, rows.E);
